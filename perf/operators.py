@@ -12,7 +12,7 @@ Four operators, in the order in which a server calls them:
            together into another cache.
 
 The formulas, with c = codes of a block, a = its scale and top = 127 (int8) or 448 (e4m3):
-  a = max(max|x| / top, 2^-126) over the block's rows and d, c = round(x / a) to nearest even,
+  a = max(max|x| / top, 2^-126) over the block's rows and d, c = round(x (1 / a)) to nearest even,
   the value that a code stands for = c a (all in float32);
   o_i = sum_j p_ij v_j, p_ij = exp(scale q_i.k_j - lse_i) over the keys j that row i sees.
 The 8-bit codes are returned as they are, beside their scales: they follow from float32 operations
@@ -225,7 +225,7 @@ def _quantise(x, fmt):
     """x [..., rows, d] float32 -> codes and one scale for each [rows, d]."""
     big = x.abs().amax((-2, -1))
     scale = torch.maximum(big / torch.full_like(big, TOP[fmt]), torch.full_like(big, 2.0 ** -126))
-    y = x / scale[..., None, None]
+    y = x * (torch.ones_like(scale) / scale)[..., None, None]
     return (y.round().clamp(-127, 127) if fmt == S8 else y).to(CODE[fmt]), scale
 
 
