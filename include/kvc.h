@@ -9,7 +9,9 @@
  *   h2o_decode_step  one decode step: attention, score accumulation, <= 1 eviction
  * and, beyond those five, NestedKV's key-only scorer (kv_score_nested), a
  * layer-level budget shared by the heads of a layer (kv_select_budget,
- * kv_compact_ragged) and the _ex variants (sinks, HubKV comparison variants).
+ * kv_compact_ragged), the _ex variants (sinks, HubKV comparison variants), the
+ * attention of the prompt itself (kv_attn_prompt) and a slot cache held in 8 bits
+ * (kv_compact_q8, h2o_decode_step_q8, kv_evict_q8).
  *
  * Sources (page title, section):
  *   [H2O]    "H2O 完全拆解：抓住 KV Cache 里的「重击者」，20% 预算无损生成（NeurIPS 2023）"
@@ -91,8 +93,38 @@ enum {
   KV_OP_SELECT_TOPK = 3,
   KV_OP_DECODE = 4,
   KV_OP_SCORE_NESTED = 5,
-  KV_OP_HUBKV_SELECT = 6
+  KV_OP_HUBKV_SELECT = 6,
+  KV_OP_ATTN_PROMPT = 7,
+  KV_OP_DECODE_Q8 = 8
 };
+
+/* formats of the 8-bit slot cache's codes: int8 (-127..127) or e4m3 (largest 448) */
+typedef enum { KV_Q8_S8 = 0, KV_Q8_E4M3 = 1 } kv_q8_format;
+
+/*
+ * A slot cache held in 8 bits.  Slots 0..len-1 of unit (b, h) are filled, in the
+ * order of their positions; every operation below keeps that order.  The len / block
+ * whole blocks of `block` slots are codes with one float32 scale a per block and
+ * head for K and one for V (the value of a code c is c a):
+ *     a = max(max|x| / top, 2^-126) over the block, c = round-to-even(x (1 / a)),
+ * top = 127 or 448, each step one float32 operation.  The rows of the last,
+ * unfinished block (len % block of them) stay in the model's dtype in Kt, Vt; a
+ * block is quantised once, when it becomes full.
+ */
+typedef struct kv_q8_cache {
+  void *K, *V;     /* codes [B][Hkv][cap][d], one byte each */
+  float *Ks, *Vs;  /* scales [B][Hkv][cap / block] */
+  void *Kt, *Vt;   /* rows of the unfinished block [B][Hkv][block][d], dtype */
+  int32_t *pos;    /* positions [B][Hkv][cap] */
+  float *acc;      /* accumulated attention [B][Hkv][cap], may be NULL (kv_evict_q8 needs it) */
+  int32_t *len;    /* filled slots [B][Hkv] */
+  int B, Hkv;
+  int cap;         /* slots, a multiple of block */
+  int d;           /* 64 or 128 */
+  int block;       /* 32, 64 or 128 */
+  int dtype;       /* kv_dtype of Kt, Vt and of the rows that come in */
+  int format;      /* kv_q8_format */
+} kv_q8_cache;
 
 typedef void *kv_stream_t;
 
@@ -429,9 +461,113 @@ KVC_API int kv_score_obs_noalloc(const void *Q_obs, const void *K, int B, int Hq
                                  int d, int W, float scale, int dtype, float *s_out,
                                  int *dev_status, kv_stream_t stream);
 
+/*
+ * kv_attn_prompt -- attention of a whole prompt (or of a chunk of it behind keys
+ * that are cached already), causal, with grouped heads ([KVblog] §1.1, §3.3).  A
+ * sequence with nq query rows and nk keys: row i sees the keys j <= i + nk - nq, so
+ * that its last row sees every key, and
+ *     O_i = sum_j P_i(j) V_j,  P_i(j) = exp(scale <Q_i, K_j> - lse_i),
+ *     lse_i = log sum_j exp(scale <Q_i, K_j>).
+ * A row that sees no key (nk < nq) gets O = 0 and lse = -inf.
+ *
+ *   Q, O       [B][Hq][Tq][d];  K, V [B][Hkv][Tk][d]; dtype (O is rounded to it once)
+ *   strides    host array of 12 element strides: batch, head and token of Q, K, V, O
+ *              (the d elements of a row are adjacent), each with stride * element
+ *              size a multiple of 16 bytes; NULL = dense.  [tokens][heads][d]
+ *              tensors and slices of a fused projection are given this way.
+ *   n_seq      0: each of the B rows is one sequence; seq_q, seq_k are its query
+ *              rows and keys [B] (NULL = Tq, Tk).
+ *              > 0: B = 1 and n_seq sequences are packed along the token axis;
+ *              seq_q, seq_k [n_seq + 1] are their offsets: sequence i has the query
+ *              rows seq_q[i] .. seq_q[i+1]-1 and the keys seq_k[i] .. seq_k[i+1]-1.
+ *   O          rows that belong to no sequence are left as they were
+ *   lse_out    [B][Hq][Tq] float32, may be NULL (rows as for O)
+ *   workspace  >= kv_workspace_size(KV_OP_ATTN_PROMPT, B, Hq, Hkv, Tk, d, Tq, n_seq)
+ *   dev_status device int, may be NULL; KV_ERR_INVALID_ARG when lengths or offsets
+ *              are out of range or decrease (that sequence is left as it was),
+ *              KV_ERR_TIMEOUT when a bounded device-side wait gave up; never cleared
+ * K, V rows behind a sequence's last key are not used, whatever they hold.
+ * Preconditions: Hq % Hkv == 0, d in {64, 128}, scale not NaN.
+ * bf16: products on the tensor cores (tcgen05, TMA) with fp32 accumulation, the
+ * weights rounded to bf16 before the second product; fp32: CUDA cores throughout.
+ */
+KVC_API int kv_attn_prompt(const void *Q, const void *K, const void *V, int B, int Hq, int Hkv, int Tq,
+                           int Tk, int d, const int64_t *strides, const int32_t *seq_q,
+                           const int32_t *seq_k, int n_seq, float scale, int dtype, void *O,
+                           float *lse_out, void *workspace, size_t workspace_bytes, int *dev_status,
+                           kv_stream_t stream);
+
+/*
+ * kv_compact_q8 -- kv_compact into an 8-bit slot cache: for every head and m < k the
+ * row K[idx[m]], V[idx[m]] goes to slot m, pos = idx[m], acc = s[idx[m]], and
+ * len = k.  Slots k.. and the blocks behind them are not touched.
+ *
+ *   K, V       [B][Hkv][T][d] of out->dtype, device or pinned host memory (as for
+ *              kv_compact);  s [B][Hkv][T] float32, NULL: acc starts at 0
+ *   idx        [B][Hkv][k] int32 ascending, each in [0, T); NULL (k == T only): every
+ *              row, the whole prompt
+ *   dev_status device int, may be NULL; KV_ERR_INVALID_ARG when an index is out of
+ *              range (its slot then holds a row of zeros at position -1, acc 0)
+ * Preconditions: 1 <= k <= T, k <= out->cap.
+ */
+KVC_API int kv_compact_q8(const void *K, const void *V, const float *s, const int32_t *idx, int T, int k,
+                          const kv_q8_cache *out, int *dev_status, kv_stream_t stream);
+
+/*
+ * h2o_decode_step_q8 -- one decode step over an 8-bit slot cache: as h2o_decode_step
+ * without its eviction (a slot among codes with a common scale cannot be overwritten
+ * by another row; kv_evict_q8 makes room for many steps at once).  The attended set
+ * is the slots 0..len-1 and the new token; per query head g of a group
+ *     P_g = softmax of scale <q_g, k_j>,  o_out[b][g] = sum_j P_g(j) v_j
+ * over the values that the codes stand for.  Each cached accumulator gains
+ * sum_g P_g(j); the new token starts with its own sum.  It goes to slot len as a row
+ * of the unfinished block, which is quantised when that makes it full, and
+ * len_out = len + 1.
+ *
+ *   q          [B][Hq][d];  k_new, v_new [B][Hkv][d] (cache->dtype)
+ *   new_pos    the new tokens' position; row_pos [B] int32 instead, when given
+ *   len_out    [B][Hkv] int32: cache->len itself (the usual case) or another array,
+ *              for a step that may be taken back
+ *   o_out      [B][Hq][d] float32
+ *   workspace  >= kv_workspace_size(KV_OP_DECODE_Q8, B, Hq, Hkv, cap, d, 0, 0) bytes
+ *   dev_status device int, may be NULL; KV_ERR_INVALID_ARG when a len is outside
+ *              [0, cap - 1] (that unit is left untouched, its o and len_out too)
+ * Preconditions: 1 <= Hq / Hkv <= 8, every position below the new one.
+ */
+KVC_API int h2o_decode_step_q8(const void *q, const void *k_new, const void *v_new,
+                               const kv_q8_cache *cache, int Hq, int32_t new_pos,
+                               const int32_t *row_pos, int32_t *len_out, float scale, float *o_out,
+                               void *workspace, size_t workspace_bytes, int *dev_status,
+                               kv_stream_t stream);
+
+/*
+ * kv_evict_q8 -- eviction by accumulated attention ([H2O] 贪心驱逐算法, 双缓冲), many
+ * slots at once: every unit that holds more than `keep` slots drops the
+ * (acc, position)-smallest until `keep` are left, never one of its last `recent`
+ * slots nor one with a position below `sink`.  The others move together, in their
+ * order, into `out` (len = min(len, keep)); units with at most `keep` slots move as
+ * they are.  A destination block whose rows are one whole source block keeps its
+ * codes and scale; the others are quantised anew from the values that the codes
+ * stand for.  Rows of the new unfinished block that were codes are rounded to dtype.
+ *
+ *   cache      is left as it was; out: another cache (no memory in common) of the
+ *              same B, Hkv, d, block, dtype and format with out->cap >= keep.  One
+ *              spare cache serves all layers: each layer moves into it and leaves
+ *              its own as the next one's spare.
+ *   idx_out    [B][Hkv][keep] int32: the slot that each new slot came from, -1 behind
+ *              the new len
+ *   dev_status device int, may be NULL; KV_ERR_INVALID_ARG when a len is outside
+ *              [0, cap] (that unit's part of out and idx_out is left untouched)
+ * Preconditions: recent >= 0, sink >= 0, recent + sink < keep, cache->acc and
+ * out->acc given.
+ */
+KVC_API int kv_evict_q8(const kv_q8_cache *cache, int keep, int recent, int sink, int32_t *idx_out,
+                        const kv_q8_cache *out, int *dev_status, kv_stream_t stream);
+
 /* Device workspace (bytes) that `op` needs for these sizes; 0 if none.
  * Arguments that an op does not use are ignored; for KV_OP_HUBKV_REFINE pass the
- * refine call's head count H as Hkv; for KV_OP_DECODE pass the slot capacity as T;
+ * refine call's head count H as Hkv; for KV_OP_DECODE and KV_OP_DECODE_Q8 pass the slot
+ * capacity as T; for KV_OP_ATTN_PROMPT pass Tk as T, Tq as W and n_seq as k;
  * for KV_OP_SCORE_NESTED pass H as Hkv and n_blocks as W.
  * Returns 0 for invalid sizes. */
 KVC_API size_t kv_workspace_size(int op, int B, int Hq, int Hkv, int T, int d, int W, int k);

@@ -9,6 +9,7 @@ are allocated with torch on the input's device.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -30,7 +31,8 @@ KV_BF16, KV_F32 = 0, 1
 KV_H2O_ALG1 = 1
 KV_HUB_AVGPOOL, KV_HUB_FIXED_HEAD = 1, 2
 KV_OP_SCORE_OBS, KV_OP_HUBKV_REFINE, KV_OP_SELECT_TOPK, KV_OP_DECODE, KV_OP_SCORE_NESTED = 1, 2, 3, 4, 5
-KV_OP_HUBKV_SELECT = 6
+KV_OP_HUBKV_SELECT, KV_OP_ATTN_PROMPT, KV_OP_DECODE_Q8 = 6, 7, 8
+KV_Q8_S8, KV_Q8_E4M3 = 0, 1
 
 _P, _I, _F, _Z = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
 _lib.kv_score_obs.restype = _I
@@ -67,6 +69,23 @@ _lib.h2o_decode_steps.argtypes = [_P, _P, _P, _I, _P, _P, _P, _P, _P, _I, _I, _I
                                   _F, _I, _I, _P, _P, _P, _Z, _P, _P]
 _lib.kv_score_obs_noalloc.restype = _I
 _lib.kv_score_obs_noalloc.argtypes = [_P, _P, _I, _I, _I, _I, _I, _I, _F, _I, _P, _P, _P]
+
+
+class _Q8Cache(ctypes.Structure):
+    _fields_ = ([(n, _P) for n in ("K", "V", "Ks", "Vs", "Kt", "Vt", "pos", "acc", "len")]
+                + [(n, _I) for n in ("B", "Hkv", "cap", "d", "block", "dtype", "format")])
+
+
+_Q8P = ctypes.POINTER(_Q8Cache)
+_lib.kv_attn_prompt.restype = _I
+_lib.kv_attn_prompt.argtypes = [_P, _P, _P, _I, _I, _I, _I, _I, _I, ctypes.POINTER(ctypes.c_int64), _P,
+                                _P, _I, _F, _I, _P, _P, _P, _Z, _P, _P]
+_lib.kv_compact_q8.restype = _I
+_lib.kv_compact_q8.argtypes = [_P, _P, _P, _P, _I, _I, _Q8P, _P, _P]
+_lib.h2o_decode_step_q8.restype = _I
+_lib.h2o_decode_step_q8.argtypes = [_P, _P, _P, _Q8P, _I, _I, _P, _P, _F, _P, _P, _Z, _P, _P]
+_lib.kv_evict_q8.restype = _I
+_lib.kv_evict_q8.argtypes = [_Q8P, _I, _I, _I, _P, _Q8P, _P, _P]
 _lib.kv_workspace_size.restype = _Z
 _lib.kv_workspace_size.argtypes = [_I, _I, _I, _I, _I, _I, _I, _I]
 _lib.kv_status_string.restype = ctypes.c_char_p
@@ -396,6 +415,205 @@ def compress_prefill(Q_obs, K, V, k: int, recent: int, r: float | None, gamma: f
     Kc, Vc, pos, acc, ln = kv_compact(K, V, s, idx, cap, stream=stream)
     return {"s": s, "z": z, "beta": beta, "idx": idx, "K": Kc, "V": Vc, "pos": pos, "acc": acc,
             "len": ln}
+
+
+def _side(stream):
+    """Allocations made for a call on `stream` belong to that stream, so that their memory
+    is not handed out again while the call still uses it."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
+def _strided(*ts):
+    """Tensors whose d elements are adjacent; the other strides are handed to the library."""
+    for t in ts:
+        if t is not None:
+            if not t.is_cuda or t.stride(-1) != 1:
+                raise ValueError("tensors must be CUDA tensors with adjacent elements along d")
+            _on_current_device(t)
+
+
+def kv_attn_prompt(Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, scale: float | None = None,
+                   seq_q=None, seq_k=None, packed: bool = False, out=None, lse_out=None,
+                   workspace=None, dev_status=None, stream=None):
+    """Causal attention of a prompt: Q [B][Hq][Tq][d], K, V [B][Hkv][Tk][d] ->
+    (o [B][Hq][Tq][d] in Q's dtype, lse [B][Hq][Tq] float32).
+
+    Row i of a sequence with nq query rows and nk keys sees the keys j <= i + nk - nq.
+    Batch, head and token strides are free (a [tokens][heads][d] tensor goes in as
+    ``x.transpose(0, 1).unsqueeze(0)``); only the d elements must be adjacent.
+    seq_q, seq_k: int32 CUDA tensors.  Without `packed` the lengths [B] of the rows'
+    sequences (None: Tq, Tk); with it the offsets [n + 1] of n sequences packed along
+    the token axis of the one batch row.  Rows of no sequence are left as they were
+    in `out` and `lse_out` (and undefined in tensors made here).  `out` made here has
+    Q's memory order."""
+    B, Hq, Tq, d = Q.shape
+    B2, Hkv, Tk, d2 = K.shape
+    if B2 != B or d2 != d or V.shape != K.shape or not Q.dtype == K.dtype == V.dtype:
+        raise ValueError("Q, K and V disagree in batch, head dim or dtype")
+    if packed and (seq_q is None or seq_k is None or seq_q.shape != seq_k.shape or seq_q.dim() != 1
+                   or seq_q.numel() < 2):
+        raise ValueError("packed sequences need offsets seq_q and seq_k, [n + 1] each")
+    for t in (seq_q, seq_k):
+        if t is not None and (t.dtype != torch.int32 or (not packed and tuple(t.shape) != (B,))):
+            raise ValueError("seq_q and seq_k must be int32, one length per batch row unless packed")
+    with _side(stream):
+        o = out if out is not None else torch.empty_like(Q)
+        lse = lse_out if lse_out is not None else torch.empty(B, Hq, Tq, dtype=torch.float32,
+                                                              device=Q.device)
+    if o.shape != Q.shape or o.dtype != Q.dtype:
+        raise ValueError("out must match Q")
+    if tuple(lse.shape) != (B, Hq, Tq) or lse.dtype != torch.float32:
+        raise ValueError("lse_out must be [B][Hq][Tq] float32")
+    _strided(Q, K, V, o)
+    _dev(seq_q, seq_k, lse, workspace, dev_status)
+    if scale is None:
+        scale = d ** -0.5
+    n_seq = seq_q.numel() - 1 if packed else 0
+    strides = (ctypes.c_int64 * 12)(*[t.stride(i) for t in (Q, K, V, o) for i in range(3)])
+    with _side(stream):
+        ws, nbytes = _workspace(kv_workspace_size(KV_OP_ATTN_PROMPT, B, Hq, Hkv, max(1, Tk), d, Tq, n_seq),
+                                Q.device, workspace)
+    _check("kv_attn_prompt", _lib.kv_attn_prompt(
+        _ptr(Q), _ptr(K), _ptr(V), B, Hq, Hkv, Tq, Tk, d, strides, _ptr(seq_q), _ptr(seq_k), n_seq,
+        float(scale), _dtype_code(Q), _ptr(o), _ptr(lse), _ptr(ws), nbytes, _ptr(dev_status),
+        _stream(stream)))
+    return o, lse
+
+
+_Q8_CODES = {torch.int8: KV_Q8_S8, torch.float8_e4m3fn: KV_Q8_E4M3}
+
+
+def q8_cache(B: int, Hkv: int, cap: int, d: int, block: int = 64, dtype=torch.bfloat16,
+             codes=torch.int8, device="cuda"):
+    """An empty 8-bit slot cache: a dict of the codes K, V [B][Hkv][cap][d] (torch.int8 or
+    torch.float8_e4m3fn), their scales Ks, Vs [B][Hkv][cap / block] float32, the unfinished
+    block's rows Kt, Vt [B][Hkv][block][d] in `dtype`, pos, acc [B][Hkv][cap] and len [B][Hkv].
+    `cap` is a multiple of `block` (32, 64 or 128)."""
+    if codes not in _Q8_CODES:
+        raise TypeError("codes must be torch.int8 or torch.float8_e4m3fn")
+    if cap % block:
+        raise ValueError("cap must be a multiple of block")
+    z = lambda *shape, dtype=torch.float32: torch.zeros(*shape, dtype=dtype, device=device)  # noqa: E731
+    return {"K": z(B, Hkv, cap, d, dtype=torch.uint8).view(codes), "Ks": z(B, Hkv, cap // block),
+            "V": z(B, Hkv, cap, d, dtype=torch.uint8).view(codes), "Vs": z(B, Hkv, cap // block),
+            "Kt": z(B, Hkv, block, d, dtype=dtype), "Vt": z(B, Hkv, block, d, dtype=dtype),
+            "pos": z(B, Hkv, cap, dtype=torch.int32), "acc": z(B, Hkv, cap),
+            "len": z(B, Hkv, dtype=torch.int32)}
+
+
+def _q8(c) -> _Q8Cache:
+    K, Kt = c["K"], c["Kt"]
+    if K.dim() != 4 or Kt.dim() != 4 or K.dtype not in _Q8_CODES:
+        raise ValueError("not an 8-bit slot cache: see q8_cache")
+    B, H, cap, d = K.shape
+    block = Kt.shape[2]
+    acc = c.get("acc")
+    want = {"V": ((B, H, cap, d), K.dtype), "Ks": ((B, H, cap // max(1, block)), torch.float32),
+            "Vs": ((B, H, cap // max(1, block)), torch.float32), "Kt": ((B, H, block, d), Kt.dtype),
+            "Vt": ((B, H, block, d), Kt.dtype), "pos": ((B, H, cap), torch.int32),
+            "acc": ((B, H, cap), torch.float32), "len": ((B, H), torch.int32)}
+    for name, (shape, dtype) in want.items():
+        t = c[name] if name != "acc" else acc
+        if t is not None and (tuple(t.shape) != shape or t.dtype != dtype):
+            raise ValueError(f"8-bit slot cache: {name} must be {list(shape)} {dtype}")
+    _dev(K, c["V"], c["Ks"], c["Vs"], Kt, c["Vt"], c["pos"], acc, c["len"])
+    return _Q8Cache(*[c[n].data_ptr() for n in ("K", "V", "Ks", "Vs", "Kt", "Vt", "pos")],
+                    None if acc is None else acc.data_ptr(), c["len"].data_ptr(), B, H, cap, d, block,
+                    _dtype_code(Kt), _Q8_CODES[K.dtype])
+
+
+def kv_compact_q8(K: torch.Tensor, V: torch.Tensor, s, idx, cache, dev_status=None, stream=None):
+    """The kept rows of a prompt into an 8-bit slot cache (see q8_cache): K, V [B][Hkv][T][d]
+    (CUDA or pinned host), s [B][Hkv][T] float32 or None, idx [B][Hkv][k] int32 ascending or None
+    (every row).  Returns `cache`, whose slots 0..k-1 and len are written."""
+    c = _q8(cache)
+    B, H, T, d = K.shape
+    if V.shape != K.shape or V.dtype != K.dtype or (B, H, d) != (c.B, c.Hkv, c.d) \
+            or K.dtype != cache["Kt"].dtype:
+        raise ValueError("K, V and the cache disagree in batch, heads, head dim or dtype")
+    if idx is not None and (idx.dtype != torch.int32 or idx.dim() != 3 or tuple(idx.shape[:2]) != (B, H)):
+        raise ValueError("idx must be [B][Hkv][k] int32")
+    if s is not None and (s.dtype != torch.float32 or tuple(s.shape) != (B, H, T)):
+        raise ValueError("s must be [B][Hkv][T] float32")
+    _dev(s, idx, dev_status)
+    _dev_or_pinned(K, V)
+    k = T if idx is None else idx.shape[-1]
+    _check("kv_compact_q8", _lib.kv_compact_q8(_ptr(K), _ptr(V), _ptr(s), _ptr(idx), T, k,
+                                               ctypes.byref(c), _ptr(dev_status), _stream(stream)))
+    return cache
+
+
+def h2o_decode_step_q8(q, k_new, v_new, cache, new_pos, scale: float | None = None, len_out=None,
+                       o_out=None, workspace=None, dev_status=None, stream=None):
+    """One decode step over an 8-bit slot cache, updated in place; returns o [B][Hq][d] float32.
+
+    q [B][Hq][d], k_new, v_new [B][Hkv][d]; new_pos an int, or an int32 CUDA tensor [B] of
+    positions.  No slot is evicted: a unit must have room (len < cap; kv_evict_q8 makes it).
+    len_out [B][Hkv] int32 (default cache["len"]) receives len + 1."""
+    c = _q8(cache)
+    B, Hq, d = q.shape
+    kv = (c.B, c.Hkv, c.d)
+    if (B, d) != (c.B, c.d) or tuple(k_new.shape) != kv or tuple(v_new.shape) != kv \
+            or not q.dtype == k_new.dtype == v_new.dtype == cache["Kt"].dtype:
+        raise ValueError("q, k_new, v_new and the cache disagree in batch, heads, head dim or dtype")
+    row_pos = new_pos if isinstance(new_pos, torch.Tensor) else None
+    if row_pos is not None and (row_pos.dtype != torch.int32 or tuple(row_pos.shape) != (B,)):
+        raise ValueError("new_pos must be an int or [B] int32")
+    ln = cache["len"] if len_out is None else len_out
+    if ln.dtype != torch.int32 or tuple(ln.shape) != (c.B, c.Hkv):
+        raise ValueError("len_out must be [B][Hkv] int32")
+    with _side(stream):
+        o = o_out if o_out is not None else torch.empty(B, Hq, d, dtype=torch.float32, device=q.device)
+        ws, nbytes = _workspace(kv_workspace_size(KV_OP_DECODE_Q8, B, Hq, c.Hkv, c.cap, d), q.device, workspace)
+    if tuple(o.shape) != (B, Hq, d) or o.dtype != torch.float32:
+        raise ValueError("o_out must be [B][Hq][d] float32")
+    _dev(q, k_new, v_new, row_pos, ln, o, workspace, dev_status)
+    if scale is None:
+        scale = d ** -0.5
+    _check("h2o_decode_step_q8", _lib.h2o_decode_step_q8(
+        _ptr(q), _ptr(k_new), _ptr(v_new), ctypes.byref(c), Hq, 0 if row_pos is not None else int(new_pos),
+        _ptr(row_pos), _ptr(ln), float(scale), _ptr(o), _ptr(ws), nbytes, _ptr(dev_status),
+        _stream(stream)))
+    return o
+
+
+def kv_evict_q8(cache, keep: int, recent: int, into, sink: int = 0, idx_out=None, dev_status=None,
+                stream=None):
+    """Every unit of an 8-bit slot cache down to its `keep` slots with the most accumulated
+    attention (its last `recent` slots and positions below `sink` always stay), moved together
+    into the cache `into`; `cache` itself is left as it was.  Returns idx [B][Hkv][keep] int32, the
+    slot that each new slot came from (-1 behind the new len)."""
+    c, out = _q8(cache), _q8(into)
+    if cache.get("acc") is None or into.get("acc") is None:
+        raise ValueError("eviction needs the caches' accumulated attention")
+    with _side(stream):
+        idx = idx_out if idx_out is not None else torch.empty(c.B, c.Hkv, keep, dtype=torch.int32,
+                                                              device=cache["K"].device)
+    if idx.dtype != torch.int32 or tuple(idx.shape) != (c.B, c.Hkv, keep):
+        raise ValueError("idx_out must be [B][Hkv][keep] int32")
+    _dev(idx, dev_status)
+    _check("kv_evict_q8", _lib.kv_evict_q8(ctypes.byref(c), int(keep), int(recent), int(sink), _ptr(idx),
+                                           ctypes.byref(out), _ptr(dev_status), _stream(stream)))
+    return idx
+
+
+def compress_prefill_q8(Q, K, V, W: int, k: int, recent: int, r: float | None, cap: int | None = None,
+                        block: int = 64, codes=torch.int8, gamma: float = 0.5, pool_width: int = 5,
+                        beta_lo: float = 0.8, beta_hi: float = 1.2, scale: float | None = None, stream=None):
+    """A prompt's attention and its compressed 8-bit cache: attention of all T queries Q
+    [B][Hq][T][d] over K, V [B][Hkv][T][d], then the eviction chain scored by the last W of them
+    (score -> HubKV refine, unless r is None -> Top-K -> compact into codes).
+
+    Returns (o, lse, cache); cache has `cap` slots (default: k rounded up to whole blocks)."""
+    T = K.shape[2]
+    with _side(stream):
+        o, lse = kv_attn_prompt(Q, K, V, scale)
+        s = kv_score_obs(Q[:, :, T - W:].contiguous(), K, scale)
+        idx = (kv_select_topk(s, k, recent) if r is None else
+               hubkv_select_topk(s, k, recent, r, gamma, pool_width, beta_lo, beta_hi))
+        cap = (k + block - 1) // block * block if cap is None else cap
+        cache = q8_cache(K.shape[0], K.shape[1], cap, K.shape[3], block, K.dtype, codes, K.device)
+        return o, lse, kv_compact_q8(K, V, s, idx, cache)
 
 
 def prefill_host_buffers(hQ: torch.Tensor, hK: torch.Tensor, k: int, r: float | None,

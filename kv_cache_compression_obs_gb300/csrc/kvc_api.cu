@@ -184,6 +184,22 @@ int decode_run(const void *q, const void *k_new, const void *v_new, int n_steps,
   return rc;
 }
 
+// Geometry of an 8-bit cache: KV_OK or the status to return.
+int check_q8_shape(const kv_q8_cache *c) {
+  if (!c || c->B < 0 || c->Hkv <= 0 || c->cap <= 0 || c->block <= 0 || c->cap % c->block != 0 || !dtype_ok(c->dtype) ||
+      !(c->format == KV_Q8_S8 || c->format == KV_Q8_E4M3))
+    return KV_ERR_INVALID_ARG;
+  if (!dim_ok(c->d) || !(c->block == 32 || c->block == 64 || c->block == 128)) return KV_ERR_UNSUPPORTED;
+  if (!fits((long long)c->B * c->Hkv, (long long)c->cap * c->d)) return KV_ERR_INVALID_ARG;
+  return KV_OK;
+}
+bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+bool q8_pointers_ok(const kv_q8_cache *c) {
+  return c->K && c->V && c->Ks && c->Vs && c->Kt && c->Vt && c->pos && c->len && aligned16(c->K) && aligned16(c->V) &&
+         aligned16(c->Kt) && aligned16(c->Vt) && aligned4(c->Ks) && aligned4(c->Vs) && aligned4(c->pos) &&
+         aligned4(c->acc) && aligned4(c->len);
+}
+
 }  // namespace
 
 extern "C" {
@@ -230,6 +246,12 @@ size_t kv_workspace_size(int op, int B, int Hq, int Hkv, int T, int d, int W, in
     case KV_OP_DECODE:  // T is the slot capacity
       if (Hq <= 0 || Hkv <= 0 || Hq % Hkv || !(d == 64 || d == 128)) return 0;
       return decode_ws_split(B, Hkv, Hq / Hkv, T, d);
+    case KV_OP_ATTN_PROMPT:  // T is Tk, W is Tq, k is n_seq
+      if (Hq <= 0 || Hkv <= 0 || Hq % Hkv || W < 0 || k < 0 || !(d == 64 || d == 128)) return 0;
+      return attn_prompt_workspace_bytes(B, Hq, Hkv, W, T, d, k);
+    case KV_OP_DECODE_Q8:  // T is the slot capacity
+      if (Hq <= 0 || Hkv <= 0 || Hq % Hkv || !(d == 64 || d == 128)) return 0;
+      return decode_q8_workspace_bytes((long)B * Hkv, Hq / Hkv, T, d);
     default:
       return 0;
   }
@@ -440,6 +462,89 @@ int h2o_decode_step(const void *q, const void *k_new, const void *v_new, void *K
   return h2o_decode_step_ex(q, k_new, v_new, K_cache, V_cache, pos, acc, len, B, Hq, Hkv, cap, d,
                             recent, 0, new_pos, scale, flags, dtype, o_out, evicted_pos, workspace,
                             workspace_bytes, dev_status, stream);
+}
+
+int kv_attn_prompt(const void *Q, const void *K, const void *V, int B, int Hq, int Hkv, int Tq, int Tk,
+                   int d, const int64_t *strides, const int32_t *seq_q, const int32_t *seq_k, int n_seq,
+                   float scale, int dtype, void *O, float *lse_out, void *workspace, size_t workspace_bytes,
+                   int *dev_status, kv_stream_t stream) {
+  if (B < 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0 || Tq < 0 || Tk < 0 || n_seq < 0 || !dtype_ok(dtype) ||
+      !(scale == scale) || (n_seq > 0 && (B != 1 || !seq_q || !seq_k)))
+    return KV_ERR_INVALID_ARG;
+  if (!dim_ok(d)) return KV_ERR_UNSUPPORTED;
+  if (!fits((long long)B * Hq, (long long)Tq * d) || !fits((long long)B * Hkv, (long long)Tk * d))
+    return KV_ERR_INVALID_ARG;
+  if (B == 0 || Tq == 0) return KV_OK;
+  AttnShape S{B, Hq, Hkv, Tq, Tk, d, n_seq, {}, {}, {}, {}, seq_q, seq_k};
+  long long *const st[4] = {S.q, S.k, S.v, S.o};
+  const int eb = dtype == KV_F32 ? 4 : 2;
+  for (int i = 0; i < 4; ++i) {
+    const long long H = (i == 0 || i == 3) ? Hq : Hkv, T = (i == 0 || i == 3) ? Tq : Tk;
+    const long long dense[3] = {H * T * d, T * d, d}, count[3] = {B, H, T};
+    for (int a = 0; a < 3; ++a) {
+      st[i][a] = strides ? strides[3 * i + a] : dense[a];
+      if (count[a] <= 1 || T == 0) st[i][a] = d;  // never stepped: any value will do
+      if (st[i][a] <= 0 || (st[i][a] * eb) % 16 != 0 || st[i][a] > (1LL << 38)) return KV_ERR_INVALID_ARG;
+    }
+  }
+  if (!Q || !O || !aligned16(Q) || !aligned16(O) || (Tk > 0 && (!K || !V)) || !aligned16(K) || !aligned16(V) ||
+      !aligned4(lse_out) || !aligned4(seq_q) || !aligned4(seq_k))
+    return KV_ERR_INVALID_ARG;
+  const size_t need = attn_prompt_workspace_bytes(B, Hq, Hkv, Tq, Tk, d, n_seq);
+  if (need && (!workspace || workspace_bytes < need || !aligned16(workspace))) return KV_ERR_WORKSPACE;
+  return launch_attn_prompt(Q, K, V, S, scale, dtype, O, lse_out, workspace, dev_status,
+                            static_cast<cudaStream_t>(stream));
+}
+
+int kv_compact_q8(const void *K, const void *V, const float *s, const int32_t *idx, int T, int k,
+                  const kv_q8_cache *out, int *dev_status, kv_stream_t stream) {
+  const int rc = check_q8_shape(out);
+  if (rc != KV_OK) return rc;
+  if (T <= 0 || k <= 0 || k > T || k > out->cap || (!idx && k != T)) return KV_ERR_INVALID_ARG;
+  if (!fits((long long)out->B * out->Hkv, (long long)T * out->d)) return KV_ERR_INVALID_ARG;
+  if (out->B == 0) return KV_OK;
+  if (!K || !V || !aligned16(K) || !aligned16(V) || !aligned4(s) || !aligned4(idx) || !q8_pointers_ok(out))
+    return KV_ERR_INVALID_ARG;
+  return launch_compact_q8(K, V, s, idx, T, k, *out, dev_status, static_cast<cudaStream_t>(stream));
+}
+
+int h2o_decode_step_q8(const void *q, const void *k_new, const void *v_new, const kv_q8_cache *cache, int Hq,
+                       int32_t new_pos, const int32_t *row_pos, int32_t *len_out, float scale, float *o_out,
+                       void *workspace, size_t workspace_bytes, int *dev_status, kv_stream_t stream) {
+  const int rc = check_q8_shape(cache);
+  if (rc != KV_OK) return rc;
+  if (Hq <= 0 || Hq % cache->Hkv != 0 || !(scale == scale) || (!row_pos && new_pos < 0)) return KV_ERR_INVALID_ARG;
+  const int G = Hq / cache->Hkv;
+  if (G > 8) return KV_ERR_UNSUPPORTED;
+  if (cache->B == 0) return KV_OK;
+  if (!q || !k_new || !v_new || !len_out || !o_out || !aligned16(q) || !aligned16(k_new) || !aligned16(v_new) ||
+      !aligned4(o_out) || !aligned4(len_out) || !aligned4(row_pos) || !q8_pointers_ok(cache))
+    return KV_ERR_INVALID_ARG;
+  if (!workspace || !aligned16(workspace) ||
+      workspace_bytes < decode_q8_workspace_bytes((long)cache->B * cache->Hkv, G, cache->cap, cache->d))
+    return KV_ERR_WORKSPACE;
+  return launch_decode_q8(q, k_new, v_new, *cache, Hq, new_pos, row_pos, len_out, scale, o_out, workspace,
+                          dev_status, static_cast<cudaStream_t>(stream));
+}
+
+int kv_evict_q8(const kv_q8_cache *cache, int keep, int recent, int sink, int32_t *idx_out,
+                const kv_q8_cache *out, int *dev_status, kv_stream_t stream) {
+  int rc = check_q8_shape(cache);
+  if (rc == KV_OK) rc = check_q8_shape(out);
+  if (rc != KV_OK) return rc;
+  if (recent < 0 || sink < 0 || (long long)recent + sink >= keep || keep > out->cap || out->B != cache->B ||
+      out->Hkv != cache->Hkv || out->d != cache->d || out->block != cache->block || out->dtype != cache->dtype ||
+      out->format != cache->format || !fits((long long)cache->B * cache->Hkv, keep))
+    return KV_ERR_INVALID_ARG;
+  if (cache->B == 0) return KV_OK;
+  if (!idx_out || !aligned4(idx_out) || !q8_pointers_ok(cache) || !q8_pointers_ok(out) || !cache->acc || !out->acc)
+    return KV_ERR_INVALID_ARG;
+  const void *const a[9] = {cache->K,  cache->V,  cache->Ks,  cache->Vs, cache->Kt,
+                            cache->Vt, cache->pos, cache->acc, cache->len};
+  const void *const b[9] = {out->K, out->V, out->Ks, out->Vs, out->Kt, out->Vt, out->pos, out->acc, out->len};
+  for (int i = 0; i < 9; ++i)
+    if (a[i] == b[i]) return KV_ERR_INVALID_ARG;  // the source is read while the destination is written
+  return launch_evict_q8(*cache, keep, recent, sink, idx_out, *out, dev_status, static_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"

@@ -140,4 +140,23 @@ int launch_decode_step(const void *q, const void *k_new, const void *v_new, void
                        int *dev_status, cudaStream_t st);
 size_t decode_workspace_bytes(long units, int G, int cap, int d);
 
+// Element strides and sequence lengths of a prompt attention call.
+struct AttnShape {
+  int B, Hq, Hkv, Tq, Tk, d, n_seq;
+  long long q[3], k[3], v[3], o[3];  // batch, head, token
+  const int32_t *seq_q, *seq_k;
+};
+int launch_attn_prompt(const void *Q, const void *K, const void *V, const AttnShape &S, float scale, int dtype,
+                       void *O, float *lse, void *ws, int *status, cudaStream_t st);
+size_t attn_prompt_workspace_bytes(int B, int Hq, int Hkv, int Tq, int Tk, int d, int n_seq);
+
+int launch_compact_q8(const void *K, const void *V, const float *s, const int32_t *idx, int T, int k,
+                      const kv_q8_cache &out, int *status, cudaStream_t st);
+int launch_evict_q8(const kv_q8_cache &from, int keep, int recent, int sink, int32_t *idx,
+                    const kv_q8_cache &out, int *status, cudaStream_t st);
+int launch_decode_q8(const void *q, const void *k_new, const void *v_new, const kv_q8_cache &c, int Hq,
+                     int32_t new_pos, const int32_t *row_pos, int32_t *len_out, float scale, float *o, void *ws,
+                     int *status, cudaStream_t st);
+size_t decode_q8_workspace_bytes(long units, int G, int cap, int d);
+
 }  // namespace kvc

@@ -1,0 +1,565 @@
+// q8_decode.cu -- one decode step over the 8-bit slot cache (H2O page, 问题形式化:
+// attention renormalised over the kept keys; 贪心驱逐算法: the softmax accumulates
+// into a per-token score).
+//
+// A unit is (b, KV head); its rows are the n cached slots and the new token (row n).
+// With codes c and block scales a (q8_common.cuh), for the G query heads of a unit:
+//     l_gj = scale a_j <q_g, c_j>,  P_g = softmax_j(l_gj),  o_g = sum_j P_gj b_j v_j,
+//     acc_j += sum_g P_gj  (the new token's starts with its own sum).
+// Two launches:
+//
+//   stream   -- the codes of the full blocks in ns splits per unit, one CTA each,
+//               and one more CTA per unit for the unfinished block's rows and the
+//               new token.  A warp takes 16 slots at a time and feeds them to
+//               mma.m16n8k16 straight from registers: codes are exact in fp16, so
+//               an int8 becomes 1024 + 128 + c by a byte permutation and a packed
+//               subtraction, an e4m3 by the hardware conversion.  Which element of
+//               d stands at which k of the product is free as long as both operands
+//               agree, so every lane loads 16 consecutive bytes and no shared memory
+//               or transposition is needed: for K the k index runs over d, for V over
+//               the slots, two neighbouring slots' bytes interleaved.
+//               fp32 accuracy: the queries and the weights P enter as hi + lo pairs of
+//               fp16 (22 bits; each scaled by a power of two so that nothing that
+//               matters is subnormal) in neighbouring columns of the 8-column operand:
+//               columns 2i, 2i+1 are query i's hi and lo, and a lane's two
+//               accumulators of a row add up to the result.  Four queries fill one
+//               operand; five to eight take two.
+//               Logits (log2 units) also go to the workspace.
+//   finalize -- combines the splits into o, turns the stored logits into
+//               probabilities and adds them to acc, and quantises the unfinished
+//               block when the new token fills it.
+#include <cuda_fp16.h>
+
+#include <cmath>
+
+#include "q8_common.cuh"
+#include "tc_common.cuh"
+
+namespace kvc {
+namespace {
+
+constexpr int NW = 4;            // warps of a stream CTA
+constexpr int NT = 32 * NW;
+constexpr int NTF = 256;         // finalize threads
+constexpr int SLOTS_F = 1024;    // slots per finalize CTA
+constexpr float kLazy = 6.f;     // log2 units a logit may pass the running reference by
+constexpr int kMinExp = -118;    // smallest exponent of a V scale that is told apart (2^(8 + 118) is finite)
+constexpr int kPScale = 8;       // weights enter the product as P 2^kPScale (at most 2^(6 + 8 + 1))
+
+struct DecArgs {
+  const void *q, *k_new, *v_new;
+  kv_q8_cache c;
+  const int32_t *row_pos;
+  int32_t new_pos;
+  int32_t *len_out;
+  int Hq, G, ns;
+  float c_log2;      // scale log2(e)
+  float *o;
+  float *lgw;        // [units][cap + 1][G] logits
+  float2 *pmz;       // [units][ns + 1][G] max and normaliser
+  float *po;         // [units][ns + 1][G][d]
+  int32_t *nsave;    // [units] len at entry, -1 when out of range
+  int *status;
+};
+
+// slots [k0, k1) of split s of a unit with nf slots in full blocks
+__device__ __forceinline__ int split_len(int nf, int ns) { return ((nf + ns - 1) / ns + 63) & ~63; }
+
+template <int FMT>
+__device__ __forceinline__ uint32_t to_half2_lo(uint32_t w);  // codes 0, 1 of a word
+template <int FMT>
+__device__ __forceinline__ uint32_t to_half2_hi(uint32_t w);  // codes 2, 3
+
+__device__ __forceinline__ uint32_t sub_bias(uint32_t h) {
+  uint32_t r;
+  asm("sub.f16x2 %0, %1, %2;" : "=r"(r) : "r"(h), "r"(0x64806480u));  // (1024 + 128 + c) - 1152
+  return r;
+}
+__device__ __forceinline__ uint32_t cvt_e4m3(uint32_t two) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"((unsigned short)two));
+  return r;
+}
+// int8 words arrive with every sign bit flipped (c + 128)
+template <> __device__ __forceinline__ uint32_t to_half2_lo<KV_Q8_S8>(uint32_t w) {
+  return sub_bias(__byte_perm(w, 0x64646464u, 0x4140));
+}
+template <> __device__ __forceinline__ uint32_t to_half2_hi<KV_Q8_S8>(uint32_t w) {
+  return sub_bias(__byte_perm(w, 0x64646464u, 0x4342));
+}
+template <> __device__ __forceinline__ uint32_t to_half2_lo<KV_Q8_E4M3>(uint32_t w) { return cvt_e4m3(w); }
+template <> __device__ __forceinline__ uint32_t to_half2_hi<KV_Q8_E4M3>(uint32_t w) { return cvt_e4m3(w >> 16); }
+template <int FMT> __device__ __forceinline__ uint32_t fix(uint32_t w) {
+  return FMT == KV_Q8_S8 ? w ^ 0x80808080u : w;
+}
+
+__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                         uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t r;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
+}
+__device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t *>(&h);
+}
+__device__ __forceinline__ float exp2i(int e) { return __int_as_float((e + 127) << 23); }  // -126 <= e <= 127
+
+// The largest |x| of a query row -> the exponent e with max 2^e in [2^13, 2^14).
+__device__ __forceinline__ int query_shift(float big) {
+  if (!(big > 0.f)) return 0;
+  int ex;
+  frexpf(big, &ex);  // big = f 2^ex, 0.5 <= f < 1
+  return max(-126, min(126, 14 - ex));
+}
+
+// ---- the unfinished block's rows and the new token ------------------------------------
+template <typename T, int D>
+__device__ void tail_part(const DecArgs &A, long u, int n, float *sm) {
+  const int G = A.G, block = A.c.block;
+  const int nf = n / block * block, rows = n - nf + 1;  // at most block
+  float *qs = sm;                 // [G][D], premultiplied by scale log2(e)
+  float *ps = qs + 8 * D;         // [G][128]
+  const T *q = static_cast<const T *>(A.q) + u * (long)G * D;
+  const T *kn = static_cast<const T *>(A.k_new) + u * (long)D, *vn = static_cast<const T *>(A.v_new) + u * (long)D;
+  T *kt = static_cast<T *>(A.c.Kt) + u * (long)block * D, *vt = static_cast<T *>(A.c.Vt) + u * (long)block * D;
+  for (int i = threadIdx.x; i < G * D; i += NT) qs[i] = to_f32(q[i]) * A.c_log2;
+  for (int i = threadIdx.x; i < D; i += NT) {  // append: nobody reads this row as a cached one
+    kt[(long)(rows - 1) * D + i] = kn[i];
+    vt[(long)(rows - 1) * D + i] = vn[i];
+  }
+  if (threadIdx.x == 0) A.c.pos[u * (long)A.c.cap + n] = A.row_pos ? A.row_pos[u / A.c.Hkv] : A.new_pos;
+  __syncthreads();
+  if ((int)threadIdx.x < rows) {
+    const T *k = (int)threadIdx.x == rows - 1 ? kn : kt + (long)threadIdx.x * D;
+    float l[8];
+#pragma unroll
+    for (int g = 0; g < 8; ++g) l[g] = 0.f;
+    for (int e = 0; e < D; e += 16) {
+      float x[16];
+      load16(k + e, x);
+#pragma unroll
+      for (int g = 0; g < 8; ++g)
+        if (g < G) {
+          const float4 *q4 = reinterpret_cast<const float4 *>(qs + g * D + e);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float4 y = q4[i];
+            l[g] += x[4 * i] * y.x + x[4 * i + 1] * y.y + x[4 * i + 2] * y.z + x[4 * i + 3] * y.w;
+          }
+        }
+    }
+#pragma unroll
+    for (int g = 0; g < 8; ++g)
+      if (g < G) {
+        ps[g * 128 + threadIdx.x] = l[g];
+        if (A.c.acc) A.lgw[(u * (long)(A.c.cap + 1) + nf + threadIdx.x) * G + g] = l[g];
+      }
+  }
+  __syncthreads();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  for (int g = warp; g < G; g += NW) {
+    float m = -INFINITY;
+    for (int i = lane; i < rows; i += 32) m = fmaxf(m, ps[g * 128 + i]);
+    for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+    float z = 0.f;
+    for (int i = lane; i < rows; i += 32) {
+      const float p = exp2f(ps[g * 128 + i] - m);
+      ps[g * 128 + i] = p;
+      z += p;
+    }
+    for (int o = 16; o; o >>= 1) z += __shfl_xor_sync(0xFFFFFFFFu, z, o);
+    if (lane == 0) A.pmz[(u * (A.ns + 1) + A.ns) * G + g] = make_float2(m, z);
+  }
+  __syncthreads();
+  for (int e = threadIdx.x; e < D; e += NT) {
+    float o[8];
+#pragma unroll
+    for (int g = 0; g < 8; ++g) o[g] = 0.f;
+#pragma unroll 8
+    for (int i = 0; i < rows; ++i) {
+      const float v = to_f32(i == rows - 1 ? vn[e] : vt[(long)i * D + e]);
+#pragma unroll
+      for (int g = 0; g < 8; ++g)
+        if (g < G) o[g] += ps[g * 128 + i] * v;
+    }
+#pragma unroll
+    for (int g = 0; g < 8; ++g)
+      if (g < G) A.po[((u * (A.ns + 1) + A.ns) * G + g) * D + e] = o[g];
+  }
+}
+
+// ---- stream -----------------------------------------------------------------------------
+// NSET operands of four queries each; D head dim.
+template <typename T, int FMT, int D, int NSET>
+__global__ void __launch_bounds__(NT) q8_stream_kernel(const __grid_constant__ DecArgs A) {
+  constexpr int VB = D / 8;       // V bytes per lane and slot
+  constexpr int MT = D / 16;      // 16-row tiles of V^T
+  constexpr int NCH = D / 64;     // 64-byte chunks of a K row
+  __shared__ __align__(16) float sm[8 * 128 + 8 * 128];
+  extern __shared__ float so[];   // [NW][G][D]
+  const long u = blockIdx.x / (A.ns + 1);
+  const int s = blockIdx.x % (A.ns + 1);
+  const int G = A.G, block = A.c.block;
+  const int n = A.c.len[u];
+  if (n < 0 || n >= A.c.cap) {
+    if (s == A.ns && threadIdx.x == 0) {
+      A.nsave[u] = -1;
+      if (A.status) atomicExch(A.status, (int)KV_ERR_INVALID_ARG);
+    }
+    return;
+  }
+  if (s == A.ns) {
+    if (threadIdx.x == 0) A.nsave[u] = n;
+    tail_part<T, D>(A, u, n, sm);
+    return;
+  }
+  const int nf = n / block * block;
+  const int per = split_len(nf, A.ns);
+  const int k0 = s * per, k1 = min(nf, k0 + per);
+  if (k0 >= k1) return;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int g = lane >> 2, t = lane & 3;
+
+  // queries: column 2i hi, 2i + 1 lo of query i of the set; this lane holds column g
+  uint32_t qb[NSET][NCH * 4][2];
+  float qf[NSET];  // query t's factor back to log2 units
+#pragma unroll
+  for (int st = 0; st < NSET; ++st) {
+    const int qi = st * 4 + (g >> 1);
+    const T *q = static_cast<const T *>(A.q) + (u * G + min(qi, G - 1)) * (long)D;
+    float x[NCH][16];
+    float big = 0.f;
+#pragma unroll
+    for (int c = 0; c < NCH; ++c) {
+      load16(q + c * 64 + t * 16, x[c]);
+      big = fmaxf(big, max_abs16(x[c]));
+    }
+    big = fmaxf(big, __shfl_xor_sync(0xFFFFFFFFu, big, 1));
+    big = fmaxf(big, __shfl_xor_sync(0xFFFFFFFFu, big, 2));
+    const int sh = query_shift(big);
+    const float f = exp2i(sh);
+    // query t's shift sits in the lanes with g = 2t
+    qf[st] = A.c_log2 * exp2i(-__shfl_sync(0xFFFFFFFFu, sh, 8 * t));
+#pragma unroll
+    for (int c = 0; c < NCH; ++c)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+          const float a = x[c][4 * i + 2 * p] * f, b = x[c][4 * i + 2 * p + 1] * f;
+          const uint32_t hi = pack_half2(a, b);
+          const float2 back = __half22float2(*reinterpret_cast<const __half2 *>(&hi));
+          const uint32_t lo = pack_half2(a - back.x, b - back.y);
+          qb[st][c * 4 + i][p] = qi < G ? ((g & 1) ? lo : hi) : 0u;
+        }
+  }
+  float o[NSET][MT][4], m[NSET], z[NSET];
+#pragma unroll
+  for (int st = 0; st < NSET; ++st) {
+    m[st] = -INFINITY;
+    z[st] = 0.f;
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) o[st][i][j] = 0.f;
+  }
+  int rv = kMinExp;  // o stands for o 2^(rv - kPScale)
+  const uint8_t *kc = static_cast<const uint8_t *>(A.c.K) + u * (long)A.c.cap * D;
+  const uint8_t *vc = static_cast<const uint8_t *>(A.c.V) + u * (long)A.c.cap * D;
+  const float *ks = A.c.Ks + u * (long)(A.c.cap / block), *vs = A.c.Vs + u * (long)(A.c.cap / block);
+  float *lg = A.lgw + u * (long)(A.c.cap + 1) * G;
+
+  for (int j = k0 + warp * 16; j < k1; j += NW * 16) {
+    uint4 kw[2][NCH];
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int c = 0; c < NCH; ++c)
+        kw[h][c] = __ldcs(reinterpret_cast<const uint4 *>(kc + (long)(j + g + 8 * h) * D + c * 64 + t * 16));
+    uint32_t vw[4][VB / 4];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const uint8_t *p = vc + (long)(j + 2 * t + (r & 1) + 8 * (r >> 1)) * D + g * VB;
+      if constexpr (VB == 16) {
+        const uint4 w = __ldcs(reinterpret_cast<const uint4 *>(p));
+        vw[r][0] = fix<FMT>(w.x);
+        vw[r][1] = fix<FMT>(w.y);
+        vw[r][2] = fix<FMT>(w.z);
+        vw[r][3] = fix<FMT>(w.w);
+      } else {
+        const uint2 w = __ldcs(reinterpret_cast<const uint2 *>(p));
+        vw[r][0] = fix<FMT>(w.x);
+        vw[r][1] = fix<FMT>(w.y);
+      }
+    }
+    const float ak = ks[j / block], av = vs[j / block];
+
+    float sc[NSET][4];
+#pragma unroll
+    for (int st = 0; st < NSET; ++st)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) sc[st][i] = 0.f;
+#pragma unroll
+    for (int c = 0; c < NCH; ++c) {
+      const uint32_t w0[4] = {kw[0][c].x, kw[0][c].y, kw[0][c].z, kw[0][c].w};
+      const uint32_t w1[4] = {kw[1][c].x, kw[1][c].y, kw[1][c].z, kw[1][c].w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t x0 = fix<FMT>(w0[i]), x1 = fix<FMT>(w1[i]);
+        const uint32_t a0 = to_half2_lo<FMT>(x0), a1 = to_half2_lo<FMT>(x1);
+        const uint32_t a2 = to_half2_hi<FMT>(x0), a3 = to_half2_hi<FMT>(x1);
+#pragma unroll
+        for (int st = 0; st < NSET; ++st)
+          mma16816(sc[st], a0, a1, a2, a3, qb[st][c * 4 + i][0], qb[st][c * 4 + i][1]);
+      }
+    }
+    // logits of query t (+ 4 st) for slots j + g and j + g + 8
+    float l0[NSET], l1[NSET];
+    bool over = false;
+#pragma unroll
+    for (int st = 0; st < NSET; ++st) {
+      const float f = qf[st] * ak;
+      l0[st] = (sc[st][0] + sc[st][1]) * f;
+      l1[st] = (sc[st][2] + sc[st][3]) * f;
+      const int qi = st * 4 + t;
+      if (A.c.acc && qi < G) {
+        lg[(long)(j + g) * G + qi] = l0[st];
+        lg[(long)(j + g + 8) * G + qi] = l1[st];
+      }
+      over |= fmaxf(l0[st], l1[st]) > m[st] + kLazy;
+    }
+    const int ev = max(kMinExp, min(126, ilogbf(av)));
+    if (__any_sync(0xFFFFFFFFu, over) || ev > rv) {
+      const int drv = ev > rv ? rv - ev : 0;
+      rv = max(rv, ev);
+      const float fv = drv < -126 ? 0.f : exp2i(drv);
+#pragma unroll
+      for (int st = 0; st < NSET; ++st) {
+        float mx = fmaxf(l0[st], l1[st]);
+        mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 4));
+        mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 8));
+        mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 16));
+        const float mn = fmaxf(m[st], mx);
+        const float f = exp2f(m[st] - mn);  // 0 on the first tile (m = -inf)
+        z[st] *= f;
+        m[st] = mn;
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+          for (int jj = 0; jj < 4; ++jj) o[st][i][jj] *= f * fv;
+      }
+    }
+    const float pf = av * exp2i(kPScale - rv);  // av 2^-rv below 2
+    uint32_t b0[NSET], b1[NSET];
+#pragma unroll
+    for (int st = 0; st < NSET; ++st) {
+      const float p0 = tc::ex2(l0[st] - m[st]), p1 = tc::ex2(l1[st] - m[st]);
+      z[st] += p0 + p1;
+      const float w0 = p0 * pf, w1 = p1 * pf;
+      const float h0 = __half2float(__float2half_rn(w0)), h1 = __half2float(__float2half_rn(w1));
+      b0[st] = transpose8x8(pack_half2(h0, w0 - h0));
+      b1[st] = transpose8x8(pack_half2(h1, w1 - h1));
+    }
+#pragma unroll
+    for (int w = 0; w < VB / 4; ++w) {
+      const uint32_t e0 = __byte_perm(vw[0][w], vw[1][w], 0x5140), e1 = __byte_perm(vw[0][w], vw[1][w], 0x7362);
+      const uint32_t f0 = __byte_perm(vw[2][w], vw[3][w], 0x5140), f1 = __byte_perm(vw[2][w], vw[3][w], 0x7362);
+      const uint32_t a0 = to_half2_lo<FMT>(e0), a1 = to_half2_hi<FMT>(e0);
+      const uint32_t a2 = to_half2_lo<FMT>(f0), a3 = to_half2_hi<FMT>(f0);
+      const uint32_t c0 = to_half2_lo<FMT>(e1), c1 = to_half2_hi<FMT>(e1);
+      const uint32_t c2 = to_half2_lo<FMT>(f1), c3 = to_half2_hi<FMT>(f1);
+#pragma unroll
+      for (int st = 0; st < NSET; ++st) {
+        mma16816(o[st][2 * w], a0, a1, a2, a3, b0[st], b1[st]);
+        mma16816(o[st][2 * w + 1], c0, c1, c2, c3, b0[st], b1[st]);
+      }
+    }
+  }
+
+  // combine the warps: sm holds m, z per (warp, query)
+  float *wm = sm, *wz = sm + NW * 8;
+  const float back = exp2i(rv - kPScale);
+#pragma unroll
+  for (int st = 0; st < NSET; ++st) {
+    float zz = z[st];
+    zz += __shfl_xor_sync(0xFFFFFFFFu, zz, 4);
+    zz += __shfl_xor_sync(0xFFFFFFFFu, zz, 8);
+    zz += __shfl_xor_sync(0xFFFFFFFFu, zz, 16);
+    if (g == 0) {
+      wm[warp * 8 + st * 4 + t] = m[st];
+      wz[warp * 8 + st * 4 + t] = zz;
+    }
+    const int qi = st * 4 + t;
+    if (qi < G) {
+      float *dst = so + (warp * G + qi) * D + g * VB;
+#pragma unroll
+      for (int i = 0; i < MT; ++i) {
+        dst[2 * i] = (o[st][i][0] + o[st][i][1]) * back;
+        dst[2 * i + 1] = (o[st][i][2] + o[st][i][3]) * back;
+      }
+    }
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < G * D; i += NT) {
+    const int qi = i / D;
+    float M = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < NW; ++w) M = fmaxf(M, wm[w * 8 + qi]);
+    float v = 0.f, Z = 0.f;
+#pragma unroll
+    for (int w = 0; w < NW; ++w) {
+      const float f = exp2f(wm[w * 8 + qi] - M);  // a warp without a tile: exp2(-inf) = 0, its o and z are 0
+      v += f * so[w * G * D + i];
+      Z += f * wz[w * 8 + qi];
+    }
+    A.po[(u * (A.ns + 1) + s) * (long)G * D + i] = v;
+    if (i % D == 0) A.pmz[(u * (A.ns + 1) + s) * G + qi] = make_float2(M, Z);
+  }
+}
+
+// ---- finalize -----------------------------------------------------------------------------
+template <typename T, int FMT>
+__global__ void __launch_bounds__(NTF) q8_finalize_kernel(const __grid_constant__ DecArgs A, int chunks) {
+  __shared__ float sM[8], sI[8];  // the unit's maximum and 1 / normaliser
+  __shared__ float red[32];
+  const int G = A.G, D = A.c.d, block = A.c.block, cap = A.c.cap;
+  const long u = blockIdx.x / chunks;
+  const int e = blockIdx.x % chunks;
+  const int n = A.nsave[u];
+  if (n < 0) return;
+  const int lo = e * SLOTS_F;
+  const bool fills = (n + 1) % block == 0;
+  if (e > 0 && lo > n) return;  // nothing left in this chunk (chunk 0 always has o to write)
+  const int nf = n / block * block;
+  const int per = split_len(nf, A.ns);
+  const int used = per ? (nf + per - 1) / per : 0;  // splits that hold rows
+  const float2 *mz = A.pmz + u * (A.ns + 1) * G;
+  if ((int)threadIdx.x < G) {
+    float M = mz[A.ns * G + threadIdx.x].x;
+    for (int s = 0; s < used; ++s) M = fmaxf(M, mz[s * G + threadIdx.x].x);
+    float Z = mz[A.ns * G + threadIdx.x].y * exp2f(mz[A.ns * G + threadIdx.x].x - M);
+    for (int s = 0; s < used; ++s) Z += mz[s * G + threadIdx.x].y * exp2f(mz[s * G + threadIdx.x].x - M);
+    sM[threadIdx.x] = M;
+    sI[threadIdx.x] = 1.f / Z;
+  }
+  __syncthreads();
+  if (e == 0) {
+    const float *po = A.po + u * (A.ns + 1) * (long)G * D;
+    for (int i = threadIdx.x; i < G * D; i += NTF) {
+      const int qi = i / D;
+      float v = po[(long)A.ns * G * D + i] * exp2f(mz[A.ns * G + qi].x - sM[qi]);
+      for (int s = 0; s < used; ++s) v += po[(long)s * G * D + i] * exp2f(mz[s * G + qi].x - sM[qi]);
+      A.o[u * (long)G * D + i] = v * sI[qi];
+    }
+    if (threadIdx.x == 0) A.len_out[u] = n + 1;
+  }
+  if (A.c.acc) {
+    const float *lg = A.lgw + u * (long)(cap + 1) * G;
+    float *acc = A.c.acc + u * (long)cap;
+    for (int j = lo + threadIdx.x; j < min(lo + SLOTS_F, n + 1); j += NTF) {
+      float p = 0.f;
+      for (int q = 0; q < G; ++q) p += exp2f(lg[(long)j * G + q] - sM[q]) * sI[q];
+      acc[j] = (j < n ? acc[j] : 0.f) + p;
+    }
+  }
+  if (fills && e == 0) {  // the new token filled its block: codes for K, then V
+    for (int kv = 0; kv < 2; ++kv) {
+      const T *rows = static_cast<const T *>(kv ? A.c.Vt : A.c.Kt) + u * (long)block * D;
+      uint4 *to = reinterpret_cast<uint4 *>(static_cast<uint8_t *>(kv ? A.c.V : A.c.K) +
+                                            (u * (long)cap + nf) * D);
+      const int pieces = block * D / 16;
+      float big = 0.f;
+      for (int i = threadIdx.x; i < pieces; i += NTF) {
+        float x[16];
+        load16(rows + (long)i * 16, x);
+        big = fmaxf(big, max_abs16(x));
+      }
+      const float a = q8_scale<FMT>(block_max(big, red));
+      const float inv = __fdiv_rn(1.f, a);
+      for (int i = threadIdx.x; i < pieces; i += NTF) {
+        float x[16];
+        load16(rows + (long)i * 16, x);
+        to[i] = q8_pack16<FMT>(x, inv);
+      }
+      if (threadIdx.x == 0) (kv ? A.c.Vs : A.c.Ks)[u * (long)(cap / block) + nf / block] = a;
+      __syncthreads();  // red is used again
+    }
+  }
+}
+
+size_t al(size_t x) { return (x + 255) & ~(size_t)255; }
+
+// Splits per unit: enough CTAs for every SM several times over, at least 256 slots each.
+int splits(long units, int cap) {
+  const long want = (8L * kNumSmsHint + units - 1) / (units > 0 ? units : 1);
+  const long most = (cap + 255) / 256;
+  return (int)(want < 1 ? 1 : want > most ? most : want);
+}
+
+template <typename T, int FMT, int D, int NSET>
+int run(const DecArgs &A, long units, cudaStream_t st) {
+  const size_t smem = (size_t)NW * A.G * D * sizeof(float);
+  if (ensure_smem((const void *)q8_stream_kernel<T, FMT, D, NSET>, smem)) return KV_ERR_CUDA;
+  const long ctas = units * (A.ns + 1);
+  const int chunks = A.c.acc ? (A.c.cap + SLOTS_F - 1) / SLOTS_F : 1;
+  if (ctas > 0x7FFFFFFFL || units * chunks > 0x7FFFFFFFL) return KV_ERR_UNSUPPORTED;
+  q8_stream_kernel<T, FMT, D, NSET><<<(unsigned)ctas, NT, smem, st>>>(A);
+  q8_finalize_kernel<T, FMT><<<(unsigned)(units * chunks), NTF, 0, st>>>(A, chunks);
+  return launch_status(2);
+}
+
+template <typename T, int FMT>
+int run_d(const DecArgs &A, long units, cudaStream_t st) {
+  if (A.c.d == 128) return A.G > 4 ? run<T, FMT, 128, 2>(A, units, st) : run<T, FMT, 128, 1>(A, units, st);
+  return A.G > 4 ? run<T, FMT, 64, 2>(A, units, st) : run<T, FMT, 64, 1>(A, units, st);
+}
+
+}  // namespace
+
+size_t decode_q8_workspace_bytes(long units, int G, int cap, int d) {
+  const int ns = splits(units, cap);
+  return al((size_t)units * (cap + 1) * G * 4) + al((size_t)units * (ns + 1) * G * 8) +
+         al((size_t)units * (ns + 1) * G * d * 4) + al((size_t)units * 4);
+}
+
+int launch_decode_q8(const void *q, const void *k_new, const void *v_new, const kv_q8_cache &c, int Hq,
+                     int32_t new_pos, const int32_t *row_pos, int32_t *len_out, float scale, float *o, void *ws,
+                     int *status, cudaStream_t st) {
+  const long units = (long)c.B * c.Hkv;
+  DecArgs A{};
+  A.q = q;
+  A.k_new = k_new;
+  A.v_new = v_new;
+  A.c = c;
+  A.row_pos = row_pos;
+  A.new_pos = new_pos;
+  A.len_out = len_out;
+  A.Hq = Hq;
+  A.G = Hq / c.Hkv;
+  A.ns = splits(units, c.cap);
+  A.c_log2 = scale * 1.4426950408889634f;
+  A.o = o;
+  A.status = status;
+  char *p = static_cast<char *>(ws);
+  A.lgw = reinterpret_cast<float *>(p);
+  p += al((size_t)units * (c.cap + 1) * A.G * 4);
+  A.pmz = reinterpret_cast<float2 *>(p);
+  p += al((size_t)units * (A.ns + 1) * A.G * 8);
+  A.po = reinterpret_cast<float *>(p);
+  p += al((size_t)units * (A.ns + 1) * A.G * c.d * 4);
+  A.nsave = reinterpret_cast<int32_t *>(p);
+  if (c.dtype == KV_BF16)
+    return c.format == KV_Q8_S8 ? run_d<__nv_bfloat16, KV_Q8_S8>(A, units, st)
+                                : run_d<__nv_bfloat16, KV_Q8_E4M3>(A, units, st);
+  return c.format == KV_Q8_S8 ? run_d<float, KV_Q8_S8>(A, units, st) : run_d<float, KV_Q8_E4M3>(A, units, st);
+}
+
+}  // namespace kvc
