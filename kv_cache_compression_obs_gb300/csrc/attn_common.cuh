@@ -82,6 +82,9 @@ __device__ __forceinline__ AttnTile attn_locate(const AttnShape &S, int index, i
   return found;
 }
 
+bool attn_tc_eligible(const AttnShape &S, float scale, int dtype);
+int launch_attn_prompt_tc(const void *Q, const void *K, const void *V, const AttnArgs &A, void *O, cudaStream_t st);
+
 // Tiles at most: every sequence may end in a partial one.
 inline long attn_tiles(const AttnShape &S, int bm) {
   if (S.n_seq == 0) return (long)S.B * ((S.Tq + bm - 1) / bm);

@@ -216,6 +216,7 @@ int launch_attn_prompt(const void *Q, const void *K, const void *V, const AttnSh
                        void *O, float *lse, void *ws, int *status, cudaStream_t st) {
   (void)ws;
   AttnArgs A{S, scale * 1.4426950408889634f, lse, status};
+  if (attn_tc_eligible(S, scale, dtype)) return launch_attn_prompt_tc(Q, K, V, A, O, st);
   if (dtype == KV_BF16)
     return S.d == 128 ? run_rows<__nv_bfloat16, 128>(Q, K, V, O, A, st) : run_rows<__nv_bfloat16, 64>(Q, K, V, O, A, st);
   return S.d == 128 ? run_rows<float, 128>(Q, K, V, O, A, st) : run_rows<float, 64>(Q, K, V, O, A, st);
