@@ -14,7 +14,7 @@
 // Roles: warpgroup i (of two) is tile i's softmax, one thread a row; warp 8 issues the
 // products, warp 9 the TMA loads.  The order P_0 V_j, Q_0 K_{j+1}, P_1 V_j,
 // Q_1 K_{j+1} keeps the tensor pipe busy with one tile while the other's softmax
-// runs.  TMEM (512 columns): S_0, S_1, O_0, O_1; P_i lies over S_i's first 64 columns,
+// runs; warp 10 clears V rows behind a sequence's end.  TMEM (512 columns): S_0, S_1, O_0, O_1; P_i lies over S_i's first 64 columns,
 // whose logits are in registers by then (products execute in the order of issue, so
 // Q_i K_{j+1} overwrites P_i only after P_i V_j has read it).
 // K and V tiles share one ring of stages in the order K_0 V_0 K_1 V_1 ...  V is used
@@ -51,7 +51,7 @@ struct Geo {
 };
 
 struct Bars {
-  uint64_t *qfull, *full, *empty, *sfull, *pfull, *ofull, *drain;
+  uint64_t *qfull, *full, *empty, *sfull, *pfull, *ofull, *drain, *vreq, *vfix;
 };
 
 struct TcArgs {
@@ -150,8 +150,8 @@ __global__ void __launch_bounds__(NT, 1)
   unsigned char *sQ = sm + Gm::Q_OFF, *sKV = sm + Gm::KV_OFF;
   uint64_t *bars = reinterpret_cast<uint64_t *>(sm + Gm::BAR_OFF);
   const Bars B{bars, bars + 1, bars + 1 + ST, bars + 1 + 2 * ST, bars + 3 + 2 * ST, bars + 5 + 2 * ST,
-               bars + 7 + 2 * ST};
-  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + Gm::BAR_OFF + 8 * (8 + 2 * ST));
+               bars + 7 + 2 * ST, bars + 8 + 2 * ST, bars + 9 + 2 * ST};
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + Gm::BAR_OFF + 8 * (10 + 2 * ST));
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
   __shared__ AttnTile stile;
   const AttnShape &S = T.A.S;
@@ -166,6 +166,8 @@ __global__ void __launch_bounds__(NT, 1)
   if (threadIdx.x == 0) {
     tc::mbar_init(B.qfull, 1);
     tc::mbar_init(B.drain, 1);
+    tc::mbar_init(B.vreq, 1);
+    tc::mbar_init(B.vfix, 1);
     for (int i = 0; i < ST; ++i) {
       tc::mbar_init(B.full + i, 1);
       tc::mbar_init(B.empty + i, 1);
@@ -195,7 +197,7 @@ __global__ void __launch_bounds__(NT, 1)
     if (warp >= 8) {
       asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     if (warp == 9) {
-      if (lane == 0 && w.nmax > 0) {
+      if (tc::elect_one() && w.nmax > 0) {
         // ---- loads ----
         const int hk = w.h[0] / (S.Hq / S.Hkv);
         tc::mbar_arrive_expect_tx(B.qfull, 2 * Gm::TILE);
@@ -222,89 +224,87 @@ __global__ void __launch_bounds__(NT, 1)
         }
       }
     } else if (warp == 8) {
-      // ---- products ----
-      const uint64_t qd = tc::sdesc_sw128(tc::smem_u32(sQ));
-      const uint64_t kd0 = tc::sdesc_sw128(tc::smem_u32(sKV));
-      const uint64_t vd0 = vdesc_sw128(tc::smem_u32(sKV), Gm::SUB);
-      const uint32_t id_s = tc::idesc_bf16(BM, BN), id_o = tc::idesc_bf16(BM, D) | kTransposeB;
-      bool ok = w.nmax > 0;
-      auto wait = [&](uint64_t *bar, uint32_t ph) {
-        if (ok && !tc::mbar_wait(bar, ph, kWaitBudget, abort_flag)) {
-          ok = false;
-          if (lane == 0) give_up();
-        }
-        ok = __all_sync(0xFFFFFFFFu, ok);
-        if (ok) tc::fence_after_sync();
-      };
-      auto qk = [&](int i, int st) {  // S_i = Q_i K^T
-        if (lane == 0) {
+      // ---- products (one elected thread: the operands then stay in uniform registers) ----
+      if (tc::elect_one() && w.nmax > 0) {
+        const uint64_t qd = tc::sdesc_sw128(tc::smem_u32(sQ));
+        const uint64_t kd0 = tc::sdesc_sw128(tc::smem_u32(sKV));
+        const uint64_t vd0 = vdesc_sw128(tc::smem_u32(sKV), Gm::SUB);
+        const uint32_t id_s = tc::idesc_bf16(BM, BN), id_o = tc::idesc_bf16(BM, D) | kTransposeB;
+        bool ok = true;
+        auto wait = [&](uint64_t *bar, uint32_t ph) {
+          if (!tc::mbar_wait(bar, ph, kWaitBudget, abort_flag)) {
+            ok = false;
+            give_up();
+          }
+          tc::fence_after_sync();
+          return ok;
+        };
+        auto qk = [&](int i, int st) {  // S_i = Q_i K^T
+          const uint64_t q = qd + (uint64_t)((i * Gm::TILE) >> 4), k = kd0 + (uint64_t)((st * Gm::TILE) >> 4);
+          const uint32_t dst = tmem + i * 128;
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk) {
             const uint64_t o = (uint64_t)(((kk / 4) * Gm::SUB + (kk % 4) * 32) >> 4);
-            tc::umma_bf16(tmem + i * 128, qd + (uint64_t)((i * Gm::TILE) >> 4) + o,
-                          kd0 + (uint64_t)((st * Gm::TILE) >> 4) + o, id_s, kk > 0);
+            tc::umma_bf16(dst, q + o, k + o, id_s, kk > 0);
           }
-        }
-      };
-      auto commit = [&](uint64_t *bar) {
-        if (lane == 0) tc::umma_commit(bar);
-      };
-      if (ok) {
-        wait(B.qfull, 0);
-        wait(B.full, 0);
-        if (ok) {
+        };
+        if (wait(B.qfull, 0) && wait(B.full, 0)) {
+#pragma unroll
           for (int i = 0; i < 2; ++i)
             if (w.n[i] > 0) {
               qk(i, 0);
-              commit(B.sfull + i);
+              tc::umma_commit(B.sfull + i);
             }
-          commit(B.empty);
-        }
-        for (int j = 0; j < w.nmax && ok; ++j) {
-          const int xv = 2 * j + 1, xk = 2 * j + 2;
-          const int sv = xv % ST, sk = xk % ST;
-          wait(B.full + sv, (xv / ST) & 1);
-          if (!ok) break;
-          const int left = tile.nk - j * BN;  // keys of the sequence in this tile
-          if (left < BN) {
-            // rows of V behind the sequence's end
-            for (int e = lane; e < (BN - left) * 8 * Gm::NKB; e += 32) {
-              const int c = e / ((BN - left) * 8), r = e % ((BN - left) * 8);
-              *reinterpret_cast<uint4 *>(sKV + sv * Gm::TILE + c * Gm::SUB + left * 128 + r * 16) =
-                  make_uint4(0, 0, 0, 0);
+          tc::umma_commit(B.empty);
+          for (int j = 0; j < w.nmax && ok; ++j) {
+            const int xv = 2 * j + 1, xk = 2 * j + 2;
+            const int sv = xv % ST, sk = xk % ST;
+            if (!wait(B.full + sv, (xv / ST) & 1)) break;
+            if (tile.nk - j * BN < BN) {  // the sequence ends inside this tile, its last
+              tc::mbar_arrive(B.vreq);
+              if (!wait(B.vfix, 0)) break;
             }
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-            __syncwarp();
-          }
-          bool have_k = false;
-          for (int i = 0; i < 2 && ok; ++i) {
-            if (j < w.n[i]) {
-              wait(B.pfull + i, j & 1);
-              if (!ok) break;
-              if (lane == 0) {
+            const uint64_t vd = vd0 + (uint64_t)((sv * Gm::TILE) >> 4);
+            bool have_k = false;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              if (j < w.n[i]) {
+                if (!wait(B.pfull + i, j & 1)) break;
 #pragma unroll
                 for (int kk = 0; kk < BN / 16; ++kk)
-                  umma_ts(tmem + 256 + i * 128, tmem + i * 128 + kk * 8,
-                          vd0 + (uint64_t)((sv * Gm::TILE + kk * 2048) >> 4), id_o, (j > 0) | (kk > 0));
+                  umma_ts(tmem + 256 + i * 128, tmem + i * 128 + kk * 8, vd + (uint64_t)((kk * 2048) >> 4), id_o,
+                          (j > 0) | (kk > 0));
+                if (j == w.n[i] - 1) tc::umma_commit(B.ofull + i);
               }
-              if (j == w.n[i] - 1) commit(B.ofull + i);
-            }
-            if (j + 1 < w.n[i]) {
-              if (!have_k) {
-                wait(B.full + sk, (xk / ST) & 1);
+              if (j + 1 < w.n[i]) {
+                if (!have_k && !wait(B.full + sk, (xk / ST) & 1)) break;
                 have_k = true;
-                if (!ok) break;
+                qk(i, sk);
+                tc::umma_commit(B.sfull + i);
               }
-              qk(i, sk);
-              commit(B.sfull + i);
             }
+            tc::umma_commit(B.empty + sv);
+            if (j + 1 < w.nmax) tc::umma_commit(B.empty + sk);
           }
-          commit(B.empty + sv);
-          if (j + 1 < w.nmax) commit(B.empty + sk);
         }
         // every product is complete before TMEM is released
-        commit(B.drain);
+        tc::umma_commit(B.drain);
         tc::mbar_wait(B.drain, 0, kDrainBudget, nullptr);
+      }
+    } else if (warp == 10) {
+      // ---- rows of V behind the sequence's end, in the one tile that it ends in ----
+      const int j = w.nmax - 1, left = tile.nk - j * BN;
+      if (w.nmax > 0 && left < BN) {
+        const int sv = (2 * j + 1) % ST;
+        if (tc::mbar_wait(B.vreq, 0, kWaitBudget, abort_flag)) {  // the tile has landed
+          for (int e = lane; e < (BN - left) * 8 * Gm::NKB; e += 32) {
+            const int cb = e / ((BN - left) * 8), r = e % ((BN - left) * 8);
+            *reinterpret_cast<uint4 *>(sKV + sv * Gm::TILE + cb * Gm::SUB + left * 128 + r * 16) = make_uint4(0, 0, 0, 0);
+          }
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive(B.vfix);
+        }
       }
     }
     } else {
