@@ -1,8 +1,10 @@
 // attn_prompt_tc.cu -- prompt attention for bf16 on the tensor cores (tcgen05, TMA).
 //
-// One CTA takes two query tiles of 128 rows against the same keys: two query heads of
-// one KV head at the same rows (G even), or the 256 rows of one head (G odd).  Per
-// tile i and key tile j of 128 keys:
+// An item of work is two query tiles of 128 rows against the same keys: two query heads
+// of one KV head at the same rows (G even), or the 256 rows of one head (G odd).  There
+// is one CTA per item; a CTA that is done takes over the next one that has not started
+// (cluster launch control), so that its loads and first products run behind the
+// writing of the last result.  Per tile i and key tile j of 128 keys:
 //     S = Q_i K_j^T (TMEM, fp32); P = 2^(c S - m) rounded to bf16 (its rounding is a
 //     relative half step 2^-9 of each weight, which averages out in O; the row sums z
 //     take P before the rounding); O_i += P V_j (TMEM, fp32), P read from TMEM.
@@ -12,11 +14,12 @@
 // announces S_j covers it.
 //
 // Roles: warpgroup i (of two) is tile i's softmax, one thread a row; warp 8 issues the
-// products, warp 9 the TMA loads.  The order P_0 V_j, Q_0 K_{j+1}, P_1 V_j,
-// Q_1 K_{j+1} keeps the tensor pipe busy with one tile while the other's softmax
-// runs; warp 10 clears V rows behind a sequence's end.  TMEM (512 columns): S_0, S_1, O_0, O_1; P_i lies over S_i's first 64 columns,
-// whose logits are in registers by then (products execute in the order of issue, so
-// Q_i K_{j+1} overwrites P_i only after P_i V_j has read it).
+// products, warp 9 the TMA loads, warp 11 fetches the items, warp 10 clears V rows behind
+// a sequence's end.  The order P_0 V_j, Q_0 K_{j+1}, P_1 V_j, Q_1 K_{j+1} keeps the tensor
+// pipe busy with one tile while the other's softmax runs.  TMEM (512 columns): S_0, S_1,
+// O_0, O_1; P_i lies over S_i's first 64 columns, whose logits are in registers by then
+// (products execute in the order of issue, so Q_i K_{j+1} overwrites P_i only after
+// P_i V_j has read it).
 // K and V tiles share one ring of stages in the order K_0 V_0 K_1 V_1 ...  V is used
 // as it lies in memory (the keys along k, d along n: a transposed operand).
 // Keys behind a sequence's end belong to another sequence or to nobody: S there is
@@ -32,6 +35,9 @@ namespace {
 
 constexpr int BM = 128, BN = 128;
 constexpr int NT = 384;
+constexpr int W_SOFTMAX = 8, W_MMA = 8, W_TMA = 9, W_SCHED = 11;  // warps 0-7: softmax, 10: V's ends
+constexpr int kMaxStages = 8;
+constexpr int kCtrlBytes = 1024;
 constexpr float kLazy = 8.f;
 constexpr long long kWaitBudget = 4000000000LL;  // clock cycles (~2 s) before a wait gives up
 constexpr long long kDrainBudget = 200000000LL;
@@ -44,14 +50,10 @@ struct Geo {
   static constexpr int STAGES = D == 128 ? 5 : 8;
   static constexpr int Q_OFF = 0;
   static constexpr int KV_OFF = 2 * TILE;
-  static constexpr int BAR_OFF = KV_OFF + STAGES * TILE;
-  static constexpr int SMEM_NEED = 1024 + BAR_OFF + 512;
+  static constexpr int CTRL_OFF = KV_OFF + STAGES * TILE;
+  static constexpr int SMEM_NEED = CTRL_OFF + kCtrlBytes;
   // more than half an SM's shared memory: a CTA takes all of TMEM, so one per SM
   static constexpr int SMEM = SMEM_NEED > 116 * 1024 ? SMEM_NEED : 116 * 1024;
-};
-
-struct Bars {
-  uint64_t *qfull, *full, *empty, *sfull, *pfull, *ofull, *drain, *vreq, *vfix;
 };
 
 struct TcArgs {
@@ -99,6 +101,14 @@ __device__ __forceinline__ void tmem_st32(uint32_t a, const uint32_t *r) {
       "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
       : "memory");
 }
+__device__ __forceinline__ void tmem_st16(uint32_t a, const uint32_t *r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(a),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // V tile as the second operand of P V: n (d) is contiguous, 64 elements per 128-byte
@@ -115,7 +125,7 @@ __device__ __forceinline__ uint64_t vdesc_sw128(uint32_t saddr, uint32_t sub) {
 }
 constexpr uint32_t kTransposeB = 1u << 16;
 
-// The work of one CTA.
+// One item of work.
 struct Work {
   AttnTile t;
   int h[2], r0[2], rows[2], n[2];  // per tile: head, first row, rows, key tiles
@@ -139,106 +149,163 @@ __device__ __forceinline__ Work make_work(const TcArgs &T, const AttnTile &t, in
   return w;
 }
 
+// Barriers and what else the roles share.
+struct Ctrl {
+  uint64_t full[kMaxStages], empty[kMaxStages];
+  uint64_t qfull[2], qempty[2], sfull[2], pfull[2], ofull[2], oempty[2], wfull[2], wempty[2];
+  uint64_t clc, drain, vreq, vfix;
+  uint4 reply;
+  Work work[2];
+  uint32_t tmem;
+  int abort_flag;
+};
+static_assert(sizeof(Ctrl) <= kCtrlBytes, "control block");
+
+// Ask the hardware for the index of a CTA of this grid that has not started; the
+// 16-byte reply arrives on `bar`.
+__device__ __forceinline__ void clc_request(uint4 &reply, uint64_t *bar) {
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the last reply has been read
+  tc::mbar_arrive_expect_tx(bar, 16);
+  asm volatile(
+      "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
+          tc::smem_u32(&reply)),
+      "r"(tc::smem_u32(bar))
+      : "memory");
+}
+// That CTA's index (it will not start any more), or -1 when none was left.
+__device__ __forceinline__ int clc_block(const uint4 &reply) {
+  int got, x;
+  asm volatile(
+      "{\n\t.reg .b128 h;\n\t.reg .pred p;\n\t"
+      "ld.shared.b128 h, [%2];\n\t"
+      "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, h;\n\t"
+      "selp.s32 %0, 1, 0, p;\n\t"
+      "mov.s32 %1, 0;\n\t"
+      "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, h;\n\t}"
+      : "=r"(got), "=r"(x)
+      : "r"(tc::smem_u32(&reply))
+      : "memory");
+  return got ? x : -1;
+}
+
 template <int D>
 __global__ void __launch_bounds__(NT, 1)
     attn_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                    const __grid_constant__ CUtensorMap tmV, const __grid_constant__ TcArgs T) {
   using Gm = Geo<D>;
   constexpr int ST = Gm::STAGES;
-  extern __shared__ unsigned char smem_raw[];
-  unsigned char *sm = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  extern __shared__ __align__(1024) unsigned char sm[];  // no static shared memory in front of it
   unsigned char *sQ = sm + Gm::Q_OFF, *sKV = sm + Gm::KV_OFF;
-  uint64_t *bars = reinterpret_cast<uint64_t *>(sm + Gm::BAR_OFF);
-  const Bars B{bars, bars + 1, bars + 1 + ST, bars + 1 + 2 * ST, bars + 3 + 2 * ST, bars + 5 + 2 * ST,
-               bars + 7 + 2 * ST, bars + 8 + 2 * ST, bars + 9 + 2 * ST};
-  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(sm + Gm::BAR_OFF + 8 * (10 + 2 * ST));
-  volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
-  __shared__ AttnTile stile;
+  Ctrl &C = *reinterpret_cast<Ctrl *>(sm + Gm::CTRL_OFF);
   const AttnShape &S = T.A.S;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int groups = T.pair_rows ? S.Hq : S.Hq / 2;
-  const int index = blockIdx.x / groups;
 
-  if (warp == 9) {
-    const AttnTile t = attn_locate(S, index, T.pair_rows ? 2 * BM : BM, blockIdx.x == 0, T.A.status);
-    if (lane == 0) stile = t;
-  }
   if (threadIdx.x == 0) {
-    tc::mbar_init(B.qfull, 1);
-    tc::mbar_init(B.drain, 1);
-    tc::mbar_init(B.vreq, 1);
-    tc::mbar_init(B.vfix, 1);
     for (int i = 0; i < ST; ++i) {
-      tc::mbar_init(B.full + i, 1);
-      tc::mbar_init(B.empty + i, 1);
+      tc::mbar_init(C.full + i, 1);
+      tc::mbar_init(C.empty + i, 1);
     }
     for (int i = 0; i < 2; ++i) {
-      tc::mbar_init(B.sfull + i, 1);
-      tc::mbar_init(B.pfull + i, 4);
-      tc::mbar_init(B.ofull + i, 1);
+      tc::mbar_init(C.qfull + i, 1);
+      tc::mbar_init(C.qempty + i, 1);
+      tc::mbar_init(C.sfull + i, 1);
+      tc::mbar_init(C.pfull + i, 4);
+      tc::mbar_init(C.ofull + i, 1);
+      tc::mbar_init(C.oempty + i, 4);
+      tc::mbar_init(C.wfull + i, 1);
+      tc::mbar_init(C.wempty + i, 11);  // loads, products, V's ends, 8 softmax warps
     }
-    *abort_flag = 0;
+    tc::mbar_init(&C.clc, 1);
+    tc::mbar_init(&C.drain, 1);
+    tc::mbar_init(&C.vreq, 1);
+    tc::mbar_init(&C.vfix, 1);
+    C.abort_flag = 0;
     tc::mbar_fence_init();
   }
-  if (warp == 8) tc::tmem_alloc(tmem_slot, 512);
+  if (warp == W_MMA) tc::tmem_alloc(&C.tmem, 512);
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
-  const uint32_t tmem = *tmem_slot;
-  const AttnTile tile = stile;
-  auto give_up = [&]() {
+  const uint32_t tmem = C.tmem;
+  volatile int *abort_flag = &C.abort_flag;
+  auto wait = [&](uint64_t *bar, uint32_t ph) -> bool {
+    if (tc::mbar_wait(bar, ph & 1, kWaitBudget, abort_flag)) return true;
     *abort_flag = 1;
     if (T.A.status) atomicExch(T.A.status, (int)KV_ERR_TIMEOUT);
+    return false;
   };
+  // Item k of this CTA (false: there is none).  Every role walks the same items.
+  auto have_item = [&](uint32_t k) -> bool { return wait(C.wfull + (k & 1), k >> 1) && C.work[k & 1].t.nq >= 0; };
 
-  if (tile.nq > 0) {
-    const Work w = make_work(T, tile, blockIdx.x % groups);
-    // registers: 256 x 216 + 128 x 72 = the 384 x 168 of the launch
-    if (warp >= 8) {
-      asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-    if (warp == 9) {
-      if (tc::elect_one() && w.nmax > 0) {
-        // ---- loads ----
-        const int hk = w.h[0] / (S.Hq / S.Hkv);
-        tc::mbar_arrive_expect_tx(B.qfull, 2 * Gm::TILE);
-        for (int i = 0; i < 2; ++i)
-          for (int c = 0; c < Gm::NKB; ++c)
-            tma_load_4d(sQ + i * Gm::TILE + c * Gm::SUB, &tmQ, c * 64, tile.q0 + w.r0[i], w.h[i], tile.b, B.qfull);
-        const int total = 2 * w.nmax;  // K_0 V_0 K_1 V_1 ...
-        int x = 0;
-        for (; x < total; ++x) {
-          const int st = x % ST;
-          if (!tc::mbar_wait(B.empty + st, ((x / ST) & 1) ^ 1, kWaitBudget, abort_flag)) {
-            give_up();
-            break;
-          }
-          tc::mbar_arrive_expect_tx(B.full + st, Gm::TILE);
-          for (int c = 0; c < Gm::NKB; ++c)
-            tma_load_4d(sKV + st * Gm::TILE + c * Gm::SUB, (x & 1) ? &tmV : &tmK, c * 64,
-                        tile.k0 + (x >> 1) * BN, hk, tile.b, B.full + st);
+  if (warp >= W_SOFTMAX) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    if (warp == W_SCHED) {
+      // ---- which work: the CTA's own index, then those of CTAs that have not started,
+      // which the hardware hands over on request (in index order: long tiles first) ----
+      int block = blockIdx.x;
+      for (uint32_t k = 0;; ++k) {
+        Work w{};
+        if (block >= 0) {
+          const AttnTile t = attn_locate(S, block / groups, T.pair_rows ? 2 * BM : BM, block == 0, T.A.status);
+          w = make_work(T, t, block % groups);
+        } else {
+          w.t.nq = -1;
         }
-        if (*abort_flag) {  // copies in flight land before the CTA may exit
-          tc::mbar_wait(B.qfull, 0, kDrainBudget, nullptr);
-          for (int k = 1; k <= ST && x - k >= 0; ++k)
-            tc::mbar_wait(B.full + (x - k) % ST, ((x - k) / ST) & 1, kDrainBudget, nullptr);
+        const bool ok = wait(C.wempty + (k & 1), (k >> 1) ^ 1);
+        if (lane == 0) {
+          C.work[k & 1] = w;
+          tc::mbar_arrive(C.wfull + (k & 1));
         }
+        if (!__all_sync(0xFFFFFFFFu, ok) || block < 0) break;
+        if (lane == 0) clc_request(C.reply, &C.clc);
+        __syncwarp();
+        block = wait(&C.clc, k) ? clc_block(C.reply) : -1;
+        block = __shfl_sync(0xFFFFFFFFu, block, 0);
       }
-    } else if (warp == 8) {
+    } else if (warp == W_TMA) {
+      // ---- loads: Q_0, Q_1 and K_0 V_0 K_1 V_1 ... of every item through one ring ----
+      if (tc::elect_one()) {
+        uint32_t x = 0, qn[2] = {0, 0};
+        bool ok = true;
+        for (uint32_t k = 0; ok && have_item(k); ++k) {
+          const Work &w = C.work[k & 1];
+          const int hk = w.h[0] / (S.Hq / S.Hkv);
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            if (ok && w.n[i] > 0) {
+              ok = wait(C.qempty + i, qn[i] ^ 1);
+              if (!ok) continue;
+              tc::mbar_arrive_expect_tx(C.qfull + i, Gm::TILE);
+              for (int c = 0; c < Gm::NKB; ++c)
+                tma_load_4d(sQ + i * Gm::TILE + c * Gm::SUB, &tmQ, c * 64, w.t.q0 + w.r0[i], w.h[i], w.t.b, C.qfull + i);
+              ++qn[i];
+            }
+          for (int y = 0; y < 2 * w.nmax && ok; ++y) {
+            const int st = x % ST;
+            ok = wait(C.empty + st, (x / ST) ^ 1);
+            if (!ok) break;
+            tc::mbar_arrive_expect_tx(C.full + st, Gm::TILE);
+            for (int c = 0; c < Gm::NKB; ++c)
+              tma_load_4d(sKV + st * Gm::TILE + c * Gm::SUB, (y & 1) ? &tmV : &tmK, c * 64, w.t.k0 + (y >> 1) * BN, hk,
+                          w.t.b, C.full + st);
+            ++x;
+          }
+          tc::mbar_arrive(C.wempty + (k & 1));
+        }
+        // copies in flight land before the CTA may exit (at once unless it gave up)
+        for (int i = 0; i < 2; ++i)
+          if (qn[i]) tc::mbar_wait(C.qfull + i, (qn[i] - 1) & 1, kDrainBudget, nullptr);
+        for (uint32_t k = 1; k <= (uint32_t)ST && k <= x; ++k)
+          tc::mbar_wait(C.full + (x - k) % ST, ((x - k) / ST) & 1, kDrainBudget, nullptr);
+      }
+    } else if (warp == W_MMA) {
       // ---- products (one elected thread: the operands then stay in uniform registers) ----
-      if (tc::elect_one() && w.nmax > 0) {
+      if (tc::elect_one()) {
         const uint64_t qd = tc::sdesc_sw128(tc::smem_u32(sQ));
         const uint64_t kd0 = tc::sdesc_sw128(tc::smem_u32(sKV));
         const uint64_t vd0 = vdesc_sw128(tc::smem_u32(sKV), Gm::SUB);
         const uint32_t id_s = tc::idesc_bf16(BM, BN), id_o = tc::idesc_bf16(BM, D) | kTransposeB;
-        bool ok = true;
-        auto wait = [&](uint64_t *bar, uint32_t ph) {
-          if (!tc::mbar_wait(bar, ph, kWaitBudget, abort_flag)) {
-            ok = false;
-            give_up();
-          }
-          tc::fence_after_sync();
-          return ok;
-        };
         auto qk = [&](int i, int st) {  // S_i = Q_i K^T
           const uint64_t q = qd + (uint64_t)((i * Gm::TILE) >> 4), k = kd0 + (uint64_t)((st * Gm::TILE) >> 4);
           const uint32_t dst = tmem + i * 128;
@@ -248,85 +315,113 @@ __global__ void __launch_bounds__(NT, 1)
             tc::umma_bf16(dst, q + o, k + o, id_s, kk > 0);
           }
         };
-        if (wait(B.qfull, 0) && wait(B.full, 0)) {
+        // Ring position and phases are counted here, not read from the items: values that
+        // come from shared memory would not stay uniform.
+        int st = 0;
+        uint32_t ph = 0, fixes = 0, items[2] = {0, 0}, ps[2] = {0, 0};
+        auto item = [&](const Work &w) -> bool {
+          const int n[2] = {w.n[0], w.n[1]}, nmax = w.nmax, nk = w.t.nk;
+          if (nmax == 0) return true;
 #pragma unroll
           for (int i = 0; i < 2; ++i)
-            if (w.n[i] > 0) {
-              qk(i, 0);
-              tc::umma_commit(B.sfull + i);
+            if (n[i] > 0 && !wait(C.qfull + i, items[i])) return false;
+          if (!wait(C.full + st, ph)) return false;
+          tc::fence_after_sync();
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            if (n[i] > 0) {
+              qk(i, st);
+              tc::umma_commit(C.sfull + i);
+              if (n[i] == 1) tc::umma_commit(C.qempty + i);
             }
-          tc::umma_commit(B.empty);
-          for (int j = 0; j < w.nmax && ok; ++j) {
-            const int xv = 2 * j + 1, xk = 2 * j + 2;
-            const int sv = xv % ST, sk = xk % ST;
-            if (!wait(B.full + sv, (xv / ST) & 1)) break;
-            if (tile.nk - j * BN < BN) {  // the sequence ends inside this tile, its last
-              tc::mbar_arrive(B.vreq);
-              if (!wait(B.vfix, 0)) break;
+          tc::umma_commit(C.empty + st);
+          for (int j = 0; j < nmax; ++j) {
+            if (++st == ST) st = 0, ph ^= 1;  // V_j
+            const int sv = st;
+            if (!wait(C.full + sv, ph)) return false;
+            if (++st == ST) st = 0, ph ^= 1;  // K_{j+1}, if there is one
+            if (nk - j * BN < BN) {           // the sequence ends inside this tile, its last
+              tc::mbar_arrive(&C.vreq);
+              if (!wait(&C.vfix, fixes++)) return false;
             }
             const uint64_t vd = vd0 + (uint64_t)((sv * Gm::TILE) >> 4);
             bool have_k = false;
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-              if (j < w.n[i]) {
-                if (!wait(B.pfull + i, j & 1)) break;
+              if (j < n[i]) {
+                if (j == 0 && !wait(C.oempty + i, items[i] ^ 1)) return false;
+                if (!wait(C.pfull + i, ps[i]++)) return false;
+                tc::fence_after_sync();
 #pragma unroll
                 for (int kk = 0; kk < BN / 16; ++kk)
                   umma_ts(tmem + 256 + i * 128, tmem + i * 128 + kk * 8, vd + (uint64_t)((kk * 2048) >> 4), id_o,
                           (j > 0) | (kk > 0));
-                if (j == w.n[i] - 1) tc::umma_commit(B.ofull + i);
+                if (j == n[i] - 1) tc::umma_commit(C.ofull + i);
               }
-              if (j + 1 < w.n[i]) {
-                if (!have_k && !wait(B.full + sk, (xk / ST) & 1)) break;
+              if (j + 1 < n[i]) {
+                if (!have_k && !wait(C.full + st, ph)) return false;
                 have_k = true;
-                qk(i, sk);
-                tc::umma_commit(B.sfull + i);
+                qk(i, st);
+                tc::umma_commit(C.sfull + i);
+                if (j + 2 == n[i]) tc::umma_commit(C.qempty + i);
               }
             }
-            tc::umma_commit(B.empty + sv);
-            if (j + 1 < w.nmax) tc::umma_commit(B.empty + sk);
+            tc::umma_commit(C.empty + sv);
+            if (j + 1 < nmax) tc::umma_commit(C.empty + st);
           }
+          items[0] += n[0] > 0;
+          items[1] += n[1] > 0;
+          return true;
+        };
+        for (uint32_t it = 0; have_item(it); ++it) {
+          if (!item(C.work[it & 1])) break;
+          tc::mbar_arrive(C.wempty + (it & 1));
         }
         // every product is complete before TMEM is released
-        tc::umma_commit(B.drain);
-        tc::mbar_wait(B.drain, 0, kDrainBudget, nullptr);
+        tc::umma_commit(&C.drain);
+        tc::mbar_wait(&C.drain, 0, kDrainBudget, nullptr);
       }
-    } else if (warp == 10) {
-      // ---- rows of V behind the sequence's end, in the one tile that it ends in ----
-      const int j = w.nmax - 1, left = tile.nk - j * BN;
-      if (w.nmax > 0 && left < BN) {
-        const int sv = (2 * j + 1) % ST;
-        if (tc::mbar_wait(B.vreq, 0, kWaitBudget, abort_flag)) {  // the tile has landed
+    } else {
+      // ---- rows of V behind a sequence's end, in the one tile that it ends in ----
+      uint32_t x = 0, fixes = 0;
+      for (uint32_t k = 0; have_item(k); ++k) {
+        const Work &w = C.work[k & 1];
+        const int left = w.t.nk - (w.nmax - 1) * BN;
+        x += 2 * w.nmax;
+        if (w.nmax > 0 && left < BN) {
+          unsigned char *v = sKV + ((x - 1) % ST) * Gm::TILE + left * 128;
+          if (!__all_sync(0xFFFFFFFFu, wait(&C.vreq, fixes++))) break;  // the tile has landed
           for (int e = lane; e < (BN - left) * 8 * Gm::NKB; e += 32) {
-            const int cb = e / ((BN - left) * 8), r = e % ((BN - left) * 8);
-            *reinterpret_cast<uint4 *>(sKV + sv * Gm::TILE + cb * Gm::SUB + left * 128 + r * 16) = make_uint4(0, 0, 0, 0);
+            const int c = e / ((BN - left) * 8), r = e % ((BN - left) * 8);
+            *reinterpret_cast<uint4 *>(v + c * Gm::SUB + r * 16) = make_uint4(0, 0, 0, 0);
           }
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
           __syncwarp();
-          if (lane == 0) tc::mbar_arrive(B.vfix);
+          if (lane == 0) tc::mbar_arrive(&C.vfix);
         }
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(C.wempty + (k & 1));
       }
     }
-    } else {
-      asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
-      // ---- softmax of tile i: one thread a row ----
-      const int i = warp >> 2;
-      const int row = (warp & 3) * 32 + lane;
-      const uint32_t ts = tmem + i * 128 + ((uint32_t)((warp & 3) * 32) << 16);
-      const uint32_t to = tmem + 256 + i * 128 + ((uint32_t)((warp & 3) * 32) << 16);
-      const float c = T.A.c_log2;
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+    // ---- softmax of tile i: one thread a row ----
+    const int i = warp >> 2;
+    const int row = (warp & 3) * 32 + lane;
+    const uint32_t ts = tmem + i * 128 + ((uint32_t)((warp & 3) * 32) << 16);
+    const uint32_t to = tmem + 256 + i * 128 + ((uint32_t)((warp & 3) * 32) << 16);
+    const float c = T.A.c_log2;
+    uint32_t ss = 0, items = 0;
+    for (uint32_t it = 0; have_item(it); ++it) {
+      const Work &w = C.work[it & 1];
       const int n = w.n[i];
-      const int first = w.r0[i] + tile.nk - tile.nq;         // last key that the tile's first row sees
-      const int mine = min(first + row, tile.nk - 1);        // ... that this row sees
-      float m = -INFINITY;                                   // reference, log2 units
+      const int first = w.r0[i] + w.t.nk - w.t.nq;     // last key that the tile's first row sees
+      const int mine = min(first + row, w.t.nk - 1);   // ... that this row sees
+      float m = -INFINITY;                             // reference, log2 units
       float2 z2 = make_float2(0.f, 0.f);
       bool ok = true;
       for (int j = 0; j < n; ++j) {
-        if (!tc::mbar_wait(B.sfull + i, j & 1, kWaitBudget, abort_flag)) {
-          ok = false;
-          give_up();
-        }
-        ok = __all_sync(0xFFFFFFFFu, ok);
+        ok = __all_sync(0xFFFFFFFFu, wait(C.sfull + i, ss++));
         if (!ok) break;
         tc::fence_after_sync();
         uint32_t r[128];
@@ -356,25 +451,25 @@ __global__ void __launch_bounds__(NT, 1)
           z2.y *= f;
           if (j > 0) {
 #pragma unroll
-            for (int q = 0; q < D / 32; ++q) {
-              uint32_t o[32];
-              tmem_ld32(to + q * 32, o);
+            for (int q = 0; q < D / 16; ++q) {
+              uint32_t o[16];
+              tc::tmem_ld16(to + q * 16, o);
               tc::tmem_ld_wait();
 #pragma unroll
-              for (int x = 0; x < 32; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * f);
-              tmem_st32(to + q * 32, o);
+              for (int x = 0; x < 16; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * f);
+              tmem_st16(to + q * 16, o);
             }
           }
         }
         const float base = m == -INFINITY ? 0.f : -m;  // a row that has seen no key yet
         const float2 c2 = make_float2(c, c), b2 = make_float2(base, base);
 #pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
-          uint32_t p[32];
+        for (int q = 0; q < 4; ++q) {
+          uint32_t p[16];
           float2 a0 = make_float2(0.f, 0.f), a1 = a0;
 #pragma unroll
-          for (int x = 0; x < 32; x += 2) {
-            const int s = hf * 64 + 2 * x;
+          for (int x = 0; x < 16; x += 2) {
+            const int s = q * 32 + 2 * x;
             const float2 u = __ffma2_rn(make_float2(__uint_as_float(r[s]), __uint_as_float(r[s + 1])), c2, b2);
             const float2 v = __ffma2_rn(make_float2(__uint_as_float(r[s + 2]), __uint_as_float(r[s + 3])), c2, b2);
             const float2 eu = make_float2(tc::ex2(u.x), tc::ex2(u.y)), ev = make_float2(tc::ex2(v.x), tc::ex2(v.y));
@@ -385,27 +480,25 @@ __global__ void __launch_bounds__(NT, 1)
             p[x + 1] = *reinterpret_cast<const uint32_t *>(&h1);
           }
           z2 = __fadd2_rn(z2, __fadd2_rn(a0, a1));
-          tmem_st32(ts + hf * 32, p);
+          tmem_st16(ts + q * 16, p);
         }
         tmem_st_wait();
         tc::fence_before_sync();
         __syncwarp();
-        if (lane == 0) tc::mbar_arrive(B.pfull + i);
+        if (lane == 0) tc::mbar_arrive(C.pfull + i);
       }
+      if (!ok) break;
       // ---- O / z ----
-      if (n > 0 && ok) {
-        if (!tc::mbar_wait(B.ofull + i, 0, kWaitBudget, abort_flag)) {
-          ok = false;
-          give_up();
-        }
-        ok = __all_sync(0xFFFFFFFFu, ok);
+      if (n > 0) {
+        ok = __all_sync(0xFFFFFFFFu, wait(C.ofull + i, items++));
+        if (!ok) break;
         tc::fence_after_sync();
       }
-      if (ok && w.rows[i] > 0) {
+      if (w.rows[i] > 0) {
         const float z = z2.x + z2.y;
         const float inv = z > 0.f ? 1.f / z : 0.f;
-        const long long at = (long long)tile.q0 + w.r0[i] + row;
-        __nv_bfloat16 *dst = T.O + tile.b * S.o[0] + w.h[i] * S.o[1] + at * S.o[2];
+        const long long at = (long long)w.t.q0 + w.r0[i] + row;
+        __nv_bfloat16 *dst = T.O + w.t.b * S.o[0] + w.h[i] * S.o[1] + at * S.o[2];
         const bool live = row < w.rows[i];
 #pragma unroll
         for (int q = 0; q < D / 32; ++q) {
@@ -428,14 +521,20 @@ __global__ void __launch_bounds__(NT, 1)
           }
         }
         if (live && T.A.lse)
-          T.A.lse[((long long)tile.b * S.Hq + w.h[i]) * S.Tq + at] =
+          T.A.lse[((long long)w.t.b * S.Hq + w.h[i]) * S.Tq + at] =
               z > 0.f ? (m + log2f(z)) * 0.6931471805599453f : -INFINITY;
+      }
+      tc::fence_before_sync();
+      __syncwarp();
+      if (lane == 0) {
+        if (n > 0) tc::mbar_arrive(C.oempty + i);
+        tc::mbar_arrive(C.wempty + (it & 1));
       }
     }
   }
   tc::fence_before_sync();
   __syncthreads();
-  if (warp == 8) tc::tmem_dealloc(tmem, 512);
+  if (warp == W_MMA) tc::tmem_dealloc(tmem, 512);
 }
 
 // [B][H][T][d] with free strides as a 4-D map of boxes of 64 elements x 128 tokens.
