@@ -111,6 +111,12 @@ __device__ __forceinline__ void tmem_st16(uint32_t a, const uint32_t *r) {
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
 // V tile as the second operand of P V: n (d) is contiguous, 64 elements per 128-byte
 // row, one row per key; 1024 bytes per group of 8 keys, `SUB` bytes to the next 64
 // elements of d.
@@ -152,7 +158,7 @@ __device__ __forceinline__ Work make_work(const TcArgs &T, const AttnTile &t, in
 // Barriers and what else the roles share.
 struct Ctrl {
   uint64_t full[kMaxStages], empty[kMaxStages];
-  uint64_t qfull[2], qempty[2], sfull[2], pfull[2], ofull[2], oempty[2], wfull[2], wempty[2];
+  uint64_t qfull[2], qempty[2], sfull[2], pfull[4], ofull[2], oempty[2], wfull[2], wempty[2];
   uint64_t clc, drain, vreq, vfix;
   uint4 reply;
   Work work[2];
@@ -211,6 +217,7 @@ __global__ void __launch_bounds__(NT, 1)
       tc::mbar_init(C.qempty + i, 1);
       tc::mbar_init(C.sfull + i, 1);
       tc::mbar_init(C.pfull + i, 4);
+      tc::mbar_init(C.pfull + 2 + i, 4);
       tc::mbar_init(C.ofull + i, 1);
       tc::mbar_init(C.oempty + i, 4);
       tc::mbar_init(C.wfull + i, 1);
@@ -350,12 +357,16 @@ __global__ void __launch_bounds__(NT, 1)
             for (int i = 0; i < 2; ++i) {
               if (j < n[i]) {
                 if (j == 0 && !wait(C.oempty + i, items[i] ^ 1)) return false;
-                if (!wait(C.pfull + i, ps[i]++)) return false;
-                tc::fence_after_sync();
 #pragma unroll
-                for (int kk = 0; kk < BN / 16; ++kk)
-                  umma_ts(tmem + 256 + i * 128, tmem + i * 128 + kk * 8, vd + (uint64_t)((kk * 2048) >> 4), id_o,
-                          (j > 0) | (kk > 0));
+                for (int hf = 0; hf < 2; ++hf) {  // P comes in two halves of 64 keys
+                  if (!wait(C.pfull + 2 * hf + i, ps[i])) return false;
+                  tc::fence_after_sync();
+#pragma unroll
+                  for (int kk = hf * 4; kk < hf * 4 + 4; ++kk)
+                    umma_ts(tmem + 256 + i * 128, tmem + i * 128 + kk * 8, vd + (uint64_t)((kk * 2048) >> 4), id_o,
+                            (j > 0) | (kk > 0));
+                }
+                ++ps[i];
                 if (j == n[i] - 1) tc::umma_commit(C.ofull + i);
               }
               if (j + 1 < n[i]) {
@@ -436,13 +447,15 @@ __global__ void __launch_bounds__(NT, 1)
         }
         float mx[4];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) mx[q] = fmaxf(__uint_as_float(r[q]), __uint_as_float(r[q + 4]));
+        for (int q = 0; q < 4; ++q) mx[q] = __uint_as_float(r[q]);
 #pragma unroll
-        for (int x = 8; x < 128; x += 8)
+        for (int x = 4; x < 124; x += 8)
 #pragma unroll
           for (int q = 0; q < 4; ++q)
-            mx[q] = fmaxf(mx[q], fmaxf(__uint_as_float(r[x + q]), __uint_as_float(r[x + q + 4])));
-        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
+            mx[q] = max3(mx[q], __uint_as_float(r[x + 2 * q]), __uint_as_float(r[x + 2 * q + 1]));
+        mx[0] = max3(mx[0], __uint_as_float(r[124]), __uint_as_float(r[125]));
+        mx[1] = max3(mx[1], __uint_as_float(r[126]), __uint_as_float(r[127]));
+        const float top = max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]) * c;
         const bool over = top > m + kLazy;
         if (__any_sync(0xFFFFFFFFu, over)) {
           const float f = over ? tc::ex2(m - top) : 1.f;
@@ -481,11 +494,13 @@ __global__ void __launch_bounds__(NT, 1)
           }
           z2 = __fadd2_rn(z2, __fadd2_rn(a0, a1));
           tmem_st16(ts + q * 16, p);
+          if (q & 1) {
+            tmem_st_wait();
+            tc::fence_before_sync();
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(C.pfull + (q & 2) + i);
+          }
         }
-        tmem_st_wait();
-        tc::fence_before_sync();
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive(C.pfull + i);
       }
       if (!ok) break;
       // ---- O / z ----
