@@ -11,13 +11,16 @@
 //   stream   -- the codes of the full blocks in ns splits per unit, one CTA each,
 //               and one more CTA per unit for the unfinished block's rows and the
 //               new token.  A warp takes 16 slots at a time and feeds them to
-//               mma.m16n8k16 straight from registers: codes are exact in fp16, so
+//               mma.m16n8k16: codes are exact in fp16, so
 //               an int8 becomes 1024 + 128 + c by a byte permutation and a packed
 //               subtraction, an e4m3 by the hardware conversion.  Which element of
 //               d stands at which k of the product is free as long as both operands
-//               agree, so every lane loads 16 consecutive bytes and no shared memory
-//               or transposition is needed: for K the k index runs over d, for V over
-//               the slots, two neighbouring slots' bytes interleaved.
+//               agree, so every lane takes 16 consecutive bytes of a row and nothing is
+//               transposed: for K the k index runs over d, for V over the slots, two
+//               neighbouring slots' bytes interleaved.  Rows go from memory to
+//               registers (through shared memory by bulk copies measured 5% slower:
+//               the warps then wait for one another), the next tile's as soon as the
+//               registers are free.
 //               fp32 accuracy: the queries and the weights P enter as hi + lo pairs of
 //               fp16 (22 bits; each scaled by a power of two so that nothing that
 //               matters is subnormal) in neighbouring columns of the 8-column operand:
@@ -32,6 +35,7 @@
 
 #include <cmath>
 
+#include "pdl.cuh"
 #include "q8_common.cuh"
 #include "tc_common.cuh"
 
@@ -42,6 +46,7 @@ constexpr int NW = 4;            // warps of a stream CTA
 constexpr int NT = 32 * NW;
 constexpr int NTF = 256;         // finalize threads
 constexpr int SLOTS_F = 1024;    // slots per finalize CTA
+constexpr int kMaxSplits = 256;
 constexpr float kLazy = 6.f;     // log2 units a logit may pass the running reference by
 constexpr int kMinExp = -118;    // smallest exponent of a V scale that is told apart (2^(8 + 118) is finite)
 constexpr int kPScale = 8;       // weights enter the product as P 2^kPScale (at most 2^(6 + 8 + 1))
@@ -121,12 +126,16 @@ __device__ __forceinline__ int query_shift(float big) {
 }
 
 // ---- the unfinished block's rows and the new token ------------------------------------
+// Rows 0 .. rows - 1 (the last one the new token) over the warps of one CTA: D / 16 lanes a
+// row, 16 elements each, all rows of a warp in flight at once.  Leaves each warp's maximum,
+// normaliser and output share where the stream's warps leave theirs.
 template <typename T, int D>
-__device__ void tail_part(const DecArgs &A, long u, int n, float *sm) {
+__device__ void tail_part(const DecArgs &A, long u, int n, float *qs, float *wm, float *wz, float *so) {
+  constexpr int LPR = D / 16, RPS = 32 / LPR, STEPS = 128 / (NW * RPS);
   const int G = A.G, block = A.c.block;
   const int nf = n / block * block, rows = n - nf + 1;  // at most block
-  float *qs = sm;                 // [G][D], premultiplied by scale log2(e)
-  float *ps = qs + 8 * D;         // [G][128]
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int sub = lane % LPR, rl = lane / LPR;
   const T *q = static_cast<const T *>(A.q) + u * (long)G * D;
   const T *kn = static_cast<const T *>(A.k_new) + u * (long)D, *vn = static_cast<const T *>(A.v_new) + u * (long)D;
   T *kt = static_cast<T *>(A.c.Kt) + u * (long)block * D, *vt = static_cast<T *>(A.c.Vt) + u * (long)block * D;
@@ -137,74 +146,121 @@ __device__ void tail_part(const DecArgs &A, long u, int n, float *sm) {
   }
   if (threadIdx.x == 0) A.c.pos[u * (long)A.c.cap + n] = A.row_pos ? A.row_pos[u / A.c.Hkv] : A.new_pos;
   __syncthreads();
-  if ((int)threadIdx.x < rows) {
-    const T *k = (int)threadIdx.x == rows - 1 ? kn : kt + (long)threadIdx.x * D;
-    float l[8];
+  for (int gb = 0; gb < G; gb += 4) {  // four query heads at a time
+    float l[STEPS][4];
+    float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY}, z[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int g = 0; g < 8; ++g) l[g] = 0.f;
-    for (int e = 0; e < D; e += 16) {
+    for (int s = 0; s < STEPS; ++s) {
+      const int row = (s * NW + warp) * RPS + rl;
+      if ((s * NW + warp) * RPS >= rows) break;
       float x[16];
-      load16(k + e, x);
+      if (row < rows) {
+        load16((row == rows - 1 ? kn : kt + (long)row * D) + sub * 16, x);
+      } else {
 #pragma unroll
-      for (int g = 0; g < 8; ++g)
-        if (g < G) {
-          const float4 *q4 = reinterpret_cast<const float4 *>(qs + g * D + e);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float4 y = q4[i];
-            l[g] += x[4 * i] * y.x + x[4 * i + 1] * y.y + x[4 * i + 2] * y.z + x[4 * i + 3] * y.w;
-          }
-        }
-    }
-#pragma unroll
-    for (int g = 0; g < 8; ++g)
-      if (g < G) {
-        ps[g * 128 + threadIdx.x] = l[g];
-        if (A.c.acc) A.lgw[(u * (long)(A.c.cap + 1) + nf + threadIdx.x) * G + g] = l[g];
+        for (int i = 0; i < 16; ++i) x[i] = 0.f;
       }
-  }
-  __syncthreads();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  for (int g = warp; g < G; g += NW) {
-    float m = -INFINITY;
-    for (int i = lane; i < rows; i += 32) m = fmaxf(m, ps[g * 128 + i]);
-    for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-    float z = 0.f;
-    for (int i = lane; i < rows; i += 32) {
-      const float p = exp2f(ps[g * 128 + i] - m);
-      ps[g * 128 + i] = p;
-      z += p;
-    }
-    for (int o = 16; o; o >>= 1) z += __shfl_xor_sync(0xFFFFFFFFu, z, o);
-    if (lane == 0) A.pmz[(u * (A.ns + 1) + A.ns) * G + g] = make_float2(m, z);
-  }
-  __syncthreads();
-  for (int e = threadIdx.x; e < D; e += NT) {
-    float o[8];
 #pragma unroll
-    for (int g = 0; g < 8; ++g) o[g] = 0.f;
-#pragma unroll 8
-    for (int i = 0; i < rows; ++i) {
-      const float v = to_f32(i == rows - 1 ? vn[e] : vt[(long)i * D + e]);
+      for (int g = 0; g < 4; ++g) {
+        float t = 0.f;
+        const float4 *q4 = reinterpret_cast<const float4 *>(qs + min(gb + g, G - 1) * D + sub * 16);
 #pragma unroll
-      for (int g = 0; g < 8; ++g)
-        if (g < G) o[g] += ps[g * 128 + i] * v;
+        for (int i = 0; i < 4; ++i) {
+          const float4 y = q4[i];
+          t += x[4 * i] * y.x + x[4 * i + 1] * y.y + x[4 * i + 2] * y.z + x[4 * i + 3] * y.w;
+        }
+#pragma unroll
+        for (int o = LPR / 2; o; o >>= 1) t += __shfl_xor_sync(0xFFFFFFFFu, t, o);
+        l[s][g] = row < rows ? t : -INFINITY;
+        m[g] = fmaxf(m[g], l[s][g]);
+        if (A.c.acc && sub == 0 && row < rows && gb + g < G)
+          A.lgw[(u * (long)(A.c.cap + 1) + nf + row) * G + gb + g] = t;
+      }
     }
 #pragma unroll
-    for (int g = 0; g < 8; ++g)
-      if (g < G) A.po[((u * (A.ns + 1) + A.ns) * G + g) * D + e] = o[g];
+    for (int g = 0; g < 4; ++g)
+#pragma unroll
+      for (int o = LPR; o < 32; o <<= 1) m[g] = fmaxf(m[g], __shfl_xor_sync(0xFFFFFFFFu, m[g], o));
+    float o[4][16];
+#pragma unroll
+    for (int g = 0; g < 4; ++g)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) o[g][i] = 0.f;
+#pragma unroll
+    for (int s = 0; s < STEPS; ++s) {
+      const int row = (s * NW + warp) * RPS + rl;
+      if ((s * NW + warp) * RPS >= rows) break;
+      float x[16];
+      if (row < rows) {
+        load16((row == rows - 1 ? vn : vt + (long)row * D) + sub * 16, x);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) x[i] = 0.f;
+      }
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        const float p = row < rows ? tc::ex2(l[s][g] - m[g]) : 0.f;
+        z[g] += p;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) o[g][i] += p * x[i];
+      }
+    }
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+#pragma unroll
+      for (int w = LPR; w < 32; w <<= 1) z[g] += __shfl_xor_sync(0xFFFFFFFFu, z[g], w);
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+#pragma unroll
+        for (int w = LPR; w < 32; w <<= 1) o[g][i] += __shfl_xor_sync(0xFFFFFFFFu, o[g][i], w);
+      if (gb + g < G && rl == 0) {
+        float *dst = so + (warp * G + gb + g) * D + sub * 16;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) dst[i] = o[g][i];
+        if (sub == 0) {
+          wm[warp * 8 + gb + g] = m[g];
+          wz[warp * 8 + gb + g] = z[g];
+        }
+      }
+    }
+  }
+}
+
+// The warps' shares (wm, wz, so) as split s of unit u.
+template <int D>
+__device__ __forceinline__ void combine_warps(const DecArgs &A, long u, int s, const float *wm, const float *wz,
+                                              const float *so) {
+  const int G = A.G;
+  __syncthreads();
+  for (int i = threadIdx.x; i < G * D; i += NT) {
+    const int qi = i / D;
+    float M = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < NW; ++w) M = fmaxf(M, wm[w * 8 + qi]);
+    float v = 0.f, Z = 0.f;
+#pragma unroll
+    for (int w = 0; w < NW; ++w) {
+      const float f = tc::ex2(wm[w * 8 + qi] - M);  // a warp without a row: 2^-inf = 0, its o and z are 0
+      v += f * so[w * G * D + i];
+      Z += f * wz[w * 8 + qi];
+    }
+    A.po[(u * (A.ns + 1) + s) * (long)G * D + i] = v;
+    if (i % D == 0) A.pmz[(u * (A.ns + 1) + s) * G + qi] = make_float2(M, Z);
   }
 }
 
 // ---- stream -----------------------------------------------------------------------------
 // NSET operands of four queries each; D head dim.
 template <typename T, int FMT, int D, int NSET>
-__global__ void __launch_bounds__(NT) q8_stream_kernel(const __grid_constant__ DecArgs A) {
+__global__ void __launch_bounds__(NT, NSET == 1 || D == 64 ? 4 : 3) q8_stream_kernel(const __grid_constant__ DecArgs A) {
   constexpr int VB = D / 8;       // V bytes per lane and slot
   constexpr int MT = D / 16;      // 16-row tiles of V^T
   constexpr int NCH = D / 64;     // 64-byte chunks of a K row
-  __shared__ __align__(16) float sm[8 * 128 + 8 * 128];
+  __shared__ __align__(16) float qs[8 * 128];
+  __shared__ float wm[NW * 8], wz[NW * 8];
   extern __shared__ float so[];   // [NW][G][D]
+  pdl_wait();
+  pdl_launch();
   const long u = blockIdx.x / (A.ns + 1);
   const int s = blockIdx.x % (A.ns + 1);
   const int G = A.G, block = A.c.block;
@@ -218,15 +274,52 @@ __global__ void __launch_bounds__(NT) q8_stream_kernel(const __grid_constant__ D
   }
   if (s == A.ns) {
     if (threadIdx.x == 0) A.nsave[u] = n;
-    tail_part<T, D>(A, u, n, sm);
+    tail_part<T, D>(A, u, n, qs, wm, wz, so);
+    combine_warps<D>(A, u, s, wm, wz, so);
     return;
   }
   const int nf = n / block * block;
   const int per = split_len(nf, A.ns);
   const int k0 = s * per, k1 = min(nf, k0 + per);
   if (k0 >= k1) return;
+  const uint8_t *kc = static_cast<const uint8_t *>(A.c.K) + u * (long)A.c.cap * D;
+  const uint8_t *vc = static_cast<const uint8_t *>(A.c.V) + u * (long)A.c.cap * D;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
+
+  // this lane's pieces of a tile: 16 bytes (or 2 x 16) of the K rows g and g + 8, VB bytes of
+  // the V rows 2t, 2t + 1, 2t + 8 and 2t + 9
+  uint4 kw[2][NCH];
+  uint32_t vw[4][VB / 4];
+  auto load_k = [&](int j) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int c = 0; c < NCH; ++c)
+        kw[h][c] = __ldcs(reinterpret_cast<const uint4 *>(kc + (long)(j + g + 8 * h) * D + c * 64 + t * 16));
+  };
+  auto load_v = [&](int j) {
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const uint8_t *p = vc + (long)(j + 2 * t + (r & 1) + 8 * (r >> 1)) * D + g * VB;
+      if constexpr (VB == 16) {
+        const uint4 w = __ldcs(reinterpret_cast<const uint4 *>(p));
+        vw[r][0] = w.x;
+        vw[r][1] = w.y;
+        vw[r][2] = w.z;
+        vw[r][3] = w.w;
+      } else {
+        const uint2 w = __ldcs(reinterpret_cast<const uint2 *>(p));
+        vw[r][0] = w.x;
+        vw[r][1] = w.y;
+      }
+    }
+  };
+  const int first = k0 + warp * 16;
+  if (first < k1) {  // on their way before the queries are read
+    load_k(first);
+    load_v(first);
+  }
 
   // queries: column 2i hi, 2i + 1 lo of query i of the set; this lane holds column g
   uint32_t qb[NSET][NCH * 4][2];
@@ -272,34 +365,11 @@ __global__ void __launch_bounds__(NT) q8_stream_kernel(const __grid_constant__ D
       for (int j = 0; j < 4; ++j) o[st][i][j] = 0.f;
   }
   int rv = kMinExp;  // o stands for o 2^(rv - kPScale)
-  const uint8_t *kc = static_cast<const uint8_t *>(A.c.K) + u * (long)A.c.cap * D;
-  const uint8_t *vc = static_cast<const uint8_t *>(A.c.V) + u * (long)A.c.cap * D;
   const float *ks = A.c.Ks + u * (long)(A.c.cap / block), *vs = A.c.Vs + u * (long)(A.c.cap / block);
   float *lg = A.lgw + u * (long)(A.c.cap + 1) * G;
 
-  for (int j = k0 + warp * 16; j < k1; j += NW * 16) {
-    uint4 kw[2][NCH];
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-      for (int c = 0; c < NCH; ++c)
-        kw[h][c] = __ldcs(reinterpret_cast<const uint4 *>(kc + (long)(j + g + 8 * h) * D + c * 64 + t * 16));
-    uint32_t vw[4][VB / 4];
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const uint8_t *p = vc + (long)(j + 2 * t + (r & 1) + 8 * (r >> 1)) * D + g * VB;
-      if constexpr (VB == 16) {
-        const uint4 w = __ldcs(reinterpret_cast<const uint4 *>(p));
-        vw[r][0] = fix<FMT>(w.x);
-        vw[r][1] = fix<FMT>(w.y);
-        vw[r][2] = fix<FMT>(w.z);
-        vw[r][3] = fix<FMT>(w.w);
-      } else {
-        const uint2 w = __ldcs(reinterpret_cast<const uint2 *>(p));
-        vw[r][0] = fix<FMT>(w.x);
-        vw[r][1] = fix<FMT>(w.y);
-      }
-    }
+  for (int j = first; j < k1; j += NW * 16) {
+    const int next = j + NW * 16;
     const float ak = ks[j / block], av = vs[j / block];
 
     float sc[NSET][4];
@@ -321,6 +391,7 @@ __global__ void __launch_bounds__(NT) q8_stream_kernel(const __grid_constant__ D
           mma16816(sc[st], a0, a1, a2, a3, qb[st][c * 4 + i][0], qb[st][c * 4 + i][1]);
       }
     }
+    if (next < k1) load_k(next);  // the registers are free; V's after the second product
     // logits of query t (+ 4 st) for slots j + g and j + g + 8
     float l0[NSET], l1[NSET];
     bool over = false;
@@ -370,8 +441,9 @@ __global__ void __launch_bounds__(NT) q8_stream_kernel(const __grid_constant__ D
     }
 #pragma unroll
     for (int w = 0; w < VB / 4; ++w) {
-      const uint32_t e0 = __byte_perm(vw[0][w], vw[1][w], 0x5140), e1 = __byte_perm(vw[0][w], vw[1][w], 0x7362);
-      const uint32_t f0 = __byte_perm(vw[2][w], vw[3][w], 0x5140), f1 = __byte_perm(vw[2][w], vw[3][w], 0x7362);
+      const uint32_t w0 = fix<FMT>(vw[0][w]), w1 = fix<FMT>(vw[1][w]), w2 = fix<FMT>(vw[2][w]), w3 = fix<FMT>(vw[3][w]);
+      const uint32_t e0 = __byte_perm(w0, w1, 0x5140), e1 = __byte_perm(w0, w1, 0x7362);
+      const uint32_t f0 = __byte_perm(w2, w3, 0x5140), f1 = __byte_perm(w2, w3, 0x7362);
       const uint32_t a0 = to_half2_lo<FMT>(e0), a1 = to_half2_hi<FMT>(e0);
       const uint32_t a2 = to_half2_lo<FMT>(f0), a3 = to_half2_hi<FMT>(f0);
       const uint32_t c0 = to_half2_lo<FMT>(e1), c1 = to_half2_hi<FMT>(e1);
@@ -382,10 +454,9 @@ __global__ void __launch_bounds__(NT) q8_stream_kernel(const __grid_constant__ D
         mma16816(o[st][2 * w + 1], c0, c1, c2, c3, b0[st], b1[st]);
       }
     }
+    if (next < k1) load_v(next);
   }
 
-  // combine the warps: sm holds m, z per (warp, query)
-  float *wm = sm, *wz = sm + NW * 8;
   const float back = exp2i(rv - kPScale);
 #pragma unroll
   for (int st = 0; st < NSET; ++st) {
@@ -407,101 +478,179 @@ __global__ void __launch_bounds__(NT) q8_stream_kernel(const __grid_constant__ D
       }
     }
   }
-  __syncthreads();
-  for (int i = threadIdx.x; i < G * D; i += NT) {
-    const int qi = i / D;
-    float M = -INFINITY;
-#pragma unroll
-    for (int w = 0; w < NW; ++w) M = fmaxf(M, wm[w * 8 + qi]);
-    float v = 0.f, Z = 0.f;
-#pragma unroll
-    for (int w = 0; w < NW; ++w) {
-      const float f = exp2f(wm[w * 8 + qi] - M);  // a warp without a tile: exp2(-inf) = 0, its o and z are 0
-      v += f * so[w * G * D + i];
-      Z += f * wz[w * 8 + qi];
-    }
-    A.po[(u * (A.ns + 1) + s) * (long)G * D + i] = v;
-    if (i % D == 0) A.pmz[(u * (A.ns + 1) + s) * G + qi] = make_float2(M, Z);
-  }
+  combine_warps<D>(A, u, s, wm, wz, so);
 }
 
 // ---- finalize -----------------------------------------------------------------------------
-template <typename T, int FMT>
+// `chunks` CTAs per unit, each SLOTS_F slots of acc; the query heads' outputs and the block
+// that the new token may have filled are shared out over the same CTAs.
+// A slot's G logits (GV = 1, 2, 4 or 8 of them as one or two vectors; 0: any G, read late).
+template <int GV>
+struct SlotLogits {
+  float l[GV ? GV : 1];
+  __device__ __forceinline__ void load(const float *p) {
+    if constexpr (GV == 1) {
+      l[0] = __ldcs(p);
+    } else if constexpr (GV == 2) {
+      const float2 v = __ldcs(reinterpret_cast<const float2 *>(p));
+      l[0] = v.x;
+      l[1] = v.y;
+    } else if constexpr (GV >= 4) {
+#pragma unroll
+      for (int i = 0; i < GV / 4; ++i) {
+        const float4 v = __ldcs(reinterpret_cast<const float4 *>(p) + i);
+        l[4 * i] = v.x;
+        l[4 * i + 1] = v.y;
+        l[4 * i + 2] = v.z;
+        l[4 * i + 3] = v.w;
+      }
+    }
+  }
+  __device__ __forceinline__ float mass(const float *p, int G, const float *sM, const float *sI) const {
+    float v = 0.f;
+    if constexpr (GV == 0) {
+      for (int q = 0; q < G; ++q) v += tc::ex2(__ldcs(p + q) - sM[q]) * sI[q];
+    } else {
+#pragma unroll
+      for (int q = 0; q < GV; ++q) v += tc::ex2(l[q] - sM[q]) * sI[q];
+    }
+    return v;
+  }
+};
+
+template <typename T, int FMT, int GV>
 __global__ void __launch_bounds__(NTF) q8_finalize_kernel(const __grid_constant__ DecArgs A, int chunks) {
-  __shared__ float sM[8], sI[8];  // the unit's maximum and 1 / normaliser
+  __shared__ float sM[8], sI[8];           // the unit's maximum and 1 / normaliser
+  __shared__ float sF[8][kMaxSplits + 1];  // the splits' factors
+  __shared__ float4 sO[NTF / 32][32];
   __shared__ float red[32];
+  pdl_wait();
+  pdl_launch();
   const int G = A.G, D = A.c.d, block = A.c.block, cap = A.c.cap;
   const long u = blockIdx.x / chunks;
   const int e = blockIdx.x % chunks;
+  // what does not depend on the unit's length is on its way before the length is known
+  const int lo = e * SLOTS_F;
+  constexpr int SPT = SLOTS_F / NTF;
+  SlotLogits<GV> lg[SPT];
+  float old[SPT];
+  const float *lgu = A.lgw + u * (long)(cap + 1) * G;
+  if (A.c.acc) {
+#pragma unroll
+    for (int k = 0; k < SPT; ++k) {
+      const int j = lo + k * NTF + threadIdx.x;
+      if (j < cap) {
+        lg[k].load(lgu + (long)j * G);
+        old[k] = A.c.acc[u * (long)cap + j];
+      }
+    }
+  }
   const int n = A.nsave[u];
   if (n < 0) return;
-  const int lo = e * SLOTS_F;
+  const int hi = min(lo + SLOTS_F, n + 1);
   const bool fills = (n + 1) % block == 0;
-  if (e > 0 && lo > n) return;  // nothing left in this chunk (chunk 0 always has o to write)
+  const bool scores = A.c.acc && lo < hi;
+  if (!scores && e >= G && !(fills && e < 2)) return;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int nf = n / block * block;
   const int per = split_len(nf, A.ns);
-  const int used = per ? (nf + per - 1) / per : 0;  // splits that hold rows
+  const int used = per ? (nf + per - 1) / per : 0;  // splits that hold rows; the tail is split ns
   const float2 *mz = A.pmz + u * (A.ns + 1) * G;
-  if ((int)threadIdx.x < G) {
-    float M = mz[A.ns * G + threadIdx.x].x;
-    for (int s = 0; s < used; ++s) M = fmaxf(M, mz[s * G + threadIdx.x].x);
-    float Z = mz[A.ns * G + threadIdx.x].y * exp2f(mz[A.ns * G + threadIdx.x].x - M);
-    for (int s = 0; s < used; ++s) Z += mz[s * G + threadIdx.x].y * exp2f(mz[s * G + threadIdx.x].x - M);
-    sM[threadIdx.x] = M;
-    sI[threadIdx.x] = 1.f / Z;
+  if (warp < G) {  // one warp per query head
+    float M = -INFINITY;
+    for (int s = lane; s <= used; s += 32) M = fmaxf(M, mz[(s < used ? s : A.ns) * G + warp].x);
+    for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, o));
+    float Z = 0.f;
+    for (int s = lane; s <= used; s += 32) {
+      const float2 v = mz[(s < used ? s : A.ns) * G + warp];
+      const float f = tc::ex2(v.x - M);
+      sF[warp][s] = f;
+      Z += v.y * f;
+    }
+    for (int o = 16; o; o >>= 1) Z += __shfl_xor_sync(0xFFFFFFFFu, Z, o);
+    if (lane == 0) {
+      sM[warp] = M;
+      sI[warp] = 1.f / Z;
+    }
   }
   __syncthreads();
-  if (e == 0) {
-    const float *po = A.po + u * (A.ns + 1) * (long)G * D;
-    for (int i = threadIdx.x; i < G * D; i += NTF) {
-      const int qi = i / D;
-      float v = po[(long)A.ns * G * D + i] * exp2f(mz[A.ns * G + qi].x - sM[qi]);
-      for (int s = 0; s < used; ++s) v += po[(long)s * G * D + i] * exp2f(mz[s * G + qi].x - sM[qi]);
-      A.o[u * (long)G * D + i] = v * sI[qi];
-    }
-    if (threadIdx.x == 0) A.len_out[u] = n + 1;
-  }
-  if (A.c.acc) {
-    const float *lg = A.lgw + u * (long)(cap + 1) * G;
+  if (scores) {
     float *acc = A.c.acc + u * (long)cap;
-    for (int j = lo + threadIdx.x; j < min(lo + SLOTS_F, n + 1); j += NTF) {
-      float p = 0.f;
-      for (int q = 0; q < G; ++q) p += exp2f(lg[(long)j * G + q] - sM[q]) * sI[q];
-      acc[j] = (j < n ? acc[j] : 0.f) + p;
+#pragma unroll
+    for (int k = 0; k < SPT; ++k) {
+      const int j = lo + k * NTF + threadIdx.x;
+      if (j < hi) acc[j] = (j < n ? old[k] : 0.f) + lg[k].mass(lgu + (long)j * G, G, sM, sI);
     }
   }
-  if (fills && e == 0) {  // the new token filled its block: codes for K, then V
-    for (int kv = 0; kv < 2; ++kv) {
-      const T *rows = static_cast<const T *>(kv ? A.c.Vt : A.c.Kt) + u * (long)block * D;
-      uint4 *to = reinterpret_cast<uint4 *>(static_cast<uint8_t *>(kv ? A.c.V : A.c.K) +
-                                            (u * (long)cap + nf) * D);
-      const int pieces = block * D / 16;
-      float big = 0.f;
-      for (int i = threadIdx.x; i < pieces; i += NTF) {
-        float x[16];
-        load16(rows + (long)i * 16, x);
-        big = fmaxf(big, max_abs16(x));
-      }
-      const float a = q8_scale<FMT>(block_max(big, red));
-      const float inv = __fdiv_rn(1.f, a);
-      for (int i = threadIdx.x; i < pieces; i += NTF) {
-        float x[16];
-        load16(rows + (long)i * 16, x);
-        to[i] = q8_pack16<FMT>(x, inv);
-      }
-      if (threadIdx.x == 0) (kv ? A.c.Vs : A.c.Ks)[u * (long)(cap / block) + nf / block] = a;
-      __syncthreads();  // red is used again
+  const int d4 = D / 4;
+  for (int q = e; q < G; q += chunks) {
+    const float4 *po = reinterpret_cast<const float4 *>(A.po + (u * (A.ns + 1) * G + q) * (long)D);
+    const int el = lane % d4, sp = warp * (32 / d4) + lane / d4, step = (NTF / 32) * (32 / d4);
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int s = sp; s <= used; s += step) {
+      const float4 x = po[(long)(s < used ? s : A.ns) * G * d4 + el];
+      const float f = sF[q][s];
+      v.x += f * x.x;
+      v.y += f * x.y;
+      v.z += f * x.z;
+      v.w += f * x.w;
     }
+    sO[warp][lane] = v;
+    __syncthreads();
+    if ((int)threadIdx.x < d4) {
+      float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int w = 0; w < NTF / 32; ++w)
+        for (int y = threadIdx.x; y < 32; y += d4) {
+          const float4 x = sO[w][y];
+          t.x += x.x;
+          t.y += x.y;
+          t.z += x.z;
+          t.w += x.w;
+        }
+      const float i = sI[q];
+      float *o = A.o + (u * (long)G + q) * D + 4 * threadIdx.x;
+      o[0] = t.x * i;
+      o[1] = t.y * i;
+      o[2] = t.z * i;
+      o[3] = t.w * i;
+    }
+    __syncthreads();
+  }
+  if (e == 0 && threadIdx.x == 0) A.len_out[u] = n + 1;
+  if (!fills) return;
+  for (int kv = e; kv < 2; kv += chunks) {  // the new token filled its block: codes for K and V
+    const T *rows = static_cast<const T *>(kv ? A.c.Vt : A.c.Kt) + u * (long)block * D;
+    uint4 *to = reinterpret_cast<uint4 *>(static_cast<uint8_t *>(kv ? A.c.V : A.c.K) + (u * (long)cap + nf) * D);
+    const int pieces = block * D / 16;
+    float big = 0.f;
+    for (int i = threadIdx.x; i < pieces; i += NTF) {
+      float x[16];
+      load16(rows + (long)i * 16, x);
+      big = fmaxf(big, max_abs16(x));
+    }
+    const float a = q8_scale<FMT>(block_max(big, red));
+    const float inv = __fdiv_rn(1.f, a);
+    for (int i = threadIdx.x; i < pieces; i += NTF) {
+      float x[16];
+      load16(rows + (long)i * 16, x);
+      to[i] = q8_pack16<FMT>(x, inv);
+    }
+    if (threadIdx.x == 0) (kv ? A.c.Vs : A.c.Ks)[u * (long)(cap / block) + nf / block] = a;
+    __syncthreads();  // red is used again
   }
 }
 
 size_t al(size_t x) { return (x + 255) & ~(size_t)255; }
 
-// Splits per unit: enough CTAs for every SM several times over, at least 256 slots each.
+// Splits per unit: CTAs of about equal length, several waves of four an SM, so that units of
+// different lengths even out; at least one tile a warp, and no more splits than the finalize
+// kernel holds factors for.
 int splits(long units, int cap) {
-  const long want = (8L * kNumSmsHint + units - 1) / (units > 0 ? units : 1);
-  const long most = (cap + 255) / 256;
-  return (int)(want < 1 ? 1 : want > most ? most : want);
+  const long want = (24L * kNumSmsHint + units - 1) / (units > 0 ? units : 1);
+  const long most = (cap + 16 * NW - 1) / (16 * NW);
+  const long ns = want < most ? want : most;
+  return (int)(ns < 1 ? 1 : ns > kMaxSplits ? kMaxSplits : ns);
 }
 
 template <typename T, int FMT, int D, int NSET>
@@ -509,11 +658,19 @@ int run(const DecArgs &A, long units, cudaStream_t st) {
   const size_t smem = (size_t)NW * A.G * D * sizeof(float);
   if (ensure_smem((const void *)q8_stream_kernel<T, FMT, D, NSET>, smem)) return KV_ERR_CUDA;
   const long ctas = units * (A.ns + 1);
-  const int chunks = A.c.acc ? (A.c.cap + SLOTS_F - 1) / SLOTS_F : 1;
+  const int chunks = A.c.acc ? (A.c.cap + SLOTS_F - 1) / SLOTS_F : A.G;
   if (ctas > 0x7FFFFFFFL || units * chunks > 0x7FFFFFFFL) return KV_ERR_UNSUPPORTED;
-  q8_stream_kernel<T, FMT, D, NSET><<<(unsigned)ctas, NT, smem, st>>>(A);
-  q8_finalize_kernel<T, FMT><<<(unsigned)(units * chunks), NTF, 0, st>>>(A, chunks);
-  return launch_status(2);
+  cudaError_t e = launch_pdl(q8_stream_kernel<T, FMT, D, NSET>, (unsigned)ctas, NT, smem, st, A);
+  if (e != cudaSuccess) return cuda_failure(e, "8-bit decode: stream kernel");
+  count_launches(1);
+  auto *fin = A.G == 1   ? q8_finalize_kernel<T, FMT, 1>
+              : A.G == 2 ? q8_finalize_kernel<T, FMT, 2>
+              : A.G == 4 ? q8_finalize_kernel<T, FMT, 4>
+              : A.G == 8 ? q8_finalize_kernel<T, FMT, 8>
+                         : q8_finalize_kernel<T, FMT, 0>;
+  e = launch_pdl(fin, (unsigned)(units * chunks), NTF, 0, st, A, chunks);
+  if (e != cudaSuccess) return cuda_failure(e, "8-bit decode: finalize kernel");
+  return launch_status();
 }
 
 template <typename T, int FMT>
