@@ -7,11 +7,13 @@
 //   evict    destination slot m takes the source cache's slot idx[m], idx chosen
 //            here: the leading slots with pos < sink and the last `recent` slots
 //            stay, and of the others the (acc, slot)-largest, in slot order.
-// Both then run the same block kernel: one CTA per (unit, destination block, K or
-// V), one thread per 16 elements of the block, so a block is read once, its
-// largest magnitude found across the CTA and its codes written from registers.
+// Both then run the same block kernel: one CTA per (unit, destination block), each
+// thread 2 x 16 elements of K and of V, all loads in flight together, so a block is
+// read once, its largest magnitudes found across the CTA and its codes written from
+// registers.
 // The rows of the unfinished block are copied (evict: decoded where they were
 // codes, rounded to the cache's dtype, half a step at most).
+#include "pdl.cuh"
 #include "q8_common.cuh"
 #include "select_common.cuh"
 
@@ -37,14 +39,78 @@ struct BlockArgs {
   int *status;
 };
 
+// 16 source elements as they lie in memory: rows of T, or codes with their scale.
+template <typename T>
+struct Piece {
+  static constexpr int NV = 16 / Vec16<T>::N;  // vectors of 16 elements of T
+  uint4 v[NV];
+  float a;     // scale, when v[0] holds 16 codes
+  bool coded;
+  __device__ __forceinline__ void load_rows(const T *p) {
+    coded = false;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) v[i] = __ldg(reinterpret_cast<const uint4 *>(p) + i);
+  }
+  __device__ __forceinline__ void zero() {
+    coded = false;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) v[i] = make_uint4(0, 0, 0, 0);
+  }
+  template <int FMT, bool CODES>
+  __device__ __forceinline__ void get(float2 (&x)[8]) const {
+    if (CODES && coded) {
+      const uint32_t w[4] = {v[0].x, v[0].y, v[0].z, v[0].w};
+      const float2 a2 = make_float2(a, a);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        Q8<FMT>::unpack4(w[i], x[2 * i], x[2 * i + 1]);
+        x[2 * i] = __fmul2_rn(x[2 * i], a2);
+        x[2 * i + 1] = __fmul2_rn(x[2 * i + 1], a2);
+      }
+    } else {
+      float y[16];
+#pragma unroll
+      for (int i = 0; i < NV; ++i) Vec16<T>::unpack(v[i], y + i * Vec16<T>::N);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[i] = make_float2(y[2 * i], y[2 * i + 1]);
+    }
+  }
+  // The largest magnitude: rounding c a to fp32 keeps the order, so the largest code's is it.
+  template <int FMT, bool CODES>
+  __device__ __forceinline__ float big() const {
+    if (CODES && coded) return __fmul_rn(Q8<FMT>::big16(v[0]), a);
+    if constexpr (sizeof(T) == 2) {  // without the sign bf16 bits order like their values
+      uint32_t m = 0;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        m = __vimax3_u16x2(m, v[i].x & 0x7FFF7FFFu, v[i].y & 0x7FFF7FFFu);
+        m = __vimax3_u16x2(m, v[i].z & 0x7FFF7FFFu, v[i].w & 0x7FFF7FFFu);
+      }
+      return __uint_as_float(max(m & 0xFFFFu, m >> 16) << 16);
+    } else {
+      float m = 0.f;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        m = fmaxf(fmaxf(m, fabsf(__uint_as_float(v[i].x))), fabsf(__uint_as_float(v[i].y)));
+        m = fmaxf(fmaxf(m, fabsf(__uint_as_float(v[i].z))), fabsf(__uint_as_float(v[i].w)));
+      }
+      return m;
+    }
+  }
+};
+
+// PP pieces of K and PP of V per thread, all loads in flight together.
+constexpr int PP = 2;
+
 template <typename T, int FMT, bool EVICT>
-__global__ void __launch_bounds__(1024) q8_block_kernel(const __grid_constant__ BlockArgs A) {
-  __shared__ float red[32];
+__global__ void __launch_bounds__(512) q8_block_kernel(const __grid_constant__ BlockArgs A) {
+  __shared__ float red[2][16];
   __shared__ int src[128];
+  pdl_wait();
+  pdl_launch();
   const int block = A.out.block, d = A.out.d;
-  const long u = blockIdx.x / (2 * A.nblk);
-  const int rest = blockIdx.x % (2 * A.nblk);
-  const int b = rest >> 1, kv = rest & 1;
+  const long u = blockIdx.x / A.nblk;
+  const int b = blockIdx.x % A.nblk;
   int n_new = A.k, n_src = A.T;
   if constexpr (EVICT) {
     n_src = A.from.len[u];
@@ -54,77 +120,118 @@ __global__ void __launch_bounds__(1024) q8_block_kernel(const __grid_constant__ 
   const int m0 = b * block;
   if (m0 >= n_new) return;
   const int rows = min(block, n_new - m0);
-  // the rows' sources, and what moves beside K and V
-  if ((int)threadIdx.x < rows) {
-    const int m = m0 + threadIdx.x;
-    int j = A.idx ? A.idx[u * (long)A.k + m] : m;
-    const bool ok = j >= 0 && j < n_src;
-    src[threadIdx.x] = ok ? j : -1;
-    if (kv == 0) {
-      const long at = u * (long)A.out.cap + m;
-      if constexpr (EVICT) {
-        const long f = u * (long)A.from.cap + j;
-        A.out.pos[at] = A.from.pos[f];
-        A.out.acc[at] = A.from.acc[f];
-      } else {
-        if (!ok) flag_bad(A.status);
-        A.out.pos[at] = ok ? j : -1;
-        if (A.out.acc) A.out.acc[at] = ok && A.s ? A.s[u * (long)A.T + j] : 0.f;
-        if (m == 0) A.out.len[u] = n_new;
-      }
-    }
+  for (int r = threadIdx.x; r < rows; r += blockDim.x) {
+    const int j = A.idx ? A.idx[u * (long)A.k + m0 + r] : m0 + r;
+    src[r] = j >= 0 && j < n_src ? j : -1;
   }
   __syncthreads();
-  const int r = (int)(threadIdx.x << 4) >> A.d_log2;       // row of the block
-  const int e = (int)(threadIdx.x << 4) & (d - 1);         // first of the thread's 16 elements
-  const int j = r < rows ? src[r] : -1;
-  float x[16];
-  if constexpr (EVICT) {
-    const int nf = n_src / block * block;  // slots held as codes
-    const uint8_t *codes = static_cast<const uint8_t *>(kv ? A.from.V : A.from.K);
-    const float *sc = (kv ? A.from.Vs : A.from.Ks) + u * (long)(A.from.cap / block);
-    if (rows == block && src[block - 1] < nf && src[0] % block == 0 && src[block - 1] - src[0] == block - 1) {
-      // a whole block moves: its codes and its scale as they are
-      const long to = (u * (long)A.out.cap + m0 + r) * d + e;
-      const long f = (u * (long)A.from.cap + j) * d + e;
-      *reinterpret_cast<uint4 *>(static_cast<uint8_t *>(kv ? A.out.V : A.out.K) + to) =
-          __ldg(reinterpret_cast<const uint4 *>(codes + f));
-      if (threadIdx.x == 0)
-        (kv ? A.out.Vs : A.out.Ks)[u * (long)(A.out.cap / block) + b] = sc[src[0] / block];
-      return;
-    }
-    if (j >= nf) {
-      load16(static_cast<const T *>(kv ? A.from.Vt : A.from.Kt) + (u * (long)block + (j - nf)) * d + e, x);
-    } else if (j >= 0) {
-      const uint4 w = __ldg(reinterpret_cast<const uint4 *>(codes + (u * (long)A.from.cap + j) * d + e));
-      const float a = __ldg(sc + j / block);
-      Q8<FMT>::unpack4(w.x, x);
-      Q8<FMT>::unpack4(w.y, x + 4);
-      Q8<FMT>::unpack4(w.z, x + 8);
-      Q8<FMT>::unpack4(w.w, x + 12);
+  const int nf = EVICT ? n_src / block * block : 0;  // slots held as codes
+  const bool full = rows == block;
+  const bool whole = EVICT && full && src[block - 1] < nf && src[0] % block == 0 && src[block - 1] - src[0] == block - 1;
+  const float *ks = A.from.Ks + u * (long)(A.from.cap / block), *vs = A.from.Vs + u * (long)(A.from.cap / block);
+  Piece<T> p[2][PP];
+  int row[PP], el[PP];
 #pragma unroll
-      for (int i = 0; i < 16; ++i) x[i] = __fmul_rn(x[i], a);
+  for (int i = 0; i < PP; ++i) {
+    const int at = (i * (int)blockDim.x + (int)threadIdx.x) << 4;  // first of 16 elements of the block
+    row[i] = at >> A.d_log2;
+    el[i] = at & (d - 1);
+    const int j = row[i] < rows ? src[row[i]] : -1;
+    if (j < 0) {
+      p[0][i].zero();
+      p[1][i].zero();
+    } else if (EVICT && j < nf) {
+      const long f = (u * (long)A.from.cap + j) * d + el[i];
+      p[0][i].v[0] = __ldg(reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(A.from.K) + f));
+      p[1][i].v[0] = __ldg(reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(A.from.V) + f));
+      p[0][i].a = __ldg(ks + j / block);
+      p[1][i].a = __ldg(vs + j / block);
+      p[0][i].coded = p[1][i].coded = true;
+    } else if (EVICT) {
+      const long f = (u * (long)block + (j - nf)) * d + el[i];
+      p[0][i].load_rows(static_cast<const T *>(A.from.Kt) + f);
+      p[1][i].load_rows(static_cast<const T *>(A.from.Vt) + f);
+    } else {
+      const long f = (u * (long)A.T + j) * d + el[i];
+      p[0][i].load_rows(static_cast<const T *>(A.src[0]) + f);
+      p[1][i].load_rows(static_cast<const T *>(A.src[1]) + f);
     }
-  } else {
-    if (j >= 0) load16(static_cast<const T *>(A.src[kv]) + (u * (long)A.T + j) * d + e, x);
   }
-  if (j < 0) {
+  // what moves beside K and V, while they are on their way
+  for (int r = threadIdx.x; r < rows; r += blockDim.x) {
+    const int j = src[r];
+    const long at = u * (long)A.out.cap + m0 + r;
+    if constexpr (EVICT) {
+      const long f = u * (long)A.from.cap + j;
+      A.out.pos[at] = A.from.pos[f];
+      A.out.acc[at] = A.from.acc[f];
+    } else {
+      if (j < 0) flag_bad(A.status);
+      A.out.pos[at] = j;
+      if (A.out.acc) A.out.acc[at] = j >= 0 && A.s ? A.s[u * (long)A.T + j] : 0.f;
+    }
+  }
+  if (!EVICT && b == 0 && threadIdx.x == 0) A.out.len[u] = n_new;
+  const long to = (u * (long)A.out.cap + m0) * d;
+  float *const so[2] = {A.out.Ks + u * (long)(A.out.cap / block) + b, A.out.Vs + u * (long)(A.out.cap / block) + b};
+  uint8_t *const co[2] = {static_cast<uint8_t *>(A.out.K) + to, static_cast<uint8_t *>(A.out.V) + to};
+  if (whole) {  // a whole block moves: its codes and its scale as they are
 #pragma unroll
-    for (int i = 0; i < 16; ++i) x[i] = 0.f;
-  }
-  if (rows < block) {  // the unfinished block keeps its rows
-    if (r < rows) store16(static_cast<T *>(kv ? A.out.Vt : A.out.Kt) + (u * (long)block + r) * d + e, x);
+    for (int kv = 0; kv < 2; ++kv) {
+#pragma unroll
+      for (int i = 0; i < PP; ++i) *reinterpret_cast<uint4 *>(co[kv] + (row[i] << A.d_log2) + el[i]) = p[kv][i].v[0];
+      if (threadIdx.x == 0) *so[kv] = p[kv][0].a;
+    }
     return;
   }
-  const float a = q8_scale<FMT>(block_max(max_abs16(x), red));
-  const float inv = __fdiv_rn(1.f, a);
-  const long to = (u * (long)A.out.cap + m0 + r) * d + e;
-  *reinterpret_cast<uint4 *>(static_cast<uint8_t *>(kv ? A.out.V : A.out.K) + to) = q8_pack16<FMT>(x, inv);
-  if (threadIdx.x == 0) (kv ? A.out.Vs : A.out.Ks)[u * (long)(A.out.cap / block) + b] = a;
+  if (!full) {  // the unfinished block keeps its rows
+#pragma unroll
+    for (int kv = 0; kv < 2; ++kv)
+#pragma unroll
+      for (int i = 0; i < PP; ++i)
+        if (row[i] < rows) {
+          float2 x[8];
+          p[kv][i].template get<FMT, EVICT>(x);
+          float y[16];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            y[2 * e] = x[e].x;
+            y[2 * e + 1] = x[e].y;
+          }
+          store16(static_cast<T *>(kv ? A.out.Vt : A.out.Kt) + (u * (long)block + row[i]) * d + el[i], y);
+        }
+    return;
+  }
+  float big[2] = {0.f, 0.f};
+#pragma unroll
+  for (int kv = 0; kv < 2; ++kv)
+#pragma unroll
+    for (int i = 0; i < PP; ++i) big[kv] = fmaxf(big[kv], p[kv][i].template big<FMT, EVICT>());
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+#pragma unroll
+  for (int kv = 0; kv < 2; ++kv) {
+#pragma unroll
+    for (int o = 16; o; o >>= 1) big[kv] = fmaxf(big[kv], __shfl_xor_sync(0xFFFFFFFFu, big[kv], o));
+    if (lane == 0) red[kv][warp] = big[kv];
+  }
+  __syncthreads();
+#pragma unroll
+  for (int kv = 0; kv < 2; ++kv) {
+    float m = 0.f;
+    for (int w = 0; w < (int)blockDim.x >> 5; ++w) m = fmaxf(m, red[kv][w]);
+    const float a = q8_scale<FMT>(m), inv = __fdiv_rn(1.f, a);
+#pragma unroll
+    for (int i = 0; i < PP; ++i) {
+      float2 x[8];
+      p[kv][i].template get<FMT, EVICT>(x);
+      *reinterpret_cast<uint4 *>(co[kv] + (row[i] << A.d_log2) + el[i]) = q8_pack16<FMT>(x, inv);
+    }
+    if (threadIdx.x == 0) *so[kv] = a;
+  }
 }
 
 // ---- which slots stay ------------------------------------------------------------
-// One CTA per unit: exact radix select over the candidates' order-preserving keys
+// Units of any length, one CTA each: exact radix select over the candidates' order-preserving keys
 // (4 passes of 8 bits, per-warp histograms), then one ordered pass.  Of the slots
 // that equal the threshold the last ones stay: eviction takes the smallest
 // (acc, slot) first, as the decode step's single victim does.
@@ -233,19 +340,147 @@ __global__ void __launch_bounds__(NTS) evict_select_kernel(const float *__restri
   for (int m = threadIdx.x; m < recent; m += NTS) out[S + nh + m] = S + nc + m;
 }
 
+// The same selection for units whose order keys fit on chip: a cluster of CTAs per unit,
+// each with a slice of the slots in shared memory, so that acc is read once.  A protected
+// slot gets the largest key (no finite acc has it), and (key, slot) is unique: the
+// `keep` largest of all slots are those that stay, the later of equal ones first.
+constexpr int NTC = 512;
+constexpr int NWC = NTC / 32;
+constexpr int kHistCopies = 4;
+constexpr int kMaxCl = 8;
+constexpr int kSliceMax = 49152;  // keys per CTA at most (192 KB)
+
+__global__ void __launch_bounds__(NTC) evict_select_resident_kernel(
+    const float *__restrict__ acc_all, const int32_t *__restrict__ pos_all, const int32_t *__restrict__ len, int cap,
+    int keep, int recent, int sink, int32_t *__restrict__ idx, int32_t *__restrict__ len_out, int *status) {
+  extern __shared__ __align__(16) uint32_t keys[];
+  __shared__ RadixScratch<NTC, kHistCopies> rx;
+  __shared__ int wcnt[NWC], cnt[kMaxCl];
+  pdl_wait();
+  pdl_launch();
+  cooperative_groups::cluster_group cl = cooperative_groups::this_cluster();
+  const int CL = (int)cl.num_blocks(), rank = (int)cl.block_rank();
+  const long u = blockIdx.x / CL;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int n = len[u];
+  int32_t *out = idx + u * (long)keep;
+  if (n < 0 || n > cap) {
+    if (rank == 0 && threadIdx.x == 0) flag_bad(status);
+    return;
+  }
+  if (rank == 0 && threadIdx.x == 0) len_out[u] = min(n, keep);
+  if (n <= keep) {
+    for (int m = rank * NTC + threadIdx.x; m < keep; m += CL * NTC) out[m] = m < n ? m : -1;
+    return;
+  }
+  const int per = ((n + CL - 1) / CL + 31) & ~31;  // at most the host's slice
+  const int lo = min(n, rank * per), m = min(n, lo + per) - lo;
+  for (int e = threadIdx.x; e < kHistCopies * 256; e += NTC) (&rx.hist[0][0])[e] = 0u;
+  __syncthreads();
+  const float *acc = acc_all + u * (long)cap + lo;
+  const int32_t *pos = pos_all + u * (long)cap + lo;
+  auto put = [&](int i, float a) {
+    const bool safe = lo + i >= n - recent || (lo + i < sink && pos[i] < sink);
+    const uint32_t k = safe ? 0xFFFFFFFFu : order_key(a);
+    keys[i] = k;
+    atomicAdd(&rx.hist[warp & (kHistCopies - 1)][k >> 24], 1u);
+  };
+  if ((reinterpret_cast<uintptr_t>(acc) & 15) == 0) {
+    const float4 *a4 = reinterpret_cast<const float4 *>(acc);
+    for (int base = threadIdx.x; base < m >> 2; base += 4 * NTC) {
+      float4 v[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (base + k * NTC < m >> 2) v[k] = __ldg(a4 + base + k * NTC);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int i = 4 * (base + k * NTC);
+        if (i < (m & ~3)) {
+          put(i, v[k].x);
+          put(i + 1, v[k].y);
+          put(i + 2, v[k].z);
+          put(i + 3, v[k].w);
+        }
+      }
+    }
+    for (int i = (m & ~3) + threadIdx.x; i < m; i += NTC) put(i, acc[i]);
+  } else {
+    for (int i = threadIdx.x; i < m; i += NTC) put(i, acc[i]);
+  }
+  cl.sync();  // slices loaded, and every CTA of the cluster is running
+  auto key64 = [&](int i) { return ((uint64_t)keys[i] << 32) | (uint32_t)(lo + i); };
+  const uint64_t thr = radix_select_ge<NTC, true>(
+      rx, keep,
+      [&](auto &&f) {
+        for (int i = threadIdx.x; i < m; i += NTC) f(key64(i));
+      },
+      [&](auto &&f) {
+        const uint4 *k4 = reinterpret_cast<const uint4 *>(keys);
+        for (int i = threadIdx.x; i < m >> 2; i += NTC) {
+          const uint4 q = k4[i];
+          f(q.x);
+          f(q.y);
+          f(q.z);
+          f(q.w);
+        }
+        for (int i = (m & ~3) + threadIdx.x; i < m; i += NTC) f(keys[i]);
+      },
+      true);
+  // kept slots per warp range, per CTA, then the CTA's place in the output
+  const int wper = ((m + NWC - 1) / NWC + 31) & ~31;
+  const int wlo = min(m, warp * wper), whi = min(m, wlo + wper);
+  int c = 0;
+  for (int i = wlo + lane; i < whi; i += 32) c += key64(i) >= thr;
+#pragma unroll
+  for (int o = 16; o; o >>= 1) c += __shfl_xor_sync(0xFFFFFFFFu, c, o);
+  if (lane == 0) wcnt[warp] = c;
+  __syncthreads();
+  if ((int)threadIdx.x < CL) {
+    int tot = 0;
+    for (int w = 0; w < NWC; ++w) tot += wcnt[w];
+    cl.map_shared_rank(&cnt[0], threadIdx.x)[rank] = tot;
+  }
+  cl.sync();  // the last remote access is above
+  int run = 0;
+  for (int r = 0; r < rank; ++r) run += cnt[r];
+  for (int w = 0; w < warp; ++w) run += wcnt[w];
+  for (int i0 = wlo; i0 < whi; i0 += 32) {
+    const int i = i0 + lane;
+    const bool stay = i < whi && key64(i) >= thr;
+    const unsigned msk = __ballot_sync(0xFFFFFFFFu, stay);
+    const int at = run + __popc(msk & ((1u << lane) - 1u));
+    if (stay && at < keep) out[at] = lo + i;
+    run += __popc(msk);
+  }
+}
+
+// CTAs per unit and slots per CTA (0: the unit does not fit).  About two CTAs an SM over
+// all units, slices of at least 2048 slots.
+void select_plan(long units, int cap, int *CL, int *slice) {
+  const long want = (2L * kNumSmsHint + units - 1) / units, most = (cap + 2047) / 2048;
+  long cl = want < most ? want : most;
+  const long least = (cap + kSliceMax - 33) / (kSliceMax - 32);
+  if (cl < least) cl = least;
+  if (cl > kMaxCl) cl = kMaxCl;
+  if (cl < 1) cl = 1;
+  *CL = (int)cl;
+  *slice = least > kMaxCl ? 0 : (int)(((cap + cl - 1) / cl + 31) & ~31L);
+}
+
 int log2_of(int d) { return d == 128 ? 7 : 6; }
 
 template <bool EVICT>
 int launch_blocks(const BlockArgs &A, long units, cudaStream_t st) {
-  const long ctas = units * 2 * A.nblk;
+  const long ctas = units * A.nblk;
   if (ctas > 0x7FFFFFFFL) return KV_ERR_UNSUPPORTED;
-  const int nt = A.out.block * A.out.d / 16;
-  const unsigned grid = (unsigned)ctas;
+  const int nt = A.out.block * A.out.d / 16 / PP;  // 64 .. 512
   const bool bf = A.out.dtype == KV_BF16, s8 = A.out.format == KV_Q8_S8;
-  if (bf && s8) q8_block_kernel<__nv_bfloat16, KV_Q8_S8, EVICT><<<grid, nt, 0, st>>>(A);
-  else if (bf) q8_block_kernel<__nv_bfloat16, KV_Q8_E4M3, EVICT><<<grid, nt, 0, st>>>(A);
-  else if (s8) q8_block_kernel<float, KV_Q8_S8, EVICT><<<grid, nt, 0, st>>>(A);
-  else q8_block_kernel<float, KV_Q8_E4M3, EVICT><<<grid, nt, 0, st>>>(A);
+  auto *fn = bf && s8 ? q8_block_kernel<__nv_bfloat16, KV_Q8_S8, EVICT>
+             : bf     ? q8_block_kernel<__nv_bfloat16, KV_Q8_E4M3, EVICT>
+             : s8     ? q8_block_kernel<float, KV_Q8_S8, EVICT>
+                      : q8_block_kernel<float, KV_Q8_E4M3, EVICT>;
+  const cudaError_t e = launch_pdl(fn, (unsigned)ctas, nt, 0, st, A);
+  if (e != cudaSuccess) return cuda_failure(e, "8-bit cache: block kernel");
   return launch_status();
 }
 
@@ -280,9 +515,21 @@ int launch_evict_q8(const kv_q8_cache &from, int keep, int recent, int sink, int
   A.d_log2 = log2_of(out.d);
   A.nblk = (min(keep, from.cap) + out.block - 1) / out.block;
   A.status = status;
-  if (units * 2 * A.nblk > 0x7FFFFFFFL) return KV_ERR_UNSUPPORTED;
-  evict_select_kernel<<<(unsigned)units, NTS, 0, st>>>(from.acc, from.pos, from.len, from.cap, keep, recent, sink,
-                                                       idx, out.len, status);
+  int CL, slice;
+  select_plan(units, from.cap, &CL, &slice);
+  if (units * A.nblk > 0x7FFFFFFFL || units * CL > 0x7FFFFFFFL) return KV_ERR_UNSUPPORTED;
+  if (slice > 0) {
+    const size_t smem = (size_t)slice * 4;
+    if (ensure_smem((const void *)evict_select_resident_kernel, smem))
+      return cuda_failure(cudaErrorInvalidValue, "eviction: shared memory");
+    const cudaError_t e = launch_pdl_cluster(evict_select_resident_kernel, (unsigned)(units * CL), NTC, smem, st, CL,
+                                             from.acc, from.pos, from.len, from.cap, keep, recent, sink, idx, out.len,
+                                             status);
+    if (e != cudaSuccess) return cuda_failure(e, "eviction: selection");
+  } else {
+    evict_select_kernel<<<(unsigned)units, NTS, 0, st>>>(from.acc, from.pos, from.len, from.cap, keep, recent, sink,
+                                                         idx, out.len, status);
+  }
   const int rc = launch_status();
   if (rc != KV_OK) return rc;
   return launch_blocks<true>(A, units, st);

@@ -19,35 +19,64 @@ namespace kvc {
 
 template <int FMT> struct Q8;
 
+// int8 codes without the conversion instructions, which run at an eighth of the rate of
+// an addition: adding 1.5 2^23 to |y| <= 2^22 leaves rne(y) in the low bits of the sum
+// (its last place is 1), and an integer c + 128 placed there is read back by subtraction.
+// A code depends on the rounding of the product and on that of the sum: both are scalar
+// intrinsics, which are never fused (the packed f32x2 multiply and add are, even as
+// mul.rn and add.rn).
 template <> struct Q8<KV_Q8_S8> {
   static constexpr float kTop = 127.f;
-  __device__ __forceinline__ static uint32_t pack4(float a, float b, float c, float d) {
-    const int i0 = max(-127, min(127, __float2int_rn(a))), i1 = max(-127, min(127, __float2int_rn(b)));
-    const int i2 = max(-127, min(127, __float2int_rn(c))), i3 = max(-127, min(127, __float2int_rn(d)));
-    return (uint32_t)(i0 & 255) | ((uint32_t)(i1 & 255) << 8) | ((uint32_t)(i2 & 255) << 16) |
-           ((uint32_t)i3 << 24);
+  __device__ __forceinline__ static uint32_t low(float y) { return __float_as_uint(__fadd_rn(y, 12582912.f)); }
+  // |y| <= 127 (1 + 2^-22): no code passes 127
+  __device__ __forceinline__ static uint32_t pack4(float2 a, float2 b) {
+    return __byte_perm(__byte_perm(low(a.x), low(a.y), 0x0040), __byte_perm(low(b.x), low(b.y), 0x0040), 0x5410);
   }
-  __device__ __forceinline__ static void unpack4(uint32_t w, float *out) {
+  __device__ __forceinline__ static void unpack4(uint32_t w, float2 &a, float2 &b) {
+    const uint32_t u = w ^ 0x80808080u;  // c + 128
+    const float2 k = make_float2(-8388736.f, -8388736.f);
+    a = __fadd2_rn(make_float2(__uint_as_float(__byte_perm(u, 0x4B000000u, 0x7440)),
+                               __uint_as_float(__byte_perm(u, 0x4B000000u, 0x7441))), k);
+    b = __fadd2_rn(make_float2(__uint_as_float(__byte_perm(u, 0x4B000000u, 0x7442)),
+                               __uint_as_float(__byte_perm(u, 0x4B000000u, 0x7443))), k);
+  }
+  // largest |c| of 16 codes: extremes of c + 128 over 16-bit lanes
+  __device__ __forceinline__ static float big16(const uint4 &v) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    uint32_t hi = 0x00800080u, lo = 0x00800080u;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) out[i] = (float)(int8_t)(w >> (8 * i));
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t u = w[i] ^ 0x80808080u, e = u & 0x00FF00FFu, o = (u >> 8) & 0x00FF00FFu;
+      hi = __vimax3_u16x2(hi, e, o);
+      lo = __vimin3_u16x2(lo, e, o);
+    }
+    const int up = max(hi & 0xFFFFu, hi >> 16), down = min(lo & 0xFFFFu, lo >> 16);
+    return (float)max(up - 128, 128 - down);
   }
 };
 
 template <> struct Q8<KV_Q8_E4M3> {
   static constexpr float kTop = 448.f;
-  __device__ __forceinline__ static uint32_t pack4(float a, float b, float c, float d) {
-    const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
-    const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3);
+  __device__ __forceinline__ static uint32_t pack4(float2 a, float2 b) {
+    const uint32_t lo = __nv_cvt_float2_to_fp8x2(a, __NV_SATFINITE, __NV_E4M3);
+    const uint32_t hi = __nv_cvt_float2_to_fp8x2(b, __NV_SATFINITE, __NV_E4M3);
     return lo | (hi << 16);
   }
-  __device__ __forceinline__ static void unpack4(uint32_t w, float *out) {
+  __device__ __forceinline__ static void unpack4(uint32_t w, float2 &a, float2 &b) {
     const __half2_raw lo = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w & 0xFFFFu), __NV_E4M3);
     const __half2_raw hi = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w >> 16), __NV_E4M3);
-    const float2 a = __half22float2(__half2(lo)), b = __half22float2(__half2(hi));
-    out[0] = a.x;
-    out[1] = a.y;
-    out[2] = b.x;
-    out[3] = b.y;
+    a = __half22float2(__half2(lo));
+    b = __half22float2(__half2(hi));
+  }
+  // largest |c| of 16 codes: without the sign their bits order like their values
+  __device__ __forceinline__ static float big16(const uint4 &v) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) m = __vimax3_u16x2(m, w[i] & 0x007F007Fu, (w[i] >> 8) & 0x007F007Fu);
+    float2 a, b;
+    unpack4(max(m & 0xFFFFu, m >> 16), a, b);
+    return a.x;
   }
 };
 
@@ -59,13 +88,22 @@ __device__ __forceinline__ float q8_scale(float big) {
 
 // 16 values as one vector of codes; inv = 1 / scale.
 template <int FMT>
-__device__ __forceinline__ uint4 q8_pack16(const float (&x)[16], float inv) {
+__device__ __forceinline__ uint4 q8_pack16(const float2 (&x)[8], float inv) {
   uint32_t w[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    w[i] = Q8<FMT>::pack4(__fmul_rn(x[4 * i], inv), __fmul_rn(x[4 * i + 1], inv),
-                          __fmul_rn(x[4 * i + 2], inv), __fmul_rn(x[4 * i + 3], inv));
+  for (int i = 0; i < 4; ++i) {
+    const float2 a = x[2 * i], b = x[2 * i + 1];
+    w[i] = Q8<FMT>::pack4(make_float2(__fmul_rn(a.x, inv), __fmul_rn(a.y, inv)),
+                          make_float2(__fmul_rn(b.x, inv), __fmul_rn(b.y, inv)));
+  }
   return make_uint4(w[0], w[1], w[2], w[3]);
+}
+template <int FMT>
+__device__ __forceinline__ uint4 q8_pack16(const float (&x)[16], float inv) {
+  float2 y[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) y[i] = make_float2(x[2 * i], x[2 * i + 1]);
+  return q8_pack16<FMT>(y, inv);
 }
 
 // 16 consecutive elements of a row in the cache's dtype (16-byte aligned).
