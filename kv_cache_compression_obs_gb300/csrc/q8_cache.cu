@@ -35,7 +35,8 @@ struct BlockArgs {
   const int32_t *idx;    // [units][k] (null: row m is prompt row m)
   int T, k;
   kv_q8_cache from, out;
-  int d_log2, nblk;      // blocks per unit that may be written (the unfinished one included)
+  int d_log2, b_log2;    // d and block are powers of two
+  int nblk;              // blocks per unit that may be written (the unfinished one included)
   int *status;
 };
 
@@ -56,9 +57,10 @@ struct Piece {
 #pragma unroll
     for (int i = 0; i < NV; ++i) v[i] = make_uint4(0, 0, 0, 0);
   }
-  template <int FMT, bool CODES>
+  // SRC 0: rows of T, 1: codes, 2: either
+  template <int FMT, int SRC>
   __device__ __forceinline__ void get(float2 (&x)[8]) const {
-    if (CODES && coded) {
+    if (SRC == 1 || (SRC == 2 && coded)) {
       const uint32_t w[4] = {v[0].x, v[0].y, v[0].z, v[0].w};
       const float2 a2 = make_float2(a, a);
 #pragma unroll
@@ -76,9 +78,9 @@ struct Piece {
     }
   }
   // The largest magnitude: rounding c a to fp32 keeps the order, so the largest code's is it.
-  template <int FMT, bool CODES>
+  template <int FMT, int SRC>
   __device__ __forceinline__ float big() const {
-    if (CODES && coded) return __fmul_rn(Q8<FMT>::big16(v[0]), a);
+    if (SRC == 1 || (SRC == 2 && coded)) return __fmul_rn(Q8<FMT>::big16(v[0]), a);
     if constexpr (sizeof(T) == 2) {  // without the sign bf16 bits order like their values
       uint32_t m = 0;
 #pragma unroll
@@ -102,57 +104,89 @@ struct Piece {
 // PP pieces of K and PP of V per thread, all loads in flight together.
 constexpr int PP = 2;
 
+// The block's two scales and its codes.  SRC 0: rows of T, 1: codes, 2: either.
+template <typename T, int FMT, int SRC>
+__device__ __forceinline__ void quantise(const Piece<T> (&p)[2][PP], const int (&at)[PP], uint8_t *const (&co)[2],
+                                         float *const (&so)[2], float (&red)[2][16]) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+#pragma unroll
+  for (int kv = 0; kv < 2; ++kv) {
+    float big = 0.f;
+#pragma unroll
+    for (int i = 0; i < PP; ++i) big = fmaxf(big, p[kv][i].template big<FMT, SRC>());
+    // magnitudes order like their bits
+    const unsigned m = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(big));
+    if (lane == 0) red[kv][warp] = __uint_as_float(m);
+  }
+  __syncthreads();
+#pragma unroll
+  for (int kv = 0; kv < 2; ++kv) {
+    const float v = lane < (int)blockDim.x >> 5 ? red[kv][lane] : 0.f;
+    const float m = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(v)));
+    const float a = q8_scale<FMT>(m), inv = __fdiv_rn(1.f, a);
+#pragma unroll
+    for (int i = 0; i < PP; ++i) {
+      float2 x[8];
+      p[kv][i].template get<FMT, SRC>(x);
+      *reinterpret_cast<uint4 *>(co[kv] + at[i]) = q8_pack16<FMT>(x, inv);
+    }
+    if (threadIdx.x == 0) *so[kv] = a;
+  }
+}
+
 template <typename T, int FMT, bool EVICT>
 __global__ void __launch_bounds__(512) q8_block_kernel(const __grid_constant__ BlockArgs A) {
   __shared__ float red[2][16];
   __shared__ int src[128];
   pdl_wait();
   pdl_launch();
-  const int block = A.out.block, d = A.out.d;
-  const long u = blockIdx.x / A.nblk;
-  const int b = blockIdx.x % A.nblk;
+  const int block = A.out.block, d = A.out.d, bl = A.b_log2;
+  const int u = (int)(blockIdx.x / (unsigned)A.nblk);
+  const int b = (int)(blockIdx.x - (unsigned)u * (unsigned)A.nblk);
   int n_new = A.k, n_src = A.T;
   if constexpr (EVICT) {
     n_src = A.from.len[u];
     if (n_src < 0 || n_src > A.from.cap) return;  // reported by the selection
     n_new = min(n_src, A.k);
   }
-  const int m0 = b * block;
+  const int m0 = b << bl;
   if (m0 >= n_new) return;
   const int rows = min(block, n_new - m0);
   for (int r = threadIdx.x; r < rows; r += blockDim.x) {
-    const int j = A.idx ? A.idx[u * (long)A.k + m0 + r] : m0 + r;
+    const int j = A.idx ? A.idx[(long)u * A.k + m0 + r] : m0 + r;
     src[r] = j >= 0 && j < n_src ? j : -1;
   }
   __syncthreads();
-  const int nf = EVICT ? n_src / block * block : 0;  // slots held as codes
+  const int nf = EVICT ? n_src >> bl << bl : 0;  // slots held as codes
   const bool full = rows == block;
-  const bool whole = EVICT && full && src[block - 1] < nf && src[0] % block == 0 && src[block - 1] - src[0] == block - 1;
-  const float *ks = A.from.Ks + u * (long)(A.from.cap / block), *vs = A.from.Vs + u * (long)(A.from.cap / block);
+  const int last = src[rows - 1];
+  const bool codes = EVICT && last < nf;          // every row of the block is codes
+  const bool whole = codes && full && (src[0] & (block - 1)) == 0 && last - src[0] == block - 1;
+  const long src0 = EVICT ? (long)u * A.from.cap : (long)u * A.T;
+  const float *ks = A.from.Ks + (src0 >> bl), *vs = A.from.Vs + (src0 >> bl);
   Piece<T> p[2][PP];
-  int row[PP], el[PP];
+  int at[PP];  // first of the piece's 16 elements within the block
 #pragma unroll
   for (int i = 0; i < PP; ++i) {
-    const int at = (i * (int)blockDim.x + (int)threadIdx.x) << 4;  // first of 16 elements of the block
-    row[i] = at >> A.d_log2;
-    el[i] = at & (d - 1);
-    const int j = row[i] < rows ? src[row[i]] : -1;
+    at[i] = (i * (int)blockDim.x + (int)threadIdx.x) << 4;
+    const int row = at[i] >> A.d_log2, el = at[i] & (d - 1);
+    const int j = row < rows ? src[row] : -1;
     if (j < 0) {
       p[0][i].zero();
       p[1][i].zero();
-    } else if (EVICT && j < nf) {
-      const long f = (u * (long)A.from.cap + j) * d + el[i];
+    } else if (EVICT && (codes || j < nf)) {
+      const long f = ((src0 + j) << A.d_log2) + el;
       p[0][i].v[0] = __ldg(reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(A.from.K) + f));
       p[1][i].v[0] = __ldg(reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(A.from.V) + f));
-      p[0][i].a = __ldg(ks + j / block);
-      p[1][i].a = __ldg(vs + j / block);
+      p[0][i].a = __ldg(ks + (j >> bl));
+      p[1][i].a = __ldg(vs + (j >> bl));
       p[0][i].coded = p[1][i].coded = true;
     } else if (EVICT) {
-      const long f = (u * (long)block + (j - nf)) * d + el[i];
+      const long f = (((long)u << bl) + (j - nf) << A.d_log2) + el;
       p[0][i].load_rows(static_cast<const T *>(A.from.Kt) + f);
       p[1][i].load_rows(static_cast<const T *>(A.from.Vt) + f);
     } else {
-      const long f = (u * (long)A.T + j) * d + el[i];
+      const long f = ((src0 + j) << A.d_log2) + el;
       p[0][i].load_rows(static_cast<const T *>(A.src[0]) + f);
       p[1][i].load_rows(static_cast<const T *>(A.src[1]) + f);
     }
@@ -160,26 +194,26 @@ __global__ void __launch_bounds__(512) q8_block_kernel(const __grid_constant__ B
   // what moves beside K and V, while they are on their way
   for (int r = threadIdx.x; r < rows; r += blockDim.x) {
     const int j = src[r];
-    const long at = u * (long)A.out.cap + m0 + r;
+    const long to = (long)u * A.out.cap + m0 + r;
     if constexpr (EVICT) {
-      const long f = u * (long)A.from.cap + j;
-      A.out.pos[at] = A.from.pos[f];
-      A.out.acc[at] = A.from.acc[f];
+      A.out.pos[to] = A.from.pos[src0 + j];
+      A.out.acc[to] = A.from.acc[src0 + j];
     } else {
       if (j < 0) flag_bad(A.status);
-      A.out.pos[at] = j;
-      if (A.out.acc) A.out.acc[at] = j >= 0 && A.s ? A.s[u * (long)A.T + j] : 0.f;
+      A.out.pos[to] = j;
+      if (A.out.acc) A.out.acc[to] = j >= 0 && A.s ? A.s[src0 + j] : 0.f;
     }
   }
   if (!EVICT && b == 0 && threadIdx.x == 0) A.out.len[u] = n_new;
-  const long to = (u * (long)A.out.cap + m0) * d;
-  float *const so[2] = {A.out.Ks + u * (long)(A.out.cap / block) + b, A.out.Vs + u * (long)(A.out.cap / block) + b};
-  uint8_t *const co[2] = {static_cast<uint8_t *>(A.out.K) + to, static_cast<uint8_t *>(A.out.V) + to};
+  const long to = (long)u * A.out.cap + m0;
+  float *const so[2] = {A.out.Ks + (to >> bl), A.out.Vs + (to >> bl)};
+  uint8_t *const co[2] = {static_cast<uint8_t *>(A.out.K) + (to << A.d_log2),
+                          static_cast<uint8_t *>(A.out.V) + (to << A.d_log2)};
   if (whole) {  // a whole block moves: its codes and its scale as they are
 #pragma unroll
     for (int kv = 0; kv < 2; ++kv) {
 #pragma unroll
-      for (int i = 0; i < PP; ++i) *reinterpret_cast<uint4 *>(co[kv] + (row[i] << A.d_log2) + el[i]) = p[kv][i].v[0];
+      for (int i = 0; i < PP; ++i) *reinterpret_cast<uint4 *>(co[kv] + at[i]) = p[kv][i].v[0];
       if (threadIdx.x == 0) *so[kv] = p[kv][0].a;
     }
     return;
@@ -189,45 +223,23 @@ __global__ void __launch_bounds__(512) q8_block_kernel(const __grid_constant__ B
     for (int kv = 0; kv < 2; ++kv)
 #pragma unroll
       for (int i = 0; i < PP; ++i)
-        if (row[i] < rows) {
+        if (at[i] >> A.d_log2 < rows) {
           float2 x[8];
-          p[kv][i].template get<FMT, EVICT>(x);
+          p[kv][i].template get<FMT, EVICT ? 2 : 0>(x);
           float y[16];
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
             y[2 * e] = x[e].x;
             y[2 * e + 1] = x[e].y;
           }
-          store16(static_cast<T *>(kv ? A.out.Vt : A.out.Kt) + (u * (long)block + row[i]) * d + el[i], y);
+          store16(static_cast<T *>(kv ? A.out.Vt : A.out.Kt) + (((long)u << bl) << A.d_log2) + at[i], y);
         }
     return;
   }
-  float big[2] = {0.f, 0.f};
-#pragma unroll
-  for (int kv = 0; kv < 2; ++kv)
-#pragma unroll
-    for (int i = 0; i < PP; ++i) big[kv] = fmaxf(big[kv], p[kv][i].template big<FMT, EVICT>());
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-#pragma unroll
-  for (int kv = 0; kv < 2; ++kv) {
-#pragma unroll
-    for (int o = 16; o; o >>= 1) big[kv] = fmaxf(big[kv], __shfl_xor_sync(0xFFFFFFFFu, big[kv], o));
-    if (lane == 0) red[kv][warp] = big[kv];
-  }
-  __syncthreads();
-#pragma unroll
-  for (int kv = 0; kv < 2; ++kv) {
-    float m = 0.f;
-    for (int w = 0; w < (int)blockDim.x >> 5; ++w) m = fmaxf(m, red[kv][w]);
-    const float a = q8_scale<FMT>(m), inv = __fdiv_rn(1.f, a);
-#pragma unroll
-    for (int i = 0; i < PP; ++i) {
-      float2 x[8];
-      p[kv][i].template get<FMT, EVICT>(x);
-      *reinterpret_cast<uint4 *>(co[kv] + (row[i] << A.d_log2) + el[i]) = q8_pack16<FMT>(x, inv);
-    }
-    if (threadIdx.x == 0) *so[kv] = a;
-  }
+  if (EVICT && codes)
+    quantise<T, FMT, 1>(p, at, co, so, red);
+  else
+    quantise<T, FMT, EVICT ? 2 : 0>(p, at, co, so, red);
 }
 
 // ---- which slots stay ------------------------------------------------------------
@@ -467,7 +479,7 @@ void select_plan(long units, int cap, int *CL, int *slice) {
   *slice = least > kMaxCl ? 0 : (int)(((cap + cl - 1) / cl + 31) & ~31L);
 }
 
-int log2_of(int d) { return d == 128 ? 7 : 6; }
+int log2_of(int d) { return d == 128 ? 7 : d == 64 ? 6 : 5; }
 
 template <bool EVICT>
 int launch_blocks(const BlockArgs &A, long units, cudaStream_t st) {
@@ -498,6 +510,7 @@ int launch_compact_q8(const void *K, const void *V, const float *s, const int32_
   A.out = out;
   A.from = out;
   A.d_log2 = log2_of(out.d);
+  A.b_log2 = log2_of(out.block);
   A.nblk = (k + out.block - 1) / out.block;
   A.status = status;
   return launch_blocks<false>(A, (long)out.B * out.Hkv, st);
@@ -513,6 +526,7 @@ int launch_evict_q8(const kv_q8_cache &from, int keep, int recent, int sink, int
   A.from = from;
   A.out = out;
   A.d_log2 = log2_of(out.d);
+  A.b_log2 = log2_of(out.block);
   A.nblk = (min(keep, from.cap) + out.block - 1) / out.block;
   A.status = status;
   int CL, slice;
