@@ -7,10 +7,9 @@
 //   evict    destination slot m takes the source cache's slot idx[m], idx chosen
 //            here: the leading slots with pos < sink and the last `recent` slots
 //            stay, and of the others the (acc, slot)-largest, in slot order.
-// Both then run the same block kernel: one CTA per (unit, destination block), each
-// thread 2 x 16 elements of K and of V, all loads in flight together, so a block is
-// read once, its largest magnitudes found across the CTA and its codes written from
-// registers.
+// Either way a destination block's rows are read once into the registers of one CTA, each
+// thread some pieces of 16 elements of K and of V, its largest magnitudes found across the
+// CTA and its codes written from the registers.
 // The rows of the unfinished block are copied (evict: decoded where they were
 // codes, rounded to the cache's dtype, half a step at most).
 #include "pdl.cuh"
@@ -101,19 +100,17 @@ struct Piece {
   }
 };
 
-// PP pieces of K and PP of V per thread, all loads in flight together.
-constexpr int PP = 2;
-
-// The block's two scales and its codes.  SRC 0: rows of T, 1: codes, 2: either.
-template <typename T, int FMT, int SRC>
-__device__ __forceinline__ void quantise(const Piece<T> (&p)[2][PP], const int (&at)[PP], uint8_t *const (&co)[2],
-                                         float *const (&so)[2], float (&red)[2][16]) {
+// The block's two scales and its codes, `bytes` of them for K and for V.  SRC 0: rows of T,
+// 1: codes, 2: either.
+template <typename T, int FMT, int SRC, int N>
+__device__ __forceinline__ void quantise(const Piece<T> (&p)[2][N], const int (&at)[N], int bytes,
+                                         uint8_t *const (&co)[2], float *const (&so)[2], float (&red)[2][16]) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 #pragma unroll
   for (int kv = 0; kv < 2; ++kv) {
     float big = 0.f;
 #pragma unroll
-    for (int i = 0; i < PP; ++i) big = fmaxf(big, p[kv][i].template big<FMT, SRC>());
+    for (int i = 0; i < N; ++i) big = fmaxf(big, p[kv][i].template big<FMT, SRC>());
     // magnitudes order like their bits
     const unsigned m = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(big));
     if (lane == 0) red[kv][warp] = __uint_as_float(m);
@@ -125,7 +122,8 @@ __device__ __forceinline__ void quantise(const Piece<T> (&p)[2][PP], const int (
     const float m = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(v)));
     const float a = q8_scale<FMT>(m), inv = __fdiv_rn(1.f, a);
 #pragma unroll
-    for (int i = 0; i < PP; ++i) {
+    for (int i = 0; i < N; ++i) {
+      if (at[i] >= bytes) continue;
       float2 x[8];
       p[kv][i].template get<FMT, SRC>(x);
       *reinterpret_cast<uint4 *>(co[kv] + at[i]) = q8_pack16<FMT>(x, inv);
@@ -134,30 +132,13 @@ __device__ __forceinline__ void quantise(const Piece<T> (&p)[2][PP], const int (
   }
 }
 
-template <typename T, int FMT, bool EVICT>
-__global__ void __launch_bounds__(512) q8_block_kernel(const __grid_constant__ BlockArgs A) {
-  __shared__ float red[2][16];
-  __shared__ int src[128];
-  pdl_wait();
-  pdl_launch();
-  const int block = A.out.block, d = A.out.d, bl = A.b_log2;
-  const int u = (int)(blockIdx.x / (unsigned)A.nblk);
-  const int b = (int)(blockIdx.x - (unsigned)u * (unsigned)A.nblk);
-  int n_new = A.k, n_src = A.T;
-  if constexpr (EVICT) {
-    n_src = A.from.len[u];
-    if (n_src < 0 || n_src > A.from.cap) return;  // reported by the selection
-    n_new = min(n_src, A.k);
-  }
-  const int m0 = b << bl;
-  if (m0 >= n_new) return;
-  const int rows = min(block, n_new - m0);
-  for (int r = threadIdx.x; r < rows; r += blockDim.x) {
-    const int j = A.idx ? A.idx[(long)u * A.k + m0 + r] : m0 + r;
-    src[r] = j >= 0 && j < n_src ? j : -1;
-  }
-  __syncthreads();
-  const int nf = EVICT ? n_src >> bl << bl : 0;  // slots held as codes
+// One destination block straight from memory: rows of a prompt (EVICT false), or any mix of a
+// cache's codes and unfinished rows.  src: the rows' sources, -1 for a row of zeros.
+// PP pieces of K and of V per thread; those beyond the block idle.
+template <typename T, int FMT, bool EVICT, int PP>
+__device__ __forceinline__ void move_block(const BlockArgs &A, int u, int b, int rows, int nf, const int *src,
+                                           float (&red)[2][16]) {
+  const int block = A.out.block, d = A.out.d, bl = A.b_log2, m0 = b << bl;
   const bool full = rows == block;
   const int last = src[rows - 1];
   const bool codes = EVICT && last < nf;          // every row of the block is codes
@@ -191,20 +172,16 @@ __global__ void __launch_bounds__(512) q8_block_kernel(const __grid_constant__ B
       p[1][i].load_rows(static_cast<const T *>(A.src[1]) + f);
     }
   }
-  // what moves beside K and V, while they are on their way
-  for (int r = threadIdx.x; r < rows; r += blockDim.x) {
-    const int j = src[r];
-    const long to = (long)u * A.out.cap + m0 + r;
-    if constexpr (EVICT) {
-      A.out.pos[to] = A.from.pos[src0 + j];
-      A.out.acc[to] = A.from.acc[src0 + j];
-    } else {
+  if constexpr (!EVICT) {  // what moves beside K and V, while they are on their way
+    for (int r = threadIdx.x; r < rows; r += blockDim.x) {
+      const int j = src[r];
+      const long to = (long)u * A.out.cap + m0 + r;
       if (j < 0) flag_bad(A.status);
       A.out.pos[to] = j;
       if (A.out.acc) A.out.acc[to] = j >= 0 && A.s ? A.s[src0 + j] : 0.f;
     }
+    if (b == 0 && threadIdx.x == 0) A.out.len[u] = A.k;
   }
-  if (!EVICT && b == 0 && threadIdx.x == 0) A.out.len[u] = n_new;
   const long to = (long)u * A.out.cap + m0;
   float *const so[2] = {A.out.Ks + (to >> bl), A.out.Vs + (to >> bl)};
   uint8_t *const co[2] = {static_cast<uint8_t *>(A.out.K) + (to << A.d_log2),
@@ -213,7 +190,8 @@ __global__ void __launch_bounds__(512) q8_block_kernel(const __grid_constant__ B
 #pragma unroll
     for (int kv = 0; kv < 2; ++kv) {
 #pragma unroll
-      for (int i = 0; i < PP; ++i) *reinterpret_cast<uint4 *>(co[kv] + at[i]) = p[kv][i].v[0];
+      for (int i = 0; i < PP; ++i)
+        if (at[i] >> A.d_log2 < block) *reinterpret_cast<uint4 *>(co[kv] + at[i]) = p[kv][i].v[0];
       if (threadIdx.x == 0) *so[kv] = p[kv][0].a;
     }
     return;
@@ -236,10 +214,140 @@ __global__ void __launch_bounds__(512) q8_block_kernel(const __grid_constant__ B
         }
     return;
   }
-  if (EVICT && codes)
-    quantise<T, FMT, 1>(p, at, co, so, red);
-  else
-    quantise<T, FMT, EVICT ? 2 : 0>(p, at, co, so, red);
+  quantise<T, FMT, EVICT ? 2 : 0>(p, at, block << A.d_log2, co, so, red);
+}
+
+constexpr int kCompactPieces = 2;  // of K and of V per thread, all loads in flight together
+
+template <typename T, int FMT>
+__global__ void __launch_bounds__(512) compact_block_kernel(const __grid_constant__ BlockArgs A) {
+  __shared__ float red[2][16];
+  __shared__ int src[128];
+  pdl_wait();
+  pdl_launch();
+  const int u = (int)(blockIdx.x / (unsigned)A.nblk);
+  const int b = (int)(blockIdx.x - (unsigned)u * (unsigned)A.nblk);
+  const int m0 = b << A.b_log2;
+  const int rows = min(A.out.block, A.k - m0);
+  for (int r = threadIdx.x; r < rows; r += blockDim.x) {
+    const int j = A.idx ? A.idx[(long)u * A.k + m0 + r] : m0 + r;
+    src[r] = j >= 0 && j < A.T ? j : -1;
+  }
+  __syncthreads();
+  move_block<T, FMT, false, kCompactPieces>(A, u, b, rows, 0, src, red);
+}
+
+// ---- moving a cache's kept slots -----------------------------------------------------
+// One CTA per (unit, run of destination blocks).  The run's slots and their scales are read
+// once, at its start; the rows then come through a ring of stages, every thread copying
+// (16 bytes at a time, asynchronously) exactly the pieces that it will decode, so that the
+// stages need no barrier and several blocks' rows are in flight while one is quantised.
+constexpr int NTM = 256;
+constexpr int kRunRows = 1024;  // rows of a run at most
+
+__device__ __forceinline__ void copy16_async(void *dst, const void *src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                   static_cast<uint32_t>(__cvta_generic_to_shared(dst))),
+               "l"(src)
+               : "memory");
+}
+
+// SQ: 16-byte pieces of a block (K or V) per thread.
+template <typename T, int FMT, int SQ, int ST>
+__global__ void __launch_bounds__(NTM) evict_move_kernel(const __grid_constant__ BlockArgs A, int runs, int run_blocks) {
+  extern __shared__ __align__(16) unsigned char ring[];  // ST stages of K codes, V codes
+  __shared__ float red[2][2][16];
+  __shared__ int src[kRunRows];
+  __shared__ float sk[kRunRows], sv[kRunRows];
+  pdl_wait();
+  pdl_launch();
+  const int block = A.out.block, d = A.out.d, bl = A.b_log2;
+  const int u = (int)(blockIdx.x / (unsigned)runs);
+  const int b0 = (int)(blockIdx.x - (unsigned)u * (unsigned)runs) * run_blocks;
+  const int n_src = A.from.len[u];
+  if (n_src < 0 || n_src > A.from.cap) return;  // reported by the selection
+  const int n_new = min(n_src, A.k);
+  const int r0 = b0 << bl;
+  if (r0 >= n_new) return;
+  const int rows = min(run_blocks << bl, n_new - r0);  // of the run
+  const int nblk = (rows + block - 1) >> bl;
+  const int nf = n_src >> bl << bl;  // slots held as codes
+  const long src0 = (long)u * A.from.cap;
+  const float *ks = A.from.Ks + (src0 >> bl), *vs = A.from.Vs + (src0 >> bl);
+  for (int r = threadIdx.x; r < rows; r += NTM) {
+    const int j = A.idx[(long)u * A.k + r0 + r];
+    src[r] = j;
+    if (j < nf) {
+      sk[r] = __ldg(ks + (j >> bl));
+      sv[r] = __ldg(vs + (j >> bl));
+    }
+  }
+  __syncthreads();
+  const int bytes = block << A.d_log2;  // codes of a block of K or V
+  // a block of which every row is codes goes through the ring
+  auto in_ring = [&](int i) { return (i << bl) + block <= rows && src[(i << bl) + block - 1] < nf; };
+  auto fetch = [&](int i) {
+    if (i < nblk && in_ring(i)) {
+      unsigned char *to = ring + (i % ST) * 2 * bytes;
+#pragma unroll
+      for (int q = 0; q < SQ; ++q) {
+        const int at = (q * NTM + (int)threadIdx.x) << 4;
+        if (at < bytes) {
+          const long f = ((src0 + src[(i << bl) + (at >> A.d_log2)]) << A.d_log2) + (at & (d - 1));
+          copy16_async(to + at, static_cast<const uint8_t *>(A.from.K) + f);
+          copy16_async(to + bytes + at, static_cast<const uint8_t *>(A.from.V) + f);
+        }
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+#pragma unroll
+  for (int i = 0; i < ST - 1; ++i) fetch(i);
+  for (int r = threadIdx.x; r < rows; r += NTM) {
+    const long to = (long)u * A.out.cap + r0 + r;
+    A.out.pos[to] = A.from.pos[src0 + src[r]];
+    A.out.acc[to] = A.from.acc[src0 + src[r]];
+  }
+  for (int i = 0; i < nblk; ++i) {
+    fetch(i + ST - 1);  // into the stage that this thread has read
+    asm volatile("cp.async.wait_group %0;" ::"n"(ST - 1) : "memory");
+    const int b = b0 + i, row0 = i << bl;
+    if (!in_ring(i)) {  // the unit's last blocks: unfinished rows among them, or not full
+      const int left = min(block, rows - row0);
+      move_block<T, FMT, true, SQ>(A, u, b, left, nf, src + row0, red[i & 1]);
+      continue;
+    }
+    const long to = (long)u * A.out.cap + ((long)b << bl);
+    float *const so[2] = {A.out.Ks + (to >> bl), A.out.Vs + (to >> bl)};
+    uint8_t *const co[2] = {static_cast<uint8_t *>(A.out.K) + (to << A.d_log2),
+                            static_cast<uint8_t *>(A.out.V) + (to << A.d_log2)};
+    const unsigned char *st = ring + (i % ST) * 2 * bytes;
+    Piece<T> p[2][SQ];
+    int at[SQ];
+#pragma unroll
+    for (int q = 0; q < SQ; ++q) {
+      at[q] = (q * NTM + (int)threadIdx.x) << 4;
+      const bool mine = at[q] < bytes;
+      const int r = mine ? row0 + (at[q] >> A.d_log2) : 0;
+      p[0][q].v[0] = mine ? *reinterpret_cast<const uint4 *>(st + at[q]) : make_uint4(0, 0, 0, 0);
+      p[1][q].v[0] = mine ? *reinterpret_cast<const uint4 *>(st + bytes + at[q]) : make_uint4(0, 0, 0, 0);
+      p[0][q].a = mine ? sk[r] : 0.f;
+      p[1][q].a = mine ? sv[r] : 0.f;
+    }
+    const int j0 = src[row0];
+    if ((j0 & (block - 1)) == 0 && src[row0 + block - 1] - j0 == block - 1) {
+      // a whole block moves: its codes and its scale as they are
+#pragma unroll
+      for (int kv = 0; kv < 2; ++kv) {
+#pragma unroll
+        for (int q = 0; q < SQ; ++q)
+          if (at[q] < bytes) *reinterpret_cast<uint4 *>(co[kv] + at[q]) = p[kv][q].v[0];
+        if (threadIdx.x == 0) *so[kv] = p[kv][0].a;
+      }
+      continue;
+    }
+    quantise<T, FMT, 1>(p, at, bytes, co, so, red[i & 1]);
+  }
 }
 
 // ---- which slots stay ------------------------------------------------------------
@@ -481,19 +589,25 @@ void select_plan(long units, int cap, int *CL, int *slice) {
 
 int log2_of(int d) { return d == 128 ? 7 : d == 64 ? 6 : 5; }
 
-template <bool EVICT>
-int launch_blocks(const BlockArgs &A, long units, cudaStream_t st) {
-  const long ctas = units * A.nblk;
-  if (ctas > 0x7FFFFFFFL) return KV_ERR_UNSUPPORTED;
-  const int nt = A.out.block * A.out.d / 16 / PP;  // 64 .. 512
-  const bool bf = A.out.dtype == KV_BF16, s8 = A.out.format == KV_Q8_S8;
-  auto *fn = bf && s8 ? q8_block_kernel<__nv_bfloat16, KV_Q8_S8, EVICT>
-             : bf     ? q8_block_kernel<__nv_bfloat16, KV_Q8_E4M3, EVICT>
-             : s8     ? q8_block_kernel<float, KV_Q8_S8, EVICT>
-                      : q8_block_kernel<float, KV_Q8_E4M3, EVICT>;
-  const cudaError_t e = launch_pdl(fn, (unsigned)ctas, nt, 0, st, A);
-  if (e != cudaSuccess) return cuda_failure(e, "8-bit cache: block kernel");
-  return launch_status();
+template <typename T, int FMT>
+int launch_move(const BlockArgs &A, long units, cudaStream_t st) {
+  // runs of blocks: about four CTAs an SM, several times over, at most kRunRows rows
+  const long want = (12L * kNumSmsHint + units - 1) / units;
+  int run = (int)((A.nblk + want - 1) / want);
+  run = run < 1 ? 1 : run > (kRunRows >> A.b_log2) ? (kRunRows >> A.b_log2) : run;
+  const int runs = (A.nblk + run - 1) / run;
+  if (units * runs > 0x7FFFFFFFL) return KV_ERR_UNSUPPORTED;
+  const int bytes = A.out.block * A.out.d;
+  auto go = [&](auto *fn, int stages) {
+    const size_t smem = (size_t)stages * 2 * bytes;
+    if (ensure_smem((const void *)fn, smem)) return cuda_failure(cudaErrorInvalidValue, "eviction: shared memory");
+    const cudaError_t e = launch_pdl(fn, (unsigned)(units * runs), NTM, smem, st, A, runs, run);
+    if (e != cudaSuccess) return cuda_failure(e, "eviction: moving the slots");
+    return launch_status();
+  };
+  if (bytes <= 16 * NTM) return go(evict_move_kernel<T, FMT, 1, 4>, 4);
+  if (bytes <= 32 * NTM) return go(evict_move_kernel<T, FMT, 2, 4>, 4);
+  return go(evict_move_kernel<T, FMT, 4, 3>, 3);
 }
 
 }  // namespace
@@ -513,7 +627,17 @@ int launch_compact_q8(const void *K, const void *V, const float *s, const int32_
   A.b_log2 = log2_of(out.block);
   A.nblk = (k + out.block - 1) / out.block;
   A.status = status;
-  return launch_blocks<false>(A, (long)out.B * out.Hkv, st);
+  const long ctas = (long)out.B * out.Hkv * A.nblk;
+  if (ctas > 0x7FFFFFFFL) return KV_ERR_UNSUPPORTED;
+  const int nt = out.block * out.d / 16 / kCompactPieces;  // 64 .. 512
+  const bool bf = out.dtype == KV_BF16, s8 = out.format == KV_Q8_S8;
+  auto *fn = bf && s8 ? compact_block_kernel<__nv_bfloat16, KV_Q8_S8>
+             : bf     ? compact_block_kernel<__nv_bfloat16, KV_Q8_E4M3>
+             : s8     ? compact_block_kernel<float, KV_Q8_S8>
+                      : compact_block_kernel<float, KV_Q8_E4M3>;
+  const cudaError_t e = launch_pdl(fn, (unsigned)ctas, nt, 0, st, A);
+  if (e != cudaSuccess) return cuda_failure(e, "8-bit compaction");
+  return launch_status();
 }
 
 int launch_evict_q8(const kv_q8_cache &from, int keep, int recent, int sink, int32_t *idx,
@@ -531,7 +655,7 @@ int launch_evict_q8(const kv_q8_cache &from, int keep, int recent, int sink, int
   A.status = status;
   int CL, slice;
   select_plan(units, from.cap, &CL, &slice);
-  if (units * A.nblk > 0x7FFFFFFFL || units * CL > 0x7FFFFFFFL) return KV_ERR_UNSUPPORTED;
+  if (units * A.nblk > 0x7FFFFFFFL || units * CL > 0x7FFFFFFFL) return KV_ERR_UNSUPPORTED;  // before the first launch
   if (slice > 0) {
     const size_t smem = (size_t)slice * 4;
     if (ensure_smem((const void *)evict_select_resident_kernel, smem))
@@ -546,7 +670,11 @@ int launch_evict_q8(const kv_q8_cache &from, int keep, int recent, int sink, int
   }
   const int rc = launch_status();
   if (rc != KV_OK) return rc;
-  return launch_blocks<true>(A, units, st);
+  if (out.dtype == KV_BF16)
+    return out.format == KV_Q8_S8 ? launch_move<__nv_bfloat16, KV_Q8_S8>(A, units, st)
+                                  : launch_move<__nv_bfloat16, KV_Q8_E4M3>(A, units, st);
+  return out.format == KV_Q8_S8 ? launch_move<float, KV_Q8_S8>(A, units, st)
+                                : launch_move<float, KV_Q8_E4M3>(A, units, st);
 }
 
 }  // namespace kvc
