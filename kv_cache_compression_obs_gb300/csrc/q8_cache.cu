@@ -51,6 +51,10 @@ struct Piece {
 #pragma unroll
     for (int i = 0; i < NV; ++i) v[i] = __ldg(reinterpret_cast<const uint4 *>(p) + i);
   }
+  __device__ __forceinline__ void store_rows(T *p) const {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) reinterpret_cast<uint4 *>(p)[i] = v[i];
+  }
   __device__ __forceinline__ void zero() {
     coded = false;
 #pragma unroll
@@ -132,109 +136,65 @@ __device__ __forceinline__ void quantise(const Piece<T> (&p)[2][N], const int (&
   }
 }
 
-// One destination block straight from memory: rows of a prompt (EVICT false), or any mix of a
-// cache's codes and unfinished rows.  src: the rows' sources, -1 for a row of zeros.
-// PP pieces of K and of V per thread; those beyond the block idle.
-template <typename T, int FMT, bool EVICT, int PP>
-__device__ __forceinline__ void move_block(const BlockArgs &A, int u, int b, int rows, int nf, const int *src,
-                                           float (&red)[2][16]) {
-  const int block = A.out.block, d = A.out.d, bl = A.b_log2, m0 = b << bl;
-  const bool full = rows == block;
-  const int last = src[rows - 1];
-  const bool codes = EVICT && last < nf;          // every row of the block is codes
-  const bool whole = codes && full && (src[0] & (block - 1)) == 0 && last - src[0] == block - 1;
-  const long src0 = EVICT ? (long)u * A.from.cap : (long)u * A.T;
-  const float *ks = A.from.Ks + (src0 >> bl), *vs = A.from.Vs + (src0 >> bl);
-  Piece<T> p[2][PP];
-  int at[PP];  // first of the piece's 16 elements within the block
-#pragma unroll
-  for (int i = 0; i < PP; ++i) {
-    at[i] = (i * (int)blockDim.x + (int)threadIdx.x) << 4;
-    const int row = at[i] >> A.d_log2, el = at[i] & (d - 1);
-    const int j = row < rows ? src[row] : -1;
-    if (j < 0) {
-      p[0][i].zero();
-      p[1][i].zero();
-    } else if (EVICT && (codes || j < nf)) {
-      const long f = ((src0 + j) << A.d_log2) + el;
-      p[0][i].v[0] = __ldg(reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(A.from.K) + f));
-      p[1][i].v[0] = __ldg(reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(A.from.V) + f));
-      p[0][i].a = __ldg(ks + (j >> bl));
-      p[1][i].a = __ldg(vs + (j >> bl));
-      p[0][i].coded = p[1][i].coded = true;
-    } else if (EVICT) {
-      const long f = (((long)u << bl) + (j - nf) << A.d_log2) + el;
-      p[0][i].load_rows(static_cast<const T *>(A.from.Kt) + f);
-      p[1][i].load_rows(static_cast<const T *>(A.from.Vt) + f);
-    } else {
-      const long f = ((src0 + j) << A.d_log2) + el;
-      p[0][i].load_rows(static_cast<const T *>(A.src[0]) + f);
-      p[1][i].load_rows(static_cast<const T *>(A.src[1]) + f);
-    }
-  }
-  if constexpr (!EVICT) {  // what moves beside K and V, while they are on their way
-    for (int r = threadIdx.x; r < rows; r += blockDim.x) {
-      const int j = src[r];
-      const long to = (long)u * A.out.cap + m0 + r;
-      if (j < 0) flag_bad(A.status);
-      A.out.pos[to] = j;
-      if (A.out.acc) A.out.acc[to] = j >= 0 && A.s ? A.s[src0 + j] : 0.f;
-    }
-    if (b == 0 && threadIdx.x == 0) A.out.len[u] = A.k;
-  }
-  const long to = (long)u * A.out.cap + m0;
-  float *const so[2] = {A.out.Ks + (to >> bl), A.out.Vs + (to >> bl)};
-  uint8_t *const co[2] = {static_cast<uint8_t *>(A.out.K) + (to << A.d_log2),
-                          static_cast<uint8_t *>(A.out.V) + (to << A.d_log2)};
-  if (whole) {  // a whole block moves: its codes and its scale as they are
-#pragma unroll
-    for (int kv = 0; kv < 2; ++kv) {
-#pragma unroll
-      for (int i = 0; i < PP; ++i)
-        if (at[i] >> A.d_log2 < block) *reinterpret_cast<uint4 *>(co[kv] + at[i]) = p[kv][i].v[0];
-      if (threadIdx.x == 0) *so[kv] = p[kv][0].a;
-    }
-    return;
-  }
-  if (!full) {  // the unfinished block keeps its rows
-#pragma unroll
-    for (int kv = 0; kv < 2; ++kv)
-#pragma unroll
-      for (int i = 0; i < PP; ++i)
-        if (at[i] >> A.d_log2 < rows) {
-          float2 x[8];
-          p[kv][i].template get<FMT, EVICT ? 2 : 0>(x);
-          float y[16];
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            y[2 * e] = x[e].x;
-            y[2 * e + 1] = x[e].y;
-          }
-          store16(static_cast<T *>(kv ? A.out.Vt : A.out.Kt) + (((long)u << bl) << A.d_log2) + at[i], y);
-        }
-    return;
-  }
-  quantise<T, FMT, EVICT ? 2 : 0>(p, at, block << A.d_log2, co, so, red);
-}
-
 constexpr int kCompactPieces = 2;  // of K and of V per thread, all loads in flight together
 
+// One CTA per (unit, destination block) of a prompt's kept rows.
 template <typename T, int FMT>
 __global__ void __launch_bounds__(512) compact_block_kernel(const __grid_constant__ BlockArgs A) {
+  constexpr int PP = kCompactPieces;
   __shared__ float red[2][16];
   __shared__ int src[128];
   pdl_wait();
   pdl_launch();
+  const int block = A.out.block, d = A.out.d, bl = A.b_log2;
   const int u = (int)(blockIdx.x / (unsigned)A.nblk);
   const int b = (int)(blockIdx.x - (unsigned)u * (unsigned)A.nblk);
-  const int m0 = b << A.b_log2;
-  const int rows = min(A.out.block, A.k - m0);
+  const int m0 = b << bl;
+  const int rows = min(block, A.k - m0);
   for (int r = threadIdx.x; r < rows; r += blockDim.x) {
     const int j = A.idx ? A.idx[(long)u * A.k + m0 + r] : m0 + r;
     src[r] = j >= 0 && j < A.T ? j : -1;
   }
   __syncthreads();
-  move_block<T, FMT, false, kCompactPieces>(A, u, b, rows, 0, src, red);
+  const long src0 = (long)u * A.T;
+  Piece<T> p[2][PP];
+  int at[PP];  // first of the piece's 16 elements within the block
+#pragma unroll
+  for (int i = 0; i < PP; ++i) {
+    at[i] = (i * (int)blockDim.x + (int)threadIdx.x) << 4;
+    const int row = at[i] >> A.d_log2;
+    const int j = row < rows ? src[row] : -1;
+    if (j < 0) {
+      p[0][i].zero();
+      p[1][i].zero();
+    } else {
+      const long f = ((src0 + j) << A.d_log2) + (at[i] & (d - 1));
+      p[0][i].load_rows(static_cast<const T *>(A.src[0]) + f);
+      p[1][i].load_rows(static_cast<const T *>(A.src[1]) + f);
+    }
+  }
+  // what moves beside K and V, while they are on their way
+  const long to = (long)u * A.out.cap + m0;
+  for (int r = threadIdx.x; r < rows; r += blockDim.x) {
+    const int j = src[r];
+    if (j < 0) flag_bad(A.status);
+    A.out.pos[to + r] = j;
+    if (A.out.acc) A.out.acc[to + r] = j >= 0 && A.s ? A.s[src0 + j] : 0.f;
+  }
+  if (b == 0 && threadIdx.x == 0) A.out.len[u] = A.k;
+  if (rows < block) {  // the unfinished block keeps its rows
+#pragma unroll
+    for (int kv = 0; kv < 2; ++kv)
+#pragma unroll
+      for (int i = 0; i < PP; ++i)
+        if (at[i] >> A.d_log2 < rows)
+          p[kv][i].store_rows(static_cast<T *>(kv ? A.out.Vt : A.out.Kt) + (((long)u << bl) << A.d_log2) + at[i]);
+    return;
+  }
+  float *const so[2] = {A.out.Ks + (to >> bl), A.out.Vs + (to >> bl)};
+  uint8_t *const co[2] = {static_cast<uint8_t *>(A.out.K) + (to << A.d_log2),
+                          static_cast<uint8_t *>(A.out.V) + (to << A.d_log2)};
+  quantise<T, FMT, 0>(p, at, block << A.d_log2, co, so, red);
 }
 
 // ---- moving a cache's kept slots -----------------------------------------------------
@@ -242,8 +202,7 @@ __global__ void __launch_bounds__(512) compact_block_kernel(const __grid_constan
 // once, at its start; the rows then come through a ring of stages, every thread copying
 // (16 bytes at a time, asynchronously) exactly the pieces that it will decode, so that the
 // stages need no barrier and several blocks' rows are in flight while one is quantised.
-constexpr int NTM = 256;
-constexpr int kRunRows = 1024;  // rows of a run at most
+constexpr int kRunRows = 512;  // rows of a run at most
 
 __device__ __forceinline__ void copy16_async(void *dst, const void *src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
@@ -252,9 +211,70 @@ __device__ __forceinline__ void copy16_async(void *dst, const void *src) {
                : "memory");
 }
 
+// A unit's last blocks: unfinished rows among the sources, or the new unfinished block.  Few,
+// so each piece is read twice (magnitude, then code) rather than held in registers.
+template <typename T, int FMT>
+__device__ __forceinline__ void move_last_block(const BlockArgs &A, int u, int b, int rows, int nf, const int *src,
+                                                const float *sk, const float *sv, float (&red)[2][16]) {
+  const int block = A.out.block, d = A.out.d, bl = A.b_log2, bytes = rows << A.d_log2;
+  const long src0 = (long)u * A.from.cap, to = (long)u * A.out.cap + ((long)b << bl);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+#pragma unroll 1
+  for (int kv = 0; kv < 2; ++kv) {
+    auto piece = [&](int at, float2 (&x)[8]) {
+      const int row = at >> A.d_log2, el = at & (d - 1), j = src[row];
+      Piece<T> p;
+      if (j < nf) {
+        p.v[0] = __ldg(reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(kv ? A.from.V : A.from.K) +
+                                                       ((src0 + j) << A.d_log2) + el));
+        p.a = (kv ? sv : sk)[row];
+        p.coded = true;
+      } else {
+        p.load_rows(static_cast<const T *>(kv ? A.from.Vt : A.from.Kt) + ((((long)u << bl) + (j - nf)) << A.d_log2) + el);
+      }
+      p.template get<FMT, 2>(x);
+    };
+    float2 x[8];
+    if (rows < block) {  // the unfinished block keeps its rows
+#pragma unroll 1
+      for (int at = threadIdx.x << 4; at < bytes; at += blockDim.x << 4) {
+        piece(at, x);
+        float y[16];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          y[2 * e] = x[e].x;
+          y[2 * e + 1] = x[e].y;
+        }
+        store16(static_cast<T *>(kv ? A.out.Vt : A.out.Kt) + (((long)u << bl) << A.d_log2) + at, y);
+      }
+      continue;
+    }
+    float big = 0.f;
+#pragma unroll 1
+    for (int at = threadIdx.x << 4; at < bytes; at += blockDim.x << 4) {
+      piece(at, x);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) big = fmaxf(big, fmaxf(fabsf(x[e].x), fabsf(x[e].y)));
+    }
+    const unsigned m = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(big));
+    if (lane == 0) red[kv][warp] = __uint_as_float(m);
+    __syncthreads();
+    float v = red[kv][0];
+    for (int w = 1; w < (int)blockDim.x >> 5; ++w) v = fmaxf(v, red[kv][w]);
+    const float a = q8_scale<FMT>(v), inv = __fdiv_rn(1.f, a);
+    uint8_t *const co = static_cast<uint8_t *>(kv ? A.out.V : A.out.K) + (to << A.d_log2);
+#pragma unroll 1
+    for (int at = threadIdx.x << 4; at < bytes; at += blockDim.x << 4) {
+      piece(at, x);
+      *reinterpret_cast<uint4 *>(co + at) = q8_pack16<FMT>(x, inv);
+    }
+    if (threadIdx.x == 0) (kv ? A.out.Vs : A.out.Ks)[to >> bl] = a;
+  }
+}
+
 // SQ: 16-byte pieces of a block (K or V) per thread.
-template <typename T, int FMT, int SQ, int ST>
-__global__ void __launch_bounds__(NTM) evict_move_kernel(const __grid_constant__ BlockArgs A, int runs, int run_blocks) {
+template <typename T, int FMT, int NTM, int SQ, int ST>
+__global__ void __launch_bounds__(NTM, 1024 / NTM) evict_move_kernel(const __grid_constant__ BlockArgs A, int runs, int run_blocks) {
   extern __shared__ __align__(16) unsigned char ring[];  // ST stages of K codes, V codes
   __shared__ float red[2][2][16];
   __shared__ int src[kRunRows];
@@ -314,7 +334,7 @@ __global__ void __launch_bounds__(NTM) evict_move_kernel(const __grid_constant__
     const int b = b0 + i, row0 = i << bl;
     if (!in_ring(i)) {  // the unit's last blocks: unfinished rows among them, or not full
       const int left = min(block, rows - row0);
-      move_block<T, FMT, true, SQ>(A, u, b, left, nf, src + row0, red[i & 1]);
+      move_last_block<T, FMT>(A, u, b, left, nf, src + row0, sk + row0, sv + row0, red[i & 1]);
       continue;
     }
     const long to = (long)u * A.out.cap + ((long)b << bl);
@@ -598,16 +618,17 @@ int launch_move(const BlockArgs &A, long units, cudaStream_t st) {
   const int runs = (A.nblk + run - 1) / run;
   if (units * runs > 0x7FFFFFFFL) return KV_ERR_UNSUPPORTED;
   const int bytes = A.out.block * A.out.d;
-  auto go = [&](auto *fn, int stages) {
+  auto go = [&](auto *fn, int threads, int stages) {
     const size_t smem = (size_t)stages * 2 * bytes;
     if (ensure_smem((const void *)fn, smem)) return cuda_failure(cudaErrorInvalidValue, "eviction: shared memory");
-    const cudaError_t e = launch_pdl(fn, (unsigned)(units * runs), NTM, smem, st, A, runs, run);
+    const cudaError_t e = launch_pdl(fn, (unsigned)(units * runs), threads, smem, st, A, runs, run);
     if (e != cudaSuccess) return cuda_failure(e, "eviction: moving the slots");
     return launch_status();
   };
-  if (bytes <= 16 * NTM) return go(evict_move_kernel<T, FMT, 1, 4>, 4);
-  if (bytes <= 32 * NTM) return go(evict_move_kernel<T, FMT, 2, 4>, 4);
-  return go(evict_move_kernel<T, FMT, 4, 3>, 3);
+  if (bytes <= 2048) return go(evict_move_kernel<T, FMT, 128, 1, 4>, 128, 4);
+  if (bytes <= 4096) return go(evict_move_kernel<T, FMT, 256, 1, 4>, 256, 4);
+  if (bytes <= 8192) return go(evict_move_kernel<T, FMT, 256, 2, 3>, 256, 3);
+  return go(evict_move_kernel<T, FMT, 512, 2, 3>, 512, 3);
 }
 
 }  // namespace
