@@ -215,7 +215,7 @@ __device__ __forceinline__ void copy16_async(void *dst, const void *src) {
 // so each piece is read twice (magnitude, then code) rather than held in registers.
 template <typename T, int FMT>
 __device__ __forceinline__ void move_last_block(const BlockArgs &A, int u, int b, int rows, int nf, const int *src,
-                                                const float *sk, const float *sv, float (&red)[2][16]) {
+                                                const float2 *skv, float (&red)[2][16]) {
   const int block = A.out.block, d = A.out.d, bl = A.b_log2, bytes = rows << A.d_log2;
   const long src0 = (long)u * A.from.cap, to = (long)u * A.out.cap + ((long)b << bl);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -227,7 +227,7 @@ __device__ __forceinline__ void move_last_block(const BlockArgs &A, int u, int b
       if (j < nf) {
         p.v[0] = __ldg(reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(kv ? A.from.V : A.from.K) +
                                                        ((src0 + j) << A.d_log2) + el));
-        p.a = (kv ? sv : sk)[row];
+        p.a = kv ? skv[row].y : skv[row].x;
         p.coded = true;
       } else {
         p.load_rows(static_cast<const T *>(kv ? A.from.Vt : A.from.Kt) + ((((long)u << bl) + (j - nf)) << A.d_log2) + el);
@@ -272,16 +272,17 @@ __device__ __forceinline__ void move_last_block(const BlockArgs &A, int u, int b
   }
 }
 
-// SQ: 16-byte pieces of a block (K or V) per thread.
+// SQ: 16-byte pieces of a block (K or V) per thread; a block is NTM * SQ of them.
 template <typename T, int FMT, int NTM, int SQ, int ST>
 __global__ void __launch_bounds__(NTM, 1024 / NTM) evict_move_kernel(const __grid_constant__ BlockArgs A, int runs, int run_blocks) {
+  constexpr int BYTES = NTM * SQ * 16;  // codes of a block of K or V
   extern __shared__ __align__(16) unsigned char ring[];  // ST stages of K codes, V codes
   __shared__ float red[2][2][16];
   __shared__ int src[kRunRows];
-  __shared__ float sk[kRunRows], sv[kRunRows];
+  __shared__ float2 skv[kRunRows];  // the rows' scales
   pdl_wait();
   pdl_launch();
-  const int block = A.out.block, d = A.out.d, bl = A.b_log2;
+  const int block = A.out.block, bl = A.b_log2;
   const int u = (int)(blockIdx.x / (unsigned)runs);
   const int b0 = (int)(blockIdx.x - (unsigned)u * (unsigned)runs) * run_blocks;
   const int n_src = A.from.len[u];
@@ -293,80 +294,115 @@ __global__ void __launch_bounds__(NTM, 1024 / NTM) evict_move_kernel(const __gri
   const int nblk = (rows + block - 1) >> bl;
   const int nf = n_src >> bl << bl;  // slots held as codes
   const long src0 = (long)u * A.from.cap;
-  const float *ks = A.from.Ks + (src0 >> bl), *vs = A.from.Vs + (src0 >> bl);
+  int coded = 0;  // rows whose source is codes: the first ones, slots ascend
   for (int r = threadIdx.x; r < rows; r += NTM) {
     const int j = A.idx[(long)u * A.k + r0 + r];
     src[r] = j;
     if (j < nf) {
-      sk[r] = __ldg(ks + (j >> bl));
-      sv[r] = __ldg(vs + (j >> bl));
+      skv[r] = make_float2(__ldg(A.from.Ks + ((src0 + j) >> bl)), __ldg(A.from.Vs + ((src0 + j) >> bl)));
+      coded = r + 1;
     }
   }
+  const int nring = __reduce_max_sync(0xFFFFFFFFu, coded);
+  if ((threadIdx.x & 31) == 0) red[0][0][threadIdx.x >> 5] = __int_as_float(nring);
   __syncthreads();
-  const int bytes = block << A.d_log2;  // codes of a block of K or V
-  // a block of which every row is codes goes through the ring
-  auto in_ring = [&](int i) { return (i << bl) + block <= rows && src[(i << bl) + block - 1] < nf; };
-  auto fetch = [&](int i) {
-    if (i < nblk && in_ring(i)) {
-      unsigned char *to = ring + (i % ST) * 2 * bytes;
+  int most = 0;
+  for (int w = 0; w < NTM / 32; ++w) most = max(most, __float_as_int(red[0][0][w]));
+  const int ring_blocks = most >> bl;  // blocks of codes alone go through the ring
+  __syncthreads();
+  // this thread's pieces: the same place in every block
+  int prow[SQ];
+  const uint8_t *kq[SQ], *vq[SQ];
+#pragma unroll
+  for (int q = 0; q < SQ; ++q) {
+    const int at = (q * NTM + (int)threadIdx.x) << 4;
+    prow[q] = at >> A.d_log2;
+    const long f = (src0 << A.d_log2) + (at & (A.out.d - 1));
+    kq[q] = static_cast<const uint8_t *>(A.from.K) + f;
+    vq[q] = static_cast<const uint8_t *>(A.from.V) + f;
+  }
+  auto fetch = [&](int i, int stage) {
+    if (i < ring_blocks) {
+      unsigned char *to = ring + stage * 2 * BYTES + (threadIdx.x << 4);
 #pragma unroll
       for (int q = 0; q < SQ; ++q) {
-        const int at = (q * NTM + (int)threadIdx.x) << 4;
-        if (at < bytes) {
-          const long f = ((src0 + src[(i << bl) + (at >> A.d_log2)]) << A.d_log2) + (at & (d - 1));
-          copy16_async(to + at, static_cast<const uint8_t *>(A.from.K) + f);
-          copy16_async(to + bytes + at, static_cast<const uint8_t *>(A.from.V) + f);
-        }
+        const unsigned long long off = (unsigned long long)(unsigned)src[(i << bl) + prow[q]] * (unsigned)A.out.d;
+        copy16_async(to + q * NTM * 16, kq[q] + off);
+        copy16_async(to + q * NTM * 16 + BYTES, vq[q] + off);
       }
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
 #pragma unroll
-  for (int i = 0; i < ST - 1; ++i) fetch(i);
+  for (int i = 0; i < ST - 1; ++i) fetch(i, i);
   for (int r = threadIdx.x; r < rows; r += NTM) {
     const long to = (long)u * A.out.cap + r0 + r;
     A.out.pos[to] = A.from.pos[src0 + src[r]];
     A.out.acc[to] = A.from.acc[src0 + src[r]];
   }
-  for (int i = 0; i < nblk; ++i) {
-    fetch(i + ST - 1);  // into the stage that this thread has read
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const long out0 = (long)u * A.out.cap + r0;
+  uint8_t *ck = static_cast<uint8_t *>(A.out.K) + (out0 << A.d_log2) + (threadIdx.x << 4);
+  uint8_t *cv = static_cast<uint8_t *>(A.out.V) + (out0 << A.d_log2) + (threadIdx.x << 4);
+  float *sok = A.out.Ks + (out0 >> bl), *sov = A.out.Vs + (out0 >> bl);
+  int stage = 0;
+  for (int i = 0; i < ring_blocks; ++i, ck += BYTES, cv += BYTES) {
+    fetch(i + ST - 1, stage == 0 ? ST - 1 : stage - 1);  // into the stage that this thread has just read
     asm volatile("cp.async.wait_group %0;" ::"n"(ST - 1) : "memory");
-    const int b = b0 + i, row0 = i << bl;
-    if (!in_ring(i)) {  // the unit's last blocks: unfinished rows among them, or not full
-      const int left = min(block, rows - row0);
-      move_last_block<T, FMT>(A, u, b, left, nf, src + row0, sk + row0, sv + row0, red[i & 1]);
-      continue;
-    }
-    const long to = (long)u * A.out.cap + ((long)b << bl);
-    float *const so[2] = {A.out.Ks + (to >> bl), A.out.Vs + (to >> bl)};
-    uint8_t *const co[2] = {static_cast<uint8_t *>(A.out.K) + (to << A.d_log2),
-                            static_cast<uint8_t *>(A.out.V) + (to << A.d_log2)};
-    const unsigned char *st = ring + (i % ST) * 2 * bytes;
-    Piece<T> p[2][SQ];
-    int at[SQ];
+    const unsigned char *st = ring + stage * 2 * BYTES + (threadIdx.x << 4);
+    stage = stage + 1 == ST ? 0 : stage + 1;
+    const int row0 = i << bl;
+    uint4 k[SQ], v[SQ];
+    float2 a[SQ];
 #pragma unroll
     for (int q = 0; q < SQ; ++q) {
-      at[q] = (q * NTM + (int)threadIdx.x) << 4;
-      const bool mine = at[q] < bytes;
-      const int r = mine ? row0 + (at[q] >> A.d_log2) : 0;
-      p[0][q].v[0] = mine ? *reinterpret_cast<const uint4 *>(st + at[q]) : make_uint4(0, 0, 0, 0);
-      p[1][q].v[0] = mine ? *reinterpret_cast<const uint4 *>(st + bytes + at[q]) : make_uint4(0, 0, 0, 0);
-      p[0][q].a = mine ? sk[r] : 0.f;
-      p[1][q].a = mine ? sv[r] : 0.f;
+      k[q] = *reinterpret_cast<const uint4 *>(st + q * NTM * 16);
+      v[q] = *reinterpret_cast<const uint4 *>(st + q * NTM * 16 + BYTES);
+      a[q] = skv[row0 + prow[q]];
     }
     const int j0 = src[row0];
     if ((j0 & (block - 1)) == 0 && src[row0 + block - 1] - j0 == block - 1) {
       // a whole block moves: its codes and its scale as they are
 #pragma unroll
-      for (int kv = 0; kv < 2; ++kv) {
-#pragma unroll
-        for (int q = 0; q < SQ; ++q)
-          if (at[q] < bytes) *reinterpret_cast<uint4 *>(co[kv] + at[q]) = p[kv][q].v[0];
-        if (threadIdx.x == 0) *so[kv] = p[kv][0].a;
+      for (int q = 0; q < SQ; ++q) {
+        *reinterpret_cast<uint4 *>(ck + q * NTM * 16) = k[q];
+        *reinterpret_cast<uint4 *>(cv + q * NTM * 16) = v[q];
+      }
+      if (threadIdx.x == 0) {
+        sok[i] = a[0].x;
+        sov[i] = a[0].y;
       }
       continue;
     }
-    quantise<T, FMT, 1>(p, at, bytes, co, so, red[i & 1]);
+    // rounding c a to fp32 keeps the order: a piece's largest code gives its largest value
+    float bk = 0.f, bv = 0.f;
+#pragma unroll
+    for (int q = 0; q < SQ; ++q) {
+      bk = fmaxf(bk, __fmul_rn(Q8<FMT>::big16(k[q]), a[q].x));
+      bv = fmaxf(bv, __fmul_rn(Q8<FMT>::big16(v[q]), a[q].y));
+    }
+    // magnitudes order like their bits
+    const unsigned mk = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(bk));
+    const unsigned mv = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(bv));
+    float (&rd)[2][16] = red[i & 1];
+    if (lane < 2) rd[lane][warp] = __uint_as_float(lane ? mv : mk);
+    __syncthreads();
+    // the lower half of a warp finds K's scale, the upper half V's
+    float big = (lane & 15) < NTM / 32 ? rd[lane >> 4][lane & 15] : 0.f;
+#pragma unroll
+    for (int o = 8; o; o >>= 1) big = fmaxf(big, __shfl_xor_sync(0xFFFFFFFFu, big, o));
+    const float mine = q8_scale<FMT>(big), minv = __fdiv_rn(1.f, mine);
+    const float ik = __shfl_sync(0xFFFFFFFFu, minv, 0), iv = __shfl_sync(0xFFFFFFFFu, minv, 16);
+    if (warp == 0 && (lane & 15) == 0) (lane ? sov : sok)[i] = mine;
+#pragma unroll
+    for (int q = 0; q < SQ; ++q) {
+      *reinterpret_cast<uint4 *>(ck + q * NTM * 16) = q8_requantise16<FMT>(k[q], a[q].x, ik);
+      *reinterpret_cast<uint4 *>(cv + q * NTM * 16) = q8_requantise16<FMT>(v[q], a[q].y, iv);
+    }
+  }
+  for (int i = ring_blocks; i < nblk; ++i) {
+    __syncthreads();
+    move_last_block<T, FMT>(A, u, b0 + i, min(block, rows - (i << bl)), nf, src + (i << bl), skv + (i << bl), red[0]);
   }
 }
 

@@ -52,18 +52,18 @@ template <> struct Q8<KV_Q8_S8> {
     b = __fadd2_rn(make_float2(__uint_as_float(__byte_perm(u, 0x4B000000u, 0x7442)),
                                __uint_as_float(__byte_perm(u, 0x4B000000u, 0x7443))), k);
   }
-  // largest |c| of 16 codes: extremes of c + 128 over 16-bit lanes
+  // Largest |c| of 16 codes: a 16-bit lane orders by its upper byte, so the lanes' maxima
+  // hold the largest upper bytes, and those of the swapped bytes the largest lower ones.
   __device__ __forceinline__ static float big16(const uint4 &v) {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-    uint32_t hi = 0x00800080u, lo = 0x00800080u;
+    uint32_t m[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint32_t u = w[i] ^ 0x80808080u, e = u & 0x00FF00FFu, o = (u >> 8) & 0x00FF00FFu;
-      hi = __vimax3_u16x2(hi, e, o);
-      lo = __vimin3_u16x2(lo, e, o);
-    }
-    const int up = max(hi & 0xFFFFu, hi >> 16), down = min(lo & 0xFFFFu, lo >> 16);
-    return (float)max(up - 128, 128 - down);
+    for (int i = 0; i < 4; ++i) m[i] = __vabsdiffu4(w[i] ^ 0x80808080u, 0x80808080u);
+    uint32_t hi = __vimax3_u16x2(m[0], m[1], __vimax3_u16x2(m[2], m[3], 0u));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) m[i] = __byte_perm(m[i], 0u, 0x2301);
+    hi = __vimax3_u16x2(hi, __vimax3_u16x2(m[0], m[1], m[2]), m[3]);
+    return (float)(max(hi & 0xFFFFu, hi >> 16) >> 8);
   }
 };
 
@@ -116,6 +116,21 @@ __device__ __forceinline__ uint4 q8_pack16(const float (&x)[16], float inv) {
 #pragma unroll
   for (int i = 0; i < 8; ++i) y[i] = make_float2(x[2 * i], x[2 * i + 1]);
   return q8_pack16<FMT>(y, inv);
+}
+
+// 16 codes of scale a as codes of the scale whose reciprocal is inv.
+template <int FMT>
+__device__ __forceinline__ uint4 q8_requantise16(const uint4 &v, float a, float inv) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  const float2 a2 = make_float2(a, a);
+  float2 x[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    Q8<FMT>::unpack4(w[i], x[2 * i], x[2 * i + 1]);
+    x[2 * i] = __fmul2_rn(x[2 * i], a2);
+    x[2 * i + 1] = __fmul2_rn(x[2 * i + 1], a2);
+  }
+  return q8_pack16<FMT>(x, inv);
 }
 
 // 16 consecutive elements of a row in the cache's dtype (16-byte aligned).
