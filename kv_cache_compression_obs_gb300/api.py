@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 import os
 
 import torch
@@ -423,13 +424,46 @@ def _side(stream):
     return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
 
 
-def _strided(*ts):
-    """Tensors whose d elements are adjacent; the other strides are handed to the library."""
+# The calls below are made once per layer and token: their checks read each property of a
+# tensor once, sizes that only depend on sizes are remembered, and the current device and
+# stream are asked of torch's C layer.
+_get_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _device_of(t: torch.Tensor) -> int:
+    """The index of the tensor's CUDA device, which has to be the current one."""
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError("tensors must be contiguous CUDA tensors")
+    if dev != _get_device():
+        _on_current_device(t)
+    return dev
+
+
+def _on(dev: int, *ts):
     for t in ts:
-        if t is not None:
-            if not t.is_cuda or t.stride(-1) != 1:
-                raise ValueError("tensors must be CUDA tensors with adjacent elements along d")
-            _on_current_device(t)
+        if t is not None and (t.get_device() != dev or not t.is_contiguous()):
+            raise ValueError(f"tensors must be contiguous CUDA tensors on cuda:{dev}")
+
+
+def _stream_of(dev: int, stream) -> int:
+    if stream is not None:
+        return stream.cuda_stream
+    return _raw_stream(dev) if _raw_stream is not None else torch.cuda.current_stream().cuda_stream
+
+
+def _at(t):
+    return None if t is None else t.data_ptr()
+
+
+_workspace_bytes = functools.lru_cache(maxsize=4096)(kv_workspace_size)
+
+
+@functools.lru_cache(maxsize=4096)
+def _strides(*st):
+    """Batch, head and token strides of Q, K, V and O as the library takes them."""
+    return (ctypes.c_int64 * 12)(*[x for t in st for x in t[:3]])
 
 
 def kv_attn_prompt(Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, scale: float | None = None,
@@ -448,35 +482,37 @@ def kv_attn_prompt(Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, scale: flo
     Q's memory order."""
     B, Hq, Tq, d = Q.shape
     B2, Hkv, Tk, d2 = K.shape
-    if B2 != B or d2 != d or V.shape != K.shape or not Q.dtype == K.dtype == V.dtype:
+    dt = Q.dtype
+    if B2 != B or d2 != d or V.shape != K.shape or K.dtype != dt or V.dtype != dt:
         raise ValueError("Q, K and V disagree in batch, head dim or dtype")
-    if packed and (seq_q is None or seq_k is None or seq_q.shape != seq_k.shape or seq_q.dim() != 1
-                   or seq_q.numel() < 2):
-        raise ValueError("packed sequences need offsets seq_q and seq_k, [n + 1] each")
+    if packed:
+        if seq_q is None or seq_k is None or seq_q.shape != seq_k.shape or seq_q.dim() != 1 or seq_q.numel() < 2:
+            raise ValueError("packed sequences need offsets seq_q and seq_k, [n + 1] each")
     for t in (seq_q, seq_k):
-        if t is not None and (t.dtype != torch.int32 or (not packed and tuple(t.shape) != (B,))):
+        if t is not None and (t.dtype != torch.int32 or (not packed and t.shape != (B,))):
             raise ValueError("seq_q and seq_k must be int32, one length per batch row unless packed")
+    dev = _device_of(Q)
+    n_seq = seq_q.numel() - 1 if packed else 0
+    need = _workspace_bytes(KV_OP_ATTN_PROMPT, B, Hq, Hkv, max(1, Tk), d, Tq, n_seq)
     with _side(stream):
         o = out if out is not None else torch.empty_like(Q)
-        lse = lse_out if lse_out is not None else torch.empty(B, Hq, Tq, dtype=torch.float32,
-                                                              device=Q.device)
-    if o.shape != Q.shape or o.dtype != Q.dtype:
+        lse = lse_out if lse_out is not None else Q.new_empty((B, Hq, Tq), dtype=torch.float32)
+        ws, nbytes = _workspace(need, Q.device, workspace)
+    if out is not None and (o.shape != Q.shape or o.dtype != dt):
         raise ValueError("out must match Q")
-    if tuple(lse.shape) != (B, Hq, Tq) or lse.dtype != torch.float32:
+    if lse_out is not None and (lse.shape != (B, Hq, Tq) or lse.dtype != torch.float32):
         raise ValueError("lse_out must be [B][Hq][Tq] float32")
-    _strided(Q, K, V, o)
-    _dev(seq_q, seq_k, lse, workspace, dev_status)
+    st = (Q.stride(), K.stride(), V.stride(), o.stride())
+    for t, s in zip((Q, K, V, o), st):
+        if s[3] != 1 or t.get_device() != dev:
+            raise ValueError(f"tensors must be on cuda:{dev} with adjacent elements along d")
+    _on(dev, seq_q, seq_k, lse, workspace, dev_status)
     if scale is None:
         scale = d ** -0.5
-    n_seq = seq_q.numel() - 1 if packed else 0
-    strides = (ctypes.c_int64 * 12)(*[t.stride(i) for t in (Q, K, V, o) for i in range(3)])
-    with _side(stream):
-        ws, nbytes = _workspace(kv_workspace_size(KV_OP_ATTN_PROMPT, B, Hq, Hkv, max(1, Tk), d, Tq, n_seq),
-                                Q.device, workspace)
     _check("kv_attn_prompt", _lib.kv_attn_prompt(
-        _ptr(Q), _ptr(K), _ptr(V), B, Hq, Hkv, Tq, Tk, d, strides, _ptr(seq_q), _ptr(seq_k), n_seq,
-        float(scale), _dtype_code(Q), _ptr(o), _ptr(lse), _ptr(ws), nbytes, _ptr(dev_status),
-        _stream(stream)))
+        Q.data_ptr(), K.data_ptr(), V.data_ptr(), B, Hq, Hkv, Tq, Tk, d, _strides(*st), _at(seq_q), _at(seq_k),
+        n_seq, float(scale), _dtype_code(Q), o.data_ptr(), lse.data_ptr(), _at(ws), nbytes, _at(dev_status),
+        _stream_of(dev, stream)))
     return o, lse
 
 
@@ -501,45 +537,48 @@ def q8_cache(B: int, Hkv: int, cap: int, d: int, block: int = 64, dtype=torch.bf
             "len": z(B, Hkv, dtype=torch.int32)}
 
 
-def _q8(c) -> _Q8Cache:
-    K, Kt = c["K"], c["Kt"]
-    if K.dim() != 4 or Kt.dim() != 4 or K.dtype not in _Q8_CODES:
+_F32, _I32 = torch.float32, torch.int32
+
+
+def _q8(c, dev: int | None = None) -> _Q8Cache:
+    K, V, Ks, Vs, Kt, Vt = c["K"], c["V"], c["Ks"], c["Vs"], c["Kt"], c["Vt"]
+    pos, acc, ln = c["pos"], c.get("acc"), c["len"]
+    shape, tail, fmt = K.shape, Kt.shape, _Q8_CODES.get(K.dtype)
+    if len(shape) != 4 or len(tail) != 4 or fmt is None or tail[2] == 0:
         raise ValueError("not an 8-bit slot cache: see q8_cache")
-    B, H, cap, d = K.shape
-    block = Kt.shape[2]
-    acc = c.get("acc")
-    want = {"V": ((B, H, cap, d), K.dtype), "Ks": ((B, H, cap // max(1, block)), torch.float32),
-            "Vs": ((B, H, cap // max(1, block)), torch.float32), "Kt": ((B, H, block, d), Kt.dtype),
-            "Vt": ((B, H, block, d), Kt.dtype), "pos": ((B, H, cap), torch.int32),
-            "acc": ((B, H, cap), torch.float32), "len": ((B, H), torch.int32)}
-    for name, (shape, dtype) in want.items():
-        t = c[name] if name != "acc" else acc
-        if t is not None and (tuple(t.shape) != shape or t.dtype != dtype):
-            raise ValueError(f"8-bit slot cache: {name} must be {list(shape)} {dtype}")
-    _dev(K, c["V"], c["Ks"], c["Vs"], Kt, c["Vt"], c["pos"], acc, c["len"])
-    return _Q8Cache(*[c[n].data_ptr() for n in ("K", "V", "Ks", "Vs", "Kt", "Vt", "pos")],
-                    None if acc is None else acc.data_ptr(), c["len"].data_ptr(), B, H, cap, d, block,
-                    _dtype_code(Kt), _Q8_CODES[K.dtype])
+    B, H, cap, d = shape
+    block = tail[2]
+    units, blocks, slots = (B, H), (B, H, cap // block), (B, H, cap)
+    if V.shape != shape or tail != (B, H, block, d) or Vt.shape != tail or Ks.shape != blocks or Vs.shape != blocks \
+            or pos.shape != slots or ln.shape != units or (acc is not None and acc.shape != slots):
+        raise ValueError("8-bit slot cache: shapes disagree, see q8_cache")
+    if V.dtype != K.dtype or Vt.dtype != Kt.dtype or Ks.dtype != _F32 or Vs.dtype != _F32 or pos.dtype != _I32 \
+            or ln.dtype != _I32 or (acc is not None and acc.dtype != _F32):
+        raise ValueError("8-bit slot cache: dtypes disagree, see q8_cache")
+    _on(_device_of(K) if dev is None else dev, K, V, Ks, Vs, Kt, Vt, pos, acc, ln)
+    return _Q8Cache(K.data_ptr(), V.data_ptr(), Ks.data_ptr(), Vs.data_ptr(), Kt.data_ptr(), Vt.data_ptr(),
+                    pos.data_ptr(), _at(acc), ln.data_ptr(), B, H, cap, d, block, _dtype_code(Kt), fmt)
 
 
 def kv_compact_q8(K: torch.Tensor, V: torch.Tensor, s, idx, cache, dev_status=None, stream=None):
     """The kept rows of a prompt into an 8-bit slot cache (see q8_cache): K, V [B][Hkv][T][d]
     (CUDA or pinned host), s [B][Hkv][T] float32 or None, idx [B][Hkv][k] int32 ascending or None
     (every row).  Returns `cache`, whose slots 0..k-1 and len are written."""
-    c = _q8(cache)
+    dev = _device_of(cache["K"])
+    c = _q8(cache, dev)
     B, H, T, d = K.shape
     if V.shape != K.shape or V.dtype != K.dtype or (B, H, d) != (c.B, c.Hkv, c.d) \
             or K.dtype != cache["Kt"].dtype:
         raise ValueError("K, V and the cache disagree in batch, heads, head dim or dtype")
-    if idx is not None and (idx.dtype != torch.int32 or idx.dim() != 3 or tuple(idx.shape[:2]) != (B, H)):
+    if idx is not None and (idx.dtype != _I32 or idx.dim() != 3 or idx.shape[:2] != (B, H)):
         raise ValueError("idx must be [B][Hkv][k] int32")
-    if s is not None and (s.dtype != torch.float32 or tuple(s.shape) != (B, H, T)):
+    if s is not None and (s.dtype != _F32 or s.shape != (B, H, T)):
         raise ValueError("s must be [B][Hkv][T] float32")
-    _dev(s, idx, dev_status)
-    _dev_or_pinned(K, V)
-    k = T if idx is None else idx.shape[-1]
-    _check("kv_compact_q8", _lib.kv_compact_q8(_ptr(K), _ptr(V), _ptr(s), _ptr(idx), T, k,
-                                               ctypes.byref(c), _ptr(dev_status), _stream(stream)))
+    _on(dev, s, idx, dev_status)
+    _dev_or_pinned(K, V) if not (K.is_cuda and V.is_cuda) else _on(dev, K, V)
+    k = T if idx is None else idx.shape[2]
+    _check("kv_compact_q8", _lib.kv_compact_q8(K.data_ptr(), V.data_ptr(), _at(s), _at(idx), T, k, ctypes.byref(c),
+                                               _at(dev_status), _stream_of(dev, stream)))
     return cache
 
 
@@ -550,30 +589,33 @@ def h2o_decode_step_q8(q, k_new, v_new, cache, new_pos, scale: float | None = No
     q [B][Hq][d], k_new, v_new [B][Hkv][d]; new_pos an int, or an int32 CUDA tensor [B] of
     positions.  No slot is evicted: a unit must have room (len < cap; kv_evict_q8 makes it).
     len_out [B][Hkv] int32 (default cache["len"]) receives len + 1."""
-    c = _q8(cache)
+    dev = _device_of(q)
+    c = _q8(cache, dev)
     B, Hq, d = q.shape
-    kv = (c.B, c.Hkv, c.d)
-    if (B, d) != (c.B, c.d) or tuple(k_new.shape) != kv or tuple(v_new.shape) != kv \
-            or not q.dtype == k_new.dtype == v_new.dtype == cache["Kt"].dtype:
+    kv, dt = (c.B, c.Hkv, c.d), q.dtype
+    if (B, d) != (c.B, c.d) or k_new.shape != kv or v_new.shape != kv or k_new.dtype != dt or v_new.dtype != dt \
+            or cache["Kt"].dtype != dt:
         raise ValueError("q, k_new, v_new and the cache disagree in batch, heads, head dim or dtype")
     row_pos = new_pos if isinstance(new_pos, torch.Tensor) else None
-    if row_pos is not None and (row_pos.dtype != torch.int32 or tuple(row_pos.shape) != (B,)):
+    if row_pos is not None and (row_pos.dtype != _I32 or row_pos.shape != (B,)):
         raise ValueError("new_pos must be an int or [B] int32")
-    ln = cache["len"] if len_out is None else len_out
-    if ln.dtype != torch.int32 or tuple(ln.shape) != (c.B, c.Hkv):
+    if len_out is None:
+        len_out = cache["len"]
+    elif len_out.dtype != _I32 or len_out.shape != (c.B, c.Hkv):
         raise ValueError("len_out must be [B][Hkv] int32")
+    need = _workspace_bytes(KV_OP_DECODE_Q8, B, Hq, c.Hkv, c.cap, d)
     with _side(stream):
-        o = o_out if o_out is not None else torch.empty(B, Hq, d, dtype=torch.float32, device=q.device)
-        ws, nbytes = _workspace(kv_workspace_size(KV_OP_DECODE_Q8, B, Hq, c.Hkv, c.cap, d), q.device, workspace)
-    if tuple(o.shape) != (B, Hq, d) or o.dtype != torch.float32:
+        o = o_out if o_out is not None else q.new_empty((B, Hq, d), dtype=_F32)
+        ws, nbytes = _workspace(need, q.device, workspace)
+    if o_out is not None and (o.shape != (B, Hq, d) or o.dtype != _F32):
         raise ValueError("o_out must be [B][Hq][d] float32")
-    _dev(q, k_new, v_new, row_pos, ln, o, workspace, dev_status)
+    _on(dev, q, k_new, v_new, row_pos, len_out, o, workspace, dev_status)
     if scale is None:
         scale = d ** -0.5
     _check("h2o_decode_step_q8", _lib.h2o_decode_step_q8(
-        _ptr(q), _ptr(k_new), _ptr(v_new), ctypes.byref(c), Hq, 0 if row_pos is not None else int(new_pos),
-        _ptr(row_pos), _ptr(ln), float(scale), _ptr(o), _ptr(ws), nbytes, _ptr(dev_status),
-        _stream(stream)))
+        q.data_ptr(), k_new.data_ptr(), v_new.data_ptr(), ctypes.byref(c), Hq, 0 if row_pos is not None else int(new_pos),
+        _at(row_pos), len_out.data_ptr(), float(scale), o.data_ptr(), _at(ws), nbytes, _at(dev_status),
+        _stream_of(dev, stream)))
     return o
 
 
@@ -583,18 +625,20 @@ def kv_evict_q8(cache, keep: int, recent: int, into, sink: int = 0, idx_out=None
     attention (its last `recent` slots and positions below `sink` always stay), moved together
     into the cache `into`; `cache` itself is left as it was.  Returns idx [B][Hkv][keep] int32, the
     slot that each new slot came from (-1 behind the new len)."""
-    c, out = _q8(cache), _q8(into)
     if cache.get("acc") is None or into.get("acc") is None:
         raise ValueError("eviction needs the caches' accumulated attention")
-    with _side(stream):
-        idx = idx_out if idx_out is not None else torch.empty(c.B, c.Hkv, keep, dtype=torch.int32,
-                                                              device=cache["K"].device)
-    if idx.dtype != torch.int32 or tuple(idx.shape) != (c.B, c.Hkv, keep):
+    dev = _device_of(cache["K"])
+    c, out = _q8(cache, dev), _q8(into, dev)
+    keep = int(keep)
+    if idx_out is None:
+        with _side(stream):
+            idx_out = cache["len"].new_empty((c.B, c.Hkv, max(0, keep)))
+    elif idx_out.dtype != _I32 or idx_out.shape != (c.B, c.Hkv, keep):
         raise ValueError("idx_out must be [B][Hkv][keep] int32")
-    _dev(idx, dev_status)
-    _check("kv_evict_q8", _lib.kv_evict_q8(ctypes.byref(c), int(keep), int(recent), int(sink), _ptr(idx),
-                                           ctypes.byref(out), _ptr(dev_status), _stream(stream)))
-    return idx
+    _on(dev, idx_out, dev_status)
+    _check("kv_evict_q8", _lib.kv_evict_q8(ctypes.byref(c), keep, int(recent), int(sink), idx_out.data_ptr(),
+                                           ctypes.byref(out), _at(dev_status), _stream_of(dev, stream)))
+    return idx_out
 
 
 def compress_prefill_q8(Q, K, V, W: int, k: int, recent: int, r: float | None, cap: int | None = None,
