@@ -6,8 +6,11 @@
 //     m' = max(m, max_j l_j), z' = z 2^(m - m') + sum_j 2^(l_j - m'), O likewise,
 // l in log2 units, so that 2^l is one instruction.  256 threads as 16 x 16: thread
 // (ty, tx) holds rows ty RT .. ty RT + RT - 1 against keys tx + 16 i, and of O the
-// columns 4 tx .. 4 tx + 3 (+ 64).  K and V take turns in one shared buffer.
-// All arithmetic is fp32.
+// columns 4 tx .. 4 tx + 3 (+ 64).  All arithmetic is fp32.
+// fp32 tiles come by asynchronous copies, K and V double buffered, so that a short prompt
+// (one CTA an SM, nothing else to run meanwhile) does not wait for memory in every tile:
+// 4 heads of 512 tokens 13 us against 36 us with one buffer that K and V take turns in,
+// which bf16 (converted on the way; the tensor cores take all but odd scales) keeps.
 #include <cmath>
 
 #include "attn_common.cuh"
@@ -24,7 +27,8 @@ struct Geo {
   static constexpr int BM = 16 * RT;
   static constexpr int LD = D + 4;   // padded row of the Q and K/V buffers
   static constexpr int LP = BN + 4;  // padded row of P
-  static constexpr int SMEM = (BM * LD + BN * LD + BM * LP) * 4;
+  static constexpr bool ASYNC = sizeof(T) == 4;
+  static constexpr int SMEM = (BM * LD + (ASYNC ? 4 : 1) * BN * LD + BM * LP) * 4;
 };
 
 template <typename T, int D, int RT>
@@ -34,7 +38,7 @@ __global__ void __launch_bounds__(NT) attn_kernel(const T *__restrict__ Q, const
   using Gm = Geo<T, D, RT>;
   constexpr int BM = Gm::BM, LD = Gm::LD, LP = Gm::LP, NV = D / 64, EV = Vec16<T>::N;
   extern __shared__ __align__(16) float sh[];
-  float *sQ = sh, *sX = sQ + BM * LD, *sP = sX + BN * LD;
+  float *sQ = sh, *sP = sQ + BM * LD, *sX = sP + BM * LP;  // sX: K, or K K V V in turns of two
   __shared__ AttnTile st;
   const AttnShape &S = A.S;
   const int h = blockIdx.x % S.Hq;
@@ -82,6 +86,17 @@ __global__ void __launch_bounds__(NT) attn_kernel(const T *__restrict__ Q, const
         *reinterpret_cast<float4 *>(sX + r * LD + c + i) = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
     }
   };
+  auto copy_tile = [&](float *dst, const T *p, long long stride, int j0) {  // the same, asynchronously
+    if (j0 < kend)
+      for (int e = threadIdx.x; e < BN * (D / 4); e += NT) {
+        const int r = e / (D / 4), c = (e % (D / 4)) * 4;
+        const bool have = j0 + r < kend;
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(tc::smem_u32(dst + r * LD + c)),
+                     "l"(p + (have ? (j0 + r) * stride : 0) + c), "r"(have ? 16 : 0)
+                     : "memory");
+      }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
   float m[RT], z[RT], o[RT][NV][4];
 #pragma unroll
   for (int i = 0; i < RT; ++i) {
@@ -92,9 +107,24 @@ __global__ void __launch_bounds__(NT) attn_kernel(const T *__restrict__ Q, const
 #pragma unroll
       for (int x = 0; x < 4; ++x) o[i][c][x] = 0.f;
   }
-  for (int j0 = 0; j0 < kend; j0 += BN) {
-    load_tile(k, S.k[2], j0);
-    __syncthreads();
+  if constexpr (Gm::ASYNC) {
+    copy_tile(sX, k, S.k[2], 0);
+    copy_tile(sX + 2 * BN * LD, v, S.v[2], 0);
+  }
+  int buf = 0;
+  for (int j0 = 0; j0 < kend; j0 += BN, buf ^= 1) {
+    const float *sK = sX, *sV = sX;
+    if constexpr (Gm::ASYNC) {
+      asm volatile("cp.async.wait_group 1;" ::: "memory");  // K
+      __syncthreads();  // everyone's pieces, and the other buffers have been read
+      copy_tile(sX + (buf ^ 1) * BN * LD, k, S.k[2], j0 + BN);
+      copy_tile(sX + (2 + (buf ^ 1)) * BN * LD, v, S.v[2], j0 + BN);
+      sK = sX + buf * BN * LD;
+      sV = sX + (2 + buf) * BN * LD;
+    } else {
+      load_tile(k, S.k[2], j0);
+      __syncthreads();
+    }
     float s[RT][4];
 #pragma unroll
     for (int i = 0; i < RT; ++i)
@@ -106,7 +136,7 @@ __global__ void __launch_bounds__(NT) attn_kernel(const T *__restrict__ Q, const
 #pragma unroll
       for (int i = 0; i < RT; ++i) a[i] = *reinterpret_cast<const float4 *>(sQ + (ty * RT + i) * LD + c);
 #pragma unroll
-      for (int x = 0; x < 4; ++x) b[x] = *reinterpret_cast<const float4 *>(sX + (tx + 16 * x) * LD + c);
+      for (int x = 0; x < 4; ++x) b[x] = *reinterpret_cast<const float4 *>(sK + (tx + 16 * x) * LD + c);
 #pragma unroll
       for (int i = 0; i < RT; ++i)
 #pragma unroll
@@ -136,9 +166,14 @@ __global__ void __launch_bounds__(NT) attn_kernel(const T *__restrict__ Q, const
 #pragma unroll
         for (int x = 0; x < 4; ++x) o[i][c][x] *= f;
     }
-    __syncthreads();
-    load_tile(v, S.v[2], j0);
-    __syncthreads();
+    if constexpr (Gm::ASYNC) {
+      asm volatile("cp.async.wait_group 2;" ::: "memory");  // V
+      __syncthreads();
+    } else {
+      __syncthreads();
+      load_tile(v, S.v[2], j0);
+      __syncthreads();
+    }
 #pragma unroll 4
     for (int j = 0; j < BN; j += 4) {
       float4 p[RT];
@@ -148,7 +183,7 @@ __global__ void __launch_bounds__(NT) attn_kernel(const T *__restrict__ Q, const
       for (int c = 0; c < NV; ++c) {
         float4 x[4];
 #pragma unroll
-        for (int y = 0; y < 4; ++y) x[y] = *reinterpret_cast<const float4 *>(sX + (j + y) * LD + 4 * tx + 64 * c);
+        for (int y = 0; y < 4; ++y) x[y] = *reinterpret_cast<const float4 *>(sV + (j + y) * LD + 4 * tx + 64 * c);
 #pragma unroll
         for (int i = 0; i < RT; ++i) {
           o[i][c][0] += p[i].x * x[0].x + p[i].y * x[1].x + p[i].z * x[2].x + p[i].w * x[3].x;
@@ -158,7 +193,7 @@ __global__ void __launch_bounds__(NT) attn_kernel(const T *__restrict__ Q, const
         }
       }
     }
-    __syncthreads();
+    if constexpr (!Gm::ASYNC) __syncthreads();
   }
 #pragma unroll
   for (int i = 0; i < RT; ++i) {
