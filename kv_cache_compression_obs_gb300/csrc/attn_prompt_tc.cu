@@ -117,6 +117,32 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return d;
 }
 
+// Loads of N registers issued before have landed: nothing that uses them moves above this.
+template <int N>
+__device__ __forceinline__ void tmem_landed(uint32_t *r) {
+  tc::tmem_ld_wait();
+#pragma unroll
+  for (int x = 0; x < N; ++x) asm volatile("" : "+r"(r[x]));
+}
+
+// Largest of 64 logits; those behind index lim become -inf first (lim >= 63: none).
+__device__ __forceinline__ float half_max(uint32_t *r, int lim) {
+  if (lim < 63) {
+#pragma unroll
+    for (int x = 0; x < 64; ++x) r[x] = x <= lim ? r[x] : 0xFF800000u;
+  }
+  float mx[4];
+#pragma unroll
+  for (int q = 0; q < 4; ++q) mx[q] = __uint_as_float(r[q]);
+#pragma unroll
+  for (int x = 4; x < 60; x += 8)
+#pragma unroll
+    for (int q = 0; q < 4; ++q) mx[q] = max3(mx[q], __uint_as_float(r[x + 2 * q]), __uint_as_float(r[x + 2 * q + 1]));
+  mx[0] = max3(mx[0], __uint_as_float(r[60]), __uint_as_float(r[61]));
+  mx[1] = max3(mx[1], __uint_as_float(r[62]), __uint_as_float(r[63]));
+  return max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]);
+}
+
 // V tile as the second operand of P V: n (d) is contiguous, 64 elements per 128-byte
 // row, one row per key; 1024 bytes per group of 8 keys, `SUB` bytes to the next 64
 // elements of d.
@@ -158,7 +184,7 @@ __device__ __forceinline__ Work make_work(const TcArgs &T, const AttnTile &t, in
 // Barriers and what else the roles share.
 struct Ctrl {
   uint64_t full[kMaxStages], empty[kMaxStages];
-  uint64_t qfull[2], qempty[2], sfull[2], pfull[4], ofull[2], oempty[2], wfull[2], wempty[2];
+  uint64_t qfull[2], qempty[2], sfull[2], pfull[4], pva[2], ofull[2], oempty[2], wfull[2], wempty[2];
   uint64_t clc, drain, vreq, vfix;
   uint4 reply;
   Work work[2];
@@ -218,6 +244,7 @@ __global__ void __launch_bounds__(NT, 1)
       tc::mbar_init(C.sfull + i, 1);
       tc::mbar_init(C.pfull + i, 4);
       tc::mbar_init(C.pfull + 2 + i, 4);
+      tc::mbar_init(C.pva + i, 1);
       tc::mbar_init(C.ofull + i, 1);
       tc::mbar_init(C.oempty + i, 4);
       tc::mbar_init(C.wfull + i, 1);
@@ -365,6 +392,7 @@ __global__ void __launch_bounds__(NT, 1)
                   for (int kk = hf * 4; kk < hf * 4 + 4; ++kk)
                     umma_ts(tmem + 256 + i * 128, tmem + i * 128 + kk * 8, vd + (uint64_t)((kk * 2048) >> 4), id_o,
                             (j > 0) | (kk > 0));
+                  if (hf == 0) tc::umma_commit(C.pva + i);
                 }
                 ++ps[i];
                 if (j == n[i] - 1) tc::umma_commit(C.ofull + i);
@@ -435,72 +463,75 @@ __global__ void __launch_bounds__(NT, 1)
         ok = __all_sync(0xFFFFFFFFu, wait(C.sfull + i, ss++));
         if (!ok) break;
         tc::fence_after_sync();
+        // The tile in two steps of 64 keys: the second half's logits arrive and are searched for
+        // their maximum while the first half's weights are computed, and the first half's
+        // product runs while the second half's are.
         uint32_t r[128];
+        tmem_ld32(ts, r);
+        tmem_ld32(ts + 32, r + 32);
+        tmem_landed<64>(r);
+        tmem_ld32(ts + 64, r + 64);
+        tmem_ld32(ts + 96, r + 96);
+        const int lim = mine - j * BN;                   // last key of the tile that this row sees
+        const bool part = j * BN + BN - 1 > first;       // some row sees only part of the tile
+        float top[2];
+        top[0] = half_max(r, part ? lim : BN) * c;
+        tmem_landed<64>(r + 64);
+        top[1] = half_max(r + 64, part ? lim - 64 : BN) * c;
 #pragma unroll
-        for (int q = 0; q < 4; ++q) tmem_ld32(ts + q * 32, r + q * 32);
-        tc::tmem_ld_wait();
-        const int j0 = j * BN;
-        if (j0 + BN - 1 > first) {  // some row sees only part of the tile
-          const int lim = mine - j0;
+        for (int hf = 0; hf < 2; ++hf) {
+          const bool over = top[hf] > m + kLazy;
+          if (__any_sync(0xFFFFFFFFu, over)) {
+            const float f = over ? tc::ex2(m - top[hf]) : 1.f;
+            if (over) m = top[hf];
+            z2.x *= f;
+            z2.y *= f;
+            // O holds every product before this half: those of the tiles before are complete
+            // (the commit that announced S covers them), the first half's has its own
+            if (hf == 1) {
+              ok = __all_sync(0xFFFFFFFFu, wait(C.pva + i, ss - 1));
+              if (!ok) break;
+              tc::fence_after_sync();
+            }
+            if (j > 0 || hf == 1) {
 #pragma unroll
-          for (int x = 0; x < 128; ++x) r[x] = x <= lim ? r[x] : 0xFF800000u;
-        }
-        float mx[4];
+              for (int q = 0; q < D / 16; ++q) {
+                uint32_t o[16];
+                tc::tmem_ld16(to + q * 16, o);
+                tc::tmem_ld_wait();
 #pragma unroll
-        for (int q = 0; q < 4; ++q) mx[q] = __uint_as_float(r[q]);
-#pragma unroll
-        for (int x = 4; x < 124; x += 8)
-#pragma unroll
-          for (int q = 0; q < 4; ++q)
-            mx[q] = max3(mx[q], __uint_as_float(r[x + 2 * q]), __uint_as_float(r[x + 2 * q + 1]));
-        mx[0] = max3(mx[0], __uint_as_float(r[124]), __uint_as_float(r[125]));
-        mx[1] = max3(mx[1], __uint_as_float(r[126]), __uint_as_float(r[127]));
-        const float top = max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]) * c;
-        const bool over = top > m + kLazy;
-        if (__any_sync(0xFFFFFFFFu, over)) {
-          const float f = over ? tc::ex2(m - top) : 1.f;
-          if (over) m = top;
-          z2.x *= f;
-          z2.y *= f;
-          if (j > 0) {
-#pragma unroll
-            for (int q = 0; q < D / 16; ++q) {
-              uint32_t o[16];
-              tc::tmem_ld16(to + q * 16, o);
-              tc::tmem_ld_wait();
-#pragma unroll
-              for (int x = 0; x < 16; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * f);
-              tmem_st16(to + q * 16, o);
+                for (int x = 0; x < 16; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * f);
+                tmem_st16(to + q * 16, o);
+              }
             }
           }
-        }
-        const float base = m == -INFINITY ? 0.f : -m;  // a row that has seen no key yet
-        const float2 c2 = make_float2(c, c), b2 = make_float2(base, base);
+          const float base = m == -INFINITY ? 0.f : -m;  // a row that has seen no key yet
+          const float2 c2 = make_float2(c, c), b2 = make_float2(base, base);
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          uint32_t p[16];
-          float2 a0 = make_float2(0.f, 0.f), a1 = a0;
+          for (int q = 2 * hf; q < 2 * hf + 2; ++q) {
+            uint32_t p[16];
+            float2 a0 = make_float2(0.f, 0.f), a1 = a0;
 #pragma unroll
-          for (int x = 0; x < 16; x += 2) {
-            const int s = q * 32 + 2 * x;
-            const float2 u = __ffma2_rn(make_float2(__uint_as_float(r[s]), __uint_as_float(r[s + 1])), c2, b2);
-            const float2 v = __ffma2_rn(make_float2(__uint_as_float(r[s + 2]), __uint_as_float(r[s + 3])), c2, b2);
-            const float2 eu = make_float2(tc::ex2(u.x), tc::ex2(u.y)), ev = make_float2(tc::ex2(v.x), tc::ex2(v.y));
-            a0 = __fadd2_rn(a0, eu);
-            a1 = __fadd2_rn(a1, ev);
-            const __nv_bfloat162 h0 = __floats2bfloat162_rn(eu.x, eu.y), h1 = __floats2bfloat162_rn(ev.x, ev.y);
-            p[x] = *reinterpret_cast<const uint32_t *>(&h0);
-            p[x + 1] = *reinterpret_cast<const uint32_t *>(&h1);
+            for (int x = 0; x < 16; x += 2) {
+              const int s = q * 32 + 2 * x;
+              const float2 u = __ffma2_rn(make_float2(__uint_as_float(r[s]), __uint_as_float(r[s + 1])), c2, b2);
+              const float2 v = __ffma2_rn(make_float2(__uint_as_float(r[s + 2]), __uint_as_float(r[s + 3])), c2, b2);
+              const float2 eu = make_float2(tc::ex2(u.x), tc::ex2(u.y)), ev = make_float2(tc::ex2(v.x), tc::ex2(v.y));
+              a0 = __fadd2_rn(a0, eu);
+              a1 = __fadd2_rn(a1, ev);
+              const __nv_bfloat162 h0 = __floats2bfloat162_rn(eu.x, eu.y), h1 = __floats2bfloat162_rn(ev.x, ev.y);
+              p[x] = *reinterpret_cast<const uint32_t *>(&h0);
+              p[x + 1] = *reinterpret_cast<const uint32_t *>(&h1);
+            }
+            z2 = __fadd2_rn(z2, __fadd2_rn(a0, a1));
+            tmem_st16(ts + q * 16, p);
           }
-          z2 = __fadd2_rn(z2, __fadd2_rn(a0, a1));
-          tmem_st16(ts + q * 16, p);
-          if (q & 1) {
-            tmem_st_wait();
-            tc::fence_before_sync();
-            __syncwarp();
-            if (lane == 0) tc::mbar_arrive(C.pfull + (q & 2) + i);
-          }
+          tmem_st_wait();
+          tc::fence_before_sync();
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive(C.pfull + 2 * hf + i);
         }
+        if (!ok) break;
       }
       if (!ok) break;
       // ---- O / z ----
