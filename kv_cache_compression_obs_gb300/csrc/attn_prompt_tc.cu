@@ -28,6 +28,7 @@
 #include <cmath>
 
 #include "attn_common.cuh"
+#include "pdl.cuh"
 #include "tc_common.cuh"
 
 namespace kvc {
@@ -60,6 +61,7 @@ struct TcArgs {
   AttnArgs A;
   __nv_bfloat16 *O;
   int pair_rows;  // 1: the two tiles are the halves of 256 rows; 0: two heads
+  int wide;       // O's rows start on 32-byte boundaries
 };
 
 __device__ __forceinline__ void tma_load_4d(void *dst, const CUtensorMap *map, int x, int y, int z, int w,
@@ -115,6 +117,12 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   float d;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
+}
+
+__device__ __forceinline__ void st_global_32(void *a, const uint32_t *r) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(a), "r"(r[0]), "r"(r[1]), "r"(r[2]),
+               "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
 }
 
 // Loads of N registers issued before have landed: nothing that uses them moves above this.
@@ -185,7 +193,7 @@ __device__ __forceinline__ Work make_work(const TcArgs &T, const AttnTile &t, in
 struct Ctrl {
   uint64_t full[kMaxStages], empty[kMaxStages];
   uint64_t qfull[2], qempty[2], sfull[2], pfull[4], pva[2], ofull[2], oempty[2], wfull[2], wempty[2];
-  uint64_t clc, drain, vreq, vfix;
+  uint64_t clc, drain, vreq, vfix, want;
   uint4 reply;
   Work work[2];
   uint32_t tmem;
@@ -254,10 +262,22 @@ __global__ void __launch_bounds__(NT, 1)
     tc::mbar_init(&C.drain, 1);
     tc::mbar_init(&C.vreq, 1);
     tc::mbar_init(&C.vfix, 1);
+    tc::mbar_init(&C.want, 1);
     C.abort_flag = 0;
     tc::mbar_fence_init();
   }
   if (warp == W_MMA) tc::tmem_alloc(&C.tmem, 512);
+  if (warp == W_TMA && lane == 0) {
+    tc::tma_prefetch_desc(&tmQ);
+    tc::tma_prefetch_desc(&tmK);
+    tc::tma_prefetch_desc(&tmV);
+  }
+  pdl_wait();
+  pdl_launch();
+  Work first_work{};
+  if (warp == W_SCHED)
+    first_work = make_work(T, attn_locate(S, blockIdx.x / groups, T.pair_rows ? 2 * BM : BM, blockIdx.x == 0, T.A.status),
+                           blockIdx.x % groups);
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
@@ -277,25 +297,25 @@ __global__ void __launch_bounds__(NT, 1)
     if (warp == W_SCHED) {
       // ---- which work: the CTA's own index, then those of CTAs that have not started,
       // which the hardware hands over on request (in index order: long tiles first) ----
-      int block = blockIdx.x;
+      // A request goes out when the loads of the item at hand are all issued: early enough for
+      // the reply, late enough that a CTA with a long item does not sit on the next one.
+      Work w = first_work;
       for (uint32_t k = 0;; ++k) {
-        Work w{};
-        if (block >= 0) {
-          const AttnTile t = attn_locate(S, block / groups, T.pair_rows ? 2 * BM : BM, block == 0, T.A.status);
-          w = make_work(T, t, block % groups);
-        } else {
-          w.t.nq = -1;
-        }
         const bool ok = wait(C.wempty + (k & 1), (k >> 1) ^ 1);
         if (lane == 0) {
           C.work[k & 1] = w;
           tc::mbar_arrive(C.wfull + (k & 1));
         }
-        if (!__all_sync(0xFFFFFFFFu, ok) || block < 0) break;
+        if (!__all_sync(0xFFFFFFFFu, ok) || w.t.nq < 0) break;
+        if (!__all_sync(0xFFFFFFFFu, wait(&C.want, k))) break;
         if (lane == 0) clc_request(C.reply, &C.clc);
         __syncwarp();
-        block = wait(&C.clc, k) ? clc_block(C.reply) : -1;
+        int block = wait(&C.clc, k) ? clc_block(C.reply) : -1;
         block = __shfl_sync(0xFFFFFFFFu, block, 0);
+        if (block >= 0)
+          w = make_work(T, attn_locate(S, block / groups, T.pair_rows ? 2 * BM : BM, false, T.A.status), block % groups);
+        else
+          w.t.nq = -1;
       }
     } else if (warp == W_TMA) {
       // ---- loads: Q_0, Q_1 and K_0 V_0 K_1 V_1 ... of every item through one ring ----
@@ -325,6 +345,7 @@ __global__ void __launch_bounds__(NT, 1)
                           w.t.b, C.full + st);
             ++x;
           }
+          tc::mbar_arrive(&C.want);
           tc::mbar_arrive(C.wempty + (k & 1));
         }
         // copies in flight land before the CTA may exit (at once unless it gave up)
@@ -560,7 +581,11 @@ __global__ void __launch_bounds__(NT, 1)
                                                            z > 0.f ? __uint_as_float(o[2 * x + 1]) * inv : 0.f);
             p[x] = *reinterpret_cast<const uint32_t *>(&v);
           }
-          if (live) {
+          // every lane writes its own row: whole 32-byte sectors where they are aligned
+          if (live && T.wide) {
+            st_global_32(dst + q * 32, p);
+            st_global_32(dst + q * 32 + 16, p + 8);
+          } else if (live) {
 #pragma unroll
             for (int x = 0; x < 4; ++x)
               reinterpret_cast<uint4 *>(dst + q * 32)[x] = make_uint4(p[4 * x], p[4 * x + 1], p[4 * x + 2], p[4 * x + 3]);
@@ -605,7 +630,8 @@ int run(const void *Q, const void *K, const void *V, const TcArgs &T, cudaStream
   const long ctas = attn_tiles(S, T.pair_rows ? 2 * BM : BM) * (T.pair_rows ? S.Hq : S.Hq / 2);
   if (ctas > 0x7FFFFFFFL) return KV_ERR_UNSUPPORTED;
   if (ensure_smem((const void *)attn_tc_kernel<D>, Geo<D>::SMEM)) return KV_ERR_CUDA;
-  attn_tc_kernel<D><<<(unsigned)ctas, NT, Geo<D>::SMEM, st>>>(tmQ, tmK, tmV, T);
+  const cudaError_t e = launch_pdl(attn_tc_kernel<D>, (unsigned)ctas, NT, Geo<D>::SMEM, st, tmQ, tmK, tmV, T);
+  if (e != cudaSuccess) return cuda_failure(e, "prompt attention");
   return launch_status();
 }
 
@@ -617,7 +643,9 @@ bool attn_tc_eligible(const AttnShape &S, float scale, int dtype) {
 }
 
 int launch_attn_prompt_tc(const void *Q, const void *K, const void *V, const AttnArgs &A, void *O, cudaStream_t st) {
-  TcArgs T{A, static_cast<__nv_bfloat16 *>(O), (A.S.Hq / A.S.Hkv) % 2};
+  bool wide = (reinterpret_cast<uintptr_t>(O) & 31) == 0;
+  for (int i = 0; i < 3; ++i) wide = wide && A.S.o[i] % 16 == 0;
+  TcArgs T{A, static_cast<__nv_bfloat16 *>(O), (A.S.Hq / A.S.Hkv) % 2, wide};
   return A.S.d == 128 ? run<128>(Q, K, V, T, st) : run<64>(Q, K, V, T, st);
 }
 
