@@ -493,7 +493,7 @@ def kv_attn_prompt(Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, scale: flo
             raise ValueError("seq_q and seq_k must be int32, one length per batch row unless packed")
     dev = _device_of(Q)
     n_seq = seq_q.numel() - 1 if packed else 0
-    need = _workspace_bytes(KV_OP_ATTN_PROMPT, B, Hq, Hkv, max(1, Tk), d, Tq, n_seq)
+    need = _workspace_bytes(KV_OP_ATTN_PROMPT, B, Hq, Hkv, max(1, Tk), d, Tq, n_seq) if dt == torch.bfloat16 else 0
     with _side(stream):
         o = out if out is not None else torch.empty_like(Q)
         lse = lse_out if lse_out is not None else Q.new_empty((B, Hq, Tq), dtype=torch.float32)

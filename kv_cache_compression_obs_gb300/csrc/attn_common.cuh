@@ -83,7 +83,9 @@ __device__ __forceinline__ AttnTile attn_locate(const AttnShape &S, int index, i
 }
 
 bool attn_tc_eligible(const AttnShape &S, float scale, int dtype);
-int launch_attn_prompt_tc(const void *Q, const void *K, const void *V, const AttnArgs &A, void *O, cudaStream_t st);
+size_t attn_tc_workspace_bytes(const AttnShape &S);
+int launch_attn_prompt_tc(const void *Q, const void *K, const void *V, const AttnArgs &A, void *O, void *ws,
+                          cudaStream_t st);
 
 // Tiles at most: every sequence may end in a partial one.
 inline long attn_tiles(const AttnShape &S, int bm) {

@@ -242,16 +242,23 @@ int run_rows(const void *Q, const void *K, const void *V, void *O, const AttnArg
 
 }  // namespace
 
+// For bf16, whose rows may be split over their keys; fp32 needs none.
 size_t attn_prompt_workspace_bytes(int B, int Hq, int Hkv, int Tq, int Tk, int d, int n_seq) {
-  (void)B; (void)Hq; (void)Hkv; (void)Tq; (void)Tk; (void)d; (void)n_seq;
-  return 0;
+  AttnShape S{};
+  S.B = B;
+  S.Hq = Hq;
+  S.Hkv = Hkv;
+  S.Tq = Tq;
+  S.Tk = Tk;
+  S.d = d;
+  S.n_seq = n_seq;
+  return attn_tc_workspace_bytes(S);
 }
 
 int launch_attn_prompt(const void *Q, const void *K, const void *V, const AttnShape &S, float scale, int dtype,
                        void *O, float *lse, void *ws, int *status, cudaStream_t st) {
-  (void)ws;
   AttnArgs A{S, scale * 1.4426950408889634f, lse, status};
-  if (attn_tc_eligible(S, scale, dtype)) return launch_attn_prompt_tc(Q, K, V, A, O, st);
+  if (attn_tc_eligible(S, scale, dtype)) return launch_attn_prompt_tc(Q, K, V, A, O, ws, st);
   if (dtype == KV_BF16)
     return S.d == 128 ? run_rows<__nv_bfloat16, 128>(Q, K, V, O, A, st) : run_rows<__nv_bfloat16, 64>(Q, K, V, O, A, st);
   return S.d == 128 ? run_rows<float, 128>(Q, K, V, O, A, st) : run_rows<float, 64>(Q, K, V, O, A, st);

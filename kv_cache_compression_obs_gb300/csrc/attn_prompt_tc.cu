@@ -62,6 +62,9 @@ struct TcArgs {
   __nv_bfloat16 *O;
   int pair_rows;  // 1: the two tiles are the halves of 256 rows; 0: two heads
   int wide;       // O's rows start on 32-byte boundaries
+  int splits;     // items per query tile, each with a share of its key tiles
+  float *part;    // splits > 1: [splits][B][Hq][Tq][D] sums of P V, not yet divided
+  float2 *stat;   // [splits][B][Hq][Tq] reference (log2 units) and sum of weights
 };
 
 __device__ __forceinline__ void tma_load_4d(void *dst, const CUtensorMap *map, int x, int y, int z, int w,
@@ -170,12 +173,15 @@ struct Work {
   AttnTile t;
   int h[2], r0[2], rows[2], n[2];  // per tile: head, first row, rows, key tiles
   int nmax;
+  int split, j0;  // share of the key tiles: the first of them
 };
 
-__device__ __forceinline__ Work make_work(const TcArgs &T, const AttnTile &t, int hi) {
+__device__ __forceinline__ Work make_work(const TcArgs &T, const AttnTile &t, int part) {
   Work w;
   w.t = t;
   w.nmax = 0;
+  const int hi = part / T.splits;
+  w.split = part - hi * T.splits;
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     w.h[i] = T.pair_rows ? hi : 2 * hi + i;
@@ -185,6 +191,14 @@ __device__ __forceinline__ Work make_work(const TcArgs &T, const AttnTile &t, in
     const int kend = w.rows[i] ? min(t.nk, max(0, w.r0[i] + w.rows[i] + t.nk - t.nq)) : 0;
     w.n[i] = (kend + BN - 1) / BN;
     w.nmax = max(w.nmax, w.n[i]);
+  }
+  w.j0 = 0;
+  if (T.splits > 1) {
+    const int per = (w.nmax + T.splits - 1) / T.splits;
+    w.j0 = w.split * per;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) w.n[i] = max(0, min(per, w.n[i] - w.j0));
+    w.nmax = max(w.n[0], w.n[1]);
   }
   return w;
 }
@@ -239,7 +253,7 @@ __global__ void __launch_bounds__(NT, 1)
   Ctrl &C = *reinterpret_cast<Ctrl *>(sm + Gm::CTRL_OFF);
   const AttnShape &S = T.A.S;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int groups = T.pair_rows ? S.Hq : S.Hq / 2;
+  const int groups = (T.pair_rows ? S.Hq : S.Hq / 2) * T.splits;  // items per query tile
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < ST; ++i) {
@@ -341,7 +355,7 @@ __global__ void __launch_bounds__(NT, 1)
             if (!ok) break;
             tc::mbar_arrive_expect_tx(C.full + st, Gm::TILE);
             for (int c = 0; c < Gm::NKB; ++c)
-              tma_load_4d(sKV + st * Gm::TILE + c * Gm::SUB, (y & 1) ? &tmV : &tmK, c * 64, w.t.k0 + (y >> 1) * BN, hk,
+              tma_load_4d(sKV + st * Gm::TILE + c * Gm::SUB, (y & 1) ? &tmV : &tmK, c * 64, w.t.k0 + (w.j0 + (y >> 1)) * BN, hk,
                           w.t.b, C.full + st);
             ++x;
           }
@@ -375,7 +389,7 @@ __global__ void __launch_bounds__(NT, 1)
         int st = 0;
         uint32_t ph = 0, fixes = 0, items[2] = {0, 0}, ps[2] = {0, 0};
         auto item = [&](const Work &w) -> bool {
-          const int n[2] = {w.n[0], w.n[1]}, nmax = w.nmax, nk = w.t.nk;
+          const int n[2] = {w.n[0], w.n[1]}, nmax = w.nmax, nk = w.t.nk - w.j0 * BN;
           if (nmax == 0) return true;
 #pragma unroll
           for (int i = 0; i < 2; ++i)
@@ -446,7 +460,7 @@ __global__ void __launch_bounds__(NT, 1)
       uint32_t x = 0, fixes = 0;
       for (uint32_t k = 0; have_item(k); ++k) {
         const Work &w = C.work[k & 1];
-        const int left = w.t.nk - (w.nmax - 1) * BN;
+        const int left = w.t.nk - (w.j0 + w.nmax - 1) * BN;
         x += 2 * w.nmax;
         if (w.nmax > 0 && left < BN) {
           unsigned char *v = sKV + ((x - 1) % ST) * Gm::TILE + left * 128;
@@ -475,8 +489,8 @@ __global__ void __launch_bounds__(NT, 1)
     for (uint32_t it = 0; have_item(it); ++it) {
       const Work &w = C.work[it & 1];
       const int n = w.n[i];
-      const int first = w.r0[i] + w.t.nk - w.t.nq;     // last key that the tile's first row sees
-      const int mine = min(first + row, w.t.nk - 1);   // ... that this row sees
+      const int first = w.r0[i] + w.t.nk - w.t.nq - w.j0 * BN;     // last key that the tile's first row sees
+      const int mine = min(first + row, w.t.nk - 1 - w.j0 * BN);   // ... that this row sees
       float m = -INFINITY;                             // reference, log2 units
       float2 z2 = make_float2(0.f, 0.f);
       bool ok = true;
@@ -561,7 +575,24 @@ __global__ void __launch_bounds__(NT, 1)
         if (!ok) break;
         tc::fence_after_sync();
       }
-      if (w.rows[i] > 0) {
+      if (T.splits > 1 && w.rows[i] > 0) {
+        // this share of the keys, for attn_join_kernel
+        const long long at = (((long long)w.split * S.B + w.t.b) * S.Hq + w.h[i]) * S.Tq + w.t.q0 + w.r0[i] + row;
+        const bool live = row < w.rows[i];
+        if (live) T.stat[at] = make_float2(m, z2.x + z2.y);
+        if (n > 0) {
+#pragma unroll
+          for (int q = 0; q < D / 32; ++q) {
+            uint32_t o[32];
+            tmem_ld32(to + q * 32, o);
+            tc::tmem_ld_wait();
+            if (live) {
+#pragma unroll
+              for (int x = 0; x < 32; x += 8) st_global_32(T.part + at * D + q * 32 + x, o + x);
+            }
+          }
+        }
+      } else if (w.rows[i] > 0) {
         const float z = z2.x + z2.y;
         const float inv = z > 0.f ? 1.f / z : 0.f;
         const long long at = (long long)w.t.q0 + w.r0[i] + row;
@@ -608,6 +639,83 @@ __global__ void __launch_bounds__(NT, 1)
   if (warp == W_MMA) tc::tmem_dealloc(tmem, 512);
 }
 
+// Joins the shares of split rows: O = sum_s 2^(m_s - M) O_s / sum_s 2^(m_s - M) z_s.  One CTA
+// per (query tile, head); a row is D / 4 threads, all its shares in flight.
+constexpr int kMaxSplits = 16;
+constexpr int NTJ = 256, JM = 32;  // threads and rows of a CTA
+template <int D>
+__global__ void __launch_bounds__(NTJ) attn_join_kernel(const __grid_constant__ TcArgs T) {
+  __shared__ AttnTile tile;
+  const AttnShape &S = T.A.S;
+  pdl_wait();
+  pdl_launch();
+  const int h = blockIdx.x % S.Hq;
+  if (threadIdx.x < 32) {
+    const AttnTile t = attn_locate(S, blockIdx.x / S.Hq, JM, false, nullptr);
+    if (threadIdx.x == 0) tile = t;
+  }
+  __syncthreads();
+  const AttnTile t = tile;
+  const int rows = min(JM, t.nq - t.r0);
+  const long long step = (long long)S.B * S.Hq * S.Tq;
+  const int lane = threadIdx.x % (D / 4);
+  for (int r = threadIdx.x / (D / 4); r < rows; r += NTJ / (D / 4)) {
+    const long long tok = (long long)t.q0 + t.r0 + r, at = ((long long)t.b * S.Hq + h) * S.Tq + tok;
+    float2 st[kMaxSplits];
+    float M = -INFINITY;
+#pragma unroll
+    for (int s = 0; s < kMaxSplits; ++s)
+      if (s < T.splits) {
+        st[s] = T.stat[s * step + at];
+        if (st[s].y > 0.f) M = fmaxf(M, st[s].x);
+      }
+    float z = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int s = 0; s < kMaxSplits; ++s)
+      if (s < T.splits && st[s].y > 0.f) {  // a share without a visible key was not written
+        const float f = tc::ex2(st[s].x - M);
+        const float4 x = __ldcs(reinterpret_cast<const float4 *>(T.part + (s * step + at) * D) + lane);
+        z += f * st[s].y;
+        o.x += f * x.x;
+        o.y += f * x.y;
+        o.z += f * x.z;
+        o.w += f * x.w;
+      }
+    const float inv = z > 0.f ? 1.f / z : 0.f;
+    const __nv_bfloat162 a = __floats2bfloat162_rn(o.x * inv, o.y * inv), b = __floats2bfloat162_rn(o.z * inv, o.w * inv);
+    *reinterpret_cast<uint2 *>(T.O + t.b * S.o[0] + h * S.o[1] + tok * S.o[2] + 4 * lane) =
+        make_uint2(*reinterpret_cast<const uint32_t *>(&a), *reinterpret_cast<const uint32_t *>(&b));
+    if (T.A.lse && lane == 0) T.A.lse[at] = z > 0.f ? (M + log2f(z)) * 0.6931471805599453f : -INFINITY;
+  }
+}
+
+// Items per query tile.  `items` of about `tiles` key tiles each, split in s, take
+// ceil(items s / SMs) rounds of tiles / s + 2 steps on the SMs (a step is about 1.4 us, two are
+// what an item costs besides its tiles); the shares' fp32 sums are written and read again
+// by the join.  Splitting pays where items leave SMs idle (16 rows of 32 heads over 32768
+// keys, 16 items: 56 us against 352), not where it only evens out the last round: a chunk of
+// 2000 rows behind 30001 keys, 256 items, took 725 us in 4 shares and 663 whole.
+int choose_splits(long items, int tiles) {
+  const long sms = kNumSmsHint;
+  int best = 1;
+  double least = 0.;
+  for (int s = 1; s <= kMaxSplits && (s == 1 || s * 4 <= tiles); ++s) {
+    const double t = (double)((items * s + sms - 1) / sms) * ((double)tiles / s + 2.) + (s > 1 ? 3. + items * s / 60. : 0.);
+    if (s == 1 || t < (best == 1 ? 0.75 : 0.95) * least) {
+      best = s;
+      least = t;
+    }
+    if (s == 1 && items >= sms) break;
+  }
+  return best;
+}
+
+long tc_items(const AttnShape &S) {
+  const bool pair_rows = (S.Hq / S.Hkv) % 2;
+  return attn_tiles(S, pair_rows ? 2 * BM : BM) * (pair_rows ? S.Hq : S.Hq / 2);
+}
+
 // [B][H][T][d] with free strides as a 4-D map of boxes of 64 elements x 128 tokens.
 bool encode_heads(CUtensorMap *map, const void *base, int d, long T, long H, long B, const long long *st) {
   tc::EncodeTiledFn fn = tc::encode_tiled_fn();
@@ -627,11 +735,16 @@ int run(const void *Q, const void *K, const void *V, const TcArgs &T, cudaStream
   if (!encode_heads(&tmQ, Q, D, S.Tq, S.Hq, S.B, S.q) || !encode_heads(&tmK, K, D, S.Tk, S.Hkv, S.B, S.k) ||
       !encode_heads(&tmV, V, D, S.Tk, S.Hkv, S.B, S.v))
     return KV_ERR_CUDA;
-  const long ctas = attn_tiles(S, T.pair_rows ? 2 * BM : BM) * (T.pair_rows ? S.Hq : S.Hq / 2);
-  if (ctas > 0x7FFFFFFFL) return KV_ERR_UNSUPPORTED;
+  const long ctas = tc_items(S) * T.splits, joins = attn_tiles(S, JM) * S.Hq;
+  if (ctas > 0x7FFFFFFFL || joins > 0x7FFFFFFFL) return KV_ERR_UNSUPPORTED;
   if (ensure_smem((const void *)attn_tc_kernel<D>, Geo<D>::SMEM)) return KV_ERR_CUDA;
   const cudaError_t e = launch_pdl(attn_tc_kernel<D>, (unsigned)ctas, NT, Geo<D>::SMEM, st, tmQ, tmK, tmV, T);
   if (e != cudaSuccess) return cuda_failure(e, "prompt attention");
+  if (T.splits > 1) {
+    count_launches(1);
+    const cudaError_t f = launch_pdl(attn_join_kernel<D>, (unsigned)joins, NTJ, 0, st, T);
+    if (f != cudaSuccess) return cuda_failure(f, "prompt attention: joining the splits");
+  }
   return launch_status();
 }
 
@@ -642,10 +755,21 @@ bool attn_tc_eligible(const AttnShape &S, float scale, int dtype) {
   return dtype == KV_BF16 && S.Tk > 0 && scale > 0.f && std::isfinite(scale);
 }
 
-int launch_attn_prompt_tc(const void *Q, const void *K, const void *V, const AttnArgs &A, void *O, cudaStream_t st) {
+// Sizes alone decide (the lengths are on the device): Tk stands for every sequence's keys.
+int attn_tc_splits(const AttnShape &S) { return choose_splits(tc_items(S), (S.Tk + BN - 1) / BN); }
+
+size_t attn_tc_workspace_bytes(const AttnShape &S) {
+  const int n = attn_tc_splits(S);
+  return n > 1 ? (size_t)n * S.B * S.Hq * S.Tq * (S.d * sizeof(float) + sizeof(float2)) + 32 : 0;
+}
+
+int launch_attn_prompt_tc(const void *Q, const void *K, const void *V, const AttnArgs &A, void *O, void *ws,
+                          cudaStream_t st) {
   bool wide = (reinterpret_cast<uintptr_t>(O) & 31) == 0;
   for (int i = 0; i < 3; ++i) wide = wide && A.S.o[i] % 16 == 0;
-  TcArgs T{A, static_cast<__nv_bfloat16 *>(O), (A.S.Hq / A.S.Hkv) % 2, wide};
+  TcArgs T{A, static_cast<__nv_bfloat16 *>(O), (A.S.Hq / A.S.Hkv) % 2, wide, attn_tc_splits(A.S), nullptr, nullptr};
+  T.part = reinterpret_cast<float *>((reinterpret_cast<uintptr_t>(ws) + 31) & ~uintptr_t(31));  // 32-byte stores
+  T.stat = reinterpret_cast<float2 *>(T.part + (size_t)T.splits * A.S.B * A.S.Hq * A.S.Tq * A.S.d);
   return A.S.d == 128 ? run<128>(Q, K, V, T, st) : run<64>(Q, K, V, T, st);
 }
 

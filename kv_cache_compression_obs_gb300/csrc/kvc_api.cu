@@ -490,7 +490,7 @@ int kv_attn_prompt(const void *Q, const void *K, const void *V, int B, int Hq, i
   if (!Q || !O || !aligned16(Q) || !aligned16(O) || (Tk > 0 && (!K || !V)) || !aligned16(K) || !aligned16(V) ||
       !aligned4(lse_out) || !aligned4(seq_q) || !aligned4(seq_k))
     return KV_ERR_INVALID_ARG;
-  const size_t need = attn_prompt_workspace_bytes(B, Hq, Hkv, Tq, Tk, d, n_seq);
+  const size_t need = dtype == KV_BF16 ? attn_prompt_workspace_bytes(B, Hq, Hkv, Tq, Tk, d, n_seq) : 0;
   if (need && (!workspace || workspace_bytes < need || !aligned16(workspace))) return KV_ERR_WORKSPACE;
   return launch_attn_prompt(Q, K, V, S, scale, dtype, O, lse_out, workspace, dev_status,
                             static_cast<cudaStream_t>(stream));

@@ -64,6 +64,12 @@ DENSE = [
     (1, 1, 1, 513, 513, 128, BF),
     (1, 2, 2, 256, 256, 128, BF),
     (1, 2, 2, 384, 640, 64, BF),
+    # few rows, many keys: the keys in shares that are joined
+    (1, 4, 2, 130, 5000, 128, BF),
+    (1, 3, 1, 5, 3003, 64, BF),
+    (2, 8, 2, 1, 2500, 128, BF),
+    (1, 2, 1, 600, 1300, 128, BF),
+    (1, 1, 1, 700, 1200, 64, BF),
 ]
 
 
@@ -89,6 +95,8 @@ PACKED = [
     (4, 1, 128, BF, [1, 0, 0, 300, 129, 77, 0], [0, 0, 5, 0, 33, 200, 0]),
     (2, 1, 64, BF, [256, 255, 257, 2], [0, 1, 0, 400]),
     (1, 1, 128, BF, [3] * 40, [0] * 40),
+    (2, 1, 128, BF, [7, 0, 200, 1], [3000, 5, 0, 1100]),   # in shares, some of them without a key
+    (3, 1, 64, BF, [300, 2], [0, 4000]),
 ]
 
 
