@@ -530,6 +530,7 @@ KVC_API int kv_compact_q8(const void *K, const void *V, const float *s, const in
  *              for a step that may be taken back
  *   o_out      [B][Hq][d] float32
  *   workspace  >= kv_workspace_size(KV_OP_DECODE_Q8, B, Hq, Hkv, cap, d, 0, 0) bytes
+ *              (0 for caches short enough for the one-launch kernel)
  *   dev_status device int, may be NULL; KV_ERR_INVALID_ARG when a len is outside
  *              [0, cap - 1] (that unit is left untouched, its o and len_out too)
  * Preconditions: 1 <= Hq / Hkv <= 8, every position below the new one.

@@ -520,9 +520,8 @@ int h2o_decode_step_q8(const void *q, const void *k_new, const void *v_new, cons
   if (!q || !k_new || !v_new || !len_out || !o_out || !aligned16(q) || !aligned16(k_new) || !aligned16(v_new) ||
       !aligned4(o_out) || !aligned4(len_out) || !aligned4(row_pos) || !q8_pointers_ok(cache))
     return KV_ERR_INVALID_ARG;
-  if (!workspace || !aligned16(workspace) ||
-      workspace_bytes < decode_q8_workspace_bytes((long)cache->B * cache->Hkv, G, cache->cap, cache->d))
-    return KV_ERR_WORKSPACE;
+  const size_t need = decode_q8_workspace_bytes((long)cache->B * cache->Hkv, G, cache->cap, cache->d);
+  if (need && (!workspace || workspace_bytes < need || !aligned16(workspace))) return KV_ERR_WORKSPACE;
   return launch_decode_q8(q, k_new, v_new, *cache, Hq, new_pos, row_pos, len_out, scale, o_out, workspace,
                           dev_status, static_cast<cudaStream_t>(stream));
 }

@@ -31,6 +31,7 @@
 //   finalize -- combines the splits into o, turns the stored logits into
 //               probabilities and adds them to acc, and quantises the unfinished
 //               block when the new token fills it.
+#include <cooperative_groups.h>
 #include <cuda_fp16.h>
 
 #include <cmath>
@@ -57,7 +58,7 @@ struct DecArgs {
   const int32_t *row_pos;
   int32_t new_pos;
   int32_t *len_out;
-  int Hq, G, ns;
+  int Hq, G, ns, b_log2;
   float c_log2;      // scale log2(e)
   float *o;
   float *lgw;        // [units][cap + 1][G] logits
@@ -128,9 +129,9 @@ __device__ __forceinline__ int query_shift(float big) {
 // ---- the unfinished block's rows and the new token ------------------------------------
 // Rows 0 .. rows - 1 (the last one the new token) over the warps of one CTA: D / 16 lanes a
 // row, 16 elements each, all rows of a warp in flight at once.  Leaves each warp's maximum,
-// normaliser and output share where the stream's warps leave theirs.
+// normaliser and output share where the stream's warps leave theirs, and the rows' logits in lg.
 template <typename T, int D>
-__device__ void tail_part(const DecArgs &A, long u, int n, float *qs, float *wm, float *wz, float *so) {
+__device__ void tail_part(const DecArgs &A, long u, int n, float *lg, float *qs, float *wm, float *wz, float *so) {
   constexpr int LPR = D / 16, RPS = 32 / LPR, STEPS = 128 / (NW * RPS);
   const int G = A.G, block = A.c.block;
   const int nf = n / block * block, rows = n - nf + 1;  // at most block
@@ -174,7 +175,7 @@ __device__ void tail_part(const DecArgs &A, long u, int n, float *qs, float *wm,
         l[s][g] = row < rows ? t : -INFINITY;
         m[g] = fmaxf(m[g], l[s][g]);
         if (A.c.acc && sub == 0 && row < rows && gb + g < G)
-          A.lgw[(u * (long)(A.c.cap + 1) + nf + row) * G + gb + g] = t;
+          lg[row * G + gb + g] = t;
       }
     }
 #pragma unroll
@@ -226,11 +227,10 @@ __device__ void tail_part(const DecArgs &A, long u, int n, float *qs, float *wm,
   }
 }
 
-// The warps' shares (wm, wz, so) as split s of unit u.
+// The warps' shares (wm, wz, so) as one: po [G][D], pmz [G].
 template <int D>
-__device__ __forceinline__ void combine_warps(const DecArgs &A, long u, int s, const float *wm, const float *wz,
-                                              const float *so) {
-  const int G = A.G;
+__device__ __forceinline__ void combine_warps(int G, const float *wm, const float *wz, const float *so, float *po,
+                                              float2 *pmz) {
   __syncthreads();
   for (int i = threadIdx.x; i < G * D; i += NT) {
     const int qi = i / D;
@@ -244,44 +244,22 @@ __device__ __forceinline__ void combine_warps(const DecArgs &A, long u, int s, c
       v += f * so[w * G * D + i];
       Z += f * wz[w * 8 + qi];
     }
-    A.po[(u * (A.ns + 1) + s) * (long)G * D + i] = v;
-    if (i % D == 0) A.pmz[(u * (A.ns + 1) + s) * G + qi] = make_float2(M, Z);
+    po[i] = v;
+    if (i % D == 0) pmz[qi] = make_float2(M, Z);
   }
 }
 
 // ---- stream -----------------------------------------------------------------------------
+// Slots [k0, k1) (whole blocks) of unit u over the warps of one CTA; their logits to lg, each
+// warp's maximum, normaliser and output share to wm, wz and so.
 // NSET operands of four queries each; D head dim.
 template <typename T, int FMT, int D, int NSET>
-__global__ void __launch_bounds__(NT, NSET == 1 || D == 64 ? 4 : 3) q8_stream_kernel(const __grid_constant__ DecArgs A) {
+__device__ __forceinline__ void stream_range(const DecArgs &A, long u, int k0, int k1, float *lg, float *wm, float *wz,
+                                             float *so) {
   constexpr int VB = D / 8;       // V bytes per lane and slot
   constexpr int MT = D / 16;      // 16-row tiles of V^T
   constexpr int NCH = D / 64;     // 64-byte chunks of a K row
-  __shared__ __align__(16) float qs[8 * 128];
-  __shared__ float wm[NW * 8], wz[NW * 8];
-  extern __shared__ float so[];   // [NW][G][D]
-  pdl_wait();
-  pdl_launch();
-  const long u = blockIdx.x / (A.ns + 1);
-  const int s = blockIdx.x % (A.ns + 1);
-  const int G = A.G, block = A.c.block;
-  const int n = A.c.len[u];
-  if (n < 0 || n >= A.c.cap) {
-    if (s == A.ns && threadIdx.x == 0) {
-      A.nsave[u] = -1;
-      if (A.status) atomicExch(A.status, (int)KV_ERR_INVALID_ARG);
-    }
-    return;
-  }
-  if (s == A.ns) {
-    if (threadIdx.x == 0) A.nsave[u] = n;
-    tail_part<T, D>(A, u, n, qs, wm, wz, so);
-    combine_warps<D>(A, u, s, wm, wz, so);
-    return;
-  }
-  const int nf = n / block * block;
-  const int per = split_len(nf, A.ns);
-  const int k0 = s * per, k1 = min(nf, k0 + per);
-  if (k0 >= k1) return;
+  const int G = A.G, bl = A.b_log2;
   const uint8_t *kc = static_cast<const uint8_t *>(A.c.K) + u * (long)A.c.cap * D;
   const uint8_t *vc = static_cast<const uint8_t *>(A.c.V) + u * (long)A.c.cap * D;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -365,12 +343,11 @@ __global__ void __launch_bounds__(NT, NSET == 1 || D == 64 ? 4 : 3) q8_stream_ke
       for (int j = 0; j < 4; ++j) o[st][i][j] = 0.f;
   }
   int rv = kMinExp;  // o stands for o 2^(rv - kPScale)
-  const float *ks = A.c.Ks + u * (long)(A.c.cap / block), *vs = A.c.Vs + u * (long)(A.c.cap / block);
-  float *lg = A.lgw + u * (long)(A.c.cap + 1) * G;
+  const float *ks = A.c.Ks + u * (long)(A.c.cap >> bl), *vs = A.c.Vs + u * (long)(A.c.cap >> bl);
 
   for (int j = first; j < k1; j += NW * 16) {
     const int next = j + NW * 16;
-    const float ak = ks[j / block], av = vs[j / block];
+    const float ak = ks[j >> bl], av = vs[j >> bl];
 
     float sc[NSET][4];
 #pragma unroll
@@ -402,8 +379,8 @@ __global__ void __launch_bounds__(NT, NSET == 1 || D == 64 ? 4 : 3) q8_stream_ke
       l1[st] = (sc[st][2] + sc[st][3]) * f;
       const int qi = st * 4 + t;
       if (A.c.acc && qi < G) {
-        lg[(long)(j + g) * G + qi] = l0[st];
-        lg[(long)(j + g + 8) * G + qi] = l1[st];
+        lg[(long)(j - k0 + g) * G + qi] = l0[st];
+        lg[(long)(j - k0 + g + 8) * G + qi] = l1[st];
       }
       over |= fmaxf(l0[st], l1[st]) > m[st] + kLazy;
     }
@@ -478,7 +455,168 @@ __global__ void __launch_bounds__(NT, NSET == 1 || D == 64 ? 4 : 3) q8_stream_ke
       }
     }
   }
-  combine_warps<D>(A, u, s, wm, wz, so);
+}
+
+template <typename T, int FMT, int D, int NSET>
+__global__ void __launch_bounds__(NT, NSET == 1 || D == 64 ? 4 : 3) q8_stream_kernel(const __grid_constant__ DecArgs A) {
+  __shared__ __align__(16) float qs[8 * 128];
+  __shared__ float wm[NW * 8], wz[NW * 8];
+  extern __shared__ float so[];   // [NW][G][D]
+  pdl_wait();
+  pdl_launch();
+  const long u = blockIdx.x / (A.ns + 1);
+  const int s = blockIdx.x % (A.ns + 1);
+  const int n = A.c.len[u];
+  if (n < 0 || n >= A.c.cap) {
+    if (s == A.ns && threadIdx.x == 0) {
+      A.nsave[u] = -1;
+      if (A.status) atomicExch(A.status, (int)KV_ERR_INVALID_ARG);
+    }
+    return;
+  }
+  const int nf = n >> A.b_log2 << A.b_log2;
+  const long at = u * (A.ns + 1) + s;
+  float *lg = A.lgw + u * (long)(A.c.cap + 1) * A.G;
+  if (s == A.ns) {
+    if (threadIdx.x == 0) A.nsave[u] = n;
+    tail_part<T, D>(A, u, n, lg + (long)nf * A.G, qs, wm, wz, so);
+  } else {
+    const int per = split_len(nf, A.ns);
+    const int k0 = s * per, k1 = min(nf, k0 + per);
+    if (k0 >= k1) return;
+    stream_range<T, FMT, D, NSET>(A, u, k0, k1, lg + (long)k0 * A.G, wm, wz, so);
+  }
+  combine_warps<D>(A.G, wm, wz, so, A.po + at * A.G * D, A.pmz + at * A.G);
+}
+
+// ---- quantising the block that the new token fills -------------------------------------------
+template <typename T, int FMT>
+__device__ __forceinline__ void quantise_tail(const DecArgs &A, long u, int n, int kv, float *red) {
+  const int D = A.c.d, block = A.c.block, nf = n >> A.b_log2 << A.b_log2;
+  const T *rows = static_cast<const T *>(kv ? A.c.Vt : A.c.Kt) + u * (long)block * D;
+  // the new token's row as it came in: its copy in the cache may be this kernel's own
+  const T *fresh = static_cast<const T *>(kv ? A.v_new : A.k_new) + u * (long)D;
+  uint4 *to = reinterpret_cast<uint4 *>(static_cast<uint8_t *>(kv ? A.c.V : A.c.K) + (u * (long)A.c.cap + nf) * D);
+  const int pieces = block * D / 16, old = (block - 1) * D / 16;
+  auto load = [&](int i, float (&x)[16]) { load16(i < old ? rows + (long)i * 16 : fresh + (i - old) * 16, x); };
+  float big = 0.f;
+  for (int i = threadIdx.x; i < pieces; i += blockDim.x) {
+    float x[16];
+    load(i, x);
+    big = fmaxf(big, max_abs16(x));
+  }
+  const float a = q8_scale<FMT>(block_max(big, red));
+  const float inv = __fdiv_rn(1.f, a);
+  for (int i = threadIdx.x; i < pieces; i += blockDim.x) {
+    float x[16];
+    load(i, x);
+    to[i] = q8_pack16<FMT>(x, inv);
+  }
+  if (threadIdx.x == 0) (kv ? A.c.Vs : A.c.Ks)[(u * (long)A.c.cap + nf) >> A.b_log2] = a;
+  __syncthreads();  // red is used again
+}
+
+// ---- short caches: one launch ------------------------------------------------------------------
+// A cluster of CTAs per unit, each with a range of its slots, whose logits stay in shared memory;
+// maxima, normalisers and output shares are exchanged through distributed shared memory, then
+// every CTA adds its own slots' probabilities to acc.  The last CTA takes the unfinished block
+// and the new token, and slots as well where the ranges are long.
+template <typename T, int FMT, int D, int NSET>
+__global__ void __launch_bounds__(NT, NSET == 1 || D == 64 ? 4 : 3)
+    q8_cluster_kernel(const __grid_constant__ DecArgs A, int slots) {
+  __shared__ __align__(16) float qs[8 * 128];
+  __shared__ float wm[NW * 8], wz[NW * 8];
+  __shared__ float2 mz[2][8];       // this CTA's shares: slots, unfinished block
+  __shared__ float2 all[9][8];      // everybody's
+  __shared__ float sM[8], sI[8];
+  __shared__ float red[32];
+  extern __shared__ __align__(16) float dyn[];
+  const int G = A.G;
+  float *so = dyn;                  // [NW][G][D]
+  float *sh = so + NW * G * D;      // [2][G][D] shares
+  float *lg = sh + 2 * G * D;       // [slots][G], then [128][G] of the unfinished block
+  float *lgt = lg + (long)slots * G;
+  pdl_wait();
+  pdl_launch();
+  cooperative_groups::cluster_group cl = cooperative_groups::this_cluster();
+  const int CL = (int)cl.num_blocks(), rank = (int)cl.block_rank();
+  const long u = blockIdx.x / CL;
+  const int n = A.c.len[u];
+  if (n < 0 || n >= A.c.cap) {  // every CTA of the cluster alike
+    if (rank == 0 && threadIdx.x == 0 && A.status) atomicExch(A.status, (int)KV_ERR_INVALID_ARG);
+    return;
+  }
+  const int nf = n >> A.b_log2 << A.b_log2;
+  const bool tail = rank == CL - 1;
+  const int mr = CL > 1 && nf <= (CL - 1) * 256 ? CL - 1 : CL;  // CTAs with slots
+  const int per = split_len(nf, mr);
+  const int k0 = min(nf, rank * per), k1 = rank < mr ? min(nf, k0 + per) : k0;
+  if (k0 < k1) {
+    stream_range<T, FMT, D, NSET>(A, u, k0, k1, lg, wm, wz, so);
+    combine_warps<D>(G, wm, wz, so, sh, mz[0]);
+  } else if ((int)threadIdx.x < 8) {
+    mz[0][threadIdx.x] = make_float2(-INFINITY, 0.f);
+  }
+  if (tail) {
+    __syncthreads();
+    tail_part<T, D>(A, u, n, lgt, qs, wm, wz, so);
+    combine_warps<D>(G, wm, wz, so, sh + G * D, mz[1]);
+  }
+  // the slots' accumulators are on their way while the others finish
+  float *acc = A.c.acc ? A.c.acc + u * (long)A.c.cap : nullptr;
+  constexpr int AP = 8;
+  float old[AP];
+  if (acc) {
+#pragma unroll
+    for (int k = 0; k < AP; ++k) {
+      const int j = k0 + k * NT + (int)threadIdx.x;
+      old[k] = j < k1 ? acc[j] : 0.f;
+    }
+  }
+  cl.sync();
+  const int shares = mr + 1;  // CTAs with slots, then the unfinished block
+  for (int i = threadIdx.x; i < shares * G; i += NT) {
+    const int s = i / G, q = i - s * G;
+    all[s][q] = s < mr ? cl.map_shared_rank(&mz[0][0], s)[q] : cl.map_shared_rank(&mz[1][0], CL - 1)[q];
+  }
+  __syncthreads();
+  if ((int)threadIdx.x < G) {
+    float M = -INFINITY, Z = 0.f;
+    for (int s = 0; s < shares; ++s) M = fmaxf(M, all[s][threadIdx.x].x);
+    for (int s = 0; s < shares; ++s) Z += all[s][threadIdx.x].y * tc::ex2(all[s][threadIdx.x].x - M);
+    sM[threadIdx.x] = M;
+    sI[threadIdx.x] = 1.f / Z;
+  }
+  __syncthreads();
+  for (int i = rank * NT + threadIdx.x; i < G * D; i += CL * NT) {
+    const int q = i / D;
+    float v = 0.f;
+    for (int s = 0; s < shares; ++s) {
+      const float f = tc::ex2(all[s][q].x - sM[q]);
+      if (f == 0.f) continue;  // a CTA without slots has no share
+      v += f * (s < mr ? cl.map_shared_rank(sh, s)[i] : cl.map_shared_rank(sh, CL - 1)[G * D + i]);
+    }
+    A.o[u * (long)G * D + i] = v * sI[q];
+  }
+  if (acc) {
+    auto mass = [&](const float *l) {
+      float p = 0.f;
+      for (int q = 0; q < G; ++q) p += tc::ex2(l[q] - sM[q]) * sI[q];
+      return p;
+    };
+#pragma unroll
+    for (int k = 0; k < AP; ++k) {
+      const int j = k0 + k * NT + (int)threadIdx.x;
+      if (j < k1) acc[j] = old[k] + mass(lg + (j - k0) * G);
+    }
+    for (int j = k0 + AP * NT + threadIdx.x; j < k1; j += NT) acc[j] += mass(lg + (j - k0) * G);
+    if (tail)
+      for (int j = nf + threadIdx.x; j <= n; j += NT) acc[j] = (j < n ? acc[j] : 0.f) + mass(lgt + (j - nf) * G);
+  }
+  if (rank == 0 && threadIdx.x == 0) A.len_out[u] = n + 1;  // every CTA has read len
+  if (((n + 1) & (A.c.block - 1)) == 0)
+    for (int kv = rank; kv < 2; kv += CL) quantise_tail<T, FMT>(A, u, n, kv, red);
+  cl.sync();  // nobody leaves while its shares are read
 }
 
 // ---- finalize -----------------------------------------------------------------------------
@@ -619,26 +757,7 @@ __global__ void __launch_bounds__(NTF) q8_finalize_kernel(const __grid_constant_
   }
   if (e == 0 && threadIdx.x == 0) A.len_out[u] = n + 1;
   if (!fills) return;
-  for (int kv = e; kv < 2; kv += chunks) {  // the new token filled its block: codes for K and V
-    const T *rows = static_cast<const T *>(kv ? A.c.Vt : A.c.Kt) + u * (long)block * D;
-    uint4 *to = reinterpret_cast<uint4 *>(static_cast<uint8_t *>(kv ? A.c.V : A.c.K) + (u * (long)cap + nf) * D);
-    const int pieces = block * D / 16;
-    float big = 0.f;
-    for (int i = threadIdx.x; i < pieces; i += NTF) {
-      float x[16];
-      load16(rows + (long)i * 16, x);
-      big = fmaxf(big, max_abs16(x));
-    }
-    const float a = q8_scale<FMT>(block_max(big, red));
-    const float inv = __fdiv_rn(1.f, a);
-    for (int i = threadIdx.x; i < pieces; i += NTF) {
-      float x[16];
-      load16(rows + (long)i * 16, x);
-      to[i] = q8_pack16<FMT>(x, inv);
-    }
-    if (threadIdx.x == 0) (kv ? A.c.Vs : A.c.Ks)[u * (long)(cap / block) + nf / block] = a;
-    __syncthreads();  // red is used again
-  }
+  for (int kv = e; kv < 2; kv += chunks) quantise_tail<T, FMT>(A, u, n, kv, red);
 }
 
 size_t al(size_t x) { return (x + 255) & ~(size_t)255; }
@@ -647,14 +766,37 @@ size_t al(size_t x) { return (x + 255) & ~(size_t)255; }
 // different lengths even out; at least one tile a warp, and no more splits than the finalize
 // kernel holds factors for.
 int splits(long units, int cap) {
-  const long want = (24L * kNumSmsHint + units - 1) / (units > 0 ? units : 1);
+  const long want = (16L * kNumSmsHint + units - 1) / (units > 0 ? units : 1);
   const long most = (cap + 16 * NW - 1) / (16 * NW);
   const long ns = want < most ? want : most;
   return (int)(ns < 1 ? 1 : ns > kMaxSplits ? kMaxSplits : ns);
 }
 
+// The one-launch kernel where its CTAs all run at once and hold short ranges: CTAs per unit (0:
+// not), slots of a CTA.  One KV group of 8 with 1638 slots 11.0 us (two launches: 12.3), 64 units
+// of up to 8192 slots 32.7 us (34.0); but 256 units of up to 8192 slots 84 us (66), where CTAs
+// that wait for the rest of their cluster leave the memory idle.
+int cluster_plan(long units, int G, int cap, int *slots) {
+  const long room = 4L * kNumSmsHint;
+  int cl = 1;
+  while (cl < 8 && (cl + 1) * units <= room) cl *= 2;
+  if (cl > 8) cl = 8;
+  *slots = ((cap + cl - 1) / cl + 127) & ~63;  // split_len over one CTA less, or over all
+  if (cl > 1 && *slots < 256) *slots = 256;
+  return *slots <= 1088 && (long)*slots * G * 4 <= 36 * 1024 && units * cl <= room ? cl : 0;
+}
+
 template <typename T, int FMT, int D, int NSET>
 int run(const DecArgs &A, long units, cudaStream_t st) {
+  int slots;
+  if (const int cl = cluster_plan(units, A.G, A.c.cap, &slots)) {
+    const size_t bytes = ((size_t)(NW + 2) * A.G * D + (size_t)(slots + 128) * A.G) * sizeof(float);
+    if (ensure_smem((const void *)q8_cluster_kernel<T, FMT, D, NSET>, bytes)) return KV_ERR_CUDA;
+    const cudaError_t e = launch_pdl_cluster(q8_cluster_kernel<T, FMT, D, NSET>, (unsigned)(units * cl), NT, bytes, st,
+                                             cl, A, slots);
+    if (e != cudaSuccess) return cuda_failure(e, "8-bit decode: cluster kernel");
+    return launch_status();
+  }
   const size_t smem = (size_t)NW * A.G * D * sizeof(float);
   if (ensure_smem((const void *)q8_stream_kernel<T, FMT, D, NSET>, smem)) return KV_ERR_CUDA;
   const long ctas = units * (A.ns + 1);
@@ -682,6 +824,8 @@ int run_d(const DecArgs &A, long units, cudaStream_t st) {
 }  // namespace
 
 size_t decode_q8_workspace_bytes(long units, int G, int cap, int d) {
+  int slots;
+  if (units == 0 || cluster_plan(units, G, cap, &slots)) return 0;
   const int ns = splits(units, cap);
   return al((size_t)units * (cap + 1) * G * 4) + al((size_t)units * (ns + 1) * G * 8) +
          al((size_t)units * (ns + 1) * G * d * 4) + al((size_t)units * 4);
@@ -702,6 +846,7 @@ int launch_decode_q8(const void *q, const void *k_new, const void *v_new, const 
   A.Hq = Hq;
   A.G = Hq / c.Hkv;
   A.ns = splits(units, c.cap);
+  A.b_log2 = c.block == 128 ? 7 : c.block == 64 ? 6 : 5;
   A.c_log2 = scale * 1.4426950408889634f;
   A.o = o;
   A.status = status;

@@ -67,10 +67,12 @@ def test_decode_refusals(api):
     assert call(q=None) == -1
     assert call(q=P16 + 8) == -1
     assert call(ln=None) == -1
-    assert call(ws=None) == -5
-    assert call(nbytes=100) == -5
+    assert call(ws=None, cap=1 << 17) == -5    # short caches need none
+    assert call(nbytes=100, cap=1 << 17) == -5
+    assert call(ws=P16 + 8, cap=1 << 17) == -5
     assert call(B=0) == 0
-    assert lib.kv_workspace_size(8, 2, 8, 2, 128, 64, 0, 0) > 0
+    assert lib.kv_workspace_size(8, 2, 8, 2, 1 << 17, 64, 0, 0) > 0
+    assert lib.kv_workspace_size(8, 2, 8, 2, 128, 64, 0, 0) == 0
     assert lib.kv_workspace_size(8, 2, 7, 2, 128, 64, 0, 0) == 0
 
 

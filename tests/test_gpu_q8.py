@@ -116,6 +116,12 @@ DECODE = [
     (2, 1, 3, 4096, 128, 64, BF, "s8", [4095, 1]),
     (1, 2, 7, 320, 128, 64, BF, "s8", [256, 319]),
     (1, 1, 6, 5120, 64, 128, F32, "s8", [5000]),
+    # past the one-launch kernel's caches
+    (1, 2, 8, 16384, 64, 64, BF, "s8", [16000, 130]),
+    (1, 3, 4, 20480, 128, 64, BF, "e4m3", [20479, 9000, 0]),
+    (1, 2, 1, 65536, 64, 128, BF, "s8", [65535, 40001]),
+    (1, 2, 3, 24576, 128, 32, F32, "s8", [24000, 31]),
+    (1, 2, 2, 32768, 128, 64, BF, "e4m3", [32703, 20000]),
 ]
 
 
