@@ -540,24 +540,27 @@ def q8_cache(B: int, Hkv: int, cap: int, d: int, block: int = 64, dtype=torch.bf
 _F32, _I32 = torch.float32, torch.int32
 
 
-def _q8(c, dev: int | None = None) -> _Q8Cache:
+def _q8(c, dev: int) -> _Q8Cache:
+    """The cache's tensors, checked, as the library takes them."""
     K, V, Ks, Vs, Kt, Vt = c["K"], c["V"], c["Ks"], c["Vs"], c["Kt"], c["Vt"]
     pos, acc, ln = c["pos"], c.get("acc"), c["len"]
-    shape, tail, fmt = K.shape, Kt.shape, _Q8_CODES.get(K.dtype)
+    shape, tail, dk, dt = K.shape, Kt.shape, K.dtype, Kt.dtype
+    fmt = _Q8_CODES.get(dk)
     if len(shape) != 4 or len(tail) != 4 or fmt is None or tail[2] == 0:
         raise ValueError("not an 8-bit slot cache: see q8_cache")
     B, H, cap, d = shape
     block = tail[2]
-    units, blocks, slots = (B, H), (B, H, cap // block), (B, H, cap)
+    blocks, slots = (B, H, cap // block), (B, H, cap)
     if V.shape != shape or tail != (B, H, block, d) or Vt.shape != tail or Ks.shape != blocks or Vs.shape != blocks \
-            or pos.shape != slots or ln.shape != units or (acc is not None and acc.shape != slots):
+            or pos.shape != slots or ln.shape != (B, H) or (acc is not None and acc.shape != slots):
         raise ValueError("8-bit slot cache: shapes disagree, see q8_cache")
-    if V.dtype != K.dtype or Vt.dtype != Kt.dtype or Ks.dtype != _F32 or Vs.dtype != _F32 or pos.dtype != _I32 \
+    if V.dtype != dk or Vt.dtype != dt or Ks.dtype != _F32 or Vs.dtype != _F32 or pos.dtype != _I32 \
             or ln.dtype != _I32 or (acc is not None and acc.dtype != _F32):
         raise ValueError("8-bit slot cache: dtypes disagree, see q8_cache")
-    _on(_device_of(K) if dev is None else dev, K, V, Ks, Vs, Kt, Vt, pos, acc, ln)
+    _on(dev, K, V, Ks, Vs, Kt, Vt, pos, acc, ln)
     return _Q8Cache(K.data_ptr(), V.data_ptr(), Ks.data_ptr(), Vs.data_ptr(), Kt.data_ptr(), Vt.data_ptr(),
-                    pos.data_ptr(), _at(acc), ln.data_ptr(), B, H, cap, d, block, _dtype_code(Kt), fmt)
+                    pos.data_ptr(), None if acc is None else acc.data_ptr(), ln.data_ptr(), B, H, cap, d, block,
+                    _dtype_code(Kt), fmt)
 
 
 def kv_compact_q8(K: torch.Tensor, V: torch.Tensor, s, idx, cache, dev_status=None, stream=None):
@@ -605,7 +608,7 @@ def h2o_decode_step_q8(q, k_new, v_new, cache, new_pos, scale: float | None = No
         raise ValueError("len_out must be [B][Hkv] int32")
     need = _workspace_bytes(KV_OP_DECODE_Q8, B, Hq, c.Hkv, c.cap, d)
     with _side(stream):
-        o = o_out if o_out is not None else q.new_empty((B, Hq, d), dtype=_F32)
+        o = o_out if o_out is not None else torch.empty((B, Hq, d), dtype=_F32, device=q.device)
         ws, nbytes = _workspace(need, q.device, workspace)
     if o_out is not None and (o.shape != (B, Hq, d) or o.dtype != _F32):
         raise ValueError("o_out must be [B][Hq][d] float32")

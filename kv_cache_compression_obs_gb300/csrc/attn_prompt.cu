@@ -1,16 +1,27 @@
 // attn_prompt.cu -- causal attention of a prompt, grouped heads, packed sequences
-// (KV-cache survey blog §1.1: softmax(Q K^T / sqrt(d)) V): the CUDA-core kernel.
+// (KV-cache survey blog §1.1: softmax(Q K^T / sqrt(d)) V): fp32, and bf16 calls that the
+// tcgen05 kernel (attn_prompt_tc.cu) does not take.
 //
-// One CTA per (query tile of BM rows, query head) walks the sequence's keys in tiles
-// of 64 with a running row maximum m and sum z:
 //     m' = max(m, max_j l_j), z' = z 2^(m - m') + sum_j 2^(l_j - m'), O likewise,
-// l in log2 units, so that 2^l is one instruction.  256 threads as 16 x 16: thread
-// (ty, tx) holds rows ty RT .. ty RT + RT - 1 against keys tx + 16 i, and of O the
-// columns 4 tx .. 4 tx + 3 (+ 64).  All arithmetic is fp32.
-// fp32 tiles come by asynchronous copies, K and V double buffered, so that a short prompt
-// (one CTA an SM, nothing else to run meanwhile) does not wait for memory in every tile:
-// 4 heads of 512 tokens 13 us against 36 us with one buffer that K and V take turns in,
-// which bf16 (converted on the way; the tensor cores take all but odd scales) keeps.
+// over key tiles of BN, l in log2 units, so that 2^l is one instruction.
+//
+// The products keep fp32 accuracy on the tensor cores: every operand x is hi + lo, hi = x
+// rounded to tf32 (11 significant bits) and lo the exact rest, and a product is
+// hi hi + hi lo + lo hi in mma.m16n8k8 with fp32 sums; lo lo, below 2^-22 of the product,
+// and lo's own bits past its 11 are dropped.  On the CUDA cores the same tiles were bound by
+// shared memory: a 16-byte load takes four cycles whatever it shares, and a thread's few
+// results do not pay for its operands (4 heads of 512 tokens
+// 26.7 us; here 11.8 us, and 59 TFLOP/s over 4096 tokens of 32/8 heads).
+//
+// A warp holds 16 query rows.  Which element of d (or which key) stands at which k is free as
+// long as both operands agree: a lane takes 16 consecutive bytes of a K row for two k steps,
+// the weights of keys 2t and 2t + 1, which it holds after the first product, are columns t
+// and t + 4 of the second's operand, and 16 consecutive bytes of V rows 2t and 2t + 1 serve
+// four of its n tiles.  Row strides of D + 16 and D + 4 words make both reads free of bank
+// conflicts.  K and V tiles come by asynchronous copies (bf16: converted on the way).
+//   SPLIT 0: four warps, 64 rows, share the tiles, double buffered.
+//   SPLIT 1: all warps have the same 16 rows and every NW-th tile each, in buffers of their
+//            own, and are joined at the end: where 64-row tiles would leave SMs idle.
 #include <cmath>
 
 #include "attn_common.cuh"
@@ -19,32 +30,60 @@
 namespace kvc {
 namespace {
 
-constexpr int NT = 256;
-constexpr int BN = 64;
+constexpr int BN = 32;
 
-template <typename T, int D, int RT>
+template <int D, int SPLIT>
 struct Geo {
-  static constexpr int BM = 16 * RT;
-  static constexpr int LD = D + 4;   // padded row of the Q and K/V buffers
-  static constexpr int LP = BN + 4;  // padded row of P
-  static constexpr bool ASYNC = sizeof(T) == 4;
-  static constexpr int SMEM = (BM * LD + (ASYNC ? 4 : 1) * BN * LD + BM * LP) * 4;
+  static constexpr int NW = SPLIT ? (D == 64 ? 8 : 4) : 4;  // warps
+  static constexpr int BM = SPLIT ? 16 : 64;
+  static constexpr int LK = D + 16, LV = D + 4;    // padded rows, in floats
+  static constexpr int TILE = BN * (LK + LV);      // a K and a V tile
+  static constexpr int BUFS = SPLIT ? NW : 2;
+  static constexpr int SMEM = (BM * LK + BUFS * TILE) * 4;
 };
 
-template <typename T, int D, int RT>
-__global__ void __launch_bounds__(NT) attn_kernel(const T *__restrict__ Q, const T *__restrict__ K,
-                                                  const T *__restrict__ V, T *__restrict__ O,
-                                                  const __grid_constant__ AttnArgs A) {
-  using Gm = Geo<T, D, RT>;
-  constexpr int BM = Gm::BM, LD = Gm::LD, LP = Gm::LP, NV = D / 64, EV = Vec16<T>::N;
+__device__ __forceinline__ uint32_t tf32_hi(float x) {
+  uint32_t r;
+  asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(r) : "f"(x));
+  return r;
+}
+struct Split {
+  uint32_t hi, lo;
+  __device__ __forceinline__ void set(float x) {
+    hi = tf32_hi(x);
+    lo = __float_as_uint(x - __uint_as_float(hi));
+  }
+};
+__device__ __forceinline__ void mma1688(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// c += a b to fp32 accuracy
+__device__ __forceinline__ void mma_split(float (&c)[4], const Split (&a)[4], const Split &b0, const Split &b1) {
+  mma1688(c, a[0].lo, a[1].lo, a[2].lo, a[3].lo, b0.hi, b1.hi);
+  mma1688(c, a[0].hi, a[1].hi, a[2].hi, a[3].hi, b0.lo, b1.lo);
+  mma1688(c, a[0].hi, a[1].hi, a[2].hi, a[3].hi, b0.hi, b1.hi);
+}
+
+template <typename T, int D, int SPLIT>
+__global__ void __launch_bounds__(32 * Geo<D, SPLIT>::NW) attn_kernel(const T *__restrict__ Q, const T *__restrict__ K,
+                                                                      const T *__restrict__ V, T *__restrict__ O,
+                                                                      const __grid_constant__ AttnArgs A) {
+  using Gm = Geo<D, SPLIT>;
+  constexpr int NW = Gm::NW, NT = 32 * NW, BM = Gm::BM, LK = Gm::LK, LV = Gm::LV, EV = Vec16<T>::N;
+  constexpr int NO = D / 8;  // n tiles of O
   extern __shared__ __align__(16) float sh[];
-  float *sQ = sh, *sP = sQ + BM * LD, *sX = sP + BM * LP;  // sX: K, or K K V V in turns of two
+  float *sQ = sh, *sX = sh + BM * LK;
   __shared__ AttnTile st;
   const AttnShape &S = A.S;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t4 = lane & 3;
   const int h = blockIdx.x % S.Hq;
-  const int index = blockIdx.x / S.Hq;
   if (threadIdx.x < 32) {
-    const AttnTile t = attn_locate(S, index, BM, blockIdx.x == 0, A.status);
+    const AttnTile t = attn_locate(S, blockIdx.x / S.Hq, BM, blockIdx.x == 0, A.status);
     if (threadIdx.x == 0) st = t;
   }
   __syncthreads();
@@ -55,189 +94,256 @@ __global__ void __launch_bounds__(NT) attn_kernel(const T *__restrict__ Q, const
   const T *k = K + t.b * S.k[0] + hk * S.k[1] + (long long)t.k0 * S.k[2];
   const T *v = V + t.b * S.v[0] + hk * S.v[1] + (long long)t.k0 * S.v[2];
   const int rows = min(BM, t.nq - t.r0);
-  const int off = t.nk - t.nq + t.r0;                 // row i of the tile sees keys <= off + i
-  const int kend = min(t.nk, off + rows);             // keys that some row sees
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+  const int off = t.nk - t.nq + t.r0;      // row i of the tile sees keys <= off + i
+  const int kend = min(t.nk, off + rows);  // keys that some row sees
+  const int ntile = kend > 0 ? (kend + BN - 1) / BN : 0;
 
-  for (int e = threadIdx.x; e < BM * (D / EV); e += NT) {
-    const int r = e / (D / EV), c = (e % (D / EV)) * EV;
-    float x[EV];
-    if (r < rows) {
-      Vec16<T>::unpack(__ldg(reinterpret_cast<const uint4 *>(q + r * S.q[2] + c)), x);
-    } else {
-#pragma unroll
-      for (int i = 0; i < EV; ++i) x[i] = 0.f;
-    }
-#pragma unroll
-    for (int i = 0; i < EV; ++i) sQ[r * LD + c + i] = x[i] * A.c_log2;
-  }
-  auto load_tile = [&](const T *p, long long stride, int j0) {  // rows behind the last key become 0
-    for (int e = threadIdx.x; e < BN * (D / EV); e += NT) {
+  // Rows [0, n) of a tile with ld floats each; rows behind `have` become 0.  first / step: this
+  // thread's part of the copying threads.
+  auto copy_rows = [&](float *dst, int ld, const T *p, long long stride, int n, int have, int first, int step) {
+    for (int e = first; e < n * (D / EV); e += step) {
       const int r = e / (D / EV), c = (e % (D / EV)) * EV;
-      float x[EV];
-      if (j0 + r < kend) {
-        Vec16<T>::unpack(__ldg(reinterpret_cast<const uint4 *>(p + (j0 + r) * stride + c)), x);
+      if constexpr (sizeof(T) == 4) {
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(tc::smem_u32(dst + r * ld + c)),
+                     "l"(p + (r < have ? r * stride : 0) + c), "r"(r < have ? 16 : 0)
+                     : "memory");
       } else {
+        float x[EV];
 #pragma unroll
         for (int i = 0; i < EV; ++i) x[i] = 0.f;
-      }
+        if (r < have) Vec16<T>::unpack(__ldg(reinterpret_cast<const uint4 *>(p + r * stride + c)), x);
 #pragma unroll
-      for (int i = 0; i < EV; i += 4)
-        *reinterpret_cast<float4 *>(sX + r * LD + c + i) = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
+        for (int i = 0; i < EV; i += 4)
+          *reinterpret_cast<float4 *>(dst + r * ld + c + i) = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
+      }
     }
   };
-  auto copy_tile = [&](float *dst, const T *p, long long stride, int j0) {  // the same, asynchronously
-    if (j0 < kend)
-      for (int e = threadIdx.x; e < BN * (D / 4); e += NT) {
-        const int r = e / (D / 4), c = (e % (D / 4)) * 4;
-        const bool have = j0 + r < kend;
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(tc::smem_u32(dst + r * LD + c)),
-                     "l"(p + (have ? (j0 + r) * stride : 0) + c), "r"(have ? 16 : 0)
-                     : "memory");
-      }
+  auto fetch = [&](int j, float *buf, int first, int step) {  // tile j's K and V, one copy group
+    if (j < ntile) {
+      copy_rows(buf, LK, k + (long long)j * BN * S.k[2], S.k[2], BN, kend - j * BN, first, step);
+      copy_rows(buf + BN * LK, LV, v + (long long)j * BN * S.v[2], S.v[2], BN, kend - j * BN, first, step);
+    }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
-  float m[RT], z[RT], o[RT][NV][4];
+  copy_rows(sQ, LK, q, S.q[2], BM, rows, threadIdx.x, NT);  // joins the first tile's group
+  if (SPLIT) fetch(warp, sX + warp * Gm::TILE, lane, 32);
+  else fetch(0, sX, threadIdx.x, NT);
+
+  const int r0 = SPLIT ? 0 : warp * 16;                    // this warp's rows of the tile
+  const float *mq = sQ + r0 * LK;
+  // last keys that rows g and g + 8 of the warp see
+  const int lim0 = min(kend - 1, off + r0 + g), lim1 = min(kend - 1, off + r0 + g + 8);
+  const int wend = SPLIT ? kend : min(t.nk, off + min(rows, r0 + 16));  // keys that some row of the warp sees
+  float m0 = -INFINITY, m1 = -INFINITY, z0 = 0.f, z1 = 0.f, o[NO][4];
 #pragma unroll
-  for (int i = 0; i < RT; ++i) {
-    m[i] = -INFINITY;
-    z[i] = 0.f;
+  for (int i = 0; i < NO; ++i)
 #pragma unroll
-    for (int c = 0; c < NV; ++c)
-#pragma unroll
-      for (int x = 0; x < 4; ++x) o[i][c][x] = 0.f;
+    for (int x = 0; x < 4; ++x) o[i][x] = 0.f;
+  if (SPLIT) {  // Q is everyone's
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    __syncthreads();
   }
-  if constexpr (Gm::ASYNC) {
-    copy_tile(sX, k, S.k[2], 0);
-    copy_tile(sX + 2 * BN * LD, v, S.v[2], 0);
-  }
-  int buf = 0;
-  for (int j0 = 0; j0 < kend; j0 += BN, buf ^= 1) {
-    const float *sK = sX, *sV = sX;
-    if constexpr (Gm::ASYNC) {
-      asm volatile("cp.async.wait_group 1;" ::: "memory");  // K
-      __syncthreads();  // everyone's pieces, and the other buffers have been read
-      copy_tile(sX + (buf ^ 1) * BN * LD, k, S.k[2], j0 + BN);
-      copy_tile(sX + (2 + (buf ^ 1)) * BN * LD, v, S.v[2], j0 + BN);
-      sK = sX + buf * BN * LD;
-      sV = sX + (2 + buf) * BN * LD;
+  int turn = 0;
+  for (int j = SPLIT ? warp : 0; j < ntile; j += SPLIT ? NW : 1, turn ^= 1) {
+    const float *sK;
+    if (SPLIT) {
+      if (j != warp) fetch(j, sX + warp * Gm::TILE, lane, 32);
+      asm volatile("cp.async.wait_group 0;" ::: "memory");
+      __syncwarp();
+      sK = sX + warp * Gm::TILE;
     } else {
-      load_tile(k, S.k[2], j0);
-      __syncthreads();
+      asm volatile("cp.async.wait_group 0;" ::: "memory");
+      __syncthreads();  // everyone's pieces have landed, and the other buffer has been read
+      fetch(j + 1, sX + (turn ^ 1) * Gm::TILE, threadIdx.x, NT);
+      sK = sX + turn * Gm::TILE;
     }
-    float s[RT][4];
+    const float *sV = sK + BN * LK;
+    const int j0 = j * BN;
+    if (j0 < wend) {
+      float s[BN / 8][4];
 #pragma unroll
-    for (int i = 0; i < RT; ++i)
+      for (int n = 0; n < BN / 8; ++n)
 #pragma unroll
-      for (int x = 0; x < 4; ++x) s[i][x] = 0.f;
-#pragma unroll 8
-    for (int c = 0; c < D; c += 4) {
-      float4 a[RT], b[4];
+        for (int x = 0; x < 4; ++x) s[n][x] = 0.f;
 #pragma unroll
-      for (int i = 0; i < RT; ++i) a[i] = *reinterpret_cast<const float4 *>(sQ + (ty * RT + i) * LD + c);
+      for (int c = 0; c < D / 16; ++c) {  // two k steps
+        const float4 qa = *reinterpret_cast<const float4 *>(mq + g * LK + c * 16 + t4 * 4);
+        const float4 qb = *reinterpret_cast<const float4 *>(mq + (g + 8) * LK + c * 16 + t4 * 4);
+        Split a[2][4];
+        a[0][0].set(qa.x);
+        a[0][1].set(qb.x);
+        a[0][2].set(qa.y);
+        a[0][3].set(qb.y);
+        a[1][0].set(qa.z);
+        a[1][1].set(qb.z);
+        a[1][2].set(qa.w);
+        a[1][3].set(qb.w);
 #pragma unroll
-      for (int x = 0; x < 4; ++x) b[x] = *reinterpret_cast<const float4 *>(sK + (tx + 16 * x) * LD + c);
-#pragma unroll
-      for (int i = 0; i < RT; ++i)
-#pragma unroll
-        for (int x = 0; x < 4; ++x)
-          s[i][x] += a[i].x * b[x].x + a[i].y * b[x].y + a[i].z * b[x].z + a[i].w * b[x].w;
-    }
-#pragma unroll
-    for (int i = 0; i < RT; ++i) {
-      const int lim = min(kend - 1, off + ty * RT + i) - j0;  // last key of the tile that the row sees
-      float mx = m[i];
-#pragma unroll
-      for (int x = 0; x < 4; ++x) mx = tx + 16 * x <= lim ? fmaxf(mx, s[i][x]) : mx;
-#pragma unroll
-      for (int w = 8; w; w >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, w));
-      const float f = mx == m[i] ? 1.f : tc::ex2(m[i] - mx);
-      m[i] = mx;
-      float sum = 0.f;
-#pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        const float p = tx + 16 * x <= lim ? tc::ex2(s[i][x] - mx) : 0.f;
-        sP[(ty * RT + i) * LP + tx + 16 * x] = p;
-        sum += p;
+        for (int n = 0; n < BN / 8; ++n) {
+          const float4 kb = *reinterpret_cast<const float4 *>(sK + (n * 8 + g) * LK + c * 16 + t4 * 4);
+          Split b[4];
+          b[0].set(kb.x);
+          b[1].set(kb.y);
+          b[2].set(kb.z);
+          b[3].set(kb.w);
+          mma_split(s[n], a[0], b[0], b[1]);
+          mma_split(s[n], a[1], b[2], b[3]);
+        }
       }
-      z[i] = z[i] * f + sum;
+      // logits of keys j0 + 8 n + 2 t4 (+ 1)
+      float x0 = m0, x1 = m1;
+      const bool part = j0 + BN - 1 > min(lim0, off + r0);
 #pragma unroll
-      for (int c = 0; c < NV; ++c)
+      for (int n = 0; n < BN / 8; ++n)
 #pragma unroll
-        for (int x = 0; x < 4; ++x) o[i][c][x] *= f;
-    }
-    if constexpr (Gm::ASYNC) {
-      asm volatile("cp.async.wait_group 2;" ::: "memory");  // V
-      __syncthreads();
-    } else {
-      __syncthreads();
-      load_tile(v, S.v[2], j0);
-      __syncthreads();
-    }
-#pragma unroll 4
-    for (int j = 0; j < BN; j += 4) {
-      float4 p[RT];
+        for (int x = 0; x < 2; ++x) {
+          const int key = j0 + n * 8 + 2 * t4 + x;
+          s[n][x] = part && key > lim0 ? -INFINITY : s[n][x] * A.c_log2;
+          s[n][2 + x] = part && key > lim1 ? -INFINITY : s[n][2 + x] * A.c_log2;
+          x0 = fmaxf(x0, s[n][x]);
+          x1 = fmaxf(x1, s[n][2 + x]);
+        }
 #pragma unroll
-      for (int i = 0; i < RT; ++i) p[i] = *reinterpret_cast<const float4 *>(sP + (ty * RT + i) * LP + j);
+      for (int w = 1; w < 4; w <<= 1) {
+        x0 = fmaxf(x0, __shfl_xor_sync(0xFFFFFFFFu, x0, w));
+        x1 = fmaxf(x1, __shfl_xor_sync(0xFFFFFFFFu, x1, w));
+      }
+      if (__any_sync(0xFFFFFFFFu, x0 > m0 || x1 > m1)) {
+        const float f0 = x0 > m0 ? tc::ex2(m0 - x0) : 1.f, f1 = x1 > m1 ? tc::ex2(m1 - x1) : 1.f;
+        m0 = x0;
+        m1 = x1;
+        z0 *= f0;
+        z1 *= f1;
 #pragma unroll
-      for (int c = 0; c < NV; ++c) {
-        float4 x[4];
+        for (int i = 0; i < NO; ++i) {
+          o[i][0] *= f0;
+          o[i][1] *= f0;
+          o[i][2] *= f1;
+          o[i][3] *= f1;
+        }
+      }
+      const float b0 = m0 == -INFINITY ? 0.f : m0, b1 = m1 == -INFINITY ? 0.f : m1;  // no key seen yet
 #pragma unroll
-        for (int y = 0; y < 4; ++y) x[y] = *reinterpret_cast<const float4 *>(sV + (j + y) * LD + 4 * tx + 64 * c);
+      for (int n = 0; n < BN / 8; ++n) {
+        Split a[4];  // rows g, g + 8 against keys 2 t4, 2 t4 + 1: columns t4 and t4 + 4
+        const float p0 = tc::ex2(s[n][0] - b0), p1 = tc::ex2(s[n][1] - b0);
+        const float p2 = tc::ex2(s[n][2] - b1), p3 = tc::ex2(s[n][3] - b1);
+        z0 += p0 + p1;
+        z1 += p2 + p3;
+        a[0].set(p0);
+        a[1].set(p2);
+        a[2].set(p1);
+        a[3].set(p3);
 #pragma unroll
-        for (int i = 0; i < RT; ++i) {
-          o[i][c][0] += p[i].x * x[0].x + p[i].y * x[1].x + p[i].z * x[2].x + p[i].w * x[3].x;
-          o[i][c][1] += p[i].x * x[0].y + p[i].y * x[1].y + p[i].z * x[2].y + p[i].w * x[3].y;
-          o[i][c][2] += p[i].x * x[0].z + p[i].y * x[1].z + p[i].z * x[2].z + p[i].w * x[3].z;
-          o[i][c][3] += p[i].x * x[0].w + p[i].y * x[1].w + p[i].z * x[2].w + p[i].w * x[3].w;
+        for (int c = 0; c < D / 32; ++c) {
+          const float4 va = *reinterpret_cast<const float4 *>(sV + (n * 8 + 2 * t4) * LV + c * 32 + g * 4);
+          const float4 vb = *reinterpret_cast<const float4 *>(sV + (n * 8 + 2 * t4 + 1) * LV + c * 32 + g * 4);
+          const float xa[4] = {va.x, va.y, va.z, va.w}, xb[4] = {vb.x, vb.y, vb.z, vb.w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            Split ba, bb;
+            ba.set(xa[i]);
+            bb.set(xb[i]);
+            mma_split(o[c * 4 + i], a, ba, bb);
+          }
         }
       }
     }
-    if constexpr (!Gm::ASYNC) __syncthreads();
+    if (SPLIT) __syncwarp();  // the buffer has been read
   }
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
 #pragma unroll
-  for (int i = 0; i < RT; ++i) {
-    float sum = z[i];
+  for (int w = 1; w < 4; w <<= 1) {
+    z0 += __shfl_xor_sync(0xFFFFFFFFu, z0, w);
+    z1 += __shfl_xor_sync(0xFFFFFFFFu, z1, w);
+  }
+  // O's tile 4 c + i holds columns 32 c + 8 t4 + i and + 4: four tiles give the lane columns
+  // 32 c + 8 t4 .. + 7
+  auto store = [&](int r, int col, float4 w) {
+    T *dst = O + t.b * S.o[0] + h * S.o[1] + (long long)(t.q0 + t.r0 + r) * S.o[2] + col;
+    if constexpr (sizeof(T) == 4) {
+      *reinterpret_cast<float4 *>(dst) = w;
+    } else {
+      const __nv_bfloat162 a = __floats2bfloat162_rn(w.x, w.y), b = __floats2bfloat162_rn(w.z, w.w);
+      *reinterpret_cast<uint2 *>(dst) = make_uint2(*reinterpret_cast<const uint32_t *>(&a), *reinterpret_cast<const uint32_t *>(&b));
+    }
+  };
+  auto store_lse = [&](int r, float m, float z) {
+    if (A.lse)
+      A.lse[((long long)t.b * S.Hq + h) * S.Tq + t.q0 + t.r0 + r] =
+          z > 0.f ? (m + log2f(z)) * 0.6931471805599453f : -INFINITY;
+  };
+  if constexpr (!SPLIT) {
 #pragma unroll
-    for (int w = 8; w; w >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, w);
-    const int r = ty * RT + i;
-    if (r >= rows) continue;
-    const float inv = sum > 0.f ? 1.f / sum : 0.f;  // no key seen: 0
-    T *dst = O + t.b * S.o[0] + h * S.o[1] + (long long)(t.q0 + t.r0 + r) * S.o[2];
+    for (int half = 0; half < 2; ++half) {
+      const int r = r0 + g + 8 * half;
+      if (r >= rows) continue;
+      const float z = half ? z1 : z0, inv = z > 0.f ? 1.f / z : 0.f;  // no key seen: 0
 #pragma unroll
-    for (int c = 0; c < NV; ++c) {
-      const float4 w = make_float4(o[i][c][0] * inv, o[i][c][1] * inv, o[i][c][2] * inv, o[i][c][3] * inv);
-      if constexpr (sizeof(T) == 4) {
-        *reinterpret_cast<float4 *>(dst + 4 * tx + 64 * c) = w;
-      } else {
-        const __nv_bfloat162 a = __floats2bfloat162_rn(w.x, w.y), b = __floats2bfloat162_rn(w.z, w.w);
-        *reinterpret_cast<uint2 *>(dst + 4 * tx + 64 * c) =
-            make_uint2(*reinterpret_cast<const uint32_t *>(&a), *reinterpret_cast<const uint32_t *>(&b));
+      for (int c = 0; c < D / 32; ++c)
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+          store(r, c * 32 + 8 * t4 + 4 * x,
+                make_float4(o[4 * c][2 * half + x] * inv, o[4 * c + 1][2 * half + x] * inv, o[4 * c + 2][2 * half + x] * inv,
+                            o[4 * c + 3][2 * half + x] * inv));
+      if (t4 == 0) store_lse(r, half ? m1 : m0, z);
+    }
+  } else {
+    __shared__ float sm[NW][16], sz[NW][16];
+    __syncthreads();
+    float *mine = sX + warp * Gm::TILE;  // [16][D]
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+#pragma unroll
+      for (int c = 0; c < D / 32; ++c)
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+          *reinterpret_cast<float4 *>(mine + (g + 8 * half) * D + c * 32 + 8 * t4 + 4 * x) =
+              make_float4(o[4 * c][2 * half + x], o[4 * c + 1][2 * half + x], o[4 * c + 2][2 * half + x],
+                          o[4 * c + 3][2 * half + x]);
+      if (t4 == 0) {
+        sm[warp][g + 8 * half] = half ? m1 : m0;
+        sz[warp][g + 8 * half] = half ? z1 : z0;
       }
     }
-    if (A.lse && tx == 0)
-      A.lse[((long long)t.b * S.Hq + h) * S.Tq + t.q0 + t.r0 + r] =
-          sum > 0.f ? (m[i] + log2f(sum)) * 0.6931471805599453f : -INFINITY;
+    __syncthreads();
+    for (int e = threadIdx.x; e < rows * (D / 4); e += NT) {
+      const int r = e / (D / 4), col = (e % (D / 4)) * 4;
+      float M = -INFINITY, Z = 0.f;
+#pragma unroll
+      for (int w = 0; w < NW; ++w) M = fmaxf(M, sm[w][r]);
+      float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int w = 0; w < NW; ++w) {
+        const float f = sz[w][r] > 0.f ? tc::ex2(sm[w][r] - M) : 0.f;  // a warp without a visible key
+        const float4 x = *reinterpret_cast<const float4 *>(sX + w * Gm::TILE + r * D + col);
+        Z += f * sz[w][r];
+        y = make_float4(y.x + f * x.x, y.y + f * x.y, y.z + f * x.z, y.w + f * x.w);
+      }
+      const float inv = Z > 0.f ? 1.f / Z : 0.f;
+      store(r, col, make_float4(y.x * inv, y.y * inv, y.z * inv, y.w * inv));
+      if (col == 0) store_lse(r, M, Z);
+    }
   }
 }
 
-template <typename T, int D, int RT>
+template <typename T, int D, int SPLIT>
 int run(const void *Q, const void *K, const void *V, void *O, const AttnArgs &A, cudaStream_t st) {
-  using Gm = Geo<T, D, RT>;
+  using Gm = Geo<D, SPLIT>;
   const long ctas = attn_tiles(A.S, Gm::BM) * A.S.Hq;
   if (ctas > 0x7FFFFFFFL) return KV_ERR_UNSUPPORTED;
-  if (ensure_smem((const void *)attn_kernel<T, D, RT>, Gm::SMEM)) return KV_ERR_CUDA;
-  attn_kernel<T, D, RT><<<(unsigned)ctas, NT, Gm::SMEM, st>>>(static_cast<const T *>(Q), static_cast<const T *>(K),
-                                                            static_cast<const T *>(V), static_cast<T *>(O), A);
+  if (ensure_smem((const void *)attn_kernel<T, D, SPLIT>, Gm::SMEM)) return KV_ERR_CUDA;
+  attn_kernel<T, D, SPLIT><<<(unsigned)ctas, 32 * Gm::NW, Gm::SMEM, st>>>(
+      static_cast<const T *>(Q), static_cast<const T *>(K), static_cast<const T *>(V), static_cast<T *>(O), A);
   return launch_status();
 }
 
-// Tiles of 64 rows reuse K and V four times as often as tiles of 16, which give four
-// times the CTAs: the small ones when the large ones would leave SMs without work.
+// 64-row tiles read K and V a quarter as often; the split form only where they would leave
+// SMs without work.
 template <typename T, int D>
 int run_rows(const void *Q, const void *K, const void *V, void *O, const AttnArgs &A, cudaStream_t st) {
   if (attn_tiles(A.S, 64) * A.S.Hq < kNumSmsHint) return run<T, D, 1>(Q, K, V, O, A, st);
-  return run<T, D, 4>(Q, K, V, O, A, st);
+  return run<T, D, 0>(Q, K, V, O, A, st);
 }
 
 }  // namespace

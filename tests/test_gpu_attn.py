@@ -54,6 +54,9 @@ DENSE = [
     (1, 8, 1, 65, 200, 64, F32),        # a chunk behind cached keys
     (1, 2, 2, 100, 37, 128, F32),       # rows that see no key
     (1, 2, 1, 3, 0, 64, F32),           # no keys at all
+    (1, 16, 4, 650, 650, 64, F32),      # tiles of 64 rows
+    (2, 16, 16, 333, 400, 128, F32),
+    (1, 16, 8, 700, 20, 128, F32),
     (2, 4, 2, 257, 257, 128, BF),
     (1, 3, 1, 300, 300, 64, BF),
     (1, 2, 2, 1, 777, 128, BF),         # one token
@@ -201,6 +204,24 @@ def test_large_logits_and_descending_maxima(kvc, q8, dtype):
     torch.cuda.synchronize()
     for h in range(3):
         _check(q8, o[0, h], lse[0, h], Q[0, h], K[0, h], V[0, h], d ** -0.5, h)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("scale", [0.0, -0.2])
+@pytest.mark.parametrize("shape", [(2, 1, 90, 130, 128), (8, 4, 700, 700, 64)], ids=str)
+def test_odd_scales(kvc, q8, dtype, scale, shape):
+    """Scales that turn the order of the logits round, or make them all equal."""
+    Hq, Hkv, Tq, Tk, d = shape
+    Q, K, V = _rand((1, Hq, Tq, d), dtype, 1), _rand((1, Hkv, Tk, d), dtype, 2), _rand((1, Hkv, Tk, d), dtype, 3)
+    o, lse = kvc.kv_attn_prompt(Q, K, V, scale=scale)
+    torch.cuda.synchronize()
+    for h in range(Hq):
+        hk = h // (Hq // Hkv)
+        want, wl, mass = q8.attn_prompt(np64(Q[0, h]), np64(K[0, hk]), np64(V[0, hk]), scale)
+        dl = C_CUDA * abs(scale) * (np.abs(np64(Q[0, h])) @ np.abs(np64(K[0, hk])).T).max(-1)
+        half = 2.0 ** -8 if dtype == BF else 0.0
+        within(np64(o[0, h]), want, (2 * dl + 2.0 ** -18)[:, None] * mass + half * np.abs(want) + 1e-37, f"o {h}")
+        within(np64(lse[0, h]), wl, dl + 2.0 ** -20 + 2.0 ** -22 * np.abs(wl), f"lse {h}")
 
 
 def test_long_rows(kvc, q8):
