@@ -296,7 +296,8 @@ __global__ void __launch_bounds__(NTM, 1024 / NTM) evict_move_kernel(const __gri
   const long src0 = (long)u * A.from.cap;
   int coded = 0;  // rows whose source is codes: the first ones, slots ascend
   for (int r = threadIdx.x; r < rows; r += NTM) {
-    const int j = A.idx[(long)u * A.k + r0 + r];
+    // one of the unit's slots, by the selection; held to it all the same: it is an address
+    const int j = max(0, min(n_src - 1, A.idx[(long)u * A.k + r0 + r]));
     src[r] = j;
     if (j < nf) {
       skv[r] = make_float2(__ldg(A.from.Ks + ((src0 + j) >> bl)), __ldg(A.from.Vs + ((src0 + j) >> bl)));
@@ -518,8 +519,9 @@ __global__ void __launch_bounds__(NTS) evict_select_kernel(const float *__restri
 
 // The same selection for units whose order keys fit on chip: a cluster of CTAs per unit,
 // each with a slice of the slots in shared memory, so that acc is read once.  A protected
-// slot gets the largest key (no finite acc has it), and (key, slot) is unique: the
-// `keep` largest of all slots are those that stay, the later of equal ones first.
+// slot gets the largest key (no finite acc has it): the `keep` largest of all slots stay.
+// Four passes find the threshold's key; of the slots that equal it the last ones stay, which
+// takes no more passes but a count of the equal slots in front of each CTA, warp and slot.
 constexpr int NTC = 512;
 constexpr int NWC = NTC / 32;
 constexpr int kHistCopies = 4;
@@ -531,7 +533,7 @@ __global__ void __launch_bounds__(NTC) evict_select_resident_kernel(
     int keep, int recent, int sink, int32_t *__restrict__ idx, int32_t *__restrict__ len_out, int *status) {
   extern __shared__ __align__(16) uint32_t keys[];
   __shared__ RadixScratch<NTC, kHistCopies> rx;
-  __shared__ int wcnt[NWC], cnt[kMaxCl];
+  __shared__ int2 wcnt[NWC], cnt[kMaxCl];  // slots above the threshold, slots equal to it
   pdl_wait();
   pdl_launch();
   cooperative_groups::cluster_group cl = cooperative_groups::this_cluster();
@@ -555,11 +557,21 @@ __global__ void __launch_bounds__(NTC) evict_select_resident_kernel(
   __syncthreads();
   const float *acc = acc_all + u * (long)cap + lo;
   const int32_t *pos = pos_all + u * (long)cap + lo;
+  // The first digit (sign and seven bits of the exponent) is counted here.  Neighbouring
+  // accumulators mostly share it: a thread adds up runs before it touches the histogram,
+  // where equal bins would queue.
+  uint32_t *const hist = rx.hist[warp & (kHistCopies - 1)];
+  uint32_t bin = 0, count = 0;
   auto put = [&](int i, float a) {
     const bool safe = lo + i >= n - recent || (lo + i < sink && pos[i] < sink);
     const uint32_t k = safe ? 0xFFFFFFFFu : order_key(a);
     keys[i] = k;
-    atomicAdd(&rx.hist[warp & (kHistCopies - 1)][k >> 24], 1u);
+    if (k >> 24 != bin) {
+      if (count) atomicAdd(hist + bin, count);
+      bin = k >> 24;
+      count = 0;
+    }
+    ++count;
   };
   if ((reinterpret_cast<uintptr_t>(acc) & 15) == 0) {
     const float4 *a4 = reinterpret_cast<const float4 *>(acc);
@@ -583,50 +595,68 @@ __global__ void __launch_bounds__(NTC) evict_select_resident_kernel(
   } else {
     for (int i = threadIdx.x; i < m; i += NTC) put(i, acc[i]);
   }
+  if (count) atomicAdd(hist + bin, count);
   cl.sync();  // slices loaded, and every CTA of the cluster is running
-  auto key64 = [&](int i) { return ((uint64_t)keys[i] << 32) | (uint32_t)(lo + i); };
-  const uint64_t thr = radix_select_ge<NTC, true>(
-      rx, keep,
-      [&](auto &&f) {
-        for (int i = threadIdx.x; i < m; i += NTC) f(key64(i));
-      },
-      [&](auto &&f) {
-        const uint4 *k4 = reinterpret_cast<const uint4 *>(keys);
-        for (int i = threadIdx.x; i < m >> 2; i += NTC) {
-          const uint4 q = k4[i];
-          f(q.x);
-          f(q.y);
-          f(q.z);
-          f(q.w);
-        }
-        for (int i = (m & ~3) + threadIdx.x; i < m; i += NTC) f(keys[i]);
-      },
-      true);
-  // kept slots per warp range, per CTA, then the CTA's place in the output
+  const uint32_t thr = (uint32_t)(radix_select_ge<NTC, true>(
+                                      rx, keep,
+                                      [&](auto &&f) {
+                                        for (int i = threadIdx.x; i < m; i += NTC) f((uint64_t)keys[i] << 32);
+                                      },
+                                      [&](auto &&f) {
+                                        const uint4 *k4 = reinterpret_cast<const uint4 *>(keys);
+                                        for (int i = threadIdx.x; i < m >> 2; i += NTC) {
+                                          const uint4 q = k4[i];
+                                          f(q.x);
+                                          f(q.y);
+                                          f(q.z);
+                                          f(q.w);
+                                        }
+                                        for (int i = (m & ~3) + threadIdx.x; i < m; i += NTC) f(keys[i]);
+                                      },
+                                      true, 4) >>
+                                  32);
+  // all keys at or above thr stay, or of those that equal it only some
+  const bool whole = rx.sh_done != 0;
+  const int wanted = rx.sh_need;
+  // counts per warp range, per CTA, then what stands in front of the CTA
   const int wper = ((m + NWC - 1) / NWC + 31) & ~31;
   const int wlo = min(m, warp * wper), whi = min(m, wlo + wper);
-  int c = 0;
-  for (int i = wlo + lane; i < whi; i += 32) c += key64(i) >= thr;
-#pragma unroll
-  for (int o = 16; o; o >>= 1) c += __shfl_xor_sync(0xFFFFFFFFu, c, o);
+  int2 c = make_int2(0, 0);
+  for (int i = wlo + lane; i < whi; i += 32) {
+    c.x += whole ? keys[i] >= thr : keys[i] > thr;
+    c.y += !whole && keys[i] == thr;
+  }
+  c.x = __reduce_add_sync(0xFFFFFFFFu, c.x);
+  c.y = __reduce_add_sync(0xFFFFFFFFu, c.y);
   if (lane == 0) wcnt[warp] = c;
   __syncthreads();
   if ((int)threadIdx.x < CL) {
-    int tot = 0;
-    for (int w = 0; w < NWC; ++w) tot += wcnt[w];
+    int2 tot = make_int2(0, 0);
+    for (int w = 0; w < NWC; ++w) {
+      tot.x += wcnt[w].x;
+      tot.y += wcnt[w].y;
+    }
     cl.map_shared_rank(&cnt[0], threadIdx.x)[rank] = tot;
   }
   cl.sync();  // the last remote access is above
-  int run = 0;
-  for (int r = 0; r < rank; ++r) run += cnt[r];
-  for (int w = 0; w < warp; ++w) run += wcnt[w];
+  int above = 0, equal = 0, all_equal = 0;
+  for (int r = 0; r < CL; ++r) {
+    if (r < rank) above += cnt[r].x, equal += cnt[r].y;
+    all_equal += cnt[r].y;
+  }
+  for (int w = 0; w < warp; ++w) above += wcnt[w].x, equal += wcnt[w].y;
+  const int skip = whole ? 0 : all_equal - wanted;  // so many of the equal slots go, the first ones
+  const unsigned before = (1u << lane) - 1u;
   for (int i0 = wlo; i0 < whi; i0 += 32) {
     const int i = i0 + lane;
-    const bool stay = i < whi && key64(i) >= thr;
-    const unsigned msk = __ballot_sync(0xFFFFFFFFu, stay);
-    const int at = run + __popc(msk & ((1u << lane) - 1u));
-    if (stay && at < keep) out[at] = lo + i;
-    run += __popc(msk);
+    const uint32_t k = i < whi ? keys[i] : 0u;
+    const bool gt = i < whi && (whole ? k >= thr : k > thr), eq = i < whi && !whole && k == thr;
+    const unsigned mg = __ballot_sync(0xFFFFFFFFu, gt), me = __ballot_sync(0xFFFFFFFFu, eq);
+    const int rank_eq = equal + __popc(me & before);
+    const int at = above + __popc(mg & before) + max(0, rank_eq - skip);
+    if ((gt || (eq && rank_eq >= skip)) && at < keep) out[at] = lo + i;
+    above += __popc(mg);
+    equal += __popc(me);
   }
 }
 

@@ -109,16 +109,18 @@ __device__ __forceinline__ void digit_boundary(const uint32_t *h, int need, uint
 // decisions and runs the same passes.  Every thread of every CTA must call.
 //
 // visit_hi (optional): visit_hi(f) calls f(key >> 32) for every candidate; the
-// four passes over the high word then use 32-bit keys.  pass0_filled: the caller
+// four passes over the high word then use 32-bit keys.  max_pass: stop after that many
+// passes even when sm.sh_done is 0: sm.sh_need keys of those that share the returned
+// prefix are then still wanted.  pass0_filled: the caller
 // has already histogrammed the top byte (key >> 56) into sm.hist (per warp).
 template <int NT, bool CLUSTER, typename Visit, typename VisitHi = std::nullptr_t, int HC = NT / 32>
 __device__ uint64_t radix_select_ge(RadixScratch<NT, HC> &sm, int need, Visit visit,
-                                    VisitHi visit_hi = nullptr, bool pass0_filled = false) {
+                                    VisitHi visit_hi = nullptr, bool pass0_filled = false, int max_pass = 8) {
   const int hw = (threadIdx.x >> 5) & (HC - 1);  // this warp's histogram copy
   constexpr bool HI32 = !std::is_same<VisitHi, std::nullptr_t>::value;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   uint64_t prefix = 0, hmask = 0;
-  for (int pass = 0; pass < 8; ++pass) {
+  for (int pass = 0; pass < max_pass; ++pass) {
     const int shift = 56 - 8 * pass;
     const int buf = pass & 1;
     if (!(pass == 0 && pass0_filled)) {
