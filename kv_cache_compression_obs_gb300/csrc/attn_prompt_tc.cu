@@ -62,7 +62,8 @@ struct TcArgs {
   __nv_bfloat16 *O;
   int pair_rows;  // 1: the two tiles are the halves of 256 rows; 0: two heads
   int wide;       // O's rows start on 32-byte boundaries
-  int splits;     // items per query tile, each with a share of its key tiles
+  int whole;      // query tiles (in the order of attn_locate) whose items are not split
+  int splits;     // the others' items: each with a share of its key tiles
   float *part;    // splits > 1: [splits][B][Hq][Tq][D] sums of P V, not yet divided
   float2 *stat;   // [splits][B][Hq][Tq] reference (log2 units) and sum of weights
 };
@@ -173,15 +174,26 @@ struct Work {
   AttnTile t;
   int h[2], r0[2], rows[2], n[2];  // per tile: head, first row, rows, key tiles
   int nmax;
-  int split, j0;  // share of the key tiles: the first of them
+  int split, j0;  // share of the key tiles (-1: all) and the first of them
 };
 
-__device__ __forceinline__ Work make_work(const TcArgs &T, const AttnTile &t, int part) {
+// CTA `block`'s item; executed by one whole warp.
+__device__ __forceinline__ Work make_work(const TcArgs &T, int block, bool check_all) {
+  const int pairs = T.pair_rows ? T.A.S.Hq : T.A.S.Hq / 2;  // items per query tile, unsplit
+  int index = block / pairs, hi = block - index * pairs;
   Work w;
+  w.split = -1;
+  if (index >= T.whole) {
+    const int b = block - T.whole * pairs;
+    index = b / (pairs * T.splits);
+    const int part = b - index * pairs * T.splits;
+    index += T.whole;
+    hi = part / T.splits;
+    w.split = part - hi * T.splits;
+  }
+  const AttnTile t = attn_locate(T.A.S, index, T.pair_rows ? 2 * BM : BM, check_all, T.A.status);
   w.t = t;
   w.nmax = 0;
-  const int hi = part / T.splits;
-  w.split = part - hi * T.splits;
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     w.h[i] = T.pair_rows ? hi : 2 * hi + i;
@@ -193,7 +205,7 @@ __device__ __forceinline__ Work make_work(const TcArgs &T, const AttnTile &t, in
     w.nmax = max(w.nmax, w.n[i]);
   }
   w.j0 = 0;
-  if (T.splits > 1) {
+  if (w.split >= 0) {
     const int per = (w.nmax + T.splits - 1) / T.splits;
     w.j0 = w.split * per;
 #pragma unroll
@@ -253,7 +265,6 @@ __global__ void __launch_bounds__(NT, 1)
   Ctrl &C = *reinterpret_cast<Ctrl *>(sm + Gm::CTRL_OFF);
   const AttnShape &S = T.A.S;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int groups = (T.pair_rows ? S.Hq : S.Hq / 2) * T.splits;  // items per query tile
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < ST; ++i) {
@@ -290,8 +301,7 @@ __global__ void __launch_bounds__(NT, 1)
   pdl_launch();
   Work first_work{};
   if (warp == W_SCHED)
-    first_work = make_work(T, attn_locate(S, blockIdx.x / groups, T.pair_rows ? 2 * BM : BM, blockIdx.x == 0, T.A.status),
-                           blockIdx.x % groups);
+    first_work = make_work(T, blockIdx.x, blockIdx.x == 0);
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
@@ -327,7 +337,7 @@ __global__ void __launch_bounds__(NT, 1)
         int block = wait(&C.clc, k) ? clc_block(C.reply) : -1;
         block = __shfl_sync(0xFFFFFFFFu, block, 0);
         if (block >= 0)
-          w = make_work(T, attn_locate(S, block / groups, T.pair_rows ? 2 * BM : BM, false, T.A.status), block % groups);
+          w = make_work(T, block, false);
         else
           w.t.nq = -1;
       }
@@ -575,7 +585,7 @@ __global__ void __launch_bounds__(NT, 1)
         if (!ok) break;
         tc::fence_after_sync();
       }
-      if (T.splits > 1 && w.rows[i] > 0) {
+      if (w.split >= 0 && w.rows[i] > 0) {
         // this share of the keys, for attn_join_kernel
         const long long at = (((long long)w.split * S.B + w.t.b) * S.Hq + w.h[i]) * S.Tq + w.t.q0 + w.r0[i] + row;
         const bool live = row < w.rows[i];
@@ -639,7 +649,7 @@ __global__ void __launch_bounds__(NT, 1)
   if (warp == W_MMA) tc::tmem_dealloc(tmem, 512);
 }
 
-// Joins the shares of split rows: O = sum_s 2^(m_s - M) O_s / sum_s 2^(m_s - M) z_s.  One CTA
+// Joins the shares of the split tiles' rows: O = sum_s 2^(m_s - M) O_s / sum_s 2^(m_s - M) z_s.  One CTA
 // per (query tile, head); a row is D / 4 threads, all its shares in flight.
 constexpr int kMaxSplits = 16;
 constexpr int NTJ = 256, JM = 32;  // threads and rows of a CTA
@@ -649,13 +659,15 @@ __global__ void __launch_bounds__(NTJ) attn_join_kernel(const __grid_constant__ 
   const AttnShape &S = T.A.S;
   pdl_wait();
   pdl_launch();
-  const int h = blockIdx.x % S.Hq;
+  const int bm = T.pair_rows ? 2 * BM : BM, subs = bm / JM;
+  const int h = blockIdx.x % S.Hq, sub = blockIdx.x / S.Hq % subs;
   if (threadIdx.x < 32) {
-    const AttnTile t = attn_locate(S, blockIdx.x / S.Hq, JM, false, nullptr);
+    const AttnTile t = attn_locate(S, T.whole + blockIdx.x / S.Hq / subs, bm, false, nullptr);
     if (threadIdx.x == 0) tile = t;
   }
   __syncthreads();
-  const AttnTile t = tile;
+  AttnTile t = tile;
+  t.r0 += sub * JM;
   const int rows = min(JM, t.nq - t.r0);
   const long long step = (long long)S.B * S.Hq * S.Tq;
   const int lane = threadIdx.x % (D / 4);
@@ -690,30 +702,49 @@ __global__ void __launch_bounds__(NTJ) attn_join_kernel(const __grid_constant__ 
   }
 }
 
-// Items per query tile.  `items` of about `tiles` key tiles each, split in s, take
-// ceil(items s / SMs) rounds of tiles / s + 2 steps on the SMs (a step is about 1.4 us, two are
-// what an item costs besides its tiles); the shares' fp32 sums are written and read again
-// by the join.  Splitting pays where items leave SMs idle (16 rows of 32 heads over 32768
-// keys, 16 items: 56 us against 352), not where it only evens out the last round: a chunk of
-// 2000 rows behind 30001 keys, 256 items, took 725 us in 4 shares and 663 whole.
-int choose_splits(long items, int tiles) {
-  const long sms = kNumSmsHint;
-  int best = 1;
-  double least = 0.;
-  for (int s = 1; s <= kMaxSplits && (s == 1 || s * 4 <= tiles); ++s) {
-    const double t = (double)((items * s + sms - 1) / sms) * ((double)tiles / s + 2.) + (s > 1 ? 3. + items * s / 60. : 0.);
-    if (s == 1 || t < (best == 1 ? 0.75 : 0.95) * least) {
-      best = s;
-      least = t;
-    }
-    if (s == 1 && items >= sms) break;
-  }
-  return best;
+// How the items are split over their keys: `whole` query tiles are not, the others in `splits`.
+struct Plan {
+  long tiles, pairs;  // query tiles, items per tile
+  int whole, splits;
+};
+
+// A round of `items` equal items of `tiles` key tiles on all SMs, split in s, takes
+// ceil(items s / SMs) (tiles / s + 2) steps of about 1.4 us (two are what an item costs
+// besides its tiles); the shares' fp32 sums are written and read again by the join.
+double round_steps(long items, int tiles, int s) {
+  return (double)((items * s + kNumSmsHint - 1) / kNumSmsHint) * ((double)tiles / s + 2.) + (s > 1 ? 3. + items * s / 60. : 0.);
 }
 
-long tc_items(const AttnShape &S) {
+// Sizes alone decide (the lengths are on the device): Tk stands for every sequence's keys.
+// Fewer items than SMs: all of them are split if that pays (16 rows of 32 heads over 32768
+// keys, 16 items: 56 us against 352).  A few rounds of about equal items (a chunk behind
+// many more keys): the tiles of the last, partial round are (2000 rows of 32 heads behind 30001
+// keys, 256 items: 651 us against 672; all in 4 shares 725).  Otherwise the items are
+// many or shrink towards the end, and evening out is the claims' work.
+Plan make_plan(const AttnShape &S) {
   const bool pair_rows = (S.Hq / S.Hkv) % 2;
-  return attn_tiles(S, pair_rows ? 2 * BM : BM) * (pair_rows ? S.Hq : S.Hq / 2);
+  const int bm = pair_rows ? 2 * BM : BM, tiles = (S.Tk + BN - 1) / BN;
+  Plan p{attn_tiles(S, bm), pair_rows ? S.Hq : S.Hq / 2, 0, 1};
+  const long items = p.tiles * p.pairs;
+  p.whole = (int)p.tiles;
+  long rest = items;
+  if (items >= kNumSmsHint) {
+    if (items > 4 * kNumSmsHint || S.Tk < 2L * S.Tq) return p;
+    p.whole = (int)(items / kNumSmsHint * kNumSmsHint / p.pairs);
+    rest = items - p.whole * p.pairs;
+  }
+  const double one = round_steps(rest, tiles, 1);
+  double least = one;
+  for (int s = 2; s <= kMaxSplits && s * 4 <= tiles; ++s) {
+    const double t = round_steps(rest, tiles, s);
+    if (t < 0.85 * one && t < 0.95 * least) {
+      p.splits = s;
+      least = t;
+    }
+  }
+  if (p.splits == 1) p.whole = (int)p.tiles;
+  else if (items < kNumSmsHint) p.whole = 0;
+  return p;
 }
 
 // [B][H][T][d] with free strides as a 4-D map of boxes of 64 elements x 128 tokens.
@@ -735,12 +766,15 @@ int run(const void *Q, const void *K, const void *V, const TcArgs &T, cudaStream
   if (!encode_heads(&tmQ, Q, D, S.Tq, S.Hq, S.B, S.q) || !encode_heads(&tmK, K, D, S.Tk, S.Hkv, S.B, S.k) ||
       !encode_heads(&tmV, V, D, S.Tk, S.Hkv, S.B, S.v))
     return KV_ERR_CUDA;
-  const long ctas = tc_items(S) * T.splits, joins = attn_tiles(S, JM) * S.Hq;
+  const Plan plan = make_plan(S);
+  const long split = plan.tiles - plan.whole;  // split tiles
+  const long ctas = (plan.whole + split * plan.splits) * plan.pairs;
+  const long joins = plan.splits > 1 ? split * ((T.pair_rows ? 2 : 1) * BM / JM) * S.Hq : 0;
   if (ctas > 0x7FFFFFFFL || joins > 0x7FFFFFFFL) return KV_ERR_UNSUPPORTED;
   if (ensure_smem((const void *)attn_tc_kernel<D>, Geo<D>::SMEM)) return KV_ERR_CUDA;
   const cudaError_t e = launch_pdl(attn_tc_kernel<D>, (unsigned)ctas, NT, Geo<D>::SMEM, st, tmQ, tmK, tmV, T);
   if (e != cudaSuccess) return cuda_failure(e, "prompt attention");
-  if (T.splits > 1) {
+  if (joins > 0) {
     count_launches(1);
     const cudaError_t f = launch_pdl(attn_join_kernel<D>, (unsigned)joins, NTJ, 0, st, T);
     if (f != cudaSuccess) return cuda_failure(f, "prompt attention: joining the splits");
@@ -755,11 +789,9 @@ bool attn_tc_eligible(const AttnShape &S, float scale, int dtype) {
   return dtype == KV_BF16 && S.Tk > 0 && scale > 0.f && std::isfinite(scale);
 }
 
-// Sizes alone decide (the lengths are on the device): Tk stands for every sequence's keys.
-int attn_tc_splits(const AttnShape &S) { return choose_splits(tc_items(S), (S.Tk + BN - 1) / BN); }
-
 size_t attn_tc_workspace_bytes(const AttnShape &S) {
-  const int n = attn_tc_splits(S);
+  if (S.Tq <= 0 || S.Tk <= 0) return 0;
+  const int n = make_plan(S).splits;
   return n > 1 ? (size_t)n * S.B * S.Hq * S.Tq * (S.d * sizeof(float) + sizeof(float2)) + 32 : 0;
 }
 
@@ -767,7 +799,8 @@ int launch_attn_prompt_tc(const void *Q, const void *K, const void *V, const Att
                           cudaStream_t st) {
   bool wide = (reinterpret_cast<uintptr_t>(O) & 31) == 0;
   for (int i = 0; i < 3; ++i) wide = wide && A.S.o[i] % 16 == 0;
-  TcArgs T{A, static_cast<__nv_bfloat16 *>(O), (A.S.Hq / A.S.Hkv) % 2, wide, attn_tc_splits(A.S), nullptr, nullptr};
+  const Plan plan = make_plan(A.S);
+  TcArgs T{A, static_cast<__nv_bfloat16 *>(O), (A.S.Hq / A.S.Hkv) % 2, wide, plan.whole, plan.splits, nullptr, nullptr};
   T.part = reinterpret_cast<float *>((reinterpret_cast<uintptr_t>(ws) + 31) & ~uintptr_t(31));  // 32-byte stores
   T.stat = reinterpret_cast<float2 *>(T.part + (size_t)T.splits * A.S.B * A.S.Hq * A.S.Tq * A.S.d);
   return A.S.d == 128 ? run<128>(Q, K, V, T, st) : run<64>(Q, K, V, T, st);

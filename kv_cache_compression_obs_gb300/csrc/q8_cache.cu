@@ -660,10 +660,10 @@ __global__ void __launch_bounds__(NTC) evict_select_resident_kernel(
   }
 }
 
-// CTAs per unit and slots per CTA (0: the unit does not fit).  About two CTAs an SM over
-// all units, slices of at least 2048 slots.
+// CTAs per unit and slots per CTA (0: the unit does not fit).  About one CTA an SM over
+// all units (more spend longer at the cluster's barriers), slices of at least 2048 slots.
 void select_plan(long units, int cap, int *CL, int *slice) {
-  const long want = (2L * kNumSmsHint + units - 1) / units, most = (cap + 2047) / 2048;
+  const long want = (kNumSmsHint + units - 1) / units, most = (cap + 2047) / 2048;
   long cl = want < most ? want : most;
   const long least = (cap + kSliceMax - 33) / (kSliceMax - 32);
   if (cl < least) cl = least;

@@ -73,6 +73,9 @@ DENSE = [
     (2, 8, 2, 1, 2500, 128, BF),
     (1, 2, 1, 600, 1300, 128, BF),
     (1, 1, 1, 700, 1200, 64, BF),
+    (1, 64, 32, 700, 2100, 64, BF),     # the last, partial round of tiles in shares
+    (2, 40, 8, 300, 1900, 128, BF),
+    (1, 35, 7, 1100, 3000, 64, BF),
 ]
 
 
