@@ -197,6 +197,17 @@ def test_decode_without_scores_row_positions_and_len_out(kvc, q8):
     _check_step(q8, before, c, o, q, kn, vn, pos.tolist(), "s8", scale=0.2, len_out=ln)
 
 
+@pytest.mark.parametrize("G", [1, 4, 5])
+def test_decode_without_scores_in_a_long_cache(kvc, q8, G):
+    """The two-launch path without accumulators, a block that becomes full among the units."""
+    before = filled_cache(kvc, 1, 3, 32768, 64, 64, BF, "s8", [32767, 20000, 64 * 300 - 1], 33, acc=False)
+    c = clone(before)
+    q, kn, vn = _step_inputs(1, 3, G, 64, BF, 34)
+    o = kvc.h2o_decode_step_q8(q, kn, vn, c, 10 ** 6)
+    torch.cuda.synchronize()
+    _check_step(q8, before, c, o, q, kn, vn, 10 ** 6, "s8")
+
+
 @pytest.mark.parametrize("fmt", ["s8", "e4m3"])
 def test_decode_wide_ranges(kvc, q8, fmt):
     """Block scales over many powers of two, large logits, queries of very different sizes, one of zeros."""
@@ -290,6 +301,8 @@ EVICT = [
     (1, 1, 64, 32, 128, 32, BF, "s8", [64], 1, 0, 0),
     (1, 2, 2048, 2048, 128, 64, BF, "s8", [2048, 2000], 1999, 64, 4),
     (1, 1, 4096, 4096, 64, 64, BF, "s8", [4095], 4094, 2000, 2000),
+    (1, 3, 64, 128, 64, 32, BF, "s8", [64, 33, 0], 100, 10, 2),          # keep past the capacity
+    (2, 8, 1024, 512, 128, 128, F32, "s8", [1024, 1000, 900, 513] * 4, 500, 17, 1),
 ]
 
 
