@@ -472,8 +472,8 @@ KVC_API int kv_score_obs_noalloc(const void *Q_obs, const void *K, int B, int Hq
  *
  *   Q, O       [B][Hq][Tq][d];  K, V [B][Hkv][Tk][d]; dtype (O is rounded to it once)
  *   strides    host array of 12 element strides: batch, head and token of Q, K, V, O
- *              (the d elements of a row are adjacent), each with stride * element
- *              size a multiple of 16 bytes; NULL = dense.  [tokens][heads][d]
+ *              (the d elements of a row are adjacent), each positive and stride *
+ *              element size a multiple of 16 bytes; NULL = dense.  [tokens][heads][d]
  *              tensors and slices of a fused projection are given this way.
  *   n_seq      0: each of the B rows is one sequence; seq_q, seq_k are its query
  *              rows and keys [B] (NULL = Tq, Tk).
@@ -489,7 +489,8 @@ KVC_API int kv_score_obs_noalloc(const void *Q_obs, const void *K, int B, int Hq
  * K, V rows behind a sequence's last key are not used, whatever they hold.
  * Preconditions: Hq % Hkv == 0, d in {64, 128}, scale not NaN.
  * bf16: products on the tensor cores (tcgen05, TMA) with fp32 accumulation, the
- * weights rounded to bf16 before the second product; fp32: CUDA cores throughout.
+ * weights rounded to bf16 before the second product (scale <= 0 takes the fp32
+ * kernel); fp32: products of operands split in two tf32 parts, fp32 accuracy.
  */
 KVC_API int kv_attn_prompt(const void *Q, const void *K, const void *V, int B, int Hq, int Hkv, int Tq,
                            int Tk, int d, const int64_t *strides, const int32_t *seq_q,

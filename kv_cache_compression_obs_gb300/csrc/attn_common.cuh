@@ -38,16 +38,25 @@ __device__ __forceinline__ AttnTile attn_sequence(const AttnShape &S, int i) {
   return t;
 }
 
+// How far a warp has walked the sequences: `before` tiles in those in front of `base`.
+struct AttnScan {
+  int base, before;
+};
+
 // The index-th query tile of bm rows over all sequences, a sequence's last rows
 // (which see the most keys) first.  Executed by one whole warp; every lane gets the
-// tile.  check_all: also look at every sequence and report bad ones.
-__device__ __forceinline__ AttnTile attn_locate(const AttnShape &S, int index, int bm, bool check_all, int *status) {
+// tile.  scan: where the last call found its tile; a later tile is looked for from there,
+// so that a CTA walks thousands of short sequences once and not once per tile.
+// check_all: also look at every sequence and report bad ones.
+__device__ __forceinline__ AttnTile attn_locate(const AttnShape &S, int index, int bm, bool check_all, int *status,
+                                                AttnScan &scan) {
   const int lane = threadIdx.x & 31;
   const int n = S.n_seq > 0 ? S.n_seq : S.B;
   AttnTile found{0, 0, 0, 0, 0, 0};
   bool have = false;
-  int before = 0;
-  for (int base = 0; base < n && (!have || check_all); base += 32) {
+  const bool ahead = index >= scan.before;
+  int before = ahead ? scan.before : 0;
+  for (int base = ahead ? scan.base : 0; base < n && (!have || check_all); base += 32) {
     AttnTile t{0, 0, 0, 0, 0, 0};
     if (base + lane < n) {
       t = attn_sequence(S, base + lane);
@@ -76,10 +85,17 @@ __device__ __forceinline__ AttnTile attn_locate(const AttnShape &S, int index, i
       found.nk = __shfl_sync(0xFFFFFFFFu, t.nk, src);
       found.r0 = __shfl_sync(0xFFFFFFFFu, t.r0, src);
       have = true;
+      scan = AttnScan{base, before};
     }
     before += __shfl_sync(0xFFFFFFFFu, incl, 31);
   }
   return found;
+}
+
+// The same for a warp that takes one tile only.
+__device__ __forceinline__ AttnTile attn_locate(const AttnShape &S, int index, int bm, bool check_all, int *status) {
+  AttnScan scan{0, 0};
+  return attn_locate(S, index, bm, check_all, status, scan);
 }
 
 bool attn_tc_eligible(const AttnShape &S, float scale, int dtype);

@@ -178,7 +178,7 @@ struct Work {
 };
 
 // CTA `block`'s item; executed by one whole warp.
-__device__ __forceinline__ Work make_work(const TcArgs &T, int block, bool check_all) {
+__device__ __forceinline__ Work make_work(const TcArgs &T, int block, bool check_all, AttnScan &scan) {
   const int pairs = T.pair_rows ? T.A.S.Hq : T.A.S.Hq / 2;  // items per query tile, unsplit
   int index = block / pairs, hi = block - index * pairs;
   Work w;
@@ -191,7 +191,7 @@ __device__ __forceinline__ Work make_work(const TcArgs &T, int block, bool check
     hi = part / T.splits;
     w.split = part - hi * T.splits;
   }
-  const AttnTile t = attn_locate(T.A.S, index, T.pair_rows ? 2 * BM : BM, check_all, T.A.status);
+  const AttnTile t = attn_locate(T.A.S, index, T.pair_rows ? 2 * BM : BM, check_all, T.A.status, scan);
   w.t = t;
   w.nmax = 0;
 #pragma unroll
@@ -300,8 +300,9 @@ __global__ void __launch_bounds__(NT, 1)
   pdl_wait();
   pdl_launch();
   Work first_work{};
+  AttnScan scan{0, 0};
   if (warp == W_SCHED)
-    first_work = make_work(T, blockIdx.x, blockIdx.x == 0);
+    first_work = make_work(T, blockIdx.x, blockIdx.x == 0, scan);
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
@@ -337,7 +338,7 @@ __global__ void __launch_bounds__(NT, 1)
         int block = wait(&C.clc, k) ? clc_block(C.reply) : -1;
         block = __shfl_sync(0xFFFFFFFFu, block, 0);
         if (block >= 0)
-          w = make_work(T, block, false);
+          w = make_work(T, block, false, scan);
         else
           w.t.nq = -1;
       }

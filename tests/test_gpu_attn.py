@@ -140,6 +140,26 @@ def test_packed(kvc, q8, case, layout):
                    k[0, hk, b[i]:b[i + 1]], v[0, hk, b[i]:b[i + 1]], 0.15, (i, h))
 
 
+@pytest.mark.parametrize("dtype,d", [(F32, 64), (BF, 128), (BF, 64)])
+def test_many_packed_sequences(kvc, q8, dtype, d):
+    """More sequences than one look at the offsets covers, empty ones among them."""
+    r = np.random.default_rng(8)
+    lens = [int(x) for x in r.integers(0, 40, 700)]
+    lens[3] = lens[600] = 300
+    case = (4, 2, d, dtype, lens, [int(x) for x in r.integers(0, 3, 700)])
+    q, k, v, sq, sk = _packed(case, "token")
+    o, lse = kvc.kv_attn_prompt(q, k, v, seq_q=sq, seq_k=sk, packed=True)
+    torch.cuda.synchronize()
+    a, b = sq.tolist(), sk.tolist()
+    for i in (0, 3, 31, 32, 127, 128, 129, 255, 256, 511, 512, 600, 640, 698, 699):
+        for h in range(4):
+            _check(q8, o[0, h, a[i]:a[i + 1]], lse[0, h, a[i]:a[i + 1]], q[0, h, a[i]:a[i + 1]],
+                   k[0, h // 2, b[i]:b[i + 1]], v[0, h // 2, b[i]:b[i + 1]], d ** -0.5, (i, h))
+    # every row is some sequence's
+    one, _ = kvc.kv_attn_prompt(q, k, v, seq_q=sq, seq_k=sk, packed=True, out=torch.full_like(q, float("nan")))
+    assert not one.isnan().any() and same_bits(one, o)
+
+
 @pytest.mark.parametrize("dtype", [F32, BF])
 def test_padded_batch_and_garbage_behind_it(kvc, q8, dtype):
     """Rows of different lengths; NaN and infinities behind them change nothing and stay unread."""
