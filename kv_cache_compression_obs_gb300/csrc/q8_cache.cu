@@ -60,10 +60,10 @@ struct Piece {
 #pragma unroll
     for (int i = 0; i < NV; ++i) v[i] = make_uint4(0, 0, 0, 0);
   }
-  // SRC 0: rows of T, 1: codes, 2: either
-  template <int FMT, int SRC>
+  // the values; CODES: of codes as well as of rows
+  template <int FMT, bool CODES>
   __device__ __forceinline__ void get(float2 (&x)[8]) const {
-    if (SRC == 1 || (SRC == 2 && coded)) {
+    if (CODES && coded) {
       const uint32_t w[4] = {v[0].x, v[0].y, v[0].z, v[0].w};
       const float2 a2 = make_float2(a, a);
 #pragma unroll
@@ -80,10 +80,8 @@ struct Piece {
       for (int i = 0; i < 8; ++i) x[i] = make_float2(y[2 * i], y[2 * i + 1]);
     }
   }
-  // The largest magnitude: rounding c a to fp32 keeps the order, so the largest code's is it.
-  template <int FMT, int SRC>
+  // the largest magnitude of a piece of rows
   __device__ __forceinline__ float big() const {
-    if (SRC == 1 || (SRC == 2 && coded)) return __fmul_rn(Q8<FMT>::big16(v[0]), a);
     if constexpr (sizeof(T) == 2) {  // without the sign bf16 bits order like their values
       uint32_t m = 0;
 #pragma unroll
@@ -104,9 +102,8 @@ struct Piece {
   }
 };
 
-// The block's two scales and its codes, `bytes` of them for K and for V.  SRC 0: rows of T,
-// 1: codes, 2: either.
-template <typename T, int FMT, int SRC, int N>
+// The block's two scales and its codes, `bytes` of them for K and for V, from pieces of rows.
+template <typename T, int FMT, int N>
 __device__ __forceinline__ void quantise(const Piece<T> (&p)[2][N], const int (&at)[N], int bytes,
                                          uint8_t *const (&co)[2], float *const (&so)[2], float (&red)[2][16]) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -114,7 +111,7 @@ __device__ __forceinline__ void quantise(const Piece<T> (&p)[2][N], const int (&
   for (int kv = 0; kv < 2; ++kv) {
     float big = 0.f;
 #pragma unroll
-    for (int i = 0; i < N; ++i) big = fmaxf(big, p[kv][i].template big<FMT, SRC>());
+    for (int i = 0; i < N; ++i) big = fmaxf(big, p[kv][i].big());
     // magnitudes order like their bits
     const unsigned m = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(big));
     if (lane == 0) red[kv][warp] = __uint_as_float(m);
@@ -129,7 +126,7 @@ __device__ __forceinline__ void quantise(const Piece<T> (&p)[2][N], const int (&
     for (int i = 0; i < N; ++i) {
       if (at[i] >= bytes) continue;
       float2 x[8];
-      p[kv][i].template get<FMT, SRC>(x);
+      p[kv][i].template get<FMT, false>(x);
       *reinterpret_cast<uint4 *>(co[kv] + at[i]) = q8_pack16<FMT>(x, inv);
     }
     if (threadIdx.x == 0) *so[kv] = a;
@@ -194,7 +191,7 @@ __global__ void __launch_bounds__(512) compact_block_kernel(const __grid_constan
   float *const so[2] = {A.out.Ks + (to >> bl), A.out.Vs + (to >> bl)};
   uint8_t *const co[2] = {static_cast<uint8_t *>(A.out.K) + (to << A.d_log2),
                           static_cast<uint8_t *>(A.out.V) + (to << A.d_log2)};
-  quantise<T, FMT, 0>(p, at, block << A.d_log2, co, so, red);
+  quantise<T, FMT>(p, at, block << A.d_log2, co, so, red);
 }
 
 // ---- moving a cache's kept slots -----------------------------------------------------
@@ -232,7 +229,7 @@ __device__ __forceinline__ void move_last_block(const BlockArgs &A, int u, int b
       } else {
         p.load_rows(static_cast<const T *>(kv ? A.from.Vt : A.from.Kt) + ((((long)u << bl) + (j - nf)) << A.d_log2) + el);
       }
-      p.template get<FMT, 2>(x);
+      p.template get<FMT, true>(x);
     };
     float2 x[8];
     if (rows < block) {  // the unfinished block keeps its rows
@@ -673,7 +670,7 @@ void select_plan(long units, int cap, int *CL, int *slice) {
   *slice = least > kMaxCl ? 0 : (int)(((cap + cl - 1) / cl + 31) & ~31L);
 }
 
-int log2_of(int d) { return d == 128 ? 7 : d == 64 ? 6 : 5; }
+int log2_of(int d) { return d == 128 ? 7 : 6; }
 
 template <typename T, int FMT>
 int launch_move(const BlockArgs &A, long units, cudaStream_t st) {
@@ -716,7 +713,7 @@ int launch_compact_q8(const void *K, const void *V, const float *s, const int32_
   A.status = status;
   const long ctas = (long)out.B * out.Hkv * A.nblk;
   if (ctas > 0x7FFFFFFFL) return KV_ERR_UNSUPPORTED;
-  const int nt = out.block * out.d / 16 / kCompactPieces;  // 64 .. 512
+  const int nt = out.block * out.d / 16 / kCompactPieces;  // 64 .. 512 (d is 64 or 128)
   const bool bf = out.dtype == KV_BF16, s8 = out.format == KV_Q8_S8;
   auto *fn = bf && s8 ? compact_block_kernel<__nv_bfloat16, KV_Q8_S8>
              : bf     ? compact_block_kernel<__nv_bfloat16, KV_Q8_E4M3>

@@ -17,18 +17,6 @@
 
 namespace kvc {
 
-// max.f32 and min.f32 with three operands.
-__device__ __forceinline__ float max3(float a, float b, float c) {
-  float d;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
-  return d;
-}
-__device__ __forceinline__ float min3(float a, float b, float c) {
-  float d;
-  asm("min.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
-  return d;
-}
-
 template <int FMT> struct Q8;
 
 // int8 codes without the conversion instructions, which run at an eighth of the rate of

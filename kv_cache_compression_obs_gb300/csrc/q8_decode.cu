@@ -34,8 +34,6 @@
 #include <cooperative_groups.h>
 #include <cuda_fp16.h>
 
-#include <cmath>
-
 #include "pdl.cuh"
 #include "q8_common.cuh"
 #include "tc_common.cuh"
@@ -58,7 +56,7 @@ struct DecArgs {
   const int32_t *row_pos;
   int32_t new_pos;
   int32_t *len_out;
-  int Hq, G, ns, b_log2;
+  int G, ns, b_log2;
   float c_log2;      // scale log2(e)
   float *o;
   float *lgw;        // [units][cap + 1][G] logits
@@ -843,7 +841,6 @@ int launch_decode_q8(const void *q, const void *k_new, const void *v_new, const 
   A.row_pos = row_pos;
   A.new_pos = new_pos;
   A.len_out = len_out;
-  A.Hq = Hq;
   A.G = Hq / c.Hkv;
   A.ns = splits(units, c.cap);
   A.b_log2 = c.block == 128 ? 7 : c.block == 64 ? 6 : 5;
