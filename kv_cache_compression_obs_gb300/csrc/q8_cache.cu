@@ -343,7 +343,7 @@ __global__ void __launch_bounds__(NTM, 1024 / NTM) evict_move_kernel(const __gri
   uint8_t *ck = static_cast<uint8_t *>(A.out.K) + (out0 << A.d_log2) + (threadIdx.x << 4);
   uint8_t *cv = static_cast<uint8_t *>(A.out.V) + (out0 << A.d_log2) + (threadIdx.x << 4);
   float *sok = A.out.Ks + (out0 >> bl), *sov = A.out.Vs + (out0 >> bl);
-  int stage = 0;
+  int stage = 0, turn = 0;
   for (int i = 0; i < ring_blocks; ++i, ck += BYTES, cv += BYTES) {
     fetch(i + ST - 1, stage == 0 ? ST - 1 : stage - 1);  // into the stage that this thread has just read
     asm volatile("cp.async.wait_group %0;" ::"n"(ST - 1) : "memory");
@@ -382,7 +382,10 @@ __global__ void __launch_bounds__(NTM, 1024 / NTM) evict_move_kernel(const __gri
     // magnitudes order like their bits
     const unsigned mk = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(bk));
     const unsigned mv = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(bv));
-    float (&rd)[2][16] = red[i & 1];
+    // Two buffers in turn over the blocks that get here, each with a barrier (a whole block
+    // has none): who writes a buffer again knows that everybody has read it.
+    float (&rd)[2][16] = red[turn];
+    turn ^= 1;
     if (lane < 2) rd[lane][warp] = __uint_as_float(lane ? mv : mk);
     __syncthreads();
     // the lower half of a warp finds K's scale, the upper half V's

@@ -371,6 +371,43 @@ def test_evict_orders(kvc, q8, acc):
     _check_evicted(q8, src, before, out, idx, 333, 10, 2, "s8")
 
 
+def test_evict_whole_blocks_between_mixed_ones(kvc, q8):
+    """Long runs in which every other destination block is a source block moved as it is: half of
+    blocks 0 and 1 mod 3 go, blocks 2 mod 3 stay whole."""
+    B, H, block, d, nb = 1, 4, 32, 64, 3 * 700
+    cap = nb * block
+    src = filled_cache(kvc, B, H, cap, d, block, BF, "s8", [cap] * H, 93)
+    acc = torch.full((nb, block), 4.0, device="cuda")
+    acc[0::3, ::2] = 1.0
+    acc[1::3, 1::2] = 1.0
+    src["acc"].copy_(acc.flatten())
+    keep = cap // 3 * 2
+    before = filled_cache(kvc, B, H, keep, d, block, BF, "s8", [0] * H, 94)
+    out = clone(before)
+    idx = kvc.kv_evict_q8(src, keep, 0, out, sink=0)
+    torch.cuda.synchronize()
+    stay = torch.arange(cap, device="cuda")[acc.flatten() > 2]
+    assert torch.equal(idx.long(), stay.expand(B, H, -1)) and (out["len"] == keep).all()
+    rows = stay.view(-1, block)
+    whole = rows[:, -1] - rows[:, 0] == block - 1
+    assert whole[1::2].all() and not whole[0::2].any()
+    for name in ("K", "V"):
+        code, scale = src[name][0].view(H, nb, block, d), src[name + "s"][0]
+        got, gs = out[name][0].view(H, -1, block, d), out[name + "s"][0]
+        assert torch.equal(got[:, 1::2], code[:, 2::3]) and torch.equal(gs[:, 1::2], scale[:, 2::3])
+        x = (src[name][0].float() * scale.repeat_interleave(block, 1)[..., None])[:, stay].view(H, -1, block, d)
+        for h in range(H):
+            for i in range(0, rows.shape[0], 2):
+                want, a = q8.quantise(np64(x[h, i]), "s8") if i % 64 == 0 else (None, None)
+                if want is not None:
+                    assert gs[h, i].item() == a
+                    np.testing.assert_array_equal(np64(got[h, i]), want)
+        # every mixed block's largest code is 127 by its own scale: no other block's scale was used
+        assert (got[:, 0::2].int().abs().amax((-1, -2)) == 127).all()
+        top = x[:, 0::2].abs().amax((-1, -2)) / 127
+        assert ((gs[:, 0::2] - top).abs() <= top * 2.0 ** -23).all()
+
+
 def test_evict_long_unit(kvc, q8):
     """A unit longer than any on-chip buffer: the kept slots against a sort."""
     cap, keep, recent = 300032, 100001, 77
