@@ -519,7 +519,8 @@ __global__ void __launch_bounds__(NTS) evict_select_kernel(const float *__restri
 
 // The same selection for units whose order keys fit on chip: a cluster of CTAs per unit,
 // each with a slice of the slots in shared memory, so that acc is read once.  A protected
-// slot gets the largest key (no finite acc has it): the `keep` largest of all slots stay.
+// slot gets the largest key (that of no acc: a NaN with it is held to the one below): the
+// `keep` largest of all slots stay.
 // Four passes find the threshold's key; of the slots that equal it the last ones stay, which
 // takes no more passes but a count of the equal slots in front of each CTA, warp and slot.
 constexpr int NTC = 512;
@@ -564,7 +565,7 @@ __global__ void __launch_bounds__(NTC) evict_select_resident_kernel(
   uint32_t bin = 0, count = 0;
   auto put = [&](int i, float a) {
     const bool safe = lo + i >= n - recent || (lo + i < sink && pos[i] < sink);
-    const uint32_t k = safe ? 0xFFFFFFFFu : order_key(a);
+    const uint32_t k = safe ? 0xFFFFFFFFu : min(order_key(a), 0xFFFFFFFEu);
     keys[i] = k;
     if (k >> 24 != bin) {
       if (count) atomicAdd(hist + bin, count);
@@ -673,7 +674,7 @@ void select_plan(long units, int cap, int *CL, int *slice) {
   *slice = least > kMaxCl ? 0 : (int)(((cap + cl - 1) / cl + 31) & ~31L);
 }
 
-int log2_of(int d) { return d == 128 ? 7 : 6; }
+int log2_of(int n) { return n == 128 ? 7 : n == 64 ? 6 : 5; }  // a head dim or a block
 
 template <typename T, int FMT>
 int launch_move(const BlockArgs &A, long units, cudaStream_t st) {

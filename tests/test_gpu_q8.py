@@ -430,6 +430,46 @@ def test_evict_long_unit(kvc, q8):
     np.testing.assert_array_equal(out["pos"][0, 0, :keep].cpu().numpy(), stay)
 
 
+@pytest.mark.parametrize("cap", [640, 400000])
+def test_evict_keeps_protected_slots_among_nan_scores(kvc, q8, cap):
+    """More slots of NaN score than stay: sinks and recent slots stay all the same."""
+    block, d, keep, recent, sink = 32, 64, 200, 10, 3
+    src = kvc.q8_cache(1, 2, cap, d, block)
+    src["pos"].copy_(torch.arange(cap, device="cuda").expand(1, 2, cap))
+    src["acc"].copy_(torch.rand(1, 2, cap, device="cuda"))
+    src["acc"][..., ::2] = float("nan")
+    src["len"].fill_(cap - 1)
+    out = kvc.q8_cache(1, 2, 224, d, block)
+    idx = kvc.kv_evict_q8(src, keep, recent, out, sink=sink)
+    torch.cuda.synchronize()
+    for h in range(2):
+        got = idx[0, h].cpu().numpy()
+        assert (np.diff(got) > 0).all() and (out["len"] == keep).all()
+        np.testing.assert_array_equal(got[:sink], np.arange(sink))
+        np.testing.assert_array_equal(got[-recent:], np.arange(cap - 1 - recent, cap - 1))
+
+
+@pytest.mark.parametrize("levels", [1, 5000, 10 ** 9])
+def test_evict_unit_past_the_cluster(kvc, q8, levels):
+    """Units whose scores no cluster holds, with equal slots at the threshold and without."""
+    cap, keep, recent, sink = 400000, 150001, 1001, 4
+    src = kvc.q8_cache(1, 2, cap, 64, 64)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(6)
+    src["acc"].copy_((torch.rand(1, 2, cap, generator=g, device="cuda") * levels).floor())
+    src["pos"].copy_(torch.arange(cap, device="cuda").expand(1, 2, cap))
+    src["len"].copy_(torch.tensor([[cap, cap - 77]]))
+    out = kvc.q8_cache(1, 2, 150016, 64, 64)
+    idx = kvc.kv_evict_q8(src, keep, recent, out, sink=sink)
+    for h in range(2):
+        n = int(src["len"][0, h])
+        a, free = src["acc"][0, h].cpu().numpy(), np.arange(sink, n - recent)
+        stay = np.setdiff1d(np.arange(n), free[np.lexsort((free, a[free]))[:n - keep]])
+        np.testing.assert_array_equal(idx[0, h].cpu().numpy(), stay)
+        np.testing.assert_array_equal(out["pos"][0, h, :keep].cpu().numpy(), stay)
+    assert (out["len"] == keep).all()
+
+
 def test_evict_reports_bad_lengths(kvc):
     src = filled_cache(kvc, 1, 3, 64, 64, 32, BF, "s8", [65, 40, -3], 95)
     before = filled_cache(kvc, 1, 3, 32, 64, 32, BF, "s8", [1, 2, 3], 96)
