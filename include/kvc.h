@@ -486,7 +486,9 @@ KVC_API int kv_score_obs_noalloc(const void *Q_obs, const void *K, int B, int Hq
  *   dev_status device int, may be NULL; KV_ERR_INVALID_ARG when lengths or offsets
  *              are out of range or decrease (that sequence is left as it was),
  *              KV_ERR_TIMEOUT when a bounded device-side wait gave up; never cleared
- * K, V rows behind a sequence's last key are not used, whatever they hold.
+ * K, V rows behind a sequence's last key are not used, whatever they hold.  Inside a
+ * sequence a NaN in Q or K makes the rows that see it NaN; V is finite (weights of 0
+ * are multiplied with the V rows of up to 127 keys that a row does not see).
  * Preconditions: Hq % Hkv == 0, d in {64, 128}, scale not NaN.
  * bf16: products on the tensor cores (tcgen05, TMA) with fp32 accumulation, the
  * weights rounded to bf16 before the second product (scale <= 0 takes the fp32

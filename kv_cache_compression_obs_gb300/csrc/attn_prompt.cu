@@ -271,14 +271,14 @@ __global__ void __launch_bounds__(32 * Geo<D, SPLIT>::NW) attn_kernel(const T *_
   auto store_lse = [&](int r, float m, float z) {
     if (A.lse)
       A.lse[((long long)t.b * S.Hq + h) * S.Tq + t.q0 + t.r0 + r] =
-          z > 0.f ? (m + log2f(z)) * 0.6931471805599453f : -INFINITY;
+          z != 0.f ? (m + log2f(z)) * 0.6931471805599453f : -INFINITY;
   };
   if constexpr (!SPLIT) {
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
       const int r = r0 + g + 8 * half;
       if (r >= rows) continue;
-      const float z = half ? z1 : z0, inv = z > 0.f ? 1.f / z : 0.f;  // no key seen: 0
+      const float z = half ? z1 : z0, inv = z != 0.f ? 1.f / z : 0.f;  // no key seen: 0 (a NaN is passed on)
 #pragma unroll
       for (int c = 0; c < D / 32; ++c)
 #pragma unroll
@@ -315,12 +315,12 @@ __global__ void __launch_bounds__(32 * Geo<D, SPLIT>::NW) attn_kernel(const T *_
       float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
       for (int w = 0; w < NW; ++w) {
-        const float f = sz[w][r] > 0.f ? tc::ex2(sm[w][r] - M) : 0.f;  // a warp without a visible key
+        const float f = sz[w][r] != 0.f ? tc::ex2(sm[w][r] - M) : 0.f;  // a warp without a visible key
         const float4 x = *reinterpret_cast<const float4 *>(sX + w * Gm::TILE + r * D + col);
         Z += f * sz[w][r];
         y = make_float4(y.x + f * x.x, y.y + f * x.y, y.z + f * x.z, y.w + f * x.w);
       }
-      const float inv = Z > 0.f ? 1.f / Z : 0.f;
+      const float inv = Z != 0.f ? 1.f / Z : 0.f;
       store(r, col, make_float4(y.x * inv, y.y * inv, y.z * inv, y.w * inv));
       if (col == 0) store_lse(r, M, Z);
     }

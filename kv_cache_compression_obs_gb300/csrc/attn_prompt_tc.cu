@@ -604,8 +604,8 @@ __global__ void __launch_bounds__(NT, 1)
           }
         }
       } else if (w.rows[i] > 0) {
-        const float z = z2.x + z2.y;
-        const float inv = z > 0.f ? 1.f / z : 0.f;
+        const float z = z2.x + z2.y;  // 0: no key seen; a NaN is passed on
+        const float inv = z != 0.f ? 1.f / z : 0.f;
         const long long at = (long long)w.t.q0 + w.r0[i] + row;
         __nv_bfloat16 *dst = T.O + w.t.b * S.o[0] + w.h[i] * S.o[1] + at * S.o[2];
         const bool live = row < w.rows[i];
@@ -619,8 +619,8 @@ __global__ void __launch_bounds__(NT, 1)
           uint32_t p[16];
 #pragma unroll
           for (int x = 0; x < 16; ++x) {
-            const __nv_bfloat162 v = __floats2bfloat162_rn(z > 0.f ? __uint_as_float(o[2 * x]) * inv : 0.f,
-                                                           z > 0.f ? __uint_as_float(o[2 * x + 1]) * inv : 0.f);
+            const __nv_bfloat162 v = __floats2bfloat162_rn(z != 0.f ? __uint_as_float(o[2 * x]) * inv : 0.f,
+                                                           z != 0.f ? __uint_as_float(o[2 * x + 1]) * inv : 0.f);
             p[x] = *reinterpret_cast<const uint32_t *>(&v);
           }
           // every lane writes its own row: whole 32-byte sectors where they are aligned
@@ -635,7 +635,7 @@ __global__ void __launch_bounds__(NT, 1)
         }
         if (live && T.A.lse)
           T.A.lse[((long long)w.t.b * S.Hq + w.h[i]) * S.Tq + at] =
-              z > 0.f ? (m + log2f(z)) * 0.6931471805599453f : -INFINITY;
+              z != 0.f ? (m + log2f(z)) * 0.6931471805599453f : -INFINITY;
       }
       tc::fence_before_sync();
       __syncwarp();
@@ -680,13 +680,13 @@ __global__ void __launch_bounds__(NTJ) attn_join_kernel(const __grid_constant__ 
     for (int s = 0; s < kMaxSplits; ++s)
       if (s < T.splits) {
         st[s] = T.stat[s * step + at];
-        if (st[s].y > 0.f) M = fmaxf(M, st[s].x);
+        if (st[s].y != 0.f) M = fmaxf(M, st[s].x);
       }
     float z = 0.f;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
     for (int s = 0; s < kMaxSplits; ++s)
-      if (s < T.splits && st[s].y > 0.f) {  // a share without a visible key was not written
+      if (s < T.splits && st[s].y != 0.f) {  // a share without a visible key was not written
         const float f = tc::ex2(st[s].x - M);
         const float4 x = __ldcs(reinterpret_cast<const float4 *>(T.part + (s * step + at) * D) + lane);
         z += f * st[s].y;
@@ -695,11 +695,11 @@ __global__ void __launch_bounds__(NTJ) attn_join_kernel(const __grid_constant__ 
         o.z += f * x.z;
         o.w += f * x.w;
       }
-    const float inv = z > 0.f ? 1.f / z : 0.f;
+    const float inv = z != 0.f ? 1.f / z : 0.f;
     const __nv_bfloat162 a = __floats2bfloat162_rn(o.x * inv, o.y * inv), b = __floats2bfloat162_rn(o.z * inv, o.w * inv);
     *reinterpret_cast<uint2 *>(T.O + t.b * S.o[0] + h * S.o[1] + tok * S.o[2] + 4 * lane) =
         make_uint2(*reinterpret_cast<const uint32_t *>(&a), *reinterpret_cast<const uint32_t *>(&b));
-    if (T.A.lse && lane == 0) T.A.lse[at] = z > 0.f ? (M + log2f(z)) * 0.6931471805599453f : -INFINITY;
+    if (T.A.lse && lane == 0) T.A.lse[at] = z != 0.f ? (M + log2f(z)) * 0.6931471805599453f : -INFINITY;
   }
 }
 

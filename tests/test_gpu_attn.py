@@ -198,6 +198,26 @@ def test_garbage_between_packed_sequences(kvc, dtype):
 
 
 @pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("shape", [(2, 1, 40, 40, 128), (4, 2, 600, 600, 64), (32, 8, 500, 500, 128), (2, 1, 7, 5000, 128),
+                                   (3, 1, 300, 300, 128)], ids=str)
+def test_nan_reaches_the_rows_that_see_it_and_no_others(kvc, dtype, shape):
+    """A NaN query makes its row NaN, a NaN key the rows from its own on; the others keep their bits."""
+    Hq, Hkv, Tq, Tk, d = shape
+    Q, K, V = _rand((1, Hq, Tq, d), dtype, 1), _rand((1, Hkv, Tk, d), dtype, 2), _rand((1, Hkv, Tk, d), dtype, 3)
+    o, lse = kvc.kv_attn_prompt(Q, K, V)
+    Q2, K2 = Q.clone(), K.clone()
+    Q2[:, 1, 3] = float("nan")
+    K2[:, :, Tk - 2, 5] = float("nan")   # seen by the last two rows
+    o2, lse2 = kvc.kv_attn_prompt(Q2, K2, V)
+    torch.cuda.synchronize()
+    bad = torch.zeros((1, Hq, Tq), dtype=torch.bool, device="cuda")
+    bad[:, 1, 3] = True
+    bad[:, :, -2:] = True
+    assert o2[bad].isnan().all() and lse2[bad].isnan().all()
+    assert same_bits(o2[~bad], o[~bad]) and same_bits(lse2[~bad], lse[~bad])
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
 def test_bad_offsets_are_reported(kvc, dtype):
     q, k, v = (_rand((1, 2, 100, 64), dtype, s) for s in (1, 2, 3))
     out = torch.full_like(q, 5.0)
