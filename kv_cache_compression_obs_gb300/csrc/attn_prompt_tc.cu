@@ -25,6 +25,13 @@
 // Keys behind a sequence's end belong to another sequence or to nobody: S there is
 // replaced by -inf and the V rows are cleared in shared memory, so NaN in them
 // cannot reach the result.
+//
+// Bound by the tensor pipe and, in long calls, by power: 32768 tokens of 32/8 heads 5.28 ms,
+// 1650 TFLOP/s over the causal half (0.85 of the library's burst rate, 0.94 of what it
+// sustains); 8192 tokens 334 us with the tensor pipe active 71% of the time; 4096 tokens
+// 104 us, where an item's end and the next one's start (2.9 us) weigh more.  One set of
+// 128-row tiles per CTA left the tensor pipe idle during its softmax; two threads a row
+// (four warpgroups) spilled.
 #include <cmath>
 
 #include "attn_common.cuh"

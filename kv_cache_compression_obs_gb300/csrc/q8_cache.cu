@@ -12,6 +12,11 @@
 // CTA and its codes written from the registers.
 // The rows of the unfinished block are copied (evict: decoded where they were
 // codes, rounded to the cache's dtype, half a step at most).
+//
+// compact is bound by memory: a tenth of 32768 rows, 32 layers of 8 heads, 102 us, 0.95 of the
+// copy rate.  evict by arithmetic (nine instructions a code) and by the selection's barriers:
+// 64 units of 60000 to 65536 slots to 32768, 195 us for the move (0.82 of the copy rate) and
+// 37 us for the selection; 32 heads of 2048 slots 17 us, all latency.
 #include "pdl.cuh"
 #include "q8_common.cuh"
 #include "select_common.cuh"
