@@ -29,9 +29,9 @@
 // Bound by the tensor pipe and, in long calls, by power: 32768 tokens of 32/8 heads 5.28 ms,
 // 1650 TFLOP/s over the causal half (0.85 of the library's burst rate, 0.94 of what it
 // sustains); 8192 tokens 334 us with the tensor pipe active 71% of the time; 4096 tokens
-// 104 us, where an item's end and the next one's start (2.9 us) weigh more.  One set of
-// 128-row tiles per CTA left the tensor pipe idle during its softmax; two threads a row
-// (four warpgroups) spilled.
+// 104 us, where an item's end and the next one's start (2.9 us) weigh more.  Two threads a
+// row (four softmax warpgroups) spilled; O out of TMEM in one go instead of by 32 columns
+// changed nothing that could be measured.
 #include <cmath>
 
 #include "attn_common.cuh"
