@@ -29,7 +29,7 @@
 // Bound by the tensor pipe and, in long calls, by power: 32768 tokens of 32/8 heads 5.28 ms,
 // 1650 TFLOP/s over the causal half (0.85 of the library's burst rate, 0.94 of what it
 // sustains); 8192 tokens 334 us with the tensor pipe active 71% of the time; 4096 tokens
-// 104 us, where an item's end and the next one's start (2.9 us) weigh more.  Two threads a
+// 100 us, where an item's end and the next one's start (2.9 us) weigh more.  Two threads a
 // row (four softmax warpgroups) spilled; O out of TMEM in one go instead of by 32 columns
 // changed nothing that could be measured.
 #include <cmath>
@@ -45,6 +45,9 @@ constexpr int BM = 128, BN = 128;
 constexpr int NT = 384;
 constexpr int W_SOFTMAX = 8, W_MMA = 8, W_TMA = 9, W_SCHED = 11;  // warps 0-7: softmax, 10: V's ends
 constexpr int kMaxStages = 8;
+// The next item is asked for when the loads are this many key tiles from the end of the one at hand
+// (a layer of 4096 tokens: 0 tiles 103.3 us, 1 101.8, 2 100.9, 4 100.4, 6 100.8).
+constexpr int kClaimTiles = 4;
 constexpr int kCtrlBytes = 1024;
 constexpr float kLazy = 8.f;
 constexpr long long kWaitBudget = 4000000000LL;  // clock cycles (~2 s) before a wait gives up
@@ -329,8 +332,9 @@ __global__ void __launch_bounds__(NT, 1)
     if (warp == W_SCHED) {
       // ---- which work: the CTA's own index, then those of CTAs that have not started,
       // which the hardware hands over on request (in index order: long tiles first) ----
-      // A request goes out when the loads of the item at hand are all issued: early enough for
-      // the reply, late enough that a CTA with a long item does not sit on the next one.
+      // A request goes out when the loads of the item at hand are nearly all issued: early enough
+      // for the reply and the next item's first loads, late enough that a CTA with a long item does
+      // not sit on the next one.
       Work w = first_work;
       for (uint32_t k = 0;; ++k) {
         const bool ok = wait(C.wempty + (k & 1), (k >> 1) ^ 1);
@@ -367,7 +371,9 @@ __global__ void __launch_bounds__(NT, 1)
                 tma_load_4d(sQ + i * Gm::TILE + c * Gm::SUB, &tmQ, c * 64, w.t.q0 + w.r0[i], w.h[i], w.t.b, C.qfull + i);
               ++qn[i];
             }
+          const int ask = max(0, 2 * (w.nmax - kClaimTiles));
           for (int y = 0; y < 2 * w.nmax && ok; ++y) {
+            if (y == ask) tc::mbar_arrive(&C.want);
             const int st = x % ST;
             ok = wait(C.empty + st, (x / ST) ^ 1);
             if (!ok) break;
@@ -377,7 +383,7 @@ __global__ void __launch_bounds__(NT, 1)
                           w.t.b, C.full + st);
             ++x;
           }
-          tc::mbar_arrive(&C.want);
+          if (w.nmax == 0) tc::mbar_arrive(&C.want);
           tc::mbar_arrive(C.wempty + (k & 1));
         }
         // copies in flight land before the CTA may exit (at once unless it gave up)
