@@ -354,13 +354,28 @@ __global__ void __launch_bounds__(NT, 1)
           w.t.nq = -1;
       }
     } else if (warp == W_TMA) {
-      // ---- loads: Q_0, Q_1 and K_0 V_0 K_1 V_1 ... of every item through one ring ----
+      // ---- loads: K_0 V_0 K_1 V_1 ... of every item through one ring, Q_0 and Q_1 ----
       if (tc::elect_one()) {
         uint32_t x = 0, qn[2] = {0, 0};
         bool ok = true;
         for (uint32_t k = 0; ok && have_item(k); ++k) {
           const Work &w = C.work[k & 1];
           const int hk = w.h[0] / (S.Hq / S.Hkv);
+          const int ask = max(0, 2 * (w.nmax - kClaimTiles));
+          auto kv = [&](int y) {
+            if (y == ask) tc::mbar_arrive(&C.want);
+            const int st = x % ST;
+            if (!wait(C.empty + st, (x / ST) ^ 1)) return false;
+            tc::mbar_arrive_expect_tx(C.full + st, Gm::TILE);
+            for (int c = 0; c < Gm::NKB; ++c)
+              tma_load_4d(sKV + st * Gm::TILE + c * Gm::SUB, (y & 1) ? &tmV : &tmK, c * 64, w.t.k0 + (w.j0 + (y >> 1)) * BN, hk,
+                          w.t.b, C.full + st);
+            ++x;
+            return true;
+          };
+          // K_0 does not wait for Q's buffers; the loads behind Q wait until it has landed, as copies
+          // in flight together share the way and Q is what the next product needs.
+          if (w.nmax > 0) ok = kv(0);
 #pragma unroll
           for (int i = 0; i < 2; ++i)
             if (ok && w.n[i] > 0) {
@@ -371,18 +386,10 @@ __global__ void __launch_bounds__(NT, 1)
                 tma_load_4d(sQ + i * Gm::TILE + c * Gm::SUB, &tmQ, c * 64, w.t.q0 + w.r0[i], w.h[i], w.t.b, C.qfull + i);
               ++qn[i];
             }
-          const int ask = max(0, 2 * (w.nmax - kClaimTiles));
-          for (int y = 0; y < 2 * w.nmax && ok; ++y) {
-            if (y == ask) tc::mbar_arrive(&C.want);
-            const int st = x % ST;
-            ok = wait(C.empty + st, (x / ST) ^ 1);
-            if (!ok) break;
-            tc::mbar_arrive_expect_tx(C.full + st, Gm::TILE);
-            for (int c = 0; c < Gm::NKB; ++c)
-              tma_load_4d(sKV + st * Gm::TILE + c * Gm::SUB, (y & 1) ? &tmV : &tmK, c * 64, w.t.k0 + (w.j0 + (y >> 1)) * BN, hk,
-                          w.t.b, C.full + st);
-            ++x;
-          }
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            if (ok && w.n[i] > 0) ok = wait(C.qfull + i, qn[i] - 1);
+          for (int y = 1; y < 2 * w.nmax && ok; ++y) ok = kv(y);
           if (w.nmax == 0) tc::mbar_arrive(&C.want);
           tc::mbar_arrive(C.wempty + (k & 1));
         }
