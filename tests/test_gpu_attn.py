@@ -301,3 +301,21 @@ def test_captured_and_on_another_stream(kvc, dtype):
     o4, lse4 = kvc.kv_attn_prompt(q, k, v, seq_q=sq, seq_k=sk, packed=True)
     torch.cuda.synchronize()
     assert same_bits(o3, o4) and same_bits(lse3, lse4)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_offsets_past_32_bits(kvc, q8, dtype):
+    """A sequence at the end of tensors of more than 2^32 bytes."""
+    T, n, d, Hq = 2 ** 24, 300, 128, 2
+    q, k, v = _rand((1, Hq, n, d), dtype, 1), _rand((1, 1, n, d), dtype, 2), _rand((1, 1, n, d), dtype, 3)
+    Q, K, V = (torch.zeros((1, x.shape[1], T, d), dtype=dtype, device="cuda") for x in (q, k, v))
+    for x, y in ((Q, q), (K, k), (V, v)):
+        x[:, :, -n:] = y
+    off = torch.tensor([T - n, T], dtype=torch.int32, device="cuda")
+    out = torch.zeros_like(Q)
+    lse = torch.full((1, Hq, T), 5.0, device="cuda")
+    kvc.kv_attn_prompt(Q, K, V, seq_q=off, seq_k=off, packed=True, out=out, lse_out=lse)
+    torch.cuda.synchronize()
+    for h in range(Hq):
+        _check(q8, out[0, h, -n:], lse[0, h, -n:], q[0, h], k[0, 0], v[0, 0], d ** -0.5, h)
+    assert not out[:, :, :-n].any() and (lse[:, :, :-n] == 5).all()

@@ -510,3 +510,109 @@ def test_prompt_compress_decode_evict_together(kvc, q8, fmt):
         _check_evicted(q8, c, before, spare, idx, 90, 20, 1, fmt)
         c, spare = spare, c
     assert (c["len"] == 90).all()
+
+
+def _chain(kvc, K, V, s, idx, rows, c, spare, pos0, stream=None):
+    """Compaction, steps until a block has filled, eviction, one more step; returns the outputs."""
+    kvc.kv_compact_q8(K, V, s, idx, c, stream=stream)
+    out = [kvc.h2o_decode_step_q8(q, kn, vn, c, pos0 + i, stream=stream) for i, (q, kn, vn) in enumerate(rows[:-1])]
+    back = kvc.kv_evict_q8(c, 90, 20, spare, sink=1, stream=stream)
+    out.append(kvc.h2o_decode_step_q8(*rows[-1], spare, pos0 + len(rows), stream=stream))
+    return out + [back]
+
+
+@pytest.mark.parametrize("cap", [128, 32768])
+def test_chain_captured_and_on_two_streams(kvc, cap):
+    """The operators in one graph, replayed with other inputs, and two chains at once on streams of
+    their own: the bits of the eager calls.  Both decode paths (one launch, two launches)."""
+    B, Hkv, G, T, d, k = 1, 2, 4, 500, 64, 122
+    g = torch.Generator(device="cuda")
+
+    def inputs(seed):
+        g.manual_seed(seed)
+        K, V = (torch.randn(B, Hkv, T, d, generator=g, device="cuda").to(BF) for _ in range(2))
+        s = torch.rand(B, Hkv, T, generator=g, device="cuda")
+        idx = torch.rand(B, Hkv, T, generator=g, device="cuda").argsort(-1)[..., :k].sort(-1).values.int().contiguous()
+        return K, V, s, idx, [_step_inputs(B, Hkv, G, d, BF, 10 * seed + i) for i in range(7)]
+
+    def caches():
+        return [kvc.q8_cache(B, Hkv, cap, d, 64) for _ in range(2)]
+
+    want = []
+    for seed in (1, 2):
+        c = caches()
+        want.append((_chain(kvc, *inputs(seed), *c, T), c))
+    torch.cuda.synchronize()
+
+    def same(got, c, i):
+        torch.cuda.synchronize()
+        assert all(same_bits(a, b) for a, b in zip(got, want[i][0]))
+        assert all(same_bits(x[n], y[n]) for x, y in zip(c, want[i][1]) for n in x)
+
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    both = [(inputs(seed), caches()) for seed in (1, 2)]
+    torch.cuda.synchronize()
+    got = [_chain(kvc, *x, *c, T, stream=st) for (x, c), st in zip(both, streams)]
+    for i in range(2):
+        same(got[i], both[i][1], i)
+
+    x, c = inputs(1), caches()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y = _chain(kvc, *x, *c, T)
+    for i, seed in ((0, 1), (1, 2)):
+        new = inputs(seed)
+        for a, b in zip((*x[:4], *sum(x[4], [])), (*new[:4], *sum(new[4], []))):
+            a.copy_(b)
+        for z in c:
+            for t in z.values():
+                t.view(torch.uint8).zero_()
+        graph.replay()
+        same(y, c, i)
+
+
+def test_offsets_past_32_bits(kvc):
+    """Rows and slots whose byte and element offsets pass 2^32: a prompt's last rows into a cache, a
+    step that looks at a slot near the end of the last unit, whole blocks from there moved."""
+    H, T, d, block = 3, 2 ** 24, 128, 128
+    K = torch.zeros((1, H, T, d), dtype=BF, device="cuda")
+    V = torch.zeros((1, H, T, d), dtype=BF, device="cuda")
+    r = torch.randn(2, H, 200, d, device="cuda").to(BF)
+    K[0, :, -200:] = r[0]
+    V[0, :, -200:] = r[1]
+    small = kvc.q8_cache(1, H, 256, d, block)
+    idx = torch.arange(T - 200, T, dtype=torch.int32, device="cuda").expand(1, H, 200).contiguous()
+    kvc.kv_compact_q8(K, V, None, idx, small)
+    near = kvc.q8_cache(1, H, 256, d, block)
+    kvc.kv_compact_q8(r[0][None], r[1][None], None, None, near)
+    torch.cuda.synchronize()
+    assert all(same_bits(small[n], near[n]) for n in ("K", "V", "Ks", "Vs", "Kt", "Vt", "len"))
+    del K, V
+
+    c = kvc.q8_cache(1, H, T, d, block)
+    c["pos"].copy_(torch.arange(T, dtype=torch.int32, device="cuda").expand(1, H, T))
+    c["Ks"].fill_(1.0)
+    c["Vs"].fill_(1.0)
+    c["len"].fill_(T - 1)
+    at = T - 2 * block + 5
+    code = torch.randint(-127, 128, (H, d), device="cuda").to(torch.int8)
+    c["K"][0, :, at] = 1                     # <q, k> = 128 with q of ones: the other logits are 0
+    c["V"][0, :, at] = code
+    kt = torch.zeros(1, H, d, device="cuda", dtype=BF)
+    o = kvc.h2o_decode_step_q8(torch.ones(1, H, d, device="cuda", dtype=BF), kt, kt, c, T, scale=0.5)
+    torch.cuda.synchronize()
+    # its weight is 1 / (1 + 2^24 e^-64) = 1 to 2^-68; the error is that of a weight, 2 dl + 2^-18 with
+    # dl = 2^-18 64
+    assert ((o[0] - code).abs() <= code.abs() * (2.0 ** -11 + 2.0 ** -18)).all()
+    assert (c["len"] == T).all() and ((c["acc"][0, :, at] - 1).abs() <= 2.0 ** -10).all()
+
+    # the last four blocks and nothing else among the recent slots: whole blocks, moved as they are
+    c["acc"].zero_()
+    c["acc"][0, :, -4 * block:-2 * block] = 1.0
+    c["K"][0, :, -4 * block:] = torch.randint(-127, 128, (H, 4 * block, d), device="cuda").to(torch.int8)
+    out = kvc.q8_cache(1, H, 4 * block, d, block)
+    back = kvc.kv_evict_q8(c, 4 * block, 2 * block, out)
+    torch.cuda.synchronize()
+    assert torch.equal(back[0], torch.arange(T - 4 * block, T, dtype=torch.int32, device="cuda").expand(H, -1))
+    for n in ("K", "V"):
+        assert same_bits(out[n][0], c[n][0, :, -4 * block:]) and same_bits(out[n + "s"][0], c[n + "s"][0, :, -4:])
