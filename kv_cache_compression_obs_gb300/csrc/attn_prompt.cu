@@ -11,7 +11,10 @@
 // and lo's own bits past its 11 are dropped.  On the CUDA cores the same tiles were bound by
 // shared memory: a 16-byte load takes four cycles whatever it shares, and a thread's few
 // results do not pay for its operands (4 heads of 512 tokens
-// 26.7 us; here 11.8 us, and 59 TFLOP/s over 4096 tokens of 32/8 heads).
+// 26.7 us; here 11.6 us, and 55 TFLOP/s over 4096 tokens of 32/8 heads).  With one running sum
+// for everything, which the unit cuts off at every step, 4000 tokens were off by 4e-6 of the
+// output's norm and ran at 59; with sums of their own for the small products and for each tile
+// they are off by 4.6e-7, where fp32 matrix products are off by 5.6e-7.
 //
 // A warp holds 16 query rows.  Which element of d (or which key) stands at which k is free as
 // long as both operands agree: a lane takes 16 consecutive bytes of a K row for two k steps,
@@ -62,11 +65,14 @@ __device__ __forceinline__ void mma1688(float (&c)[4], uint32_t a0, uint32_t a1,
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-// c += a b to fp32 accuracy
-__device__ __forceinline__ void mma_split(float (&c)[4], const Split (&a)[4], const Split &b0, const Split &b1) {
-  mma1688(c, a[0].lo, a[1].lo, a[2].lo, a[3].lo, b0.hi, b1.hi);
-  mma1688(c, a[0].hi, a[1].hi, a[2].hi, a[3].hi, b0.lo, b1.lo);
+// c + small += a b to fp32 accuracy.  The unit cuts its sums off rather than rounding them: the
+// two small products have a sum of their own, so that only the large one's steps are cut at
+// the sum's own size.
+__device__ __forceinline__ void mma_split(float (&c)[4], float (&small)[4], const Split (&a)[4], const Split &b0,
+                                          const Split &b1) {
+  mma1688(small, a[0].lo, a[1].lo, a[2].lo, a[3].lo, b0.hi, b1.hi);
   mma1688(c, a[0].hi, a[1].hi, a[2].hi, a[3].hi, b0.hi, b1.hi);
+  mma1688(small, a[0].hi, a[1].hi, a[2].hi, a[3].hi, b0.lo, b1.lo);
 }
 
 template <typename T, int D, int SPLIT>
@@ -160,11 +166,11 @@ __global__ void __launch_bounds__(32 * Geo<D, SPLIT>::NW) attn_kernel(const T *_
     const float *sV = sK + BN * LK;
     const int j0 = j * BN;
     if (j0 < wend) {
-      float s[BN / 8][4];
+      float s[BN / 8][4], sl[BN / 8][4];
 #pragma unroll
       for (int n = 0; n < BN / 8; ++n)
 #pragma unroll
-        for (int x = 0; x < 4; ++x) s[n][x] = 0.f;
+        for (int x = 0; x < 4; ++x) s[n][x] = sl[n][x] = 0.f;
 #pragma unroll
       for (int c = 0; c < D / 16; ++c) {  // two k steps
         const float4 qa = *reinterpret_cast<const float4 *>(mq + g * LK + c * 16 + t4 * 4);
@@ -186,8 +192,8 @@ __global__ void __launch_bounds__(32 * Geo<D, SPLIT>::NW) attn_kernel(const T *_
           b[1].set(kb.y);
           b[2].set(kb.z);
           b[3].set(kb.w);
-          mma_split(s[n], a[0], b[0], b[1]);
-          mma_split(s[n], a[1], b[2], b[3]);
+          mma_split(s[n], sl[n], a[0], b[0], b[1]);
+          mma_split(s[n], sl[n], a[1], b[2], b[3]);
         }
       }
       // logits of keys j0 + 8 n + 2 t4 (+ 1)
@@ -198,8 +204,8 @@ __global__ void __launch_bounds__(32 * Geo<D, SPLIT>::NW) attn_kernel(const T *_
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
           const int key = j0 + n * 8 + 2 * t4 + x;
-          s[n][x] = part && key > lim0 ? -INFINITY : s[n][x] * A.c_log2;
-          s[n][2 + x] = part && key > lim1 ? -INFINITY : s[n][2 + x] * A.c_log2;
+          s[n][x] = part && key > lim0 ? -INFINITY : (s[n][x] + sl[n][x]) * A.c_log2;
+          s[n][2 + x] = part && key > lim1 ? -INFINITY : (s[n][2 + x] + sl[n][2 + x]) * A.c_log2;
           x0 = fmaxf(x0, s[n][x]);
           x1 = fmaxf(x1, s[n][2 + x]);
         }
@@ -223,19 +229,29 @@ __global__ void __launch_bounds__(32 * Geo<D, SPLIT>::NW) attn_kernel(const T *_
         }
       }
       const float b0 = m0 == -INFINITY ? 0.f : m0, b1 = m1 == -INFINITY ? 0.f : m1;  // no key seen yet
+      Split a[BN / 8][4];  // rows g, g + 8 against keys 2 t4, 2 t4 + 1: columns t4 and t4 + 4
 #pragma unroll
       for (int n = 0; n < BN / 8; ++n) {
-        Split a[4];  // rows g, g + 8 against keys 2 t4, 2 t4 + 1: columns t4 and t4 + 4
         const float p0 = tc::ex2(s[n][0] - b0), p1 = tc::ex2(s[n][1] - b0);
         const float p2 = tc::ex2(s[n][2] - b1), p3 = tc::ex2(s[n][3] - b1);
         z0 += p0 + p1;
         z1 += p2 + p3;
-        a[0].set(p0);
-        a[1].set(p2);
-        a[2].set(p1);
-        a[3].set(p3);
+        a[n][0].set(p0);
+        a[n][1].set(p2);
+        a[n][2].set(p1);
+        a[n][3].set(p3);
+      }
+      // a tile's sums start at 0 and join O by an addition that rounds: O's error does not
+      // grow with every step that the unit cuts off
 #pragma unroll
-        for (int c = 0; c < D / 32; ++c) {
+      for (int c = 0; c < D / 32; ++c) {
+        float y[4][4], yl[4][4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int x = 0; x < 4; ++x) y[i][x] = yl[i][x] = 0.f;
+#pragma unroll
+        for (int n = 0; n < BN / 8; ++n) {
           const float4 va = *reinterpret_cast<const float4 *>(sV + (n * 8 + 2 * t4) * LV + c * 32 + g * 4);
           const float4 vb = *reinterpret_cast<const float4 *>(sV + (n * 8 + 2 * t4 + 1) * LV + c * 32 + g * 4);
           const float xa[4] = {va.x, va.y, va.z, va.w}, xb[4] = {vb.x, vb.y, vb.z, vb.w};
@@ -244,9 +260,13 @@ __global__ void __launch_bounds__(32 * Geo<D, SPLIT>::NW) attn_kernel(const T *_
             Split ba, bb;
             ba.set(xa[i]);
             bb.set(xb[i]);
-            mma_split(o[c * 4 + i], a, ba, bb);
+            mma_split(y[i], yl[i], a[n], ba, bb);
           }
         }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int x = 0; x < 4; ++x) o[c * 4 + i][x] += y[i][x] + yl[i][x];
       }
     }
     if (SPLIT) __syncwarp();  // the buffer has been read

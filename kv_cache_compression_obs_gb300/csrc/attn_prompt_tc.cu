@@ -26,10 +26,10 @@
 // replaced by -inf and the V rows are cleared in shared memory, so NaN in them
 // cannot reach the result.
 //
-// Bound by the tensor pipe and, in long calls, by power: 32768 tokens of 32/8 heads 5.28 ms,
-// 1650 TFLOP/s over the causal half (0.85 of the library's burst rate, 0.94 of what it
+// Bound by the tensor pipe and, in long calls, by power: 32768 tokens of 32/8 heads 5.20 ms,
+// 1690 TFLOP/s over the causal half (0.87 of the library's burst rate, 0.97 of what it
 // sustains); 8192 tokens 334 us with the tensor pipe active 71% of the time; 4096 tokens
-// 100 us, where an item's end and the next one's start (2.9 us) weigh more.  Two threads a
+// 100 us, where an item's end and the next one's start (2 to 3 us) weigh more.  Two threads a
 // row (four softmax warpgroups) spilled; O out of TMEM in one go instead of by 32 columns
 // changed nothing that could be measured.
 #include <cmath>

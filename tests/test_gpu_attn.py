@@ -267,6 +267,22 @@ def test_odd_scales(kvc, q8, dtype, scale, shape):
         within(np64(lse[0, h]), wl, dl + 2.0 ** -20 + 2.0 ** -22 * np.abs(wl), f"lse {h}")
 
 
+@pytest.mark.parametrize("shape", [(4, 512, 512, 64), (2, 4000, 4000, 128), (2, 500, 20000, 128)], ids=str)
+def test_fp32_error_of_the_whole_output(kvc, shape):
+    """The error in norm stays that of fp32 sums.  A logit of unit size gathers at most d / 8 = 16 cut
+    sums of 2^-23 (half of that on average, of partial sums that are smaller): 2^-20.  A tile's share
+    of O has four such steps, and the shares are added with roundings that average out.  Sums cut
+    at every step over all keys would be off by (keys / 8) 2^-24, 2^-17 at 1000 keys already."""
+    H, Tq, Tk, d = shape
+    Q, K, V = _rand((1, H, Tq, d), F32, 1), _rand((1, H, Tk, d), F32, 2), _rand((1, H, Tk, d), F32, 3)
+    o, _ = kvc.kv_attn_prompt(Q, K, V)
+    hidden = ~torch.ones((Tq, Tk), dtype=torch.bool, device="cuda").tril(Tk - Tq)
+    for h in range(H):
+        w = (Q[0, h].double() @ K[0, h].double().T * d ** -0.5).masked_fill(hidden, float("-inf")).softmax(-1)
+        want = w @ V[0, h].double()
+        assert (o[0, h].double() - want).norm() <= 2.0 ** -20 * want.norm()
+
+
 def test_long_rows(kvc, q8):
     """A long sequence, some rows of it (the first, the last, around tile borders)."""
     T, d = 9001, 128
