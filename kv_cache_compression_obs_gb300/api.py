@@ -479,7 +479,8 @@ def kv_attn_prompt(Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, scale: flo
     sequences (None: Tq, Tk); with it the offsets [n + 1] of n sequences packed along
     the token axis of the one batch row.  Rows of no sequence are left as they were
     in `out` and `lse_out` (and undefined in tensors made here).  `out` made here has
-    Q's memory order."""
+    Q's memory order.  V must be finite inside a sequence (a row may multiply V rows of keys that
+    it does not see by 0); what stands behind a sequence is not used."""
     B, Hq, Tq, d = Q.shape
     B2, Hkv, Tk, d2 = K.shape
     dt = Q.dtype
@@ -653,6 +654,8 @@ def compress_prefill_q8(Q, K, V, W: int, k: int, recent: int, r: float | None, c
 
     Returns (o, lse, cache); cache has `cap` slots (default: k rounded up to whole blocks)."""
     T = K.shape[2]
+    if Q.shape[2] != T or not 1 <= W <= T:
+        raise ValueError("Q must hold the prompt's T queries and W be 1 to T of them")
     with _side(stream):
         o, lse = kv_attn_prompt(Q, K, V, scale)
         s = kv_score_obs(Q[:, :, T - W:].contiguous(), K, scale)

@@ -142,3 +142,12 @@ def test_binding_checks_shapes(api):
         api.kv_evict_q8(dict(c, acc=None), 10, 2, c)
     with pytest.raises(ValueError):
         api.h2o_decode_step_q8(x[:, :, 0], x[:, :, 0], x[:, :, 0], dict(c, pos=c["acc"]), 5)
+
+
+@pytest.mark.parametrize("tq,W", [(10, 0), (10, 11), (9, 4)])
+def test_binding_checks_the_observed_queries(api, tq, W):
+    """More observed queries than the prompt has would be fewer, without a word."""
+    import torch
+    kv = torch.zeros(1, 2, 10, 64)
+    with pytest.raises(ValueError):
+        api.compress_prefill_q8(torch.zeros(1, 4, tq, 64), kv, kv, W=W, k=4, recent=2, r=None)
