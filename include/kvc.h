@@ -107,7 +107,9 @@ typedef enum { KV_Q8_S8 = 0, KV_Q8_E4M3 = 1 } kv_q8_format;
  * whole blocks of `block` slots are codes with one float32 scale a per block and
  * head for K and one for V (the value of a code c is c a):
  *     a = max(max|x| / top, 2^-126) over the block, c = round-to-even(x (1 / a)),
- * top = 127 or 448, each step one float32 operation.  The rows of the last,
+ * top = 127 or 448, each step one float32 operation.  A block with a NaN or an
+ * infinity has a = NaN: every value that it stands for is NaN, and so is every block
+ * that kv_evict_q8 mixes its rows into.  The rows of the last,
  * unfinished block (len % block of them) stay in the model's dtype in Kt, Vt; a
  * block is quantised once, when it becomes full.
  */

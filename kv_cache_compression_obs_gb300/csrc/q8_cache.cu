@@ -85,8 +85,8 @@ struct Piece {
       for (int i = 0; i < 8; ++i) x[i] = make_float2(y[2 * i], y[2 * i + 1]);
     }
   }
-  // the largest magnitude of a piece of rows
-  __device__ __forceinline__ float big() const {
+  // the bits of the largest magnitude of a piece of rows
+  __device__ __forceinline__ uint32_t big() const {
     if constexpr (sizeof(T) == 2) {  // without the sign bf16 bits order like their values
       uint32_t m = 0;
 #pragma unroll
@@ -94,13 +94,13 @@ struct Piece {
         m = __vimax3_u16x2(m, v[i].x & 0x7FFF7FFFu, v[i].y & 0x7FFF7FFFu);
         m = __vimax3_u16x2(m, v[i].z & 0x7FFF7FFFu, v[i].w & 0x7FFF7FFFu);
       }
-      return __uint_as_float(max(m & 0xFFFFu, m >> 16) << 16);
+      return max(m & 0xFFFFu, m >> 16) << 16;
     } else {
-      float m = 0.f;
+      uint32_t m = 0;
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        m = fmaxf(fmaxf(m, fabsf(__uint_as_float(v[i].x))), fabsf(__uint_as_float(v[i].y)));
-        m = fmaxf(fmaxf(m, fabsf(__uint_as_float(v[i].z))), fabsf(__uint_as_float(v[i].w)));
+        m = __vimax3_u32(m, v[i].x & 0x7FFFFFFFu, v[i].y & 0x7FFFFFFFu);
+        m = __vimax3_u32(m, v[i].z & 0x7FFFFFFFu, v[i].w & 0x7FFFFFFFu);
       }
       return m;
     }
@@ -110,22 +110,20 @@ struct Piece {
 // The block's two scales and its codes, `bytes` of them for K and for V, from pieces of rows.
 template <typename T, int FMT, int N>
 __device__ __forceinline__ void quantise(const Piece<T> (&p)[2][N], const int (&at)[N], int bytes,
-                                         uint8_t *const (&co)[2], float *const (&so)[2], float (&red)[2][16]) {
+                                         uint8_t *const (&co)[2], float *const (&so)[2], uint32_t (&red)[2][16]) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 #pragma unroll
   for (int kv = 0; kv < 2; ++kv) {
-    float big = 0.f;
+    uint32_t big = 0;
 #pragma unroll
-    for (int i = 0; i < N; ++i) big = fmaxf(big, p[kv][i].big());
-    // magnitudes order like their bits
-    const unsigned m = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(big));
-    if (lane == 0) red[kv][warp] = __uint_as_float(m);
+    for (int i = 0; i < N; ++i) big = max(big, p[kv][i].big());
+    big = __reduce_max_sync(0xFFFFFFFFu, big);
+    if (lane == 0) red[kv][warp] = big;
   }
   __syncthreads();
 #pragma unroll
   for (int kv = 0; kv < 2; ++kv) {
-    const float v = lane < (int)blockDim.x >> 5 ? red[kv][lane] : 0.f;
-    const float m = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(v)));
+    const uint32_t m = __reduce_max_sync(0xFFFFFFFFu, lane < (int)blockDim.x >> 5 ? red[kv][lane] : 0u);
     const float a = q8_scale<FMT>(m), inv = __fdiv_rn(1.f, a);
 #pragma unroll
     for (int i = 0; i < N; ++i) {
@@ -144,7 +142,7 @@ constexpr int kCompactPieces = 2;  // of K and of V per thread, all loads in fli
 template <typename T, int FMT>
 __global__ void __launch_bounds__(512) compact_block_kernel(const __grid_constant__ BlockArgs A) {
   constexpr int PP = kCompactPieces;
-  __shared__ float red[2][16];
+  __shared__ uint32_t red[2][16];
   __shared__ int src[128];
   pdl_wait();
   pdl_launch();
@@ -217,7 +215,7 @@ __device__ __forceinline__ void copy16_async(void *dst, const void *src) {
 // so each piece is read twice (magnitude, then code) rather than held in registers.
 template <typename T, int FMT>
 __device__ __forceinline__ void move_last_block(const BlockArgs &A, int u, int b, int rows, int nf, const int *src,
-                                                const float2 *skv, float (&red)[2][16]) {
+                                                const float2 *skv, uint32_t (&red)[2][16]) {
   const int block = A.out.block, d = A.out.d, bl = A.b_log2, bytes = rows << A.d_log2;
   const long src0 = (long)u * A.from.cap, to = (long)u * A.out.cap + ((long)b << bl);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -251,18 +249,18 @@ __device__ __forceinline__ void move_last_block(const BlockArgs &A, int u, int b
       }
       continue;
     }
-    float big = 0.f;
+    uint32_t big = 0;
 #pragma unroll 1
     for (int at = threadIdx.x << 4; at < bytes; at += blockDim.x << 4) {
       piece(at, x);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) big = fmaxf(big, fmaxf(fabsf(x[e].x), fabsf(x[e].y)));
+      for (int e = 0; e < 8; ++e) big = __vimax3_u32(big, mag(x[e].x), mag(x[e].y));
     }
-    const unsigned m = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(big));
-    if (lane == 0) red[kv][warp] = __uint_as_float(m);
+    big = __reduce_max_sync(0xFFFFFFFFu, big);
+    if (lane == 0) red[kv][warp] = big;
     __syncthreads();
-    float v = red[kv][0];
-    for (int w = 1; w < (int)blockDim.x >> 5; ++w) v = fmaxf(v, red[kv][w]);
+    uint32_t v = red[kv][0];
+    for (int w = 1; w < (int)blockDim.x >> 5; ++w) v = max(v, red[kv][w]);
     const float a = q8_scale<FMT>(v), inv = __fdiv_rn(1.f, a);
     uint8_t *const co = static_cast<uint8_t *>(kv ? A.out.V : A.out.K) + (to << A.d_log2);
 #pragma unroll 1
@@ -279,7 +277,7 @@ template <typename T, int FMT, int NTM, int SQ, int ST>
 __global__ void __launch_bounds__(NTM, 1024 / NTM) evict_move_kernel(const __grid_constant__ BlockArgs A, int runs, int run_blocks) {
   constexpr int BYTES = NTM * SQ * 16;  // codes of a block of K or V
   extern __shared__ __align__(16) unsigned char ring[];  // ST stages of K codes, V codes
-  __shared__ float red[2][2][16];
+  __shared__ uint32_t red[2][2][16];
   __shared__ int src[kRunRows];
   __shared__ float2 skv[kRunRows];  // the rows' scales
   pdl_wait();
@@ -307,10 +305,10 @@ __global__ void __launch_bounds__(NTM, 1024 / NTM) evict_move_kernel(const __gri
     }
   }
   const int nring = __reduce_max_sync(0xFFFFFFFFu, coded);
-  if ((threadIdx.x & 31) == 0) red[0][0][threadIdx.x >> 5] = __int_as_float(nring);
+  if ((threadIdx.x & 31) == 0) red[0][0][threadIdx.x >> 5] = (uint32_t)nring;
   __syncthreads();
   int most = 0;
-  for (int w = 0; w < NTM / 32; ++w) most = max(most, __float_as_int(red[0][0][w]));
+  for (int w = 0; w < NTM / 32; ++w) most = max(most, (int)red[0][0][w]);
   const int ring_blocks = most >> bl;  // blocks of codes alone go through the ring
   __syncthreads();
   // this thread's pieces: the same place in every block
@@ -378,25 +376,24 @@ __global__ void __launch_bounds__(NTM, 1024 / NTM) evict_move_kernel(const __gri
       continue;
     }
     // rounding c a to fp32 keeps the order: a piece's largest code gives its largest value
-    float bk = 0.f, bv = 0.f;
+    // (NaN with a NaN scale, whatever the code)
+    uint32_t bk = 0, bv = 0;
 #pragma unroll
     for (int q = 0; q < SQ; ++q) {
-      bk = fmaxf(bk, __fmul_rn(Q8<FMT>::big16(k[q]), a[q].x));
-      bv = fmaxf(bv, __fmul_rn(Q8<FMT>::big16(v[q]), a[q].y));
+      bk = max(bk, mag(__fmul_rn(Q8<FMT>::big16(k[q]), a[q].x)));
+      bv = max(bv, mag(__fmul_rn(Q8<FMT>::big16(v[q]), a[q].y)));
     }
-    // magnitudes order like their bits
-    const unsigned mk = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(bk));
-    const unsigned mv = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(bv));
+    const uint32_t mk = __reduce_max_sync(0xFFFFFFFFu, bk), mv = __reduce_max_sync(0xFFFFFFFFu, bv);
     // Two buffers in turn over the blocks that get here, each with a barrier (a whole block
     // has none): who writes a buffer again knows that everybody has read it.
-    float (&rd)[2][16] = red[turn];
+    uint32_t (&rd)[2][16] = red[turn];
     turn ^= 1;
-    if (lane < 2) rd[lane][warp] = __uint_as_float(lane ? mv : mk);
+    if (lane < 2) rd[lane][warp] = lane ? mv : mk;
     __syncthreads();
     // the lower half of a warp finds K's scale, the upper half V's
-    float big = (lane & 15) < NTM / 32 ? rd[lane >> 4][lane & 15] : 0.f;
+    uint32_t big = (lane & 15) < NTM / 32 ? rd[lane >> 4][lane & 15] : 0u;
 #pragma unroll
-    for (int o = 8; o; o >>= 1) big = fmaxf(big, __shfl_xor_sync(0xFFFFFFFFu, big, o));
+    for (int o = 8; o; o >>= 1) big = max(big, __shfl_xor_sync(0xFFFFFFFFu, big, o));
     const float mine = q8_scale<FMT>(big), minv = __fdiv_rn(1.f, mine);
     const float ik = __shfl_sync(0xFFFFFFFFu, minv, 0), iv = __shfl_sync(0xFFFFFFFFu, minv, 16);
     if (warp == 0 && (lane & 15) == 0) (lane ? sov : sok)[i] = mine;

@@ -7,6 +7,9 @@
 // each step one fp32 operation rounded to nearest (the floor keeps 1 / a finite
 // for blocks of zeros and subnormals).  |x - c a| is then at most half a code step
 // (int8: a / 2; e4m3: 2^-4 |x|, or half its smallest step 2^-10 a) up to fp32 rounding.
+// A block with a NaN or an infinity has the scale NaN, so that all its values are NaN and stay
+// it when its rows move: magnitudes are searched as bits, which order a NaN above every number
+// where fmaxf would drop it.
 #pragma once
 
 #include <cuda_fp8.h>
@@ -28,7 +31,7 @@ template <int FMT> struct Q8;
 template <> struct Q8<KV_Q8_S8> {
   static constexpr float kTop = 127.f;
   __device__ __forceinline__ static uint32_t low(float y) { return __float_as_uint(__fadd_rn(y, 12582912.f)); }
-  // |y| <= 127 (1 + 2^-22): no code passes 127
+  // |y| <= 127 (1 + 2^-22): no code passes 127 (with a NaN scale a code is any byte)
   __device__ __forceinline__ static uint32_t pack4(float2 a, float2 b) {
     return __byte_perm(__byte_perm(low(a.x), low(a.y), 0x0040), __byte_perm(low(b.x), low(b.y), 0x0040), 0x5410);
   }
@@ -80,10 +83,14 @@ template <> struct Q8<KV_Q8_E4M3> {
   }
 };
 
-// The scale of a block whose largest magnitude is `big`.
+// |x| as bits: they order like the values, a NaN above infinity.
+__device__ __forceinline__ uint32_t mag(float x) { return __float_as_uint(x) & 0x7FFFFFFFu; }
+
+// The scale of a block whose largest magnitude has the bits `big`; NaN when that is not finite.
 template <int FMT>
-__device__ __forceinline__ float q8_scale(float big) {
-  return fmaxf(__fdiv_rn(big, Q8<FMT>::kTop), FLT_MIN);
+__device__ __forceinline__ float q8_scale(uint32_t big) {
+  return big < 0x7F800000u ? fmaxf(__fdiv_rn(__uint_as_float(big), Q8<FMT>::kTop), FLT_MIN)
+                           : __uint_as_float(0x7FFFFFFFu);
 }
 
 // 16 values as one vector of codes; inv = 1 / scale.
@@ -144,24 +151,20 @@ __device__ __forceinline__ void store16(float *p, const float (&x)[16]) {
   for (int i = 0; i < 4; ++i)
     reinterpret_cast<float4 *>(p)[i] = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
 }
-__device__ __forceinline__ float max_abs16(const float (&x)[16]) {
-  float m = 0.f;
+__device__ __forceinline__ uint32_t max_mag16(const float (&x)[16]) {
+  uint32_t m = 0;
 #pragma unroll
-  for (int i = 0; i < 16; ++i) m = fmaxf(m, fabsf(x[i]));
+  for (int i = 0; i < 16; ++i) m = max(m, mag(x[i]));
   return m;
 }
 
-// Largest v of the block (blockDim.x a multiple of 32, at most 1024); sm: 32 floats.
-__device__ __forceinline__ float block_max(float v, float *sm) {
-#pragma unroll
-  for (int o = 16; o; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
+// Largest v of the block (blockDim.x a multiple of 32, at most 1024); sm: 32 words.
+__device__ __forceinline__ uint32_t block_max(uint32_t v, uint32_t *sm) {
+  v = __reduce_max_sync(0xFFFFFFFFu, v);
   if ((threadIdx.x & 31) == 0) sm[threadIdx.x >> 5] = v;
   __syncthreads();
   const int nw = blockDim.x >> 5, lane = threadIdx.x & 31;
-  float m = lane < nw ? sm[lane] : 0.f;
-#pragma unroll
-  for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-  return m;
+  return __reduce_max_sync(0xFFFFFFFFu, lane < nw ? sm[lane] : 0u);
 }
 
 }  // namespace kvc

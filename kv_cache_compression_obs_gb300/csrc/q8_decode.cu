@@ -308,15 +308,15 @@ __device__ __forceinline__ void stream_range(const DecArgs &A, long u, int k0, i
     const int qi = st * 4 + (g >> 1);
     const T *q = static_cast<const T *>(A.q) + (u * G + min(qi, G - 1)) * (long)D;
     float x[NCH][16];
-    float big = 0.f;
+    uint32_t big = 0;
 #pragma unroll
     for (int c = 0; c < NCH; ++c) {
       load16(q + c * 64 + t * 16, x[c]);
-      big = fmaxf(big, max_abs16(x[c]));
+      big = max(big, max_mag16(x[c]));
     }
-    big = fmaxf(big, __shfl_xor_sync(0xFFFFFFFFu, big, 1));
-    big = fmaxf(big, __shfl_xor_sync(0xFFFFFFFFu, big, 2));
-    const int sh = query_shift(big);
+    big = max(big, __shfl_xor_sync(0xFFFFFFFFu, big, 1));
+    big = max(big, __shfl_xor_sync(0xFFFFFFFFu, big, 2));
+    const int sh = query_shift(__uint_as_float(big));
     const float f = exp2i(sh);
     // query t's shift sits in the lanes with g = 2t
     qf[st] = A.c_log2 * exp2i(-__shfl_sync(0xFFFFFFFFu, sh, 8 * t));
@@ -492,7 +492,7 @@ __global__ void __launch_bounds__(NT, NSET == 1 || D == 64 ? 4 : 3) q8_stream_ke
 
 // ---- quantising the block that the new token fills -------------------------------------------
 template <typename T, int FMT>
-__device__ __forceinline__ void quantise_tail(const DecArgs &A, long u, int n, int kv, float *red) {
+__device__ __forceinline__ void quantise_tail(const DecArgs &A, long u, int n, int kv, uint32_t *red) {
   const int D = A.c.d, block = A.c.block, nf = n >> A.b_log2 << A.b_log2;
   const T *rows = static_cast<const T *>(kv ? A.c.Vt : A.c.Kt) + u * (long)block * D;
   // the new token's row as it came in: its copy in the cache may be this kernel's own
@@ -500,11 +500,11 @@ __device__ __forceinline__ void quantise_tail(const DecArgs &A, long u, int n, i
   uint4 *to = reinterpret_cast<uint4 *>(static_cast<uint8_t *>(kv ? A.c.V : A.c.K) + (u * (long)A.c.cap + nf) * D);
   const int pieces = block * D / 16, old = (block - 1) * D / 16;
   auto load = [&](int i, float (&x)[16]) { load16(i < old ? rows + (long)i * 16 : fresh + (i - old) * 16, x); };
-  float big = 0.f;
+  uint32_t big = 0;
   for (int i = threadIdx.x; i < pieces; i += blockDim.x) {
     float x[16];
     load(i, x);
-    big = fmaxf(big, max_abs16(x));
+    big = max(big, max_mag16(x));
   }
   const float a = q8_scale<FMT>(block_max(big, red));
   const float inv = __fdiv_rn(1.f, a);
@@ -530,7 +530,7 @@ __global__ void __launch_bounds__(NT, NSET == 1 || D == 64 ? 4 : 3)
   __shared__ float2 mz[2][8];       // this CTA's shares: slots, unfinished block
   __shared__ float2 all[9][8];      // everybody's
   __shared__ float sM[8], sI[8];
-  __shared__ float red[32];
+  __shared__ uint32_t red[32];
   extern __shared__ __align__(16) float dyn[];
   const int G = A.G;
   float *so = dyn;                  // [NW][G][D]
@@ -662,7 +662,7 @@ __global__ void __launch_bounds__(NTF) q8_finalize_kernel(const __grid_constant_
   __shared__ float sM[8], sI[8];           // the unit's maximum and 1 / normaliser
   __shared__ float sF[8][kMaxSplits + 1];  // the splits' factors
   __shared__ float4 sO[NTF / 32][32];
-  __shared__ float red[32];
+  __shared__ uint32_t red[32];
   pdl_wait();
   pdl_launch();
   const int G = A.G, D = A.c.d, block = A.c.block, cap = A.c.cap;
