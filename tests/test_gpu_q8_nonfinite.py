@@ -169,3 +169,22 @@ def test_evict_whole_block_and_unfinished_rows(kvc, fmt):
     assert out["Vs"][0, 1, 3].isnan() and out["Vs"][0, 1, 4].isnan() == (nf > 4)
     at = int((idx[0, 2] == 5 * block + 1).nonzero())
     assert not out["Kt"][0, 2, at % block, 3].isfinite() if at >= nf * block else out["Ks"][0, 2, at // block].isnan()
+
+
+@FORMATS
+@pytest.mark.parametrize("cap,n", [(1024, 970), (32768, 30000)])
+def test_decode_nan_behind_vanishing_weights(kvc, fmt, cap, n):
+    """P_g(j) > 0 for every slot, however small: a NaN in V reaches the output where fp32 weights are 0 too.
+    The slots of the first half have logits of -1016; both decode paths."""
+    H, G, d, block = 2, 2, 64, 64
+    c = kvc.q8_cache(1, H, cap, d, block, F32, CODES[fmt])
+    c["K"][:, :, :n // 2 // block * block] = torch.tensor(-127.0 if fmt == "s8" else -128.0, device="cuda").to(CODES[fmt])
+    c["Ks"].fill_(1.0)
+    c["Vs"].fill_(1.0)
+    c["Vs"][0, 0, 0] = NAN
+    c["len"].fill_(n)
+    q = torch.ones(1, H * G, d, device="cuda")
+    new = torch.zeros(1, H, d, device="cuda")
+    o = kvc.h2o_decode_step_q8(q, new, new, c, 2 * cap)
+    torch.cuda.synchronize()
+    assert o[0, :G].isnan().all() and (o[0, G:] == 0).all() and c["acc"].isfinite().all()
