@@ -74,8 +74,17 @@ struct TcArgs {
   int wide;       // O's rows start on 32-byte boundaries
   int whole;      // query tiles (in the order of attn_locate) whose items are not split
   int splits;     // the others' items: each with a share of its key tiles
-  float *part;    // splits > 1: [splits][B][Hq][Tq][D] sums of P V, not yet divided
-  float2 *stat;   // [splits][B][Hq][Tq] reference (log2 units) and sum of weights
+  // splits > 1, one row for each row of a share (share_row):
+  int by_tile;          // 1: [splits][split tiles][Hq][tile rows]; 0: [splits][B][Hq][Tq]
+  long long share_rows; // rows of one share of everything that is split
+  float *part;          // [splits][share_rows][D] sums of P V, not yet divided
+  float2 *stat;         // [splits][share_rows] reference (log2 units) and sum of weights
+
+  // Row `row` of split tile `tile`, token `tok` of batch row b, in the first share.
+  __device__ __forceinline__ long long share_row(int b, int h, int tile, int row, long long tok) const {
+    return by_tile ? ((long long)tile * A.S.Hq + h) * (pair_rows ? 2 * BM : BM) + row
+                   : ((long long)b * A.S.Hq + h) * A.S.Tq + tok;
+  }
 };
 
 __device__ __forceinline__ void tma_load_4d(void *dst, const CUtensorMap *map, int x, int y, int z, int w,
@@ -185,6 +194,7 @@ struct Work {
   int h[2], r0[2], rows[2], n[2];  // per tile: head, first row, rows, key tiles
   int nmax;
   int split, j0;  // share of the key tiles (-1: all) and the first of them
+  int tile;       // with a share: index among the split tiles
 };
 
 // CTA `block`'s item; executed by one whole warp.
@@ -193,10 +203,12 @@ __device__ __forceinline__ Work make_work(const TcArgs &T, int block, bool check
   int index = block / pairs, hi = block - index * pairs;
   Work w;
   w.split = -1;
+  w.tile = 0;
   if (index >= T.whole) {
     const int b = block - T.whole * pairs;
     index = b / (pairs * T.splits);
     const int part = b - index * pairs * T.splits;
+    w.tile = index;
     index += T.whole;
     hi = part / T.splits;
     w.split = part - hi * T.splits;
@@ -608,7 +620,8 @@ __global__ void __launch_bounds__(NT, 1)
       }
       if (w.split >= 0 && w.rows[i] > 0) {
         // this share of the keys, for attn_join_kernel
-        const long long at = (((long long)w.split * S.B + w.t.b) * S.Hq + w.h[i]) * S.Tq + w.t.q0 + w.r0[i] + row;
+        const long long at = w.split * T.share_rows + T.share_row(w.t.b, w.h[i], w.tile, w.r0[i] - w.t.r0 + row,
+                                                                  (long long)w.t.q0 + w.r0[i] + row);
         const bool live = row < w.rows[i];
         if (live) T.stat[at] = make_float2(m, z2.x + z2.y);
         if (n > 0) {
@@ -681,25 +694,24 @@ __global__ void __launch_bounds__(NTJ) attn_join_kernel(const __grid_constant__ 
   pdl_wait();
   pdl_launch();
   const int bm = T.pair_rows ? 2 * BM : BM, subs = bm / JM;
-  const int h = blockIdx.x % S.Hq, sub = blockIdx.x / S.Hq % subs;
+  const int h = blockIdx.x % S.Hq, sub = blockIdx.x / S.Hq % subs, split_tile = blockIdx.x / S.Hq / subs;
   if (threadIdx.x < 32) {
-    const AttnTile t = attn_locate(S, T.whole + blockIdx.x / S.Hq / subs, bm, false, nullptr);
+    const AttnTile t = attn_locate(S, T.whole + split_tile, bm, false, nullptr);
     if (threadIdx.x == 0) tile = t;
   }
   __syncthreads();
   AttnTile t = tile;
   t.r0 += sub * JM;
   const int rows = min(JM, t.nq - t.r0);
-  const long long step = (long long)S.B * S.Hq * S.Tq;
   const int lane = threadIdx.x % (D / 4);
   for (int r = threadIdx.x / (D / 4); r < rows; r += NTJ / (D / 4)) {
-    const long long tok = (long long)t.q0 + t.r0 + r, at = ((long long)t.b * S.Hq + h) * S.Tq + tok;
+    const long long tok = (long long)t.q0 + t.r0 + r, at = T.share_row(t.b, h, split_tile, sub * JM + r, tok);
     float2 st[kMaxSplits];
     float M = -INFINITY;
 #pragma unroll
     for (int s = 0; s < kMaxSplits; ++s)
       if (s < T.splits) {
-        st[s] = T.stat[s * step + at];
+        st[s] = T.stat[s * T.share_rows + at];
         if (st[s].y != 0.f) M = fmaxf(M, st[s].x);
       }
     float z = 0.f;
@@ -708,7 +720,7 @@ __global__ void __launch_bounds__(NTJ) attn_join_kernel(const __grid_constant__ 
     for (int s = 0; s < kMaxSplits; ++s)
       if (s < T.splits && st[s].y != 0.f) {  // a share without a visible key was not written
         const float f = tc::ex2(st[s].x - M);
-        const float4 x = __ldcs(reinterpret_cast<const float4 *>(T.part + (s * step + at) * D) + lane);
+        const float4 x = __ldcs(reinterpret_cast<const float4 *>(T.part + (s * T.share_rows + at) * D) + lane);
         z += f * st[s].y;
         o.x += f * x.x;
         o.y += f * x.y;
@@ -719,7 +731,7 @@ __global__ void __launch_bounds__(NTJ) attn_join_kernel(const __grid_constant__ 
     const __nv_bfloat162 a = __floats2bfloat162_rn(o.x * inv, o.y * inv), b = __floats2bfloat162_rn(o.z * inv, o.w * inv);
     *reinterpret_cast<uint2 *>(T.O + t.b * S.o[0] + h * S.o[1] + tok * S.o[2] + 4 * lane) =
         make_uint2(*reinterpret_cast<const uint32_t *>(&a), *reinterpret_cast<const uint32_t *>(&b));
-    if (T.A.lse && lane == 0) T.A.lse[at] = z != 0.f ? (M + log2f(z)) * 0.6931471805599453f : -INFINITY;
+    if (T.A.lse && lane == 0) T.A.lse[((long long)t.b * S.Hq + h) * S.Tq + tok] = z != 0.f ? (M + log2f(z)) * 0.6931471805599453f : -INFINITY;
   }
 }
 
@@ -768,6 +780,14 @@ Plan make_plan(const AttnShape &S) {
   return p;
 }
 
+// Rows of one share: those of the split tiles (the last round of a chunk: few of all tokens), or
+// every token's where the split tiles are not full (packed short sequences).
+long long share_rows(const AttnShape &S, const Plan &p, bool *by_tile) {
+  const long long tile = (p.tiles - p.whole) * ((S.Hq / S.Hkv) % 2 ? 2 * BM : BM), token = (long long)S.B * S.Tq;
+  *by_tile = tile < token;
+  return (*by_tile ? tile : token) * S.Hq;
+}
+
 // [B][H][T][d] with free strides as a 4-D map of boxes of 64 elements x 128 tokens.
 bool encode_heads(CUtensorMap *map, const void *base, int d, long T, long H, long B, const long long *st) {
   tc::EncodeTiledFn fn = tc::encode_tiled_fn();
@@ -812,8 +832,9 @@ bool attn_tc_eligible(const AttnShape &S, float scale, int dtype) {
 
 size_t attn_tc_workspace_bytes(const AttnShape &S) {
   if (S.Tq <= 0 || S.Tk <= 0) return 0;
-  const int n = make_plan(S).splits;
-  return n > 1 ? (size_t)n * S.B * S.Hq * S.Tq * (S.d * sizeof(float) + sizeof(float2)) + 32 : 0;
+  const Plan plan = make_plan(S);
+  bool by_tile;
+  return plan.splits > 1 ? (size_t)plan.splits * share_rows(S, plan, &by_tile) * (S.d * sizeof(float) + sizeof(float2)) + 32 : 0;
 }
 
 int launch_attn_prompt_tc(const void *Q, const void *K, const void *V, const AttnArgs &A, void *O, void *ws,
@@ -821,9 +842,12 @@ int launch_attn_prompt_tc(const void *Q, const void *K, const void *V, const Att
   bool wide = (reinterpret_cast<uintptr_t>(O) & 31) == 0;
   for (int i = 0; i < 3; ++i) wide = wide && A.S.o[i] % 16 == 0;
   const Plan plan = make_plan(A.S);
-  TcArgs T{A, static_cast<__nv_bfloat16 *>(O), (A.S.Hq / A.S.Hkv) % 2, wide, plan.whole, plan.splits, nullptr, nullptr};
+  bool by_tile;
+  const long long rows = share_rows(A.S, plan, &by_tile);
+  TcArgs T{A, static_cast<__nv_bfloat16 *>(O), (A.S.Hq / A.S.Hkv) % 2, wide, plan.whole, plan.splits, by_tile, rows,
+           nullptr, nullptr};
   T.part = reinterpret_cast<float *>((reinterpret_cast<uintptr_t>(ws) + 31) & ~uintptr_t(31));  // 32-byte stores
-  T.stat = reinterpret_cast<float2 *>(T.part + (size_t)T.splits * A.S.B * A.S.Hq * A.S.Tq * A.S.d);
+  T.stat = reinterpret_cast<float2 *>(T.part + (size_t)T.splits * rows * A.S.d);
   return A.S.d == 128 ? run<128>(Q, K, V, T, st) : run<64>(Q, K, V, T, st);
 }
 
