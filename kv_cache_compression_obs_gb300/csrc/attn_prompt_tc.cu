@@ -358,7 +358,9 @@ __global__ void __launch_bounds__(NT, 1)
         if (!__all_sync(0xFFFFFFFFu, wait(&C.want, k))) break;
         if (lane == 0) clc_request(C.reply, &C.clc);
         __syncwarp();
-        int block = wait(&C.clc, k) ? clc_block(C.reply) : -1;
+        const bool got = wait(&C.clc, k);
+        if (!got) tc::mbar_wait(&C.clc, k & 1, kDrainBudget, nullptr);  // the reply lands before the CTA may exit
+        int block = got ? clc_block(C.reply) : -1;
         block = __shfl_sync(0xFFFFFFFFu, block, 0);
         if (block >= 0)
           w = make_work(T, block, false, scan);
