@@ -593,7 +593,7 @@ __global__ void __launch_bounds__(NT, NSET == 1 || D == 64 ? 4 : 3)
     const int q = i / D;
     float v = 0.f;
     for (int s = 0; s < shares; ++s) {
-      if (all[s][q].y == 0.f) continue;  // a CTA without slots has no share: those that have are at least 1
+      if (all[s][q].y == 0.f) continue;  // a CTA without slots has no share (one with slots: at least 1)
       const float f = tc::ex2(all[s][q].x - sM[q]);
       v += f * (s < mr ? cl.map_shared_rank(sh, s)[i] : cl.map_shared_rank(sh, CL - 1)[G * D + i]);
     }
