@@ -96,13 +96,13 @@ struct Piece {
       }
       return max(m & 0xFFFFu, m >> 16) << 16;
     } else {
-      uint32_t m = 0;
+      float m = 0.f;
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        m = __vimax3_u32(m, v[i].x & 0x7FFFFFFFu, v[i].y & 0x7FFFFFFFu);
-        m = __vimax3_u32(m, v[i].z & 0x7FFFFFFFu, v[i].w & 0x7FFFFFFFu);
+        m = max_nan(max_nan(m, fabsf(__uint_as_float(v[i].x))), fabsf(__uint_as_float(v[i].y)));
+        m = max_nan(max_nan(m, fabsf(__uint_as_float(v[i].z))), fabsf(__uint_as_float(v[i].w)));
       }
-      return m;
+      return __float_as_uint(m);
     }
   }
 };
@@ -249,15 +249,15 @@ __device__ __forceinline__ void move_last_block(const BlockArgs &A, int u, int b
       }
       continue;
     }
-    uint32_t big = 0;
+    float big = 0.f;
 #pragma unroll 1
     for (int at = threadIdx.x << 4; at < bytes; at += blockDim.x << 4) {
       piece(at, x);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) big = __vimax3_u32(big, mag(x[e].x), mag(x[e].y));
+      for (int e = 0; e < 8; ++e) big = max_nan(big, max_nan(fabsf(x[e].x), fabsf(x[e].y)));
     }
-    big = __reduce_max_sync(0xFFFFFFFFu, big);
-    if (lane == 0) red[kv][warp] = big;
+    const uint32_t m = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(big));
+    if (lane == 0) red[kv][warp] = m;
     __syncthreads();
     uint32_t v = red[kv][0];
     for (int w = 1; w < (int)blockDim.x >> 5; ++w) v = max(v, red[kv][w]);
@@ -377,13 +377,14 @@ __global__ void __launch_bounds__(NTM, 1024 / NTM) evict_move_kernel(const __gri
     }
     // rounding c a to fp32 keeps the order: a piece's largest code gives its largest value
     // (NaN with a NaN scale, whatever the code)
-    uint32_t bk = 0, bv = 0;
+    float bk = 0.f, bv = 0.f;
 #pragma unroll
     for (int q = 0; q < SQ; ++q) {
-      bk = max(bk, mag(__fmul_rn(Q8<FMT>::big16(k[q]), a[q].x)));
-      bv = max(bv, mag(__fmul_rn(Q8<FMT>::big16(v[q]), a[q].y)));
+      bk = max_nan(bk, __fmul_rn(Q8<FMT>::big16(k[q]), a[q].x));
+      bv = max_nan(bv, __fmul_rn(Q8<FMT>::big16(v[q]), a[q].y));
     }
-    const uint32_t mk = __reduce_max_sync(0xFFFFFFFFu, bk), mv = __reduce_max_sync(0xFFFFFFFFu, bv);
+    const uint32_t mk = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(bk));
+    const uint32_t mv = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(bv));
     // Two buffers in turn over the blocks that get here, each with a barrier (a whole block
     // has none): who writes a buffer again knows that everybody has read it.
     uint32_t (&rd)[2][16] = red[turn];

@@ -8,8 +8,8 @@
 // for blocks of zeros and subnormals).  |x - c a| is then at most half a code step
 // (int8: a / 2; e4m3: 2^-4 |x|, or half its smallest step 2^-10 a) up to fp32 rounding.
 // A block with a NaN or an infinity has the scale NaN, so that all its values are NaN and stay
-// it when its rows move: magnitudes are searched as bits, which order a NaN above every number
-// where fmaxf would drop it.
+// it when its rows move: magnitudes are searched with maxima that keep a NaN, where fmaxf would
+// drop it, and across threads as bits, which order a NaN above every number.
 #pragma once
 
 #include <cuda_fp8.h>
@@ -83,8 +83,12 @@ template <> struct Q8<KV_Q8_E4M3> {
   }
 };
 
-// |x| as bits: they order like the values, a NaN above infinity.
-__device__ __forceinline__ uint32_t mag(float x) { return __float_as_uint(x) & 0x7FFFFFFFu; }
+// The larger one; NaN (0x7FFFFFFF) when either is.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float m;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(a), "f"(b));
+  return m;
+}
 
 // The scale of a block whose largest magnitude has the bits `big`; NaN when that is not finite.
 template <int FMT>
@@ -151,17 +155,17 @@ __device__ __forceinline__ void store16(float *p, const float (&x)[16]) {
   for (int i = 0; i < 4; ++i)
     reinterpret_cast<float4 *>(p)[i] = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
 }
-__device__ __forceinline__ uint32_t max_mag16(const float (&x)[16]) {
-  uint32_t m = 0;
+__device__ __forceinline__ float max_abs16(const float (&x)[16]) {
+  float m = 0.f;
 #pragma unroll
-  for (int i = 0; i < 16; ++i) m = max(m, mag(x[i]));
+  for (int i = 0; i < 16; ++i) m = max_nan(m, fabsf(x[i]));
   return m;
 }
 
-// Largest v of the block (blockDim.x a multiple of 32, at most 1024); sm: 32 words.
-__device__ __forceinline__ uint32_t block_max(uint32_t v, uint32_t *sm) {
-  v = __reduce_max_sync(0xFFFFFFFFu, v);
-  if ((threadIdx.x & 31) == 0) sm[threadIdx.x >> 5] = v;
+// Bits of the largest magnitude v of the block (blockDim.x a multiple of 32, at most 1024); sm: 32 words.
+__device__ __forceinline__ uint32_t block_max(float v, uint32_t *sm) {
+  const uint32_t w = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(v));
+  if ((threadIdx.x & 31) == 0) sm[threadIdx.x >> 5] = w;
   __syncthreads();
   const int nw = blockDim.x >> 5, lane = threadIdx.x & 31;
   return __reduce_max_sync(0xFFFFFFFFu, lane < nw ? sm[lane] : 0u);

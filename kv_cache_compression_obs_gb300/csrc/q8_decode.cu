@@ -308,15 +308,15 @@ __device__ __forceinline__ void stream_range(const DecArgs &A, long u, int k0, i
     const int qi = st * 4 + (g >> 1);
     const T *q = static_cast<const T *>(A.q) + (u * G + min(qi, G - 1)) * (long)D;
     float x[NCH][16];
-    uint32_t big = 0;
+    float big = 0.f;
 #pragma unroll
     for (int c = 0; c < NCH; ++c) {
       load16(q + c * 64 + t * 16, x[c]);
-      big = max(big, max_mag16(x[c]));
+      big = fmaxf(big, max_abs16(x[c]));
     }
-    big = max(big, __shfl_xor_sync(0xFFFFFFFFu, big, 1));
-    big = max(big, __shfl_xor_sync(0xFFFFFFFFu, big, 2));
-    const int sh = query_shift(__uint_as_float(big));
+    big = fmaxf(big, __shfl_xor_sync(0xFFFFFFFFu, big, 1));
+    big = fmaxf(big, __shfl_xor_sync(0xFFFFFFFFu, big, 2));
+    const int sh = query_shift(big);
     const float f = exp2i(sh);
     // query t's shift sits in the lanes with g = 2t
     qf[st] = A.c_log2 * exp2i(-__shfl_sync(0xFFFFFFFFu, sh, 8 * t));
@@ -500,11 +500,11 @@ __device__ __forceinline__ void quantise_tail(const DecArgs &A, long u, int n, i
   uint4 *to = reinterpret_cast<uint4 *>(static_cast<uint8_t *>(kv ? A.c.V : A.c.K) + (u * (long)A.c.cap + nf) * D);
   const int pieces = block * D / 16, old = (block - 1) * D / 16;
   auto load = [&](int i, float (&x)[16]) { load16(i < old ? rows + (long)i * 16 : fresh + (i - old) * 16, x); };
-  uint32_t big = 0;
+  float big = 0.f;
   for (int i = threadIdx.x; i < pieces; i += blockDim.x) {
     float x[16];
     load(i, x);
-    big = max(big, max_mag16(x));
+    big = max_nan(big, max_abs16(x));
   }
   const float a = q8_scale<FMT>(block_max(big, red));
   const float inv = __fdiv_rn(1.f, a);
