@@ -348,6 +348,7 @@ __global__ void __launch_bounds__(NT, 1)
       // for the reply and the next item's first loads, late enough that a CTA with a long item does
       // not sit on the next one.
       Work w = first_work;
+      int pending = -1;  // the request whose reply was not waited for
       for (uint32_t k = 0;; ++k) {
         const bool ok = wait(C.wempty + (k & 1), (k >> 1) ^ 1);
         if (lane == 0) {
@@ -358,15 +359,19 @@ __global__ void __launch_bounds__(NT, 1)
         if (!__all_sync(0xFFFFFFFFu, wait(&C.want, k))) break;
         if (lane == 0) clc_request(C.reply, &C.clc);
         __syncwarp();
-        const bool got = wait(&C.clc, k);
-        if (!got) tc::mbar_wait(&C.clc, k & 1, kDrainBudget, nullptr);  // the reply lands before the CTA may exit
-        int block = got ? clc_block(C.reply) : -1;
+        int block = -1;
+        if (wait(&C.clc, k))
+          block = clc_block(C.reply);
+        else
+          pending = (int)k;
         block = __shfl_sync(0xFFFFFFFFu, block, 0);
         if (block >= 0)
           w = make_work(T, block, false, scan);
         else
           w.t.nq = -1;
       }
+      // the reply lands before the CTA may exit
+      if (pending >= 0) tc::mbar_wait(&C.clc, pending & 1, kDrainBudget, nullptr);
     } else if (warp == W_TMA) {
       // ---- loads: K_0 V_0 K_1 V_1 ... of every item through one ring, Q_0 and Q_1 ----
       if (tc::elect_one()) {
