@@ -103,7 +103,7 @@ typedef enum { KV_Q8_S8 = 0, KV_Q8_E4M3 = 1 } kv_q8_format;
 
 /*
  * A slot cache held in 8 bits.  Slots 0..len-1 of unit (b, h) are filled, in the
- * order of their positions; every operation below keeps that order.  The len / block
+ * order of their positions (no two alike); every operation below keeps that order.  The len / block
  * whole blocks of `block` slots are codes with one float32 scale a per block and
  * head for K and one for V (the value of a code c is c a):
  *     a = max(max|x| / top, 2^-126) over the block, c = round-to-even(x (1 / a)),
@@ -509,11 +509,12 @@ KVC_API int kv_attn_prompt(const void *Q, const void *K, const void *V, int B, i
  *
  *   K, V       [B][Hkv][T][d] of out->dtype, device or pinned host memory (as for
  *              kv_compact);  s [B][Hkv][T] float32, NULL: acc starts at 0
- *   idx        [B][Hkv][k] int32 ascending, each in [0, T); NULL (k == T only): every
- *              row, the whole prompt
+ *   idx        [B][Hkv][k] int32 ascending, none twice, each in [0, T); NULL (k == T
+ *              only): every row, the whole prompt
  *   dev_status device int, may be NULL; KV_ERR_INVALID_ARG when an index is out of
  *              range (its slot then holds a row of zeros at position -1, acc 0)
- * Preconditions: 1 <= k <= T, k <= out->cap.
+ * Preconditions: 1 <= k <= T, k <= out->cap; K, V finite (a row that is not makes its
+ * whole block NaN, see kv_q8_cache).
  */
 KVC_API int kv_compact_q8(const void *K, const void *V, const float *s, const int32_t *idx, int T, int k,
                           const kv_q8_cache *out, int *dev_status, kv_stream_t stream);
@@ -555,6 +556,8 @@ KVC_API int h2o_decode_step_q8(const void *q, const void *k_new, const void *v_n
  * they are.  A destination block whose rows are one whole source block keeps its
  * codes and scale; the others are quantised anew from the values that the codes
  * stand for.  Rows of the new unfinished block that were codes are rounded to dtype.
+ * A NaN in acc has no rank (which of such slots stay is not defined), but protected
+ * slots stay in front of it.
  *
  *   cache      is left as it was; out: another cache (no memory in common) of the
  *              same B, Hkv, d, block, dtype and format with out->cap >= keep.  One

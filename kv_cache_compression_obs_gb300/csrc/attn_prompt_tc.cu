@@ -5,9 +5,14 @@
 // is one CTA per item; a CTA that is done takes over the next one that has not started
 // (cluster launch control), so that its loads and first products run behind the
 // writing of the last result.  Per tile i and key tile j of 128 keys:
-//     S = Q_i K_j^T (TMEM, fp32); P = 2^(c S - m) rounded to bf16 (its rounding is a
-//     relative half step 2^-9 of each weight, which averages out in O; the row sums z
-//     take P before the rounding); O_i += P V_j (TMEM, fp32), P read from TMEM.
+//     S = Q_i K_j^T (TMEM, fp32); P = 2^(c S - m) rounded to bf16; O_i += P V_j (TMEM,
+//     fp32), P read from TMEM.
+// P is rounded because the product takes both operands in V's type: each weight is off by at
+// most a half step, 2^-8 of it, and O by about 1e-3 of its norm (1.5e-3 for rows behind
+// 30000 keys), beside the 1.6e-3 of rounding O itself; hi + lo weights would be half as
+// much tensor work again.  The row sums z take P before the rounding: lse is fp32 and needs
+// them so, and sums of the rounded weights would change O's error little (in a float64 model
+// 1.91e-3 of the norm in all for 1.92e-3 over 2048 tokens, 2.27e-3 for 2.26e-3 behind 11000 keys).
 // The reference m of a row moves only when a logit passes it by more than kLazy (log2
 // units; weights stay below 2^kLazy): only then is O rescaled, by the softmax warps
 // themselves, which know that the product before is complete because the commit that
@@ -26,10 +31,10 @@
 // replaced by -inf and the V rows are cleared in shared memory, so NaN in them
 // cannot reach the result.
 //
-// Bound by the tensor pipe and, in long calls, by power: 32768 tokens of 32/8 heads 5.20 ms,
-// 1690 TFLOP/s over the causal half (0.87 of the library's burst rate, 0.97 of what it
-// sustains); 8192 tokens 334 us with the tensor pipe active 71% of the time; 4096 tokens
-// 100 us, where an item's end and the next one's start (2 to 3 us) weigh more.  Two threads a
+// Bound by the tensor pipe and, in long calls, by power: 32768 tokens of 32/8 heads 5.20 to
+// 5.42 ms from one GPU to the next, 1690 to 1620 TFLOP/s over the causal half (0.87 to 0.83 of
+// the library's burst rate, 0.97 to 0.93 of what it sustains); 8192 tokens 334 us with the tensor
+// pipe active 71% of the time; 4096 tokens 99 to 102 us, where an item's end and the next one's start (2 to 3 us) weigh more.  Two threads a
 // row (four softmax warpgroups) spilled; O out of TMEM in one go instead of by 32 columns
 // changed nothing that could be measured.
 #include <cmath>
@@ -759,7 +764,7 @@ double round_steps(long items, int tiles, int s) {
 // Fewer items than SMs: all of them are split if that pays (16 rows of 32 heads over 32768
 // keys, 16 items: 56 us against 352).  A few rounds of about equal items (a chunk behind
 // many more keys): the tiles of the last, partial round are (2000 rows of 32 heads behind 30001
-// keys, 256 items: 651 us against 672; all in 4 shares 725).  Otherwise the items are
+// keys, 256 items: 651 us against 672 on one GPU, to 683 on others; all in 4 shares 725).  Otherwise the items are
 // many or shrink towards the end, and evening out is the claims' work.
 Plan make_plan(const AttnShape &S) {
   const bool pair_rows = (S.Hq / S.Hkv) % 2;

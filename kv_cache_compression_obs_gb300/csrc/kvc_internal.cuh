@@ -11,7 +11,9 @@
 
 namespace kvc {
 
-constexpr int kNumSmsHint = 152;  // GB300; the launchers query the real count
+// GB300.  The plans that go by this constant (shares, splits, clusters, and the workspace sizes that follow from
+// them) are tuned for it; with another count they are slower, not wrong.  device_sm_count() is the real count.
+constexpr int kNumSmsHint = 152;
 
 int device_sm_count();
 // Opt a kernel into `bytes` of dynamic shared memory when that plus its static

@@ -773,10 +773,12 @@ int splits(long units, int cap) {
   return (int)(ns < 1 ? 1 : ns > kMaxSplits ? kMaxSplits : ns);
 }
 
-// The one-launch kernel where its CTAs all run at once and hold short ranges: CTAs per unit (0:
-// not), slots of a CTA.  One KV group of 8 with 1638 slots 11.0 us (two launches: 12.3), 64 units
-// of up to 8192 slots 32.7 us (34.0); but 256 units of up to 8192 slots 84 us (66), where CTAs
-// that wait for the rest of their cluster leave the memory idle.
+// The one-launch kernel where its CTAs hold short ranges and nearly all run at once (four an SM;
+// three for G > 4 and d = 128, the rest then follow: a cluster waits for its own CTAs alone): CTAs
+// per unit (0: not), slots of a CTA.  One KV group of 8 with 1638 slots 11.0 us (two launches: 12.3),
+// 64 units of up to 8192 slots 32.7 us (34.0); but 256 units of up to 8192 slots 84 us (66), where
+// CTAs that wait for the rest of their cluster leave the memory idle.  As the doubling looks one CTA
+// a unit ahead, 77 to 121 units and 153 to 202 are taken past the room and get two launches.
 int cluster_plan(long units, int G, int cap, int *slots) {
   const long room = 4L * kNumSmsHint;
   int cl = 1;
