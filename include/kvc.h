@@ -10,8 +10,12 @@
  * and, beyond those five, NestedKV's key-only scorer (kv_score_nested), a
  * layer-level budget shared by the heads of a layer (kv_select_budget,
  * kv_compact_ragged), the _ex variants (sinks, HubKV comparison variants), the
- * attention of the prompt itself (kv_attn_prompt) and a slot cache held in 8 bits
- * (kv_compact_q8, h2o_decode_step_q8, kv_evict_q8).
+ * attention of the prompt itself (kv_attn_prompt), a slot cache held in 8 bits
+ * (kv_compact_q8, h2o_decode_step_q8, kv_evict_q8), and what makes and reads a long
+ * cache that is kept whole: norm, rotary positions and the cache's rows in one pass
+ * (kv_qk_norm_rope), attention over the blocks that a cheap bound chooses
+ * (kv_block_digest, kv_attn_blocks) and over a prefix that a batch has in common
+ * (kv_attn_shared).
  *
  * Sources (page title, section):
  *   [H2O]    "H2O 完全拆解：抓住 KV Cache 里的「重击者」，20% 预算无损生成（NeurIPS 2023）"
@@ -95,7 +99,8 @@ enum {
   KV_OP_SCORE_NESTED = 5,
   KV_OP_HUBKV_SELECT = 6,
   KV_OP_ATTN_PROMPT = 7,
-  KV_OP_DECODE_Q8 = 8
+  KV_OP_DECODE_Q8 = 8,
+  KV_OP_ATTN_SHARED = 9
 };
 
 /* formats of the 8-bit slot cache's codes: int8 (-127..127) or e4m3 (largest 448) */
@@ -129,6 +134,47 @@ typedef struct kv_q8_cache {
 } kv_q8_cache;
 
 typedef void *kv_stream_t;
+
+/* kv_qk_norm_rope flags */
+enum {
+  KV_ROPE_INTERLEAVED = 1, /* pairs are neighbours (2i, 2i+1), not halves (i, i + rot/2) */
+  KV_ROPE_NORM = 2,        /* RMS norm of each query and key head first */
+  KV_ROPE_ONE_PLUS = 4     /* the norm's weights are 1 + q_weight, 1 + k_weight */
+};
+
+/* What kv_qk_norm_rope reads and writes. */
+typedef struct kv_qkv_heads {
+  const void *q, *k, *v;           /* [B][Hq][T][d], [B][Hkv][T][d] twice; each may be NULL */
+  void *q_out, *k_out, *v_out;     /* [B][Hq][T][d], [B][Hkv][cap][d] twice; NULL where the input is */
+  const void *q_weight, *k_weight; /* [d] of dtype, may be NULL (weights of 1) */
+  const double *inv_freq;          /* [rot / 2] radians per position (kv_rope_freqs makes them) */
+  const int32_t *pos;              /* [B][T] positions, any sign; NULL: token t stands at t */
+  const int32_t *slot;             /* [B][Hkv]: token t's key and value go to row slot + t; NULL: row t */
+  const int32_t *seq;              /* [B]: only the first seq tokens of a row; NULL: all T */
+  int64_t strides[18];             /* batch, head and token of q, k, v, q_out, k_out, v_out, in elements */
+  int B, Hq, Hkv, T;
+  int cap;                         /* rows of k_out, v_out */
+  int d;                           /* 64 or 128 */
+  int rot;                         /* the first rot elements of a head turn (even, 0..d) */
+  float eps, rot_scale;
+  int flags, dtype;
+} kv_qkv_heads;
+
+/* How rotary frequencies are scaled for a longer context (kv_rope_freqs). */
+typedef enum {
+  KV_ROPE_PLAIN = 0,
+  KV_ROPE_LINEAR = 1, /* positions divided by factor */
+  KV_ROPE_BASE = 2,   /* theta times factor^(rot / (rot - 2)): the slowest pair is divided by factor */
+  KV_ROPE_BANDS = 3,  /* by turns within `context`: kept from `high` on, divided up to `low`, linear between */
+  KV_ROPE_YARN = 4    /* the same by pair index, between the pairs that turn `high` and `low` times (YaRN), and
+                         rot_scale = 0.1 ln(factor) + 1 */
+} kv_rope_kind;
+typedef struct kv_rope_scaling {
+  int kind;            /* kv_rope_kind */
+  double factor;       /* >= 1 */
+  double low, high;    /* turns, 0 < low < high (BANDS, YARN) */
+  double context;      /* tokens of the unscaled context, > 0 (BANDS, YARN) */
+} kv_rope_scaling;
 
 /*
  * kv_score_obs -- per-head importance score of every prompt token.
@@ -573,10 +619,126 @@ KVC_API int h2o_decode_step_q8(const void *q, const void *k_new, const void *v_n
 KVC_API int kv_evict_q8(const kv_q8_cache *cache, int keep, int recent, int sink, int32_t *idx_out,
                         const kv_q8_cache *out, int *dev_status, kv_stream_t stream);
 
+/*
+ * kv_qk_norm_rope -- the heads of a projection made ready for attention and for the
+ * cache, in one pass: RMS norm of each query and key head, rotary positions, and the
+ * layout.  With x a head's d elements and w its weights
+ *     y = x w / sqrt(mean(x^2) + eps)           (KV_ROPE_NORM; else y = x),
+ * and each pair (a, b) = (y_i, y_{i + rot/2}), or (y_2i, y_{2i+1}) when interleaved, at
+ * position p turns by the angle p inv_freq[i]:
+ *     (a cos - b sin, b cos + a sin) rot_scale;
+ * what stands behind the first rot elements stays y.  Values are copied.  All in fp32
+ * (the angle exact to 2^-26 turns at any position), rounded to dtype once.
+ *
+ *   k_out, v_out  e.g. a slot cache: token t of unit (b, h) goes to row slot[b][h] + t,
+ *              so `slot` is the cache's len and the caller adds T to it afterwards;
+ *              other rows are left as they were
+ *   seq        tokens behind a row's seq are neither read nor written
+ *   in place   q_out == q with the same strides (and k, v likewise) is allowed; any other
+ *              overlap of inputs and outputs is not
+ *   dev_status device int, may be NULL; KV_ERR_INVALID_ARG when a row of k_out, v_out
+ *              would be outside [0, cap) (that row is not written) or a seq is outside [0, T]
+ *              (nothing of that batch row is written); never cleared
+ * Keys alone, with flags 0 and differences as positions, moves cached keys to other
+ * positions.  Preconditions: every row starts on a 16-byte boundary; d in {64, 128};
+ * inv_freq finite.
+ */
+KVC_API int kv_qk_norm_rope(const kv_qkv_heads *heads, int *dev_status, kv_stream_t stream);
+
+/*
+ * kv_rope_freqs -- rotary frequencies theta^(-2i / rot), i < rot / 2, scaled as `scaling`
+ * says (NULL: plain), to the HOST array inv_freq; *rot_scale (may be NULL) receives the
+ * factor of the rotated elements that goes with them.  A host function: no GPU work.
+ */
+KVC_API int kv_rope_freqs(int rot, double theta, const kv_rope_scaling *scaling, double *inv_freq,
+                          float *rot_scale);
+
+/*
+ * kv_block_digest -- least and largest key of each block of a slot cache, per channel:
+ *     digest[b][h][j][0][c] = min over the filled slots of block j of K[slot][c],
+ *     digest[b][h][j][1][c] = max.
+ * Exact (the values are keys); a NaN stays.
+ *
+ *   K          [B][Hkv][cap][d];  len [B][Hkv] filled slots (NULL: cap)
+ *   block      slots of a block: 16, 32, 64 or 128; the last one may be cut off by cap
+ *   n_new      only the blocks that hold one of the n_new newest slots are written (a
+ *              decode step's one token: 1); cap: all that hold a filled slot.  Others
+ *              are left as they were.
+ *   digest     [B][Hkv][ceil(cap / block)][2][d] of dtype
+ *   dev_status device int, may be NULL; KV_ERR_INVALID_ARG when a len is outside [0, cap]
+ *              (that unit is left as it was); never cleared
+ * Preconditions: cap >= 1, 1 <= n_new.
+ */
+KVC_API int kv_block_digest(const void *K, const int32_t *len, int B, int Hkv, int cap, int d, int block,
+                            int n_new, int dtype, void *digest, int *dev_status, kv_stream_t stream);
+
+/*
+ * kv_attn_blocks -- attention of nq new tokens per row over a slot cache of which each
+ * token and KV head reads only some blocks.  The new tokens are the last nq filled
+ * slots: token t sees the slots j < len - nq + t + 1.  With the group's queries q_g
+ *     u_j = max_g sum_c max(q_gc, 0) digest_j1c + min(q_gc, 0) digest_j0c,
+ * which no <q_g, k> of block j passes (a NaN counts as +inf), the blocks are the first
+ * `sink` and the last `recent` of those that the token sees and, up to n_sel in all, the
+ * others in the order (u descending, j ascending); all that it sees when they are at most
+ * n_sel.  The choice is that of u in 64 bits.  Then, over the visible slots of these
+ *     P_g = softmax of scale <q_g, k>,  o = sum P_g v,  lse = log sum exp(scale <q_g, k>).
+ * A token that sees nothing gets o = 0, lse = -inf and no blocks.
+ *
+ *   q, o       [B][Hq][nq][d]; dtype (o is rounded to it once)
+ *   strides    host array of 6 element strides: batch, head and token of q, o (the d
+ *              elements of a row are adjacent), each positive and stride * element size a
+ *              multiple of 16 bytes; NULL = dense
+ *   K, V       [B][Hkv][cap][d];  len [B][Hkv]
+ *   digest     as kv_block_digest writes it, up to date for every filled slot
+ *   lse_out    [B][Hq][nq] float32, may be NULL
+ *   sel_out    [B][Hkv][nq][n_sel] int32: the blocks ascending, -1 behind the last; may
+ *              be NULL
+ *   dev_status device int, may be NULL; KV_ERR_INVALID_ARG when a len is outside [0, cap]
+ *              (that unit's outputs are left as they were); never cleared
+ * Preconditions: Hq % Hkv == 0, Hq / Hkv <= 8, d in {64, 128}, block as kv_block_digest,
+ * 0 <= sink, 1 <= recent, sink + recent <= n_sel, scale > 0, at most 12288 blocks.
+ * No workspace.  V is finite in the slots that len covers (a token multiplies up to 15 that
+ * it does not see by 0); what stands behind len is not used.
+ */
+KVC_API int kv_attn_blocks(const void *q, const void *K, const void *V, const int32_t *len, const void *digest,
+                           int B, int Hq, int Hkv, int nq, int cap, int d, int block, int n_sel, int sink,
+                           int recent, const int64_t *strides, float scale, int dtype, void *o,
+                           float *lse_out, int32_t *sel_out, int *dev_status, kv_stream_t stream);
+
+/*
+ * kv_attn_shared -- attention of nq new tokens of each of B rows over a prefix that all
+ * rows have in common and the row's own slot cache.  The prefix's P keys are seen by every
+ * token; the new tokens are the last nq own slots, so that token t sees the own slots
+ * j < len - nq + t + 1.  Over all that it sees
+ *     P_g = softmax of scale <q_g, k>,  o = sum P_g v,  lse = log sum exp(scale <q_g, k>);
+ * a token that sees nothing gets o = 0, lse = -inf.
+ *
+ *   q, o       [B][Hq][nq][d]; dtype (o is rounded to it once)
+ *   Kp, Vp     [Hkv][P][d], may be NULL when P == 0
+ *   K, V       [B][Hkv][cap][d], len [B][Hkv]; may be NULL when cap == 0
+ *   strides    host array of 10 element strides: batch, head and token of q; head and token
+ *              of Kp; of Vp; batch, head and token of o; conditions as for kv_attn_blocks;
+ *              NULL = dense
+ *   lse_out    [B][Hq][nq] float32, may be NULL
+ *   workspace  >= kv_workspace_size(KV_OP_ATTN_SHARED, B, Hq, Hkv, P, d, nq, 0)
+ *   dev_status device int, may be NULL; KV_ERR_INVALID_ARG when a len is outside [0, cap]
+ *              (that unit's outputs are left as they were), KV_ERR_TIMEOUT when a bounded
+ *              device-side wait gave up; never cleared
+ * Preconditions: Hq % Hkv == 0, d in {64, 128}, scale > 0.  V is finite in the slots that
+ * len covers; what stands behind len is not used.
+ * bf16: the prefix's products on the tensor cores (tcgen05, TMA), its weights rounded to
+ * bf16 before the second product; fp32 and the own slots: fp32 accuracy.
+ */
+KVC_API int kv_attn_shared(const void *q, const void *Kp, const void *Vp, const void *K, const void *V,
+                           const int32_t *len, int B, int Hq, int Hkv, int nq, int P, int cap, int d,
+                           const int64_t *strides, float scale, int dtype, void *o, float *lse_out,
+                           void *workspace, size_t workspace_bytes, int *dev_status, kv_stream_t stream);
+
 /* Device workspace (bytes) that `op` needs for these sizes; 0 if none.
  * Arguments that an op does not use are ignored; for KV_OP_HUBKV_REFINE pass the
  * refine call's head count H as Hkv; for KV_OP_DECODE and KV_OP_DECODE_Q8 pass the slot
- * capacity as T; for KV_OP_ATTN_PROMPT pass Tk as T, Tq as W and n_seq as k;
+ * capacity as T; for KV_OP_ATTN_PROMPT pass Tk as T, Tq as W and n_seq as k; for
+ * KV_OP_ATTN_SHARED pass P as T and nq as W;
  * for KV_OP_SCORE_NESTED pass H as Hkv and n_blocks as W.
  * Returns 0 for invalid sizes. */
 KVC_API size_t kv_workspace_size(int op, int B, int Hq, int Hkv, int T, int d, int W, int k);

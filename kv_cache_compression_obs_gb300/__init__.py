@@ -15,6 +15,12 @@ cache held in 8 bits with a scale per block and head: ``q8_cache``,
 ``kv_compact_q8``, ``h2o_decode_step_q8``, ``kv_evict_q8`` and the chain
 ``compress_prefill_q8``.
 
+Around a long cache that is kept whole: ``kv_qk_norm_rope`` (norm of the query and
+key heads, rotary positions, rows of the cache; ``kv_rope_freqs``),
+``kv_block_digest`` and ``kv_attn_blocks`` (attention over the blocks that a cheap
+bound chooses for each token), ``kv_attn_shared`` (a prefix that a batch has in
+common, read once for all rows).
+
 The binding (``kv_cache_compression_obs_gb300.api``) only marshals arguments;
 importing it loads the CUDA library and raises if it is missing.  ``gen`` and
 ``configs`` are plain Python and do not load the library.
@@ -25,7 +31,8 @@ _API_NAMES = {"kv_score_obs", "hubkv_refine", "kv_select_topk", "kv_compact",
               "h2o_decode_step", "kv_workspace_size", "KvcError", "compress_prefill",
               "compress_prefill_host", "kv_select_budget", "kv_compact_ragged", "kv_score_nested",
               "kv_attn_prompt", "q8_cache", "kv_compact_q8", "h2o_decode_step_q8", "kv_evict_q8",
-              "compress_prefill_q8"}
+              "compress_prefill_q8", "kv_qk_norm_rope", "kv_rope_freqs", "kv_block_digest", "kv_attn_blocks",
+              "kv_attn_shared"}
 
 
 def __getattr__(name):

@@ -32,8 +32,9 @@ KV_BF16, KV_F32 = 0, 1
 KV_H2O_ALG1 = 1
 KV_HUB_AVGPOOL, KV_HUB_FIXED_HEAD = 1, 2
 KV_OP_SCORE_OBS, KV_OP_HUBKV_REFINE, KV_OP_SELECT_TOPK, KV_OP_DECODE, KV_OP_SCORE_NESTED = 1, 2, 3, 4, 5
-KV_OP_HUBKV_SELECT, KV_OP_ATTN_PROMPT, KV_OP_DECODE_Q8 = 6, 7, 8
+KV_OP_HUBKV_SELECT, KV_OP_ATTN_PROMPT, KV_OP_DECODE_Q8, KV_OP_ATTN_SHARED = 6, 7, 8, 9
 KV_Q8_S8, KV_Q8_E4M3 = 0, 1
+KV_ROPE_INTERLEAVED, KV_ROPE_NORM, KV_ROPE_ONE_PLUS = 1, 2, 4
 
 _P, _I, _F, _Z = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
 _lib.kv_score_obs.restype = _I
@@ -87,6 +88,33 @@ _lib.h2o_decode_step_q8.restype = _I
 _lib.h2o_decode_step_q8.argtypes = [_P, _P, _P, _Q8P, _I, _I, _P, _P, _F, _P, _P, _Z, _P, _P]
 _lib.kv_evict_q8.restype = _I
 _lib.kv_evict_q8.argtypes = [_Q8P, _I, _I, _I, _P, _Q8P, _P, _P]
+
+
+class _QkvHeads(ctypes.Structure):
+    _fields_ = ([(n, _P) for n in ("q", "k", "v", "q_out", "k_out", "v_out", "q_weight", "k_weight", "inv_freq", "pos",
+                                   "slot", "seq")]
+                + [("strides", ctypes.c_int64 * 18)]
+                + [(n, _I) for n in ("B", "Hq", "Hkv", "T", "cap", "d", "rot")]
+                + [("eps", _F), ("rot_scale", _F), ("flags", _I), ("dtype", _I)])
+
+
+class _RopeScaling(ctypes.Structure):
+    _fields_ = [("kind", _I), ("factor", ctypes.c_double), ("low", ctypes.c_double), ("high", ctypes.c_double),
+                ("context", ctypes.c_double)]
+
+
+_lib.kv_qk_norm_rope.restype = _I
+_lib.kv_qk_norm_rope.argtypes = [ctypes.POINTER(_QkvHeads), _P, _P]
+_I64P = ctypes.POINTER(ctypes.c_int64)
+_lib.kv_block_digest.restype = _I
+_lib.kv_block_digest.argtypes = [_P, _P, _I, _I, _I, _I, _I, _I, _I, _P, _P, _P]
+_lib.kv_attn_blocks.restype = _I
+_lib.kv_attn_blocks.argtypes = [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _I, _I, _I64P, _F, _I, _P, _P, _P, _P, _P]
+_lib.kv_attn_shared.restype = _I
+_lib.kv_attn_shared.argtypes = [_P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I64P, _F, _I, _P, _P, _P, _Z, _P, _P]
+_lib.kv_rope_freqs.restype = _I
+_lib.kv_rope_freqs.argtypes = [_I, ctypes.c_double, ctypes.POINTER(_RopeScaling), ctypes.POINTER(ctypes.c_double),
+                               ctypes.POINTER(_F)]
 _lib.kv_workspace_size.restype = _Z
 _lib.kv_workspace_size.argtypes = [_I, _I, _I, _I, _I, _I, _I, _I]
 _lib.kv_status_string.restype = ctypes.c_char_p
@@ -664,6 +692,228 @@ def compress_prefill_q8(Q, K, V, W: int, k: int, recent: int, r: float | None, c
         cap = (k + block - 1) // block * block if cap is None else cap
         cache = q8_cache(K.shape[0], K.shape[1], cap, K.shape[3], block, K.dtype, codes, K.device)
         return o, lse, kv_compact_q8(K, V, s, idx, cache)
+
+
+_ROPE_KINDS = {None: 0, "linear": 1, "base": 2, "bands": 3, "yarn": 4}
+
+
+def kv_rope_freqs(rot: int, theta: float = 10000.0, scaling: str | None = None, factor: float = 1.0, low: float = 1.0,
+                  high: float = 32.0, context: float = 8192.0, device="cuda"):
+    """Rotary frequencies for kv_qk_norm_rope: (inv_freq [rot / 2] float64 on `device`, rot_scale).
+
+    theta^(-2i / rot), for longer contexts scaled by `factor`: "linear" (all of them), "base" (through theta),
+    "bands" (those that turn fewer than `high` times within `context` tokens, in full from `low` down) or "yarn"
+    (the same by pair index, with the scale of the rotated elements that belongs to it)."""
+    if scaling not in _ROPE_KINDS:
+        raise ValueError(f"scaling must be one of {sorted(k for k in _ROPE_KINDS if k)} or None")
+    f, scale = (ctypes.c_double * max(1, rot // 2))(), _F()
+    how = _RopeScaling(_ROPE_KINDS[scaling], float(factor), float(low), float(high), float(context))
+    _check("kv_rope_freqs", _lib.kv_rope_freqs(int(rot), float(theta), ctypes.byref(how), f, ctypes.byref(scale)))
+    return torch.tensor(f[:rot // 2], dtype=torch.float64, device=device), scale.value
+
+
+@functools.lru_cache(maxsize=4096)
+def _strides6(*st):
+    return (ctypes.c_int64 * 18)(*[x for t in st for x in (t[:3] if t else (0, 0, 0))])
+
+
+def kv_qk_norm_rope(q, k, v, inv_freq, pos=None, q_weight=None, k_weight=None, eps: float | None = None,
+                    interleaved: bool = False, one_plus: bool = False, rot_scale: float = 1.0, slot=None, seq=None,
+                    q_out=None, k_out=None, v_out=None, dev_status=None, stream=None):
+    """The heads of a projection made ready: RMS norm of each query and key head (unless eps is None), rotary
+    positions, and the rows of the cache.  q [B][Hq][T][d], k, v [B][Hkv][T][d], each may be None; strides are
+    free but for the d adjacent elements (a slice of a fused projection [B][T][heads][d] goes in transposed).
+    Returns (q_out, k_out, v_out).
+
+    inv_freq [rot / 2] float64 (kv_rope_freqs; None: no rotation); the first 2 * numel elements of a head turn.
+    pos [B][T] int32 (None: 0..T-1).  q_weight, k_weight [d] in q's dtype or None; one_plus: the weights are
+    1 + those.  k_out, v_out [B][Hkv][cap][d]: with slot [B][Hkv] int32 (a slot cache's len) token t goes to row
+    slot + t, without it to row t; other rows stay.  seq [B] int32: only the first tokens of each row.  Outputs
+    not given are dense tensors of T rows (with slot, k_out and v_out have to be given)."""
+    given = [t for t in (q, k, v) if t is not None]
+    if not given:
+        raise ValueError("one of q, k and v must be given")
+    x = given[0]
+    B, _, T, d = x.shape
+    dt, dev = x.dtype, _device_of(x)
+    kv = k if k is not None else v
+    if k is not None and v is not None and k.shape != v.shape:
+        raise ValueError("k and v disagree in shape")
+    for t in given:
+        if t.dim() != 4 or t.shape[0] != B or t.shape[2] != T or t.shape[3] != d or t.dtype != dt:
+            raise ValueError("q, k and v disagree in batch, tokens, head dim or dtype")
+    if slot is not None and ((k is not None and k_out is None) or (v is not None and v_out is None)):
+        raise ValueError("slot needs k_out and v_out")
+    for t, n in ((q_weight, (d,)), (k_weight, (d,))):
+        if t is not None and (t.shape != n or t.dtype != dt):
+            raise ValueError("weights must be [d] in q's dtype")
+    if inv_freq is not None and (inv_freq.dtype != torch.float64 or inv_freq.dim() != 1):
+        raise ValueError("inv_freq must be [rot / 2] float64")
+    Hkv = kv.shape[1] if kv is not None else 0
+    for t, shape in ((pos, (B, T)), (slot, (B, Hkv)), (seq, (B,))):
+        if t is not None and (t.dtype != _I32 or t.shape != shape):
+            raise ValueError("pos must be [B][T], slot [B][Hkv] and seq [B], all int32")
+    with _side(stream):
+        if q is not None and q_out is None:
+            q_out = q.new_empty(q.shape)
+        if k is not None and k_out is None:
+            k_out = k.new_empty(k.shape)
+        if v is not None and v_out is None:
+            v_out = v.new_empty(v.shape)
+    if q is not None and (q_out.shape != q.shape or q_out.dtype != dt):
+        raise ValueError("q_out must match q")
+    cap = 0
+    for t, o in ((k, k_out), (v, v_out)):
+        if t is not None:
+            if o.dim() != 4 or o.shape[0] != B or o.shape[1] != Hkv or o.shape[3] != d or o.dtype != dt \
+                    or (cap and o.shape[2] != cap):
+                raise ValueError("k_out and v_out must be [B][Hkv][cap][d] in q's dtype")
+            cap = o.shape[2]
+    six = (q, k, v, q_out if q is not None else None, k_out if k is not None else None, v_out if v is not None else None)
+    for t in six:
+        if t is not None and (t.get_device() != dev or t.stride(3) != 1):
+            raise ValueError(f"tensors must be on cuda:{dev} with adjacent elements along d")
+    _on(dev, inv_freq, pos, q_weight, k_weight, slot, seq, dev_status)
+    flags = (KV_ROPE_INTERLEAVED if interleaved else 0) | (KV_ROPE_ONE_PLUS if one_plus else 0)
+    if eps is not None:
+        flags |= KV_ROPE_NORM
+    a = _QkvHeads(*[_at(t) for t in six], _at(q_weight), _at(k_weight), _at(inv_freq), _at(pos), _at(slot), _at(seq),
+                  _strides6(*[None if t is None else t.stride() for t in six]), B, 0 if q is None else q.shape[1], Hkv, T, cap,
+                  d, 0 if inv_freq is None else 2 * inv_freq.numel(), 0.0 if eps is None else float(eps), float(rot_scale),
+                  flags, _dtype_code(x))
+    _check("kv_qk_norm_rope", _lib.kv_qk_norm_rope(ctypes.byref(a), _at(dev_status), _stream_of(dev, stream)))
+    return six[3:]
+
+
+def _slot_cache(K, V, len_, dt, dev: int):
+    """Checks of a slot cache [B][Hkv][cap][d] that is read; returns its shape."""
+    if K.dim() != 4 or V.shape != K.shape or K.dtype != dt or V.dtype != dt:
+        raise ValueError("K and V must be [B][Hkv][cap][d] in q's dtype")
+    if len_.dtype != _I32 or len_.shape != K.shape[:2]:
+        raise ValueError("len must be [B][Hkv] int32")
+    _on(dev, K, V, len_)
+    return K.shape
+
+
+def _out_rows(q, out, lse_out, dev: int):
+    """Output tensors of an attention call with queries q [B][Hq][n][d], made where they are not given."""
+    B, Hq, n, _ = q.shape
+    o = out if out is not None else torch.empty_like(q)
+    lse = lse_out if lse_out is not None else q.new_empty((B, Hq, n), dtype=_F32)
+    if out is not None and (o.shape != q.shape or o.dtype != q.dtype):
+        raise ValueError("out must match q")
+    if lse_out is not None and (lse.shape != (B, Hq, n) or lse.dtype != _F32):
+        raise ValueError("lse_out must be [B][Hq][n] float32")
+    for t in (q, o):
+        if t.stride(3) != 1 or t.get_device() != dev:
+            raise ValueError(f"tensors must be on cuda:{dev} with adjacent elements along d")
+    _on(dev, lse)
+    return o, lse
+
+
+@functools.lru_cache(maxsize=4096)
+def _row_strides(*st):
+    flat = [x for t in st for x in t[:-1]]
+    return (ctypes.c_int64 * len(flat))(*flat)
+
+
+def kv_block_digest(K: torch.Tensor, block: int, len_=None, n_new: int | None = None, out=None, dev_status=None, stream=None):
+    """Least and largest key per block of a slot cache and channel: K [B][Hkv][cap][d] -> digest
+    [B][Hkv][ceil(cap / block)][2][d] in K's dtype.
+
+    len_ [B][Hkv] int32: the filled slots (None: all).  n_new: only the blocks that hold one of the n_new newest
+    slots are written (None: all that hold a filled slot); the others stay as they were in `out` (and are undefined
+    in a tensor made here).  block: 16, 32, 64 or 128."""
+    B, Hkv, cap, d = K.shape
+    dev = _device_of(K)
+    if len_ is not None and (len_.dtype != _I32 or len_.shape != (B, Hkv)):
+        raise ValueError("len must be [B][Hkv] int32")
+    shape = (B, Hkv, -(-cap // block) if block > 0 else 0, 2, d)
+    with _side(stream):
+        dig = out if out is not None else K.new_empty(shape)
+    if out is not None and (dig.shape != shape or dig.dtype != K.dtype):
+        raise ValueError("out must be [B][Hkv][ceil(cap / block)][2][d] in K's dtype")
+    _on(dev, K, len_, dig, dev_status)
+    _check("kv_block_digest", _lib.kv_block_digest(
+        K.data_ptr(), _at(len_), B, Hkv, cap, d, int(block), cap if n_new is None else int(n_new), _dtype_code(K), dig.data_ptr(),
+        _at(dev_status), _stream_of(dev, stream)))
+    return dig
+
+
+def kv_attn_blocks(q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, len_: torch.Tensor, digest: torch.Tensor, block: int,
+                   n_sel: int, sink: int = 0, recent: int = 1, scale: float | None = None, out=None, lse_out=None,
+                   sel_out=None, dev_status=None, stream=None):
+    """Attention of new tokens over the blocks of a slot cache that their digests choose: q [B][Hq][n][d], K, V
+    [B][Hkv][cap][d], len_ [B][Hkv] int32, digest as kv_block_digest makes it -> (o [B][Hq][n][d] in q's dtype, lse
+    [B][Hq][n] float32, sel [B][Hkv][n][n_sel] int32, ascending, -1 behind the last).
+
+    The new tokens are the last n filled slots; token t sees the slots j < len - n + t + 1.  Each (token, KV head)
+    attends the first `sink` and last `recent` of the blocks that it sees and the others with the largest bounds on
+    their logits, n_sel in all.  q's and out's batch, head and token strides are free."""
+    B, Hq, n, d = q.shape
+    dev, dt = _device_of(q), q.dtype
+    shape = _slot_cache(K, V, len_, dt, dev)
+    if shape[0] != B or shape[3] != d:
+        raise ValueError("q and the cache disagree in batch or head dim")
+    Hkv, cap = shape[1], shape[2]
+    if digest.dtype != dt or block <= 0 or digest.shape != (B, Hkv, -(-cap // block), 2, d):
+        raise ValueError("digest must be [B][Hkv][ceil(cap / block)][2][d] in q's dtype")
+    with _side(stream):
+        o, lse = _out_rows(q, out, lse_out, dev)
+        sel = sel_out if sel_out is not None else len_.new_empty((B, Hkv, n, max(0, n_sel)))
+    if sel_out is not None and (sel.shape != (B, Hkv, n, n_sel) or sel.dtype != _I32):
+        raise ValueError("sel_out must be [B][Hkv][n][n_sel] int32")
+    _on(dev, digest, sel, dev_status)
+    if scale is None:
+        scale = d ** -0.5
+    _check("kv_attn_blocks", _lib.kv_attn_blocks(
+        q.data_ptr(), K.data_ptr(), V.data_ptr(), len_.data_ptr(), digest.data_ptr(), B, Hq, Hkv, n, cap, d, int(block),
+        int(n_sel), int(sink), int(recent), _row_strides(q.stride(), o.stride()), float(scale), _dtype_code(q), o.data_ptr(),
+        lse.data_ptr(), sel.data_ptr(), _at(dev_status), _stream_of(dev, stream)))
+    return o, lse, sel
+
+
+def kv_attn_shared(q: torch.Tensor, K_prefix, V_prefix, K, V, len_, scale: float | None = None, out=None, lse_out=None,
+                   workspace=None, dev_status=None, stream=None):
+    """Attention of new tokens over a prefix that all rows have in common and each row's own slots: q [B][Hq][n][d],
+    K_prefix, V_prefix [Hkv][P][d] (None: no prefix), K, V [B][Hkv][cap][d] with len_ [B][Hkv] int32 (None: no own
+    slots) -> (o [B][Hq][n][d] in q's dtype, lse [B][Hq][n] float32).
+
+    Every token sees the whole prefix; the new tokens are the last n own slots and token t sees the own slots
+    j < len - n + t + 1.  Strides of q, out and the prefix are free but for the d adjacent elements."""
+    B, Hq, n, d = q.shape
+    dev, dt = _device_of(q), q.dtype
+    if (K_prefix is None) != (V_prefix is None) or (K is None) != (V is None) or (K is None) != (len_ is None) \
+            or (K is None and K_prefix is None):
+        raise ValueError("a prefix (K_prefix, V_prefix) or own slots (K, V, len_) must be given, each whole")
+    cap = P = 0
+    Hkv = (K_prefix.shape[0] if K is None else K.shape[1])
+    if K is not None:
+        shape = _slot_cache(K, V, len_, dt, dev)
+        if shape[0] != B or shape[3] != d:
+            raise ValueError("q and the cache disagree in batch or head dim")
+        cap = shape[2]
+    st = q.stride()
+    kp = vp = (0, 0, 1)
+    if K_prefix is not None:
+        P = K_prefix.shape[1]
+        if K_prefix.shape != (Hkv, P, d) or V_prefix.shape != K_prefix.shape or K_prefix.dtype != dt or V_prefix.dtype != dt:
+            raise ValueError("the prefix must be [Hkv][P][d] in q's dtype")
+        kp, vp = K_prefix.stride(), V_prefix.stride()
+        if kp[2] != 1 or vp[2] != 1 or K_prefix.get_device() != dev or V_prefix.get_device() != dev:
+            raise ValueError(f"tensors must be on cuda:{dev} with adjacent elements along d")
+    need = _workspace_bytes(KV_OP_ATTN_SHARED, B, Hq, Hkv, P, d, n, 0)
+    with _side(stream):
+        o, lse = _out_rows(q, out, lse_out, dev)
+        ws, nbytes = _workspace(need, q.device, workspace)
+    _on(dev, workspace, dev_status)
+    if scale is None:
+        scale = d ** -0.5
+    _check("kv_attn_shared", _lib.kv_attn_shared(
+        q.data_ptr(), _at(K_prefix), _at(V_prefix), _at(K), _at(V), _at(len_), B, Hq, Hkv, n, P, cap, d,
+        _row_strides(st, kp, vp, o.stride()), float(scale), _dtype_code(q), o.data_ptr(), lse.data_ptr(), _at(ws), nbytes,
+        _at(dev_status), _stream_of(dev, stream)))
+    return o, lse
 
 
 def prefill_host_buffers(hQ: torch.Tensor, hK: torch.Tensor, k: int, r: float | None,

@@ -28,6 +28,7 @@
 #include <cmath>
 
 #include "attn_common.cuh"
+#include "mma_common.cuh"
 #include "tc_common.cuh"
 
 namespace kvc {
@@ -44,36 +45,6 @@ struct Geo {
   static constexpr int BUFS = SPLIT ? NW : 2;
   static constexpr int SMEM = (BM * LK + BUFS * TILE) * 4;
 };
-
-__device__ __forceinline__ uint32_t tf32_hi(float x) {
-  uint32_t r;
-  asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(r) : "f"(x));
-  return r;
-}
-struct Split {
-  uint32_t hi, lo;
-  __device__ __forceinline__ void set(float x) {
-    hi = tf32_hi(x);
-    lo = __float_as_uint(x - __uint_as_float(hi));
-  }
-};
-__device__ __forceinline__ void mma1688(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                        uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-      "{%0, %1, %2, %3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-// c + small += a b to fp32 accuracy.  The unit cuts its sums off rather than rounding them: the
-// two small products have a sum of their own, so that only the large one's steps are cut at
-// the sum's own size.
-__device__ __forceinline__ void mma_split(float (&c)[4], float (&small)[4], const Split (&a)[4], const Split &b0,
-                                          const Split &b1) {
-  mma1688(small, a[0].lo, a[1].lo, a[2].lo, a[3].lo, b0.hi, b1.hi);
-  mma1688(c, a[0].hi, a[1].hi, a[2].hi, a[3].hi, b0.hi, b1.hi);
-  mma1688(small, a[0].hi, a[1].hi, a[2].hi, a[3].hi, b0.lo, b1.lo);
-}
 
 template <typename T, int D, int SPLIT>
 __global__ void __launch_bounds__(32 * Geo<D, SPLIT>::NW) attn_kernel(const T *__restrict__ Q, const T *__restrict__ K,

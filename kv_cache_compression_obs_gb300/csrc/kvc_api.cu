@@ -95,9 +95,22 @@ namespace {
 
 bool dtype_ok(int dt) { return dt == KV_BF16 || dt == KV_F32; }
 bool dim_ok(int d) { return d == 64 || d == 128; }
+bool block_ok(int b) { return b == 16 || b == 32 || b == 64 || b == 128; }
 // product of non-negative ints without overflow of 2^62
 bool fits(long long a, long long b) { return a >= 0 && b >= 0 && (b == 0 || a <= (1LL << 62) / b); }
 
+// The n element strides (NULL: dense) of rows of d elements, count[i] of them along each; a stride that
+// is never stepped becomes d.  False when one is out of range.
+bool row_strides(const int64_t *given, const long long *count, int n, int d, int dtype, long long *out) {
+  const int eb = dtype == KV_F32 ? 4 : 2;
+  long long dense = d;
+  for (int i = n - 1; i >= 0; --i) {
+    out[i] = count[i] <= 1 ? d : given ? given[i] : dense;
+    dense *= count[i] > 0 ? count[i] : 1;
+    if (out[i] <= 0 || out[i] * eb % 16 != 0 || out[i] > (1LL << 38)) return false;
+  }
+  return true;
+}
 
 // A decode call's batch rows run in two halves: rows [0, B/2) on the caller's
 // stream and [B/2, B) on a library-owned side stream (one per device, created on
@@ -252,6 +265,14 @@ size_t kv_workspace_size(int op, int B, int Hq, int Hkv, int T, int d, int W, in
     case KV_OP_DECODE_Q8:  // T is the slot capacity
       if (Hq <= 0 || Hkv <= 0 || Hq % Hkv || !(d == 64 || d == 128)) return 0;
       return decode_q8_workspace_bytes((long)B * Hkv, Hq / Hkv, T, d);
+    case KV_OP_ATTN_SHARED: {  // T is P, W is nq; enough for either dtype
+      if (Hq <= 0 || Hkv <= 0 || Hq % Hkv || W < 0 || !(d == 64 || d == 128) || (long long)B * (Hq / Hkv) > INT_MAX ||
+          !fits((long long)B * (Hq / Hkv), W) || (long long)B * (Hq / Hkv) * W > INT_MAX)
+        return 0;
+      const size_t bf = attn_shared_workspace_bytes(B, Hq, Hkv, W, T, d, KV_BF16);
+      const size_t f32 = attn_shared_workspace_bytes(B, Hq, Hkv, W, T, d, KV_F32);
+      return bf > f32 ? bf : f32;
+    }
     default:
       return 0;
   }
@@ -544,6 +565,105 @@ int kv_evict_q8(const kv_q8_cache *cache, int keep, int recent, int sink, int32_
   for (int i = 0; i < 9; ++i)
     if (a[i] == b[i]) return KV_ERR_INVALID_ARG;  // the source is read while the destination is written
   return launch_evict_q8(*cache, keep, recent, sink, idx_out, *out, dev_status, static_cast<cudaStream_t>(stream));
+}
+
+int kv_qk_norm_rope(const kv_qkv_heads *heads, int *dev_status, kv_stream_t stream) {
+  if (!heads) return KV_ERR_INVALID_ARG;
+  kv_qkv_heads h = *heads;
+  if (h.B < 0 || h.T < 0 || h.cap < 0 || h.Hq < 0 || h.Hkv < 0 || (h.q && h.Hq == 0) || ((h.k || h.v) && h.Hkv == 0) ||
+      !dtype_ok(h.dtype) || h.rot < 0 || h.rot > h.d || h.rot % 2 || !std::isfinite(h.rot_scale) ||
+      (h.flags & ~(KV_ROPE_INTERLEAVED | KV_ROPE_NORM | KV_ROPE_ONE_PLUS)) ||
+      ((h.flags & KV_ROPE_NORM) && !(h.eps >= 0 && std::isfinite(h.eps))))
+    return KV_ERR_INVALID_ARG;
+  if (!dim_ok(h.d)) return KV_ERR_UNSUPPORTED;
+  const void *const in[3] = {h.q, h.k, h.v};
+  void *const out[3] = {h.q_out, h.k_out, h.v_out};
+  if (!fits((long long)h.B * h.T, ((long long)h.Hq + 2LL * h.Hkv) * h.d) || !fits((long long)h.B * h.Hkv, (long long)h.cap * h.d) ||
+      (long long)h.B * h.T > INT_MAX || (long long)h.Hq + 2LL * h.Hkv > 65536)
+    return KV_ERR_INVALID_ARG;
+  if (h.B == 0 || h.T == 0 || (!h.q && !h.k && !h.v)) return KV_OK;
+  const int eb = h.dtype == KV_F32 ? 4 : 2;
+  for (int i = 0; i < 6; ++i) {
+    const bool o = i >= 3;
+    const int n = i % 3;
+    if (!in[n] != !out[n] || !aligned16(in[n]) || !aligned16(out[n])) return KV_ERR_INVALID_ARG;
+    if (!in[n]) continue;
+    const long long count[3] = {h.B, n == 0 ? h.Hq : h.Hkv, o && n > 0 ? h.cap : h.T};
+    for (int a = 0; a < 3; ++a) {
+      int64_t &s = h.strides[3 * i + a];
+      if (count[a] <= 1) s = h.d;  // never stepped: any value will do
+      if (s < 0 || (s == 0 && o) || (s * eb) % 16 != 0 || s > (1LL << 38)) return KV_ERR_INVALID_ARG;
+    }
+  }
+  if ((h.rot > 0 && (h.q || h.k) && !h.inv_freq) || ((uintptr_t)h.inv_freq & 7u) || !aligned4(h.pos) || !aligned4(h.slot) ||
+      !aligned4(h.seq) || ((uintptr_t)h.q_weight % eb) || ((uintptr_t)h.k_weight % eb))
+    return KV_ERR_INVALID_ARG;
+  return launch_qk_norm_rope(h, dev_status, static_cast<cudaStream_t>(stream));
+}
+
+int kv_block_digest(const void *K, const int32_t *len, int B, int Hkv, int cap, int d, int block, int n_new, int dtype,
+                    void *digest, int *dev_status, kv_stream_t stream) {
+  if (B < 0 || Hkv <= 0 || cap <= 0 || n_new <= 0 || !dtype_ok(dtype)) return KV_ERR_INVALID_ARG;
+  if (!dim_ok(d) || !block_ok(block)) return KV_ERR_UNSUPPORTED;
+  if (!fits((long long)B * Hkv, (long long)cap * d)) return KV_ERR_INVALID_ARG;
+  if (B == 0) return KV_OK;
+  if (!K || !digest || !aligned16(K) || !aligned16(digest) || !aligned4(len)) return KV_ERR_INVALID_ARG;
+  return launch_block_digest(K, len, (long)B * Hkv, cap, d, block, n_new, dtype, digest, dev_status,
+                             static_cast<cudaStream_t>(stream));
+}
+
+int kv_attn_blocks(const void *q, const void *K, const void *V, const int32_t *len, const void *digest, int B, int Hq,
+                   int Hkv, int nq, int cap, int d, int block, int n_sel, int sink, int recent, const int64_t *strides,
+                   float scale, int dtype, void *o, float *lse_out, int32_t *sel_out, int *dev_status,
+                   kv_stream_t stream) {
+  if (B < 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0 || nq < 0 || cap <= 0 || !dtype_ok(dtype) || sink < 0 || recent < 1 ||
+      (long long)sink + recent > n_sel || !(scale > 0) || !std::isfinite(scale))
+    return KV_ERR_INVALID_ARG;
+  if (!dim_ok(d) || !block_ok(block) || Hq / Hkv > 8 || !attn_blocks_fits((int)(((long long)cap + block - 1) / block)))
+    return KV_ERR_UNSUPPORTED;
+  if (!fits((long long)B * Hkv, (long long)cap * d) || !fits((long long)B * Hq, (long long)nq * d) ||
+      !fits((long long)B * Hkv * nq, n_sel))
+    return KV_ERR_INVALID_ARG;
+  if (B == 0 || nq == 0) return KV_OK;
+  long long st[2][3];
+  const long long count[3] = {B, Hq, nq};
+  for (int i = 0; i < 2; ++i)
+    if (!row_strides(strides ? strides + 3 * i : nullptr, count, 3, d, dtype, st[i])) return KV_ERR_INVALID_ARG;
+  if (!q || !K || !V || !len || !digest || !o || !aligned16(q) || !aligned16(K) || !aligned16(V) || !aligned16(digest) ||
+      !aligned16(o) || !aligned4(len) || !aligned4(lse_out) || !aligned4(sel_out))
+    return KV_ERR_INVALID_ARG;
+  return launch_attn_blocks(q, K, V, len, digest, B, Hq, Hkv, nq, cap, d, block, n_sel, sink, recent, st[0], st[1], scale, dtype,
+                            o, lse_out, sel_out, dev_status, static_cast<cudaStream_t>(stream));
+}
+
+int kv_attn_shared(const void *q, const void *Kp, const void *Vp, const void *K, const void *V, const int32_t *len, int B,
+                   int Hq, int Hkv, int nq, int P, int cap, int d, const int64_t *strides, float scale, int dtype, void *o,
+                   float *lse_out, void *workspace, size_t workspace_bytes, int *dev_status, kv_stream_t stream) {
+  if (B < 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0 || nq < 0 || P < 0 || cap < 0 || !dtype_ok(dtype) || !(scale > 0) ||
+      !std::isfinite(scale))
+    return KV_ERR_INVALID_ARG;
+  if (!dim_ok(d)) return KV_ERR_UNSUPPORTED;
+  if (!fits((long long)B * Hkv, (long long)cap * d) || !fits((long long)B * Hq, (long long)nq * d) ||
+      !fits(Hkv, (long long)P * d) || (long long)B * (Hq / Hkv) > INT_MAX || (long long)B * (Hq / Hkv) * nq > INT_MAX)
+    return KV_ERR_INVALID_ARG;
+  if (B == 0 || nq == 0) return KV_OK;
+  long long st[10];
+  const long long rows[3] = {B, Hq, nq}, keys[2] = {P > 0 ? Hkv : 0, P};
+  if (!row_strides(strides, rows, 3, d, dtype, st) || !row_strides(strides ? strides + 3 : nullptr, keys, 2, d, dtype, st + 3) ||
+      !row_strides(strides ? strides + 5 : nullptr, keys, 2, d, dtype, st + 5) ||
+      !row_strides(strides ? strides + 7 : nullptr, rows, 3, d, dtype, st + 7))
+    return KV_ERR_INVALID_ARG;
+  if (!q || !o || (P > 0 && (!Kp || !Vp)) || (cap > 0 && (!K || !V || !len)) || !aligned16(q) || !aligned16(o) || !aligned16(Kp) ||
+      !aligned16(Vp) || !aligned16(K) || !aligned16(V) || !aligned4(len) || !aligned4(lse_out))
+    return KV_ERR_INVALID_ARG;
+  const size_t need = attn_shared_workspace_bytes(B, Hq, Hkv, nq, P, d, dtype);
+  if (need && (!workspace || workspace_bytes < need || !aligned16(workspace))) return KV_ERR_WORKSPACE;
+  return launch_attn_shared(q, Kp, Vp, K, V, len, B, Hq, Hkv, nq, P, cap, d, st, scale, dtype, o, lse_out, workspace,
+                            dev_status, static_cast<cudaStream_t>(stream));
+}
+
+int kv_rope_freqs(int rot, double theta, const kv_rope_scaling *scaling, double *inv_freq, float *rot_scale) {
+  return rope_freqs(rot, theta, scaling, inv_freq, rot_scale);
 }
 
 }  // extern "C"

@@ -161,4 +161,19 @@ int launch_decode_q8(const void *q, const void *k_new, const void *v_new, const 
                      int *status, cudaStream_t st);
 size_t decode_q8_workspace_bytes(long units, int G, int cap, int d);
 
+int launch_qk_norm_rope(const kv_qkv_heads &h, int *status, cudaStream_t st);
+int launch_block_digest(const void *K, const int32_t *len, long units, int cap, int d, int block, int n_new, int dtype,
+                        void *digest, int *status, cudaStream_t st);
+bool attn_blocks_fits(int nb);
+int launch_attn_blocks(const void *q, const void *K, const void *V, const int32_t *len, const void *digest, int B, int Hq,
+                       int Hkv, int nq, int cap, int d, int block, int n_sel, int sink, int recent, const long long *sq,
+                       const long long *so, float scale, int dtype, void *o, float *lse, int32_t *sel, int *status,
+                       cudaStream_t st);
+// strides: batch, head, token of q; head, token of the prefix's K and V; batch, head, token of o
+int launch_attn_shared(const void *q, const void *Kp, const void *Vp, const void *K, const void *V, const int32_t *len, int B,
+                       int Hq, int Hkv, int nq, int P, int cap, int d, const long long *strides, float scale, int dtype, void *o,
+                       float *lse, void *ws, int *status, cudaStream_t st);
+size_t attn_shared_workspace_bytes(int B, int Hq, int Hkv, int nq, int P, int d, int dtype);
+int rope_freqs(int rot, double theta, const kv_rope_scaling *s, double *f, float *rot_scale);
+
 }  // namespace kvc

@@ -1,0 +1,244 @@
+// rows_stream.cuh -- softmax attention of up to 8 query rows over a stream of cache slots, one
+// warp's share: what block-sparse attention and the shared prefix's own slots have in common.
+//
+// The warp takes 16 slots at a time as the long side of warp-level products: logits
+// L^T = K Q^T (16 slots x 8 rows), outputs O^T += V^T P^T (d x 8 rows).  Which element of d stands at
+// which k is free as long as both operands agree, so a lane takes 16 consecutive bytes of a
+// row and K, V and the digests go from memory to registers as they lie; only P is transposed
+// (in registers).  A lane holds the rows 2t and 2t + 1 of the 8, t = lane % 4.
+//   bf16: K and q are exact; P enters as hi + lo, so that the weights keep 16 bits.
+//   fp32: every operand as two tf32 parts (mma_common.cuh), O's tiles added outside the unit.
+// The reference m of a row moves only when a logit passes it by kLazyRows (log2 units), so O
+// is rarely rescaled.
+// Loads go past the first-level cache: a kernel that has not yet waited for the one in front of
+// it (but knows that those before that one are complete) may read what they wrote.
+#pragma once
+
+#include "kvc_internal.cuh"
+#include "mma_common.cuh"
+#include "tc_common.cuh"
+
+namespace kvc {
+
+constexpr float kLazyRows = 6.f;
+
+// c (+)= 16 rows x 8 columns over the 32 (bf16) or 16 (fp32) elements that four lanes' vectors hold.
+__device__ __forceinline__ void dot16(float (&c)[4], float (&)[4], const uint4 &x0, const uint4 &x1, const uint4 &q,
+                                      __nv_bfloat16) {
+  mma_bf16(c, x0.x, x1.x, x0.y, x1.y, q.x, q.y);
+  mma_bf16(c, x0.z, x1.z, x0.w, x1.w, q.z, q.w);
+}
+__device__ __forceinline__ void dot16(float (&c)[4], float (&small)[4], const uint4 &x0, const uint4 &x1, const uint4 &q,
+                                      float) {
+  Split a[4], b0, b1;
+  a[0].set(__uint_as_float(x0.x));
+  a[1].set(__uint_as_float(x1.x));
+  a[2].set(__uint_as_float(x0.y));
+  a[3].set(__uint_as_float(x1.y));
+  b0.set(__uint_as_float(q.x));
+  b1.set(__uint_as_float(q.y));
+  mma_split(c, small, a, b0, b1);
+  a[0].set(__uint_as_float(x0.z));
+  a[1].set(__uint_as_float(x1.z));
+  a[2].set(__uint_as_float(x0.w));
+  a[3].set(__uint_as_float(x1.w));
+  b0.set(__uint_as_float(q.z));
+  b1.set(__uint_as_float(q.w));
+  mma_split(c, small, a, b0, b1);
+}
+
+// log2 units
+__device__ __forceinline__ float rows_max(float x) {  // over the 16 slots: the lanes with the same t
+  x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 4));
+  x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 8));
+  return fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 16));
+}
+
+template <typename T, int D>
+struct RowStream {
+  static constexpr int NCH = D * (int)sizeof(T) / 64;  // 64-byte chunks of a row
+  static constexpr int VV = D / 8 * (int)sizeof(T) / 16;  // vectors of a lane's D / 8 elements of a V row
+  static constexpr int MT = D / 16;
+
+  uint4 q[NCH];      // column g = lane / 4 of the 8: its row's chunks, bytes 16 t
+  uint4 kw[2][NCH];  // K rows of slots g and g + 8
+  uint4 vw[4][VV];   // V rows of four slots, elements g D / 8 ..
+  float o[MT][4];    // elements g D / 8 + 2 i + {0, 0, 1, 1}, rows 2t + {0, 1, 0, 1}
+  float m[2], z[2];
+  int g, t;
+
+  __device__ __forceinline__ void init() {
+    const int lane = threadIdx.x & 31;
+    g = lane >> 2;
+    t = lane & 3;
+    m[0] = m[1] = -INFINITY;
+    z[0] = z[1] = 0.f;
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) o[i][j] = 0.f;
+  }
+  // `row`: the query row of column g
+  __device__ __forceinline__ void load_q(const T *row) {
+#pragma unroll
+    for (int c = 0; c < NCH; ++c) q[c] = __ldcg(reinterpret_cast<const uint4 *>(reinterpret_cast<const char *>(row) + c * 64 + t * 16));
+  }
+  // Slots j .. j + 15 of the dense rows at k; slots behind `last` stand for it (they are hidden later).
+  __device__ __forceinline__ void load_k(const T *k, long st, int j, int last) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const char *p = reinterpret_cast<const char *>(k + (long)min(j + g + 8 * h, last) * st) + t * 16;
+#pragma unroll
+      for (int c = 0; c < NCH; ++c) kw[h][c] = __ldcg(reinterpret_cast<const uint4 *>(p + c * 64));
+    }
+  }
+  // bf16: slots 2t, 2t + 1, 2t + 8, 2t + 9 (the k indices of a lane); fp32: t, t + 4, t + 8, t + 12.
+  __device__ __forceinline__ void load_v(const T *v, long st, int j, int last) {
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int s = sizeof(T) == 2 ? 2 * t + (r & 1) + 8 * (r >> 1) : t + 4 * r;
+      const uint4 *p = reinterpret_cast<const uint4 *>(v + (long)min(j + s, last) * st + g * (D / 8));
+#pragma unroll
+      for (int c = 0; c < VV; ++c) vw[r][c] = __ldcg(p + c);
+    }
+  }
+  // Logits of the loaded K tile, log2 units: l[0], l[1] slot g of rows 2t, 2t + 1; l[2], l[3] slot g + 8.
+  __device__ __forceinline__ void logits(float c_log2, float (&l)[4]) {
+    float small[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) l[i] = 0.f;
+#pragma unroll
+    for (int c = 0; c < NCH; ++c) dot16(l, small, kw[0][c], kw[1][c], q[c], T());
+#pragma unroll
+    for (int i = 0; i < 4; ++i) l[i] = (sizeof(T) == 4 ? l[i] + small[i] : l[i]) * c_log2;
+  }
+  // Row 2t + x sees the slots below n[x]; j: the tile's first slot.
+  __device__ __forceinline__ static void hide(float (&l)[4], int g, int j, const int (&n)[2]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (j + g + 8 * (i >> 1) >= n[i & 1]) l[i] = -INFINITY;
+  }
+  // The softmax's step and O += P V with the loaded V tile.
+  __device__ __forceinline__ void add(const float (&l)[4]) {
+    const float a = fmaxf(l[0], l[2]), b = fmaxf(l[1], l[3]);
+    if (__any_sync(0xFFFFFFFFu, a > m[0] + kLazyRows || b > m[1] + kLazyRows)) {
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const float mn = fmaxf(m[x], rows_max(x ? b : a));
+        const float f = mn == -INFINITY ? 1.f : tc::ex2(m[x] - mn);
+        m[x] = mn;
+        z[x] *= f;
+#pragma unroll
+        for (int i = 0; i < MT; ++i) {
+          o[i][x] *= f;
+          o[i][2 + x] *= f;
+        }
+      }
+    }
+    float p[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float ref = m[i & 1];
+      p[i] = tc::ex2(l[i] - (ref == -INFINITY ? 0.f : ref));
+    }
+    z[0] += p[0] + p[2];
+    z[1] += p[1] + p[3];
+    product(p, T());
+  }
+  __device__ __forceinline__ void product(const float (&p)[4], __nv_bfloat16) {
+    uint32_t b[2][2];  // hi, lo
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const __nv_bfloat162 hi = __floats2bfloat162_rn(p[2 * h], p[2 * h + 1]);
+      const uint32_t w = *reinterpret_cast<const uint32_t *>(&hi);
+      const __nv_bfloat162 lo =
+          __floats2bfloat162_rn(p[2 * h] - __uint_as_float(w << 16), p[2 * h + 1] - __uint_as_float(w & 0xFFFF0000u));
+      b[0][h] = transpose8x8(w);
+      b[1][h] = transpose8x8(*reinterpret_cast<const uint32_t *>(&lo));
+    }
+#pragma unroll
+    for (int c = 0; c < VV; ++c) {
+      const uint32_t w0[4] = {vw[0][c].x, vw[0][c].y, vw[0][c].z, vw[0][c].w};
+      const uint32_t w1[4] = {vw[1][c].x, vw[1][c].y, vw[1][c].z, vw[1][c].w};
+      const uint32_t w2[4] = {vw[2][c].x, vw[2][c].y, vw[2][c].z, vw[2][c].w};
+      const uint32_t w3[4] = {vw[3][c].x, vw[3][c].y, vw[3][c].z, vw[3][c].w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t a0 = __byte_perm(w0[i], w1[i], 0x5410), a1 = __byte_perm(w0[i], w1[i], 0x7632);
+        const uint32_t a2 = __byte_perm(w2[i], w3[i], 0x5410), a3 = __byte_perm(w2[i], w3[i], 0x7632);
+        mma_bf16(o[c * 4 + i], a0, a1, a2, a3, b[0][0], b[0][1]);
+        mma_bf16(o[c * 4 + i], a0, a1, a2, a3, b[1][0], b[1][1]);
+      }
+    }
+  }
+  __device__ __forceinline__ void product(const float (&p)[4], float) {
+    // operand of the two k steps: slots t, t + 4 and t + 8, t + 12 of row g; lane 4 s + r / 2 holds slot s of row r
+    Split b[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int src = (t + 4 * (k & 1)) * 4 + (g >> 1);
+      const float even = __shfl_sync(0xFFFFFFFFu, p[2 * (k >> 1)], src), odd = __shfl_sync(0xFFFFFFFFu, p[2 * (k >> 1) + 1], src);
+      b[k].set(g & 1 ? odd : even);
+    }
+#pragma unroll
+    for (int i = 0; i < MT; ++i) {
+      float c[4] = {0.f, 0.f, 0.f, 0.f}, small[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        Split a[4];
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {  // (element, slot): (0, t), (1, t), (0, t + 4), (1, t + 4)
+          const uint4 &w = vw[2 * k + (x >> 1)][i >> 1];
+          a[x].set(__uint_as_float(i & 1 ? (x & 1 ? w.w : w.z) : (x & 1 ? w.y : w.x)));
+        }
+        mma_split(c, small, a, b[2 * k], b[2 * k + 1]);
+      }
+#pragma unroll
+      for (int x = 0; x < 4; ++x) o[i][x] += c[x] + small[x];
+    }
+  }
+  // This warp's share of the rows below R: reference, sum of weights, output sums [R][D].
+  __device__ __forceinline__ void leave(int R, float *wm, float *wz, float *so) {
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      z[x] += __shfl_xor_sync(0xFFFFFFFFu, z[x], 4);
+      z[x] += __shfl_xor_sync(0xFFFFFFFFu, z[x], 8);
+      z[x] += __shfl_xor_sync(0xFFFFFFFFu, z[x], 16);
+      const int r = 2 * t + x;
+      if (r < R) {
+        if (g == 0) {
+          wm[r] = m[x];
+          wz[r] = z[x];
+        }
+        float *dst = so + r * D + g * (D / 8);
+#pragma unroll
+        for (int i = 0; i < MT; ++i) *reinterpret_cast<float2 *>(dst + 2 * i) = make_float2(o[i][x], o[i][2 + x]);
+      }
+    }
+  }
+};
+
+// The shares of NW warps (wm, wz [NW][8], so [NW][R][D]) as one: sh [R][D], mz [R].  A share without
+// slots has z = 0 and weighs nothing; a NaN in z is passed on.
+template <int D, int NW>
+__device__ __forceinline__ void join_warps(int R, const float *wm, const float *wz, const float *so, float *sh, float2 *mz) {
+  for (int i = threadIdx.x; i < R * D; i += 32 * NW) {
+    const int r = i / D;
+    float M = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < NW; ++w)
+      if (wz[w * 8 + r] != 0.f) M = fmaxf(M, wm[w * 8 + r]);
+    float v = 0.f, Z = 0.f;
+#pragma unroll
+    for (int w = 0; w < NW; ++w)
+      if (wz[w * 8 + r] != 0.f) {
+        const float f = M == -INFINITY ? 1.f : tc::ex2(wm[w * 8 + r] - M);
+        v += f * so[w * R * D + i];
+        Z += f * wz[w * 8 + r];
+      }
+    sh[i] = v;
+    if (i % D == 0) mz[r] = make_float2(M, Z);
+  }
+}
+
+}  // namespace kvc
