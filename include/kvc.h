@@ -720,7 +720,7 @@ KVC_API int kv_attn_blocks(const void *q, const void *K, const void *V, const in
  *              of Kp; of Vp; batch, head and token of o; conditions as for kv_attn_blocks;
  *              NULL = dense
  *   lse_out    [B][Hq][nq] float32, may be NULL
- *   workspace  >= kv_workspace_size(KV_OP_ATTN_SHARED, B, Hq, Hkv, P, d, nq, 0)
+ *   workspace  >= kv_workspace_size(KV_OP_ATTN_SHARED, B, Hq, Hkv, max(1, P), d, nq, P)
  *   dev_status device int, may be NULL; KV_ERR_INVALID_ARG when a len is outside [0, cap]
  *              (that unit's outputs are left as they were), KV_ERR_TIMEOUT when a bounded
  *              device-side wait gave up; never cleared
@@ -738,7 +738,7 @@ KVC_API int kv_attn_shared(const void *q, const void *Kp, const void *Vp, const 
  * Arguments that an op does not use are ignored; for KV_OP_HUBKV_REFINE pass the
  * refine call's head count H as Hkv; for KV_OP_DECODE and KV_OP_DECODE_Q8 pass the slot
  * capacity as T; for KV_OP_ATTN_PROMPT pass Tk as T, Tq as W and n_seq as k; for
- * KV_OP_ATTN_SHARED pass P as T and nq as W;
+ * KV_OP_ATTN_SHARED pass max(1, P) as T, nq as W and P as k;
  * for KV_OP_SCORE_NESTED pass H as Hkv and n_blocks as W.
  * Returns 0 for invalid sizes. */
 KVC_API size_t kv_workspace_size(int op, int B, int Hq, int Hkv, int T, int d, int W, int k);

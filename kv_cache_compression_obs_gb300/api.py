@@ -712,9 +712,64 @@ def kv_rope_freqs(rot: int, theta: float = 10000.0, scaling: str | None = None, 
     return torch.tensor(f[:rot // 2], dtype=torch.float64, device=device), scale.value
 
 
+def _sig(t):
+    """What a call's checks read of a tensor."""
+    return None if t is None else (t.shape, t.stride(), t.dtype)
+
+
+# Checks that depend on shapes, strides and types alone are made once for each combination of them: a call
+# then reads each property of a tensor once and looks the answer up.
 @functools.lru_cache(maxsize=4096)
-def _strides6(*st):
-    return (ctypes.c_int64 * 18)(*[x for t in st for x in (t[:3] if t else (0, 0, 0))])
+def _rope_plan(q, k, v, q_out, k_out, v_out, inv_freq, pos, q_weight, k_weight, slot, seq):
+    """The call's strides and sizes as the library takes them, or ValueError."""
+    x = q or k or v
+    (B, _, T, d), _, dt = x
+    if k and v and k[0] != v[0]:
+        raise ValueError("k and v disagree in shape")
+    for t in (q, k, v):
+        if t and (len(t[0]) != 4 or t[0][0] != B or t[0][2] != T or t[0][3] != d or t[2] != dt):
+            raise ValueError("q, k and v disagree in batch, tokens, head dim or dtype")
+    for t in (q_weight, k_weight):
+        if t and (t[0] != (d,) or t[2] != dt or t[1] != (1,)):
+            raise ValueError("weights must be [d] in q's dtype")
+    if inv_freq and (inv_freq[2] != torch.float64 or len(inv_freq[0]) != 1 or (inv_freq[0][0] > 1 and inv_freq[1] != (1,))):
+        raise ValueError("inv_freq must be [rot / 2] float64")
+    kv = k or v
+    Hkv = kv[0][1] if kv else 0
+    for t, shape in ((pos, (B, T)), (slot, (B, Hkv)), (seq, (B,))):
+        if t and (t[2] != _I32 or t[0] != shape or not _dense(t)):
+            raise ValueError("pos must be [B][T], slot [B][Hkv] and seq [B], all int32 and contiguous")
+    if q and (q_out[0] != q[0] or q_out[2] != dt):
+        raise ValueError("q_out must match q")
+    cap = None
+    for t, o in ((k, k_out), (v, v_out)):
+        if t:
+            if len(o[0]) != 4 or o[0][0] != B or o[0][1] != Hkv or o[0][3] != d or o[2] != dt or cap not in (None, o[0][2]):
+                raise ValueError("k_out and v_out must be [B][Hkv][cap][d] in q's dtype")
+            cap = o[0][2]
+    strides = []
+    for t, on in ((q, q), (k, k), (v, v), (q_out, q), (k_out, k), (v_out, v)):
+        if on and t[1][3] != 1:
+            raise ValueError("the d elements of a row must be adjacent")
+        strides += t[1][:3] if on else (0, 0, 0)
+    return ((ctypes.c_int64 * 18)(*strides), B, q[0][1] if q else 0, Hkv, T, cap or 0, d, 2 * inv_freq[0][0] if inv_freq else 0,
+            {torch.bfloat16: KV_BF16, torch.float32: KV_F32}.get(dt, -1))
+
+
+def _dense(t) -> bool:
+    """Whether a signature is that of a contiguous tensor."""
+    step = 1
+    for n, s in zip(reversed(t[0]), reversed(t[1])):
+        if n > 1 and s != step:
+            return False
+        step *= n
+    return True
+
+
+def _same_device(dev: int, *ts):
+    for t in ts:
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"tensors must be on cuda:{dev}")
 
 
 def kv_qk_norm_rope(q, k, v, inv_freq, pos=None, q_weight=None, k_weight=None, eps: float | None = None,
@@ -730,91 +785,108 @@ def kv_qk_norm_rope(q, k, v, inv_freq, pos=None, q_weight=None, k_weight=None, e
     1 + those.  k_out, v_out [B][Hkv][cap][d]: with slot [B][Hkv] int32 (a slot cache's len) token t goes to row
     slot + t, without it to row t; other rows stay.  seq [B] int32: only the first tokens of each row.  Outputs
     not given are dense tensors of T rows (with slot, k_out and v_out have to be given)."""
-    given = [t for t in (q, k, v) if t is not None]
-    if not given:
+    x = q if q is not None else k if k is not None else v
+    if x is None:
         raise ValueError("one of q, k and v must be given")
-    x = given[0]
-    B, _, T, d = x.shape
-    dt, dev = x.dtype, _device_of(x)
-    kv = k if k is not None else v
-    if k is not None and v is not None and k.shape != v.shape:
-        raise ValueError("k and v disagree in shape")
-    for t in given:
-        if t.dim() != 4 or t.shape[0] != B or t.shape[2] != T or t.shape[3] != d or t.dtype != dt:
-            raise ValueError("q, k and v disagree in batch, tokens, head dim or dtype")
-    if slot is not None and ((k is not None and k_out is None) or (v is not None and v_out is None)):
-        raise ValueError("slot needs k_out and v_out")
-    for t, n in ((q_weight, (d,)), (k_weight, (d,))):
-        if t is not None and (t.shape != n or t.dtype != dt):
-            raise ValueError("weights must be [d] in q's dtype")
-    if inv_freq is not None and (inv_freq.dtype != torch.float64 or inv_freq.dim() != 1):
-        raise ValueError("inv_freq must be [rot / 2] float64")
-    Hkv = kv.shape[1] if kv is not None else 0
-    for t, shape in ((pos, (B, T)), (slot, (B, Hkv)), (seq, (B,))):
-        if t is not None and (t.dtype != _I32 or t.shape != shape):
-            raise ValueError("pos must be [B][T], slot [B][Hkv] and seq [B], all int32")
-    with _side(stream):
-        if q is not None and q_out is None:
-            q_out = q.new_empty(q.shape)
-        if k is not None and k_out is None:
-            k_out = k.new_empty(k.shape)
-        if v is not None and v_out is None:
-            v_out = v.new_empty(v.shape)
-    if q is not None and (q_out.shape != q.shape or q_out.dtype != dt):
-        raise ValueError("q_out must match q")
-    cap = 0
-    for t, o in ((k, k_out), (v, v_out)):
-        if t is not None:
-            if o.dim() != 4 or o.shape[0] != B or o.shape[1] != Hkv or o.shape[3] != d or o.dtype != dt \
-                    or (cap and o.shape[2] != cap):
-                raise ValueError("k_out and v_out must be [B][Hkv][cap][d] in q's dtype")
-            cap = o.shape[2]
-    six = (q, k, v, q_out if q is not None else None, k_out if k is not None else None, v_out if v is not None else None)
-    for t in six:
-        if t is not None and (t.get_device() != dev or t.stride(3) != 1):
-            raise ValueError(f"tensors must be on cuda:{dev} with adjacent elements along d")
-    _on(dev, inv_freq, pos, q_weight, k_weight, slot, seq, dev_status)
+    dev = _device_of(x)
+    if (q_out is None and q is not None) or (k_out is None and k is not None) or (v_out is None and v is not None):
+        if slot is not None and ((k is not None and k_out is None) or (v is not None and v_out is None)):
+            raise ValueError("slot needs k_out and v_out")
+        with _side(stream):
+            if q is not None and q_out is None:
+                q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+            if k is not None and k_out is None:
+                k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
+            if v is not None and v_out is None:
+                v_out = torch.empty(v.shape, dtype=v.dtype, device=v.device)
+    if q is None:
+        q_out = None
+    if k is None:
+        k_out = None
+    if v is None:
+        v_out = None
+    strides, B, Hq, Hkv, T, cap, d, rot, code = _rope_plan(
+        _sig(q), _sig(k), _sig(v), _sig(q_out), _sig(k_out), _sig(v_out), _sig(inv_freq), _sig(pos), _sig(q_weight),
+        _sig(k_weight), _sig(slot), _sig(seq))
+    if code < 0:
+        _dtype_code(x)
+    _same_device(dev, q, k, v, q_out, k_out, v_out, inv_freq, pos, q_weight, k_weight, slot, seq, dev_status)
     flags = (KV_ROPE_INTERLEAVED if interleaved else 0) | (KV_ROPE_ONE_PLUS if one_plus else 0)
     if eps is not None:
         flags |= KV_ROPE_NORM
-    a = _QkvHeads(*[_at(t) for t in six], _at(q_weight), _at(k_weight), _at(inv_freq), _at(pos), _at(slot), _at(seq),
-                  _strides6(*[None if t is None else t.stride() for t in six]), B, 0 if q is None else q.shape[1], Hkv, T, cap,
-                  d, 0 if inv_freq is None else 2 * inv_freq.numel(), 0.0 if eps is None else float(eps), float(rot_scale),
-                  flags, _dtype_code(x))
-    _check("kv_qk_norm_rope", _lib.kv_qk_norm_rope(ctypes.byref(a), _at(dev_status), _stream_of(dev, stream)))
-    return six[3:]
+    a = _QkvHeads(_at(q), _at(k), _at(v), _at(q_out), _at(k_out), _at(v_out), _at(q_weight), _at(k_weight), _at(inv_freq),
+                  _at(pos), _at(slot), _at(seq), strides, B, Hq, Hkv, T, cap, d, rot, 0.0 if eps is None else eps, rot_scale,
+                  flags, code)
+    status = _lib.kv_qk_norm_rope(a, _at(dev_status), _stream_of(dev, stream))
+    if status:
+        _check("kv_qk_norm_rope", status)
+    return q_out, k_out, v_out
 
 
-def _slot_cache(K, V, len_, dt, dev: int):
-    """Checks of a slot cache [B][Hkv][cap][d] that is read; returns its shape."""
-    if K.dim() != 4 or V.shape != K.shape or K.dtype != dt or V.dtype != dt:
-        raise ValueError("K and V must be [B][Hkv][cap][d] in q's dtype")
-    if len_.dtype != _I32 or len_.shape != K.shape[:2]:
-        raise ValueError("len must be [B][Hkv] int32")
-    _on(dev, K, V, len_)
-    return K.shape
+_CODES = {torch.bfloat16: KV_BF16, torch.float32: KV_F32}
 
 
-def _out_rows(q, out, lse_out, dev: int):
-    """Output tensors of an attention call with queries q [B][Hq][n][d], made where they are not given."""
-    B, Hq, n, _ = q.shape
-    o = out if out is not None else torch.empty_like(q)
-    lse = lse_out if lse_out is not None else q.new_empty((B, Hq, n), dtype=_F32)
-    if out is not None and (o.shape != q.shape or o.dtype != q.dtype):
-        raise ValueError("out must match q")
-    if lse_out is not None and (lse.shape != (B, Hq, n) or lse.dtype != _F32):
-        raise ValueError("lse_out must be [B][Hq][n] float32")
-    for t in (q, o):
-        if t.stride(3) != 1 or t.get_device() != dev:
-            raise ValueError(f"tensors must be on cuda:{dev} with adjacent elements along d")
-    _on(dev, lse)
-    return o, lse
+def _rows_plan(q, o, lse):
+    """Checks of queries [B][Hq][n][d] and of the outputs that are given."""
+    if len(q[0]) != 4 or q[1][3] != 1:
+        raise ValueError("q must be [B][Hq][n][d] with adjacent elements along d")
+    if o and (o[0] != q[0] or o[2] != q[2] or o[1][3] != 1):
+        raise ValueError("out must match q, with adjacent elements along d")
+    if lse and (lse[0] != q[0][:3] or lse[2] != _F32 or not _dense(lse)):
+        raise ValueError("lse_out must be [B][Hq][n] float32, contiguous")
+    if q[2] not in _CODES:
+        raise TypeError(f"expected bfloat16 or float32, got {q[2]}")
+
+
+def _cache_plan(q, K, V, ln):
+    """Checks of a dense slot cache [B][Hkv][cap][d] that queries read."""
+    if len(K[0]) != 4 or V[0] != K[0] or K[2] != q[2] or V[2] != q[2] or not _dense(K) or not _dense(V):
+        raise ValueError("K and V must be [B][Hkv][cap][d] in q's dtype, contiguous")
+    if ln[2] != _I32 or ln[0] != K[0][:2] or not _dense(ln):
+        raise ValueError("len must be [B][Hkv] int32, contiguous")
+    if K[0][0] != q[0][0] or K[0][3] != q[0][3]:
+        raise ValueError("q and the cache disagree in batch or head dim")
+
+
+def _flat(*st):
+    return (ctypes.c_int64 * sum(len(t) for t in st))(*[x for t in st for x in t])
 
 
 @functools.lru_cache(maxsize=4096)
-def _row_strides(*st):
-    flat = [x for t in st for x in t[:-1]]
-    return (ctypes.c_int64 * len(flat))(*flat)
+def _blocks_plan(q, K, V, ln, dig, o, lse, sel, block, n_sel):
+    _rows_plan(q, o, lse)
+    _cache_plan(q, K, V, ln)
+    B, Hq, n, d = q[0]
+    _, Hkv, cap, _ = K[0]
+    if block <= 0 or dig[2] != q[2] or dig[0] != (B, Hkv, -(-cap // block), 2, d) or not _dense(dig):
+        raise ValueError("digest must be [B][Hkv][ceil(cap / block)][2][d] in q's dtype, contiguous")
+    if sel and (sel[0] != (B, Hkv, n, n_sel) or sel[2] != _I32 or not _dense(sel)):
+        raise ValueError("sel_out must be [B][Hkv][n][n_sel] int32, contiguous")
+    return B, Hq, Hkv, n, cap, d, _CODES[q[2]], d ** -0.5
+
+
+@functools.lru_cache(maxsize=4096)
+def _out_strides(q, o, prefix=()):
+    return _flat(q[:3], *[t[:2] for t in prefix], o[:3])
+
+
+@functools.lru_cache(maxsize=4096)
+def _shared_plan(q, kp, vp, K, V, ln, o, lse):
+    _rows_plan(q, o, lse)
+    if (not kp) != (not vp) or (not K) != (not V) or (not K) != (not ln) or not (K or kp):
+        raise ValueError("a prefix (K_prefix, V_prefix) or own slots (K, V, len_) must be given, each whole")
+    B, Hq, n, d = q[0]
+    cap = P = 0
+    Hkv = K[0][1] if K else kp[0][0]
+    if K:
+        _cache_plan(q, K, V, ln)
+        cap = K[0][2]
+    if kp:
+        P = kp[0][1] if len(kp[0]) == 3 else -1
+        if kp[0] != (Hkv, P, d) or vp[0] != kp[0] or kp[2] != q[2] or vp[2] != q[2] or kp[1][2] != 1 or vp[1][2] != 1:
+            raise ValueError("the prefix must be [Hkv][P][d] in q's dtype, with adjacent elements along d")
+    return (B, Hq, Hkv, n, P, cap, d, _CODES[q[2]], d ** -0.5, kv_workspace_size(KV_OP_ATTN_SHARED, B, Hq, Hkv, max(1, P), d, n, P),
+            (kp[1], vp[1]) if kp else ((0, 0, 1), (0, 0, 1)))
 
 
 def kv_block_digest(K: torch.Tensor, block: int, len_=None, n_new: int | None = None, out=None, dev_status=None, stream=None):
@@ -850,27 +922,25 @@ def kv_attn_blocks(q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, len_: torc
     The new tokens are the last n filled slots; token t sees the slots j < len - n + t + 1.  Each (token, KV head)
     attends the first `sink` and last `recent` of the blocks that it sees and the others with the largest bounds on
     their logits, n_sel in all.  q's and out's batch, head and token strides are free."""
-    B, Hq, n, d = q.shape
-    dev, dt = _device_of(q), q.dtype
-    shape = _slot_cache(K, V, len_, dt, dev)
-    if shape[0] != B or shape[3] != d:
-        raise ValueError("q and the cache disagree in batch or head dim")
-    Hkv, cap = shape[1], shape[2]
-    if digest.dtype != dt or block <= 0 or digest.shape != (B, Hkv, -(-cap // block), 2, d):
-        raise ValueError("digest must be [B][Hkv][ceil(cap / block)][2][d] in q's dtype")
-    with _side(stream):
-        o, lse = _out_rows(q, out, lse_out, dev)
-        sel = sel_out if sel_out is not None else len_.new_empty((B, Hkv, n, max(0, n_sel)))
-    if sel_out is not None and (sel.shape != (B, Hkv, n, n_sel) or sel.dtype != _I32):
-        raise ValueError("sel_out must be [B][Hkv][n][n_sel] int32")
-    _on(dev, digest, sel, dev_status)
-    if scale is None:
-        scale = d ** -0.5
-    _check("kv_attn_blocks", _lib.kv_attn_blocks(
-        q.data_ptr(), K.data_ptr(), V.data_ptr(), len_.data_ptr(), digest.data_ptr(), B, Hq, Hkv, n, cap, d, int(block),
-        int(n_sel), int(sink), int(recent), _row_strides(q.stride(), o.stride()), float(scale), _dtype_code(q), o.data_ptr(),
-        lse.data_ptr(), sel.data_ptr(), _at(dev_status), _stream_of(dev, stream)))
-    return o, lse, sel
+    dev, qs = _device_of(q), q.stride()
+    B, Hq, Hkv, n, cap, d, code, default_scale = _blocks_plan((q.shape, qs, q.dtype), _sig(K), _sig(V), _sig(len_), _sig(digest),
+                                                              _sig(out), _sig(lse_out), _sig(sel_out), block, n_sel)
+    _same_device(dev, K, V, len_, digest, out, lse_out, sel_out, dev_status)
+    if out is None or lse_out is None or sel_out is None:
+        with _side(stream):
+            if out is None:
+                out = torch.empty_like(q)
+            if lse_out is None:
+                lse_out = torch.empty((B, Hq, n), dtype=_F32, device=q.device)
+            if sel_out is None:
+                sel_out = torch.empty((B, Hkv, n, max(0, n_sel)), dtype=_I32, device=q.device)
+    status = _lib.kv_attn_blocks(
+        q.data_ptr(), K.data_ptr(), V.data_ptr(), len_.data_ptr(), digest.data_ptr(), B, Hq, Hkv, n, cap, d, block, n_sel, sink,
+        recent, _out_strides(qs, out.stride()), default_scale if scale is None else scale, code, out.data_ptr(),
+        lse_out.data_ptr(), sel_out.data_ptr(), _at(dev_status), _stream_of(dev, stream))
+    if status:
+        _check("kv_attn_blocks", status)
+    return out, lse_out, sel_out
 
 
 def kv_attn_shared(q: torch.Tensor, K_prefix, V_prefix, K, V, len_, scale: float | None = None, out=None, lse_out=None,
@@ -881,39 +951,25 @@ def kv_attn_shared(q: torch.Tensor, K_prefix, V_prefix, K, V, len_, scale: float
 
     Every token sees the whole prefix; the new tokens are the last n own slots and token t sees the own slots
     j < len - n + t + 1.  Strides of q, out and the prefix are free but for the d adjacent elements."""
-    B, Hq, n, d = q.shape
-    dev, dt = _device_of(q), q.dtype
-    if (K_prefix is None) != (V_prefix is None) or (K is None) != (V is None) or (K is None) != (len_ is None) \
-            or (K is None and K_prefix is None):
-        raise ValueError("a prefix (K_prefix, V_prefix) or own slots (K, V, len_) must be given, each whole")
-    cap = P = 0
-    Hkv = (K_prefix.shape[0] if K is None else K.shape[1])
-    if K is not None:
-        shape = _slot_cache(K, V, len_, dt, dev)
-        if shape[0] != B or shape[3] != d:
-            raise ValueError("q and the cache disagree in batch or head dim")
-        cap = shape[2]
-    st = q.stride()
-    kp = vp = (0, 0, 1)
-    if K_prefix is not None:
-        P = K_prefix.shape[1]
-        if K_prefix.shape != (Hkv, P, d) or V_prefix.shape != K_prefix.shape or K_prefix.dtype != dt or V_prefix.dtype != dt:
-            raise ValueError("the prefix must be [Hkv][P][d] in q's dtype")
-        kp, vp = K_prefix.stride(), V_prefix.stride()
-        if kp[2] != 1 or vp[2] != 1 or K_prefix.get_device() != dev or V_prefix.get_device() != dev:
-            raise ValueError(f"tensors must be on cuda:{dev} with adjacent elements along d")
-    need = _workspace_bytes(KV_OP_ATTN_SHARED, B, Hq, Hkv, P, d, n, 0)
+    dev, qs = _device_of(q), q.stride()
+    B, Hq, Hkv, n, P, cap, d, code, default_scale, need, prefix = _shared_plan(
+        (q.shape, qs, q.dtype), _sig(K_prefix), _sig(V_prefix), _sig(K), _sig(V), _sig(len_), _sig(out), _sig(lse_out))
+    _same_device(dev, K_prefix, V_prefix, K, V, len_, out, lse_out, workspace, dev_status)
     with _side(stream):
-        o, lse = _out_rows(q, out, lse_out, dev)
+        if out is None:
+            out = torch.empty_like(q)
+        if lse_out is None:
+            lse_out = torch.empty((B, Hq, n), dtype=_F32, device=q.device)
         ws, nbytes = _workspace(need, q.device, workspace)
-    _on(dev, workspace, dev_status)
-    if scale is None:
-        scale = d ** -0.5
-    _check("kv_attn_shared", _lib.kv_attn_shared(
+    if workspace is not None and not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    status = _lib.kv_attn_shared(
         q.data_ptr(), _at(K_prefix), _at(V_prefix), _at(K), _at(V), _at(len_), B, Hq, Hkv, n, P, cap, d,
-        _row_strides(st, kp, vp, o.stride()), float(scale), _dtype_code(q), o.data_ptr(), lse.data_ptr(), _at(ws), nbytes,
-        _at(dev_status), _stream_of(dev, stream)))
-    return o, lse
+        _out_strides(qs, out.stride(), prefix), default_scale if scale is None else scale, code, out.data_ptr(),
+        lse_out.data_ptr(), _at(ws), nbytes, _at(dev_status), _stream_of(dev, stream))
+    if status:
+        _check("kv_attn_shared", status)
+    return out, lse_out
 
 
 def prefill_host_buffers(hQ: torch.Tensor, hK: torch.Tensor, k: int, r: float | None,

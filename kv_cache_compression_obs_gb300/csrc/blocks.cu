@@ -40,7 +40,7 @@ struct BlkArgs {
   long long sq[3], so[3];  // batch, head, token
   int Hq, Hkv, G, nq, cap, nb;
   int b_log2, n_sel, sink, recent;
-  int area;   // bytes of the part of shared memory that the choice and the warps' shares take in turn
+  int area;   // bytes of the part of shared memory that the choice, the warps' rings and their shares take in turn
   float c_log2;
 };
 
@@ -217,7 +217,7 @@ __device__ void choose(const BlkArgs &A, const Choice &c, const T *q, const T *d
 }
 
 template <typename T, int D>
-__global__ void __launch_bounds__(NT, sizeof(T) == 2 ? 4 : 2) blocks_kernel(const __grid_constant__ BlkArgs A) {
+__global__ void __launch_bounds__(NT, sizeof(T) == 2 || D == 64 ? 2 : 1) blocks_kernel(const __grid_constant__ BlkArgs A) {
   extern __shared__ __align__(16) unsigned char dyn[];
   __shared__ float wm[NW * 8], wz[NW * 8];
   __shared__ float2 mz[8], all[16][8];
@@ -259,7 +259,7 @@ __global__ void __launch_bounds__(NT, sizeof(T) == 2 ? 4 : 2) blocks_kernel(cons
   const int nbk = (seen + block - 1) >> A.b_log2;
   const T *q = static_cast<const T *>(A.q) + b * A.sq[0] + (long)h * G * A.sq[1] + t * A.sq[2];
   RowStream<T, D> R;
-  R.init();
+  R.init(area + warp * R.RING);
   R.load_q(q + min(R.g, G - 1) * A.sq[1]);
 
   // ---- which blocks ----
@@ -374,26 +374,14 @@ __global__ void __launch_bounds__(NT, sizeof(T) == 2 ? 4 : 2) blocks_kernel(cons
     const int tiles = ((ns - 1) << tl) + in_last, per = (tiles + CL - 1) / CL;
     const int x0 = min(tiles, rank * per), x1 = min(tiles, x0 + per);
     const T *K = static_cast<const T *>(A.K) + bh * A.cap * (long)D, *V = static_cast<const T *>(A.V) + bh * A.cap * (long)D;
-    auto slot = [&](int x) { return ((int)c.list[x >> tl] << A.b_log2) + ((x & ((1 << tl) - 1)) << 4); };
     const int lim[2] = {seen, seen};
-    int x = x0 + warp;
-    int j = 0;
-    if (x < x1) {
-      j = slot(x);
-      R.load_k(K, D, j, seen - 1);
-      R.load_v(V, D, j, seen - 1);
-    }
-    while (x < x1) {
-      const int nx = x + NW, nj = nx < x1 ? slot(nx) : 0;
-      float l[4];
-      R.logits(A.c_log2, l);
-      if (nx < x1) R.load_k(K, D, nj, seen - 1);
-      if (j + 16 > seen) R.hide(l, R.g, j, lim);
-      R.add(l);
-      if (nx < x1) R.load_v(V, D, nj, seen - 1);
-      x = nx;
-      j = nj;
-    }
+    R.run((x1 - x0 - warp + NW - 1) / NW,
+          [&](int y) {
+            const int x = x0 + y * NW + warp;
+            return ((int)c.list[x >> tl] << A.b_log2) + ((x & ((1 << tl) - 1)) << 4);
+          },
+          K, D, V, D, seen - 1, A.c_log2, lim, seen);
+    __syncthreads();
     R.leave(G, wm + warp * 8, wz + warp * 8, so + warp * G * D);
     __syncthreads();
     join_warps<D, NW>(G, wm, wz, so, sh, mz);
@@ -424,11 +412,11 @@ __global__ void __launch_bounds__(NT, sizeof(T) == 2 ? 4 : 2) blocks_kernel(cons
 
 template <typename T, int D>
 int run(BlkArgs A, long units, cudaStream_t st) {
-  // CTAs per unit: as many as run at once, four an SM (fp32: two)
-  const long room = (sizeof(T) == 2 ? 4L : 2L) * kNumSmsHint;
+  // CTAs per unit: as many as run at once, two an SM (fp32, d = 128: one)
+  const long room = (sizeof(T) == 2 || D == 64 ? 2L : 1L) * kNumSmsHint;
   int CL = 16;
   while (CL > 1 && units * CL > room) CL /= 2;
-  const size_t warps = (size_t)NW * A.G * D * 4, choice = (size_t)A.nb * 12;
+  const size_t warps = NW * RowStream<T, D>::RING, choice = (size_t)A.nb * 12;
   A.area = (int)(((warps > choice ? warps : choice) + 15) & ~(size_t)15);
   const size_t bytes = (size_t)A.G * D * 4 + A.area + ((size_t)(A.nb + CL - 1) / CL + 16) * 4 + (size_t)A.nb * 2 + 16;
   if (units * CL > 0x7FFFFFFFL) return KV_ERR_UNSUPPORTED;

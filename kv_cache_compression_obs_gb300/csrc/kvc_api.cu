@@ -265,12 +265,12 @@ size_t kv_workspace_size(int op, int B, int Hq, int Hkv, int T, int d, int W, in
     case KV_OP_DECODE_Q8:  // T is the slot capacity
       if (Hq <= 0 || Hkv <= 0 || Hq % Hkv || !(d == 64 || d == 128)) return 0;
       return decode_q8_workspace_bytes((long)B * Hkv, Hq / Hkv, T, d);
-    case KV_OP_ATTN_SHARED: {  // T is P, W is nq; enough for either dtype
-      if (Hq <= 0 || Hkv <= 0 || Hq % Hkv || W < 0 || !(d == 64 || d == 128) || (long long)B * (Hq / Hkv) > INT_MAX ||
+    case KV_OP_ATTN_SHARED: {  // k is P, W is nq; enough for either dtype
+      if (Hq <= 0 || Hkv <= 0 || Hq % Hkv || W < 0 || k < 0 || !(d == 64 || d == 128) || (long long)B * (Hq / Hkv) > INT_MAX ||
           !fits((long long)B * (Hq / Hkv), W) || (long long)B * (Hq / Hkv) * W > INT_MAX)
         return 0;
-      const size_t bf = attn_shared_workspace_bytes(B, Hq, Hkv, W, T, d, KV_BF16);
-      const size_t f32 = attn_shared_workspace_bytes(B, Hq, Hkv, W, T, d, KV_F32);
+      const size_t bf = attn_shared_workspace_bytes(B, Hq, Hkv, W, k, d, KV_BF16);
+      const size_t f32 = attn_shared_workspace_bytes(B, Hq, Hkv, W, k, d, KV_F32);
       return bf > f32 ? bf : f32;
     }
     default:
@@ -646,6 +646,10 @@ int kv_attn_shared(const void *q, const void *Kp, const void *Vp, const void *K,
   if (!fits((long long)B * Hkv, (long long)cap * d) || !fits((long long)B * Hq, (long long)nq * d) ||
       !fits(Hkv, (long long)P * d) || (long long)B * (Hq / Hkv) > INT_MAX || (long long)B * (Hq / Hkv) * nq > INT_MAX)
     return KV_ERR_INVALID_ARG;
+  // tiles of 16 slots over all rows, heads and groups of 8 query rows are counted in 32 bits
+  const long long groups = ((long long)(Hq / Hkv) * nq + 7) / 8;
+  if (!fits((long long)B * Hkv, groups * ((cap + 15LL) / 16 + 1)) || (long long)B * Hkv * groups * ((cap + 15LL) / 16 + 1) > INT_MAX / 2)
+    return KV_ERR_UNSUPPORTED;
   if (B == 0 || nq == 0) return KV_OK;
   long long st[10];
   const long long rows[3] = {B, Hq, nq}, keys[2] = {P > 0 ? Hkv : 0, P};

@@ -4,14 +4,21 @@
 // The warp takes 16 slots at a time as the long side of warp-level products: logits
 // L^T = K Q^T (16 slots x 8 rows), outputs O^T += V^T P^T (d x 8 rows).  Which element of d stands at
 // which k is free as long as both operands agree, so a lane takes 16 consecutive bytes of a
-// row and K, V and the digests go from memory to registers as they lie; only P is transposed
+// row and K and V are used as they lie in memory; only P is transposed
 // (in registers).  A lane holds the rows 2t and 2t + 1 of the 8, t = lane % 4.
 //   bf16: K and q are exact; P enters as hi + lo, so that the weights keep 16 bits.
 //   fp32: every operand as two tf32 parts (mma_common.cuh), O's tiles added outside the unit.
 // The reference m of a row moves only when a logit passes it by kLazyRows (log2 units), so O
 // is rarely rescaled.
-// Loads go past the first-level cache: a kernel that has not yet waited for the one in front of
-// it (but knows that those before that one are complete) may read what they wrote.
+//
+// K and V rows come by asynchronous 16-byte copies into a ring of tiles that belongs to the warp
+// alone, so that no barrier holds warps up and what is in flight takes no registers (with the
+// next tile in registers and four CTAs an SM, 512 ragged units of 1124 slots ran at 4.6 TB/s, half of
+// the stalls waiting for the one tile ahead).  16-byte pieces of a row are permuted so that the
+// eight lanes of a shared-memory phase read different banks: K lanes read pieces 4c + t of rows g
+// and g + 1, V lanes pieces 8c + g of four rows.  Rows that do not exist are filled with 0.
+// The copies go past the first-level cache: a kernel that has not yet waited for the one in front
+// of it (but knows that those before that one are complete) may read what they wrote.
 #pragma once
 
 #include "kvc_internal.cuh"
@@ -57,20 +64,24 @@ __device__ __forceinline__ float rows_max(float x) {  // over the 16 slots: the 
 template <typename T, int D>
 struct RowStream {
   static constexpr int NCH = D * (int)sizeof(T) / 64;  // 64-byte chunks of a row
-  static constexpr int VV = D / 8 * (int)sizeof(T) / 16;  // vectors of a lane's D / 8 elements of a V row
+  static constexpr int EV = 16 / (int)sizeof(T);       // elements of a 16-byte piece
+  static constexpr int VV = D / 8 / EV;                // pieces of a lane's D / 8 elements of a V row
   static constexpr int MT = D / 16;
+  static constexpr int ROW = D * (int)sizeof(T), TILE = 32 * ROW;  // bytes; 16 rows of K, then 16 of V
+  static constexpr int STAGES = D == 64 && sizeof(T) == 2 ? 6 : D == 128 && sizeof(T) == 4 ? 2 : 3;
+  static constexpr int RING = STAGES * TILE;  // bytes of a warp
 
-  uint4 q[NCH];      // column g = lane / 4 of the 8: its row's chunks, bytes 16 t
-  uint4 kw[2][NCH];  // K rows of slots g and g + 8
-  uint4 vw[4][VV];   // V rows of four slots, elements g D / 8 ..
-  float o[MT][4];    // elements g D / 8 + 2 i + {0, 0, 1, 1}, rows 2t + {0, 1, 0, 1}
+  uint4 q[NCH];    // column g = lane / 4 of the 8: its row's chunks, bytes 16 t
+  float o[MT][4];  // elements at(i) + {0, 0, 1, 1}, rows 2t + {0, 1, 0, 1}
   float m[2], z[2];
   int g, t;
+  unsigned char *ring;
 
-  __device__ __forceinline__ void init() {
+  __device__ __forceinline__ void init(unsigned char *warp_ring) {
     const int lane = threadIdx.x & 31;
     g = lane >> 2;
     t = lane & 3;
+    ring = warp_ring;
     m[0] = m[1] = -INFINITY;
     z[0] = z[1] = 0.f;
 #pragma unroll
@@ -78,37 +89,73 @@ struct RowStream {
 #pragma unroll
       for (int j = 0; j < 4; ++j) o[i][j] = 0.f;
   }
+  __device__ __forceinline__ int at(int i) const { return 2 * i / EV * 8 * EV + EV * g + 2 * i % EV; }
   // `row`: the query row of column g
   __device__ __forceinline__ void load_q(const T *row) {
 #pragma unroll
     for (int c = 0; c < NCH; ++c) q[c] = __ldcg(reinterpret_cast<const uint4 *>(reinterpret_cast<const char *>(row) + c * 64 + t * 16));
   }
-  // Slots j .. j + 15 of the dense rows at k; slots behind `last` stand for it (they are hidden later).
-  __device__ __forceinline__ void load_k(const T *k, long st, int j, int last) {
+  __device__ __forceinline__ static int k_swizzle(int row) { return (row & 1) << 2; }
+  // the slots of a lane: bf16 2t, 2t + 1, 2t + 8, 2t + 9 (the k indices of its operand); fp32 t, t + 4, t + 8, t + 12
+  __device__ __forceinline__ static int v_slot(int t, int r) { return sizeof(T) == 2 ? 2 * t + (r & 1) + 8 * (r >> 1) : t + 4 * r; }
+  __device__ __forceinline__ static int v_swizzle(int row) { return (sizeof(T) == 2 ? row >> 1 & 3 : row & 3) << 1; }
+  // Slots j .. j + 15 into a stage; those behind `last` become 0.
+  __device__ __forceinline__ void fill(int stage, const T *k, long ks, const T *v, long vs, int j, int last) {
+    constexpr int CPR = ROW / 16;
+    unsigned char *dst = ring + stage * TILE;
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const char *p = reinterpret_cast<const char *>(k + (long)min(j + g + 8 * h, last) * st) + t * 16;
-#pragma unroll
-      for (int c = 0; c < NCH; ++c) kw[h][c] = __ldcg(reinterpret_cast<const uint4 *>(p + c * 64));
+    for (int i = 0; i < 16 * CPR / 32; ++i) {
+      const int e = i * 32 + (threadIdx.x & 31), row = e / CPR, c = e % CPR;
+      const bool there = j + row <= last;
+      const long at = there ? j + row : last;
+      const uint32_t n = there ? 16 : 0;
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(tc::smem_u32(dst + row * ROW + ((c ^ k_swizzle(row)) << 4))),
+                   "l"(reinterpret_cast<const char *>(k + at * ks) + c * 16), "r"(n)
+                   : "memory");
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                       tc::smem_u32(dst + 16 * ROW + row * ROW + ((c ^ v_swizzle(row)) << 4))),
+                   "l"(reinterpret_cast<const char *>(v + at * vs) + c * 16), "r"(n)
+                   : "memory");
     }
   }
-  // bf16: slots 2t, 2t + 1, 2t + 8, 2t + 9 (the k indices of a lane); fp32: t, t + 4, t + 8, t + 12.
-  __device__ __forceinline__ void load_v(const T *v, long st, int j, int last) {
+  // Attends `count` tiles of 16 slots; slot(y): tile y's first.  Slots behind `last` are not there; row 2t + x sees
+  // those below lim[x], and all of them below `whole`.
+  template <typename F>
+  __device__ __forceinline__ void run(int count, F slot, const T *k, long ks, const T *v, long vs, int last, float c_log2,
+                                      const int (&lim)[2], int whole) {
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int s = sizeof(T) == 2 ? 2 * t + (r & 1) + 8 * (r >> 1) : t + 4 * r;
-      const uint4 *p = reinterpret_cast<const uint4 *>(v + (long)min(j + s, last) * st + g * (D / 8));
-#pragma unroll
-      for (int c = 0; c < VV; ++c) vw[r][c] = __ldcg(p + c);
+    for (int s = 0; s < STAGES - 1; ++s) {
+      if (s < count) fill(s, k, ks, v, vs, slot(s), last);
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    }
+    int stage = 0;
+    for (int y = 0; y < count; ++y) {
+      const int ahead = y + STAGES - 1;
+      if (ahead < count) fill(stage == 0 ? STAGES - 1 : stage - 1, k, ks, v, vs, slot(ahead), last);
+      asm volatile("cp.async.commit_group;" ::: "memory");
+      asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 1) : "memory");
+      __syncwarp();
+      float l[4];
+      logits(stage, c_log2, l);
+      const int j = slot(y);
+      if (j + 16 > whole) hide(l, g, j, lim);
+      add(stage, l);
+      __syncwarp();  // the stage may be filled again
+      if (++stage == STAGES) stage = 0;
     }
   }
-  // Logits of the loaded K tile, log2 units: l[0], l[1] slot g of rows 2t, 2t + 1; l[2], l[3] slot g + 8.
-  __device__ __forceinline__ void logits(float c_log2, float (&l)[4]) {
+  // Logits of a stage's K tile, log2 units: l[0], l[1] slot g of rows 2t, 2t + 1; l[2], l[3] slot g + 8.
+  __device__ __forceinline__ void logits(int stage, float c_log2, float (&l)[4]) {
     float small[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int i = 0; i < 4; ++i) l[i] = 0.f;
+    const unsigned char *p = ring + stage * TILE + g * ROW;
+    const int sw = k_swizzle(g);  // of row g + 8 too
 #pragma unroll
-    for (int c = 0; c < NCH; ++c) dot16(l, small, kw[0][c], kw[1][c], q[c], T());
+    for (int c = 0; c < NCH; ++c) {
+      const int at = ((4 * c + t) ^ sw) << 4;
+      dot16(l, small, *reinterpret_cast<const uint4 *>(p + at), *reinterpret_cast<const uint4 *>(p + 8 * ROW + at), q[c], T());
+    }
 #pragma unroll
     for (int i = 0; i < 4; ++i) l[i] = (sizeof(T) == 4 ? l[i] + small[i] : l[i]) * c_log2;
   }
@@ -118,8 +165,8 @@ struct RowStream {
     for (int i = 0; i < 4; ++i)
       if (j + g + 8 * (i >> 1) >= n[i & 1]) l[i] = -INFINITY;
   }
-  // The softmax's step and O += P V with the loaded V tile.
-  __device__ __forceinline__ void add(const float (&l)[4]) {
+  // The softmax's step and O += P V with a stage's V tile.
+  __device__ __forceinline__ void add(int stage, const float (&l)[4]) {
     const float a = fmaxf(l[0], l[2]), b = fmaxf(l[1], l[3]);
     if (__any_sync(0xFFFFFFFFu, a > m[0] + kLazyRows || b > m[1] + kLazyRows)) {
 #pragma unroll
@@ -143,9 +190,17 @@ struct RowStream {
     }
     z[0] += p[0] + p[2];
     z[1] += p[1] + p[3];
-    product(p, T());
+    uint4 vw[4][VV];  // pieces 8c + g of the lane's four slots
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int row = v_slot(t, r);
+      const unsigned char *src = ring + stage * TILE + (16 + row) * ROW;
+#pragma unroll
+      for (int c = 0; c < VV; ++c) vw[r][c] = *reinterpret_cast<const uint4 *>(src + (((8 * c + g) ^ v_swizzle(row)) << 4));
+    }
+    product(vw, p, T());
   }
-  __device__ __forceinline__ void product(const float (&p)[4], __nv_bfloat16) {
+  __device__ __forceinline__ void product(const uint4 (&vw)[4][VV], const float (&p)[4], __nv_bfloat16) {
     uint32_t b[2][2];  // hi, lo
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
@@ -171,7 +226,7 @@ struct RowStream {
       }
     }
   }
-  __device__ __forceinline__ void product(const float (&p)[4], float) {
+  __device__ __forceinline__ void product(const uint4 (&vw)[4][VV], const float (&p)[4], float) {
     // operand of the two k steps: slots t, t + 4 and t + 8, t + 12 of row g; lane 4 s + r / 2 holds slot s of row r
     Split b[4];
 #pragma unroll
@@ -210,9 +265,9 @@ struct RowStream {
           wm[r] = m[x];
           wz[r] = z[x];
         }
-        float *dst = so + r * D + g * (D / 8);
+        float *dst = so + r * D;
 #pragma unroll
-        for (int i = 0; i < MT; ++i) *reinterpret_cast<float2 *>(dst + 2 * i) = make_float2(o[i][x], o[i][2 + x]);
+        for (int i = 0; i < MT; ++i) *reinterpret_cast<float2 *>(dst + at(i)) = make_float2(o[i][x], o[i][2 + x]);
       }
     }
   }
