@@ -82,12 +82,7 @@ struct RowStream {
     g = lane >> 2;
     t = lane & 3;
     ring = warp_ring;
-    m[0] = m[1] = -INFINITY;
-    z[0] = z[1] = 0.f;
-#pragma unroll
-    for (int i = 0; i < MT; ++i)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) o[i][j] = 0.f;
+    fresh();
   }
   __device__ __forceinline__ int at(int i) const { return 2 * i / EV * 8 * EV + EV * g + 2 * i % EV; }
   // `row`: the query row of column g
@@ -117,6 +112,14 @@ struct RowStream {
                    "l"(reinterpret_cast<const char *>(v + at * vs) + c * 16), "r"(n)
                    : "memory");
     }
+  }
+  __device__ __forceinline__ void fresh() {  // nothing attended yet
+    m[0] = m[1] = -INFINITY;
+    z[0] = z[1] = 0.f;
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) o[i][j] = 0.f;
   }
   // Attends `count` tiles of 16 slots; slot(y): tile y's first.  Slots behind `last` are not there; row 2t + x sees
   // those below lim[x], and all of them below `whole`.
@@ -252,7 +255,22 @@ struct RowStream {
       for (int x = 0; x < 4; ++x) o[i][x] += c[x] + small[x];
     }
   }
-  // This warp's share of the rows below R: reference, sum of weights, output sums [R][D].
+  // A warp's share of the rows below R alone: mz [R] and output sums [R][D].
+  __device__ __forceinline__ void leave(int R, float2 *mz, float *so) {
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      z[x] += __shfl_xor_sync(0xFFFFFFFFu, z[x], 4);
+      z[x] += __shfl_xor_sync(0xFFFFFFFFu, z[x], 8);
+      z[x] += __shfl_xor_sync(0xFFFFFFFFu, z[x], 16);
+      const int r = 2 * t + x;
+      if (r < R) {
+        if (g == 0) mz[r] = make_float2(m[x], z[x]);
+#pragma unroll
+        for (int i = 0; i < MT; ++i) *reinterpret_cast<float2 *>(so + r * D + at(i)) = make_float2(o[i][x], o[i][2 + x]);
+      }
+    }
+  }
+  // The same for join_warps: reference, sum of weights, output sums [R][D].
   __device__ __forceinline__ void leave(int R, float *wm, float *wz, float *so) {
 #pragma unroll
     for (int x = 0; x < 2; ++x) {

@@ -59,38 +59,58 @@ __global__ void __launch_bounds__(NT, kPerSm<T, D>) prefix_rows_kernel(const __g
 
 // ---- own slots ----
 // The units (batch row, KV head, 8 of its query rows) one behind the other are a line of tiles of 16
-// slots, and every CTA takes an equal stretch of it: lengths differ, and a CTA per unit would wait for
-// the longest.  A stretch inside one unit is a piece; piece number = CTA + unit, which no two share.
+// slots, and every warp takes an equal stretch of it: lengths differ, and what is done unit by unit
+// waits for the longest.  A stretch inside one unit is a piece; piece number = warp + unit, which no
+// two share.  The warp's ring runs on across the units, and no barrier follows the first one.
 struct OwnArgs {
   float *part;   // [pieces][8][D]
   float2 *stat;  // [pieces][8]
   int2 *info;    // [units] first piece, pieces
   int groups;    // of 8 query rows
-  int units;
 };
-constexpr int kMinTiles = 8;  // of a stretch
+constexpr int kMinTiles = 4;      // of a stretch
+constexpr int kLongShare = 90;    // per cent of the tiles
+constexpr int kKeptHeads = 2048;  // lengths that are kept in shared memory
+
+// Where the warps' stretches begin.  The first half of the warps, all of which run at once, have the larger
+// part of the tiles; the others, which follow as CTAs end, have short stretches that even out
+// what some SMs are slower than others.
+struct Stretches {
+  int total, half, big, small;
+  __device__ __forceinline__ Stretches(int tiles, int warps) : total(tiles), half(warps / 2) {
+    big = max(kMinTiles, (int)((long)tiles * kLongShare / 100 / half));
+    const int rest = tiles - min((long)tiles, (long)big * half);
+    small = max(kMinTiles, (rest + half - 1) / half);
+  }
+  __device__ __forceinline__ int first(int w) const {
+    return (int)min((long)total, w <= half ? (long)big * w : (long)big * half + (long)small * (w - half));
+  }
+  __device__ __forceinline__ int of(int tile) const {
+    return tile / big < half ? tile / big : half + (tile - big * half) / small;
+  }
+};
 
 template <typename T, int D>
 __global__ void __launch_bounds__(NT, kPerSm<T, D>) own_slots_kernel(const __grid_constant__ SharedArgs A,
                                                                     const __grid_constant__ OwnArgs W) {
   extern __shared__ __align__(16) unsigned char rings[];
-  float *so = reinterpret_cast<float *>(rings);  // [NW][8][D]
-  __shared__ float wm[NW * 8], wz[NW * 8];
-  __shared__ int wsum[NW], at_tile, at_unit;
+  __shared__ int wsum[NW], upto[NT], kept[kKeptHeads];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   // Without a prefix launch in front nothing has waited for the kernels before this one.
   if (A.splits == 0) pdl_wait();
   pdl_launch();
   const int heads = A.B * A.Hkv;
-  auto length = [&](int bh) {
+  auto fetch = [&](int bh) {
     const int n = __ldcg(A.len + bh);
     return n < 0 || n > A.cap ? 0 : n;
   };
-  // tiles of this thread's stretch of heads, then of those in front
-  const int each = (heads + NT - 1) / NT, h0 = min(heads, (int)threadIdx.x * each), h1 = min(heads, h0 + each);
+  auto length = [&](int bh) { return bh < kKeptHeads ? kept[bh] : fetch(bh); };
+#pragma unroll 4
+  for (int bh = threadIdx.x; bh < min(heads, kKeptHeads); bh += NT) kept[bh] = fetch(bh);
+  __syncthreads();
+  const int each = (heads + NT - 1) / NT, mine0 = threadIdx.x * each;
   int mine = 0;
-  for (int bh = h0; bh < h1; ++bh) mine += (length(bh) + 15) >> 4;
-  mine *= W.groups;
+  for (int bh = mine0; bh < min(heads, mine0 + each); ++bh) mine += (length(bh) + 15) >> 4;
   int incl = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -99,145 +119,197 @@ __global__ void __launch_bounds__(NT, kPerSm<T, D>) own_slots_kernel(const __gri
   }
   if (lane == 31) wsum[warp] = incl;
   __syncthreads();
-  int total = 0, before = incl - mine;
+  int total = 0;
 #pragma unroll
   for (int w = 0; w < NW; ++w) {
-    if (w < warp) before += wsum[w];
+    if (w < warp) incl += wsum[w];
     total += wsum[w];
   }
-  const int per = max(kMinTiles, (int)(((unsigned)total + gridDim.x - 1) / gridDim.x));
-  const int lo = (int)min((long)total, (long)per * blockIdx.x), hi = min(total - lo, per) + lo;
-  if (lo < total && before <= lo && lo < before + mine) {  // the thread whose heads hold tile lo
-    int x = before;
-    int u = h0 * W.groups;
-    for (int bh = h0; bh < h1; ++bh) {
-      const int t = (length(bh) + 15) >> 4;
-      if (x + t * W.groups <= lo) {
-        x += t * W.groups;
-        u += W.groups;
-        continue;
-      }
-      const int g = (lo - x) / t;
-      x += g * t;
-      u += g;
-      break;
-    }
-    at_unit = u;
-    at_tile = x;
-  }
+  upto[threadIdx.x] = incl * W.groups;  // tiles up to this thread's last head
   __syncthreads();
+  const Stretches P(total * W.groups, (int)gridDim.x * NW);
+  const int me = blockIdx.x * NW + warp, lo = P.first(me), hi = P.first(me + 1);
   if (lo < hi) {
-    int u = at_unit;
-    int start = at_tile;  // unit u's first tile
-    for (int x = lo; x < hi;) {
-      const int bh = u / W.groups, grp = u - bh * W.groups, n = length(bh), t = (n + 15) >> 4;
-      if (t == 0) {
-        ++u;
-        continue;
-      }
-      const int b = bh / A.Hkv, h = bh - b * A.Hkv, gn = A.G * A.nq, r0 = grp * 8, R = min(8, gn - r0);
-      const int x0 = x - start, x1 = min(t, hi - start);
-      RowStream<T, D> S;
-      S.init(rings + warp * S.RING);
-      S.load_q(static_cast<const T *>(A.q) + q_offset(A.sq, b, h, A.G, A.nq, r0 + min(S.g, R - 1)));
-      int lim[2];  // slots that rows 2t, 2t + 1 see
+    // the head that tile lo is in
+    int src = 0;
 #pragma unroll
-      for (int i = 0; i < 2; ++i) lim[i] = n - A.nq + (r0 + min(2 * S.t + i, R - 1)) % A.nq + 1;
-      S.run((x1 - x0 - warp + NW - 1) / NW, [&](int y) { return (x0 + y * NW + warp) * 16; },
-            static_cast<const T *>(A.K) + (long)bh * A.cap * D, D, static_cast<const T *>(A.V) + (long)bh * A.cap * D, D, n - 1,
-            A.c_log2, lim, n - A.nq + 1);
-      __syncthreads();
-      S.leave(R, wm + warp * 8, wz + warp * 8, so + warp * R * D);
-      __syncthreads();
-      const long piece = (long)blockIdx.x + u;
-      join_warps<D, NW>(R, wm, wz, so, W.part + piece * 8 * D, W.stat + piece * 8);
-      if (x0 == 0 && threadIdx.x == 0) {
-        const int first = start / per, last = (start + t - 1) / per;
-        W.info[u] = make_int2(first + u, last - first + 1);
+    for (int i = 0; i < NT / 32; ++i) src += __popc(__ballot_sync(0xFFFFFFFFu, upto[i * 32 + lane] <= lo));
+    int bh = src * each, before = src > 0 ? upto[src - 1] : 0;
+    for (;; ++bh) {
+      const int t = ((length(bh) + 15) >> 4) * W.groups;
+      if (before + t > lo) break;
+      before += t;
+    }
+    struct Cursor {
+      int bh, grp, n, tiles, x;  // head, group, its slots and tiles, the tile at hand
+    };
+    Cursor at;
+    at.bh = bh;
+    at.n = length(bh);
+    at.tiles = (at.n + 15) >> 4;
+    at.grp = (lo - before) / at.tiles;
+    at.x = lo - before - at.grp * at.tiles;
+    auto advance = [&](Cursor &c) {
+      if (++c.x < c.tiles) return;
+      c.x = 0;
+      if (++c.grp < W.groups) return;
+      c.grp = 0;
+      do {
+        c.n = length(++c.bh);
+      } while (c.n == 0);  // only called where a tile follows
+      c.tiles = (c.n + 15) >> 4;
+    };
+    const int gn = A.G * A.nq;
+    RowStream<T, D> S;
+    S.init(rings + warp * S.RING);
+    Cursor ahead = at;
+    auto fill = [&](int stage) {
+      S.fill(stage, static_cast<const T *>(A.K) + (long)ahead.bh * A.cap * D, D,
+             static_cast<const T *>(A.V) + (long)ahead.bh * A.cap * D, D, ahead.x * 16, ahead.n - 1);
+    };
+    const int count = hi - lo;
+#pragma unroll
+    for (int s = 0; s < S.STAGES - 1; ++s) {
+      if (s < count) {
+        if (s > 0) advance(ahead);
+        fill(s);
       }
-      __syncthreads();  // the shares are read before the next piece's
-      x = start + x1;
-      start += t;
-      ++u;
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    }
+    int stage = 0, lim[2];
+    bool first = true;  // of a piece
+    for (int y = 0; y < count; ++y) {
+      const int R = min(8, gn - at.grp * 8);
+      if (first) {
+        const int b = at.bh / A.Hkv, h = at.bh - b * A.Hkv, r0 = at.grp * 8;
+        S.load_q(static_cast<const T *>(A.q) + q_offset(A.sq, b, h, A.G, A.nq, r0 + min(S.g, R - 1)));
+        // slots that rows 2t, 2t + 1 see
+#pragma unroll
+        for (int i = 0; i < 2; ++i) lim[i] = at.n - A.nq + (r0 + min(2 * S.t + i, R - 1)) % A.nq + 1;
+        first = false;
+        if (at.x == 0 && lane == 0) {
+          const int u = at.bh * W.groups + at.grp, from = P.of(lo + y), to = P.of(lo + y + at.tiles - 1);
+          W.info[u] = make_int2(from + u, to - from + 1);
+        }
+      }
+      if (y + S.STAGES - 1 < count) {
+        advance(ahead);
+        fill(stage == 0 ? S.STAGES - 1 : stage - 1);
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+      asm volatile("cp.async.wait_group %0;" ::"n"(S.STAGES - 1) : "memory");
+      __syncwarp();
+      float l[4];
+      S.logits(stage, A.c_log2, l);
+      if (at.x * 16 + 16 > at.n - A.nq + 1) S.hide(l, S.g, at.x * 16, lim);
+      S.add(stage, l);
+      __syncwarp();  // the stage may be filled again
+      if (++stage == S.STAGES) stage = 0;
+      if (at.x + 1 == at.tiles || y + 1 == count) {
+        const long piece = (long)me + at.bh * W.groups + at.grp;
+        S.leave(R, W.stat + piece * 8, W.part + piece * 8 * D);
+        S.fresh();
+        first = true;
+      }
+      if (y + 1 < count) advance(at);
     }
   }
   if (A.splits) pdl_wait();  // this kernel does not end before the prefix's
 }
 
 // ---- everything joined: one warp a query row ----
+// Latency counts: the row's length is read before the wait, and the prefix's first sums are on
+// their way beside the statistics that say what they weigh (a share that saw nothing has left none:
+// whatever stands there is not taken).
 template <typename T, int D>
 __global__ void __launch_bounds__(NT) shared_join_kernel(const __grid_constant__ SharedArgs A, const __grid_constant__ OwnArgs W) {
-  constexpr int E = D / 32;  // elements of a lane
-  pdl_wait();
-  pdl_launch();
+  constexpr int E = D / 32, N = 16;  // elements of a lane, sums in flight
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int gn = A.G * A.nq;
   const long at = (long)blockIdx.x * NW + warp;
-  if (at >= (long)A.B * A.Hkv * gn) return;
-  const long bh = at / gn;
-  const int row = (int)(at - bh * gn), b = (int)(bh / A.Hkv), h = (int)(bh - (long)b * A.Hkv);
-  const int n = A.cap ? A.len[bh] : 0;
+  const bool mine = at < (long)A.B * A.Hkv * gn;
+  const int bh = mine ? (int)(at / gn) : 0;
+  const int row = mine ? (int)(at - (long)bh * gn) : 0, b = bh / A.Hkv, h = bh - b * A.Hkv;
+  // The launch before waits for the one before it, so what precedes the call is complete (nothing is known
+  // of it where that launch is the call's first and may still be waiting).
+  const bool early = A.splits > 0 && A.cap > 0;
+  int n = 0;
+  if (early) n = __ldcg(A.len + bh);
+  pdl_wait();
+  pdl_launch();
+  if (!mine) return;
+  if (!early && A.cap > 0) n = A.len[bh];
   if (n < 0 || n > A.cap) {
     if (row == 0 && lane == 0 && A.status) atomicExch(A.status, (int)KV_ERR_INVALID_ARG);
     return;
   }
-  const int2 own = n > 0 ? W.info[bh * W.groups + row / 8] : make_int2(0, 0);
-  const int shares = A.splits + own.y;
-  // share s: the prefix's first, then the pieces
-  auto stat = [&](int s) {
-    return s < A.splits ? A.stat[((long)s * A.Hkv + h) * A.rows + (long)b * gn + row]
-                        : W.stat[((long)own.x + s - A.splits) * 8 + row % 8];
+  float x[N][E];
+  auto load = [&](int i, const float *p, bool there) {
+#pragma unroll
+    for (int y = 0; y < E; ++y) x[i][y] = 0.f;
+    if (there) {
+      if constexpr (E == 4) {
+        const float4 v = __ldcs(reinterpret_cast<const float4 *>(p) + lane);
+        x[i][0] = v.x;
+        x[i][1] = v.y;
+        x[i][2] = v.z;
+        x[i][3] = v.w;
+      } else {
+        const float2 v = __ldcs(reinterpret_cast<const float2 *>(p) + lane);
+        x[i][0] = v.x;
+        x[i][1] = v.y;
+      }
+    }
   };
+  const long share = (long)A.Hkv * A.rows, first = (long)h * A.rows + (long)b * gn + row;
+  const int2 own = n > 0 ? W.info[bh * W.groups + row / 8] : make_int2(0, 0);
+  float2 st0 = make_float2(-INFINITY, 0.f), st1 = st0;  // prefix shares `lane` and 32 + lane (at most 64)
+  if (lane < A.splits) st0 = A.stat[lane * share + first];
+  if (32 + lane < A.splits) st1 = A.stat[(32 + lane) * share + first];
+#pragma unroll
+  for (int i = 0; i < N; ++i) load(i, A.part + (i * share + first) * D, i < A.splits);
+  const float2 *ws = W.stat + (long)own.x * 8 + row % 8;
+  const float *wp = W.part + ((long)own.x * 8 + row % 8) * D;
   float M = -INFINITY;
-  for (int s = lane; s < shares; s += 32) {
-    const float2 x = stat(s);
-    if (x.y != 0.f) M = fmaxf(M, x.x);
+  for (int s = lane; s < own.y; s += 32) {
+    const float2 v = ws[s * 8];
+    if (v.y != 0.f) M = fmaxf(M, v.x);
   }
+  if (st0.y != 0.f) M = fmaxf(M, st0.x);
+  if (st1.y != 0.f) M = fmaxf(M, st1.x);
 #pragma unroll
   for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, o));
+  auto factor = [&](const float2 &v) { return v.y != 0.f ? tc::ex2(M == -INFINITY ? 0.f : v.x - M) : 0.f; };
   float Z = 0.f, v[E];
 #pragma unroll
   for (int i = 0; i < E; ++i) v[i] = 0.f;
-  for (int s0 = 0; s0 < shares; s0 += 32) {
-    float f = 0.f;  // share s0 + lane's factor; 0: it saw nothing and left no sums
-    if (s0 + lane < shares) {
-      const float2 x = stat(s0 + lane);
-      if (x.y != 0.f) f = tc::ex2(M == -INFINITY ? 0.f : x.x - M);
-      Z += f * x.y;
+  // the N sums in registers, weighed by lanes from .. from + N - 1's f
+  auto take = [&](float f, int from) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const float w = __shfl_sync(0xFFFFFFFFu, f, from + i);
+#pragma unroll
+      for (int y = 0; y < E; ++y) v[y] += w != 0.f ? w * x[i][y] : 0.f;
     }
-    const unsigned live = __ballot_sync(0xFFFFFFFFu, f != 0.f);
+  };
+  const float f0 = factor(st0), f1 = factor(st1);
+  Z = f0 * st0.y + f1 * st1.y;
+  if (A.splits > 0) take(f0, 0);
+  for (int s0 = N; s0 < A.splits; s0 += N) {
 #pragma unroll
-    for (int half = 0; half < 32; half += 16) {
-      if (s0 + half >= shares) break;
-      float x[16][E];  // all on their way together
+    for (int i = 0; i < N; ++i) load(i, A.part + ((s0 + i) * share + first) * D, s0 + i < A.splits);
+    take(s0 < 32 ? f0 : f1, s0 % 32);
+  }
+  for (int s0 = 0; s0 < own.y; s0 += N) {
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const int s = s0 + half + i;
-        const float *p = s < A.splits ? A.part + (((long)s * A.Hkv + h) * A.rows + (long)b * gn + row) * D
-                                      : W.part + (((long)own.x + s - A.splits) * 8 + row % 8) * D;
-#pragma unroll
-        for (int y = 0; y < E; ++y) x[i][y] = 0.f;
-        if (live >> (half + i) & 1) {
-          if constexpr (E == 4) {
-            const float4 y = __ldcs(reinterpret_cast<const float4 *>(p) + lane);
-            x[i][0] = y.x;
-            x[i][1] = y.y;
-            x[i][2] = y.z;
-            x[i][3] = y.w;
-          } else {
-            const float2 y = __ldcs(reinterpret_cast<const float2 *>(p) + lane);
-            x[i][0] = y.x;
-            x[i][1] = y.y;
-          }
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const float w = __shfl_sync(0xFFFFFFFFu, f, half + i);
-#pragma unroll
-        for (int y = 0; y < E; ++y) v[y] += w * x[i][y];
-      }
+    for (int i = 0; i < N; ++i) load(i, wp + (long)(s0 + i) * 8 * D, s0 + i < own.y);
+    float f = 0.f;
+    if (lane < N && s0 + lane < own.y) {
+      const float2 y = ws[(s0 + lane) * 8];
+      f = factor(y);
+      Z += f * y.y;
     }
+    take(f, 0);
   }
 #pragma unroll
   for (int o = 16; o; o >>= 1) Z += __shfl_xor_sync(0xFFFFFFFFu, Z, o);
@@ -270,8 +342,8 @@ SharedPlan make_plan(long rows, int Hkv, int P, int dtype) {
   return dtype == KV_BF16 ? shared_tc_plan(rows, Hkv, P) : rows_plan(rows, Hkv, P);
 }
 
-// CTAs of the own slots' kernel: those that run at once.
-int own_ctas(int elem_bytes, int d) { return (elem_bytes == 4 && d == 128 ? 1 : 2) * kNumSmsHint; }
+// CTAs of the own slots' kernel: those that run at once, and as many again with short stretches.
+int own_ctas(int elem_bytes, int d) { return 2 * (elem_bytes == 4 && d == 128 ? 1 : 2) * kNumSmsHint; }
 
 template <typename T, int D>
 int run(const SharedArgs &A, const OwnArgs &W, const SharedPlan &plan, cudaStream_t st) {
@@ -307,7 +379,7 @@ int run(const SharedArgs &A, const OwnArgs &W, const SharedPlan &plan, cudaStrea
 struct Layout {
   size_t prefix, prefix_stat, own, own_stat, info, bytes;
   Layout(const SharedPlan &plan, int Hkv, long rows, long units, int d, int dtype) {
-    const size_t n = (size_t)plan.splits * Hkv * rows, pieces = (size_t)own_ctas(dtype == KV_BF16 ? 2 : 4, d) + units;
+    const size_t n = (size_t)plan.splits * Hkv * rows, pieces = (size_t)own_ctas(dtype == KV_BF16 ? 2 : 4, d) * NW + units;
     prefix = 0;
     own = prefix + n * d * sizeof(float);
     prefix_stat = own + pieces * 8 * d * sizeof(float);
@@ -358,9 +430,8 @@ int launch_attn_shared(const void *q, const void *Kp, const void *Vp, const void
   A.c_log2 = scale * 1.4426950408889634f;
   OwnArgs W{};
   W.groups = (A.G * nq + 7) / 8;
-  W.units = B * Hkv * W.groups;
   char *p = reinterpret_cast<char *>((reinterpret_cast<uintptr_t>(ws) + 31) & ~uintptr_t(31));
-  const Layout l(plan, Hkv, A.rows, W.units, d, dtype);
+  const Layout l(plan, Hkv, A.rows, (long)B * Hkv * W.groups, d, dtype);
   A.part = reinterpret_cast<float *>(p + l.prefix);
   A.stat = reinterpret_cast<float2 *>(p + l.prefix_stat);
   W.part = reinterpret_cast<float *>(p + l.own);

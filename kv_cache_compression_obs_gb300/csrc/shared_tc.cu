@@ -91,6 +91,23 @@ __global__ void __launch_bounds__(NT, 1) prefix_tc_kernel(const __grid_constant_
     tc::tma_prefetch_desc(&tmK);
     tc::tma_prefetch_desc(&tmV);
   }
+  const int share = blockIdx.x % T.shares, rest = blockIdx.x / T.shares;
+  const int h = rest % A.Hkv, pair = rest / A.Hkv;
+  const int j0 = share * T.tiles;                        // first key tile
+  const int n = min(T.tiles, (A.P + BN - 1) / BN - j0);  // at least 1
+  const int row0 = pair * 2 * BM;                        // first row, of head h's
+  const bool turn = T.turn;
+  const bool two = turn || row0 + BM < A.rows;           // the second tile has work
+  constexpr int CH = D / 8;                              // 16-byte pieces of a row
+  struct {
+    int b, g, t;
+  } at{0, 0, 0};  // the first query row that a softmax lane fetches
+  if (warp < 8) {
+    const int gn = A.G * A.nq, r = row0 + (turn ? 0 : (warp >> 2) * BM) + (warp & 3) * 32 + lane / CH;
+    at.b = r / gn;
+    at.g = (r - at.b * gn) / A.nq;
+    at.t = r - at.b * gn - at.g * A.nq;
+  }
   pdl_wait();
   pdl_launch();
   tc::fence_before_sync();
@@ -104,14 +121,6 @@ __global__ void __launch_bounds__(NT, 1) prefix_tc_kernel(const __grid_constant_
     if (A.status) atomicExch(A.status, (int)KV_ERR_TIMEOUT);
     return false;
   };
-  const int share = blockIdx.x % T.shares, rest = blockIdx.x / T.shares;
-  const int h = rest % A.Hkv, pair = rest / A.Hkv;
-  const int j0 = share * T.tiles;                                  // first key tile
-  const int n = min(T.tiles, (A.P + BN - 1) / BN - j0);            // at least 1
-  const int row0 = pair * 2 * BM;                                  // first row, of head h's
-  const bool turn = T.turn;
-  const bool two = turn || row0 + BM < A.rows;                     // the second tile has work
-
   if (warp >= 8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
     if (warp == W_TMA) {
@@ -239,18 +248,22 @@ __global__ void __launch_bounds__(NT, 1) prefix_tc_kernel(const __grid_constant_
     const int cnt = turn ? (n - i + 1) / 2 : (i == 0 || two ? n : 0);
     if (two || i == 0) {
       // this warp's rows of Q, 16 bytes a lane, where the swizzled layout wants them; rows that do not exist are 0
-      const int gn = A.G * A.nq;
-      constexpr int CH = D / 8;  // 16-byte chunks of a row
-#pragma unroll 4
-      for (int e = lane; e < 32 * CH; e += 32) {
-        const int r = (warp & 3) * 32 + e / CH, c = e % CH, at = tile0 + r;
-        uint4 x = make_uint4(0, 0, 0, 0);
-        if (at < A.rows) {
-          const int b = at / gn, y = at - b * gn, g = y / A.nq, t = y - g * A.nq;
-          x = *reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(A.q) + b * A.sq[0] + ((long)h * A.G + g) * A.sq[1] +
-                                               t * A.sq[2] + c * 8);
-        }
-        *reinterpret_cast<uint4 *>(sQ + i * Gm::TILE + (c / 8) * Gm::SUB + r * 128 + (((c & 7) ^ (r & 7)) << 4)) = x;
+      // all on their way together: in four batches, each behind the ring's tiles, they took 12 us
+      uint4 x[CH];
+#pragma unroll
+      for (int e = 0; e < CH; ++e) {
+        x[e] = make_uint4(0, 0, 0, 0);
+        if (at.b < A.B)
+          x[e] = *reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(A.q) + at.b * A.sq[0] +
+                                                  ((long)h * A.G + at.g) * A.sq[1] + at.t * A.sq[2] + lane % CH * 8);
+        at.t += 32 / CH;
+        while (at.t >= A.nq) at.t -= A.nq, ++at.g;
+        while (at.g >= A.G) at.g -= A.G, ++at.b;
+      }
+#pragma unroll
+      for (int e = 0; e < CH; ++e) {
+        const int r = (warp & 3) * 32 + (e * 32 + lane) / CH, c = lane % CH;
+        *reinterpret_cast<uint4 *>(sQ + i * Gm::TILE + (c / 8) * Gm::SUB + r * 128 + (((c & 7) ^ (r & 7)) << 4)) = x[e];
       }
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncwarp();
@@ -279,6 +292,7 @@ __global__ void __launch_bounds__(NT, 1) prefix_tc_kernel(const __grid_constant_
       top[0] = half_max(r, lim) * c;
       tmem_landed<64>(r + 64);
       top[1] = half_max(r + 64, lim - 64) * c;
+      if (y == 0) top[0] = fmaxf(top[0], top[1]);  // not to wait for the first half's product, whose V may be far
 #pragma unroll
       for (int hf = 0; hf < 2; ++hf) {
         const bool over = top[hf] > m + kLazy;
