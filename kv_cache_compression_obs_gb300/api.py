@@ -712,18 +712,23 @@ def kv_rope_freqs(rot: int, theta: float = 10000.0, scaling: str | None = None, 
     return torch.tensor(f[:rot // 2], dtype=torch.float64, device=device), scale.value
 
 
-def _sig(t):
-    """What a call's checks read of a tensor."""
-    return None if t is None else (t.shape, t.stride(), t.dtype)
+def _sigs(dev: int, *ts):
+    """What a call's checks read of its tensors, which have to be on device `dev`."""
+    for t in ts:
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"tensors must be on cuda:{dev}")
+    return tuple([None if t is None else (t.shape, t.stride(), t.dtype) for t in ts])
 
 
 # Checks that depend on shapes, strides and types alone are made once for each combination of them: a call
 # then reads each property of a tensor once and looks the answer up.
 @functools.lru_cache(maxsize=4096)
-def _rope_plan(q, k, v, q_out, k_out, v_out, inv_freq, pos, q_weight, k_weight, slot, seq):
+def _rope_plan(sigs):
     """The call's strides and sizes as the library takes them, or ValueError."""
-    x = q or k or v
-    (B, _, T, d), _, dt = x
+    q, k, v, q_out, k_out, v_out, inv_freq, pos, q_weight, k_weight, slot, seq, _ = sigs
+    (B, _, T, d), _, dt = q or k or v
+    if dt not in _CODES:
+        raise TypeError(f"expected bfloat16 or float32, got {dt}")
     if k and v and k[0] != v[0]:
         raise ValueError("k and v disagree in shape")
     for t in (q, k, v):
@@ -753,7 +758,7 @@ def _rope_plan(q, k, v, q_out, k_out, v_out, inv_freq, pos, q_weight, k_weight, 
             raise ValueError("the d elements of a row must be adjacent")
         strides += t[1][:3] if on else (0, 0, 0)
     return ((ctypes.c_int64 * 18)(*strides), B, q[0][1] if q else 0, Hkv, T, cap or 0, d, 2 * inv_freq[0][0] if inv_freq else 0,
-            {torch.bfloat16: KV_BF16, torch.float32: KV_F32}.get(dt, -1))
+            _CODES[dt])
 
 
 def _dense(t) -> bool:
@@ -766,10 +771,7 @@ def _dense(t) -> bool:
     return True
 
 
-def _same_device(dev: int, *ts):
-    for t in ts:
-        if t is not None and t.get_device() != dev:
-            raise ValueError(f"tensors must be on cuda:{dev}")
+_CODES = {torch.bfloat16: KV_BF16, torch.float32: KV_F32}
 
 
 def kv_qk_norm_rope(q, k, v, inv_freq, pos=None, q_weight=None, k_weight=None, eps: float | None = None,
@@ -806,11 +808,7 @@ def kv_qk_norm_rope(q, k, v, inv_freq, pos=None, q_weight=None, k_weight=None, e
     if v is None:
         v_out = None
     strides, B, Hq, Hkv, T, cap, d, rot, code = _rope_plan(
-        _sig(q), _sig(k), _sig(v), _sig(q_out), _sig(k_out), _sig(v_out), _sig(inv_freq), _sig(pos), _sig(q_weight),
-        _sig(k_weight), _sig(slot), _sig(seq))
-    if code < 0:
-        _dtype_code(x)
-    _same_device(dev, q, k, v, q_out, k_out, v_out, inv_freq, pos, q_weight, k_weight, slot, seq, dev_status)
+        _sigs(dev, q, k, v, q_out, k_out, v_out, inv_freq, pos, q_weight, k_weight, slot, seq, dev_status))
     flags = (KV_ROPE_INTERLEAVED if interleaved else 0) | (KV_ROPE_ONE_PLUS if one_plus else 0)
     if eps is not None:
         flags |= KV_ROPE_NORM
@@ -823,9 +821,6 @@ def kv_qk_norm_rope(q, k, v, inv_freq, pos=None, q_weight=None, k_weight=None, e
     return q_out, k_out, v_out
 
 
-_CODES = {torch.bfloat16: KV_BF16, torch.float32: KV_F32}
-
-
 def _rows_plan(q, o, lse):
     """Checks of queries [B][Hq][n][d] and of the outputs that are given."""
     if len(q[0]) != 4 or q[1][3] != 1:
@@ -836,6 +831,8 @@ def _rows_plan(q, o, lse):
         raise ValueError("lse_out must be [B][Hq][n] float32, contiguous")
     if q[2] not in _CODES:
         raise TypeError(f"expected bfloat16 or float32, got {q[2]}")
+    # strides of the output, which has q's memory order where it is made here
+    return o[1] if o else torch.empty_like(torch.empty_strided(q[0], q[1], dtype=q[2], device="meta")).stride()
 
 
 def _cache_plan(q, K, V, ln):
@@ -853,8 +850,9 @@ def _flat(*st):
 
 
 @functools.lru_cache(maxsize=4096)
-def _blocks_plan(q, K, V, ln, dig, o, lse, sel, block, n_sel):
-    _rows_plan(q, o, lse)
+def _blocks_plan(sigs, block, n_sel):
+    q, K, V, ln, dig, o, lse, sel, _ = sigs
+    so = _rows_plan(q, o, lse)
     _cache_plan(q, K, V, ln)
     B, Hq, n, d = q[0]
     _, Hkv, cap, _ = K[0]
@@ -862,17 +860,15 @@ def _blocks_plan(q, K, V, ln, dig, o, lse, sel, block, n_sel):
         raise ValueError("digest must be [B][Hkv][ceil(cap / block)][2][d] in q's dtype, contiguous")
     if sel and (sel[0] != (B, Hkv, n, n_sel) or sel[2] != _I32 or not _dense(sel)):
         raise ValueError("sel_out must be [B][Hkv][n][n_sel] int32, contiguous")
-    return B, Hq, Hkv, n, cap, d, _CODES[q[2]], d ** -0.5
+    return B, Hq, Hkv, n, cap, d, _CODES[q[2]], d ** -0.5, _flat(q[1][:3], so[:3])
 
 
 @functools.lru_cache(maxsize=4096)
-def _out_strides(q, o, prefix=()):
-    return _flat(q[:3], *[t[:2] for t in prefix], o[:3])
-
-
-@functools.lru_cache(maxsize=4096)
-def _shared_plan(q, kp, vp, K, V, ln, o, lse):
-    _rows_plan(q, o, lse)
+def _shared_plan(sigs):
+    q, kp, vp, K, V, ln, o, lse, ws, _ = sigs
+    so = _rows_plan(q, o, lse)
+    if ws and not _dense(ws):
+        raise ValueError("workspace must be contiguous")
     if (not kp) != (not vp) or (not K) != (not V) or (not K) != (not ln) or not (K or kp):
         raise ValueError("a prefix (K_prefix, V_prefix) or own slots (K, V, len_) must be given, each whole")
     B, Hq, n, d = q[0]
@@ -886,7 +882,7 @@ def _shared_plan(q, kp, vp, K, V, ln, o, lse):
         if kp[0] != (Hkv, P, d) or vp[0] != kp[0] or kp[2] != q[2] or vp[2] != q[2] or kp[1][2] != 1 or vp[1][2] != 1:
             raise ValueError("the prefix must be [Hkv][P][d] in q's dtype, with adjacent elements along d")
     return (B, Hq, Hkv, n, P, cap, d, _CODES[q[2]], d ** -0.5, kv_workspace_size(KV_OP_ATTN_SHARED, B, Hq, Hkv, max(1, P), d, n, P),
-            (kp[1], vp[1]) if kp else ((0, 0, 1), (0, 0, 1)))
+            _flat(q[1][:3], kp[1][:2] if kp else (0, 0), vp[1][:2] if kp else (0, 0), so[:3]))
 
 
 def kv_block_digest(K: torch.Tensor, block: int, len_=None, n_new: int | None = None, out=None, dev_status=None, stream=None):
@@ -922,10 +918,9 @@ def kv_attn_blocks(q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, len_: torc
     The new tokens are the last n filled slots; token t sees the slots j < len - n + t + 1.  Each (token, KV head)
     attends the first `sink` and last `recent` of the blocks that it sees and the others with the largest bounds on
     their logits, n_sel in all.  q's and out's batch, head and token strides are free."""
-    dev, qs = _device_of(q), q.stride()
-    B, Hq, Hkv, n, cap, d, code, default_scale = _blocks_plan((q.shape, qs, q.dtype), _sig(K), _sig(V), _sig(len_), _sig(digest),
-                                                              _sig(out), _sig(lse_out), _sig(sel_out), block, n_sel)
-    _same_device(dev, K, V, len_, digest, out, lse_out, sel_out, dev_status)
+    dev = _device_of(q)
+    B, Hq, Hkv, n, cap, d, code, default_scale, strides = _blocks_plan(
+        _sigs(dev, q, K, V, len_, digest, out, lse_out, sel_out, dev_status), block, n_sel)
     if out is None or lse_out is None or sel_out is None:
         with _side(stream):
             if out is None:
@@ -936,7 +931,7 @@ def kv_attn_blocks(q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, len_: torc
                 sel_out = torch.empty((B, Hkv, n, max(0, n_sel)), dtype=_I32, device=q.device)
     status = _lib.kv_attn_blocks(
         q.data_ptr(), K.data_ptr(), V.data_ptr(), len_.data_ptr(), digest.data_ptr(), B, Hq, Hkv, n, cap, d, block, n_sel, sink,
-        recent, _out_strides(qs, out.stride()), default_scale if scale is None else scale, code, out.data_ptr(),
+        recent, strides, default_scale if scale is None else scale, code, out.data_ptr(),
         lse_out.data_ptr(), sel_out.data_ptr(), _at(dev_status), _stream_of(dev, stream))
     if status:
         _check("kv_attn_blocks", status)
@@ -951,21 +946,18 @@ def kv_attn_shared(q: torch.Tensor, K_prefix, V_prefix, K, V, len_, scale: float
 
     Every token sees the whole prefix; the new tokens are the last n own slots and token t sees the own slots
     j < len - n + t + 1.  Strides of q, out and the prefix are free but for the d adjacent elements."""
-    dev, qs = _device_of(q), q.stride()
-    B, Hq, Hkv, n, P, cap, d, code, default_scale, need, prefix = _shared_plan(
-        (q.shape, qs, q.dtype), _sig(K_prefix), _sig(V_prefix), _sig(K), _sig(V), _sig(len_), _sig(out), _sig(lse_out))
-    _same_device(dev, K_prefix, V_prefix, K, V, len_, out, lse_out, workspace, dev_status)
+    dev = _device_of(q)
+    B, Hq, Hkv, n, P, cap, d, code, default_scale, need, strides = _shared_plan(
+        _sigs(dev, q, K_prefix, V_prefix, K, V, len_, out, lse_out, workspace, dev_status))
     with _side(stream):
         if out is None:
             out = torch.empty_like(q)
         if lse_out is None:
             lse_out = torch.empty((B, Hq, n), dtype=_F32, device=q.device)
         ws, nbytes = _workspace(need, q.device, workspace)
-    if workspace is not None and not workspace.is_contiguous():
-        raise ValueError("workspace must be contiguous")
     status = _lib.kv_attn_shared(
         q.data_ptr(), _at(K_prefix), _at(V_prefix), _at(K), _at(V), _at(len_), B, Hq, Hkv, n, P, cap, d,
-        _out_strides(qs, out.stride(), prefix), default_scale if scale is None else scale, code, out.data_ptr(),
+        strides, default_scale if scale is None else scale, code, out.data_ptr(),
         lse_out.data_ptr(), _at(ws), nbytes, _at(dev_status), _stream_of(dev, stream))
     if status:
         _check("kv_attn_shared", status)

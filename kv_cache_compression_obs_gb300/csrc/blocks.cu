@@ -7,18 +7,24 @@
 // of the blocks that a token sees and the best others by (u descending, j ascending) are
 // attended, all of their visible slots with a plain softmax.
 //
-// The choice is the one that u in 64 bits makes.  The bounds are computed by warp-level
-// products with fp32 sums, which are off by at most e = 2^-16 max|digest| max_g |q_g|_1 (16 steps
-// of a sum that may be cut off, 2^-22 each; the products are exact, or 2^-21 from split fp32
-// operands).  With a the m-th largest of them, a block above a + 2e is among the true best m, one
+// The choice is the one that u in 64 bits makes.  The bounds are computed by warp-level products,
+// whose terms are exact (2^-21 from split fp32 operands) and whose fp32 sums the unit may cut off
+// at each term: by 2^-23 of the sum so far, which never passes S = max_g sum_c |q_gc| max_j |digest_jc|.
+// In four sums of 64 terms each they are off by at most e = 2^-16 S, a factor of two to spare.  With a the m-th largest of them, a block above a + 2e is among the true best m, one
 // below a - 2e is not; when those between (mostly one block, the m-th itself) are more than
-// the places left, they alone are computed again in 64 bits.
+// the places left, they alone are computed again, in pairs of fp32 (error-free products and sums: 47
+// bits; the 64-bit unit is 40 times slower), or in 64 bits where fp32 would over- or underflow.
 //
 // One launch, a cluster of CTAs for each (row, KV head, token): the CTAs share out the digests,
 // exchange the bounds through distributed shared memory, find the same m-th
-// largest each for itself (by halving the range of their bits), share out the chosen blocks'
-// slots and join their softmax shares as they exchanged the bounds.
+// largest each for itself (a histogram over the range of their bits, then the few in its bin),
+// share out the chosen blocks' slots and join their softmax shares as they exchanged the bounds.  Digests and slots come
+// through the same rings (rows_stream.cuh), whose memory the choice borrows between.
 #include <cooperative_groups.h>
+
+#include <map>
+#include <mutex>
+#include <tuple>
 
 #include "pdl.cuh"
 #include "rows_stream.cuh"
@@ -28,6 +34,12 @@ namespace {
 
 constexpr int NW = 4, NT = 32 * NW;
 constexpr int kMaxBlocks = 12288;  // 14 bytes of shared memory each
+constexpr int kBins = 256, kFew = 64;
+template <typename T, int D>
+using Rows = RowStream<T, D, (D == 64 && sizeof(T) == 2 ? 4 : 2)>;
+// CTAs an SM holds.
+template <typename T, int D>
+constexpr int kPerSm = sizeof(T) == 4 ? (D == 64 ? 2 : 1) : 3;
 
 struct BlkArgs {
   const void *q, *K, *V;
@@ -57,7 +69,7 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   return r;
 }
 
-// max(q, 0) and min(q, 0) of a vector, NaN kept; the largest magnitude in a vector.
+// max(q, 0) and min(q, 0) of a vector, NaN kept.
 __device__ __forceinline__ uint32_t part2(uint32_t q, bool pos, __nv_bfloat16) {
   const __nv_bfloat162 x = *reinterpret_cast<__nv_bfloat162 *>(&q), z = __float2bfloat162_rn(0.f);
   const __nv_bfloat162 r = pos ? __hmax2_nan(x, z) : __hmin2_nan(x, z);
@@ -71,35 +83,21 @@ template <typename T>
 __device__ __forceinline__ uint4 part(const uint4 &q, bool pos) {
   return make_uint4(part2(q.x, pos, T()), part2(q.y, pos, T()), part2(q.z, pos, T()), part2(q.w, pos, T()));
 }
-__device__ __forceinline__ void grow(uint32_t &big, const uint4 &x, __nv_bfloat16) {
-  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint32_t a = w[i] & 0x7FFF7FFFu;
-    const __nv_bfloat162 r = __hmax2(*reinterpret_cast<__nv_bfloat162 *>(&big), *reinterpret_cast<const __nv_bfloat162 *>(&a));
-    big = *reinterpret_cast<const uint32_t *>(&r);
-  }
+// The larger magnitudes, element by element (a NaN is not kept).
+__device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b, __nv_bfloat16) {
+  b &= 0x7FFF7FFFu;
+  const __nv_bfloat162 r = __hmax2(*reinterpret_cast<__nv_bfloat162 *>(&a), *reinterpret_cast<__nv_bfloat162 *>(&b));
+  return *reinterpret_cast<const uint32_t *>(&r);
 }
-__device__ __forceinline__ void grow(uint32_t &big, const uint4 &x, float) {
-  const float a = fmaxf(fabsf(__uint_as_float(x.x)), fabsf(__uint_as_float(x.y)));
-  const float b = fmaxf(fabsf(__uint_as_float(x.z)), fabsf(__uint_as_float(x.w)));
-  big = __float_as_uint(fmaxf(__uint_as_float(big), fmaxf(a, b)));
+__device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b, float) {
+  return __float_as_uint(fmaxf(__uint_as_float(a), fabsf(__uint_as_float(b))));
 }
-__device__ __forceinline__ float magnitude(uint32_t big, __nv_bfloat16) {
-  return fmaxf(__uint_as_float(big << 16), __uint_as_float(big & 0xFFFF0000u));
+// |a| |b| summed over a word's elements
+__device__ __forceinline__ float products(uint32_t a, uint32_t b, __nv_bfloat16) {
+  return fabsf(__uint_as_float(a << 16) * __uint_as_float(b << 16)) +
+         fabsf(__uint_as_float(a & 0xFFFF0000u) * __uint_as_float(b & 0xFFFF0000u));
 }
-__device__ __forceinline__ float magnitude(uint32_t big, float) { return __uint_as_float(big); }
-
-// Sum over the CTA; `slot` alternates between calls so that one barrier is enough.
-__device__ __forceinline__ int cta_sum(int x, int (*red)[NW], int slot) {
-  x = __reduce_add_sync(0xFFFFFFFFu, x);
-  if ((threadIdx.x & 31) == 0) red[slot][threadIdx.x >> 5] = x;
-  __syncthreads();
-  int s = 0;
-#pragma unroll
-  for (int w = 0; w < NW; ++w) s += red[slot][w];
-  return s;
-}
+__device__ __forceinline__ float products(uint32_t a, uint32_t b, float) { return fabsf(__uint_as_float(a) * __uint_as_float(b)); }
 
 // u of block j in 64 bits: one warp, lanes over the channels; every lane gets it.
 template <typename T, int D>
@@ -123,109 +121,213 @@ __device__ double bound64(const BlkArgs &A, const T *q, const T *digest, int j) 
   return best;
 }
 
+// The same in pairs of fp32: hi + lo is the sum to about 2^-47 of the terms' size.
+__device__ __forceinline__ void two_sum(float a, float b, float &s, float &e) {
+  s = __fadd_rn(a, b);
+  const float x = __fsub_rn(s, a);
+  e = __fadd_rn(__fsub_rn(a, __fsub_rn(s, x)), __fsub_rn(b, x));
+}
+template <typename T, int D>
+__device__ double bound_pairs(const BlkArgs &A, const T *q, const T *digest, int j) {
+  const int lane = threadIdx.x & 31;
+  const T *row = digest + (long)j * 2 * D;
+  float low[D / 32], top[D / 32];
+#pragma unroll
+  for (int i = 0; i < D / 32; ++i) {
+    low[i] = to_f32(row[lane + 32 * i]);
+    top[i] = to_f32(row[D + lane + 32 * i]);
+  }
+  double best = -INFINITY;
+  for (int g = 0; g < A.G; ++g) {
+    float hi = 0.f, lo = 0.f;
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) {
+      const float x = to_f32(q[g * A.sq[1] + lane + 32 * i]), y = x >= 0.f ? top[i] : low[i];
+      const float p = __fmul_rn(x, y), pe = __fmaf_rn(x, y, -p);
+      float e;
+      two_sum(hi, p, hi, e);
+      lo = __fadd_rn(lo, __fadd_rn(e, pe));
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+      const float a = __shfl_xor_sync(0xFFFFFFFFu, hi, o), b = __shfl_xor_sync(0xFFFFFFFFu, lo, o);
+      float e;
+      // the same sum in both lanes: larger lane's first
+      two_sum(lane & o ? a : hi, lane & o ? hi : a, hi, e);
+      lo = __fadd_rn(__fadd_rn(lo, b), e);
+    }
+    const double s = (double)hi + (double)lo;
+    best = s > best ? s : best;
+  }
+  return best;
+}
+
 // Shared memory of the choice.
 struct Choice {
-  uint32_t *key;   // [blocks] bounds' bits, then 1 (chosen) or 0
+  uint32_t *key;   // [blocks] bounds' bits
   double *exact;   // [blocks] of the undecided blocks
   uint16_t *list;  // [blocks] undecided blocks; then the chosen ones, ascending
+  int *hist;       // [kBins]
+  uint32_t *few;   // [kFew]
 };
+constexpr uint32_t kIn = 0xFFFFFFFFu;  // no bound's bits
 
-// Marks the best `m` of the n candidates (block lo + i) in c.key; err: how far a bound may be off.
-template <typename T, int D>
-__device__ void choose(const BlkArgs &A, const Choice &c, const T *q, const T *digest, int lo, int n, int m, float err,
-                       int (*red)[NW], uint32_t (*redu)[NW], int &undecided) {
+// The m-th largest of the n keys, whose least and largest this thread's `least`, `most` are a part of.
+__device__ uint32_t mth_largest(const Choice &c, int n, int m, uint32_t least, uint32_t most, int (*red)[NW],
+                                uint32_t (*redu)[NW], int &count) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  uint32_t least = 0xFFFFFFFFu, most = 0u;
-  for (int i = threadIdx.x; i < n; i += NT) {
-    least = min(least, c.key[i]);
-    most = max(most, c.key[i]);
-  }
   least = __reduce_min_sync(0xFFFFFFFFu, least);
   most = __reduce_max_sync(0xFFFFFFFFu, most);
   if (lane == 0) {
     redu[0][warp] = least;
     redu[1][warp] = most;
   }
-  if (threadIdx.x == 0) undecided = 0;
-  __syncthreads();
+  for (int i = threadIdx.x; i < kBins; i += NT) c.hist[i] = 0;
+  __syncthreads();  // the keys too
 #pragma unroll
   for (int w = 0; w < NW; ++w) {
     least = min(least, redu[0][w]);
     most = max(most, redu[1][w]);
   }
-  // at least m keys are >= L, fewer than m are >= H
-  uint32_t L = least, H = most + 1;
-  int slot = 0;
-  bool split = false;
-  while (H - L > 1) {
-    const uint32_t mid = L + (H - L) / 2;
-    int x = 0;
-    for (int i = threadIdx.x; i < n; i += NT) x += c.key[i] >= mid;
-    x = cta_sum(x, red, slot);
-    slot ^= 1;
-    if (x >= m) L = mid; else H = mid;
-    if (x == m) {
-      split = true;
-      break;
+  for (;;) {
+    const uint32_t range = most - least;
+    const int s = max(0, 24 - __clz(range));  // range >> s is below kBins
+#pragma unroll 4
+    for (int i = threadIdx.x; i < n; i += NT) {
+      const uint32_t k = c.key[i] - least;
+      if (k <= range) atomicAdd(c.hist + (k >> s), 1);
     }
-  }
-  if (split) {  // the m-th largest is the least key from here on
-    uint32_t k = 0xFFFFFFFFu;
-    for (int i = threadIdx.x; i < n; i += NT)
-      if (c.key[i] >= L) k = min(k, c.key[i]);
-    k = __reduce_min_sync(0xFFFFFFFFu, k);
-    __syncthreads();  // redu was read above
-    if (lane == 0) redu[0][warp] = k;
     __syncthreads();
-    L = redu[0][0];
+    // keys in this thread's two bins and in all above
+    const int b = kBins - 2 - 2 * (int)threadIdx.x, h1 = c.hist[b + 1], h0 = c.hist[b];
+    int incl = h0 + h1;
 #pragma unroll
-    for (int w = 1; w < NW; ++w) L = min(L, redu[0][w]);
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+      if (lane >= o) incl += y;
+    }
+    if (lane == 31) red[0][warp] = incl;
+    __syncthreads();
+    for (int w = 0; w < warp; ++w) incl += red[0][w];
+    const int above = incl - h0 - h1;
+    if (above < m && m <= incl) {  // one thread
+      const bool upper = m <= above + h1;
+      redu[0][0] = b + upper;
+      redu[0][1] = upper ? above : above + h1;
+      redu[0][2] = upper ? h1 : h0;
+      count = 0;
+    }
+    __syncthreads();
+    const uint32_t bin = redu[0][0];
+    const int held = (int)redu[0][2];
+    m -= (int)redu[0][1];
+    least += bin << s;
+    most = min(most, least + (uint32_t)((1ull << s) - 1));
+    if (most == least) return least;
+    if (held <= kFew) {
+#pragma unroll 4
+      for (int i = threadIdx.x; i < n; i += NT) {
+        const uint32_t k = c.key[i];
+        if (k >= least && k <= most) c.few[atomicAdd(&count, 1)] = k;
+      }
+      __syncthreads();
+      // every warp alike: the range of the bits halved
+      const uint32_t k0 = lane < held ? c.few[lane] : 0u, k1 = lane + 32 < held ? c.few[lane + 32] : 0u;
+      uint32_t L = least, H = most;  // at least m keys are >= L, fewer than m are > H
+      while (L < H) {
+        const uint32_t mid = L + (H - L) / 2 + 1;
+        const int x = __popc(__ballot_sync(0xFFFFFFFFu, k0 >= mid)) + __popc(__ballot_sync(0xFFFFFFFFu, k1 >= mid));
+        if (x >= m) L = mid; else H = mid - 1;
+        if (x == m) return __reduce_min_sync(0xFFFFFFFFu, min(k0 >= mid ? k0 : kIn, k1 >= mid ? k1 : kIn));
+      }
+      return L;
+    }
+    for (int i = threadIdx.x; i < kBins; i += NT) c.hist[i] = 0;
+    __syncthreads();
   }
-  const float a = unorder(L), above = a + 2.f * err, below = a - 2.f * err;
-  int sure = 0, maybe = 0;
-  for (int i = threadIdx.x; i < n; i += NT) {
-    const float x = unorder(c.key[i]);
-    if (x > above) ++sure;
-    else if (!(x < below)) ++maybe;
+}
+
+// The best `m` of the n candidates (block lo + i; their bounds' bits in c.key) to c.list, ascending, as blocks.
+// err: how far a bound may be off; wide: only 64 bits tell them apart.
+template <typename T, int D>
+__device__ void choose(const BlkArgs &A, const Choice &c, const T *q, const T *digest, int lo, int n, int m, float err,
+                       bool wide, uint32_t least, uint32_t most, int (*red)[NW], uint32_t (*redu)[NW], int &count) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const float a = unorder(mth_largest(c, n, m, least, most, red, redu, count));
+  const float above = a + 2.f * err, below = a - 2.f * err;
+  // each warp has a stretch of the candidates, 32 at a time
+  const int stretch = (n + NT - 1) / NT * 32, i0 = min(n, warp * stretch), i1 = min(n, i0 + stretch);
+  int sure = 0, open = 0;
+#pragma unroll 4
+  for (int i = i0 + lane; i < i0 + stretch; i += 32) {
+    const float x = i < i1 ? unorder(c.key[i]) : -INFINITY;
+    sure += __popc(__ballot_sync(0xFFFFFFFFu, i < i1 && x > above));
+    open += __popc(__ballot_sync(0xFFFFFFFFu, i < i1 && !(x > above) && !(x < below)));
   }
-  const int both = cta_sum(sure + (maybe << 16), red, slot);
-  slot ^= 1;
-  sure = both & 0xFFFF;
-  maybe = both >> 16;
-  const bool again = maybe > m - sure;
-  for (int i = threadIdx.x; i < n; i += NT) {
-    const float x = unorder(c.key[i]);
-    const bool in = x > above, open = !in && !(x < below);
-    if (again && open) c.list[atomicAdd(&undecided, 1)] = (uint16_t)i;
-    c.key[i] = in || (open && !again);
+  if (lane == 0) {
+    red[0][warp] = sure;
+    red[1][warp] = open;
   }
+  if (threadIdx.x == 0) count = 0;
   __syncthreads();
-  if (!again) return;
-  for (int i = warp; i < maybe; i += NW) {
-    const double x = bound64<T, D>(A, q, digest, lo + c.list[i]);
-    if (lane == 0) c.exact[i] = x;
+  int at = 0, all_sure = 0, all_open = 0;
+#pragma unroll
+  for (int w = 0; w < NW; ++w) {
+    if (w < warp) at += red[0][w] + red[1][w];
+    all_sure += red[0][w];
+    all_open += red[1][w];
   }
-  __syncthreads();
-  for (int i = threadIdx.x; i < maybe; i += NT) {
-    const double x = c.exact[i];
-    const int j = c.list[i];
-    int better = 0;
-    for (int k = 0; k < maybe; ++k) better += c.exact[k] > x || (c.exact[k] == x && c.list[k] < j);
-    if (better < m - sure) c.key[j] = 1;
+  const int places = m - all_sure;
+  const bool again = all_open > places;
+  if (again) {
+    for (int i = i0 + lane; i < i1; i += 32) {
+      const float x = unorder(c.key[i]);
+      if (!(x > above) && !(x < below)) c.list[atomicAdd(&count, 1)] = (uint16_t)i;
+    }
+    __syncthreads();
+    for (int i = warp; i < all_open; i += NW) {
+      const int j = lo + c.list[i];
+      const double x = wide ? bound64<T, D>(A, q, digest, j) : bound_pairs<T, D>(A, q, digest, j);
+      if (lane == 0) c.exact[i] = x;
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < all_open; i += NT) {
+      const double x = c.exact[i];
+      const int j = c.list[i];
+      int better = 0;
+      for (int k = 0; k < all_open; ++k) better += c.exact[k] > x || (c.exact[k] == x && c.list[k] < j);
+      if (better < places) c.key[j] = kIn;
+    }
+    __syncthreads();
+    // how many of those each warp's stretch has now
+    int in = 0;
+    for (int i = i0 + lane; i < i0 + stretch; i += 32) in += __popc(__ballot_sync(0xFFFFFFFFu, i < i1 && c.key[i] == kIn));
+    if (lane == 0) red[1][warp] = in;
+    __syncthreads();
+    at = 0;
+    for (int w = 0; w < warp; ++w) at += red[0][w] + red[1][w];
   }
-  __syncthreads();
+#pragma unroll 4
+  for (int i = i0 + lane; i < i0 + stretch; i += 32) {
+    const uint32_t k = i < i1 ? c.key[i] : 0u;
+    const float x = unorder(k);
+    const bool in = i < i1 && (k == kIn || x > above || (!again && !(x < below)));
+    const unsigned who = __ballot_sync(0xFFFFFFFFu, in);
+    if (in) c.list[at + __popc(who & ((1u << lane) - 1))] = (uint16_t)(lo + i);
+    at += __popc(who);
+  }
 }
 
 template <typename T, int D>
-__global__ void __launch_bounds__(NT, sizeof(T) == 2 || D == 64 ? 2 : 1) blocks_kernel(const __grid_constant__ BlkArgs A) {
+__global__ void __launch_bounds__(NT, kPerSm<T, D>) blocks_kernel(const __grid_constant__ BlkArgs A) {
   extern __shared__ __align__(16) unsigned char dyn[];
   __shared__ float wm[NW * 8], wz[NW * 8];
   __shared__ float2 mz[8], all[16][8];
-  __shared__ float sM[8], sI[8];
+  __shared__ float sI[8];
   __shared__ float err_part[NW], err_cta;
-  __shared__ int red[2][NW], undecided;
-  __shared__ uint32_t redu[2][NW];
-  constexpr int NCH = RowStream<T, D>::NCH;
+  __shared__ int red[2][NW], counter, hist[kBins];
+  __shared__ uint32_t redu[2][NW], few[kFew];
+  constexpr int NCH = Rows<T, D>::NCH;
   const int G = A.G;
   float *sh = reinterpret_cast<float *>(dyn);              // [G][D] this CTA's share
   unsigned char *area = dyn + G * D * 4;
@@ -258,7 +360,7 @@ __global__ void __launch_bounds__(NT, sizeof(T) == 2 || D == 64 ? 2 : 1) blocks_
   const int block = 1 << A.b_log2;
   const int nbk = (seen + block - 1) >> A.b_log2;
   const T *q = static_cast<const T *>(A.q) + b * A.sq[0] + (long)h * G * A.sq[1] + t * A.sq[2];
-  RowStream<T, D> R;
+  Rows<T, D> R;
   R.init(area + warp * R.RING);
   R.load_q(q + min(R.g, G - 1) * A.sq[1]);
 
@@ -269,52 +371,60 @@ __global__ void __launch_bounds__(NT, sizeof(T) == 2 || D == 64 ? 2 : 1) blocks_
   const bool choice = nbk > A.n_sel;
   const int cap_c = choice && m > 0 ? nm : 0;
   Choice c;
+  c.hist = hist;
+  c.few = few;
   c.exact = reinterpret_cast<double *>(area);
   c.key = reinterpret_cast<uint32_t *>(c.exact + A.nb);
-  c.list = reinterpret_cast<uint16_t *>(mine + (A.nb + CL - 1) / CL + 16);
+  c.list = reinterpret_cast<uint16_t *>(mine + ((A.nb / CL + 20) & ~3));
   if (cap_c > 0) {
     const T *digest = static_cast<const T *>(A.digest) + bh * A.nb * 2L * D;
     const int per = (((nm + CL - 1) / CL) + 15) & ~15;
     const int i0 = min(nm, rank * per), i1 = min(nm, i0 + per);
-    uint32_t big = 0u;
-    float norm = 0.f;
+    uint32_t big[NCH * 4];  // largest magnitudes of this lane's channels
 #pragma unroll
-    for (int x = 0; x < NCH; ++x) {
-      const uint32_t w[4] = {R.q[x].x, R.q[x].y, R.q[x].z, R.q[x].w};
+    for (int x = 0; x < NCH * 4; ++x) big[x] = 0u;
+    // tiles of 16 blocks: low rows where K's stand, top rows where V's do
+    const int count = (i1 - i0 + 15) / 16, tiles = (count - warp + NW - 1) / NW;
+    const T *rows = digest + (long)lo * 2 * D;
+    auto first = [&](int y) { return i0 + (y * NW + warp) * 16; };
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        norm += sizeof(T) == 4 ? fabsf(__uint_as_float(w[i]))
-                               : fabsf(__uint_as_float(w[i] << 16)) + fabsf(__uint_as_float(w[i] & 0xFFFF0000u));
+    for (int y = 0; y < R.STAGES - 1; ++y) {
+      if (y < tiles) R.fill(y, rows, 2 * D, rows + D, 2 * D, first(y), i1 - 1);
+      asm volatile("cp.async.commit_group;" ::: "memory");
     }
-    norm += __shfl_xor_sync(0xFFFFFFFFu, norm, 1);
-    norm += __shfl_xor_sync(0xFFFFFFFFu, norm, 2);
-    norm = rows_max(norm);
-    for (int i = i0 + warp * 16; i < i1; i += NW * 16) {
-      uint4 x[2][2][NCH];  // low, top of blocks i + g and i + g + 8
+    for (int y = 0, stage = 0; y < tiles; ++y) {
+      const int ahead = y + R.STAGES - 1;
+      if (ahead < tiles) R.fill(stage == 0 ? R.STAGES - 1 : stage - 1, rows, 2 * D, rows + D, 2 * D, first(ahead), i1 - 1);
+      asm volatile("cp.async.commit_group;" ::: "memory");
+      asm volatile("cp.async.wait_group %0;" ::"n"(R.STAGES - 1) : "memory");
+      __syncwarp();
+      float sum[4][4], small[4] = {0.f, 0.f, 0.f, 0.f}, s[4];
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const char *p = reinterpret_cast<const char *>(digest + (long)(lo + min(i + R.g + 8 * k, i1 - 1)) * 2 * D) + R.t * 16;
+      for (int x = 0; x < 16; ++x) sum[x / 4][x % 4] = 0.f;
+      const unsigned char *low = R.ring + stage * R.TILE + R.g * R.ROW, *top = low + 16 * R.ROW;
 #pragma unroll
-        for (int y = 0; y < NCH; ++y) {
-          x[0][k][y] = __ldcs(reinterpret_cast<const uint4 *>(p + y * 64));
-          x[1][k][y] = __ldcs(reinterpret_cast<const uint4 *>(p + D * sizeof(T) + y * 64));
-        }
+      for (int x = 0; x < NCH; ++x) {
+        const int at = ((4 * x + R.t) ^ R.k_swizzle(R.g)) << 4, bt = ((4 * x + R.t) ^ R.v_swizzle(R.g)) << 4;
+        const uint4 l0 = *reinterpret_cast<const uint4 *>(low + at), l1 = *reinterpret_cast<const uint4 *>(low + 8 * R.ROW + at);
+        const uint4 t0 = *reinterpret_cast<const uint4 *>(top + bt);
+        const uint4 t1 = *reinterpret_cast<const uint4 *>(top + 8 * R.ROW + (((4 * x + R.t) ^ R.v_swizzle(R.g + 8)) << 4));
+        auto grow = [&](const uint4 &v) {
+          big[4 * x] = larger(big[4 * x], v.x, T());
+          big[4 * x + 1] = larger(big[4 * x + 1], v.y, T());
+          big[4 * x + 2] = larger(big[4 * x + 2], v.z, T());
+          big[4 * x + 3] = larger(big[4 * x + 3], v.w, T());
+        };
+        grow(l0);
+        grow(l1);
+        grow(t0);
+        grow(t1);
+        dot16(sum[x & 1], small, l0, l1, part<T>(R.q[x], false), T());
+        dot16(sum[2 + (x & 1)], small, t0, t1, part<T>(R.q[x], true), T());
       }
-      float s[4] = {0.f, 0.f, 0.f, 0.f}, small[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int y = 0; y < NCH; ++y) {
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          grow(big, x[0][k][y], T());
-          grow(big, x[1][k][y], T());
-        }
-        dot16(s, small, x[0][0][y], x[0][1][y], part<T>(R.q[y], false), T());
-        dot16(s, small, x[1][0][y], x[1][1][y], part<T>(R.q[y], true), T());
-      }
-      if (sizeof(T) == 4)
-#pragma unroll
-        for (int k = 0; k < 4; ++k) s[k] += small[k];
+      for (int k = 0; k < 4; ++k) s[k] = (sum[0][k] + sum[1][k]) + (sum[2][k] + sum[3][k]) + (sizeof(T) == 4 ? small[k] : 0.f);
       // the largest of the group's: columns behind G repeat its last query
+      const int i = first(y);
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         float v = max_nan(s[2 * k], s[2 * k + 1]);
@@ -322,49 +432,57 @@ __global__ void __launch_bounds__(NT, sizeof(T) == 2 || D == 64 ? 2 : 1) blocks_
         v = max_nan(v, __shfl_xor_sync(0xFFFFFFFFu, v, 2));
         if (R.t == 0 && i + R.g + 8 * k < i1) mine[i - i0 + R.g + 8 * k] = v;
       }
+      __syncwarp();  // the stage may be filled again
+      if (++stage == R.STAGES) stage = 0;
     }
-    float e = magnitude(big, T());
+    // S over this warp's blocks: the channels' largest over the lanes with the same ones, times |q|, each lane
+    // for the query of its column
+    float e = 0.f;
 #pragma unroll
-    for (int x = 16; x; x >>= 1) e = fmaxf(e, __shfl_xor_sync(0xFFFFFFFFu, e, x));
+    for (int x = 0; x < NCH * 4; ++x) {
+#pragma unroll
+      for (int o = 4; o < 32; o <<= 1) big[x] = larger(big[x], __shfl_xor_sync(0xFFFFFFFFu, big[x], o), T());
+      const uint4 &q4 = R.q[x / 4];
+      e += products(big[x], x % 4 == 0 ? q4.x : x % 4 == 1 ? q4.y : x % 4 == 2 ? q4.z : q4.w, T());
+    }
+    e += __shfl_xor_sync(0xFFFFFFFFu, e, 1);
+    e += __shfl_xor_sync(0xFFFFFFFFu, e, 2);
+    if (!(e < INFINITY)) e = INFINITY;  // a NaN in q
+    e = rows_max(e);
     if (lane == 0) err_part[warp] = e;
     __syncthreads();
     if (threadIdx.x == 0) err_cta = fmaxf(fmaxf(err_part[0], err_part[1]), fmaxf(err_part[2], err_part[3]));
     cl.sync();
-    float err = 0.f;
-    bool wild = false;
-    for (int r = 0; r < CL; ++r) err = fmaxf(err, *cl.map_shared_rank(&err_cta, r));
-    err *= norm * 0x1p-16f;
-    for (int i = threadIdx.x; i < nm; i += NT) {
+    float size = 0.f;  // of the terms of a bound
+    bool wide = false;
+    for (int r = 0; r < CL; ++r) size = fmaxf(size, *cl.map_shared_rank(&err_cta, r));
+    uint32_t least = 0xFFFFFFFFu, most = 0u;
+    // a stretch of four (of a CTA's bounds, whose number is a multiple of 16) at a time
+#pragma unroll 4
+    for (int i = threadIdx.x * 4; i < nm; i += NT * 4) {
       const int r = i / per;
-      const float v = cl.map_shared_rank(mine, r)[i - r * per];
-      wild |= !(fabsf(v) < INFINITY);
-      c.key[i] = order(v);
-    }
-    // a bound that is no number, or too large for fp32: 64 bits decide for all of them
-    if (__syncthreads_or(wild || !(err < INFINITY))) err = INFINITY;
-    choose<T, D>(A, c, q, digest, lo, nm, m, err, red, redu, undecided);
-  }
-  {
-    // the chosen ones in order
-    const int chunk = (nbk + NT - 1) / NT, j0 = min(nbk, (int)threadIdx.x * chunk), j1 = min(nbk, j0 + chunk);
-    auto chosen = [&](int j) { return !choice || j < lo || j >= nbk - A.recent || (m > 0 && c.key[j - lo]); };
-    int cnt = 0;
-    for (int j = j0; j < j1; ++j) cnt += chosen(j);
-    int incl = cnt;
+      const float4 v = *reinterpret_cast<const float4 *>(cl.map_shared_rank(mine, r) + (i - r * per));
+      const float x[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-    for (int x = 1; x < 32; x <<= 1) {
-      const int y = __shfl_up_sync(0xFFFFFFFFu, incl, x);
-      if (lane >= x) incl += y;
+      for (int k = 0; k < 4; ++k)
+        if (i + k < nm) {
+          wide |= !(fabsf(x[k]) < INFINITY);
+          const uint32_t y = order(x[k]);
+          c.key[i + k] = y;
+          least = min(least, y);
+          most = max(most, y);
+        }
     }
-    __syncthreads();
-    if (lane == 31) red[0][warp] = incl;
-    __syncthreads();
-    int at = incl - cnt;
-    for (int w = 0; w < warp; ++w) at += red[0][w];
-    for (int j = j0; j < j1; ++j)
-      if (chosen(j)) c.list[at++] = (uint16_t)j;
-    __syncthreads();
+    // a bound that is no number, or terms that fp32 does not hold: 64 bits decide for all of them
+    wide = __syncthreads_or(wide || !(size < 0x1p120f) || (size > 0.f && size < 0x1p-60f));
+    c.list += A.sink;  // behind the first blocks
+    choose<T, D>(A, c, q, digest, lo, nm, m, wide ? INFINITY : size * 0x1p-16f, wide, least, most, red, redu, counter);
+    c.list -= A.sink;
   }
+  for (int i = threadIdx.x; i < ns; i += NT)  // those that no bound decides
+    if (!choice || i < A.sink) c.list[i] = (uint16_t)i;
+    else if (i >= ns - A.recent) c.list[i] = (uint16_t)(nbk - ns + i);
+  __syncthreads();
   if (rank == 0 && sel)
     for (int i = threadIdx.x; i < A.n_sel; i += NT) sel[i] = i < ns ? (int)c.list[i] : -1;
 
@@ -390,41 +508,81 @@ __global__ void __launch_bounds__(NT, sizeof(T) == 2 || D == 64 ? 2 : 1) blocks_
   for (int i = threadIdx.x; i < CL * G; i += NT) all[i / G][i % G] = cl.map_shared_rank(mz, i / G)[i % G];
   __syncthreads();
   if ((int)threadIdx.x < G) {
+    const int r = threadIdx.x;
     float M = -INFINITY, Z = 0.f;
     for (int s = 0; s < CL; ++s)
-      if (all[s][threadIdx.x].y != 0.f) M = fmaxf(M, all[s][threadIdx.x].x);
-    for (int s = 0; s < CL; ++s)
-      if (all[s][threadIdx.x].y != 0.f) Z += all[s][threadIdx.x].y * tc::ex2(M == -INFINITY ? 0.f : all[s][threadIdx.x].x - M);
-    sM[threadIdx.x] = M;
-    sI[threadIdx.x] = 1.f / Z;
-    if (rank == 0 && lse) lse[(long)threadIdx.x * A.nq] = (M + log2f(Z)) * 0.6931471805599453f;
+      if (all[s][r].y != 0.f) M = fmaxf(M, all[s][r].x);
+    for (int s = 0; s < CL; ++s) {
+      const float f = all[s][r].y != 0.f ? tc::ex2(M == -INFINITY ? 0.f : all[s][r].x - M) : 0.f;
+      Z += f * all[s][r].y;
+      all[s][r].x = f;  // the share's factor
+    }
+    sI[r] = 1.f / Z;
+    if (rank == 0 && lse) lse[(long)r * A.nq] = (M + log2f(Z)) * 0.6931471805599453f;
   }
   __syncthreads();
   for (int i = rank * NT + threadIdx.x; i < G * D; i += CL * NT) {
     const int r = i / D;
-    float v = 0.f;
-    for (int s = 0; s < CL; ++s)
-      if (all[s][r].y != 0.f) v += tc::ex2(sM[r] == -INFINITY ? 0.f : all[s][r].x - sM[r]) * cl.map_shared_rank(sh, s)[i];
+    float x[16], v = 0.f;
+#pragma unroll
+    for (int s = 0; s < 16; ++s) x[s] = s < CL ? cl.map_shared_rank(sh, s)[i] : 0.f;
+#pragma unroll
+    for (int s = 0; s < 16; ++s)
+      if (s < CL) v += all[s][r].x * x[s];
     o[r * A.so[1] + i % D] = T(v * sI[r]);
   }
   cl.sync();  // nobody leaves while its shares are read
 }
 
+// How many clusters of `size` such CTAs the current device holds at once (remembered; 0: none).
+long clusters_at_once(const void *kernel, int threads, size_t bytes, int size) {
+  static std::mutex mu;
+  static std::map<std::tuple<int, const void *, size_t, int>, int> known;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+  std::lock_guard<std::mutex> lock(mu);
+  const auto key = std::make_tuple(dev, kernel, bytes, size);
+  const auto it = known.find(key);
+  if (it != known.end()) return it->second;
+  int n = 0;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)size);
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = bytes;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = (unsigned)size;
+  at[0].val.clusterDim.y = 1;
+  at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  if (ensure_smem(kernel, bytes) ||
+      (size > 8 && cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess) ||
+      cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) {
+    cudaGetLastError();
+    n = 0;
+  }
+  if (known.size() < 4096) known[key] = n;
+  return n;
+}
+
 template <typename T, int D>
 int run(BlkArgs A, long units, cudaStream_t st) {
-  // CTAs per unit: as many as run at once, two an SM (fp32, d = 128: one)
-  const long room = (sizeof(T) == 2 || D == 64 ? 2L : 1L) * kNumSmsHint;
-  int CL = 16;
-  while (CL > 1 && units * CL > room) CL /= 2;
-  const size_t warps = NW * RowStream<T, D>::RING, choice = (size_t)A.nb * 12;
+  const size_t warps = NW * Rows<T, D>::RING, choice = (size_t)A.nb * 12;
   A.area = (int)(((warps > choice ? warps : choice) + 15) & ~(size_t)15);
-  const size_t bytes = (size_t)A.G * D * 4 + A.area + ((size_t)(A.nb + CL - 1) / CL + 16) * 4 + (size_t)A.nb * 2 + 16;
+  auto need = [&](int CL) {
+    return (size_t)A.G * D * 4 + A.area + (((size_t)A.nb / CL + 20) & ~(size_t)3) * 4 + (size_t)A.nb * 2 + 16;
+  };
+  // CTAs per unit: the largest cluster of which every unit's is on the GPU at once.  Clusters do not
+  // cross groups of SMs, so that is asked for and not computed (448 CTAs in clusters of 7 on room for
+  // 456 ran in two rounds: 69 us, 59 in clusters of 4).
+  const long share = (long)kPerSm<T, D> * kNumSmsHint / units;
+  int CL = (int)(share > 16 ? 16 : share < 1 ? 1 : share);
+  for (; CL > 1; --CL)
+    if (clusters_at_once((const void *)blocks_kernel<T, D>, NT, need(CL), CL) >= units) break;
+  const size_t bytes = need(CL);
   if (units * CL > 0x7FFFFFFFL) return KV_ERR_UNSUPPORTED;
   if (ensure_smem((const void *)blocks_kernel<T, D>, bytes)) return KV_ERR_CUDA;
-  if (CL > 8) {
-    const cudaError_t e = cudaFuncSetAttribute(blocks_kernel<T, D>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-    if (e != cudaSuccess) return cuda_failure(e, "block-sparse attention: clusters of 16");
-  }
   const cudaError_t e = launch_pdl_cluster(blocks_kernel<T, D>, (unsigned)(units * CL), NT, bytes, st, CL, A);
   if (e != cudaSuccess) return cuda_failure(e, "block-sparse attention");
   return launch_status();

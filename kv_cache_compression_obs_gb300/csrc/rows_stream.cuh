@@ -61,14 +61,14 @@ __device__ __forceinline__ float rows_max(float x) {  // over the 16 slots: the 
   return fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 16));
 }
 
-template <typename T, int D>
+template <typename T, int D, int NS>  // NS: tiles of a warp's ring
 struct RowStream {
   static constexpr int NCH = D * (int)sizeof(T) / 64;  // 64-byte chunks of a row
   static constexpr int EV = 16 / (int)sizeof(T);       // elements of a 16-byte piece
   static constexpr int VV = D / 8 / EV;                // pieces of a lane's D / 8 elements of a V row
   static constexpr int MT = D / 16;
   static constexpr int ROW = D * (int)sizeof(T), TILE = 32 * ROW;  // bytes; 16 rows of K, then 16 of V
-  static constexpr int STAGES = D == 64 && sizeof(T) == 2 ? 6 : D == 128 && sizeof(T) == 4 ? 2 : 3;
+  static constexpr int STAGES = NS;
   static constexpr int RING = STAGES * TILE;  // bytes of a warp
 
   uint4 q[NCH];    // column g = lane / 4 of the 8: its row's chunks, bytes 16 t

@@ -21,9 +21,12 @@ __device__ __forceinline__ long q_offset(const long long (&s)[3], int b, int h, 
   return (long)b * s[0] + ((long)h * G + g) * s[1] + t * s[2];
 }
 
+// Two CTAs an SM (fp32, d = 128: one) of four warps with what shared memory holds of tiles.
+template <typename T, int D>
+using Rows = RowStream<T, D, (D == 64 && sizeof(T) == 2 ? 6 : 3)>;
 // Dynamic shared memory of a streaming CTA: the warps' rings, which their shares take over at the end.
 template <typename T, int D>
-constexpr int kRings = NW * RowStream<T, D>::RING;
+constexpr int kRings = NW * Rows<T, D>::RING;
 static_assert(kRings<__nv_bfloat16, 64> >= NW * 8 * 64 * 4, "shares");
 // CTAs an SM holds.
 template <typename T, int D>
@@ -40,7 +43,7 @@ __global__ void __launch_bounds__(NT, kPerSm<T, D>) prefix_rows_kernel(const __g
   const int grp = blockIdx.x % groups, rest = blockIdx.x / groups, h = rest % A.Hkv, s = rest / A.Hkv;
   const int r0 = grp * 8, R = min(8, A.rows - r0), gn = A.G * A.nq;
   const int k0 = s * per, k1 = min(A.P, k0 + per);
-  RowStream<T, D> S;
+  Rows<T, D> S;
   S.init(rings + warp * S.RING);
   {
     const int row = r0 + min(S.g, R - 1), b = row / gn;
@@ -160,7 +163,7 @@ __global__ void __launch_bounds__(NT, kPerSm<T, D>) own_slots_kernel(const __gri
       c.tiles = (c.n + 15) >> 4;
     };
     const int gn = A.G * A.nq;
-    RowStream<T, D> S;
+    Rows<T, D> S;
     S.init(rings + warp * S.RING);
     Cursor ahead = at;
     auto fill = [&](int stage) {
