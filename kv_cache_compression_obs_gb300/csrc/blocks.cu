@@ -99,18 +99,21 @@ __device__ __forceinline__ float products(uint32_t a, uint32_t b, __nv_bfloat16)
 }
 __device__ __forceinline__ float products(uint32_t a, uint32_t b, float) { return fabsf(__uint_as_float(a) * __uint_as_float(b)); }
 
-// u of block j in 64 bits: one warp, lanes over the channels; every lane gets it.
+// The passes below run once or twice per launch, so their instructions come from memory: short loops beat
+// unrolled ones (keys held in registers and everything unrolled: 13.8 us for 12.2).
+
+// u of block j in 64 bits (q [G][D] as floats): one warp, lanes over the channels; every lane gets it.
 template <typename T, int D>
-__device__ double bound64(const BlkArgs &A, const T *q, const T *digest, int j) {
+__device__ __noinline__ double bound64(int G, const float *q, const T *digest, int j) {
   const int lane = threadIdx.x & 31;
   const T *low = digest + (long)j * 2 * D, *top = low + D;
   double best = -INFINITY;
-  for (int g = 0; g < A.G; ++g) {
+  for (int g = 0; g < G; ++g) {
     double s = 0.;
 #pragma unroll
     for (int i = 0; i < D / 32; ++i) {
       const int c = lane + 32 * i;
-      const double x = (double)to_f32(q[g * A.sq[1] + c]);
+      const double x = (double)q[g * D + c];
       s += (x != x || x > 0. ? x : 0.) * (double)to_f32(top[c]) + (x != x || x < 0. ? x : 0.) * (double)to_f32(low[c]);
     }
 #pragma unroll
@@ -128,31 +131,30 @@ __device__ __forceinline__ void two_sum(float a, float b, float &s, float &e) {
   e = __fadd_rn(__fsub_rn(a, __fsub_rn(s, x)), __fsub_rn(b, x));
 }
 template <typename T, int D>
-__device__ double bound_pairs(const BlkArgs &A, const T *q, const T *digest, int j) {
+__device__ __noinline__ double bound_pairs(int G, const float *q, const T *digest, int j) {
   const int lane = threadIdx.x & 31;
-  const T *row = digest + (long)j * 2 * D;
+  const T *row = digest + (long)j * 2 * D + lane;
   float low[D / 32], top[D / 32];
 #pragma unroll
   for (int i = 0; i < D / 32; ++i) {
-    low[i] = to_f32(row[lane + 32 * i]);
-    top[i] = to_f32(row[D + lane + 32 * i]);
+    low[i] = to_f32(row[32 * i]);
+    top[i] = to_f32(row[D + 32 * i]);
   }
   double best = -INFINITY;
-  for (int g = 0; g < A.G; ++g) {
-    float hi = 0.f, lo = 0.f;
+#pragma unroll 1
+  for (int g = 0; g < G; ++g) {
+    float hi = 0.f, lo = 0.f, e;
 #pragma unroll
     for (int i = 0; i < D / 32; ++i) {
-      const float x = to_f32(q[g * A.sq[1] + lane + 32 * i]), y = x >= 0.f ? top[i] : low[i];
+      const float x = q[g * D + lane + 32 * i], y = x >= 0.f ? top[i] : low[i];
       const float p = __fmul_rn(x, y), pe = __fmaf_rn(x, y, -p);
-      float e;
       two_sum(hi, p, hi, e);
       lo = __fadd_rn(lo, __fadd_rn(e, pe));
     }
-#pragma unroll
+#pragma unroll 1
     for (int o = 16; o; o >>= 1) {
       const float a = __shfl_xor_sync(0xFFFFFFFFu, hi, o), b = __shfl_xor_sync(0xFFFFFFFFu, lo, o);
-      float e;
-      // the same sum in both lanes: larger lane's first
+      // the same sum in both lanes
       two_sum(lane & o ? a : hi, lane & o ? hi : a, hi, e);
       lo = __fadd_rn(__fadd_rn(lo, b), e);
     }
@@ -192,7 +194,6 @@ __device__ uint32_t mth_largest(const Choice &c, int n, int m, uint32_t least, u
   for (;;) {
     const uint32_t range = most - least;
     const int s = max(0, 24 - __clz(range));  // range >> s is below kBins
-#pragma unroll 4
     for (int i = threadIdx.x; i < n; i += NT) {
       const uint32_t k = c.key[i] - least;
       if (k <= range) atomicAdd(c.hist + (k >> s), 1);
@@ -225,7 +226,6 @@ __device__ uint32_t mth_largest(const Choice &c, int n, int m, uint32_t least, u
     most = min(most, least + (uint32_t)((1ull << s) - 1));
     if (most == least) return least;
     if (held <= kFew) {
-#pragma unroll 4
       for (int i = threadIdx.x; i < n; i += NT) {
         const uint32_t k = c.key[i];
         if (k >= least && k <= most) c.few[atomicAdd(&count, 1)] = k;
@@ -250,7 +250,7 @@ __device__ uint32_t mth_largest(const Choice &c, int n, int m, uint32_t least, u
 // The best `m` of the n candidates (block lo + i; their bounds' bits in c.key) to c.list, ascending, as blocks.
 // err: how far a bound may be off; wide: only 64 bits tell them apart.
 template <typename T, int D>
-__device__ void choose(const BlkArgs &A, const Choice &c, const T *q, const T *digest, int lo, int n, int m, float err,
+__device__ void choose(int G, const Choice &c, const float *q, const T *digest, int lo, int n, int m, float err,
                        bool wide, uint32_t least, uint32_t most, int (*red)[NW], uint32_t (*redu)[NW], int &count) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const float a = unorder(mth_largest(c, n, m, least, most, red, redu, count));
@@ -258,7 +258,6 @@ __device__ void choose(const BlkArgs &A, const Choice &c, const T *q, const T *d
   // each warp has a stretch of the candidates, 32 at a time
   const int stretch = (n + NT - 1) / NT * 32, i0 = min(n, warp * stretch), i1 = min(n, i0 + stretch);
   int sure = 0, open = 0;
-#pragma unroll 4
   for (int i = i0 + lane; i < i0 + stretch; i += 32) {
     const float x = i < i1 ? unorder(c.key[i]) : -INFINITY;
     sure += __popc(__ballot_sync(0xFFFFFFFFu, i < i1 && x > above));
@@ -287,7 +286,7 @@ __device__ void choose(const BlkArgs &A, const Choice &c, const T *q, const T *d
     __syncthreads();
     for (int i = warp; i < all_open; i += NW) {
       const int j = lo + c.list[i];
-      const double x = wide ? bound64<T, D>(A, q, digest, j) : bound_pairs<T, D>(A, q, digest, j);
+      const double x = wide ? bound64<T, D>(G, q, digest, j) : bound_pairs<T, D>(G, q, digest, j);
       if (lane == 0) c.exact[i] = x;
     }
     __syncthreads();
@@ -307,7 +306,6 @@ __device__ void choose(const BlkArgs &A, const Choice &c, const T *q, const T *d
     at = 0;
     for (int w = 0; w < warp; ++w) at += red[0][w] + red[1][w];
   }
-#pragma unroll 4
   for (int i = i0 + lane; i < i0 + stretch; i += 32) {
     const uint32_t k = i < i1 ? c.key[i] : 0u;
     const float x = unorder(k);
@@ -377,6 +375,7 @@ __global__ void __launch_bounds__(NT, kPerSm<T, D>) blocks_kernel(const __grid_c
   c.key = reinterpret_cast<uint32_t *>(c.exact + A.nb);
   c.list = reinterpret_cast<uint16_t *>(mine + ((A.nb / CL + 20) & ~3));
   if (cap_c > 0) {
+    for (int i = threadIdx.x; i < G * D; i += NT) sh[i] = to_f32(q[i / D * A.sq[1] + i % D]);  // for the near bounds
     const T *digest = static_cast<const T *>(A.digest) + bh * A.nb * 2L * D;
     const int per = (((nm + CL - 1) / CL) + 15) & ~15;
     const int i0 = min(nm, rank * per), i1 = min(nm, i0 + per);
@@ -458,7 +457,6 @@ __global__ void __launch_bounds__(NT, kPerSm<T, D>) blocks_kernel(const __grid_c
     for (int r = 0; r < CL; ++r) size = fmaxf(size, *cl.map_shared_rank(&err_cta, r));
     uint32_t least = 0xFFFFFFFFu, most = 0u;
     // a stretch of four (of a CTA's bounds, whose number is a multiple of 16) at a time
-#pragma unroll 4
     for (int i = threadIdx.x * 4; i < nm; i += NT * 4) {
       const int r = i / per;
       const float4 v = *reinterpret_cast<const float4 *>(cl.map_shared_rank(mine, r) + (i - r * per));
@@ -476,7 +474,7 @@ __global__ void __launch_bounds__(NT, kPerSm<T, D>) blocks_kernel(const __grid_c
     // a bound that is no number, or terms that fp32 does not hold: 64 bits decide for all of them
     wide = __syncthreads_or(wide || !(size < 0x1p120f) || (size > 0.f && size < 0x1p-60f));
     c.list += A.sink;  // behind the first blocks
-    choose<T, D>(A, c, q, digest, lo, nm, m, wide ? INFINITY : size * 0x1p-16f, wide, least, most, red, redu, counter);
+    choose<T, D>(G, c, sh, digest, lo, nm, m, wide ? INFINITY : size * 0x1p-16f, wide, least, most, red, redu, counter);
     c.list -= A.sink;
   }
   for (int i = threadIdx.x; i < ns; i += NT)  // those that no bound decides
