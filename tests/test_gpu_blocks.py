@@ -161,6 +161,40 @@ def test_nan_and_overflow_in_digests(kvc):
     assert sel[0, 0, 0].tolist() == choose(q[0, :, 0].double(), dig[0, 0].double(), 3200, 32, 5, 0, 1)
 
 
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+def test_many_blocks(kvc, dtype):
+    """Thousands of blocks, many of which have the same or nearly the same bounds: bins that overflow, whole
+    ranges of equal bounds."""
+    d, block, nb = 64, 16, 9000
+    g = torch.Generator(device="cuda").manual_seed(24)
+    K = torch.zeros(1, 2, nb * block, d, dtype=dtype, device="cuda")
+    # head 0: 40 different blocks, each many times; head 1: differences in the last places around a large value
+    kinds = rand((40, d), F32, 25)
+    K.view(1, 2, nb, block, d)[0, 0] = kinds[torch.randint(0, 40, (nb,), generator=g, device="cuda")].to(dtype)[:, None]
+    K[0, 1, :, 0] = 64.0
+    K.view(1, 2, nb, block, d)[0, 1, :, :, 1] = (torch.randint(0, 256, (nb,), generator=g, device="cuda").float() / 256).to(dtype)[:, None]
+    V, q = rand(K.shape, dtype, 26), rand((1, 4, 1, d), dtype, 27)
+    q[..., 0], q[..., 1] = 100.0, 0.01
+    ln = torch.full((1, 2), nb * block - 5, dtype=torch.int32)
+    dig = kvc.kv_block_digest(K, block, ln.cuda())
+    for n_sel in (8, 700, 5000):
+        o, lse, sel = kvc.kv_attn_blocks(q, K, V, ln.cuda(), dig, block, n_sel, sink=2, recent=3)
+        _check(q, K, V, ln, dig, block, n_sel, 2, 3, o, lse, sel, d ** -0.5)
+
+
+def test_as_many_blocks_as_there_may_be(kvc):
+    nb = 12288
+    K, V, q = _keys(1, 2, nb * 16, 128, BF, 80), rand((1, 2, nb * 16, 128), BF, 81), rand((1, 16, 1, 128), BF, 82)
+    ln = torch.tensor([[nb * 16, nb * 16 - 40]], dtype=torch.int32)
+    dig = kvc.kv_block_digest(K, 16, ln.cuda(), out=torch.zeros(1, 2, nb, 2, 128, dtype=BF, device="cuda"))
+    o, lse, sel = kvc.kv_attn_blocks(q, K, V, ln.cuda(), dig, 16, 50, sink=1, recent=2)
+    _check(q, K, V, ln, dig, 16, 50, 1, 2, o, lse, sel, 128 ** -0.5)
+    K = K.float()
+    dig = kvc.kv_block_digest(K, 16, ln.cuda(), out=torch.zeros(1, 2, nb, 2, 128, device="cuda"))
+    o, lse, sel = kvc.kv_attn_blocks(q.float(), K, V.float(), ln.cuda(), dig, 16, 50, sink=1, recent=2)
+    _check(q.float(), K, V.float(), ln, dig, 16, 50, 1, 2, o, lse, sel, 128 ** -0.5)
+
+
 def test_layouts_scale_and_given_outputs(kvc):
     B, Hq, Hkv, nq, cap, d = 2, 8, 2, 3, 500, 128
     K, V = _keys(B, Hkv, cap, d, BF, 40), rand((B, Hkv, cap, d), BF, 41)

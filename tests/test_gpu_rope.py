@@ -159,6 +159,38 @@ def test_lengths_and_slots_out_of_range(kvc):
         assert torch.equal(o[1, 0, :3], w[1, 0, 3:]) and (o[1, 0, 3:] == 5).all() and (o[2, 0] == 5).all()
 
 
+@pytest.mark.parametrize("case", [
+    # B, T, Hq, Hkv, d, rot, interleaved, dtype, keys and values only: thousands of tokens through the ring
+    (1, 9001, 32, 8, 128, 128, False, BF, False),
+    (3, 2000, 5, 3, 64, 32, True, F32, False),
+    (2, 5003, 9, 9, 128, 64, False, BF, False),
+    (1, 9001, 32, 8, 128, 128, True, BF, True),
+    (1, 6000, 1, 40, 64, 24, False, BF, False),
+], ids=str)
+def test_many_tokens(kvc, case):
+    B, T, Hq, Hkv, d, rot, inter, dtype, only = case
+    q, k, v = rand((B, T, Hq + 2 * Hkv, d), dtype, 60).transpose(1, 2).split([Hq, Hkv, Hkv], 1)
+    f, _ = kvc.kv_rope_freqs(rot)
+    pos = (torch.arange(B * T, device="cuda") * 17 % 100003).int().view(B, T)
+    wk = (1 + 0.3 * rand((d,), F32, 61)).to(dtype)
+    slot = torch.arange(B * Hkv, dtype=torch.int32, device="cuda").view(B, Hkv) % 5 - 1  # token 0 of some heads has no row
+    K, V = torch.full((B, Hkv, T, d), 3.0, dtype=dtype, device="cuda"), torch.full((B, Hkv, T, d), 4.0, dtype=dtype, device="cuda")
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    qo = kvc.kv_qk_norm_rope(None if only else q, k, v, f, pos, k_weight=wk, eps=EPS, interleaved=inter, slot=slot, k_out=K, v_out=V,
+                             dev_status=st)[0]
+    assert int(st) == -1
+    if not only:
+        _near(qo, _want(q, None, f, pos, inter, EPS, False, 1.0), "q")
+    want = _want(k, wk, f, pos, inter, EPS, False, 1.0)
+    for b in range(B):
+        for h in range(Hkv):
+            s = int(slot[b, h])
+            lo, hi = max(0, s), min(T, T + s)
+            _near(K[b, h, lo:hi], (want[0][b, h, lo - s:hi - s], want[1][b, h, lo - s:hi - s]), f"k {b} {h}")
+            assert torch.equal(V[b, h, lo:hi], v[b, h, lo - s:hi - s])
+            assert (K[b, h, :lo] == 3).all() and (V[b, h, :lo] == 4).all() and (K[b, h, hi:] == 3).all()
+
+
 def test_captured(kvc):
     """A decode step's call, replayed with other positions and slots in the same tensors."""
     B, Hq, Hkv, d, cap = 4, 8, 2, 128, 16

@@ -107,6 +107,45 @@ def test_rising_logits_and_large_values(kvc, dtype):
     _check(q, Kp.flip(1), Vp, K, V, ln, o, lse, d ** -0.5)
 
 
+@pytest.mark.parametrize("case", [
+    # B, Hq, Hkv, nq, P, cap, d, dtype, lens: many rows of little; more heads than lengths are kept on chip
+    (300, 16, 8, 1, 40, 64, 64, BF, "some empty"),
+    (600, 8, 4, 1, 17, 40, 64, F32, "some empty"),
+    (3, 4, 4, 1, 200, 5000, 128, BF, "one long"),
+    (64, 2, 2, 1, 100, 3000, 128, BF, "one long"),
+    (2, 2, 1, 1, 100, 50, 64, BF, "none"),
+], ids=str)
+def test_uneven_lengths(kvc, case):
+    B, Hq, Hkv, nq, P, cap, d, dtype, how = case
+    Kp, Vp, q = rand((Hkv, P, d), dtype, 60), rand((Hkv, P, d), dtype, 61), rand((B, Hq, nq, d), dtype, 62)
+    K, V = rand((B, Hkv, cap, d), dtype, 63), rand((B, Hkv, cap, d), dtype, 64)
+    ln = _lens(B, Hkv, 0, cap, 65) * (_lens(B, Hkv, 0, 3, 66) > 1) if how == "some empty" else torch.zeros(B, Hkv, dtype=torch.int32)
+    if how == "one long":
+        ln[B // 2, 1], ln[0, 0], ln[-1, -1] = cap, 1, 33
+    o, lse = kvc.kv_attn_shared(q, Kp, Vp, K, V, ln.to(torch.int32).cuda())
+    g = torch.Generator().manual_seed(67)
+    units = {(int(torch.randint(0, B, (1,), generator=g)), int(torch.randint(0, Hkv, (1,), generator=g))) for _ in range(150)}
+    _check(q, Kp, Vp, K, V, ln, o, lse, d ** -0.5, units=units | {(0, 0), (B // 2, Hkv - 1), (B - 1, Hkv - 1)})
+
+
+def test_offsets_past_32_bits(kvc):
+    """Own slots of more than 2^31 elements: the last rows'."""
+    B, Hkv, cap, d = 17, 1, 1000000, 128
+    K = torch.empty(B, Hkv, cap, d, dtype=BF, device="cuda")
+    V = torch.empty(B, Hkv, cap, d, dtype=BF, device="cuda")
+    K[-1, :, :5000], V[-1, :, :5000] = rand((Hkv, 5000, d), BF, 70), rand((Hkv, 5000, d), BF, 71)
+    K[-1, :, -300:], V[-1, :, -300:] = rand((Hkv, 300, d), BF, 72), rand((Hkv, 300, d), BF, 73)
+    q, Kp, Vp = rand((B, 2, 1, d), BF, 74), rand((Hkv, 64, d), BF, 75), rand((Hkv, 64, d), BF, 76)
+    ln = torch.zeros(B, Hkv, dtype=torch.int32)
+    ln[-1] = 5000
+    o, lse = kvc.kv_attn_shared(q, Kp, Vp, K, V, ln.cuda())
+    _check(q, Kp, Vp, K, V, ln, o, lse, d ** -0.5)
+    K[-1, :, 5000:-300], V[-1, :, 5000:-300] = 0, 0
+    ln[-1] = cap
+    o, lse = kvc.kv_attn_shared(q, Kp, Vp, K, V, ln.cuda())
+    _check(q, Kp, Vp, K, V, ln, o, lse, d ** -0.5, units=[(B - 1, 0)])
+
+
 def test_nan_reaches_the_rows_that_see_it(kvc):
     B, Hq, Hkv, P, cap, d = 3, 4, 2, 500, 100, 128
     q, Kp, Vp = rand((B, Hq, 1, d), BF, 30), rand((Hkv, P, d), BF, 31), rand((Hkv, P, d), BF, 32)
