@@ -712,12 +712,17 @@ def kv_rope_freqs(rot: int, theta: float = 10000.0, scaling: str | None = None, 
     return torch.tensor(f[:rot // 2], dtype=torch.float64, device=device), scale.value
 
 
-def _sigs(dev: int, *ts):
-    """What a call's checks read of its tensors, which have to be on device `dev`."""
-    for t in ts:
-        if t is not None and t.get_device() != dev:
-            raise ValueError(f"tensors must be on cuda:{dev}")
-    return tuple([None if t is None else (t.shape, t.stride(), t.dtype) for t in ts])
+def _sigs(*ts):
+    """What a call's checks read of its tensors."""
+    return tuple([None if t is None else (t.shape, t.stride(), t.dtype, t.get_device()) for t in ts])
+
+
+def _one_device(sigs) -> int:
+    """The index of the CUDA device that all of a call's tensors are on."""
+    dev = [t[3] for t in sigs if t]
+    if dev[0] < 0 or any(d != dev[0] for d in dev):
+        raise ValueError("tensors must be CUDA tensors on one device")
+    return dev[0]
 
 
 # Checks that depend on shapes, strides and types alone are made once for each combination of them: a call
@@ -726,7 +731,8 @@ def _sigs(dev: int, *ts):
 def _rope_plan(sigs):
     """The call's strides and sizes as the library takes them, or ValueError."""
     q, k, v, q_out, k_out, v_out, inv_freq, pos, q_weight, k_weight, slot, seq, _ = sigs
-    (B, _, T, d), _, dt = q or k or v
+    dev = _one_device(sigs)
+    (B, _, T, d), _, dt, _ = q or k or v
     if dt not in _CODES:
         raise TypeError(f"expected bfloat16 or float32, got {dt}")
     if k and v and k[0] != v[0]:
@@ -758,7 +764,7 @@ def _rope_plan(sigs):
             raise ValueError("the d elements of a row must be adjacent")
         strides += t[1][:3] if on else (0, 0, 0)
     return ((ctypes.c_int64 * 18)(*strides), B, q[0][1] if q else 0, Hkv, T, cap or 0, d, 2 * inv_freq[0][0] if inv_freq else 0,
-            _CODES[dt])
+            _CODES[dt], dev)
 
 
 def _dense(t) -> bool:
@@ -774,6 +780,14 @@ def _dense(t) -> bool:
 _CODES = {torch.bfloat16: KV_BF16, torch.float32: KV_F32}
 
 
+def _new(shape, dtype, like, stream):
+    """An uninitialised dense tensor for a call on `stream`, on the device of `like`."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=like.device)
+
+
 def kv_qk_norm_rope(q, k, v, inv_freq, pos=None, q_weight=None, k_weight=None, eps: float | None = None,
                     interleaved: bool = False, one_plus: bool = False, rot_scale: float = 1.0, slot=None, seq=None,
                     q_out=None, k_out=None, v_out=None, dev_status=None, stream=None):
@@ -787,28 +801,26 @@ def kv_qk_norm_rope(q, k, v, inv_freq, pos=None, q_weight=None, k_weight=None, e
     1 + those.  k_out, v_out [B][Hkv][cap][d]: with slot [B][Hkv] int32 (a slot cache's len) token t goes to row
     slot + t, without it to row t; other rows stay.  seq [B] int32: only the first tokens of each row.  Outputs
     not given are dense tensors of T rows (with slot, k_out and v_out have to be given)."""
-    x = q if q is not None else k if k is not None else v
-    if x is None:
+    if q is None and k is None and v is None:
         raise ValueError("one of q, k and v must be given")
-    dev = _device_of(x)
-    if (q_out is None and q is not None) or (k_out is None and k is not None) or (v_out is None and v is not None):
-        if slot is not None and ((k is not None and k_out is None) or (v is not None and v_out is None)):
-            raise ValueError("slot needs k_out and v_out")
-        with _side(stream):
-            if q is not None and q_out is None:
-                q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-            if k is not None and k_out is None:
-                k_out = torch.empty(k.shape, dtype=k.dtype, device=k.device)
-            if v is not None and v_out is None:
-                v_out = torch.empty(v.shape, dtype=v.dtype, device=v.device)
+    if slot is not None and ((k is not None and k_out is None) or (v is not None and v_out is None)):
+        raise ValueError("slot needs k_out and v_out")
     if q is None:
         q_out = None
+    elif q_out is None:
+        q_out = _new(q.shape, q.dtype, q, stream)
     if k is None:
         k_out = None
+    elif k_out is None:
+        k_out = _new(k.shape, k.dtype, k, stream)
     if v is None:
         v_out = None
-    strides, B, Hq, Hkv, T, cap, d, rot, code = _rope_plan(
-        _sigs(dev, q, k, v, q_out, k_out, v_out, inv_freq, pos, q_weight, k_weight, slot, seq, dev_status))
+    elif v_out is None:
+        v_out = _new(v.shape, v.dtype, v, stream)
+    strides, B, Hq, Hkv, T, cap, d, rot, code, dev = _rope_plan(
+        _sigs(q, k, v, q_out, k_out, v_out, inv_freq, pos, q_weight, k_weight, slot, seq, dev_status))
+    if dev != _get_device():
+        _on_current_device(q if q is not None else k if k is not None else v)
     flags = (KV_ROPE_INTERLEAVED if interleaved else 0) | (KV_ROPE_ONE_PLUS if one_plus else 0)
     if eps is not None:
         flags |= KV_ROPE_NORM
@@ -852,6 +864,7 @@ def _flat(*st):
 @functools.lru_cache(maxsize=4096)
 def _blocks_plan(sigs, block, n_sel):
     q, K, V, ln, dig, o, lse, sel, _ = sigs
+    dev = _one_device(sigs)
     so = _rows_plan(q, o, lse)
     _cache_plan(q, K, V, ln)
     B, Hq, n, d = q[0]
@@ -860,12 +873,13 @@ def _blocks_plan(sigs, block, n_sel):
         raise ValueError("digest must be [B][Hkv][ceil(cap / block)][2][d] in q's dtype, contiguous")
     if sel and (sel[0] != (B, Hkv, n, n_sel) or sel[2] != _I32 or not _dense(sel)):
         raise ValueError("sel_out must be [B][Hkv][n][n_sel] int32, contiguous")
-    return B, Hq, Hkv, n, cap, d, _CODES[q[2]], d ** -0.5, _flat(q[1][:3], so[:3])
+    return B, Hq, Hkv, n, cap, d, _CODES[q[2]], dev, d ** -0.5, _flat(q[1][:3], so[:3])
 
 
 @functools.lru_cache(maxsize=4096)
 def _shared_plan(sigs):
     q, kp, vp, K, V, ln, o, lse, ws, _ = sigs
+    dev = _one_device(sigs)
     so = _rows_plan(q, o, lse)
     if ws and not _dense(ws):
         raise ValueError("workspace must be contiguous")
@@ -881,7 +895,7 @@ def _shared_plan(sigs):
         P = kp[0][1] if len(kp[0]) == 3 else -1
         if kp[0] != (Hkv, P, d) or vp[0] != kp[0] or kp[2] != q[2] or vp[2] != q[2] or kp[1][2] != 1 or vp[1][2] != 1:
             raise ValueError("the prefix must be [Hkv][P][d] in q's dtype, with adjacent elements along d")
-    return (B, Hq, Hkv, n, P, cap, d, _CODES[q[2]], d ** -0.5, kv_workspace_size(KV_OP_ATTN_SHARED, B, Hq, Hkv, max(1, P), d, n, P),
+    return (B, Hq, Hkv, n, P, cap, d, _CODES[q[2]], dev, d ** -0.5, kv_workspace_size(KV_OP_ATTN_SHARED, B, Hq, Hkv, max(1, P), d, n, P),
             _flat(q[1][:3], kp[1][:2] if kp else (0, 0), vp[1][:2] if kp else (0, 0), so[:3]))
 
 
@@ -918,17 +932,17 @@ def kv_attn_blocks(q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, len_: torc
     The new tokens are the last n filled slots; token t sees the slots j < len - n + t + 1.  Each (token, KV head)
     attends the first `sink` and last `recent` of the blocks that it sees and the others with the largest bounds on
     their logits, n_sel in all.  q's and out's batch, head and token strides are free."""
-    dev = _device_of(q)
-    B, Hq, Hkv, n, cap, d, code, default_scale, strides = _blocks_plan(
-        _sigs(dev, q, K, V, len_, digest, out, lse_out, sel_out, dev_status), block, n_sel)
-    if out is None or lse_out is None or sel_out is None:
+    B, Hq, Hkv, n, cap, d, code, dev, default_scale, strides = _blocks_plan(
+        _sigs(q, K, V, len_, digest, out, lse_out, sel_out, dev_status), block, n_sel)
+    if dev != _get_device():
+        _on_current_device(q)
+    if out is None:
         with _side(stream):
-            if out is None:
-                out = torch.empty_like(q)
-            if lse_out is None:
-                lse_out = torch.empty((B, Hq, n), dtype=_F32, device=q.device)
-            if sel_out is None:
-                sel_out = torch.empty((B, Hkv, n, max(0, n_sel)), dtype=_I32, device=q.device)
+            out = torch.empty_like(q)
+    if lse_out is None:
+        lse_out = _new((B, Hq, n), _F32, q, stream)
+    if sel_out is None:
+        sel_out = _new((B, Hkv, n, max(0, n_sel)), _I32, q, stream)
     status = _lib.kv_attn_blocks(
         q.data_ptr(), K.data_ptr(), V.data_ptr(), len_.data_ptr(), digest.data_ptr(), B, Hq, Hkv, n, cap, d, block, n_sel, sink,
         recent, strides, default_scale if scale is None else scale, code, out.data_ptr(),
@@ -946,19 +960,24 @@ def kv_attn_shared(q: torch.Tensor, K_prefix, V_prefix, K, V, len_, scale: float
 
     Every token sees the whole prefix; the new tokens are the last n own slots and token t sees the own slots
     j < len - n + t + 1.  Strides of q, out and the prefix are free but for the d adjacent elements."""
-    dev = _device_of(q)
-    B, Hq, Hkv, n, P, cap, d, code, default_scale, need, strides = _shared_plan(
-        _sigs(dev, q, K_prefix, V_prefix, K, V, len_, out, lse_out, workspace, dev_status))
-    with _side(stream):
-        if out is None:
+    B, Hq, Hkv, n, P, cap, d, code, dev, default_scale, need, strides = _shared_plan(
+        _sigs(q, K_prefix, V_prefix, K, V, len_, out, lse_out, workspace, dev_status))
+    if dev != _get_device():
+        _on_current_device(q)
+    if out is None:
+        with _side(stream):
             out = torch.empty_like(q)
-        if lse_out is None:
-            lse_out = torch.empty((B, Hq, n), dtype=_F32, device=q.device)
-        ws, nbytes = _workspace(need, q.device, workspace)
+    if lse_out is None:
+        lse_out = _new((B, Hq, n), _F32, q, stream)
+    ws, nbytes = workspace, need
+    if ws is None:
+        ws = _new(need, torch.uint8, q, stream)
+    else:
+        nbytes = ws.numel() * ws.element_size()
     status = _lib.kv_attn_shared(
         q.data_ptr(), _at(K_prefix), _at(V_prefix), _at(K), _at(V), _at(len_), B, Hq, Hkv, n, P, cap, d,
         strides, default_scale if scale is None else scale, code, out.data_ptr(),
-        lse_out.data_ptr(), _at(ws), nbytes, _at(dev_status), _stream_of(dev, stream))
+        lse_out.data_ptr(), ws.data_ptr(), nbytes, _at(dev_status), _stream_of(dev, stream))
     if status:
         _check("kv_attn_shared", status)
     return out, lse_out

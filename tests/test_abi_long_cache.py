@@ -140,17 +140,21 @@ def test_binding_refusals(api):
 def test_binding_plans(api):
     """The binding's checks of shapes, strides and types."""
     import torch
-    sig = lambda *ts: tuple(None if t is None else (t.shape, t.stride(), t.dtype) for t in ts)  # noqa: E731
+    sig = lambda *ts: tuple(None if t is None else (t.shape, t.stride(), t.dtype, 0) for t in ts)  # noqa: E731
     z = lambda *s, dtype=torch.bfloat16: torch.zeros(*s, dtype=dtype)  # noqa: E731
     i32 = torch.int32
     q, k = z(2, 4, 3, 64), z(2, 2, 3, 64)
     good = dict(q=q, k=k, v=k, q_out=q, k_out=k, v_out=k, f=z(32, dtype=torch.float64), pos=z(2, 3, dtype=i32), wq=z(64), wk=z(64),
                 slot=z(2, 2, dtype=i32), seq=z(2, dtype=i32), st=None)
-    assert api._rope_plan(sig(*good.values()))[1:] == (2, 4, 2, 3, 3, 64, 64, 0)
+    assert api._rope_plan(sig(*good.values()))[1:] == (2, 4, 2, 3, 3, 64, 64, 0, 0)
     for name, t in dict(k=z(2, 2, 4, 64), v=z(2, 3, 3, 64), q_out=z(2, 4, 4, 64), k_out=z(2, 3, 3, 64), f=z(32), pos=z(2, 3),
                         wq=z(32), slot=z(2, 3, dtype=i32), seq=z(3, dtype=i32), v_out=z(2, 2, 5, 64)).items():
         with pytest.raises(ValueError):
             api._rope_plan(sig(*{**good, name: t}.values()))
+    on_two = sig(*good.values())
+    for dev in (1, -1):
+        with pytest.raises(ValueError):
+            api._rope_plan(on_two[:1] + (on_two[1][:3] + (dev,),) + on_two[2:])
     with pytest.raises(TypeError):
         api._rope_plan(sig(*[z(2, 2, 3, 64, dtype=torch.float16)] * 6, *[None] * 7))
     K, ln, dig = z(2, 2, 100, 64), z(2, 2, dtype=i32), z(2, 2, 7, 2, 64)
