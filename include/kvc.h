@@ -634,8 +634,8 @@ KVC_API int kv_evict_q8(const kv_q8_cache *cache, int keep, int recent, int sink
  *              so `slot` is the cache's len and the caller adds T to it afterwards;
  *              other rows are left as they were
  *   seq        tokens behind a row's seq are neither read nor written
- *   in place   q_out == q with the same strides (and k, v likewise) is allowed; any other
- *              overlap of inputs and outputs is not
+ *   in place   q_out == q with the same strides is allowed, and k_out == k, v_out == v
+ *              without slot; any other overlap of inputs and outputs is not
  *   dev_status device int, may be NULL; KV_ERR_INVALID_ARG when a row of k_out, v_out
  *              would be outside [0, cap) (that row is not written) or a seq is outside [0, T]
  *              (nothing of that batch row is written); never cleared
@@ -697,8 +697,7 @@ KVC_API int kv_block_digest(const void *K, const int32_t *len, int B, int Hkv, i
  *              (that unit's outputs are left as they were); never cleared
  * Preconditions: Hq % Hkv == 0, Hq / Hkv <= 8, d in {64, 128}, block as kv_block_digest,
  * 0 <= sink, 1 <= recent, sink + recent <= n_sel, scale > 0, at most 12288 blocks.
- * No workspace.  V is finite in the slots that len covers (a token multiplies up to 15 that
- * it does not see by 0); what stands behind len is not used.
+ * No workspace.  Slots that a token does not see are not used, whatever they hold.
  */
 KVC_API int kv_attn_blocks(const void *q, const void *K, const void *V, const int32_t *len, const void *digest,
                            int B, int Hq, int Hkv, int nq, int cap, int d, int block, int n_sel, int sink,
@@ -725,7 +724,7 @@ KVC_API int kv_attn_blocks(const void *q, const void *K, const void *V, const in
  *              (that unit's outputs are left as they were), KV_ERR_TIMEOUT when a bounded
  *              device-side wait gave up; never cleared
  * Preconditions: Hq % Hkv == 0, d in {64, 128}, scale > 0.  V is finite in the slots that
- * len covers; what stands behind len is not used.
+ * len covers (a token multiplies later new tokens' by 0); what stands behind len is not used.
  * bf16: the prefix's products on the tensor cores (tcgen05, TMA), its weights rounded to
  * bf16 before the second product; fp32 and the own slots: fp32 accuracy.
  */

@@ -799,8 +799,8 @@ def kv_qk_norm_rope(q, k, v, inv_freq, pos=None, q_weight=None, k_weight=None, e
     inv_freq [rot / 2] float64 (kv_rope_freqs; None: no rotation); the first 2 * numel elements of a head turn.
     pos [B][T] int32 (None: 0..T-1).  q_weight, k_weight [d] in q's dtype or None; one_plus: the weights are
     1 + those.  k_out, v_out [B][Hkv][cap][d]: with slot [B][Hkv] int32 (a slot cache's len) token t goes to row
-    slot + t, without it to row t; other rows stay.  seq [B] int32: only the first tokens of each row.  Outputs
-    not given are dense tensors of T rows (with slot, k_out and v_out have to be given)."""
+    slot + t, without it to row t; other rows stay.  seq [B] int32: only the first tokens of each row.  An output may
+    be its input itself (k and v: without slot).  Outputs not given are dense tensors of T rows (with slot, k_out and v_out have to be given)."""
     if q is None and k is None and v is None:
         raise ValueError("one of q, k and v must be given")
     if slot is not None and ((k is not None and k_out is None) or (v is not None and v_out is None)):

@@ -579,7 +579,7 @@ int kv_qk_norm_rope(const kv_qkv_heads *heads, int *dev_status, kv_stream_t stre
   const void *const in[3] = {h.q, h.k, h.v};
   void *const out[3] = {h.q_out, h.k_out, h.v_out};
   if (!fits((long long)h.B * h.T, ((long long)h.Hq + 2LL * h.Hkv) * h.d) || !fits((long long)h.B * h.Hkv, (long long)h.cap * h.d) ||
-      (long long)h.B * h.T > INT_MAX || (long long)h.Hq + 2LL * h.Hkv > 65536)
+      (long long)h.B * h.T > INT_MAX - 65536 || (long long)h.Hq + 2LL * h.Hkv > 65536)
     return KV_ERR_INVALID_ARG;
   if (h.B == 0 || h.T == 0 || (!h.q && !h.k && !h.v)) return KV_OK;
   const int eb = h.dtype == KV_F32 ? 4 : 2;
@@ -642,7 +642,7 @@ int kv_attn_shared(const void *q, const void *Kp, const void *Vp, const void *K,
   if (B < 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0 || nq < 0 || P < 0 || cap < 0 || !dtype_ok(dtype) || !(scale > 0) ||
       !std::isfinite(scale))
     return KV_ERR_INVALID_ARG;
-  if (!dim_ok(d)) return KV_ERR_UNSUPPORTED;
+  if (!dim_ok(d) || P > (1 << 30) || cap > (1 << 30)) return KV_ERR_UNSUPPORTED;
   if (!fits((long long)B * Hkv, (long long)cap * d) || !fits((long long)B * Hq, (long long)nq * d) ||
       !fits(Hkv, (long long)P * d) || (long long)B * (Hq / Hkv) > INT_MAX || (long long)B * (Hq / Hkv) * nq > INT_MAX)
     return KV_ERR_INVALID_ARG;

@@ -195,6 +195,45 @@ def test_as_many_blocks_as_there_may_be(kvc):
     _check(q.float(), K, V.float(), ln, dig, 16, 50, 1, 2, o, lse, sel, 128 ** -0.5)
 
 
+@pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+def test_hidden_slots_hold_anything(kvc, dtype):
+    """A later new token's value does not reach an earlier one, whatever it is."""
+    K, V, q = rand((1, 2, 500, 64), dtype, 90), rand((1, 2, 500, 64), dtype, 91), rand((1, 8, 3, 64), dtype, 92)
+    ln = torch.tensor([[490, 481]], dtype=torch.int32)
+    dig = kvc.kv_block_digest(K, 16, ln.cuda())
+    want = kvc.kv_attn_blocks(q, K, V, ln.cuda(), dig, 16, 6)
+    for h in range(2):
+        V[0, h, int(ln[0, h]) - 1] = float("inf")
+    o, lse, sel = kvc.kv_attn_blocks(q, K, V, ln.cuda(), dig, 16, 6)
+    assert torch.equal(o[:, :, :2], want[0][:, :, :2]) and torch.equal(lse, want[1]) and torch.equal(sel, want[2])
+    assert not o[:, :, 2].isfinite().any()
+
+
+def test_output_over_the_queries(kvc):
+    K, V, q = rand((2, 2, 900, 128), BF, 93), rand((2, 2, 900, 128), BF, 94), rand((2, 8, 2, 128), BF, 95)
+    ln = torch.full((2, 2), 900, dtype=torch.int32, device="cuda")
+    dig = kvc.kv_block_digest(K, 32)
+    want = kvc.kv_attn_blocks(q, K, V, ln, dig, 32, 6)
+    q2 = q.clone()
+    kvc.kv_attn_blocks(q2, K, V, ln, dig, 32, 6, out=q2)
+    assert torch.equal(q2, want[0])
+    want = kvc.kv_attn_shared(q, K[0], V[0], K, V, ln)[0]
+    kvc.kv_attn_shared(q, K[0], V[0], K, V, ln, out=q)
+    assert torch.equal(q, want)
+
+
+def test_first_call_of_its_sizes_in_a_capture(kvc):
+    """What is asked of the device once (which clusters fit) may be asked while a graph is being captured."""
+    K, V, q = rand((1, 3, 1777, 64), BF, 96), rand((1, 3, 1777, 64), BF, 97), rand((1, 6, 1, 64), BF, 98)
+    ln = torch.full((1, 3), 1700, dtype=torch.int32, device="cuda")
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        dig = kvc.kv_block_digest(K, 16, ln)
+        got = kvc.kv_attn_blocks(q, K, V, ln, dig, 16, 11, sink=1, recent=2)
+    g.replay()
+    _check(q, K, V, ln.cpu(), dig, 16, 11, 1, 2, *got, 64 ** -0.5)
+
+
 def test_layouts_scale_and_given_outputs(kvc):
     B, Hq, Hkv, nq, cap, d = 2, 8, 2, 3, 500, 128
     K, V = _keys(B, Hkv, cap, d, BF, 40), rand((B, Hkv, cap, d), BF, 41)
