@@ -18,11 +18,10 @@
 // and 2^-63 of itself, the angle by |pos| times that, far below the 2^-32 turns that are cut off;
 // fp32 products would lose it from positions of a few thousand on.
 //
-// Long calls move as much as a copy, and it is the instructions between load and store that keep
-// them from its rate: 32768 tokens of 32/8 heads 141 us, 5.7 TB/s, where the same kernel without the
-// arithmetic takes 122.  Rows loaded in batches of four groups with nothing in flight meanwhile 147 us
-// (4.7 of 10 cycles of an instruction waiting for them), 8 elements a lane and twice the warps 157, heads
-// fixed to a warp that goes through the tokens 171, a ring that is refilled across tensors by a cursor 164.
+// Long calls move as much as a copy and as fast: 32768 tokens of 32/8 heads
+// 124 us, 6.5 TB/s (0.96 of a copy's rate; without the arithmetic 122).  Rows loaded in batches of four groups with nothing in flight meanwhile 147 us (4.7 of 10 cycles of an instruction
+// waiting for them), 8 elements a lane and twice the warps 157, heads fixed to a warp that goes
+// through the tokens 171.
 #include <cmath>
 
 #include "kvc_internal.cuh"
@@ -33,7 +32,7 @@ namespace {
 
 constexpr int NT = 128, NW = NT / 32;
 constexpr int kPerSm = 4;       // CTAs of an SM
-constexpr int kRingGroups = 6;  // groups ahead of the one at hand, at least
+constexpr int kDeep = 6;        // groups that may be on their way behind the one at hand
 enum { HALVES = 0, NEIGHBOURS = 1, HALVES_ODD = 2 };
 
 struct RopeArgs {
@@ -127,8 +126,8 @@ __device__ __forceinline__ int2 odd_pair(int x, int rot) {
   return x < rot / 2 ? make_int2(x, x + rot / 2) : make_int2(2 * x, 2 * x + 1);
 }
 
-// This lane's elements of a row.
-template <typename T, int MODE>
+// This lane's elements of a row; one that is read once makes way for others in the caches.
+template <typename T, int MODE, bool ONCE = true>
 __device__ __forceinline__ void load_row(const T *p, int a, int b, int rot, Raw<T> &r) {
   if constexpr (MODE == HALVES_ODD) {
     T *e = reinterpret_cast<T *>(r.v);
@@ -141,8 +140,9 @@ __device__ __forceinline__ void load_row(const T *p, int a, int b, int rot, Raw<
   } else {
 #pragma unroll
     for (int i = 0; i < Raw<T>::H; ++i) {
-      r.v[i] = __ldcs(reinterpret_cast<const uint4 *>(p + a) + i);
-      r.v[Raw<T>::H + i] = __ldcs(reinterpret_cast<const uint4 *>(p + b) + i);
+      const uint4 *x = reinterpret_cast<const uint4 *>(p + a) + i, *y = reinterpret_cast<const uint4 *>(p + b) + i;
+      r.v[i] = ONCE ? __ldcs(x) : *x;
+      r.v[Raw<T>::H + i] = ONCE ? __ldcs(y) : *y;
     }
   }
 }
@@ -237,7 +237,7 @@ struct Lane {
     const T *p = static_cast<const T *>(which ? h.k_weight : h.q_weight);
     if (p) {
       Raw<T> x;
-      load_row<T, MODE>(p, a, b, h.rot, x);
+      load_row<T, MODE, false>(p, a, b, h.rot, x);
       unpack<MODE>(x, w);
     }
 #pragma unroll
@@ -366,93 +366,89 @@ __global__ void __launch_bounds__(NT, kPerSm) rope_kernel(const __grid_constant_
   }
 }
 
-// ---- many tokens: a warp has whole tokens, and a ring with a place for each of a token's groups ----
-// When a group has been read from its place, the same group of the warp's next token is sent for: the
-// way ahead is a whole token and its addresses differ from the ones at hand by one number.  Each
-// lane copies what it reads itself, so nothing is waited for but the copies.
+// ---- many tokens: a warp has one token, all of whose rows are sent for at once ----
+// Each lane copies what it reads itself into shared memory, so nothing is waited for but the copies.
+// Warps that go on to other tokens, sending for a group of the next one as its place becomes free, are
+// slower the more tokens they have (two 122 us, four 126, fourteen 141; one token and no more
+// 124): tokens that are on their way together should lie together.
 template <typename T, int D, int MODE>
-__global__ void __launch_bounds__(NT, kPerSm) rope_ring_kernel(const __grid_constant__ RopeArgs A) {
+__global__ void __launch_bounds__(NT, kPerSm) rope_token_kernel(const __grid_constant__ RopeArgs A) {
   using L = Lane<T, D, MODE>;
   constexpr int V = 2 * Raw<T>::H;  // 16-byte pieces of a lane and group
-  extern __shared__ __align__(16) uint4 ring[];
+  extern __shared__ __align__(16) uint4 places[];
   const kv_qkv_heads &h = A.h;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int groups = A.groups[0] + A.groups[1] + A.groups[2];
-  const int tokens = h.B * h.T, stride = (int)gridDim.x * NW;
-  uint4 *mine = ring + (size_t)warp * groups * V * 32 + lane;  // piece v of group g: mine[(g V + v) 32]
+  uint4 *place = places + (size_t)warp * groups * V * 32 + lane;  // piece v of group g: place[(g V + v) 32]
+  const int token = blockIdx.x * NW + warp;
+  const bool deep = groups >= kDeep;
   L l(h.rot);
   pdl_wait();
   pdl_launch();
-  auto send = [&](uint4 *place, const T *row) {
+  if (token >= h.B * h.T) return;
+  const int bi = token / h.T, t = token - bi * h.T;
+  if (h.seq) {
+    const int n = h.seq[bi];
+    if (n < 0 || n > h.T) {
+      if (lane == 0 && A.status) atomicExch(A.status, (int)KV_ERR_INVALID_ARG);
+      return;
+    }
+    if (t >= n) return;
+  }
+#pragma unroll 1
+  for (int which = 0; which < 3; ++which) {
+    const T *in = input<T>(h, which, bi, t, l.lr);
+    const long step = L::RPW * h.strides[3 * which + 1];
+    const int heads = (which ? h.Hkv : h.Hq) - l.lr;
+#pragma unroll 1
+    for (int g = 0; g < A.groups[which]; ++g, in += step, place += V * 32) {
+      if (g * L::RPW < heads) {
 #pragma unroll
-    for (int v = 0; v < V; ++v)
-      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(place + v * 32)),
-                   "l"(reinterpret_cast<const uint4 *>(row + (v < V / 2 ? l.a : l.b)) + v % (V / 2))
-                   : "memory");
-  };
-  int token = blockIdx.x * NW + warp;
-  if (token >= tokens) return;
-  int bi = token / h.T, t = token - bi * h.T;
-  {
-    uint4 *place = mine;
-#pragma unroll 1
-    for (int which = 0; which < 3; ++which) {
-      const T *in = input<T>(h, which, bi, t, l.lr);
-      const long step = L::RPW * h.strides[3 * which + 1];
-      const int heads = (which ? h.Hkv : h.Hq) - l.lr;
-#pragma unroll 1
-      for (int g = 0; g < A.groups[which]; ++g, in += step, place += V * 32) {
-        if (g * L::RPW < heads) send(place, in);
-        asm volatile("cp.async.commit_group;" ::: "memory");
+        for (int v = 0; v < V; ++v)
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(place + v * 32)),
+                       "l"(reinterpret_cast<const uint4 *>(in + (v < V / 2 ? l.a : l.b)) + v % (V / 2))
+                       : "memory");
       }
+      asm volatile("cp.async.commit_group;" ::: "memory");
     }
   }
+  place -= groups * V * 32;
+  const int pos = h.pos ? h.pos[token] : t;
   l.frequencies(h);
   const bool norm = h.flags & KV_ROPE_NORM;
+  float2 c[PAIRS / 2], s[PAIRS / 2];
+  l.angles(h, pos, c, s);
 #pragma unroll 1
-  while (token < tokens) {
-    const int next = token + stride, nbi = next / h.T, nt = next - nbi * h.T;
-    const bool more = next < tokens;
-    float2 c[PAIRS / 2], s[PAIRS / 2];
-    l.angles(h, h.pos ? h.pos[token] : t, c, s);
-    uint4 *place = mine;
+  for (int which = 0; which < 3; ++which) {
+    const int heads = (which ? h.Hkv : h.Hq) - l.lr, cap = which ? h.cap : h.T;
+    const long step_out = L::RPW * h.strides[10 + 3 * which], token_out = h.strides[11 + 3 * which];
+    T *out = output<T>(h, which, bi, l.lr);
+    const int32_t *slot = which && h.slot ? h.slot + bi * h.Hkv + l.lr : nullptr;
+    if (!slot) out += t * token_out;
+    Pairs w;
+    if (which < 2 && norm && A.groups[which]) l.weights(h, which, w);
 #pragma unroll 1
-    for (int which = 0; which < 3; ++which) {
-      const int heads = (which ? h.Hkv : h.Hq) - l.lr, cap = which ? h.cap : h.T;
-      const T *in = input<T>(h, which, more ? nbi : bi, more ? nt : t, l.lr);  // of the next token
-      const long step_in = L::RPW * h.strides[3 * which + 1], step_out = L::RPW * h.strides[10 + 3 * which];
-      const long token_out = h.strides[11 + 3 * which];
-      T *out = output<T>(h, which, bi, l.lr);
-      const int32_t *slot = which && h.slot ? h.slot + bi * h.Hkv + l.lr : nullptr;
-      if (!slot) out += t * token_out;
-      Pairs w;
-      if (which < 2 && norm) l.weights(h, which, w);
-#pragma unroll 1
-      for (int g = 0; g < A.groups[which]; ++g) {
-        const bool there = g * L::RPW < heads;
-        int row = t;
-        if (slot && there) row += slot[g * L::RPW];
-        asm volatile("cp.async.wait_group %0;" ::"n"(kRingGroups - 1) : "memory");
-        Raw<T> raw;
+    for (int g = 0; g < A.groups[which]; ++g) {
+      const bool there = g * L::RPW < heads;
+      int row = t;
+      if (slot && there) row += slot[g * L::RPW];
+      // the commits behind the last group keep the count: at most kDeep - 1 groups are left behind this one
+      if (deep) asm volatile("cp.async.wait_group %0;" ::"n"(kDeep - 1) : "memory");
+      else asm volatile("cp.async.wait_group 0;" ::: "memory");
+      asm volatile("cp.async.commit_group;" ::: "memory");
+      Raw<T> raw;
 #pragma unroll
-        for (int v = 0; v < V; ++v) raw.v[v] = place[v * 32];
-        if (more && there) send(place, in);
-        asm volatile("cp.async.commit_group;" ::: "memory");
-        if (which < 2) l.turn(raw, norm, h.eps, w, c, s);
-        if (there) {
-          if (row >= 0 && row < cap)
-            store_row<T, MODE>(slot ? out + row * token_out : out, l.a, l.b, h.rot, raw);
-          else if (l.li == 0 && A.status)
-            atomicExch(A.status, (int)KV_ERR_INVALID_ARG);
-        }
-        place += V * 32;
-        in += step_in;
-        out += step_out;
+      for (int v = 0; v < V; ++v) raw.v[v] = place[v * 32];
+      if (which < 2) l.turn(raw, norm, h.eps, w, c, s);
+      if (there) {
+        if (row >= 0 && row < cap)
+          store_row<T, MODE>(slot ? out + row * token_out : out, l.a, l.b, h.rot, raw);
+        else if (l.li == 0 && A.status)
+          atomicExch(A.status, (int)KV_ERR_INVALID_ARG);
       }
+      place += V * 32;
+      out += step_out;
     }
-    token = next;
-    bi = nbi;
-    t = nt;
   }
 }
 
@@ -467,11 +463,12 @@ int run(RopeArgs A, cudaStream_t st) {
   const long warps = (long)kPerSm * NW * kNumSmsHint;  // that run at once
   cudaError_t e;
   if constexpr (MODE != HALVES_ODD) {
-    // Two tokens a warp at least, whose ring holds kRingGroups groups or more and 12 KB or less (four CTAs an SM).
-    const size_t ring = (size_t)groups * RPW * D * sizeof(T);
-    if (!A.h.seq && tokens >= 2 * warps && groups >= kRingGroups && ring <= 12 * 1024) {
-      if (ensure_smem((const void *)rope_ring_kernel<T, D, MODE>, NW * ring)) return KV_ERR_CUDA;
-      e = launch_pdl(rope_ring_kernel<T, D, MODE>, (unsigned)(kPerSm * kNumSmsHint), NT, NW * ring, st, A);
+    // As many tokens as warps run at once, with 12 KB each at most (four CTAs an SM); fewer tokens are
+    // shared out over the warps (64 tokens 3.2 us, a warp each 5).
+    const size_t bytes = (size_t)groups * RPW * D * sizeof(T);
+    if (tokens >= warps && bytes <= 12 * 1024) {
+      if (ensure_smem((const void *)rope_token_kernel<T, D, MODE>, NW * bytes)) return KV_ERR_CUDA;
+      e = launch_pdl(rope_token_kernel<T, D, MODE>, (unsigned)((tokens + NW - 1) / NW), NT, NW * bytes, st, A);
       if (e != cudaSuccess) return cuda_failure(e, "norm and rotary positions");
       return launch_status();
     }

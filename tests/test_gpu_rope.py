@@ -191,6 +191,26 @@ def test_many_tokens(kvc, case):
             assert (K[b, h, :lo] == 3).all() and (V[b, h, :lo] == 4).all() and (K[b, h, hi:] == 3).all()
 
 
+def test_many_tokens_of_padded_rows(kvc):
+    B, T, H, d = 3, 4000, 4, 128
+    q, k, v = (rand((B, H, T, d), BF, 70 + i) for i in range(3))
+    f, _ = kvc.kv_rope_freqs(d)
+    want = kvc.kv_qk_norm_rope(q, k, v, f, eps=EPS)
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    for lens, status in (((4000, 0, 1777), 0), ((4001, 3, -1), -1)):
+        outs = [torch.full((B, H, T, d), 5.0, dtype=BF, device="cuda") for _ in range(3)]
+        kvc.kv_qk_norm_rope(q, k, v, f, eps=EPS, seq=torch.tensor(lens, dtype=torch.int32, device="cuda"), q_out=outs[0], k_out=outs[1],
+                            v_out=outs[2], dev_status=st)
+        assert int(st) == status
+        for o, w in zip(outs, want):
+            for b, n in enumerate(lens):
+                n = n if 0 <= n <= T else 0
+                assert torch.equal(o[b, :, :n], w[b, :, :n]) and (o[b, :, n:] == 5).all()
+    # in place
+    kvc.kv_qk_norm_rope(q, k, v, f, eps=EPS, q_out=q, k_out=k, v_out=v)
+    assert all(torch.equal(a, b) for a, b in zip((q, k, v), want))
+
+
 def test_captured(kvc):
     """A decode step's call, replayed with other positions and slots in the same tensors."""
     B, Hq, Hkv, d, cap = 4, 8, 2, 128, 16
