@@ -18,10 +18,10 @@
 // and 2^-63 of itself, the angle by |pos| times that, far below the 2^-32 turns that are cut off;
 // fp32 products would lose it from positions of a few thousand on.
 //
-// Long calls move as much as a copy and as fast: 32768 tokens of 32/8 heads
-// 124 us, 6.5 TB/s (0.96 of a copy's rate; without the arithmetic 122).  Rows loaded in batches of four groups with nothing in flight meanwhile 147 us (4.7 of 10 cycles of an instruction
-// waiting for them), 8 elements a lane and twice the warps 157, heads fixed to a warp that goes
-// through the tokens 171.
+// Long calls move as much as a copy and as fast: 32768 tokens of 32/8 heads 124 us, 6.5 TB/s (0.96 of
+// a copy's rate; without the arithmetic 122).  Rows loaded in batches of four groups with nothing in
+// flight meanwhile 147 us (4.7 of 10 cycles of an instruction waiting for them), 8 elements a lane
+// and twice the warps 157, heads fixed to a warp that goes through the tokens 171.
 #include <cmath>
 
 #include "kvc_internal.cuh"
