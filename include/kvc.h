@@ -640,8 +640,8 @@ KVC_API int kv_evict_q8(const kv_q8_cache *cache, int keep, int recent, int sink
  *              would be outside [0, cap) (that row is not written) or a seq is outside [0, T]
  *              (nothing of that batch row is written); never cleared
  * Keys alone, with flags 0 and differences as positions, moves cached keys to other
- * positions.  Preconditions: every row starts on a 16-byte boundary; d in {64, 128};
- * inv_freq finite.
+ * positions.  Preconditions: every row and both weights start on a 16-byte boundary; d in
+ * {64, 128}; inv_freq finite.
  */
 KVC_API int kv_qk_norm_rope(const kv_qkv_heads *heads, int *dev_status, kv_stream_t stream);
 

@@ -596,7 +596,7 @@ int kv_qk_norm_rope(const kv_qkv_heads *heads, int *dev_status, kv_stream_t stre
     }
   }
   if ((h.rot > 0 && (h.q || h.k) && !h.inv_freq) || ((uintptr_t)h.inv_freq & 7u) || !aligned4(h.pos) || !aligned4(h.slot) ||
-      !aligned4(h.seq) || ((uintptr_t)h.q_weight % eb) || ((uintptr_t)h.k_weight % eb))
+      !aligned4(h.seq) || !aligned16(h.q_weight) || !aligned16(h.k_weight))
     return KV_ERR_INVALID_ARG;
   return launch_qk_norm_rope(h, dev_status, static_cast<cudaStream_t>(stream));
 }

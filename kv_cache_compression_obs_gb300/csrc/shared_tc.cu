@@ -408,7 +408,7 @@ Plan make_plan(long rows, int Hkv, int P) {
 template <int D>
 int run(const PrefixArgs &T, cudaStream_t st) {
   const SharedArgs &A = T.A;
-  const long long sk[3] = {(long long)A.Hkv * A.skp[0], A.skp[0], A.skp[1]}, sv[3] = {(long long)A.Hkv * A.svp[0], A.svp[0], A.svp[1]};
+  const long long sk[3] = {A.skp[0], A.skp[0], A.skp[1]}, sv[3] = {A.svp[0], A.svp[0], A.svp[1]};  // one batch row: never stepped
   CUtensorMap tmK, tmV;
   if (!encode_heads(&tmK, A.Kp, D, A.P, A.Hkv, 1, sk) || !encode_heads(&tmV, A.Vp, D, A.P, A.Hkv, 1, sv)) return KV_ERR_CUDA;
   const long ctas = (long)T.pairs * A.Hkv * T.shares;

@@ -34,7 +34,7 @@ NONE = dict(q=None, k=None, v=None, q_out=None, k_out=None, v_out=None)
     (dict(T=-1), -1), (dict(Hq=0), -1), (dict(Hkv=0), -1), (dict(eps=-1.0), -1), (dict(eps=math.inf), -1), (dict(eps=math.nan), -1),
     (dict(rot_scale=math.nan), -1), (dict(flags=8), -1), (dict(q_out=None), -1), (dict(q=None), -1), (dict(k=P16 + 8), -1),
     (dict(v_out=P16 + 2), -1), (dict(inv_freq=None), -1), (dict(inv_freq=P16 + 4), -1), (dict(pos=P16 + 2), -1),
-    (dict(slot=P16 + 1), -1), (dict(seq=P16 + 1), -1), (dict(q_weight=P16 + 1), -1), (dict(strides=[4096, 256, 60] * 6), -1),
+    (dict(slot=P16 + 1), -1), (dict(seq=P16 + 1), -1), (dict(q_weight=P16 + 8), -1), (dict(k_weight=P16 + 2), -1), (dict(strides=[4096, 256, 60] * 6), -1),
     (dict(strides=[4096, 256, 64] * 3 + [0, 256, 64] * 3), -1), (dict(strides=[-4096, 256, 64] * 6), -1),
     (dict(B=0), 0), (dict(T=0), 0), (NONE, 0), (dict(cap=-1), -1)], ids=str)
 def test_heads_refusals(api, kw, want):
