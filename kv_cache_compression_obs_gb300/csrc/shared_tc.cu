@@ -387,14 +387,6 @@ struct Plan {
 // Sizes alone decide.  A round of `items` on all SMs takes as long as its key tiles (about 1.3 us
 // each) and what a CTA costs besides (3 us); the shares' fp32 sums are written and read again (from L2).
 Plan make_plan(long rows, int Hkv, int P) {
-  // a call asks three times: for the workspace, the shares and the launch
-  struct Last {
-    long rows;
-    int Hkv, P;
-    Plan p;
-  };
-  static thread_local Last last{};
-  if (last.rows == rows && last.Hkv == Hkv && last.P == P) return last.p;
   Plan p{};
   p.turn = rows <= BM;
   p.pairs = p.turn ? 1 : (int)((rows + 2 * BM - 1) / (2 * BM));
@@ -410,7 +402,6 @@ Plan make_plan(long rows, int Hkv, int P) {
       p.shares = (all + tiles - 1) / tiles;  // none is empty
     }
   }
-  last = Last{rows, Hkv, P, p};
   return p;
 }
 
