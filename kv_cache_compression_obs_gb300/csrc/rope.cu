@@ -180,17 +180,20 @@ __device__ __forceinline__ unsigned long long turn_fraction(double x) {
 }
 
 // What a lane knows for good: its place in a row and the frequencies whose cosines it makes.
-template <typename T, int D, int MODE>
+// PART: not all pairs of a row turn.
+template <typename T, int D, int MODE, bool PART>
 struct Lane {
   static constexpr int LPR = D / (2 * RUN), RPW = 32 / LPR;  // lanes per row, rows of a group
   static constexpr int NP = PAIRS / RPW;                     // pairs whose cosines a lane makes
   int li, lr, a, b;  // lane of a row, row of a group, the lane's runs
+  int turning;       // how many of the lane's pairs turn: the first ones
   unsigned long long frac[NP];
 
   __device__ __forceinline__ Lane(int rot) {
     const int lane = threadIdx.x & 31;
     li = lane % LPR;
     lr = lane / LPR;
+    turning = min(PAIRS, max(0, rot / 2 - PAIRS * li));
     if constexpr (MODE == HALVES) {
       const int turning = rot / (2 * RUN);
       a = li < turning ? RUN * li : 2 * RUN * li;
@@ -210,16 +213,15 @@ struct Lane {
       frac[i] = x < h.rot / 2 ? turn_fraction(h.inv_freq[x]) : 0ull;
     }
   }
-  // Cosines and sines of this lane's pairs at a position; 1 and 0 for pairs that do not turn.
+  // Cosines and sines of this lane's pairs at a position; those of pairs that do not turn are not used.
   __device__ __forceinline__ void angles(const kv_qkv_heads &h, int pos, float2 (&c)[PAIRS / 2], float2 (&s)[PAIRS / 2]) const {
     float cc[NP], ss[NP], cs[PAIRS], sn[PAIRS];
 #pragma unroll
     for (int i = 0; i < NP; ++i) {
       const unsigned long long turn = (unsigned long long)(long long)pos * frac[i];
       sincospif((float)(int)(turn >> 32) * 0x1p-31f, &ss[i], &cc[i]);
-      const bool turns = PAIRS * li + lr * NP + i < h.rot / 2;
-      cc[i] = turns ? cc[i] * h.rot_scale : 1.f;
-      ss[i] = turns ? ss[i] * h.rot_scale : 0.f;
+      cc[i] *= h.rot_scale;
+      ss[i] *= h.rot_scale;
     }
 #pragma unroll
     for (int j = 0; j < PAIRS; ++j) {
@@ -246,7 +248,9 @@ struct Lane {
       w.b[j] = p ? make_float2(w.b[j].x + plus, w.b[j].y + plus) : make_float2(1.f, 1.f);
     }
   }
-  // A group's rows normalised and turned.
+  // A group's rows normalised and turned.  The two elements of a pair that does not turn have nothing to do with one
+  // another: each is only scaled, and stays as it was without the norm (a turn by 0 would hand an infinity or a NaN on
+  // to the other and lose the sign of a zero).
   __device__ __forceinline__ void turn(Raw<T> &raw, bool norm, float eps, const Pairs &w, const float2 (&c)[PAIRS / 2],
                                        const float2 (&s)[PAIRS / 2]) const {
     Pairs x;
@@ -272,6 +276,11 @@ struct Lane {
       const float2 cf = __fmul2_rn(c[j], f2), sf = __fmul2_rn(s[j], f2), nf = __fmul2_rn(s[j], n2);
       x.a[j] = __ffma2_rn(r, nf, __fmul2_rn(p, cf));
       x.b[j] = __ffma2_rn(p, sf, __fmul2_rn(r, cf));
+      if constexpr (PART) {
+        const float2 ps = __fmul2_rn(p, f2), rs = __fmul2_rn(r, f2);
+        if (2 * j >= turning) x.a[j].x = ps.x, x.b[j].x = rs.x;
+        if (2 * j + 1 >= turning) x.a[j].y = ps.y, x.b[j].y = rs.y;
+      }
     }
     pack<MODE>(x, raw);
   }
@@ -291,10 +300,10 @@ __device__ __forceinline__ T *output(const kv_qkv_heads &h, int which, int bi, i
 }
 
 // ---- few tokens, or rows that the ring below does not hold: an item is some groups of a token ----
-template <typename T, int D, int MODE>
+template <typename T, int D, int MODE, bool PART>
 __global__ void __launch_bounds__(NT, kPerSm) rope_kernel(const __grid_constant__ RopeArgs A) {
   constexpr int U = 2;  // groups in flight
-  using L = Lane<T, D, MODE>;
+  using L = Lane<T, D, MODE, PART>;
   const kv_qkv_heads &h = A.h;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const long items = (long)h.B * h.T * A.chunks, stride = (long)gridDim.x * NW;
@@ -371,9 +380,9 @@ __global__ void __launch_bounds__(NT, kPerSm) rope_kernel(const __grid_constant_
 // Warps that go on to other tokens, sending for a group of the next one as its place becomes free, are
 // slower the more tokens they have (two 122 us, four 126, fourteen 141; one token and no more
 // 124): tokens that are on their way together should lie together.
-template <typename T, int D, int MODE>
+template <typename T, int D, int MODE, bool PART>
 __global__ void __launch_bounds__(NT, kPerSm) rope_token_kernel(const __grid_constant__ RopeArgs A) {
-  using L = Lane<T, D, MODE>;
+  using L = Lane<T, D, MODE, PART>;
   constexpr int V = 2 * Raw<T>::H;  // 16-byte pieces of a lane and group
   extern __shared__ __align__(16) uint4 places[];
   const kv_qkv_heads &h = A.h;
@@ -452,9 +461,9 @@ __global__ void __launch_bounds__(NT, kPerSm) rope_token_kernel(const __grid_con
   }
 }
 
-template <typename T, int D, int MODE>
+template <typename T, int D, int MODE, bool PART>
 int run(RopeArgs A, cudaStream_t st) {
-  constexpr int RPW = Lane<T, D, MODE>::RPW;
+  constexpr int RPW = Lane<T, D, MODE, PART>::RPW;
   const long tokens = (long)A.h.B * A.h.T;
   A.groups[0] = A.h.q ? (A.h.Hq + RPW - 1) / RPW : 0;
   A.groups[1] = A.h.k ? (A.h.Hkv + RPW - 1) / RPW : 0;
@@ -467,8 +476,8 @@ int run(RopeArgs A, cudaStream_t st) {
     // shared out over the warps (64 tokens 3.2 us, a warp each 5).
     const size_t bytes = (size_t)groups * RPW * D * sizeof(T);
     if (tokens >= warps && bytes <= 12 * 1024) {
-      if (ensure_smem((const void *)rope_token_kernel<T, D, MODE>, NW * bytes)) return KV_ERR_CUDA;
-      e = launch_pdl(rope_token_kernel<T, D, MODE>, (unsigned)((tokens + NW - 1) / NW), NT, NW * bytes, st, A);
+      if (ensure_smem((const void *)rope_token_kernel<T, D, MODE, PART>, NW * bytes)) return KV_ERR_CUDA;
+      e = launch_pdl(rope_token_kernel<T, D, MODE, PART>, (unsigned)((tokens + NW - 1) / NW), NT, NW * bytes, st, A);
       if (e != cudaSuccess) return cuda_failure(e, "norm and rotary positions");
       return launch_status();
     }
@@ -478,15 +487,17 @@ int run(RopeArgs A, cudaStream_t st) {
   A.steps = A.steps < 1 ? 1 : A.steps > groups ? groups : A.steps;
   A.chunks = (groups + A.steps - 1) / A.steps;
   const long ctas = (tokens * A.chunks + NW - 1) / NW, most = 4L * kPerSm * kNumSmsHint;
-  e = launch_pdl(rope_kernel<T, D, MODE>, (unsigned)(ctas < most ? ctas : most), NT, 0, st, A);
+  e = launch_pdl(rope_kernel<T, D, MODE, PART>, (unsigned)(ctas < most ? ctas : most), NT, 0, st, A);
   if (e != cudaSuccess) return cuda_failure(e, "norm and rotary positions");
   return launch_status();
 }
 
 template <typename T, int D>
 int run_mode(const RopeArgs &A, cudaStream_t st) {
-  if (A.h.flags & KV_ROPE_INTERLEAVED) return run<T, D, NEIGHBOURS>(A, st);
-  return A.h.rot % (2 * RUN) == 0 ? run<T, D, HALVES>(A, st) : run<T, D, HALVES_ODD>(A, st);
+  const bool part = A.h.rot < D;
+  if (A.h.flags & KV_ROPE_INTERLEAVED) return part ? run<T, D, NEIGHBOURS, true>(A, st) : run<T, D, NEIGHBOURS, false>(A, st);
+  if (A.h.rot % (2 * RUN)) return run<T, D, HALVES_ODD, true>(A, st);
+  return part ? run<T, D, HALVES, true>(A, st) : run<T, D, HALVES, false>(A, st);
 }
 
 }  // namespace
