@@ -292,7 +292,7 @@ struct RowStream {
 };
 
 // The shares of NW warps (wm, wz [NW][8], so [NW][R][D]) as one: sh [R][D], mz [R].  A share without
-// slots has z = 0 and weighs nothing; a NaN in z is passed on.
+// slots has z = 0, sums of 0 and weighs nothing; a NaN in z or in the sums is passed on.
 template <int D, int NW>
 __device__ __forceinline__ void join_warps(int R, const float *wm, const float *wz, const float *so, float *sh, float2 *mz) {
   for (int i = threadIdx.x; i < R * D; i += 32 * NW) {
@@ -303,12 +303,11 @@ __device__ __forceinline__ void join_warps(int R, const float *wm, const float *
       if (wz[w * 8 + r] != 0.f) M = fmaxf(M, wm[w * 8 + r]);
     float v = 0.f, Z = 0.f;
 #pragma unroll
-    for (int w = 0; w < NW; ++w)
-      if (wz[w * 8 + r] != 0.f) {
-        const float f = M == -INFINITY ? 1.f : tc::ex2(wm[w * 8 + r] - M);
-        v += f * so[w * R * D + i];
-        Z += f * wz[w * 8 + r];
-      }
+    for (int w = 0; w < NW; ++w) {
+      const float z = wz[w * 8 + r], f = z == 0.f ? 0.f : M == -INFINITY ? 1.f : tc::ex2(wm[w * 8 + r] - M);
+      v += f * so[w * R * D + i];
+      Z += f * z;
+    }
     sh[i] = v;
     if (i % D == 0) mz[r] = make_float2(M, Z);
   }

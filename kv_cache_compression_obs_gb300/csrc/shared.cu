@@ -227,8 +227,8 @@ __global__ void __launch_bounds__(NT, kPerSm<T, D>) own_slots_kernel(const __gri
 
 // ---- everything joined: one warp a query row ----
 // Latency counts: the row's length is read before the wait, and the prefix's first sums are on
-// their way beside the statistics that say what they weigh (a share that saw nothing has left none:
-// whatever stands there is not taken).
+// their way beside the statistics that say what they weigh.  Every share has left its sums (zeros where it saw
+// nothing), and all are taken, so that a NaN reaches the output however little its share weighs.
 template <typename T, int D>
 __global__ void __launch_bounds__(NT) shared_join_kernel(const __grid_constant__ SharedArgs A, const __grid_constant__ OwnArgs W) {
   constexpr int E = D / 32, N = 16;  // elements of a lane, sums in flight
@@ -297,7 +297,7 @@ __global__ void __launch_bounds__(NT) shared_join_kernel(const __grid_constant__
     for (int i = 0; i < N; ++i) {
       const float w = __shfl_sync(0xFFFFFFFFu, f, from + i);
 #pragma unroll
-      for (int y = 0; y < E; ++y) v[y] += w != 0.f ? w * x[i][y] : 0.f;
+      for (int y = 0; y < E; ++y) v[y] += w * x[i][y];
     }
   };
   const float f0 = factor(st0), f1 = factor(st1);

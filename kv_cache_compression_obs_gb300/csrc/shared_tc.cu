@@ -361,16 +361,19 @@ __global__ void __launch_bounds__(NT, 1) prefix_tc_kernel(const __grid_constant_
       const bool live = tile0 + row < A.rows;
       const long at = ((long)(turn ? 2 * share + i : share) * A.Hkv + h) * A.rows + tile0 + row;
       if (live) A.stat[at] = make_float2(m, z2.x + z2.y);
-      if (cnt > 0) {
 #pragma unroll
-        for (int q = 0; q < D / 32; ++q) {
-          uint32_t o[32];
+      for (int q = 0; q < D / 32; ++q) {
+        uint32_t o[32];
+        if (cnt > 0) {
           tmem_ld32(to + q * 32, o);
           tc::tmem_ld_wait();
-          if (live) {
+        } else {  // no key tile: sums of 0
 #pragma unroll
-            for (int x = 0; x < 32; x += 8) st_global_32(A.part + at * D + q * 32 + x, o + x);
-          }
+          for (int x = 0; x < 32; ++x) o[x] = 0u;
+        }
+        if (live) {
+#pragma unroll
+          for (int x = 0; x < 32; x += 8) st_global_32(A.part + at * D + q * 32 + x, o + x);
         }
       }
     }
