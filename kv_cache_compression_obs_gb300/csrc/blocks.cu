@@ -98,6 +98,11 @@ __device__ __forceinline__ float products(uint32_t a, uint32_t b, __nv_bfloat16)
          fabsf(__uint_as_float(a & 0xFFFF0000u) * __uint_as_float(b & 0xFFFF0000u));
 }
 __device__ __forceinline__ float products(uint32_t a, uint32_t b, float) { return fabsf(__uint_as_float(a) * __uint_as_float(b)); }
+// whether a pair of elements has a product other than 0
+__device__ __forceinline__ bool meet(uint32_t a, uint32_t b, __nv_bfloat16) {
+  return ((a & 0x7FFFu) != 0 && (b & 0x7FFFu) != 0) || ((a & 0x7FFF0000u) != 0 && (b & 0x7FFF0000u) != 0);
+}
+__device__ __forceinline__ bool meet(uint32_t a, uint32_t b, float) { return (a & 0x7FFFFFFFu) != 0 && (b & 0x7FFFFFFFu) != 0; }
 
 // The passes below run once or twice per launch, so their instructions come from memory: short loops beat
 // unrolled ones (keys held in registers and everything unrolled: 13.8 us for 12.2).
@@ -437,13 +442,17 @@ __global__ void __launch_bounds__(NT, kPerSm<T, D>) blocks_kernel(const __grid_c
     // S over this warp's blocks: the channels' largest over the lanes with the same ones, times |q|, each lane
     // for the query of its column
     float e = 0.f;
+    bool some = false;
 #pragma unroll
     for (int x = 0; x < NCH * 4; ++x) {
 #pragma unroll
       for (int o = 4; o < 32; o <<= 1) big[x] = larger(big[x], __shfl_xor_sync(0xFFFFFFFFu, big[x], o), T());
       const uint4 &q4 = R.q[x / 4];
-      e += products(big[x], x % 4 == 0 ? q4.x : x % 4 == 1 ? q4.y : x % 4 == 2 ? q4.z : q4.w, T());
+      const uint32_t qw = x % 4 == 0 ? q4.x : x % 4 == 1 ? q4.y : x % 4 == 2 ? q4.z : q4.w;
+      e += products(big[x], qw, T());
+      some |= meet(big[x], qw, T());
     }
+    if (some) e = fmaxf(e, 0x1p-100f);  // 0 only where every term is: not where they underflow
     e += __shfl_xor_sync(0xFFFFFFFFu, e, 1);
     e += __shfl_xor_sync(0xFFFFFFFFu, e, 2);
     if (!(e < INFINITY)) e = INFINITY;  // a NaN in q

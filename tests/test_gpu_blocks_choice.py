@@ -1,0 +1,65 @@
+"""Which blocks block-sparse attention chooses where float32 bounds do not tell."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from _long import BF, F32, rand
+
+pytestmark = pytest.mark.gpu
+
+TYPES = pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+
+
+def _blocks(B, H, nb, block, d, dtype):
+    """A cache whose keys are the same within a block, and its view by blocks."""
+    K = torch.zeros(B, H, nb * block, d, dtype=dtype, device="cuda")
+    return K, K.view(B, H, nb, block, d)
+
+
+def _chosen(q, dig, seen, block, n_sel, sink, recent):
+    """As choose, each block's sum in the same order, so that equal blocks have equal bounds here too."""
+    nb = -(-seen // block)
+    if nb <= n_sel:
+        return list(range(nb))
+    q, dig = q.cpu().numpy(), dig[:nb].cpu().numpy()
+    with np.errstate(all="ignore"):
+        u = np.stack([(np.maximum(x, 0) * dig[:, 1] + np.minimum(x, 0) * dig[:, 0]).sum(-1) for x in q])
+    u = np.where(np.isnan(u), np.inf, u).max(0)
+    mid = np.arange(sink, nb - recent)
+    best = mid[np.lexsort((mid, -u[mid]))][:n_sel - sink - recent]
+    return sorted([*range(sink), *best.tolist(), *range(nb - recent, nb)])
+
+
+def _run(kvc, q, K, ln, block, n_sel, sink=1, recent=1, dig=None):
+    V = rand(K.shape, K.dtype, 99)
+    if dig is None:
+        dig = kvc.kv_block_digest(K, block)
+    o, lse, sel = kvc.kv_attn_blocks(q, K, V, ln.cuda(), dig, block, n_sel, sink=sink, recent=recent)
+    B, Hkv = K.shape[:2]
+    G = q.shape[1] // Hkv
+    for b in range(B):
+        for h in range(Hkv):
+            want = _chosen(q[b, h * G:(h + 1) * G, 0].double(), dig[b, h].double(), int(ln[b, h]), block, n_sel, sink, recent)
+            got = sel[b, h, 0].tolist()
+            assert got == want + [-1] * (n_sel - len(want)), f"b {b} h {h}: {[j for j in got if j not in want]} for {[j for j in want if j not in got]}"
+    return o, lse, sel
+
+
+def _full(B, H, n):
+    return torch.full((B, H), n, dtype=torch.int32)
+
+
+@TYPES
+@pytest.mark.parametrize("qs,ks", [(1e-30, 1e-20), (1e-25, 1e-10), (1e-10, 1e-36)])
+def test_bounds_that_underflow(kvc, dtype, qs, ks):
+    d, block, nb = 64, 16, 200
+    K = (rand((1, 2, nb * block, d), F32, 1) * ks).to(dtype)
+    q = (rand((1, 8, 1, d), F32, 2) * qs).to(dtype)
+    assert bool((q != 0).any()) and bool((K != 0).any())
+    _run(kvc, q, K, _full(1, 2, nb * block - 3), block, 21)
+    # and those of one unit alone
+    K[0, 0] = rand((nb * block, d), dtype, 3)
+    q[0, :4] = rand((4, 1, d), dtype, 4)
+    _run(kvc, q, K, _full(1, 2, nb * block), block, 21)
