@@ -12,8 +12,8 @@
 // at each term: by 2^-23 of the sum so far, which never passes S = max_g sum_c |q_gc| max_j |digest_jc|.
 // In four sums of 64 terms each they are off by at most e = 2^-16 S, a factor of two to spare.  With a the m-th largest of them, a block above a + 2e is among the true best m, one
 // below a - 2e is not; when those between (mostly one block, the m-th itself) are more than
-// the places left, they alone are computed again, in pairs of fp32 (error-free products and sums: 47
-// bits; the 64-bit unit is 40 times slower), or in 64 bits where fp32 would over- or underflow.
+// the places left, they alone are computed again, in three parts of fp32 (error-free products and sums, then
+// rounded to 64 bits; the 64-bit unit is 40 times slower), or in 64 bits where fp32 would over- or underflow.
 //
 // One launch, a cluster of CTAs for each (row, KV head, token): the CTAs share out the digests,
 // exchange the bounds through distributed shared memory, find the same m-th
@@ -129,14 +129,15 @@ __device__ __noinline__ double bound64(int G, const float *q, const T *digest, i
   return best;
 }
 
-// The same in pairs of fp32: hi + lo is the sum to about 2^-47 of the terms' size.
+// The same in three parts of fp32: hi + lo is the sum without the error of its own additions (the sum of two floats and
+// what its rounding lost, by Knuth's six operations, twice), `rest` sums up what those lose, some 2^-70 of the terms' size.
 __device__ __forceinline__ void two_sum(float a, float b, float &s, float &e) {
   s = __fadd_rn(a, b);
   const float x = __fsub_rn(s, a);
   e = __fadd_rn(__fsub_rn(a, __fsub_rn(s, x)), __fsub_rn(b, x));
 }
 template <typename T, int D>
-__device__ __noinline__ double bound_pairs(int G, const float *q, const T *digest, int j) {
+__device__ __noinline__ double bound_parts(int G, const float *q, const T *digest, int j) {
   const int lane = threadIdx.x & 31;
   const T *row = digest + (long)j * 2 * D + lane;
   float low[D / 32], top[D / 32];
@@ -148,22 +149,27 @@ __device__ __noinline__ double bound_pairs(int G, const float *q, const T *diges
   double best = -INFINITY;
 #pragma unroll 1
   for (int g = 0; g < G; ++g) {
-    float hi = 0.f, lo = 0.f, e;
+    float hi = 0.f, lo = 0.f, rest = 0.f, e, e2, e3;
 #pragma unroll
     for (int i = 0; i < D / 32; ++i) {
       const float x = q[g * D + lane + 32 * i], y = x >= 0.f ? top[i] : low[i];
       const float p = __fmul_rn(x, y), pe = __fmaf_rn(x, y, -p);
       two_sum(hi, p, hi, e);
-      lo = __fadd_rn(lo, __fadd_rn(e, pe));
+      two_sum(lo, e, lo, e2);
+      two_sum(lo, pe, lo, e3);
+      rest = __fadd_rn(rest, __fadd_rn(e2, e3));
     }
 #pragma unroll 1
     for (int o = 16; o; o >>= 1) {
       const float a = __shfl_xor_sync(0xFFFFFFFFu, hi, o), b = __shfl_xor_sync(0xFFFFFFFFu, lo, o);
+      const float c = __shfl_xor_sync(0xFFFFFFFFu, rest, o);
       // the same sum in both lanes
       two_sum(lane & o ? a : hi, lane & o ? hi : a, hi, e);
-      lo = __fadd_rn(__fadd_rn(lo, b), e);
+      two_sum(lane & o ? b : lo, lane & o ? lo : b, lo, e2);
+      two_sum(lo, e, lo, e3);
+      rest = __fadd_rn(__fadd_rn(rest, c), __fadd_rn(e2, e3));
     }
-    const double s = (double)hi + (double)lo;
+    const double s = (double)hi + ((double)lo + (double)rest);
     best = s > best ? s : best;
   }
   return best;
@@ -291,7 +297,7 @@ __device__ void choose(int G, const Choice &c, const float *q, const T *digest, 
     __syncthreads();
     for (int i = warp; i < all_open; i += NW) {
       const int j = lo + c.list[i];
-      const double x = wide ? bound64<T, D>(G, q, digest, j) : bound_pairs<T, D>(G, q, digest, j);
+      const double x = wide ? bound64<T, D>(G, q, digest, j) : bound_parts<T, D>(G, q, digest, j);
       if (lane == 0) c.exact[i] = x;
     }
     __syncthreads();

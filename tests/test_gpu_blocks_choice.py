@@ -63,3 +63,31 @@ def test_bounds_that_underflow(kvc, dtype, qs, ks):
     K[0, 0] = rand((nb * block, d), dtype, 3)
     q[0, :4] = rand((4, 1, d), dtype, 4)
     _run(kvc, q, K, _full(1, 2, nb * block), block, 21)
+
+
+@TYPES
+def test_last_places_of_64_bits(kvc, dtype):
+    """u = 1 + 2^-25 + i 2^-51, i < 4, exact in 64 bits."""
+    d, block, nb = 64, 16, 300
+    K, by_block = _blocks(1, 1, nb, block, d, dtype)
+    g = torch.Generator().manual_seed(5)
+    i = torch.randint(0, 4, (nb,), generator=g).float().cuda()
+    by_block[..., 0], by_block[..., 1], by_block[..., 2] = 1.0, 2.0 ** -13, (i * 2.0 ** -26).to(dtype)[:, None]
+    q = torch.zeros(1, 2, 1, d, dtype=dtype, device="cuda")
+    q[..., 0], q[..., 1], q[..., 2] = 1.0, 2.0 ** -12, 2.0 ** -25
+    assert 40 < int((i == 3).sum()) < 110
+    for n_sel in (20, 60, 120, 290):
+        _run(kvc, q, K, _full(1, 1, nb * block), block, n_sel)
+
+
+@TYPES
+def test_same_terms_in_other_orders(kvc, dtype):
+    """Blocks whose bounds are sums of the same terms in other channels are equal: the lower ones are chosen."""
+    d, block, nb = 64, 16, 120
+    K, by_block = _blocks(1, 1, nb, block, d, dtype)
+    terms = torch.tensor([2.0 ** -x for x in (0, 3, 13, 19, 25, 31, 38, 44)] + [0.0] * (d - 8), device="cuda")
+    for j in range(nb):
+        by_block[0, 0, j] = terms[torch.randperm(d, generator=torch.Generator().manual_seed(j))].to(dtype)
+    q = torch.ones(1, 4, 1, d, dtype=dtype, device="cuda")
+    sel = _run(kvc, q, K, _full(1, 1, nb * block), block, 30)[2]
+    assert sel[0, 0, 0].tolist() == list(range(29)) + [nb - 1]
