@@ -14,6 +14,9 @@
 // below a - 2e is not; when those between (mostly one block, the m-th itself) are more than
 // the places left, they alone are computed again, in three parts of fp32 (error-free products and sums, then
 // rounded to 64 bits; the 64-bit unit is 40 times slower), or in 64 bits where fp32 would over- or underflow.
+// Equal keys leave every block open, so the cluster's CTAs share out what is more than a few, and ranks come from
+// histograms of the bounds as whole numbers: 12000 equal blocks of 8 heads take 280 us, 66 when they differ (each
+// CTA for itself, all against all: 111 ms).  A block whose digest is no number has the bound +inf and needs none of this.
 //
 // One launch, a cluster of CTAs for each (row, KV head, token): the CTAs share out the digests,
 // exchange the bounds through distributed shared memory, find the same m-th
@@ -35,6 +38,7 @@ namespace {
 constexpr int NW = 4, NT = 32 * NW;
 constexpr int kMaxBlocks = 12288;  // 14 bytes of shared memory each
 constexpr int kBins = 256, kFew = 64;
+constexpr int kAlone = 32;  // near bounds that a CTA computes by itself, without waiting for the others of its cluster
 template <typename T, int D>
 using Rows = RowStream<T, D, (D == 64 && sizeof(T) == 2 ? 4 : 2)>;
 // CTAs an SM holds.
@@ -62,6 +66,10 @@ __device__ __forceinline__ uint32_t order(float x) {  // orders like x; a NaN li
 }
 __device__ __forceinline__ float unorder(uint32_t k) {
   return __uint_as_float(k ^ (k >> 31 ? 0x80000000u : 0xFFFFFFFFu));
+}
+__device__ __forceinline__ unsigned long long order(double x) {  // orders like x; -0 like 0
+  const unsigned long long u = (unsigned long long)__double_as_longlong(x + 0.);
+  return u ^ (u >> 63 ? ~0ull : 1ull << 63);
 }
 __device__ __forceinline__ float max_nan(float a, float b) {
   float r;
@@ -136,54 +144,91 @@ __device__ __forceinline__ void two_sum(float a, float b, float &s, float &e) {
   const float x = __fsub_rn(s, a);
   e = __fadd_rn(__fsub_rn(a, __fsub_rn(s, x)), __fsub_rn(b, x));
 }
+// Four blocks list[i .. i + 3] (below n), eight lanes each: `out` gets their bounds, ordered as whole numbers.
 template <typename T, int D>
-__device__ __noinline__ double bound_parts(int G, const float *q, const T *digest, int j) {
-  const int lane = threadIdx.x & 31;
-  const T *row = digest + (long)j * 2 * D + lane;
-  float low[D / 32], top[D / 32];
+__device__ __noinline__ void bounds_in_parts(int G, const float *q, const T *digest, const uint16_t *list, int i, int n,
+                                             unsigned long long *out) {
+  constexpr int EV = Vec16<T>::N, E = D / 8;  // elements of a 16-byte piece, of a lane
+  const int l = threadIdx.x & 7, at = i + ((threadIdx.x & 31) >> 3);
+  const uint4 *row = reinterpret_cast<const uint4 *>(digest + (long)list[min(at, n - 1)] * 2 * D) + l;
+  float low[E], top[E];
+  int nan = 0;
 #pragma unroll
-  for (int i = 0; i < D / 32; ++i) {
-    low[i] = to_f32(row[32 * i]);
-    top[i] = to_f32(row[D + 32 * i]);
+  for (int v = 0; v < E / EV; ++v) {
+    Vec16<T>::unpack(row[8 * v], low + v * EV);
+    Vec16<T>::unpack(row[D / EV + 8 * v], top + v * EV);
   }
-  double best = -INFINITY;
+#pragma unroll
+  for (int e = 0; e < E; ++e) nan |= low[e] != low[e] || top[e] != top[e];
+  for (int o = 4; o; o >>= 1) nan |= __shfl_xor_sync(0xFFFFFFFFu, nan, o);
+  double best = nan ? INFINITY : -INFINITY;
 #pragma unroll 1
   for (int g = 0; g < G; ++g) {
-    float hi = 0.f, lo = 0.f, rest = 0.f, e, e2, e3;
+    float hi = 0.f, lo = 0.f, rest = 0.f, x1, x2, x3;
 #pragma unroll
-    for (int i = 0; i < D / 32; ++i) {
-      const float x = q[g * D + lane + 32 * i], y = x >= 0.f ? top[i] : low[i];
-      const float p = __fmul_rn(x, y), pe = __fmaf_rn(x, y, -p);
-      two_sum(hi, p, hi, e);
-      two_sum(lo, e, lo, e2);
-      two_sum(lo, pe, lo, e3);
-      rest = __fadd_rn(rest, __fadd_rn(e2, e3));
+    for (int e = 0; e < E; ++e) {
+      const float x = q[g * D + (l + e / EV * 8) * EV + e % EV], y = x >= 0.f ? top[e] : low[e];
+      const float p = __fmul_rn(x, y), px = __fmaf_rn(x, y, -p);
+      two_sum(hi, p, hi, x1);
+      two_sum(lo, x1, lo, x2);
+      two_sum(lo, px, lo, x3);
+      rest = __fadd_rn(rest, __fadd_rn(x2, x3));
     }
 #pragma unroll 1
-    for (int o = 16; o; o >>= 1) {
+    for (int o = 4; o; o >>= 1) {
       const float a = __shfl_xor_sync(0xFFFFFFFFu, hi, o), b = __shfl_xor_sync(0xFFFFFFFFu, lo, o);
       const float c = __shfl_xor_sync(0xFFFFFFFFu, rest, o);
-      // the same sum in both lanes
-      two_sum(lane & o ? a : hi, lane & o ? hi : a, hi, e);
-      two_sum(lane & o ? b : lo, lane & o ? lo : b, lo, e2);
-      two_sum(lo, e, lo, e3);
-      rest = __fadd_rn(__fadd_rn(rest, c), __fadd_rn(e2, e3));
+      const bool upper = threadIdx.x & o;  // the same sum in both lanes
+      two_sum(upper ? a : hi, upper ? hi : a, hi, x1);
+      two_sum(upper ? b : lo, upper ? lo : b, lo, x2);
+      two_sum(lo, x1, lo, x3);
+      rest = __fadd_rn(__fadd_rn(rest, c), __fadd_rn(x2, x3));
     }
     const double s = (double)hi + ((double)lo + (double)rest);
     best = s > best ? s : best;
   }
-  return best;
+  if (l == 0 && at < n) out[at] = order(best);
 }
 
 // Shared memory of the choice.
 struct Choice {
-  uint32_t *key;   // [blocks] bounds' bits
-  double *exact;   // [blocks] of the undecided blocks
-  uint16_t *list;  // [blocks] undecided blocks; then the chosen ones, ascending
-  int *hist;       // [kBins]
-  uint32_t *few;   // [kFew]
+  uint32_t *key;              // [blocks] bounds' bits
+  unsigned long long *exact;  // [blocks] bounds in 64 bits of the undecided blocks, ordered as whole numbers
+  uint16_t *list;             // [blocks] undecided blocks, ascending; then the chosen ones
+  int *hist;                  // [kBins]
+  uint32_t *few;              // [kFew]
+  unsigned long long (*ends)[NW];
 };
 constexpr uint32_t kIn = 0xFFFFFFFFu;  // no bound's bits
+
+// In which of the histogram's bins the m-th largest is, how many it holds, and how many are above it.  `count` becomes 0.
+__device__ __forceinline__ int bin_of(const Choice &c, int m, int (*red)[NW], uint32_t (*redu)[NW], int &count, uint32_t &bin,
+                                      int &held) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // keys in this thread's two bins and in all above
+  const int b = kBins - 2 - 2 * (int)threadIdx.x, h1 = c.hist[b + 1], h0 = c.hist[b];
+  int incl = h0 + h1;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+    if (lane >= o) incl += y;
+  }
+  if (lane == 31) red[0][warp] = incl;
+  __syncthreads();
+  for (int w = 0; w < warp; ++w) incl += red[0][w];
+  const int above = incl - h0 - h1;
+  if (above < m && m <= incl) {  // one thread
+    const bool upper = m <= above + h1;
+    redu[0][0] = b + upper;
+    redu[0][1] = upper ? above : above + h1;
+    redu[0][2] = upper ? h1 : h0;
+    count = 0;
+  }
+  __syncthreads();
+  bin = redu[0][0];
+  held = (int)redu[0][2];
+  return (int)redu[0][1];
+}
 
 // The m-th largest of the n keys, whose least and largest this thread's `least`, `most` are a part of.
 __device__ uint32_t mth_largest(const Choice &c, int n, int m, uint32_t least, uint32_t most, int (*red)[NW],
@@ -210,29 +255,9 @@ __device__ uint32_t mth_largest(const Choice &c, int n, int m, uint32_t least, u
       if (k <= range) atomicAdd(c.hist + (k >> s), 1);
     }
     __syncthreads();
-    // keys in this thread's two bins and in all above
-    const int b = kBins - 2 - 2 * (int)threadIdx.x, h1 = c.hist[b + 1], h0 = c.hist[b];
-    int incl = h0 + h1;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(0xFFFFFFFFu, incl, o);
-      if (lane >= o) incl += y;
-    }
-    if (lane == 31) red[0][warp] = incl;
-    __syncthreads();
-    for (int w = 0; w < warp; ++w) incl += red[0][w];
-    const int above = incl - h0 - h1;
-    if (above < m && m <= incl) {  // one thread
-      const bool upper = m <= above + h1;
-      redu[0][0] = b + upper;
-      redu[0][1] = upper ? above : above + h1;
-      redu[0][2] = upper ? h1 : h0;
-      count = 0;
-    }
-    __syncthreads();
-    const uint32_t bin = redu[0][0];
-    const int held = (int)redu[0][2];
-    m -= (int)redu[0][1];
+    uint32_t bin;
+    int held;
+    m -= bin_of(c, m, red, redu, count, bin, held);
     least += bin << s;
     most = min(most, least + (uint32_t)((1ull << s) - 1));
     if (most == least) return least;
@@ -258,11 +283,69 @@ __device__ uint32_t mth_largest(const Choice &c, int n, int m, uint32_t least, u
   }
 }
 
+// Marks the m largest of c.exact[0, n), of equal ones the first, in c.key.  A histogram over the range that is left cuts
+// eight bits off it, so that any number of them, equal or not, takes a few passes.
+__device__ __noinline__ void mark_best(const Choice &c, int n, int m, int (*red)[NW], uint32_t (*redu)[NW], int &count) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  unsigned long long least = ~0ull, most = 0ull;
+  for (int i = threadIdx.x; i < n; i += NT) {
+    least = min(least, c.exact[i]);
+    most = max(most, c.exact[i]);
+  }
+#pragma unroll 1
+  for (int o = 16; o; o >>= 1) {
+    least = min(least, __shfl_xor_sync(0xFFFFFFFFu, least, o));
+    most = max(most, __shfl_xor_sync(0xFFFFFFFFu, most, o));
+  }
+  if (lane == 0) {
+    c.ends[0][warp] = least;
+    c.ends[1][warp] = most;
+  }
+  __syncthreads();
+  for (int w = 0; w < NW; ++w) {
+    least = min(least, c.ends[0][w]);
+    most = max(most, c.ends[1][w]);
+  }
+  while (least < most) {
+    const unsigned long long range = most - least;
+    const int s = max(0, 56 - __clzll(range));  // range >> s is below kBins
+    for (int i = threadIdx.x; i < kBins; i += NT) c.hist[i] = 0;
+    __syncthreads();
+    for (int i = threadIdx.x; i < n; i += NT) {
+      const unsigned long long k = c.exact[i] - least;
+      if (k <= range) atomicAdd(c.hist + (int)(k >> s), 1);
+    }
+    __syncthreads();
+    uint32_t bin;
+    int held;
+    m -= bin_of(c, m, red, redu, count, bin, held);
+    least += (unsigned long long)bin << s;
+    most = min(most, least + ((1ull << s) - 1));
+  }
+  // all above `least`, and the first m of those that are equal to it
+  const int stretch = (n + NT - 1) / NT * 32, i0 = min(n, warp * stretch), i1 = min(n, i0 + stretch);
+  int equal = 0;
+  for (int i = i0 + lane; i < i0 + stretch; i += 32) equal += __popc(__ballot_sync(0xFFFFFFFFu, i < i1 && c.exact[i] == least));
+  __syncthreads();  // `red` has been read
+  if (lane == 0) red[0][warp] = equal;
+  __syncthreads();
+  int at = 0;
+  for (int w = 0; w < warp; ++w) at += red[0][w];
+  for (int i = i0 + lane; i < i0 + stretch; i += 32) {
+    const unsigned long long k = i < i1 ? c.exact[i] : 0ull;
+    const bool same = i < i1 && k == least;
+    const unsigned who = __ballot_sync(0xFFFFFFFFu, same);
+    if (i < i1 && (k > least || (same && at + __popc(who & ((1u << lane) - 1)) < m))) c.key[c.list[i]] = kIn;
+    at += __popc(who);
+  }
+}
+
 // The best `m` of the n candidates (block lo + i; their bounds' bits in c.key) to c.list, ascending, as blocks.
 // err: how far a bound may be off; wide: only 64 bits tell them apart.
 template <typename T, int D>
 __device__ void choose(int G, const Choice &c, const float *q, const T *digest, int lo, int n, int m, float err,
-                       bool wide, uint32_t least, uint32_t most, int (*red)[NW], uint32_t (*redu)[NW], int &count) {
+                       bool wide, uint32_t least, uint32_t most, int (*red)[NW], uint32_t (*redu)[NW], int &count,
+                       const cooperative_groups::cluster_group &cl) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const float a = unorder(mth_largest(c, n, m, least, most, red, redu, count));
   const float above = a + 2.f * err, below = a - 2.f * err;
@@ -278,35 +361,59 @@ __device__ void choose(int G, const Choice &c, const float *q, const T *digest, 
     red[0][warp] = sure;
     red[1][warp] = open;
   }
-  if (threadIdx.x == 0) count = 0;
   __syncthreads();
-  int at = 0, all_sure = 0, all_open = 0;
+  int at = 0, all_sure = 0, all_open = 0, sure_before = 0;
 #pragma unroll
   for (int w = 0; w < NW; ++w) {
-    if (w < warp) at += red[0][w] + red[1][w];
+    if (w < warp) at += red[0][w] + red[1][w], sure_before += red[0][w];
     all_sure += red[0][w];
     all_open += red[1][w];
   }
   const int places = m - all_sure;
   const bool again = all_open > places;
   if (again) {
-    for (int i = i0 + lane; i < i1; i += 32) {
-      const float x = unorder(c.key[i]);
-      if (!(x > above) && !(x < below)) c.list[atomicAdd(&count, 1)] = (uint16_t)i;
+    int to = 0;
+    for (int w = 0; w < warp; ++w) to += red[1][w];
+    for (int i = i0 + lane; i < i0 + stretch; i += 32) {
+      const float x = i < i1 ? unorder(c.key[i]) : -INFINITY;
+      const bool between = i < i1 && !(x > above) && !(x < below);
+      const unsigned who = __ballot_sync(0xFFFFFFFFu, between);
+      if (between) c.list[to + __popc(who & ((1u << lane) - 1))] = (uint16_t)i;
+      to += __popc(who);
     }
     __syncthreads();
-    for (int i = warp; i < all_open; i += NW) {
-      const int j = lo + c.list[i];
-      const double x = wide ? bound64<T, D>(G, q, digest, j) : bound_parts<T, D>(G, q, digest, j);
-      if (lane == 0) c.exact[i] = x;
+    // where there are many the cluster's CTAs, which all have the same list, have a share of them each
+    const int CL = (int)cl.num_blocks(), rank = (int)cl.block_rank();
+    const bool spread = CL > 1 && all_open > kAlone;
+    const int each = spread ? (all_open + CL - 1) / CL : all_open, e0 = spread ? min(all_open, rank * each) : 0;
+    const int e1 = min(all_open, e0 + each);
+    if (wide) {
+      for (int i = e0 + warp; i < e1; i += NW) {
+        const double x = bound64<T, D>(G, q, digest, lo + c.list[i]);
+        if (lane == 0) c.exact[i] = order(x);
+      }
+    } else {
+      for (int i = e0 + 4 * warp; i < e1; i += 4 * NW)
+        bounds_in_parts<T, D>(G, q, digest + (long)lo * 2 * D, c.list, i, e1, c.exact);
     }
-    __syncthreads();
-    for (int i = threadIdx.x; i < all_open; i += NT) {
-      const double x = c.exact[i];
-      const int j = c.list[i];
+    if (spread) {
+      cl.sync();
+      for (int i = threadIdx.x; i < all_open; i += NT) {
+        const int r = i / each;
+        if (r != rank) c.exact[i] = cl.map_shared_rank(c.exact, r)[i];
+      }
+      cl.sync();  // the rings take the place of what has been read
+    } else {
+      __syncthreads();
+    }
+    if (all_open > kFew) {
+      mark_best(c, all_open, places, red, redu, count);
+    } else if ((int)threadIdx.x < all_open) {
+      const int i = threadIdx.x;
+      const unsigned long long x = c.exact[i];
       int better = 0;
-      for (int k = 0; k < all_open; ++k) better += c.exact[k] > x || (c.exact[k] == x && c.list[k] < j);
-      if (better < places) c.key[j] = kIn;
+      for (int k = 0; k < all_open; ++k) better += c.exact[k] > x || (c.exact[k] == x && k < i);
+      if (better < places) c.key[c.list[i]] = kIn;
     }
     __syncthreads();
     // how many of those each warp's stretch has now
@@ -314,8 +421,8 @@ __device__ void choose(int G, const Choice &c, const float *q, const T *digest, 
     for (int i = i0 + lane; i < i0 + stretch; i += 32) in += __popc(__ballot_sync(0xFFFFFFFFu, i < i1 && c.key[i] == kIn));
     if (lane == 0) red[1][warp] = in;
     __syncthreads();
-    at = 0;
-    for (int w = 0; w < warp; ++w) at += red[0][w] + red[1][w];
+    at = sure_before;
+    for (int w = 0; w < warp; ++w) at += red[1][w];
   }
   for (int i = i0 + lane; i < i0 + stretch; i += 32) {
     const uint32_t k = i < i1 ? c.key[i] : 0u;
@@ -336,6 +443,7 @@ __global__ void __launch_bounds__(NT, kPerSm<T, D>) blocks_kernel(const __grid_c
   __shared__ float err_part[NW], err_cta;
   __shared__ int red[2][NW], counter, hist[kBins];
   __shared__ uint32_t redu[2][NW], few[kFew];
+  __shared__ unsigned long long ends[2][NW];
   constexpr int NCH = Rows<T, D>::NCH;
   const int G = A.G;
   float *sh = reinterpret_cast<float *>(dyn);              // [G][D] this CTA's share
@@ -382,7 +490,8 @@ __global__ void __launch_bounds__(NT, kPerSm<T, D>) blocks_kernel(const __grid_c
   Choice c;
   c.hist = hist;
   c.few = few;
-  c.exact = reinterpret_cast<double *>(area);
+  c.exact = reinterpret_cast<unsigned long long *>(area);
+  c.ends = ends;
   c.key = reinterpret_cast<uint32_t *>(c.exact + A.nb);
   c.list = reinterpret_cast<uint16_t *>(mine + ((A.nb / CL + 20) & ~3));
   if (cap_c > 0) {
@@ -468,7 +577,6 @@ __global__ void __launch_bounds__(NT, kPerSm<T, D>) blocks_kernel(const __grid_c
     if (threadIdx.x == 0) err_cta = fmaxf(fmaxf(err_part[0], err_part[1]), fmaxf(err_part[2], err_part[3]));
     cl.sync();
     float size = 0.f;  // of the terms of a bound
-    bool wide = false;
     for (int r = 0; r < CL; ++r) size = fmaxf(size, *cl.map_shared_rank(&err_cta, r));
     uint32_t least = 0xFFFFFFFFu, most = 0u;
     // a stretch of four (of a CTA's bounds, whose number is a multiple of 16) at a time
@@ -479,17 +587,18 @@ __global__ void __launch_bounds__(NT, kPerSm<T, D>) blocks_kernel(const __grid_c
 #pragma unroll
       for (int k = 0; k < 4; ++k)
         if (i + k < nm) {
-          wide |= !(fabsf(x[k]) < INFINITY);
           const uint32_t y = order(x[k]);
           c.key[i + k] = y;
           least = min(least, y);
           most = max(most, y);
         }
     }
-    // a bound that is no number, or terms that fp32 does not hold: 64 bits decide for all of them
-    wide = __syncthreads_or(wide || !(size < 0x1p120f) || (size > 0.f && size < 0x1p-60f));
+    // terms that fp32 does not hold: 64 bits decide for all of them.  (Otherwise a bound that is no number comes from a
+    // digest that is none, and is +inf.)
+    const bool wide = !(size < 0x1p120f) || (size > 0.f && size < 0x1p-60f);
     c.list += A.sink;  // behind the first blocks
-    choose<T, D>(G, c, sh, digest, lo, nm, m, wide ? INFINITY : size * 0x1p-16f, wide, least, most, red, redu, counter);
+    choose<T, D>(G, c, sh, digest, lo, nm, m, wide ? INFINITY : size * 0x1p-16f, wide, least, most, red, redu, counter,
+                 cl);
     c.list -= A.sink;
   }
   for (int i = threadIdx.x; i < ns; i += NT)  // those that no bound decides

@@ -91,3 +91,75 @@ def test_same_terms_in_other_orders(kvc, dtype):
     q = torch.ones(1, 4, 1, d, dtype=dtype, device="cuda")
     sel = _run(kvc, q, K, _full(1, 1, nb * block), block, 30)[2]
     assert sel[0, 0, 0].tolist() == list(range(29)) + [nb - 1]
+
+
+@TYPES
+@pytest.mark.parametrize("nb", [700, 9000])
+def test_many_equal_bounds(kvc, dtype, nb):
+    d, block = 64, 16
+    K, by_block = _blocks(2, 2, nb, block, d, dtype)
+    by_block[0, 0] = rand((d,), dtype, 10)                       # one kind
+    few = rand((5, d), F32, 11)
+    by_block[0, 1] = few[torch.arange(nb, device="cuda") * 7 % 5].to(dtype)[:, None]   # five kinds in turn
+    K[1, 0] = 0                                                  # nothing
+    by_block[1, 1] = rand((d,), dtype, 12)
+    by_block[1, 1, 3::11, :, 5] += 2.0                           # one kind and some above
+    q = rand((2, 8, 1, d), dtype, 13)
+    for n_sel in (3, 40, 300, nb - 5):
+        _run(kvc, q, K, torch.tensor([[nb * block, nb * block - 17], [nb * block - 1, nb * block]], dtype=torch.int32), block, n_sel)
+
+
+@TYPES
+@pytest.mark.parametrize("bad", [math.nan, math.inf, -math.inf])
+def test_bad_keys_in_many_blocks(kvc, dtype, bad):
+    """Blocks whose bound is no number are the first chosen, by number, and the others are told apart as ever."""
+    d, block, nb = 64, 16, 3000
+    K = rand((1, 3, nb * block, d), dtype, 20)
+    K[0, 0, 777 * block + 3, 9] = bad
+    K[0, 1, 5 * block::37 * block, 1] = bad
+    K[0, 2, ::block, 2] = bad
+    q = rand((1, 12, 1, d), dtype, 21)
+    q[..., 9], q[..., 1] = q[..., 9].abs() + 0.1, -q[..., 1].abs() - 0.1
+    for n_sel in (5, 40, 100, 2000):
+        _run(kvc, q, K, _full(1, 3, nb * block), block, n_sel)
+
+
+@TYPES
+def test_bad_queries(kvc, dtype):
+    d, block, nb = 64, 16, 500
+    K, q = rand((1, 2, nb * block, d), dtype, 30), rand((1, 8, 1, d), dtype, 31)
+    q[0, 2, 0, 5], q[0, 5, 0, 6] = math.nan, math.inf
+    _run(kvc, q, K, _full(1, 2, nb * block), block, 30)
+
+
+@TYPES
+def test_time_of_equal_bounds(kvc, dtype):
+    """Equal bounds, and a key that is no number, cost some times an ordinary call, not hundreds of times: near
+    bounds are shared out and ranked in linear time."""
+    d, block, nb, H = 128, 16, 12000, 8
+    q = rand((1, 4 * H, 1, d), dtype, 50)
+    K = rand((1, H, nb * block, d), dtype, 51)
+    ln = _full(1, H, nb * block).cuda()
+
+    def us(K):
+        dig = kvc.kv_block_digest(K, block)
+        call = lambda: kvc.kv_attn_blocks(q, K, K, ln, dig, block, 64, sink=1, recent=1)  # noqa: E731
+        call()
+        best = math.inf
+        for _ in range(5):
+            a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+            a.record()
+            for _ in range(4):
+                call()
+            b.record()
+            b.synchronize()
+            best = min(best, a.elapsed_time(b) * 250)
+        return best
+
+    plain = us(K)
+    K[0, 3, 12345, 7] = math.nan
+    one_nan = us(K)
+    K[:] = rand((1, H, 1, d), dtype, 52)
+    equal = us(K)
+    print(f"ordinary {plain:.1f} us, one NaN {one_nan:.1f}, equal keys {equal:.1f}")
+    assert one_nan < 3 * plain and equal < 20 * plain
