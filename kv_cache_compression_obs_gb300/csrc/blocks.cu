@@ -387,7 +387,9 @@ __device__ void choose(int G, const Choice &c, const float *q, const T *digest, 
     const bool spread = CL > 1 && all_open > kAlone;
     const int each = spread ? (all_open + CL - 1) / CL : all_open, e0 = spread ? min(all_open, rank * each) : 0;
     const int e1 = min(all_open, e0 + each);
-    if (wide) {
+    if (err == 0.f) {  // every term is 0: the bounds are exact
+      for (int i = e0 + threadIdx.x; i < e1; i += NT) c.exact[i] = order((double)unorder(c.key[c.list[i]]));
+    } else if (wide) {
       for (int i = e0 + warp; i < e1; i += NW) {
         const double x = bound64<T, D>(G, q, digest, lo + c.list[i]);
         if (lane == 0) c.exact[i] = order(x);

@@ -133,6 +133,17 @@ def test_bad_queries(kvc, dtype):
 
 
 @TYPES
+def test_no_terms_at_all(kvc, dtype):
+    """Keys of 0, among them some that are no numbers."""
+    d, block, nb = 64, 16, 900
+    K = torch.zeros(1, 2, nb * block, d, dtype=dtype, device="cuda")
+    K[0, 1, 50 * block::30 * block, 3] = math.nan
+    q = rand((1, 8, 1, d), dtype, 35)
+    for n_sel in (10, 60):
+        _run(kvc, q, K, _full(1, 2, nb * block), block, n_sel)
+
+
+@TYPES
 def test_time_of_equal_bounds(kvc, dtype):
     """Equal bounds, and a key that is no number, cost some times an ordinary call, not hundreds of times: near
     bounds are shared out and ranked in linear time."""
