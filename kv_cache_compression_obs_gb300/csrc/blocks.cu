@@ -16,7 +16,7 @@
 // rounded to 64 bits; the 64-bit unit is 40 times slower), or in 64 bits where fp32 would over- or underflow.
 // Equal keys leave every block open, so the cluster's CTAs share out what is more than a few, and ranks come from
 // histograms of the bounds as whole numbers: 12000 equal blocks of 8 heads take 280 us, 66 when they differ (each
-// CTA for itself, all against all: 111 ms).  A block whose digest is no number has the bound +inf and needs none of this.
+// CTA for itself, all against all: 111 ms).  A block whose digest is no number or infinite has the bound +inf and needs none of this.
 //
 // One launch, a cluster of CTAs for each (row, KV head, token): the CTAs share out the digests,
 // exchange the bounds through distributed shared memory, find the same m-th
@@ -159,7 +159,7 @@ __device__ __noinline__ void bounds_in_parts(int G, const float *q, const T *dig
     Vec16<T>::unpack(row[D / EV + 8 * v], top + v * EV);
   }
 #pragma unroll
-  for (int e = 0; e < E; ++e) nan |= low[e] != low[e] || top[e] != top[e];
+  for (int e = 0; e < E; ++e) nan |= !(fabsf(low[e]) < INFINITY) || !(fabsf(top[e]) < INFINITY);
   for (int o = 4; o; o >>= 1) nan |= __shfl_xor_sync(0xFFFFFFFFu, nan, o);
   double best = nan ? INFINITY : -INFINITY;
 #pragma unroll 1
@@ -188,6 +188,24 @@ __device__ __noinline__ void bounds_in_parts(int G, const float *q, const T *dig
     best = s > best ? s : best;
   }
   if (l == 0 && at < n) out[at] = order(best);
+}
+
+// The part of S that the CTA's blocks [i0, i1) of `digest` have without their infinities, in every thread's `part` [NW][8]
+// by query; the caller adds them up.
+template <typename T, int D>
+__device__ __noinline__ void finite_size(int G, const float *q, const T *digest, int i0, int i1, float *part) {
+  const int c = threadIdx.x % D, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  float big = 0.f;
+  for (int i = i0 + (int)threadIdx.x / D; i < i1; i += NT / D) {
+    const float low = fabsf(to_f32(digest[(long)i * 2 * D + c])), top = fabsf(to_f32(digest[(long)i * 2 * D + D + c]));
+    if (low < INFINITY) big = fmaxf(big, low);
+    if (top < INFINITY) big = fmaxf(big, top);
+  }
+  for (int g = 0; g < G; ++g) {
+    float e = fabsf(q[g * D + c]) * big;
+    for (int o = 16; o; o >>= 1) e += __shfl_xor_sync(0xFFFFFFFFu, e, o);
+    if (lane == 0) part[warp * 8 + g] = e;
+  }
 }
 
 // Shared memory of the choice.
@@ -580,6 +598,21 @@ __global__ void __launch_bounds__(NT, kPerSm<T, D>) blocks_kernel(const __grid_c
     cl.sync();
     float size = 0.f;  // of the terms of a bound
     for (int r = 0; r < CL; ++r) size = fmaxf(size, *cl.map_shared_rank(&err_cta, r));
+    if (size == INFINITY) {  // a block with an infinite key has the bound +inf, and says nothing of the others' terms
+      finite_size<T, D>(G, sh, rows, i0, i1, wm);
+      __syncthreads();
+      cl.sync();  // all have read err_cta
+      if (threadIdx.x == 0) {
+        err_cta = 0x1p-100f;
+        for (int g = 0; g < G; ++g) {
+          const float x = (wm[g] + wm[8 + g]) + (wm[16 + g] + wm[24 + g]);
+          err_cta = fmaxf(err_cta, x < INFINITY ? x : INFINITY);
+        }
+      }
+      cl.sync();
+      size = 0.f;
+      for (int r = 0; r < CL; ++r) size = fmaxf(size, *cl.map_shared_rank(&err_cta, r));
+    }
     uint32_t least = 0xFFFFFFFFu, most = 0u;
     // a stretch of four (of a CTA's bounds, whose number is a multiple of 16) at a time
     for (int i = threadIdx.x * 4; i < nm; i += NT * 4) {
@@ -595,8 +628,8 @@ __global__ void __launch_bounds__(NT, kPerSm<T, D>) blocks_kernel(const __grid_c
           most = max(most, y);
         }
     }
-    // terms that fp32 does not hold: 64 bits decide for all of them.  (Otherwise a bound that is no number comes from a
-    // digest that is none, and is +inf.)
+    // terms that fp32 does not hold: 64 bits decide for all of them.  (Otherwise a bound that is no number or infinite comes
+    // from such a digest, and is +inf: one of max(q, 0) and min(q, 0) is 0.)
     const bool wide = !(size < 0x1p120f) || (size > 0.f && size < 0x1p-60f);
     c.list += A.sink;  // behind the first blocks
     choose<T, D>(G, c, sh, digest, lo, nm, m, wide ? INFINITY : size * 0x1p-16f, wide, least, most, red, redu, counter,

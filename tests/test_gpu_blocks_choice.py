@@ -170,7 +170,9 @@ def test_time_of_equal_bounds(kvc, dtype):
     plain = us(K)
     K[0, 3, 12345, 7] = math.nan
     one_nan = us(K)
+    K[0, 3, 12345, 7] = math.inf
+    one_inf = us(K)
     K[:] = rand((1, H, 1, d), dtype, 52)
     equal = us(K)
-    print(f"ordinary {plain:.1f} us, one NaN {one_nan:.1f}, equal keys {equal:.1f}")
-    assert one_nan < 3 * plain and equal < 20 * plain
+    print(f"ordinary {plain:.1f} us, one NaN {one_nan:.1f}, one infinity {one_inf:.1f}, equal keys {equal:.1f}")
+    assert one_nan < 3 * plain and one_inf < 3 * plain and equal < 20 * plain
