@@ -723,8 +723,9 @@ KVC_API int kv_attn_blocks(const void *q, const void *K, const void *V, const in
  *   dev_status device int, may be NULL; KV_ERR_INVALID_ARG when a len is outside [0, cap]
  *              (that unit's outputs are left as they were), KV_ERR_TIMEOUT when a bounded
  *              device-side wait gave up; never cleared
- * Preconditions: Hq % Hkv == 0, d in {64, 128}, scale > 0.  V is finite in the slots that
- * len covers (a token multiplies later new tokens' by 0); what stands behind len is not used.
+ * Preconditions: Hq % Hkv == 0, d in {64, 128}, scale > 0.  Slots that a token does not see
+ * are not used, whatever they hold.  bf16: the prefix's V stays below 2^100 (weights of up to 2^8
+ * are summed before they are divided).
  * bf16: the prefix's products on the tensor cores (tcgen05, TMA), its weights rounded to
  * bf16 before the second product; fp32 and the own slots: fp32 accuracy.
  */

@@ -457,7 +457,7 @@ __device__ void choose(int G, const Choice &c, const float *q, const T *digest, 
 template <typename T, int D>
 __global__ void __launch_bounds__(NT, kPerSm<T, D>) blocks_kernel(const __grid_constant__ BlkArgs A) {
   extern __shared__ __align__(16) unsigned char dyn[];
-  __shared__ float wm[NW * 8], wz[NW * 8];
+  __shared__ float2 wmz[NW * 8];
   __shared__ float2 mz[8], all[16][8];
   __shared__ float sI[8];
   __shared__ float err_part[NW], err_cta;
@@ -599,6 +599,7 @@ __global__ void __launch_bounds__(NT, kPerSm<T, D>) blocks_kernel(const __grid_c
     float size = 0.f;  // of the terms of a bound
     for (int r = 0; r < CL; ++r) size = fmaxf(size, *cl.map_shared_rank(&err_cta, r));
     if (size == INFINITY) {  // a block with an infinite key has the bound +inf, and says nothing of the others' terms
+      float *wm = reinterpret_cast<float *>(wmz);
       finite_size<T, D>(G, sh, rows, i0, i1, wm);
       __syncthreads();
       cl.sync();  // all have read err_cta
@@ -657,9 +658,13 @@ __global__ void __launch_bounds__(NT, kPerSm<T, D>) blocks_kernel(const __grid_c
           },
           K, D, V, D, seen - 1, A.c_log2, lim, seen);
     __syncthreads();
-    R.leave(G, wm + warp * 8, wz + warp * 8, so + warp * G * D);
+    if (R.leave(G, wmz + warp * 8, so + warp * G * D)) {
+      const AgainArgs<T> again{q, 0, A.sq[1], 0, 8, 1, 0, K, V, D, D, c.list, tl, x0 + warp, NW, (x1 - x0 - warp + NW - 1) / NW, seen, 0,
+                               A.c_log2};
+      rows_again<T, D>(again, G, wmz + warp * 8, so + warp * G * D);
+    }
     __syncthreads();
-    join_warps<D, NW>(G, wm, wz, so, sh, mz);
+    join_warps<D, NW>(G, wmz, so, sh, mz);
   }
   cl.sync();
   for (int i = threadIdx.x; i < CL * G; i += NT) all[i / G][i % G] = cl.map_shared_rank(mz, i / G)[i % G];

@@ -255,8 +255,10 @@ struct RowStream {
       for (int x = 0; x < 4; ++x) o[i][x] += c[x] + small[x];
     }
   }
-  // A warp's share of the rows below R alone: mz [R] and output sums [R][D].
-  __device__ __forceinline__ void leave(int R, float2 *mz, float *so) {
+  // A warp's share of the rows below R alone: reference and sum of weights mz [R], output sums so [R][D].  True
+  // where the products could not hold it (rows_again).
+  __device__ __forceinline__ bool leave(int R, float2 *mz, float *so) {
+    bool bad = false;
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
       z[x] += __shfl_xor_sync(0xFFFFFFFFu, z[x], 4);
@@ -265,48 +267,169 @@ struct RowStream {
       const int r = 2 * t + x;
       if (r < R) {
         if (g == 0) mz[r] = make_float2(m[x], z[x]);
+        float2 zero = make_float2(0.f, 0.f);  // stays so where all are finite
 #pragma unroll
-        for (int i = 0; i < MT; ++i) *reinterpret_cast<float2 *>(so + r * D + at(i)) = make_float2(o[i][x], o[i][2 + x]);
-      }
-    }
-  }
-  // The same for join_warps: reference, sum of weights, output sums [R][D].
-  __device__ __forceinline__ void leave(int R, float *wm, float *wz, float *so) {
-#pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      z[x] += __shfl_xor_sync(0xFFFFFFFFu, z[x], 4);
-      z[x] += __shfl_xor_sync(0xFFFFFFFFu, z[x], 8);
-      z[x] += __shfl_xor_sync(0xFFFFFFFFu, z[x], 16);
-      const int r = 2 * t + x;
-      if (r < R) {
-        if (g == 0) {
-          wm[r] = m[x];
-          wz[r] = z[x];
+        for (int i = 0; i < MT; ++i) {
+          const float2 v = make_float2(o[i][x], o[i][2 + x]);
+          *reinterpret_cast<float2 *>(so + r * D + at(i)) = v;
+          zero = __ffma2_rn(v, make_float2(0.f, 0.f), zero);
         }
-        float *dst = so + r * D;
-#pragma unroll
-        for (int i = 0; i < MT; ++i) *reinterpret_cast<float2 *>(dst + at(i)) = make_float2(o[i][x], o[i][2 + x]);
+        // bf16: a logit that is no number is so by the formula, and the row with it
+        bad |= zero.x + zero.y != 0.f && (sizeof(T) == 4 || z[x] == z[x]);
       }
     }
+    return __any_sync(0xFFFFFFFFu, bad);
   }
 };
 
-// The shares of NW warps (wm, wz [NW][8], so [NW][R][D]) as one: sh [R][D], mz [R].  A share without
+// A share made anew where sums came out that are not finite.  The products cannot hold an infinity in V (its weight's
+// lower part, or a hidden slot's weight of 0, makes it a NaN), nor in fp32 one in K or q or what is so large that its
+// upper tf32 part is infinite.  Here each weight is one float, its products are sums of fp32, slots that a row does
+// not see are left out, and weights are at most 1, so that what is finite in the end is so on the way.  32 slots at a time, a
+// lane's logits for all rows, then their V rows one by one; it costs several times what
+// the products do.
+template <typename T>
+struct AgainArgs {
+  const T *q;          // row r is row r0 + r: batch entry / gn, head / nq, token % nq
+  long sb, sg, st;
+  int gn, nq, r0;
+  const T *k, *v;
+  long ks, vs;
+  const uint16_t *list;  // tile x is that of block list[x >> tl] (NULL: slots 16 x and on)
+  int tl;
+  int x0, step, count;   // tiles x0, x0 + step, ...
+  int lim, by_token;     // slots that row r sees: lim + by_token * its token
+  float c_log2;
+};
+template <typename T, int D, int N>  // at most N rows
+__device__ __noinline__ void some_rows_again(const AgainArgs<T> &A, int R, float2 *mz, float *so) {
+  constexpr int EV = 16 / (int)sizeof(T), E = D / 32;
+  const int lane = threadIdx.x & 31;
+  __syncwarp();  // mz, so
+  int lim[N], most = 0;
+  const uint4 *q[N];
+  float ref[N], z[N], acc[N][E];
+  bool search = false;  // a reference is to be found anew
+#pragma unroll
+  for (int r = 0; r < N; ++r) {
+    const int row = A.r0 + min(r, R - 1), b = row / A.gn, in = row - b * A.gn;
+    q[r] = reinterpret_cast<const uint4 *>(A.q + b * A.sb + in / A.nq * A.sg + in % A.nq * A.st);
+    lim[r] = r < R ? A.lim + A.by_token * (row % A.nq) : 0;
+    most = max(most, lim[r]);
+    const float2 s = mz[min(r, R - 1)];
+    ref[r] = s.x == -INFINITY ? s.x : s.x + kLazyRows;
+    search |= s.y != s.y;
+    z[r] = 0.f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[r][e] = 0.f;
+  }
+  // this lane's slot of the 32 from tile y on (-1: none), and its logits
+  auto slot = [&](int y) {
+    y += lane >> 4;
+    if (y >= A.count) return -1;
+    const int x = A.x0 + y * A.step;
+    const int j = (A.list ? ((int)A.list[x >> A.tl] << (A.tl + 4)) + ((x & ((1 << A.tl) - 1)) << 4) : x << 4) + (lane & 15);
+    return j < most ? j : -1;
+  };
+  auto logits = [&](int j, float (&l)[N]) {
+    const uint4 *k = reinterpret_cast<const uint4 *>(A.k + max(j, 0) * A.ks);
+#pragma unroll
+    for (int r = 0; r < N; ++r) l[r] = 0.f;
+#pragma unroll 4
+    for (int c = 0; c < D / EV; ++c) {
+      float x[EV], y[EV];
+      Vec16<T>::unpack(k[c], x);
+#pragma unroll
+      for (int r = 0; r < N; ++r) {
+        Vec16<T>::unpack(q[r][c], y);
+#pragma unroll
+        for (int e = 0; e < EV; ++e) l[r] = __fmaf_rn(x[e], y[e], l[r]);
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < N; ++r) l[r] = j >= 0 && j < lim[r] ? l[r] * A.c_log2 : -INFINITY;
+  };
+  if (search) {
+#pragma unroll
+    for (int r = 0; r < N; ++r) ref[r] = -INFINITY;
+#pragma unroll 1
+    for (int y = 0; y < A.count; y += 2) {
+      float l[N];
+      logits(slot(y), l);
+#pragma unroll
+      for (int r = 0; r < N; ++r) ref[r] = fmaxf(ref[r], l[r]);
+    }
+#pragma unroll
+    for (int r = 0; r < N; ++r)
+      for (int o = 16; o; o >>= 1) ref[r] = fmaxf(ref[r], __shfl_xor_sync(0xFFFFFFFFu, ref[r], o));
+  }
+#pragma unroll 1
+  for (int y = 0; y < A.count; y += 2) {
+    const int j = slot(y);
+    float p[N];
+    logits(j, p);
+#pragma unroll
+    for (int r = 0; r < N; ++r) {
+      p[r] = tc::ex2(p[r] - (ref[r] == -INFINITY ? 0.f : ref[r]));
+      z[r] += p[r];
+    }
+#pragma unroll 8
+    for (int s = 0; s < 32; ++s) {
+      const int js = __shfl_sync(0xFFFFFFFFu, j, s);
+      const T *v = A.v + max(js, 0) * A.vs + lane * E;
+      float x[E];
+#pragma unroll
+      for (int e = 0; e < E; ++e) x[e] = to_f32(v[e]);
+#pragma unroll
+      for (int r = 0; r < N; ++r) {
+        const float w = __shfl_sync(0xFFFFFFFFu, p[r], s);
+        const bool sees = js >= 0 && js < lim[r];
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[r][e] = sees ? __fmaf_rn(w, x[e], acc[r][e]) : acc[r][e];
+      }
+    }
+  }
+#pragma unroll
+  for (int r = 0; r < N; ++r) {
+    for (int o = 16; o; o >>= 1) z[r] += __shfl_xor_sync(0xFFFFFFFFu, z[r], o);
+    // the reference and the sum of weights stay as they are where they can
+    constexpr float up = 1 << (int)kLazyRows;
+    bool over = search;
+#pragma unroll
+    for (int e = 0; e < E; ++e) over |= fabsf(acc[r][e]) < INFINITY && !(fabsf(acc[r][e] * up) < INFINITY);
+    over = __any_sync(0xFFFFFFFFu, over);
+    if (r < R) {
+      if (lane == 0 && over) mz[r] = make_float2(ref[r], z[r]);
+#pragma unroll
+      for (int e = 0; e < E; ++e) so[r * D + lane * E + e] = over ? acc[r][e] : acc[r][e] * up;
+    }
+  }
+}
+
+template <typename T, int D>
+__device__ __forceinline__ void rows_again(AgainArgs<T> A, int R, float2 *mz, float *so) {
+  constexpr int N = 4;  // the calling kernel has to have the registers
+#pragma unroll 1
+  for (int r = 0; r < R; r += N, A.r0 += N) some_rows_again<T, D, N>(A, min(N, R - r), mz + r, so + r * D);
+}
+
+// The shares of NW warps (wmz [NW][8], so [NW][R][D]) as one: sh [R][D], mz [R].  A share without
 // slots has z = 0, sums of 0 and weighs nothing; a NaN in z or in the sums is passed on.
 template <int D, int NW>
-__device__ __forceinline__ void join_warps(int R, const float *wm, const float *wz, const float *so, float *sh, float2 *mz) {
+__device__ __forceinline__ void join_warps(int R, const float2 *wmz, const float *so, float *sh, float2 *mz) {
   for (int i = threadIdx.x; i < R * D; i += 32 * NW) {
     const int r = i / D;
     float M = -INFINITY;
 #pragma unroll
     for (int w = 0; w < NW; ++w)
-      if (wz[w * 8 + r] != 0.f) M = fmaxf(M, wm[w * 8 + r]);
+      if (wmz[w * 8 + r].y != 0.f) M = fmaxf(M, wmz[w * 8 + r].x);
     float v = 0.f, Z = 0.f;
 #pragma unroll
     for (int w = 0; w < NW; ++w) {
-      const float z = wz[w * 8 + r], f = z == 0.f ? 0.f : M == -INFINITY ? 1.f : tc::ex2(wm[w * 8 + r] - M);
+      const float2 s = wmz[w * 8 + r];
+      const float f = s.y == 0.f ? 0.f : M == -INFINITY ? 1.f : tc::ex2(s.x - M);
       v += f * so[w * R * D + i];
-      Z += f * z;
+      Z += f * s.y;
     }
     sh[i] = v;
     if (i % D == 0) mz[r] = make_float2(M, Z);

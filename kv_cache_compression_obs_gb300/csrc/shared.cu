@@ -41,7 +41,7 @@ constexpr int kPerSm = sizeof(T) == 4 && D == 128 ? 1 : 2;
 template <typename T, int D>
 __global__ void __launch_bounds__(NT, kPerSm<T, D>) prefix_rows_kernel(const __grid_constant__ SharedArgs A, int groups, int per) {
   extern __shared__ __align__(16) unsigned char rings[];
-  __shared__ float wm[NW * 8], wz[NW * 8];
+  __shared__ float2 wmz[NW * 8];
   pdl_wait();
   pdl_launch();
   const int warp = threadIdx.x >> 5;
@@ -59,10 +59,15 @@ __global__ void __launch_bounds__(NT, kPerSm<T, D>) prefix_rows_kernel(const __g
         A.skp[1], static_cast<const T *>(A.Vp) + h * A.svp[0], A.svp[1], k1 - 1, A.c_log2, lim, k1);
   __syncthreads();
   float *so = reinterpret_cast<float *>(rings);
-  S.leave(R, wm + warp * 8, wz + warp * 8, so + warp * R * D);
+  if (S.leave(R, wmz + warp * 8, so + warp * R * D)) {
+    const AgainArgs<T> again{static_cast<const T *>(A.q) + h * A.G * A.sq[1], A.sq[0], A.sq[1], A.sq[2], gn, A.nq, r0,
+                             static_cast<const T *>(A.Kp) + h * A.skp[0], static_cast<const T *>(A.Vp) + h * A.svp[0], A.skp[1],
+                             A.svp[1], nullptr, 0, k0 / 16 + warp, NW, (tiles - warp + NW - 1) / NW, k1, 0, A.c_log2};
+    rows_again<T, D>(again, R, wmz + warp * 8, so + warp * R * D);
+  }
   __syncthreads();
   const long at = ((long)s * A.Hkv + h) * A.rows + r0;
-  join_warps<D, NW>(R, wm, wz, so, A.part + at * D, A.stat + at);
+  join_warps<D, NW>(R, wmz, so, A.part + at * D, A.stat + at);
 }
 
 // ---- own slots ----
@@ -76,6 +81,8 @@ struct OwnArgs {
   int2 *info;    // [units] first piece, pieces
   int groups;    // of 8 query rows
 };
+// CTAs of the own slots' kernel: those that run at once, and as many again with short stretches.
+__host__ __device__ constexpr int own_ctas(int elem_bytes, int d) { return 2 * (elem_bytes == 4 && d == 128 ? 1 : 2) * kNumSmsHint; }
 constexpr int kMinTiles = 4;      // of a stretch
 constexpr int kLongShare = 90;    // per cent of the tiles
 constexpr int kKeptHeads = 2048;  // lengths that are kept in shared memory
@@ -215,7 +222,7 @@ __global__ void __launch_bounds__(NT, kPerSm<T, D>) own_slots_kernel(const __gri
       if (++stage == S.STAGES) stage = 0;
       if (at.x + 1 == at.tiles || y + 1 == count) {
         const long piece = (long)me + at.bh * W.groups + at.grp;
-        S.leave(R, W.stat + piece * 8, W.part + piece * 8 * D);
+        S.leave(R, W.stat + piece * 8, W.part + piece * 8 * D);  // what it could not hold is seen at the join
         S.fresh();
         first = true;
       }
@@ -223,6 +230,46 @@ __global__ void __launch_bounds__(NT, kPerSm<T, D>) own_slots_kernel(const __gri
     }
   }
   if (A.splits) pdl_wait();  // this kernel does not end before the prefix's
+}
+
+// Piece s of a unit (of head bh, from tile `at` of its head's line on, `tiles` long): its first tile and how many.  Found
+// anew from the lengths, by a warp, where a piece has to be attended again.
+__device__ int2 piece_tiles(const int32_t *len, int cap, int heads, int groups, int warps, int bh, int at, int tiles, int s) {
+  int before = 0, all = 0;
+  for (int i = threadIdx.x & 31; i < heads; i += 32) {
+    const int n = len[i], t = n < 0 || n > cap ? 0 : ((n + 15) >> 4) * groups;
+    all += t;
+    if (i < bh) before += t;
+  }
+  for (int o = 16; o; o >>= 1) {
+    all += __shfl_xor_sync(0xFFFFFFFFu, all, o);
+    before += __shfl_xor_sync(0xFFFFFFFFu, before, o);
+  }
+  at += before;
+  const Stretches P(all, warps);
+  const int w = P.of(at) + s, first = max(at, P.first(w)), last = min(at + tiles, P.first(w + 1));
+  return make_int2(first - at, last - first);
+}
+
+// Attends again those of a row's pieces that are not finite, by a warp; whether there was one.
+template <typename T, int D>
+__device__ __noinline__ bool own_row_again(const SharedArgs &A, const OwnArgs &W, int bh, int row, int2 own, int n) {
+  const int b = bh / A.Hkv, h = bh - b * A.Hkv, tiles = (n + 15) >> 4;
+  bool some = false;
+#pragma unroll 1
+  for (int s = 0; s < own.y; ++s) {
+    const long at = (long)(own.x + s) * 8 + row % 8;
+    bool bad = W.stat[at].y != W.stat[at].y;
+    for (int i = threadIdx.x & 31; i < D; i += 32) bad |= !(fabsf(W.part[at * D + i]) < INFINITY);
+    if (!__any_sync(0xFFFFFFFFu, bad)) continue;
+    const int2 of = piece_tiles(A.len, A.cap, A.B * A.Hkv, W.groups, own_ctas(sizeof(T), D) * NW, bh, row / 8 * tiles, tiles, s);
+    const AgainArgs<T> args{static_cast<const T *>(A.q) + q_offset(A.sq, b, h, A.G, A.nq, row), 0, 0, 0, 1, 1, 0,
+                            static_cast<const T *>(A.K) + (long)bh * A.cap * D, static_cast<const T *>(A.V) + (long)bh * A.cap * D, D, D,
+                            nullptr, 0, of.x, 1, of.y, n - A.nq + row % A.nq + 1, 0, A.c_log2};
+    some_rows_again<T, D, 1>(args, 1, W.stat + at, W.part + at * D);
+    some = true;
+  }
+  return some;
 }
 
 // ---- everything joined: one warp a query row ----
@@ -274,53 +321,64 @@ __global__ void __launch_bounds__(NT) shared_join_kernel(const __grid_constant__
   float2 st0 = make_float2(-INFINITY, 0.f), st1 = st0;  // prefix shares `lane` and 32 + lane (at most 64)
   if (lane < A.splits) st0 = A.stat[lane * share + first];
   if (32 + lane < A.splits) st1 = A.stat[(32 + lane) * share + first];
-#pragma unroll
-  for (int i = 0; i < N; ++i) load(i, A.part + (i * share + first) * D, i < A.splits);
   const float2 *ws = W.stat + (long)own.x * 8 + row % 8;
   const float *wp = W.part + ((long)own.x * 8 + row % 8) * D;
-  float M = -INFINITY;
-  for (int s = lane; s < own.y; s += 32) {
-    const float2 v = ws[s * 8];
-    if (v.y != 0.f) M = fmaxf(M, v.x);
-  }
-  if (st0.y != 0.f) M = fmaxf(M, st0.x);
-  if (st1.y != 0.f) M = fmaxf(M, st1.x);
+  float M, Z, v[E];
+#pragma unroll 1
+  for (bool again = false;; again = true) {
 #pragma unroll
-  for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, o));
-  auto factor = [&](const float2 &v) { return v.y != 0.f ? tc::ex2(M == -INFINITY ? 0.f : v.x - M) : 0.f; };
-  float Z = 0.f, v[E];
-#pragma unroll
-  for (int i = 0; i < E; ++i) v[i] = 0.f;
-  // the N sums in registers, weighed by lanes from .. from + N - 1's f
-  auto take = [&](float f, int from) {
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const float w = __shfl_sync(0xFFFFFFFFu, f, from + i);
-#pragma unroll
-      for (int y = 0; y < E; ++y) v[y] += w * x[i][y];
+    for (int i = 0; i < N; ++i) load(i, A.part + (i * share + first) * D, i < A.splits);
+    M = -INFINITY;
+    for (int s = lane; s < own.y; s += 32) {
+      const float2 y = ws[s * 8];
+      if (y.y != 0.f) M = fmaxf(M, y.x);
     }
-  };
-  const float f0 = factor(st0), f1 = factor(st1);
-  Z = f0 * st0.y + f1 * st1.y;
-  if (A.splits > 0) take(f0, 0);
-  for (int s0 = N; s0 < A.splits; s0 += N) {
+    if (st0.y != 0.f) M = fmaxf(M, st0.x);
+    if (st1.y != 0.f) M = fmaxf(M, st1.x);
 #pragma unroll
-    for (int i = 0; i < N; ++i) load(i, A.part + ((s0 + i) * share + first) * D, s0 + i < A.splits);
-    take(s0 < 32 ? f0 : f1, s0 % 32);
-  }
-  for (int s0 = 0; s0 < own.y; s0 += N) {
+    for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, o));
+    auto factor = [&](const float2 &y) { return y.y != 0.f ? tc::ex2(M == -INFINITY ? 0.f : y.x - M) : 0.f; };
 #pragma unroll
-    for (int i = 0; i < N; ++i) load(i, wp + (long)(s0 + i) * 8 * D, s0 + i < own.y);
-    float f = 0.f;
-    if (lane < N && s0 + lane < own.y) {
-      const float2 y = ws[(s0 + lane) * 8];
-      f = factor(y);
-      Z += f * y.y;
+    for (int i = 0; i < E; ++i) v[i] = 0.f;
+    // the N sums in registers, weighed by lanes from .. from + N - 1's f
+    auto take = [&](float f, int from) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const float w = __shfl_sync(0xFFFFFFFFu, f, from + i);
+#pragma unroll
+        for (int y = 0; y < E; ++y) v[y] += w * x[i][y];
+      }
+    };
+    const float f0 = factor(st0), f1 = factor(st1);
+    Z = f0 * st0.y + f1 * st1.y;
+    if (A.splits > 0) take(f0, 0);
+    for (int s0 = N; s0 < A.splits; s0 += N) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) load(i, A.part + ((s0 + i) * share + first) * D, s0 + i < A.splits);
+      take(s0 < 32 ? f0 : f1, s0 % 32);
     }
-    take(f, 0);
-  }
+    for (int s0 = 0; s0 < own.y; s0 += N) {
 #pragma unroll
-  for (int o = 16; o; o >>= 1) Z += __shfl_xor_sync(0xFFFFFFFFu, Z, o);
+      for (int i = 0; i < N; ++i) load(i, wp + (long)(s0 + i) * 8 * D, s0 + i < own.y);
+      float f = 0.f;
+      if (lane < N && s0 + lane < own.y) {
+        const float2 y = ws[(s0 + lane) * 8];
+        f = factor(y);
+        Z += f * y.y;
+      }
+      take(f, 0);
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) Z += __shfl_xor_sync(0xFFFFFFFFu, Z, o);
+    // A row that is not finite: those of its own slots' pieces that are not are attended again (bf16: a sum of weights
+    // that is no number is so by the formula).
+    float zero = 0.f;  // stays so where all are finite
+#pragma unroll
+    for (int i = 0; i < E; ++i) zero = __fmaf_rn(v[i], 0.f, zero);
+    if (again || !__any_sync(0xFFFFFFFFu, zero != 0.f || Z != Z) || (sizeof(T) == 2 && Z != Z)) break;
+    if (!own_row_again<T, D>(A, W, bh, row, own, n)) break;
+    __syncwarp();
+  }
   const float inv = Z != 0.f ? 1.f / Z : 0.f;  // 0: no key seen; a NaN is passed on
   const int g = row / A.nq, t = row - g * A.nq;
   T *o = static_cast<T *>(A.o) + (long)b * A.so[0] + ((long)h * A.G + g) * A.so[1] + t * A.so[2] + lane * E;
@@ -349,9 +407,6 @@ SharedPlan make_plan(long rows, int Hkv, int P, int dtype) {
   if (P == 0 || rows == 0) return SharedPlan{0, 0};
   return dtype == KV_BF16 ? shared_tc_plan(rows, Hkv, P) : rows_plan(rows, Hkv, P);
 }
-
-// CTAs of the own slots' kernel: those that run at once, and as many again with short stretches.
-int own_ctas(int elem_bytes, int d) { return 2 * (elem_bytes == 4 && d == 128 ? 1 : 2) * kNumSmsHint; }
 
 template <typename T, int D>
 int run(const SharedArgs &A, const OwnArgs &W, const SharedPlan &plan, cudaStream_t st) {
