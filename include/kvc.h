@@ -635,7 +635,8 @@ KVC_API int kv_evict_q8(const kv_q8_cache *cache, int keep, int recent, int sink
  *              other rows are left as they were
  *   seq        tokens behind a row's seq are neither read nor written
  *   in place   q_out == q with the same strides is allowed, and k_out == k, v_out == v
- *              without slot; any other overlap of inputs and outputs is not
+ *              without slot (otherwise these are refused); no other overlap of inputs and
+ *              outputs is
  *   dev_status device int, may be NULL; KV_ERR_INVALID_ARG when a row of k_out, v_out
  *              would be outside [0, cap) (that row is not written) or a seq is outside [0, T]
  *              (nothing of that batch row is written); never cleared

@@ -595,6 +595,13 @@ int kv_qk_norm_rope(const kv_qkv_heads *heads, int *dev_status, kv_stream_t stre
       if (s < 0 || (s == 0 && o) || (s * eb) % 16 != 0 || s > (1LL << 38)) return KV_ERR_INVALID_ARG;
     }
   }
+  for (int n = 0; n < 3; ++n) {  // in place: each row onto itself
+    if (!in[n] || in[n] != out[n]) continue;
+    if (n > 0 && h.slot) return KV_ERR_INVALID_ARG;
+    const long long count[3] = {h.B, n == 0 ? h.Hq : h.Hkv, h.T};
+    for (int a = 0; a < 3; ++a)
+      if (count[a] > 1 && h.strides[3 * n + a] != h.strides[9 + 3 * n + a]) return KV_ERR_INVALID_ARG;
+  }
   if ((h.rot > 0 && (h.q || h.k) && !h.inv_freq) || ((uintptr_t)h.inv_freq & 7u) || !aligned4(h.pos) || !aligned4(h.slot) ||
       !aligned4(h.seq) || !aligned16(h.q_weight) || !aligned16(h.k_weight))
     return KV_ERR_INVALID_ARG;
