@@ -36,7 +36,7 @@ namespace kvc {
 namespace {
 
 constexpr int NW = 4, NT = 32 * NW;
-constexpr int kMaxBlocks = 12288;  // 14 bytes of shared memory each
+constexpr int kMaxBlocks = 12288;  // 14 bytes of shared memory each and 4 shared out over the cluster (18 with one CTA)
 constexpr int kBins = 256, kFew = 64;
 constexpr int kAlone = 32;  // near bounds that a CTA computes by itself, without waiting for the others of its cluster
 template <typename T, int D>

@@ -1,6 +1,9 @@
 // pdl.cuh -- programmatic dependent launch: a kernel may be set up while the one before it
 // on the stream still runs, and waits for that one's end (and its writes) in pdl_wait().
-// Every kernel launched this way calls pdl_wait() before it touches global memory.
+// Every kernel launched this way calls pdl_wait() before it touches global memory, but for two of the shared prefix:
+// own_slots_kernel, where a prefix launch stands in front of it, and what shared_join_kernel reads of the lengths.  They
+// may, because that launch's CTAs call pdl_wait() before pdl_launch(): once own_slots_kernel runs, all that came before
+// the call is complete (it waits itself before it ends, so that its end still stands for the prefix's).
 #pragma once
 
 #include <cuda_runtime.h>

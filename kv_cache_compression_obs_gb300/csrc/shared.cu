@@ -43,7 +43,7 @@ __global__ void __launch_bounds__(NT, kPerSm<T, D>) prefix_rows_kernel(const __g
   extern __shared__ __align__(16) unsigned char rings[];
   __shared__ float2 wmz[NW * 8];
   pdl_wait();
-  pdl_launch();
+  pdl_launch();  // in this order: the next launch takes it that what precedes the call is complete (pdl.cuh)
   const int warp = threadIdx.x >> 5;
   const int grp = blockIdx.x % groups, rest = blockIdx.x / groups, h = rest % A.Hkv, s = rest / A.Hkv;
   const int r0 = grp * 8, R = min(8, A.rows - r0), gn = A.G * A.nq;

@@ -114,7 +114,7 @@ __global__ void __launch_bounds__(NT, 1) prefix_tc_kernel(const __grid_constant_
     at.t = r - at.b * gn - at.g * A.nq;
   }
   pdl_wait();
-  pdl_launch();
+  pdl_launch();  // in this order: the next launch takes it that what precedes the call is complete (pdl.cuh)
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
