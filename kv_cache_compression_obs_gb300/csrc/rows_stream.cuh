@@ -7,7 +7,9 @@
 // row and K and V are used as they lie in memory; only P is transposed
 // (in registers).  A lane holds the rows 2t and 2t + 1 of the 8, t = lane % 4.
 //   bf16: K and q are exact; P enters as hi + lo, so that the weights keep 16 bits.
-//   fp32: every operand as two tf32 parts (mma_common.cuh), O's tiles added outside the unit.
+//   fp32: every operand as two tf32 parts (mma_common.cuh), sums joined outside the unit, which cuts off: logits by
+//   a tree over the steps, O's tile by tile (logits of one sum in the unit: O twice as far off, where logits are large 4.5 times
+//   as far as by plain fp32 operations; the tree takes no longer).
 // The reference m of a row moves only when a logit passes it by kLazyRows (log2 units), so O
 // is rarely rescaled.
 //
@@ -52,6 +54,34 @@ __device__ __forceinline__ void dot16(float (&c)[4], float (&small)[4], const ui
   b0.set(__uint_as_float(q.z));
   b1.set(__uint_as_float(q.w));
   mma_split(c, small, a, b0, b1);
+}
+
+__device__ __forceinline__ void add4(const float (&a)[4], const float (&b)[4], float (&c)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; i += 2) {
+    const float2 x = __fadd2_rn(make_float2(a[i], a[i + 1]), make_float2(b[i], b[i + 1]));
+    c[i] = x.x;
+    c[i + 1] = x.y;
+  }
+}
+// The same for fp32 with the large products' sums from 0 for each of the two steps, joined by an addition that rounds where
+// the unit would cut off.
+__device__ __forceinline__ void dot16_from_0(float (&c)[4], float (&small)[4], const uint4 &x0, const uint4 &x1, const uint4 &q) {
+  const uint32_t a[4] = {x0.x, x1.x, x0.y, x1.y}, b[4] = {x0.z, x1.z, x0.w, x1.w};
+  float sum[2][4];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    Split x[4], y0, y1;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      x[i].set(__uint_as_float(h ? b[i] : a[i]));
+      sum[h][i] = 0.f;
+    }
+    y0.set(__uint_as_float(h ? q.z : q.x));
+    y1.set(__uint_as_float(h ? q.w : q.y));
+    mma_split(sum[h], small, x, y0, y1);
+  }
+  add4(sum[0], sum[1], c);
 }
 
 // log2 units
@@ -138,29 +168,36 @@ struct RowStream {
       asm volatile("cp.async.commit_group;" ::: "memory");
       asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 1) : "memory");
       __syncwarp();
-      float l[4];
-      logits(stage, c_log2, l);
+      float l[4], small[4];
+      logits(stage, l, small);
       const int j = slot(y);
       if (j + 16 > whole) hide(l, g, j, lim);
-      add(stage, l);
+      add(stage, l, small, c_log2);
       __syncwarp();  // the stage may be filled again
       if (++stage == STAGES) stage = 0;
     }
   }
-  // Logits of a stage's K tile, log2 units: l[0], l[1] slot g of rows 2t, 2t + 1; l[2], l[3] slot g + 8.
-  __device__ __forceinline__ void logits(int stage, float c_log2, float (&l)[4]) {
-    float small[4] = {0.f, 0.f, 0.f, 0.f};
+  // Logits of a stage's K tile before the scale, l + small (0 in bf16): l[0], l[1] slot g of rows 2t, 2t + 1; l[2], l[3] slot g + 8.
+  __device__ __forceinline__ void logits(int stage, float (&l)[4], float (&small)[4]) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) l[i] = 0.f;
+    for (int i = 0; i < 4; ++i) l[i] = small[i] = 0.f;
     const unsigned char *p = ring + stage * TILE + g * ROW;
     const int sw = k_swizzle(g);  // of row g + 8 too
+    auto piece = [&](int c, int r) { return *reinterpret_cast<const uint4 *>(p + r * ROW + (((4 * c + t) ^ sw) << 4)); };
+    if constexpr (sizeof(T) == 2) {
 #pragma unroll
-    for (int c = 0; c < NCH; ++c) {
-      const int at = ((4 * c + t) ^ sw) << 4;
-      dot16(l, small, *reinterpret_cast<const uint4 *>(p + at), *reinterpret_cast<const uint4 *>(p + 8 * ROW + at), q[c], T());
+      for (int c = 0; c < NCH; ++c) dot16(l, small, piece(c, 0), piece(c, 8), q[c], T());
+    } else {
+      // a tree: what is added up step by step is off by 2^-24 of the whole sum each time
+#pragma unroll
+      for (int c = 0; c < NCH; c += 2) {
+        float u[4], v[4];
+        dot16_from_0(u, small, piece(c, 0), piece(c, 8), q[c]);
+        dot16_from_0(v, small, piece(c + 1, 0), piece(c + 1, 8), q[c + 1]);
+        add4(u, v, u);
+        add4(l, u, l);
+      }
     }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) l[i] = (sizeof(T) == 4 ? l[i] + small[i] : l[i]) * c_log2;
   }
   // Row 2t + x sees the slots below n[x]; j: the tile's first slot.
   __device__ __forceinline__ static void hide(float (&l)[4], int g, int j, const int (&n)[2]) {
@@ -169,8 +206,9 @@ struct RowStream {
       if (j + g + 8 * (i >> 1) >= n[i & 1]) l[i] = -INFINITY;
   }
   // The softmax's step and O += P V with a stage's V tile.
-  __device__ __forceinline__ void add(int stage, const float (&l)[4]) {
-    const float a = fmaxf(l[0], l[2]), b = fmaxf(l[1], l[3]);
+  // (The small products' sum joins the others where the reference has been subtracted: a large logit has fewer places.)
+  __device__ __forceinline__ void add(int stage, const float (&l)[4], const float (&small)[4], float c_log2) {
+    const float a = fmaxf(l[0], l[2]) * c_log2, b = fmaxf(l[1], l[3]) * c_log2;
     if (__any_sync(0xFFFFFFFFu, a > m[0] + kLazyRows || b > m[1] + kLazyRows)) {
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
@@ -189,7 +227,8 @@ struct RowStream {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const float ref = m[i & 1];
-      p[i] = tc::ex2(l[i] - (ref == -INFINITY ? 0.f : ref));
+      const float x = __fmaf_rn(l[i], c_log2, ref == -INFINITY ? 0.f : -ref);
+      p[i] = tc::ex2(sizeof(T) == 4 ? __fmaf_rn(small[i], c_log2, x) : x);
     }
     z[0] += p[0] + p[2];
     z[1] += p[1] + p[3];
@@ -347,7 +386,7 @@ __device__ __noinline__ void some_rows_again(const AgainArgs<T> &A, int R, float
       }
     }
 #pragma unroll
-    for (int r = 0; r < N; ++r) l[r] = j >= 0 && j < lim[r] ? l[r] * A.c_log2 : -INFINITY;
+    for (int r = 0; r < N; ++r) l[r] = j >= 0 && j < lim[r] ? l[r] : -INFINITY;
   };
   if (search) {
 #pragma unroll
@@ -357,7 +396,7 @@ __device__ __noinline__ void some_rows_again(const AgainArgs<T> &A, int R, float
       float l[N];
       logits(slot(y), l);
 #pragma unroll
-      for (int r = 0; r < N; ++r) ref[r] = fmaxf(ref[r], l[r]);
+      for (int r = 0; r < N; ++r) ref[r] = fmaxf(ref[r], l[r] * A.c_log2);
     }
 #pragma unroll
     for (int r = 0; r < N; ++r)
@@ -370,7 +409,7 @@ __device__ __noinline__ void some_rows_again(const AgainArgs<T> &A, int R, float
     logits(j, p);
 #pragma unroll
     for (int r = 0; r < N; ++r) {
-      p[r] = tc::ex2(p[r] - (ref[r] == -INFINITY ? 0.f : ref[r]));
+      p[r] = tc::ex2(__fmaf_rn(p[r], A.c_log2, ref[r] == -INFINITY ? 0.f : -ref[r]));
       z[r] += p[r];
     }
 #pragma unroll 8

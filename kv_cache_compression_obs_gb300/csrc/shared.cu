@@ -214,10 +214,10 @@ __global__ void __launch_bounds__(NT, kPerSm<T, D>) own_slots_kernel(const __gri
       asm volatile("cp.async.commit_group;" ::: "memory");
       asm volatile("cp.async.wait_group %0;" ::"n"(S.STAGES - 1) : "memory");
       __syncwarp();
-      float l[4];
-      S.logits(stage, A.c_log2, l);
+      float l[4], small[4];
+      S.logits(stage, l, small);
       if (at.x * 16 + 16 > at.n - A.nq + 1) S.hide(l, S.g, at.x * 16, lim);
-      S.add(stage, l);
+      S.add(stage, l, small, A.c_log2);
       __syncwarp();  // the stage may be filled again
       if (++stage == S.STAGES) stage = 0;
       if (at.x + 1 == at.tiles || y + 1 == count) {
