@@ -15,7 +15,7 @@
 // the places left, they alone are computed again, in three parts of fp32 (error-free products and sums, then
 // rounded to 64 bits; the 64-bit unit is 40 times slower), or in 64 bits where fp32 would over- or underflow.
 // Equal keys leave every block open, so the cluster's CTAs share out what is more than a few, and ranks come from
-// histograms of the bounds as whole numbers: 12000 equal blocks of 8 heads take 280 us, 66 when they differ (each
+// histograms of the bounds as whole numbers: 12000 equal blocks of 8 heads take 400 us, 66 when they differ (each
 // CTA for itself, all against all: 111 ms).  A block whose digest is no number or infinite has the bound +inf and needs none of this.
 //
 // One launch, a cluster of CTAs for each (row, KV head, token): the CTAs share out the digests,
@@ -113,7 +113,8 @@ __device__ __forceinline__ bool meet(uint32_t a, uint32_t b, __nv_bfloat16) {
 __device__ __forceinline__ bool meet(uint32_t a, uint32_t b, float) { return (a & 0x7FFFFFFFu) != 0 && (b & 0x7FFFFFFFu) != 0; }
 
 // The passes below run once or twice per launch, so their instructions come from memory: short loops beat
-// unrolled ones (keys held in registers and everything unrolled: 13.8 us for 12.2).
+// unrolled ones (keys held in registers and everything unrolled: 13.8 us for 12.2 then), and what few calls need stands in
+// functions of its own (in line with the rest: 48.4 us for 44.5, fp32, 32 units of 32768 slots).
 
 // u of block j in 64 bits (q [G][D] as floats): one warp, lanes over the channels; every lane gets it.
 template <typename T, int D>
@@ -144,58 +145,57 @@ __device__ __forceinline__ void two_sum(float a, float b, float &s, float &e) {
   const float x = __fsub_rn(s, a);
   e = __fadd_rn(__fsub_rn(a, __fsub_rn(s, x)), __fsub_rn(b, x));
 }
-// Four blocks list[i .. i + 3] (below n), eight lanes each: `out` gets their bounds, ordered as whole numbers.
-template <typename T, int D>
-__device__ __noinline__ void bounds_in_parts(int G, const float *q, const T *digest, const uint16_t *list, int i, int n,
+// The bounds of the blocks list[e0 .. e1 - 1], ordered as whole numbers: `out` (0 before) gets the larger of it and them.
+// An item is a block and a query, and has LPI lanes: one for each 16 bytes of a digest's row where there are few items and
+// they wait for one another's steps, eight where there are many (the sums over lanes cost more than those of a lane).
+template <typename T, int D, int LPI>
+__device__ __noinline__ void bounds_in_parts(int G, const float *q, const T *digest, const uint16_t *list, int e0, int e1,
                                              unsigned long long *out) {
-  constexpr int EV = Vec16<T>::N, E = D / 8;  // elements of a 16-byte piece, of a lane
-  const int l = threadIdx.x & 7, at = i + ((threadIdx.x & 31) >> 3);
-  const uint4 *row = reinterpret_cast<const uint4 *>(digest + (long)list[min(at, n - 1)] * 2 * D) + l;
-  float low[E], top[E];
-  int nan = 0;
-#pragma unroll
-  for (int v = 0; v < E / EV; ++v) {
-    Vec16<T>::unpack(row[8 * v], low + v * EV);
-    Vec16<T>::unpack(row[D / EV + 8 * v], top + v * EV);
-  }
-#pragma unroll
-  for (int e = 0; e < E; ++e) nan |= !(fabsf(low[e]) < INFINITY) || !(fabsf(top[e]) < INFINITY);
-  for (int o = 4; o; o >>= 1) nan |= __shfl_xor_sync(0xFFFFFFFFu, nan, o);
-  double best = nan ? INFINITY : -INFINITY;
+  constexpr int EV = Vec16<T>::N, IPW = 32 / LPI, NV = D / EV / LPI;  // items of a warp, 16-byte pieces of a lane
+  const int lane = threadIdx.x & 31, l = lane % LPI, items = (e1 - e0) * G;
 #pragma unroll 1
-  for (int g = 0; g < G; ++g) {
-    float hi = 0.f, lo = 0.f, rest = 0.f, x1, x2, x3;
+  for (int first = (threadIdx.x >> 5) * IPW; first < items; first += NW * IPW) {
+    const int item = min(first + lane / LPI, items - 1), i = e0 + item / G, g = item % G;
+    const uint4 *row = reinterpret_cast<const uint4 *>(digest + (long)list[i] * 2 * D) + l;
+    float low[NV * EV], top[NV * EV], hi = 0.f, lo = 0.f, rest = 0.f, x1, x2, x3;
 #pragma unroll
-    for (int e = 0; e < E; ++e) {
-      const float x = q[g * D + (l + e / EV * 8) * EV + e % EV], y = x >= 0.f ? top[e] : low[e];
+    for (int v = 0; v < NV; ++v) {
+      Vec16<T>::unpack(row[v * LPI], low + v * EV);
+      Vec16<T>::unpack(row[D / EV + v * LPI], top + v * EV);
+    }
+    int bad = 0;
+#pragma unroll
+    for (int e = 0; e < NV * EV; ++e) {
+      const float x = q[g * D + (l + e / EV * LPI) * EV + e % EV], y = x >= 0.f ? top[e] : low[e];
       const float p = __fmul_rn(x, y), px = __fmaf_rn(x, y, -p);
+      bad |= !(fabsf(low[e]) < INFINITY) || !(fabsf(top[e]) < INFINITY);
       two_sum(hi, p, hi, x1);
       two_sum(lo, x1, lo, x2);
       two_sum(lo, px, lo, x3);
       rest = __fadd_rn(rest, __fadd_rn(x2, x3));
     }
 #pragma unroll 1
-    for (int o = 4; o; o >>= 1) {
+    for (int o = LPI / 2; o; o >>= 1) {
       const float a = __shfl_xor_sync(0xFFFFFFFFu, hi, o), b = __shfl_xor_sync(0xFFFFFFFFu, lo, o);
       const float c = __shfl_xor_sync(0xFFFFFFFFu, rest, o);
-      const bool upper = threadIdx.x & o;  // the same sum in both lanes
+      const bool upper = lane & o;  // the same sum in both lanes
+      bad |= __shfl_xor_sync(0xFFFFFFFFu, bad, o);
       two_sum(upper ? a : hi, upper ? hi : a, hi, x1);
       two_sum(upper ? b : lo, upper ? lo : b, lo, x2);
       two_sum(lo, x1, lo, x3);
       rest = __fadd_rn(__fadd_rn(rest, c), __fadd_rn(x2, x3));
     }
-    const double s = (double)hi + ((double)lo + (double)rest);
-    best = s > best ? s : best;
+    if (l == 0) atomicMax(out + i, order(bad ? (double)INFINITY : (double)hi + ((double)lo + (double)rest)));
   }
-  if (l == 0 && at < n) out[at] = order(best);
 }
 
-// The part of S that the CTA's blocks [i0, i1) of `digest` have without their infinities, in every thread's `part` [NW][8]
-// by query; the caller adds them up.
+// S of the whole cluster without the digests' infinities; [i0, i1) are this CTA's blocks, part [NW][8] and mine its memory.
 template <typename T, int D>
-__device__ __noinline__ void finite_size(int G, const float *q, const T *digest, int i0, int i1, float *part) {
+__device__ __noinline__ float finite_size(int G, const float *q, const T *digest, int i0, int i1, float *part, float &mine) {
+  cooperative_groups::cluster_group cl = cooperative_groups::this_cluster();
   const int c = threadIdx.x % D, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   float big = 0.f;
+#pragma unroll 8
   for (int i = i0 + (int)threadIdx.x / D; i < i1; i += NT / D) {
     const float low = fabsf(to_f32(digest[(long)i * 2 * D + c])), top = fabsf(to_f32(digest[(long)i * 2 * D + D + c]));
     if (low < INFINITY) big = fmaxf(big, low);
@@ -206,6 +206,18 @@ __device__ __noinline__ void finite_size(int G, const float *q, const T *digest,
     for (int o = 16; o; o >>= 1) e += __shfl_xor_sync(0xFFFFFFFFu, e, o);
     if (lane == 0) part[warp * 8 + g] = e;
   }
+  cl.sync();  // all have read `mine`
+  if (threadIdx.x == 0) {
+    mine = 0x1p-100f;
+    for (int g = 0; g < G; ++g) {
+      const float x = (part[g] + part[8 + g]) + (part[16 + g] + part[24 + g]);
+      mine = fmaxf(mine, x < INFINITY ? x : INFINITY);
+    }
+  }
+  cl.sync();
+  float size = 0.f;
+  for (int r = 0; r < (int)cl.num_blocks(); ++r) size = fmaxf(size, *cl.map_shared_rank(&mine, r));
+  return size;
 }
 
 // Shared memory of the choice.
@@ -358,12 +370,72 @@ __device__ __noinline__ void mark_best(const Choice &c, int n, int m, int (*red)
   }
 }
 
+// The blocks between `below` and `above` of the n candidates (`all_open` of them) again, and the best `places` marked.  A
+// function of its own: few clusters come here, and the others should not fetch its instructions.
+template <typename T, int D>
+__device__ __noinline__ void second_look(const Choice &c, int G, const float *q, const T *digest, int n, int places, int all_open,
+                                         float err, bool wide, float above, float below, int (*red)[NW], uint32_t (*redu)[NW],
+                                         int &count) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int stretch = (n + NT - 1) / NT * 32, i0 = min(n, warp * stretch), i1 = min(n, i0 + stretch);
+  cooperative_groups::cluster_group cl = cooperative_groups::this_cluster();
+  int to = 0;
+  for (int w = 0; w < warp; ++w) to += red[1][w];
+  for (int i = i0 + lane; i < i0 + stretch; i += 32) {
+    const float u = i < i1 ? unorder(c.key[i]) : -INFINITY;
+    const bool between = i < i1 && !(u > above) && !(u < below);
+    const unsigned who = __ballot_sync(0xFFFFFFFFu, between);
+    if (between) {
+      const int x = to + __popc(who & ((1u << lane) - 1));
+      c.list[x] = (uint16_t)i;
+      c.exact[x] = 0ull;
+    }
+    to += __popc(who);
+  }
+  __syncthreads();
+  // where there are many the cluster's CTAs, which all have the same list, have a share of them each
+  const int CL = (int)cl.num_blocks(), rank = (int)cl.block_rank();
+  const bool spread = CL > 1 && all_open > kAlone;
+  const int each = spread ? (all_open + CL - 1) / CL : all_open, e0 = spread ? min(all_open, rank * each) : 0;
+  const int e1 = min(all_open, e0 + each);
+  if (err == 0.f) {  // every term is 0: the bounds are exact
+    for (int i = e0 + threadIdx.x; i < e1; i += NT) c.exact[i] = order((double)unorder(c.key[c.list[i]]));
+  } else if (wide) {
+    for (int i = e0 + warp; i < e1; i += NW) {
+      const double x = bound64<T, D>(G, q, digest, c.list[i]);
+      if (lane == 0) c.exact[i] = order(x);
+    }
+  } else {
+    if (all_open > kAlone) bounds_in_parts<T, D, 8>(G, q, digest, c.list, e0, e1, c.exact);
+    else bounds_in_parts<T, D, D / Vec16<T>::N>(G, q, digest, c.list, e0, e1, c.exact);
+  }
+  if (spread) {
+    cl.sync();
+    for (int i = threadIdx.x; i < all_open; i += NT) {
+      const int r = i / each;
+      if (r != rank) c.exact[i] = cl.map_shared_rank(c.exact, r)[i];
+    }
+    cl.sync();  // the rings take the place of what has been read
+  } else {
+    __syncthreads();
+  }
+  if (all_open > kFew) {
+    mark_best(c, all_open, places, red, redu, count);
+  } else if ((int)threadIdx.x < all_open) {
+    const int i = threadIdx.x;
+    const unsigned long long x = c.exact[i];
+    int better = 0;
+    for (int k = 0; k < all_open; ++k) better += c.exact[k] > x || (c.exact[k] == x && k < i);
+    if (better < places) c.key[c.list[i]] = kIn;
+  }
+  __syncthreads();
+}
+
 // The best `m` of the n candidates (block lo + i; their bounds' bits in c.key) to c.list, ascending, as blocks.
 // err: how far a bound may be off; wide: only 64 bits tell them apart.
 template <typename T, int D>
 __device__ void choose(int G, const Choice &c, const float *q, const T *digest, int lo, int n, int m, float err,
-                       bool wide, uint32_t least, uint32_t most, int (*red)[NW], uint32_t (*redu)[NW], int &count,
-                       const cooperative_groups::cluster_group &cl) {
+                       bool wide, uint32_t least, uint32_t most, int (*red)[NW], uint32_t (*redu)[NW], int &count) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const float a = unorder(mth_largest(c, n, m, least, most, red, redu, count));
   const float above = a + 2.f * err, below = a - 2.f * err;
@@ -390,52 +462,7 @@ __device__ void choose(int G, const Choice &c, const float *q, const T *digest, 
   const int places = m - all_sure;
   const bool again = all_open > places;
   if (again) {
-    int to = 0;
-    for (int w = 0; w < warp; ++w) to += red[1][w];
-    for (int i = i0 + lane; i < i0 + stretch; i += 32) {
-      const float x = i < i1 ? unorder(c.key[i]) : -INFINITY;
-      const bool between = i < i1 && !(x > above) && !(x < below);
-      const unsigned who = __ballot_sync(0xFFFFFFFFu, between);
-      if (between) c.list[to + __popc(who & ((1u << lane) - 1))] = (uint16_t)i;
-      to += __popc(who);
-    }
-    __syncthreads();
-    // where there are many the cluster's CTAs, which all have the same list, have a share of them each
-    const int CL = (int)cl.num_blocks(), rank = (int)cl.block_rank();
-    const bool spread = CL > 1 && all_open > kAlone;
-    const int each = spread ? (all_open + CL - 1) / CL : all_open, e0 = spread ? min(all_open, rank * each) : 0;
-    const int e1 = min(all_open, e0 + each);
-    if (err == 0.f) {  // every term is 0: the bounds are exact
-      for (int i = e0 + threadIdx.x; i < e1; i += NT) c.exact[i] = order((double)unorder(c.key[c.list[i]]));
-    } else if (wide) {
-      for (int i = e0 + warp; i < e1; i += NW) {
-        const double x = bound64<T, D>(G, q, digest, lo + c.list[i]);
-        if (lane == 0) c.exact[i] = order(x);
-      }
-    } else {
-      for (int i = e0 + 4 * warp; i < e1; i += 4 * NW)
-        bounds_in_parts<T, D>(G, q, digest + (long)lo * 2 * D, c.list, i, e1, c.exact);
-    }
-    if (spread) {
-      cl.sync();
-      for (int i = threadIdx.x; i < all_open; i += NT) {
-        const int r = i / each;
-        if (r != rank) c.exact[i] = cl.map_shared_rank(c.exact, r)[i];
-      }
-      cl.sync();  // the rings take the place of what has been read
-    } else {
-      __syncthreads();
-    }
-    if (all_open > kFew) {
-      mark_best(c, all_open, places, red, redu, count);
-    } else if ((int)threadIdx.x < all_open) {
-      const int i = threadIdx.x;
-      const unsigned long long x = c.exact[i];
-      int better = 0;
-      for (int k = 0; k < all_open; ++k) better += c.exact[k] > x || (c.exact[k] == x && k < i);
-      if (better < places) c.key[c.list[i]] = kIn;
-    }
-    __syncthreads();
+    second_look<T, D>(c, G, q, digest + (long)lo * 2 * D, n, places, all_open, err, wide, above, below, red, redu, count);
     // how many of those each warp's stretch has now
     int in = 0;
     for (int i = i0 + lane; i < i0 + stretch; i += 32) in += __popc(__ballot_sync(0xFFFFFFFFu, i < i1 && c.key[i] == kIn));
@@ -452,6 +479,15 @@ __device__ void choose(int G, const Choice &c, const float *q, const T *digest, 
     if (in) c.list[at + __popc(who & ((1u << lane) - 1))] = (uint16_t)(lo + i);
     at += __popc(who);
   }
+}
+
+// A warp's share of the chosen tiles (first, first + NW, ..., `count` of them) made anew.
+template <typename T, int D>
+__device__ __noinline__ void share_again(const BlkArgs &A, const T *q, long bh, const uint16_t *list, int first, int count, int seen,
+                                         float2 *mz, float *so) {
+  const T *K = static_cast<const T *>(A.K) + bh * A.cap * (long)D, *V = static_cast<const T *>(A.V) + bh * A.cap * (long)D;
+  rows_again<T, D>(AgainArgs<T>{q, 0, A.sq[1], 0, 8, 1, 0, K, V, D, D, list, A.b_log2 - 4, first, NW, count, seen, 0, A.c_log2}, A.G, mz,
+                   so);
 }
 
 template <typename T, int D>
@@ -598,22 +634,8 @@ __global__ void __launch_bounds__(NT, kPerSm<T, D>) blocks_kernel(const __grid_c
     cl.sync();
     float size = 0.f;  // of the terms of a bound
     for (int r = 0; r < CL; ++r) size = fmaxf(size, *cl.map_shared_rank(&err_cta, r));
-    if (size == INFINITY) {  // a block with an infinite key has the bound +inf, and says nothing of the others' terms
-      float *wm = reinterpret_cast<float *>(wmz);
-      finite_size<T, D>(G, sh, rows, i0, i1, wm);
-      __syncthreads();
-      cl.sync();  // all have read err_cta
-      if (threadIdx.x == 0) {
-        err_cta = 0x1p-100f;
-        for (int g = 0; g < G; ++g) {
-          const float x = (wm[g] + wm[8 + g]) + (wm[16 + g] + wm[24 + g]);
-          err_cta = fmaxf(err_cta, x < INFINITY ? x : INFINITY);
-        }
-      }
-      cl.sync();
-      size = 0.f;
-      for (int r = 0; r < CL; ++r) size = fmaxf(size, *cl.map_shared_rank(&err_cta, r));
-    }
+    if (size == INFINITY)  // a block with an infinite key has the bound +inf, and says nothing of the others' terms
+      size = finite_size<T, D>(G, sh, rows, i0, i1, reinterpret_cast<float *>(wmz), err_cta);
     uint32_t least = 0xFFFFFFFFu, most = 0u;
     // a stretch of four (of a CTA's bounds, whose number is a multiple of 16) at a time
     for (int i = threadIdx.x * 4; i < nm; i += NT * 4) {
@@ -633,8 +655,7 @@ __global__ void __launch_bounds__(NT, kPerSm<T, D>) blocks_kernel(const __grid_c
     // from such a digest, and is +inf: one of max(q, 0) and min(q, 0) is 0.)
     const bool wide = !(size < 0x1p120f) || (size > 0.f && size < 0x1p-60f);
     c.list += A.sink;  // behind the first blocks
-    choose<T, D>(G, c, sh, digest, lo, nm, m, wide ? INFINITY : size * 0x1p-16f, wide, least, most, red, redu, counter,
-                 cl);
+    choose<T, D>(G, c, sh, digest, lo, nm, m, wide ? INFINITY : size * 0x1p-16f, wide, least, most, red, redu, counter);
     c.list -= A.sink;
   }
   for (int i = threadIdx.x; i < ns; i += NT)  // those that no bound decides
@@ -658,11 +679,8 @@ __global__ void __launch_bounds__(NT, kPerSm<T, D>) blocks_kernel(const __grid_c
           },
           K, D, V, D, seen - 1, A.c_log2, lim, seen);
     __syncthreads();
-    if (R.leave(G, wmz + warp * 8, so + warp * G * D)) {
-      const AgainArgs<T> again{q, 0, A.sq[1], 0, 8, 1, 0, K, V, D, D, c.list, tl, x0 + warp, NW, (x1 - x0 - warp + NW - 1) / NW, seen, 0,
-                               A.c_log2};
-      rows_again<T, D>(again, G, wmz + warp * 8, so + warp * G * D);
-    }
+    if (R.leave(G, wmz + warp * 8, so + warp * G * D))
+      share_again<T, D>(A, q, bh, c.list, x0 + warp, (x1 - x0 - warp + NW - 1) / NW, seen, wmz + warp * 8, so + warp * G * D);
     __syncthreads();
     join_warps<D, NW>(G, wmz, so, sh, mz);
   }

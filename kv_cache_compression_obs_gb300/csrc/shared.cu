@@ -37,6 +37,16 @@ static_assert(kRings<__nv_bfloat16, 64> >= NW * 8 * 64 * 4, "shares");
 template <typename T, int D>
 constexpr int kPerSm = sizeof(T) == 4 && D == 128 ? 1 : 2;
 
+// A warp's share of the prefix (tiles first, first + NW, ..., `count` of them) made anew.
+template <typename T, int D>
+__device__ __noinline__ void prefix_again(const SharedArgs &A, int h, int r0, int first, int count, int last, int R, float2 *mz,
+                                          float *so) {
+  rows_again<T, D>(AgainArgs<T>{static_cast<const T *>(A.q) + h * A.G * A.sq[1], A.sq[0], A.sq[1], A.sq[2], A.G * A.nq, A.nq, r0,
+                                static_cast<const T *>(A.Kp) + h * A.skp[0], static_cast<const T *>(A.Vp) + h * A.svp[0], A.skp[1],
+                                A.svp[1], nullptr, 0, first, NW, count, last, 0, A.c_log2},
+                   R, mz, so);
+}
+
 // ---- fp32 prefix: 8 rows and a share of the keys per CTA ----
 template <typename T, int D>
 __global__ void __launch_bounds__(NT, kPerSm<T, D>) prefix_rows_kernel(const __grid_constant__ SharedArgs A, int groups, int per) {
@@ -59,12 +69,8 @@ __global__ void __launch_bounds__(NT, kPerSm<T, D>) prefix_rows_kernel(const __g
         A.skp[1], static_cast<const T *>(A.Vp) + h * A.svp[0], A.svp[1], k1 - 1, A.c_log2, lim, k1);
   __syncthreads();
   float *so = reinterpret_cast<float *>(rings);
-  if (S.leave(R, wmz + warp * 8, so + warp * R * D)) {
-    const AgainArgs<T> again{static_cast<const T *>(A.q) + h * A.G * A.sq[1], A.sq[0], A.sq[1], A.sq[2], gn, A.nq, r0,
-                             static_cast<const T *>(A.Kp) + h * A.skp[0], static_cast<const T *>(A.Vp) + h * A.svp[0], A.skp[1],
-                             A.svp[1], nullptr, 0, k0 / 16 + warp, NW, (tiles - warp + NW - 1) / NW, k1, 0, A.c_log2};
-    rows_again<T, D>(again, R, wmz + warp * 8, so + warp * R * D);
-  }
+  if (S.leave(R, wmz + warp * 8, so + warp * R * D))
+    prefix_again<T, D>(A, h, r0, k0 / 16 + warp, (tiles - warp + NW - 1) / NW, k1, R, wmz + warp * 8, so + warp * R * D);
   __syncthreads();
   const long at = ((long)s * A.Hkv + h) * A.rows + r0;
   join_warps<D, NW>(R, wmz, so, A.part + at * D, A.stat + at);
