@@ -25,6 +25,7 @@
 // through the same rings (rows_stream.cuh), whose memory the choice borrows between.
 #include <cooperative_groups.h>
 
+#include <cfloat>
 #include <map>
 #include <mutex>
 #include <tuple>
@@ -185,11 +186,13 @@ __device__ __noinline__ void bounds_in_parts(int G, const float *q, const T *dig
       two_sum(lo, x1, lo, x3);
       rest = __fadd_rn(__fadd_rn(rest, c), __fadd_rn(x2, x3));
     }
-    if (l == 0) atomicMax(out + i, order(bad ? (double)INFINITY : (double)hi + ((double)lo + (double)rest)));
+    const double s = (double)hi + ((double)lo + (double)rest);
+    if (l == 0) atomicMax(out + i, order(bad || s != s ? (double)INFINITY : s));
   }
 }
 
-// S of the whole cluster without the digests' infinities; [i0, i1) are this CTA's blocks, part [NW][8] and mine its memory.
+// S of the whole cluster without the digests' infinities and without queries with a NaN, whose bounds are all +inf; [i0, i1)
+// are this CTA's blocks, part [NW][8] and mine its memory.
 template <typename T, int D>
 __device__ __noinline__ float finite_size(int G, const float *q, const T *digest, int i0, int i1, float *part, float &mine) {
   cooperative_groups::cluster_group cl = cooperative_groups::this_cluster();
@@ -202,16 +205,18 @@ __device__ __noinline__ float finite_size(int G, const float *q, const T *digest
     if (top < INFINITY) big = fmaxf(big, top);
   }
   for (int g = 0; g < G; ++g) {
-    float e = fabsf(q[g * D + c]) * big;
+    const float x = q[g * D + c];
+    float e = fabsf(x) * big;
     for (int o = 16; o; o >>= 1) e += __shfl_xor_sync(0xFFFFFFFFu, e, o);
-    if (lane == 0) part[warp * 8 + g] = e;
+    const bool nan = __any_sync(0xFFFFFFFFu, x != x);
+    if (lane == 0) part[warp * 8 + g] = nan ? -INFINITY : fminf(e, FLT_MAX);
   }
   cl.sync();  // all have read `mine`
   if (threadIdx.x == 0) {
     mine = 0x1p-100f;
     for (int g = 0; g < G; ++g) {
       const float x = (part[g] + part[8 + g]) + (part[16 + g] + part[24 + g]);
-      mine = fmaxf(mine, x < INFINITY ? x : INFINITY);
+      mine = fmaxf(mine, x < 0.f ? 0x1p-60f : x < INFINITY ? x : INFINITY);
     }
   }
   cl.sync();
@@ -398,7 +403,7 @@ __device__ __noinline__ void second_look(const Choice &c, int G, const float *q,
   const bool spread = CL > 1 && all_open > kAlone;
   const int each = spread ? (all_open + CL - 1) / CL : all_open, e0 = spread ? min(all_open, rank * each) : 0;
   const int e1 = min(all_open, e0 + each);
-  if (err == 0.f) {  // every term is 0: the bounds are exact
+  if (err == 0.f || below == INFINITY) {  // every term is 0, or all of these are +inf: the bounds are exact
     for (int i = e0 + threadIdx.x; i < e1; i += NT) c.exact[i] = order((double)unorder(c.key[c.list[i]]));
   } else if (wide) {
     for (int i = e0 + warp; i < e1; i += NW) {
@@ -623,10 +628,10 @@ __global__ void __launch_bounds__(NT, kPerSm<T, D>) blocks_kernel(const __grid_c
       e += products(big[x], qw, T());
       some |= meet(big[x], qw, T());
     }
-    if (some) e = fmaxf(e, 0x1p-100f);  // 0 only where every term is: not where they underflow
+    if (some && e < 0x1p-100f) e = 0x1p-100f;  // 0 only where every term is: not where they underflow
     e += __shfl_xor_sync(0xFFFFFFFFu, e, 1);
     e += __shfl_xor_sync(0xFFFFFFFFu, e, 2);
-    if (!(e < INFINITY)) e = INFINITY;  // a NaN in q
+    if (!(e < INFINITY)) e = INFINITY;  // an infinity, or a NaN in q
     e = rows_max(e);
     if (lane == 0) err_part[warp] = e;
     __syncthreads();
