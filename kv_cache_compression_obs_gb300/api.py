@@ -800,7 +800,7 @@ def kv_qk_norm_rope(q, k, v, inv_freq, pos=None, q_weight=None, k_weight=None, e
     pos [B][T] int32 (None: 0..T-1).  q_weight, k_weight [d] in q's dtype or None; one_plus: the weights are
     1 + those.  k_out, v_out [B][Hkv][cap][d]: with slot [B][Hkv] int32 (a slot cache's len) token t goes to row
     slot + t, without it to row t; other rows stay.  seq [B] int32: only the first tokens of each row.  An output may
-    be its input itself (k and v: without slot).  Outputs not given are dense tensors of T rows (with slot, k_out and v_out have to be given)."""
+    be its input itself, in the same layout (k and v: without slot).  Outputs not given are dense tensors of T rows (with slot, k_out and v_out have to be given)."""
     if q is None and k is None and v is None:
         raise ValueError("one of q, k and v must be given")
     if slot is not None and ((k is not None and k_out is None) or (v is not None and v_out is None)):
@@ -931,7 +931,7 @@ def kv_attn_blocks(q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, len_: torc
 
     The new tokens are the last n filled slots; token t sees the slots j < len - n + t + 1.  Each (token, KV head)
     attends the first `sink` and last `recent` of the blocks that it sees and the others with the largest bounds on
-    their logits, n_sel in all.  q's and out's batch, head and token strides are free."""
+    their logits, n_sel in all.  q's and out's batch, head and token strides are free (positive, multiples of 16 bytes)."""
     B, Hq, Hkv, n, cap, d, code, dev, default_scale, strides = _blocks_plan(
         _sigs(q, K, V, len_, digest, out, lse_out, sel_out, dev_status), block, n_sel)
     if dev != _get_device():
@@ -959,7 +959,8 @@ def kv_attn_shared(q: torch.Tensor, K_prefix, V_prefix, K, V, len_, scale: float
     slots) -> (o [B][Hq][n][d] in q's dtype, lse [B][Hq][n] float32).
 
     Every token sees the whole prefix; the new tokens are the last n own slots and token t sees the own slots
-    j < len - n + t + 1.  Strides of q, out and the prefix are free but for the d adjacent elements."""
+    j < len - n + t + 1.  Strides of q, out and the prefix are free (positive, multiples of 16 bytes) but for the d adjacent
+    elements."""
     B, Hq, Hkv, n, P, cap, d, code, dev, default_scale, need, strides = _shared_plan(
         _sigs(q, K_prefix, V_prefix, K, V, len_, out, lse_out, workspace, dev_status))
     if dev != _get_device():

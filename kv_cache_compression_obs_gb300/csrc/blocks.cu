@@ -10,13 +10,15 @@
 // The choice is the one that u in 64 bits makes.  The bounds are computed by warp-level products,
 // whose terms are exact (2^-21 from split fp32 operands) and whose fp32 sums the unit may cut off
 // at each term: by 2^-23 of the sum so far, which never passes S = max_g sum_c |q_gc| max_j |digest_jc|.
-// In four sums of 64 terms each they are off by at most e = 2^-16 S, a factor of two to spare.  With a the m-th largest of them, a block above a + 2e is among the true best m, one
-// below a - 2e is not; when those between (mostly one block, the m-th itself) are more than
-// the places left, they alone are computed again, in three parts of fp32 (error-free products and sums, then
-// rounded to 64 bits; the 64-bit unit is 40 times slower), or in 64 bits where fp32 would over- or underflow.
-// Equal keys leave every block open, so the cluster's CTAs share out what is more than a few, and ranks come from
-// histograms of the bounds as whole numbers: 12000 equal blocks of 8 heads take 400 us, 66 when they differ (each
-// CTA for itself, all against all: 111 ms).  A block whose digest is no number or infinite has the bound +inf and needs none of this.
+// In four sums of 64 terms each they are off by at most e = 2^-16 S, a factor of two to spare.  With a
+// the m-th largest of them, a block above a + 2e is among the true best m, one below a - 2e is not; when
+// those between (mostly one block, the m-th itself) are more than the places left, they alone are
+// computed again, in three parts of fp32 (error-free products and sums, then rounded to 64 bits; the
+// 64-bit unit is 40 times slower), or in 64 bits where fp32 would over- or underflow.
+// Equal keys leave every block open, so the cluster's CTAs share out what is more than a few, and ranks
+// come from histograms of the bounds as whole numbers: 12000 equal blocks of 8 heads take 400 us, 66 when
+// they differ (each CTA for itself, all against all: 111 ms).  A block whose digest is no number or
+// infinite has the bound +inf and needs none of this.
 //
 // One launch, a cluster of CTAs for each (row, KV head, token): the CTAs share out the digests,
 // exchange the bounds through distributed shared memory, find the same m-th

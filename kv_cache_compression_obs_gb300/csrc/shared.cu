@@ -7,7 +7,7 @@
 // A second launch streams the rows' own slots, which needs nothing of the first, in equal stretches; a
 // third joins everything:  M = max m_s, z = sum z_s 2^(m_s - M), o = sum o_s 2^(m_s - M) / z.
 //
-// Bound by memory: 64 rows of 32/8 heads behind 32768 keys with 200 to 2047 slots of their own 94 us (430 MB:
+// Bound by memory: 64 rows of 32/8 heads behind 32768 keys with 200 to 2047 slots of their own 93 us (430 MB:
 // 63 us): prefix 31, own slots 47 at 6.3 TB/s, joining 8, starts and ends between.  24 rows of
 // 3 tokens and 32 heads behind 8191 keys 70 us (49).  4 rows behind 4096 keys 14 us, three kernels'
 // latencies.  With the own slots by a cluster of CTAs per unit, which also joined, 188, 113 and 21 us.
